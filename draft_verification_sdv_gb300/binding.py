@@ -20,18 +20,31 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsdv.so")
 
 SDV_OK, SDV_ERR_ARG, SDV_ERR_CUDA, SDV_ERR_OOM, SDV_ERR_DEVICE_DATA, SDV_ERR_SCRATCH = 0, 1, 2, 3, 4, 5
-SDV_BF16, SDV_F32 = 0, 1
+SDV_BF16, SDV_F32, SDV_F16, SDV_E4M3 = 0, 1, 2, 3
 SDV_FLAG_SHARED_Q = 1
 SDV_FLAG_GREEDY = 2
 SDV_FLAG_SHARED_PREFIX_ROW = 4
 STATUS_NAMES = {0: "SDV_OK", 1: "SDV_ERR_ARG", 2: "SDV_ERR_CUDA", 3: "SDV_ERR_OOM",
                 4: "SDV_ERR_DEVICE_DATA", 5: "SDV_ERR_SCRATCH"}
 STATIC_SCRATCH_BYTES = 8 << 20
+SDV_STATUS_BAD_TOKEN, SDV_STATUS_TIMEOUT = 1, 8
 SDV_STATUS_BAD_LENGTH = 16
+SDV_STATUS_BAD_PAGE = 64
+SDV_ROPE_PLAIN, SDV_ROPE_LINEAR, SDV_ROPE_BASE, SDV_ROPE_PARTS = 0, 1, 2, 3
 SDV_HOOK_SAMPLE_NO_COPY = 1
 
 # Every entry point of include/sdv.h, with its ctypes signature.
 _VP, _I, _I64, _U64, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
+
+
+class _KVCache(ctypes.Structure):
+    """sdv_kv_cache of include/sdv.h."""
+    _fields_ = [("k", _VP), ("v", _VP), ("k_exp", _VP), ("v_exp", _VP), ("page_stride", _I64),
+                ("exp_page_stride", _I64), ("pages", _I), ("page_size", _I), ("kv_heads", _I),
+                ("head_dim", _I), ("dtype", _I)]
+
+
+_KVP = ctypes.POINTER(_KVCache)
 SIGNATURES = {
     "sdv_create": (_I, [ctypes.POINTER(_VP), _I, _I, _I, _I, _I, _VP]),
     "sdv_create_ex": (_I, [ctypes.POINTER(_VP), _I, _I, _I, _I, _I, _VP, ctypes.c_uint]),
@@ -60,6 +73,21 @@ SIGNATURES = {
     "sdv_adl_state_words": (_I, [_I]),
     "sdv_adl_step_host": (_I, [_I, _I, _I, _I, _I, _I, _VP, _VP, _VP, _VP]),
     "sdv_adl_step": (_I, [_I, _I, _I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "sdv_tree_build": (_I, [_I, _I, _I] + [_VP] * 11),
+    "sdv_rope_freqs": (_I, [_I, ctypes.c_double, _I, ctypes.c_double, ctypes.c_double,
+                            ctypes.c_double, ctypes.c_double, _VP, _VP]),
+    "sdv_rope": (_I, [_I64, _I, _I, _I, _I, _I, _I, _VP, _VP, _I64, _I64, _VP, _I64, _I64, _VP, _VP,
+                      _F, _VP, _I64, _I64, _VP, _I64, _I64]),
+    "sdv_kv_write": (_I, [_KVP, _I, _I, _I, _VP, _VP, _I64, _I64, _I64, _VP, _I64, _I64, _I64, _VP,
+                          _I, _VP, _VP, _VP]),
+    "sdv_kv_read": (_I, [_KVP, _I, _I, _I, _VP, _VP, _VP, _VP, _I, _VP, _VP, _VP]),
+    "sdv_kv_commit": (_I, [_KVP, _I, _I, _I, _VP, _VP, _I, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "sdv_tree_attn_workspace": (ctypes.c_size_t, []),
+    "sdv_tree_attn": (_I, [_KVP, _I, _I, _I, _I, _VP, _VP, _I64, _I64, _I64, _VP, _I, _VP, _VP, _VP,
+                           _I64, _F, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
+    "sdv_logits_process": (_I, [_I, _I, _I, _I, _I, _VP, _VP, _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+                                _I, _VP, _VP, _VP, _VP, _VP]),
+    "sdv_counts_commit": (_I, [_I, _I, _I, _I] + [_VP] * 7),
 }
 
 _lib = None
@@ -499,3 +527,359 @@ class Verifier:
             self.close()
         except Exception:
             pass
+
+
+# --------------------------------------------------------------------------
+# The verifier's layer: draft tree, rotary positions, paged cache, attention
+# of the tree over the cache, sampling parameters.
+#
+# These run once per layer and step, so the checks here read what torch holds
+# and build no intermediate objects; whether a pointer is on the device is
+# checked by the library.
+# --------------------------------------------------------------------------
+
+_HALF_TYPES = {torch.bfloat16: SDV_BF16, torch.float16: SDV_F16}
+_CELL_TYPES = {torch.bfloat16: SDV_BF16, torch.float16: SDV_F16, torch.float8_e4m3fn: SDV_E4M3}
+_ROPE_TYPES = {torch.bfloat16: SDV_BF16, torch.float16: SDV_F16, torch.float32: SDV_F32}
+
+
+def _array(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, name: str) -> Optional[int]:
+    """Address of a contiguous device array of n entries (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with %d entries, got %s" % (name, n, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _rows_of(t: torch.Tensor, dims: int, name: str):
+    """(shape, strides) of a device tensor whose innermost dimension is contiguous."""
+    if t.dim() != dims:
+        raise ValueError("%s must have %d dimensions, got %s" % (name, dims, tuple(t.shape)))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    stride = t.stride()
+    if stride[-1] != 1 and t.shape[-1] != 1:
+        raise ValueError("%s must be contiguous in its last dimension" % name)
+    return t.shape, stride
+
+
+def _type_of(types: dict, dtype: torch.dtype, name: str) -> int:
+    code = types.get(dtype)
+    if code is None:
+        raise TypeError("%s must be one of %s, got %s" % (name, [str(t) for t in types], dtype))
+    return code
+
+
+def _cache_of(k_cache, v_cache, k_exp, v_exp) -> _KVCache:
+    shape, ks = _rows_of(k_cache, 4, "k_cache")
+    vshape, vs = _rows_of(v_cache, 4, "v_cache")
+    pages, heads, place, dim = shape
+    code = _type_of(_CELL_TYPES, k_cache.dtype, "the cache")
+    inner = (place * dim, dim, 1)
+    if vshape != shape or v_cache.dtype != k_cache.dtype or vs[0] != ks[0] \
+            or tuple(ks[1:]) != inner or tuple(vs[1:]) != inner:
+        raise ValueError("k_cache and v_cache must be [pages, kv_heads, page_size, head_dim] of one "
+                         "type and page stride, each page contiguous")
+    exp_stride, ke, ve = 0, None, None
+    if code == SDV_E4M3:
+        if k_exp is None or v_exp is None:
+            raise ValueError("an e4m3 cache needs k_exp and v_exp")
+        for t, name in ((k_exp, "k_exp"), (v_exp, "v_exp")):
+            eshape, es = _rows_of(t, 3, name)
+            if t.dtype != torch.uint8 or eshape != shape[:3] or es[1] != place:
+                raise ValueError("%s must be uint8 [pages, kv_heads, page_size], each page contiguous"
+                                 % name)
+        exp_stride = k_exp.stride(0)
+        if v_exp.stride(0) != exp_stride:
+            raise ValueError("k_exp and v_exp must have one page stride")
+        ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
+    elif k_exp is not None or v_exp is not None:
+        raise ValueError("k_exp and v_exp belong to an e4m3 cache")
+    return _KVCache(k_cache.data_ptr(), v_cache.data_ptr(), ke, ve, ks[0], exp_stride, pages, place,
+                    heads, dim, code)
+
+
+def _table_of(block_table: torch.Tensor, B: int) -> int:
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [%d, max_pages], got %s" % (B, tuple(block_table.shape)))
+    return _array(block_table, block_table.numel(), torch.int32, "block_table")
+
+
+def _status_of(status: Optional[torch.Tensor]) -> Optional[int]:
+    return _array(status, 1, torch.int32, "status")
+
+
+def sdv_tree_build(root: torch.Tensor, drafts: torch.Tensor,
+                   draft_len: Optional[torch.Tensor] = None, stream=None,
+                   out: Optional[dict] = None, status: Optional[torch.Tensor] = None) -> dict:
+    """The tree of K drafts [B, K, gamma] behind each sequence's last token
+    root [B] (all int32): its tokens, depths, ancestor mask, the drafts' nodes,
+    the node of each verifier row, and the number of nodes.  `out` (a dict this
+    returned for the same shapes) reuses the tensors."""
+    B, K, G = drafts.shape
+    N = 1 + K * G
+    W = (N + 31) // 32
+    shapes = {"tokens": (B, N), "depth": (B, N), "mask": (B, N, W), "nodes": (B, K, G),
+              "rows": (B, K, G + 1), "count": (B,)}
+    if out is None:
+        out = {n: torch.empty(s, dtype=torch.int32, device=drafts.device) for n, s in shapes.items()}
+    at = []
+    for n, s in shapes.items():
+        size = 1
+        for x in s:
+            size *= x
+        at.append(_array(out[n], size, torch.int32, n))
+    st = load().sdv_tree_build(B, K, G, _stream_handle(stream), _array(root, B, torch.int32, "root"),
+                               _array(drafts, B * K * G, torch.int32, "drafts"),
+                               _array(draft_len, B, torch.int32, "draft_len"), *at,
+                               _status_of(status))
+    if st != SDV_OK:
+        raise SdvError(st, "sdv_tree_build")
+    return out
+
+
+def sdv_rope_freqs(R: int, base: float = 10000.0, scaling: int = SDV_ROPE_PLAIN, factor: float = 1.0,
+                   original: float = 8192, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """(rotary frequencies [R / 2] float32 on `device`, attention factor),
+    scaled for long contexts by one of SDV_ROPE_*."""
+    if R < 2:
+        raise ValueError("R must be at least 2")
+    f = torch.empty(R // 2, dtype=torch.float32)
+    at = _F()
+    st = load().sdv_rope_freqs(int(R), float(base), int(scaling), float(factor), float(original),
+                               float(fast), float(slow), f.data_ptr(), ctypes.addressof(at))
+    if st != SDV_OK:
+        raise SdvError(st, "sdv_rope_freqs")
+    return f.to(device), at.value
+
+
+def sdv_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
+             inv_freq: torch.Tensor, factor: float = 1.0, interleaved: bool = False,
+             out_q: Optional[torch.Tensor] = None, out_k: Optional[torch.Tensor] = None,
+             stream=None):
+    """Rotary positions of q [T, Hq, D] and k [T, Hk, D] (or None) at
+    positions [T] int32: the first 2 * len(inv_freq) elements of each head turn.
+    q and k may be strided views; out_q=q, out_k=k works in place.  Returns
+    (out_q, out_k)."""
+    (T, Hq, D), qs = _rows_of(q, 3, "q")
+    code = _type_of(_ROPE_TYPES, q.dtype, "q")
+    if out_q is None:
+        out_q = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    oshape, os_ = _rows_of(out_q, 3, "out_q")
+    if oshape != q.shape or out_q.dtype != q.dtype:
+        raise ValueError("out_q must have q's shape and type")
+    Hk, kp, ks, okp, oks = 0, None, (0, 0), None, (0, 0)
+    if k is not None:
+        kshape, ks = _rows_of(k, 3, "k")
+        Hk = kshape[1]
+        if kshape[0] != T or kshape[2] != D or k.dtype != q.dtype:
+            raise ValueError("k must be [%d, Hk, %d] of q's type" % (T, D))
+        if out_k is None:
+            out_k = torch.empty(kshape, dtype=k.dtype, device=k.device)
+        okshape, oks = _rows_of(out_k, 3, "out_k")
+        if okshape != kshape or out_k.dtype != k.dtype:
+            raise ValueError("out_k must have k's shape and type")
+        kp, okp = k.data_ptr(), out_k.data_ptr()
+    elif out_k is not None:
+        raise ValueError("out_k without k")
+    half = inv_freq.numel()
+    st = load().sdv_rope(T, Hq, Hk, D, 2 * half, 1 if interleaved else 0, code,
+                         _stream_handle(stream), q.data_ptr(), qs[0], qs[1], kp, ks[0], ks[1],
+                         _array(positions, T, torch.int32, "positions"),
+                         _array(inv_freq, half, torch.float32, "inv_freq"), factor,
+                         out_q.data_ptr(), os_[0], os_[1], okp, oks[0], oks[1])
+    if st != SDV_OK:
+        raise SdvError(st, "sdv_rope")
+    return out_q, out_k
+
+
+def sdv_kv_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 block_table: torch.Tensor, start: torch.Tensor,
+                 count: Optional[torch.Tensor] = None, k_exp: Optional[torch.Tensor] = None,
+                 v_exp: Optional[torch.Tensor] = None, stream=None,
+                 status: Optional[torch.Tensor] = None) -> None:
+    """Write k and v [B, N, kv_heads, D] (strided views will do) at positions
+    start[b] .. start[b] + count[b] - 1 of a paged cache [pages, kv_heads,
+    page_size, D], quantised where its cells are float8_e4m3fn (k_exp, v_exp
+    uint8 [pages, kv_heads, page_size] then hold each row's power of two)."""
+    cache = _cache_of(k_cache, v_cache, k_exp, v_exp)
+    (B, N, H, D), ks = _rows_of(k, 4, "k")
+    vshape, vs = _rows_of(v, 4, "v")
+    if vshape != k.shape or v.dtype != k.dtype or H != cache.kv_heads or D != cache.head_dim:
+        raise ValueError("k and v must be [B, N, %d, %d] of one type" % (cache.kv_heads, cache.head_dim))
+    code = _type_of(_HALF_TYPES, k.dtype, "k")
+    st = load().sdv_kv_write(cache, B, N, code, _stream_handle(stream), k.data_ptr(), ks[0], ks[1],
+                             ks[2], v.data_ptr(), vs[0], vs[1], vs[2], _table_of(block_table, B),
+                             block_table.shape[1], _array(start, B, torch.int32, "start"),
+                             _array(count, B, torch.int32, "count"), _status_of(status))
+    if st != SDV_OK:
+        raise SdvError(st, "sdv_kv_write")
+
+
+def sdv_kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                start: torch.Tensor, N: int, count: Optional[torch.Tensor] = None,
+                k_exp: Optional[torch.Tensor] = None, v_exp: Optional[torch.Tensor] = None,
+                dtype: Optional[torch.dtype] = None, stream=None,
+                status: Optional[torch.Tensor] = None):
+    """(k, v) [B, N, kv_heads, D]: positions start[b] .. start[b] + count[b] - 1
+    of the cache in `dtype` (default: the cells' type, bfloat16 for e4m3); rows
+    past count[b] are 0."""
+    cache = _cache_of(k_cache, v_cache, k_exp, v_exp)
+    if dtype is None:
+        dtype = torch.bfloat16 if cache.dtype == SDV_E4M3 else k_cache.dtype
+    code = _type_of(_HALF_TYPES, dtype, "dtype")
+    B = start.numel()
+    out = torch.empty((2, B, N, cache.kv_heads, cache.head_dim), dtype=dtype, device=k_cache.device)
+    st = load().sdv_kv_read(cache, B, N, code, _stream_handle(stream), out[0].data_ptr(),
+                            out[1].data_ptr(), _table_of(block_table, B), block_table.shape[1],
+                            _array(start, B, torch.int32, "start"),
+                            _array(count, B, torch.int32, "count"), _status_of(status))
+    if st != SDV_OK:
+        raise SdvError(st, "sdv_kv_read")
+    return out[0], out[1]
+
+
+def sdv_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                  start: torch.Tensor, nodes: torch.Tensor, sel: torch.Tensor,
+                  accept_len: torch.Tensor, k_exp: Optional[torch.Tensor] = None,
+                  v_exp: Optional[torch.Tensor] = None, out_len: Optional[torch.Tensor] = None,
+                  stream=None, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """After a verification step: move the accepted path's cells behind the
+    prefix and return the new lengths [B] (start + 1 + accept_len).  `nodes`
+    [B, K, gamma] is sdv_tree_build's; out_len=start updates it in place."""
+    cache = _cache_of(k_cache, v_cache, k_exp, v_exp)
+    B, K, G = nodes.shape
+    if out_len is None:
+        out_len = torch.empty(B, dtype=torch.int32, device=nodes.device)
+    st = load().sdv_kv_commit(cache, B, K, G, _stream_handle(stream), _table_of(block_table, B),
+                              block_table.shape[1], _array(start, B, torch.int32, "start"),
+                              _array(nodes, B * K * G, torch.int32, "nodes"),
+                              _array(sel, B, torch.int32, "sel"),
+                              _array(accept_len, B, torch.int32, "accept_len"),
+                              _array(out_len, B, torch.int32, "out_len"), _status_of(status))
+    if st != SDV_OK:
+        raise SdvError(st, "sdv_kv_commit")
+    return out_len
+
+
+def sdv_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                  block_table: torch.Tensor, ctx_len: torch.Tensor,
+                  count: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                  scale: Optional[float] = None, k_exp: Optional[torch.Tensor] = None,
+                  v_exp: Optional[torch.Tensor] = None, lse: bool = False,
+                  out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream=None, status: Optional[torch.Tensor] = None):
+    """Attention of the nodes q [B, N, Hq, D] of each sequence's tree over the
+    cache: node i sees the ctx_len[b] committed positions and the nodes of its
+    mask row ([B, N, W] or [N, W] int32 bits, sdv_tree_build's; None: a causal
+    chain), whose keys and values are at positions ctx_len[b] + node.  scale
+    defaults to 1 / sqrt(D).  Returns out [B, N, Hq, D], and with `lse` also the
+    log-sum-exp [B, N, Hq].  `workspace` (uint8, sdv_tree_attn_workspace()
+    bytes) may be passed to reuse one; by default it is taken from torch's
+    allocator for the call."""
+    cache = _cache_of(k_cache, v_cache, k_exp, v_exp)
+    (B, N, Hq, D), qs = _rows_of(q, 4, "q")
+    code = _type_of(_HALF_TYPES, q.dtype, "q")
+    if D != cache.head_dim:
+        raise ValueError("q must be [B, N, Hq, %d]" % cache.head_dim)
+    lib = load()
+    handle = _stream_handle(stream)
+    mask_sb, W = 0, (N + 31) // 32
+    if mask is not None:
+        shape = tuple(mask.shape)
+        if shape != (N, W) and shape != (B, N, W):
+            raise ValueError("mask must be [%d, %d] or [%d, %d, %d]" % (N, W, B, N, W))
+        mask_sb = N * W if len(shape) == 3 else 0
+    if out is None:
+        out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
+    logs = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device) if lse else None
+    ws_bytes = lib.sdv_tree_attn_workspace()
+    if workspace is None:
+        if stream is None:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        else:       # the allocator hands memory out again in its stream's order
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+            with torch.cuda.stream(s):
+                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous uint8")
+    st = lib.sdv_tree_attn(
+        cache, B, N, Hq, code, handle, q.data_ptr(), qs[0], qs[1], qs[2], _table_of(block_table, B),
+        block_table.shape[1], _array(ctx_len, B, torch.int32, "ctx_len"),
+        _array(count, B, torch.int32, "count"),
+        None if mask is None else _array(mask, mask.numel(), torch.int32, "mask"), mask_sb,
+        D ** -0.5 if scale is None else scale,
+        _array(out, B * N * Hq * D, q.dtype, "out"), None if logs is None else logs.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _status_of(status))
+    if st != SDV_OK:
+        raise SdvError(st, "sdv_tree_attn")
+    return (out, logs) if lse else out
+
+
+def sdv_logits_process(logits: torch.Tensor, drafts: torch.Tensor,
+                       counts: Optional[torch.Tensor] = None,
+                       prompt: Optional[torch.Tensor] = None,
+                       repetition: Optional[torch.Tensor] = None,
+                       frequency: Optional[torch.Tensor] = None,
+                       presence: Optional[torch.Tensor] = None,
+                       bias_ids: Optional[torch.Tensor] = None,
+                       bias: Optional[torch.Tensor] = None, allow: Optional[torch.Tensor] = None,
+                       rows: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                       stream=None, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The sampling parameters of every draft position, on verifier logits
+    [B, K, gamma + 1, V], or with rows [B, K, gamma + 1] (sdv_tree_build's) on a
+    tree's logits [B, nodes, V]: penalties that count the history (counts [B, V]
+    int32, prompt bits [B, ceil(V / 32)] int32) and the draft's earlier tokens,
+    biases [B, M], and a grammar's allowed tokens (bits [B, K, gamma + 1,
+    ceil(V / 32)] int32).  Returns [B, K, gamma + 1, V] for a Verifier call;
+    out=logits works in place when rows is None."""
+    B, K, G = drafts.shape
+    V = logits.shape[-1]
+    code = _dtype_code(logits.dtype)
+    W = (V + 31) // 32
+    nsrc = 0
+    if rows is None:
+        if tuple(logits.shape) != (B, K, G + 1, V):
+            raise ValueError("logits must be [%d, %d, %d, V]" % (B, K, G + 1))
+    else:
+        if logits.dim() != 3 or logits.shape[0] != B:
+            raise ValueError("logits must be [%d, nodes, V]" % B)
+        nsrc = logits.shape[1]
+    M = 0 if bias_ids is None else bias_ids.numel() // B
+    if out is None:
+        out = torch.empty((B, K, G + 1, V), dtype=logits.dtype, device=logits.device)
+    i32, f32 = torch.int32, torch.float32
+    st = load().sdv_logits_process(
+        B, K, G, V, code, _stream_handle(stream), _array(logits, logits.numel(), logits.dtype, "logits"),
+        nsrc, _array(rows, B * K * (G + 1), i32, "rows"), _array(drafts, B * K * G, i32, "drafts"),
+        _array(counts, B * V, i32, "counts"), _array(prompt, B * W, i32, "prompt"),
+        _array(repetition, B, f32, "repetition"), _array(frequency, B, f32, "frequency"),
+        _array(presence, B, f32, "presence"), M, _array(bias_ids, B * M, i32, "bias_ids") if M else None,
+        _array(bias, B * M, f32, "bias") if M else None,
+        _array(allow, B * K * (G + 1) * W, i32, "allow"),
+        _array(out, B * K * (G + 1) * V, logits.dtype, "out"), _status_of(status))
+    if st != SDV_OK:
+        raise SdvError(st, "sdv_logits_process")
+    return out
+
+
+def sdv_counts_commit(counts: torch.Tensor, drafts: torch.Tensor, sel: torch.Tensor,
+                      accept_len: torch.Tensor, next_token: torch.Tensor, stream=None,
+                      status: Optional[torch.Tensor] = None) -> None:
+    """Add a verification step's committed tokens (the accepted ones and the
+    next token) to counts [B, V] int32."""
+    B, K, G = drafts.shape
+    V = counts.shape[-1]
+    i32 = torch.int32
+    st = load().sdv_counts_commit(B, K, G, V, _stream_handle(stream),
+                                  _array(drafts, B * K * G, i32, "drafts"), _array(sel, B, i32, "sel"),
+                                  _array(accept_len, B, i32, "accept_len"),
+                                  _array(next_token, B, i32, "next_token"),
+                                  _array(counts, B * V, i32, "counts"), _status_of(status))
+    if st != SDV_OK:
+        raise SdvError(st, "sdv_counts_commit")

@@ -1,0 +1,328 @@
+// k7_kvcache.cu -- the paged cache: writing new keys and values (quantising
+// them on the way), reading them back, and keeping the accepted path's.
+//
+// An e4m3 row (one position, one head) is held in units of a power of two of
+// its own, so both directions are exact but for the one rounding to e4m3: the
+// product by a power of two rounds nothing, neither here nor where attention
+// takes the row back to 16 bits.  Against a free scale (largest value at 448) a
+// row loses at most one binade of e4m3's range at its small end and none of its
+// relative precision.
+//
+// Bound by HBM: each row is read once and written once.  D / 8 lanes (the next
+// power of two of them) hold a row, eight elements each, find its largest
+// magnitude with shuffles and write it back.  A CTA covers the heads of a few
+// positions, so that its reads of one position's heads are contiguous.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "sdv_layer.h"
+#include "sdv_plan.h"
+
+namespace sdv {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ float pow2f(int e) {        // 2^e, -126 <= e <= 127
+    return __int_as_float((e + 127) << 23);
+}
+
+template <int TYPE> __device__ __forceinline__ void widen(const uint4& v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 f;
+        if constexpr (TYPE == kTypeBf16) {
+            f = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        } else {
+            f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        }
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+template <int TYPE> __device__ __forceinline__ uint32_t narrow2(float x, float y) {
+    if constexpr (TYPE == kTypeBf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+// Eight consecutive 16-bit elements, with or without 16-byte alignment.
+template <bool VEC> __device__ __forceinline__ uint4 load8(const unsigned char* p) {
+    if constexpr (VEC) {
+        return __ldcs(reinterpret_cast<const uint4*>(p));
+    } else {
+        const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = h[2 * i] | (static_cast<uint32_t>(h[2 * i + 1]) << 16);
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// The page of position `pos` of sequence b, or -1 with the status set.
+__device__ __forceinline__ int page_of(const CellsArgs& a, int b, int64_t pos, unsigned* st) {
+    if (pos < 0 || pos >= static_cast<int64_t>(a.max_pages) * a.c.P) {
+        *st = kStatusBadLength;
+        return -1;
+    }
+    const int page = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + pos / a.c.P);
+    if (page < 0 || page >= a.c.pages) {
+        *st = kStatusBadPage;
+        return -1;
+    }
+    return page;
+}
+
+struct Row {
+    int b, n, h;
+    bool isv, live;
+    int cnt;
+};
+
+// Item w of the grid: (b, n, k or v, h), heads fastest.
+__device__ __forceinline__ Row row_of(const CellsArgs& a, int64_t w) {
+    Row r;
+    const int hv = 2 * a.c.H;
+    r.live = w < static_cast<int64_t>(a.B) * a.N * hv;
+    if (!r.live) w = 0;
+    const int64_t bn = w / hv;
+    const int x = static_cast<int>(w - bn * hv);
+    r.isv = x >= a.c.H;
+    r.h = r.isv ? x - a.c.H : x;
+    r.b = static_cast<int>(bn / a.N);
+    r.n = static_cast<int>(bn - static_cast<int64_t>(r.b) * a.N);
+    r.cnt = a.count ? __ldg(a.count + r.b) : a.N;
+    return r;
+}
+
+template <int TYPE, bool E4M3, bool VEC, int LANES>
+__global__ void __launch_bounds__(kThreads) kv_write_kernel(const CellsArgs a) {
+    const int lane = threadIdx.x % LANES;
+    const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / LANES;
+    const Row r = row_of(a, w);
+    unsigned st = 0;
+    bool go = r.live;
+    if (r.cnt < 0 || r.cnt > a.N) st = kStatusBadLength, go = false;
+    if (r.n >= r.cnt) go = false;
+    const int64_t pos = static_cast<int64_t>(__ldg(a.start + r.b)) + r.n;
+    int page = 0;
+    if (go) {
+        page = page_of(a, r.b, pos, &st);
+        go = page >= 0;
+    }
+    if (st && r.live && lane == 0 && a.status) atomicOr(a.status, st);
+    const bool mine = go && lane * 8 < a.c.D;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (mine)
+        x = load8<VEC>((r.isv ? a.v + r.b * a.v_sb + r.n * a.v_sn + r.h * a.v_sh
+                              : a.k + r.b * a.k_sb + r.n * a.k_sn + r.h * a.k_sh) + lane * 16);
+    const int64_t cell = static_cast<int64_t>(r.h) * a.c.P + pos % a.c.P;   // row within the page
+    unsigned char* dst = (r.isv ? a.c.v : a.c.k) + page * a.c.page_stride;
+    if constexpr (!E4M3) {
+        if (mine) *reinterpret_cast<uint4*>(dst + cell * a.c.D * 2 + lane * 16) = x;
+    } else {
+        float f[8], top = 0.0f;
+        int bad = 0;
+        widen<TYPE>(x, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            top = fmaxf(top, fabsf(f[i]));
+            bad |= !(fabsf(f[i]) < INFINITY);
+        }
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+        }
+        // top = 1.m 2^x <= 448 2^e: e = x - 8 while 1.m <= 1.75, else x - 7
+        // (a subnormal or zero top has x = -127 and ends at the floor as well)
+        const int bits = __float_as_int(top);
+        int e = (bits >> 23) - 127 - ((bits & 0x7fffff) <= 0x600000 ? 8 : 7);
+        e = e < -126 ? -126 : e;
+        const float inv = pow2f(-e);
+        uint32_t o[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
+                make_float2(f[4 * i] * inv, f[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+            const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
+                make_float2(f[4 * i + 2] * inv, f[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+            o[i] = bad ? 0x7f7f7f7fu : static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+        }
+        if (mine) {
+            *reinterpret_cast<uint2*>(dst + cell * a.c.D + lane * 8) = make_uint2(o[0], o[1]);
+            if (lane == 0)
+                (r.isv ? a.c.ve : a.c.ke)[page * a.c.exp_page_stride + cell] =
+                    static_cast<unsigned char>(bad ? 255 : e + 127);
+        }
+    }
+}
+
+template <int TYPE, bool E4M3, int LANES>
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const CellsArgs a) {
+    const int lane = threadIdx.x % LANES;
+    const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / LANES;
+    const Row r = row_of(a, w);
+    if (!r.live || lane * 8 >= a.c.D) return;
+    unsigned st = 0;
+    int page = -1;
+    bool zero = false;
+    const int64_t pos = static_cast<int64_t>(__ldg(a.start + r.b)) + r.n;
+    if (r.cnt < 0 || r.cnt > a.N)
+        st = kStatusBadLength;
+    else if (r.n >= r.cnt)
+        zero = true;
+    else
+        page = page_of(a, r.b, pos, &st);
+    if (st && lane == 0 && a.status) atomicOr(a.status, st);
+    uint4 o = make_uint4(0, 0, 0, 0);
+    if (page >= 0) {
+        const int64_t cell = static_cast<int64_t>(r.h) * a.c.P + pos % a.c.P;
+        const unsigned char* src = (r.isv ? a.c.v : a.c.k) + page * a.c.page_stride;
+        if constexpr (!E4M3) {
+            o = __ldcs(reinterpret_cast<const uint4*>(src + cell * a.c.D * 2 + lane * 16));
+        } else {
+            const uint2 q = __ldcs(reinterpret_cast<const uint2*>(src + cell * a.c.D + lane * 8));
+            const int ex = (r.isv ? a.c.ve : a.c.ke)[page * a.c.exp_page_stride + cell];
+            // 2^(ex - 127) (0 stands for 2^-127, a subnormal), 255: not a number
+            const float unit = ex == 255 ? __int_as_float(0x7fc00000)
+                               : ex == 0 ? __int_as_float(0x00400000) : __int_as_float(ex << 23);
+            const uint32_t ww[2] = {q.x, q.y};
+            uint32_t out[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                    static_cast<__nv_fp8x2_storage_t>(ww[i / 2] >> (16 * (i % 2))), __NV_E4M3);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                out[i] = narrow2<TYPE>(f.x * unit, f.y * unit);
+            }
+            o = make_uint4(out[0], out[1], out[2], out[3]);
+        }
+    } else if (!zero) {
+        o = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);   // NaN in either type
+    }
+    unsigned char* dst = static_cast<unsigned char*>(r.isv ? a.ov : a.ok);
+    const int64_t row = (static_cast<int64_t>(r.b) * a.N + r.n) * a.c.H + r.h;
+    __stcs(reinterpret_cast<uint4*>(dst + row * a.c.D * 2 + lane * 16), o);
+}
+
+// One CTA per sequence; a thread moves one piece of a row (or one exponent) of
+// every accepted token, in the path's order.  Nodes grow along the path from 1
+// on, so token j' sits at place j' + 1 or later: its cell is read before the
+// moves overwrite it, and within a thread nothing is reordered.
+__global__ void __launch_bounds__(kThreads) kv_commit_kernel(const CommitArgs a) {
+    const int b = blockIdx.x;
+    const int start = a.start[b], sel = a.sel[b], acc = a.acc[b];
+    const int64_t places = static_cast<int64_t>(a.max_pages) * a.c.P;
+    __shared__ unsigned s_bad;
+    if (threadIdx.x == 0) s_bad = 0;
+    __syncthreads();
+    const bool skip = sel == -1;
+    const bool ok = !skip && sel >= 0 && sel < a.K && acc >= 0 && acc <= a.G && start >= 0 &&
+                    start + static_cast<int64_t>(acc) < places;
+    if (ok) {
+        const int32_t* path = a.nodes + (static_cast<int64_t>(b) * a.K + sel) * a.G;
+        const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
+        const int piece = a.cell == 1 ? 8 : 16;            // bytes a thread moves at a time
+        const int per_row = a.c.D * a.cell / piece;
+        const int pieces = 2 * a.c.H * per_row, exps = a.cell == 1 ? 2 * a.c.H : 0;
+        for (int w = threadIdx.x; w < pieces + exps; w += kThreads) {
+            const bool isx = w >= pieces;
+            const int x = isx ? w - pieces : w / per_row;
+            const int off = isx ? 0 : (w % per_row) * piece;
+            const bool isv = x >= a.c.H;
+            const int h = isv ? x - a.c.H : x;
+            unsigned char* base = isx ? (isv ? a.c.ve : a.c.ke) : (isv ? a.c.v : a.c.k);
+            const int64_t stride = isx ? a.c.exp_page_stride : a.c.page_stride;
+            const int row_bytes = isx ? 1 : a.c.D * a.cell;
+            int last = 0;
+            for (int j = 0; j < acc; ++j) {
+                const int node = path[j];
+                const int64_t from = static_cast<int64_t>(start) + node, to = static_cast<int64_t>(start) + 1 + j;
+                if (node <= last || from >= places) {      // not a path of this tree
+                    atomicOr(&s_bad, kStatusBadLength);
+                    break;
+                }
+                last = node;
+                const int pf = table[from / a.c.P], pt = table[to / a.c.P];
+                if (pf < 0 || pf >= a.c.pages || pt < 0 || pt >= a.c.pages) {
+                    atomicOr(&s_bad, kStatusBadPage);
+                    break;
+                }
+                if (from == to) continue;
+                const unsigned char* src = base + pf * stride + (static_cast<int64_t>(h) * a.c.P + from % a.c.P) * row_bytes + off;
+                unsigned char* dst = base + pt * stride + (static_cast<int64_t>(h) * a.c.P + to % a.c.P) * row_bytes + off;
+                if (isx)
+                    *dst = *src;
+                else if (a.cell == 1)
+                    *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(src);
+                else
+                    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+            }
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const unsigned st = ok ? s_bad : skip ? 0u : static_cast<unsigned>(kStatusBadLength);
+        if (st && a.status) atomicOr(a.status, st);
+        if (a.out_len) a.out_len[b] = ok && !st ? start + 1 + acc : start;
+    }
+}
+
+template <int LANES> dim3 grid_of(const CellsArgs& a) {
+    const int64_t rows = static_cast<int64_t>(a.B) * a.N * 2 * a.c.H;
+    return dim3(static_cast<unsigned>((rows * LANES + kThreads - 1) / kThreads));
+}
+
+template <int TYPE, bool E4M3, int LANES>
+cudaError_t write_lanes(const CellsArgs& a, bool vec, cudaStream_t s) {
+    if (vec)
+        kv_write_kernel<TYPE, E4M3, true, LANES><<<grid_of<LANES>(a), kThreads, 0, s>>>(a);
+    else
+        kv_write_kernel<TYPE, E4M3, false, LANES><<<grid_of<LANES>(a), kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <int TYPE, bool E4M3>
+cudaError_t write_typed(const CellsArgs& a, bool vec, cudaStream_t s) {
+    if (a.c.D <= 64) return write_lanes<TYPE, E4M3, 8>(a, vec, s);
+    if (a.c.D <= 128) return write_lanes<TYPE, E4M3, 16>(a, vec, s);
+    return write_lanes<TYPE, E4M3, 32>(a, vec, s);
+}
+
+template <int TYPE, bool E4M3>
+cudaError_t read_typed(const CellsArgs& a, cudaStream_t s) {
+    if (a.c.D <= 64)
+        kv_read_kernel<TYPE, E4M3, 8><<<grid_of<8>(a), kThreads, 0, s>>>(a);
+    else if (a.c.D <= 128)
+        kv_read_kernel<TYPE, E4M3, 16><<<grid_of<16>(a), kThreads, 0, s>>>(a);
+    else
+        kv_read_kernel<TYPE, E4M3, 32><<<grid_of<32>(a), kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_write(const CellsArgs& a, int type, bool e4m3, bool vec, cudaStream_t s) {
+    if (!e4m3) return write_typed<kTypeBf16, false>(a, vec, s);      // 16-bit cells: moved as they are
+    return type == kTypeBf16 ? write_typed<kTypeBf16, true>(a, vec, s) : write_typed<kTypeF16, true>(a, vec, s);
+}
+
+cudaError_t launch_kv_read(const CellsArgs& a, int type, bool e4m3, cudaStream_t s) {
+    if (!e4m3) return read_typed<kTypeBf16, false>(a, s);
+    return type == kTypeBf16 ? read_typed<kTypeBf16, true>(a, s) : read_typed<kTypeF16, true>(a, s);
+}
+
+cudaError_t launch_kv_commit(const CommitArgs& a, cudaStream_t s) {
+    kv_commit_kernel<<<static_cast<unsigned>(a.B), kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace sdv

@@ -1,0 +1,85 @@
+// k8_attn.cu -- tree attention (sdv_tree_attn): which kernel runs, and the join
+// of the partial results of units that several CTAs share.
+#include "k8_attn.cuh"
+
+namespace sdv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxRows = 256;        // of the largest row tile
+constexpr int kMaxCtasPerSm = 2;
+
+// out = sum_i 2^(L_i - L) out_i with L = log2 sum_i 2^(L_i), over the CTAs that
+// share a unit.  One column of the grid per CTA of the kernel before, most of
+// which find nothing to do.
+template <bool F16>
+__global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, int MT) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 d0 = a.desc[2 * blockIdx.x];
+    if (d0.x < 0) return;
+    const int b = d0.x, h = d0.y, mt = d0.z, first = d0.w, last = a.desc[2 * blockIdx.x + 1].x;
+    const int D = a.c.D, vec = D / 4;
+    const float nan_value = __int_as_float(0x7fc00000);
+    for (int w = threadIdx.x + blockIdx.y * kThreads; w < MT * vec; w += kThreads * gridDim.y) {
+        const int r = w / vec, d = (w % vec) * 4;
+        const int row = mt * MT + r, node = row / a.g;
+        if (node >= a.N) continue;
+        float top = -INFINITY;
+        bool nan = false;
+        for (int i = first; i <= last; ++i) {
+            const float L = attn::part_rows(a, i, i == first, MT)[MT * D + r];
+            nan |= L != L;
+            top = fmaxf(top, L);
+        }
+        const float base = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = first; i <= last; ++i) {
+            const float* p = attn::part_rows(a, i, i == first, MT);
+            const float f = ex2(p[MT * D + r] - base);
+            const float4 v = *reinterpret_cast<const float4*>(p + r * D + d);
+            sum += f;
+            acc[0] += v.x * f, acc[1] += v.y * f, acc[2] += v.z * f, acc[3] += v.w * f;
+        }
+        const float inv = nan ? nan_value : sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int64_t orow = (static_cast<int64_t>(b) * a.N + node) * a.Hq + h * a.g + row % a.g;
+        unsigned short* dst = static_cast<unsigned short*>(a.out) + orow * D + d;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(attn::pack2<F16>(acc[0] * inv, acc[1] * inv),
+                                                    attn::pack2<F16>(acc[2] * inv, acc[3] * inv));
+        if (d == 0 && a.lse)
+            a.lse[orow] = nan ? nan_value : sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_combine(const AttnArgs& a, bool f16, int MT, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    const int blocks = (MT * (a.c.D / 4) + kThreads - 1) / kThreads;        // 16 rows of 128: two
+    cfg.gridDim = dim3(static_cast<unsigned>(a.ctas), static_cast<unsigned>(blocks < 8 ? blocks : 8));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return f16 ? cudaLaunchKernelEx(&cfg, combine_kernel<true>, a, MT)
+               : cudaLaunchKernelEx(&cfg, combine_kernel<false>, a, MT);
+}
+
+size_t attn_workspace_bytes(int nsm) {
+    const size_t ctas = static_cast<size_t>(nsm) * kMaxCtasPerSm;
+    return ctas * (2 * sizeof(int4) + 2 * static_cast<size_t>(kMaxRows) * (kCacheMaxDim + 1) * sizeof(float));
+}
+
+cudaError_t launch_tree_attn(AttnArgs a, int type, bool e4m3, void* workspace, int nsm, cudaStream_t s) {
+    a.desc = static_cast<int4*>(workspace);
+    a.part = reinterpret_cast<float*>(a.desc + 2 * kMaxCtasPerSm * nsm);
+    const bool f16 = type == kTypeF16;
+    const int rows = a.N * a.g;
+    if (a.c.D <= 64) return launch_attn_mma64(a, f16, e4m3, rows, nsm, s);
+    if (a.c.D <= 128) return launch_attn_mma128(a, f16, e4m3, rows, nsm, s);
+    return launch_attn_mma256(a, f16, e4m3, rows, nsm, s);
+}
+
+}  // namespace sdv

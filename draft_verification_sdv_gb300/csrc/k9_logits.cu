@@ -1,0 +1,214 @@
+// k9_logits.cu -- sampling parameters (penalties for repeated tokens, biases,
+// grammar masks) on the logits of every draft position, and the update of the
+// token counts after a step.
+//
+// Row (b, k, j) counts the history of sequence b and the first j tokens of
+// draft k, so the rows of one draft differ by one token from one to the next.
+// A CTA therefore owns a slice of the vocabulary and walks the rows of one
+// draft: the counts, prompt bits and biases of its slice are read once and stay
+// in registers, and the thread that owns draft token j counts it after row j.
+//
+// Bound by HBM: each logit is read and written once (2 + 2 bytes in bf16, and a
+// bit of the grammar mask).  Four rows are in flight per thread.
+#include <cuda_bf16.h>
+
+#include "sdv_device.cuh"
+#include "sdv_layer.h"
+#include "sdv_plan.h"
+
+namespace sdv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kFlight = 4;            // rows in flight per thread
+constexpr int kBiasPass = 1024;       // biases sorted at a time
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs a) {
+    constexpr int E = BF16 ? 8 : 4;                 // logits of a 16-byte vector
+    constexpr int kSlice = kThreads * E;
+    __shared__ int s_n;
+    __shared__ int2 s_raw[kBiasPass];               // (place in the list, id)
+    __shared__ int2 s_bias[kBiasPass];              // (id, value) in the list's order
+    const unsigned slices = (static_cast<unsigned>(a.V) + kSlice - 1) / kSlice;
+    const int bk = static_cast<int>(blockIdx.x / slices);
+    const int b = bk / a.K, k = bk % a.K;
+    const int slice0 = static_cast<int>(blockIdx.x % slices) * kSlice;
+    const int v0 = slice0 + threadIdx.x * E;        // this thread's first token
+    const bool live = v0 < a.V;                     // V is a multiple of E
+    const int rows = a.G + 1;
+    const int j0 = static_cast<int>(static_cast<int64_t>(blockIdx.y) * rows / a.row_splits);
+    const int j1 = static_cast<int>(static_cast<int64_t>(blockIdx.y + 1) * rows / a.row_splits);
+
+    const float rep = a.rep ? a.rep[b] : 1.0f;
+    const float freq = a.freq ? a.freq[b] : 0.0f, pres = a.pres ? a.pres[b] : 0.0f;
+    int c[E];
+    float bias[E], add[E];
+    unsigned seen = 0;                              // bit e: the repetition penalty applies
+#pragma unroll
+    for (int e = 0; e < E; ++e) c[e] = 0, bias[e] = 0.0f;
+    if (live) {
+        if (a.counts) {
+            const int4* p = reinterpret_cast<const int4*>(a.counts + static_cast<int64_t>(b) * a.V + v0);
+#pragma unroll
+            for (int u = 0; u < E / 4; ++u) {
+                const int4 x = __ldg(p + u);
+                c[4 * u] = x.x, c[4 * u + 1] = x.y, c[4 * u + 2] = x.z, c[4 * u + 3] = x.w;
+            }
+        }
+        if (a.prompt)
+            seen = static_cast<unsigned>(__ldg(a.prompt + static_cast<int64_t>(b) * a.W + (v0 >> 5))) >> (v0 & 31);
+    }
+    for (int m0 = 0; m0 < a.M; m0 += kBiasPass) {   // the biases that fall into the slice
+        if (threadIdx.x == 0) s_n = 0;
+        __syncthreads();
+        for (int m = m0 + threadIdx.x; m < min(m0 + kBiasPass, a.M); m += kThreads) {
+            const int id = a.bias_ids[static_cast<int64_t>(b) * a.M + m];
+            if (id >= slice0 && id < slice0 + kSlice && id < a.V)
+                s_raw[atomicAdd(&s_n, 1)] = make_int2(m, id);
+        }
+        __syncthreads();
+        const int n = s_n;
+        for (int i = threadIdx.x; i < n; i += kThreads) {     // in the list's order
+            int at = 0;
+            for (int x = 0; x < n; ++x) at += s_raw[x].x < s_raw[i].x;
+            s_bias[at] = make_int2(s_raw[i].y, __float_as_int(
+                a.bias[static_cast<int64_t>(b) * a.M + s_raw[i].x]));
+        }
+        __syncthreads();
+        for (int i = 0; i < n; ++i) {
+            const int off = s_bias[i].x - v0;
+            if (off >= 0 && off < E) {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (e == off) bias[e] += __int_as_float(s_bias[i].y);
+            }
+        }
+        __syncthreads();
+    }
+    if (!live) return;
+
+    const int32_t* dr = a.drafts + (static_cast<int64_t>(b) * a.K + k) * a.G;
+    auto count_token = [&](int tok) {
+        const int off = tok - v0;
+        if (tok >= 0 && off >= 0 && off < E) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (e == off) ++c[e];
+        }
+    };
+    auto settle = [&] {                             // what the counts come to
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (c[e] > 0) seen |= 1u << e;
+            add[e] = (bias[e] - freq * static_cast<float>(c[e])) - (c[e] > 0 ? pres : 0.0f);
+        }
+    };
+    for (int i = 0; i < j0; ++i) count_token(dr[i]);
+    settle();
+
+    const int64_t row0 = (static_cast<int64_t>(b) * a.K + k) * rows;
+    const int64_t nvec = a.V / E;
+    const uint4* in = static_cast<const uint4*>(a.logits);
+    uint4* out = static_cast<uint4*>(a.out) + row0 * nvec + v0 / E;
+    const int32_t* allow = a.allow ? a.allow + row0 * a.W + (v0 >> 5) : nullptr;
+
+    for (int j = j0; j < j1; j += kFlight) {
+        uint4 x[kFlight];
+        unsigned ok[kFlight];
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            if (j + u >= j1) break;
+            int64_t src = row0 + j + u;
+            bool good = true;
+            if (a.rows) {
+                const int r = __ldg(a.rows + row0 + j + u);
+                good = r >= 0 && r < a.nsrc;
+                src = static_cast<int64_t>(b) * a.nsrc + (good ? r : 0);
+                if (!good && a.status) atomicOr(a.status, kStatusBadLength);
+            }
+            ok[u] = allow ? static_cast<unsigned>(__ldg(allow + static_cast<int64_t>(j + u) * a.W)) >> (v0 & 31)
+                          : 0xffffffffu;
+            if (good)
+                x[u] = __ldcs(in + src * nvec + v0 / E);
+            else                                    // NaN in either type
+                x[u] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u), ok[u] = ~0u;
+        }
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            if (j + u >= j1) break;
+            float f[E];
+            const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                f[e] = BF16 ? ((e & 1) ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2])) : __uint_as_float(w[e % 4]);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (seen >> e & 1) f[e] = f[e] > 0.0f ? f[e] / rep : f[e] * rep;
+                f[e] += add[e];
+                if (!(ok[u] >> e & 1)) f[e] = -INFINITY;
+            }
+            uint32_t r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (BF16) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                    r[i] = *reinterpret_cast<const uint32_t*>(&h);
+                } else {
+                    r[i] = __float_as_uint(f[i]);
+                }
+            }
+            __stcs(out + static_cast<int64_t>(j + u) * nvec, make_uint4(r[0], r[1], r[2], r[3]));
+            if (j + u < a.G) {
+                const int tok = __ldg(dr + j + u);
+                if (tok >= v0 && tok < v0 + E) {
+                    count_token(tok);
+                    settle();
+                }
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(128) counts_kernel(const CountsArgs a) {
+    const int b = blockIdx.x;
+    const int sel = a.sel[b], acc = a.acc[b];
+    if (sel == -1) return;
+    if (sel < 0 || sel >= a.K || acc < 0 || acc > a.G) {
+        if (threadIdx.x == 0 && a.status) atomicOr(a.status, kStatusBadLength);
+        return;
+    }
+    for (int i = threadIdx.x; i <= acc; i += blockDim.x) {
+        const int tok = i < acc ? a.drafts[(static_cast<int64_t>(b) * a.K + sel) * a.G + i] : a.next[b];
+        if (tok >= 0 && tok < a.V)
+            atomicAdd(a.counts + static_cast<int64_t>(b) * a.V + tok, 1);   // whole numbers: any order
+        else if (a.status)
+            atomicOr(a.status, kStatusBadDraft);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_logits(const LogitsArgs& args, bool bf16, int nsm, cudaStream_t s) {
+    LogitsArgs a = args;
+    const int slice = kThreads * (bf16 ? 8 : 4);
+    const int64_t base = static_cast<int64_t>((a.V + slice - 1) / slice) * a.B * a.K;
+    // Few drafts: their rows are shared out until every SM has about eight CTAs,
+    // a CTA keeping four rows at least (its counts are then read for those).
+    int64_t split = (static_cast<int64_t>(nsm) * 8 + base - 1) / base;
+    const int64_t most = (a.G + kFlight) / kFlight;
+    a.row_splits = static_cast<int>(split < 1 ? 1 : split > most ? most : split);
+    const dim3 grid(static_cast<unsigned>(base), static_cast<unsigned>(a.row_splits));
+    if (bf16)
+        logits_kernel<true><<<grid, kThreads, 0, s>>>(a);
+    else
+        logits_kernel<false><<<grid, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_counts_commit(const CountsArgs& a, cudaStream_t s) {
+    counts_kernel<<<static_cast<unsigned>(a.B), 128, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace sdv

@@ -89,7 +89,10 @@ typedef enum {
                               /* than SDV_STATIC_SCRATCH_BYTES                   */
 } sdv_status;
 
-typedef enum { SDV_BF16 = 0, SDV_F32 = 1 } sdv_dtype;
+/* SDV_BF16 and SDV_F32 are the logit types of a verification step.  SDV_F16 is
+ * also a type of queries, keys and values, and SDV_E4M3 one of a cache's cells
+ * (see sdv_kv_cache). */
+typedef enum { SDV_BF16 = 0, SDV_F32 = 1, SDV_F16 = 2, SDV_E4M3 = 3 } sdv_dtype;
 
 /*
  * Create a context for batches of shape (B, K, gamma, V) on the current CUDA
@@ -452,6 +455,268 @@ sdv_status sdv_verify_static(int B, int K, int gamma, int V, sdv_dtype dtype, vo
                              const float* temperature_per_seq, uint64_t seed,
                              int32_t* out_sel, int32_t* out_accept_len,
                              int32_t* out_next_token);
+
+/* ------------------------------------------------------------------------
+ * The verifier's layer around a step: a tree of drafted tokens, rotary
+ * positions, a paged cache of keys and values, attention of the tree over that
+ * cache, and the sampling parameters of every draft position.
+ *
+ * "SpecDiff-2: Scaling Diffusion Drafter Alignment For Faster Speculative
+ * Decoding", appendix B.8: the K drafts are flattened into one tree, which the
+ * verifier scores in one forward pass with a branch-aware attention mask, the
+ * cache of the shared prefix being reused.  The page gives no layouts; those
+ * below are this library's.
+ *
+ * All entry points here are stateless: they check their arguments on the host
+ * (SDV_ERR_ARG: nothing was enqueued), allocate nothing, only enqueue on
+ * `stream`, and can be captured into a CUDA graph (after one uncaptured call of
+ * each shape).  Strides are in elements, and the innermost one is 1.  Data
+ * errors that only the device can see (a page id outside the cache, a length
+ * outside its limits) set bits of *status (device int32, which the caller
+ * clears; NULL: not reported); what such an entry does to the outputs is said
+ * at each call, and no memory outside the caller's buffers is touched.
+ * --------------------------------------------------------------------- */
+#define SDV_STATUS_BAD_TOKEN 1      /* a token id outside [0, V)                      */
+#define SDV_STATUS_TIMEOUT 8        /* a bounded device wait gave up                  */
+#define SDV_STATUS_BAD_PAGE 64      /* a page id outside [0, pages)                   */
+
+/*
+ * The tree of K drafts.  Node 0 is the sequence's last committed token (the
+ * root, whose key and value are not in the cache yet); the other nodes are the
+ * drafts' tokens, drafts that begin with the same tokens sharing their nodes.
+ * Nodes are numbered draft by draft, left to right, so a node's ancestors come
+ * before it.  N = 1 + K * gamma nodes have room.
+ *   root       device int32 [B]
+ *   drafts     device int32 [B][K][gamma]
+ *   draft_len  device int32 [B], 0 <= draft_len[b] <= gamma, or NULL (gamma)
+ * Outputs (device int32, caller-owned):
+ *   tokens     [B][N] token of each node (-1 past the sequence's nodes)
+ *   depth      [B][N] distance from the root (a node's position is the number
+ *              of committed tokens in the cache + depth); 0 past the nodes
+ *   mask       [B][N][ceil(N / 32)] bit m % 32 of word m / 32 of node i's row:
+ *              node m is i itself or one of its ancestors (rows past the
+ *              nodes are 0)
+ *   nodes      [B][K][gamma] node of draft k's token j (-1 for j >= draft_len)
+ *   rows       [B][K][gamma + 1] node whose logits are the verifier's row
+ *              (b, k, j): the root for j = 0, the node of token j - 1 else
+ *              (the root past the length)
+ *   count      [B] nodes of the tree
+ * A draft_len outside [0, gamma] gives that sequence the root alone and sets
+ * SDV_STATUS_BAD_LENGTH.  K <= 64, gamma <= 128.
+ */
+sdv_status sdv_tree_build(int B, int K, int gamma, void* stream, const int32_t* root,
+                          const int32_t* drafts, const int32_t* draft_len, int32_t* tokens,
+                          int32_t* depth, int32_t* mask, int32_t* nodes, int32_t* rows,
+                          int32_t* count, int32_t* status);
+
+/*
+ * Rotary frequencies, on the host: inv_freq[i] = base^(-2i / R) for i < R / 2
+ * (R even, 2 <= R <= 512; base > 0), scaled for contexts longer than the
+ * `original` length by `factor` >= 1:
+ *   SDV_ROPE_PLAIN   unchanged
+ *   SDV_ROPE_LINEAR  every frequency divided by factor (positions interpolated)
+ *   SDV_ROPE_BASE    base * factor^(R / (R - 2)) in the place of base (R >= 4)
+ *   SDV_ROPE_PARTS   frequencies that turn at least `fast` times within
+ *                    `original` positions stay, those that turn at most `slow`
+ *                    times are divided by factor, with a linear ramp over the
+ *                    number of turns between them (fast > slow >= 0,
+ *                    original >= 1); *attn_factor, which multiplies cosine and
+ *                    sine, is 0.1 ln(factor) + 1 (1 for the other kinds)
+ * Computed in 64 bits, rounded once.  attn_factor may be NULL.
+ */
+#define SDV_ROPE_PLAIN 0
+#define SDV_ROPE_LINEAR 1
+#define SDV_ROPE_BASE 2
+#define SDV_ROPE_PARTS 3
+sdv_status sdv_rope_freqs(int R, double base, int scaling, double factor, double original,
+                          double fast, double slow, float* inv_freq, float* attn_factor);
+
+/*
+ * Rotary positions for the queries [T][Hq][D] and keys [T][Hk][D] of T tokens.
+ * Pair i < R / 2 of token t's head, (x_i, x_{i + R/2}) or with `interleaved`
+ * (x_{2i}, x_{2i + 1}), turns by the angle positions[t] * inv_freq[i]:
+ *   (a, b) -> factor * (a cos - b sin, b cos + a sin)
+ * and elements R..D-1 are copied.  Angles are exact to about 2^-32 of a turn
+ * at any int32 position; arithmetic is fp32 with one rounding at the end.
+ *   dtype      SDV_BF16, SDV_F16 or SDV_F32
+ *   q_st, q_sh strides of a token and of a head (k_*, oq_*, ok_* alike)
+ *   k, out_k   NULL with Hk = 0: queries alone
+ *   out_q may be q with the same strides (in place), and out_k k; buffers that
+ *   overlap in any other way give undefined values
+ * 2 <= R <= D <= 4096, R even, R <= 512, T >= 0, 1 <= Hq + Hk <= 4096, Hq >= 1.
+ * positions and inv_freq are device arrays ([T] int32, [R / 2] float).
+ */
+sdv_status sdv_rope(int64_t T, int Hq, int Hk, int D, int R, int interleaved, sdv_dtype dtype,
+                    void* stream, const void* q, int64_t q_st, int64_t q_sh, const void* k,
+                    int64_t k_st, int64_t k_sh, const int32_t* positions, const float* inv_freq,
+                    float factor, void* out_q, int64_t oq_st, int64_t oq_sh, void* out_k,
+                    int64_t ok_st, int64_t ok_sh);
+
+/*
+ * A paged cache of one layer's keys and values.  k and v are
+ * [pages][kv_heads][page_size][head_dim] cells, each page contiguous and
+ * page_stride elements after the one before (so k and v may be the halves of
+ * one [pages][2][...] buffer); k and v 16-byte aligned, page_stride * cell size
+ * a multiple of 16 bytes.  Position t of sequence b is place t % page_size of
+ * page block_table[b][t / page_size].
+ *
+ * dtype SDV_BF16 or SDV_F16: cells hold the values; k_exp and v_exp are NULL.
+ * dtype SDV_E4M3: a cell row (one position, one head) is held in e4m3 in units
+ * of a power of two of its own, 2^(exp - 127), with exp in k_exp / v_exp,
+ * uint8 [pages][kv_heads][page_size], exp_page_stride after one another
+ * (a row holds the smallest power, no less than 2^-126, that brings its
+ * largest magnitude to at most 448; exp 255: the row is not a number).
+ * head_dim is a multiple of 16, at most 256; page_size >= 1.
+ */
+typedef struct sdv_kv_cache {
+    void* k;
+    void* v;
+    uint8_t* k_exp;
+    uint8_t* v_exp;
+    int64_t page_stride;
+    int64_t exp_page_stride;
+    int pages;
+    int page_size;
+    int kv_heads;
+    int head_dim;
+    sdv_dtype dtype;
+} sdv_kv_cache;
+
+/*
+ * Write the keys and values of up to N new positions per sequence: row n of
+ * sequence b goes to position start[b] + n, for n < count[b] (NULL: N).
+ *   k, v       device [B][N][kv_heads][D] of `dtype` (SDV_BF16 or SDV_F16; the
+ *              cache's dtype, unless that is SDV_E4M3), strides (sb, sn, sh)
+ *   block_table device int32 [B][max_pages]
+ *   start, count  device int32 [B]
+ * A value is rounded once, to nearest even, when the cache is e4m3; a row that
+ * holds a NaN or an infinity is then stored as not a number.  A position
+ * outside [0, max_pages * page_size) or a count outside [0, N] sets
+ * SDV_STATUS_BAD_LENGTH, a bad page SDV_STATUS_BAD_PAGE; those rows are not
+ * written (a bad count writes nothing of its sequence).  Two rows that go to
+ * one cell leave either.
+ */
+sdv_status sdv_kv_write(const sdv_kv_cache* cache, int B, int N, sdv_dtype dtype, void* stream,
+                        const void* k, int64_t k_sb, int64_t k_sn, int64_t k_sh, const void* v,
+                        int64_t v_sb, int64_t v_sn, int64_t v_sh, const int32_t* block_table,
+                        int max_pages, const int32_t* start, const int32_t* count,
+                        int32_t* status);
+
+/*
+ * Read positions start[b] .. start[b] + count[b] - 1 back into contiguous
+ * out_k, out_v [B][N][kv_heads][D] of `dtype` (as for sdv_kv_write); rows past
+ * count[b] become 0.  What an e4m3 row stands for is exact in bf16 (but for
+ * magnitudes below 2^-133) and rounded once to fp16 (overflow to infinity).
+ * Rows of a bad position, page or count become NaN, with the status bits of
+ * sdv_kv_write.  Outputs are 16-byte aligned.
+ */
+sdv_status sdv_kv_read(const sdv_kv_cache* cache, int B, int N, sdv_dtype dtype, void* stream,
+                       void* out_k, void* out_v, const int32_t* block_table, int max_pages,
+                       const int32_t* start, const int32_t* count, int32_t* status);
+
+/*
+ * After a verification step: keep the accepted path.  The tree's cells sit at
+ * positions start[b] + node; the cells of draft sel[b]'s accepted tokens move
+ * to start[b] + 1 + j, j < accept_len[b] (the root's are in place), from node
+ * nodes[b][sel[b]][j] (as sdv_tree_build numbers them: at least 1 and growing
+ * with j).  Cells are moved as they are, with their exponents.
+ *   out_len  device int32 [B] or NULL: start[b] + 1 + accept_len[b]
+ * A sequence with sel = -1 (a data error of the step), or whose accept_len,
+ * positions, nodes or pages are out of range (the status bits of sdv_kv_write;
+ * SDV_STATUS_BAD_LENGTH for the nodes), gets out_len = start[b]; cells moved
+ * before a bad one stay moved.  out_len may be the start array itself.
+ */
+sdv_status sdv_kv_commit(const sdv_kv_cache* cache, int B, int K, int gamma, void* stream,
+                         const int32_t* block_table, int max_pages, const int32_t* start,
+                         const int32_t* nodes, const int32_t* sel, const int32_t* accept_len,
+                         int32_t* out_len, int32_t* status);
+
+/*
+ * Attention of the nodes of a tree over the cache.  Sequence b has
+ * ctx_len[b] committed positions and count[b] <= N nodes (NULL: N) whose keys
+ * and values are at positions ctx_len[b] + m (sdv_kv_write).  Node i sees every
+ * committed position, and node m when bit m of its mask row is set (mask NULL:
+ * when m <= i, a causal chain; so N = 1 is the decode step of one token and
+ * ctx_len = 0 the first chunk of a prompt).  With s_j = scale * q_i . k_j over
+ * what it sees,
+ *   out_i = sum_j softmax(s)_j v_j      lse_i = ln sum_j e^{s_j}
+ * in fp32 sums; a node that sees nothing has out = 0, lse = -inf, and so have
+ * the nodes from count[b] on.
+ *   q      device [B][N][Hq][D] of `dtype` (SDV_BF16 or SDV_F16; the cache's
+ *          dtype, unless that is SDV_E4M3), strides (sb, sn, sh); Hq a multiple
+ *          of the cache's kv_heads, query head h reading kv head
+ *          h / (Hq / kv_heads)
+ *   mask   device int32, rows of ceil(N / 32) words, one row per node;
+ *          mask_sb words from one sequence's to the next (0: all have the same)
+ *   out    device [B][N][Hq][D] of `dtype`, contiguous, 16-byte aligned
+ *   lse    device float [B][N][Hq] contiguous, or NULL
+ *   workspace  device memory of at least sdv_tree_attn_workspace(...) bytes,
+ *          16-byte aligned, that no other call uses until this one is done
+ * Probabilities are rounded to 16 bits for their product with the values; all
+ * sums are fp32.  What a node does not see has no influence on it, whatever it
+ * holds; a NaN or an infinity that it does see makes its output not finite
+ * (which elements, and NaN or infinite, is not fixed).  A sequence whose
+ * ctx_len, count or ctx_len + count is out of range gets NaN in out and lse;
+ * the cells of a bad page count as not a number; both set the status bits of
+ * sdv_kv_write.
+ * sdv_tree_attn_workspace: bytes for calls of any shape on the current device
+ * (0: the device cannot be asked).
+ */
+size_t sdv_tree_attn_workspace(void);
+sdv_status sdv_tree_attn(const sdv_kv_cache* cache, int B, int N, int Hq, sdv_dtype dtype,
+                         void* stream, const void* q, int64_t q_sb, int64_t q_sn, int64_t q_sh,
+                         const int32_t* block_table, int max_pages, const int32_t* ctx_len,
+                         const int32_t* count, const int32_t* mask, int64_t mask_sb, float scale,
+                         void* out, float* lse, void* workspace, size_t workspace_bytes,
+                         int32_t* status);
+
+/*
+ * The sampling parameters of every draft position, before sdv_verify.  Row
+ * (b, k, j) of the verifier's logits follows the tokens of sequence b and the
+ * first j tokens of draft k, so its penalties count both:
+ *   c = counts[b][v] + #{i < j : drafts[b][k][i] = v}
+ *   x = the logit in fp32
+ *   x = x > 0 ? x / repetition[b] : x * repetition[b]   where c > 0 or v is in
+ *                                                       the prompt
+ *   x = x - frequency[b] * c - presence[b] * [c > 0] + sum of v's biases
+ *   x = -inf                                            where v is not allowed
+ * rounded once to the logits' type.
+ *   logits     device [B][K][gamma + 1][V], or with `rows`
+ *              [B][nsrc][V] (a tree's logits), 16-byte aligned
+ *   rows       device int32 [B][K][gamma + 1] source row within the sequence's
+ *              nsrc, or NULL (nsrc is then not used).  An id outside
+ *              [0, nsrc) sets SDV_STATUS_BAD_LENGTH and gives a row of NaN
+ *   drafts     device int32 [B][K][gamma] (ids outside [0, V) count nowhere)
+ *   counts     device int32 [B][V], 16-byte aligned, or NULL: 0
+ *   prompt     device int32 [B][ceil(V / 32)] bits (v % 32 of word v / 32), or
+ *              NULL: none
+ *   repetition, frequency, presence  device float [B], or NULL: 1, 0, 0
+ *   bias_ids, bias  device int32 / float [B][M] with M >= 0, or NULL with
+ *              M = 0; ids outside [0, V) are passed over, repeated ids add up
+ *              in their order
+ *   allow      device int32 [B][K][gamma + 1][ceil(V / 32)] bits, or NULL: all
+ *   out        device [B][K][gamma + 1][V] of the logits' type, 16-byte
+ *              aligned; without `rows` it may be logits itself
+ * dtype SDV_BF16 or SDV_F32; V * elt % 16 == 0.
+ */
+sdv_status sdv_logits_process(int B, int K, int gamma, int V, sdv_dtype dtype, void* stream,
+                              const void* logits, int nsrc, const int32_t* rows,
+                              const int32_t* drafts, const int32_t* counts, const int32_t* prompt,
+                              const float* repetition, const float* frequency,
+                              const float* presence, int M, const int32_t* bias_ids,
+                              const float* bias, const int32_t* allow, void* out,
+                              int32_t* status);
+
+/*
+ * After a verification step: add the committed tokens to counts [B][V], those
+ * of draft sel[b] at positions j < accept_len[b] and next_token[b].  A sequence
+ * with sel = -1 adds nothing; sel, accept_len or a token out of range sets
+ * SDV_STATUS_BAD_LENGTH / SDV_STATUS_BAD_TOKEN and that token (or for sel and
+ * accept_len the sequence) is not counted.
+ */
+sdv_status sdv_counts_commit(int B, int K, int gamma, int V, void* stream, const int32_t* drafts,
+                             const int32_t* sel, const int32_t* accept_len,
+                             const int32_t* next_token, int32_t* counts, int32_t* status);
 
 #ifdef __cplusplus
 }
