@@ -317,9 +317,48 @@ def test_attn_tree(B, K, G, Hq, Hk, D, ctx, dtype, cdtype):
         assert not out[b, count[b]:].any()
 
 
+# many query rows: row tiles of 256 in streams of 128, cut and whole units
+@pytest.mark.parametrize("dtype,cdtype", TYPES)
+@pytest.mark.parametrize("B,N,Hq,Hk,D,P,ctx", [
+    (1, 65, 1, 1, 128, 16, [0]), (1, 17, 8, 1, 64, 16, [5]), (2, 30, 8, 1, 128, 16, [200, 0]),
+    (1, 129, 1, 1, 128, 7, [300]), (1, 257, 2, 1, 16, 16, [127]), (2, 100, 6, 2, 96, 32, [129, 1]),
+    (1, 300, 3, 1, 48, 1, [513]), (3, 40, 10, 2, 80, 64, [0, 1000, 31]), (1, 70, 7, 1, 112, 16, [64])])
+def test_attn_many_rows(B, N, Hq, Hk, D, P, ctx, dtype, cdtype):
+    case = _attn_case(B, N, Hq, Hk, D, P, ctx, dtype, cdtype, seed=B + N + D, split=P == 16)
+    count = [N - 3 * b for b in range(B)]
+    _check_attn(*case, ctx, count=count)
+
+
+@pytest.mark.parametrize("dtype,cdtype", TYPES)
+@pytest.mark.parametrize("B,K,G,Hq,Hk,D,ctx", [(2, 8, 16, 4, 1, 128, [1, 250]), (1, 16, 16, 2, 1, 64, [0]),
+                                               (3, 4, 31, 6, 2, 96, [97, 3, 128])])
+def test_attn_large_tree(B, K, G, Hq, Hk, D, ctx, dtype, cdtype):
+    g = torch.Generator(device="cuda").manual_seed(K)
+    drafts = torch.randint(0, 4, (B, K, G), generator=g, device="cuda", dtype=torch.int32)
+    t = bd.sdv_tree_build(_i32([0] * B), drafts)
+    case = _attn_case(B, 1 + K * G, Hq, Hk, D, 16, ctx, dtype, cdtype, seed=G)
+    _check_attn(*case, ctx, count=t["count"].tolist(), mask=t["mask"])
+
+
+@pytest.mark.parametrize("dtype,cdtype", TYPES)
+def test_attn_growing_scores(dtype, cdtype):
+    """Scores that grow along the positions, so that the running maximum moves
+    at every tile, by little and by much."""
+    ctx, N, Hq, D = [700], 40, 4, 64
+    for slope in (0.01, 0.2):
+        q, kc, vc, ke, ve, table = _attn_case(1, N, Hq, 1, D, 16, ctx, dtype, cdtype, seed=12)
+        k, v = (torch.randn((1, 740, 1, D), device="cuda") for _ in range(2))
+        k[..., 0] = torch.arange(740, device="cuda").view(1, 740, 1) * slope
+        bd.sdv_kv_write(k.to(dtype), v.to(dtype), kc, vc, table, _i32([0]), k_exp=ke, v_exp=ve)
+        q = q.clone()
+        q[..., 0] = 8.0
+        _check_attn(q, kc, vc, ke, ve, table, ctx)
+
+
+@pytest.mark.parametrize("heads", [4, 12])
 @pytest.mark.parametrize("cdtype", [BF, F8])
-def test_attn_rows_that_see_nothing_and_what_is_not_seen(cdtype):
-    B, N, Hq, Hk, D, P = 3, 40, 4, 2, 64, 16
+def test_attn_rows_that_see_nothing_and_what_is_not_seen(cdtype, heads):
+    B, N, Hq, Hk, D, P = 3, 40, heads, 2, 64, 16
     ctx = [0, 0, 90]
     q, kc, vc, ke, ve, table = _attn_case(B, N, Hq, Hk, D, P, ctx, BF, cdtype, seed=9)
     count = [40, 0, 37]
@@ -370,26 +409,30 @@ def test_attn_zero_values_and_tiny_ones_in_e4m3():
     assert ((out.double() * 2.0 ** 100 - 1).abs() <= 2.0 ** -8).all()
 
 
-def test_attn_large_scores():
-    q, kc, vc, ke, ve, table = _attn_case(1, 5, 4, 2, 64, 16, [150], BF, BF, seed=8)
+@pytest.mark.parametrize("N", [5, 50])
+def test_attn_large_scores(N):
+    q, kc, vc, ke, ve, table = _attn_case(1, N, 4, 2, 64, 16, [150], BF, BF, seed=8)
     _check_attn(q * 30, kc, vc, ke, ve, table, [150], scale=4.0)
     _check_attn(q, kc, vc, ke, ve, table, [150], scale=0.0)
     _check_attn(q, kc, vc, ke, ve, table, [150], scale=-0.3)
 
 
-def test_attn_bad_lengths_and_pages():
-    q, kc, vc, ke, ve, table = _attn_case(4, 2, 4, 2, 64, 16, [50] * 4, BF, BF, seed=6)
+@pytest.mark.parametrize("N", [2, 60])
+@pytest.mark.parametrize("cdtype", [BF, F8])
+def test_attn_bad_lengths_and_pages(N, cdtype):
+    q, kc, vc, ke, ve, table = _attn_case(4, N, 4, 2, 64, 16, [50] * 4, BF, cdtype, seed=6)
     st = _status()
-    good = bd.sdv_tree_attn(q, kc, vc, table, _i32([50] * 4))
-    out, lse = bd.sdv_tree_attn(q, kc, vc, table, _i32([50, -1, 50, 10 ** 6]), count=_i32([2, 2, 3, 2]), lse=True,
-                                status=st)
+    kw = {"k_exp": ke, "v_exp": ve}
+    good = bd.sdv_tree_attn(q, kc, vc, table, _i32([50] * 4), **kw)
+    out, lse = bd.sdv_tree_attn(q, kc, vc, table, _i32([50, -1, 50, 10 ** 6]), count=_i32([N, N, N + 1, N]),
+                                lse=True, status=st, **kw)
     assert int(st) == bd.SDV_STATUS_BAD_LENGTH
     assert out[1:].isnan().all() and lse[1:].isnan().all() and torch.equal(out[0], good[0])
     st.zero_()
     bad = table.clone()
     bad[2, 1] = 10 ** 6
     bad[3, 0] = -5
-    out = bd.sdv_tree_attn(q, kc, vc, bad, _i32([50] * 4), status=st)
+    out = bd.sdv_tree_attn(q, kc, vc, bad, _i32([50] * 4), status=st, **kw)
     assert int(st) == bd.SDV_STATUS_BAD_PAGE
     assert out[2:].isnan().all() and torch.equal(out[:2], good[:2])
 
