@@ -7,7 +7,8 @@
 // the softmax of one stream runs, the tensor cores multiply for the other:
 //   S_s = Q_s K^T        both operands in shared memory, accumulator in TMEM
 //   P_s = 2^(c S_s - m)  a thread per row reads S_s from TMEM and writes P_s,
-//                        16 bits wide, over S_s
+//                        16 bits wide, over S_s (each half of
+//                        the columns over the half it comes from)
 //   O_s += P_s V         P_s from TMEM, V from shared memory, O_s in TMEM
 // TMEM holds S_0, S_1, O_0, O_1: 4 x 128 columns, all 512.
 //
@@ -15,12 +16,15 @@
 // moves when a row's scores pass it by 2^8 (fp32 sums and 16-bit probabilities
 // keep their relative precision below that), and then the row's warp rescales.
 //
-// Warps 0-3 and 4-7: softmax of stream 0 and 1; 8-11: loads; 12: one thread
-// that issues the products.  Keys and values have two slots each in shared
-// memory, rows of 128 bytes in the 128-byte swizzle, [D / 64][128 rows]: the K
-// operand is read K-major, and V, whose contraction index is the row, MN-major.
-// Rows come from pages of any size, so they are brought by 16-byte asynchronous
-// copies rather than by tile copies.
+// Warps 0-3 and 4-7: softmax of stream 0 and 1; 8-10: loads; 11: one thread
+// that issues the products.  Tiles of 128 positions, keys and values in turn,
+// go through a ring of slots in shared memory, as rows of 128 bytes in the
+// 128-byte swizzle, [D / 64][128 rows]: the K operand is read K-major, and V,
+// whose contraction index is the row, MN-major.  Rows come from pages of any
+// size, so they are brought by 16-byte asynchronous copies rather than by tile
+// copies.  e4m3 rows are copied as they are into a second pair of tiles, and the
+// thread that copied a chunk brings it to the queries' type (times its row's
+// power of two) on its way to the ring.
 //
 // Every wait is bounded: a wait that gives up marks the CTA dead, after which
 // no wait waits, no product is issued, and every row that is still written is
@@ -32,36 +36,46 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 416;
+constexpr int kThreads = 384;
 constexpr int kRows = 128;               // rows of a stream
 constexpr int MT = 2 * kRows, BN = 128;
 constexpr int kBlock = BN * 128;         // bytes of 128 rows of 64 16-bit cells
 constexpr int kTile = 2 * kBlock;        // ... of 128
+constexpr int kLoadWarps = 3, kLoadThreads = 32 * kLoadWarps;
 constexpr uint32_t kPolls = 1u << 22;
 constexpr float kSlack = 8.0f;           // how far (log2) scores may pass the reference
 
 // Shared memory, bytes from its 1024-aligned start.
-constexpr int kOffK = 0, kOffV = 2 * kTile, kOffQ = 4 * kTile;
-constexpr int kOffRow = kOffQ + 2 * kTile;              // int64 [2][BN] byte offset of a row (-1: zeros)
-constexpr int kOffFlag = kOffRow + 2 * BN * 8;          // uint32 [2][4] values that are not numbers
-constexpr int kOffBar = kOffFlag + 2 * 4 * 4;
-constexpr int kBars = 18;
-constexpr int kSmem = kOffBar + kBars * 8 + 1024;
+template <bool E4> struct Smem {
+    static constexpr int kSlots = E4 ? 4 : 5;
+    static constexpr int q = kSlots * kTile;
+    static constexpr int stage = q + 2 * kTile;                 // two e4m3 tiles as they come
+    static constexpr int row = stage + (E4 ? 2 * BN * 128 : 0); // int64 [BN] byte offset of a row (-1: zeros)
+    static constexpr int exps = row + BN * 8;                   // bytes [2 tiles][keys, values][BN]
+    static constexpr int flag = exps + (E4 ? 4 * BN : 0);       // uint32 [4 tiles][3 warps][4] values that are not numbers
+    static constexpr int bar = flag + 4 * kLoadWarps * 4 * 4;
+    static constexpr int word = bar + (2 * kSlots + 9) * 8;     // TMEM address, dead
+    static constexpr int bytes = word + 8 + 1024;
+};
+static_assert(Smem<true>::bytes <= 227 * 1024 && Smem<false>::bytes <= 227 * 1024, "one CTA per SM");
 
-enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kSFull = 10, kPFull = 12, kOFull = 14, kEnd = 16 };
+// Barriers: two per stream of each kind, one for the end, then the ring's.
+enum Bar { kQFull = 0, kSFull = 2, kPFull = 4, kOFull = 6, kEnd = 8, kRing = 9 };
 
 struct Sync {
     uint64_t* bar;
     volatile int* dead;
     unsigned* status;
+    __device__ __forceinline__ bool poll(int i, uint32_t parity) const {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done) : "r"(smem_u32(bar + i)), "r"(parity) : "memory");
+        return done != 0;
+    }
     __device__ __forceinline__ void wait(int i, uint32_t parity) const {
-        const uint32_t addr = smem_u32(bar + i);
         for (uint32_t n = 0; n < kPolls; ++n) {
-            uint32_t done;
-            asm volatile(
-                "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                : "=r"(done) : "r"(addr), "r"(parity) : "memory");
-            if (done) return;
+            if (poll(i, parity)) return;
             if (*dead) return;
         }
         *dead = 1;
@@ -80,127 +94,187 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
-// 32 columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld32(float (&x)[32], uint32_t addr) {
+#define SDV_R4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
+#define SDV_R16(r, i) SDV_R4(r, i), SDV_R4(r, i + 4), SDV_R4(r, i + 8), SDV_R4(r, i + 12)
+#define SDV_I4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
+#define SDV_I16(r, i) SDV_I4(r, i), SDV_I4(r, i + 4), SDV_I4(r, i + 8), SDV_I4(r, i + 12)
+
+// 64 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld64(float* x, uint32_t addr) {
     uint32_t* r = reinterpret_cast<uint32_t*>(x);
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr) : "memory");
+        : SDV_R16(r, 0), SDV_R16(r, 16), SDV_R16(r, 32), SDV_R16(r, 48) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(float (&x)[16], uint32_t addr) {
     uint32_t* r = reinterpret_cast<uint32_t*>(x);
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr) : "memory");
+        : SDV_R16(r, 0) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const float (&x)[32]) {
-    const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
         "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]) : "memory");
+        SDV_I16(r, 0), SDV_I16(r, 16) : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const float (&x)[16]) {
+    const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+        SDV_I16(r, 0) : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Shared-memory operand: 128-byte swizzle, `lbo` / `sbo` bytes between 64-cell
-// column blocks (MN-major) and between groups of eight rows.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-           (static_cast<uint64_t>(sbo >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+// Shared-memory operand: 128-byte swizzle, `lbo` bytes between 64-cell column
+// blocks (MN-major), 1024 between groups of eight rows.  Moving it by a number
+// of bytes adds a sixteenth of them to the low word.
+__device__ __forceinline__ uint32_t operand_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
+constexpr uint32_t kOperandHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t x, uint32_t y, uint32_t idesc, uint32_t add) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(x), "r"(y), "r"(idesc), "r"(add),
+                 "r"(kOperandHi) : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t x, uint64_t y, uint32_t idesc, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(x), "l"(y), "r"(idesc),
-                 "r"(static_cast<uint32_t>(add)) : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t x, uint32_t y, uint32_t idesc, uint32_t add) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(x), "r"(y), "r"(idesc), "r"(add),
+                 "r"(kOperandHi) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t x, uint64_t y, uint32_t idesc, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(x), "l"(y), "r"(idesc),
-                 "r"(static_cast<uint32_t>(add)) : "memory");
+
+// Two fp32 operations at once.
+struct F2 { float x, y; };
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // Byte offset of 16-byte chunk c of row r in a tile.
 __device__ __forceinline__ int chunk_at(int r, int c) { return (c >> 3) * kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
 
-// Which of the 32 positions from pos0 on a live row sees, as bits.
-__device__ __forceinline__ uint32_t sees(const AttnArgs& a, const Unit& u, int node, const int32_t* row, int pos0) {
-    const int base = pos0 - u.cut.ctx;               // node of the first one
-    if (base + 32 <= 0) return 0xffffffffu;
+// The mask words that hold nodes base .. base + 127 of a row.
+__device__ __forceinline__ void mask_words(const AttnArgs& a, const int32_t* row, int base, uint32_t (&w)[5]) {
+    const int w0 = base >> 5;                        // floor
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+        w[i] = w0 + i < 0 ? 0xffffffffu : w0 + i < a.W ? static_cast<uint32_t>(__ldg(row + w0 + i)) : 0u;
+}
+
+// Which of the positions pos0 + 32 i .. + 31 a live row sees, as bits: all
+// committed ones (word 0xffffffff before the mask's first), then its mask's.
+__device__ __forceinline__ uint32_t sees(const Unit& u, bool tree, int node, const uint32_t (&w)[5], int pos0, int i) {
+    const int base = pos0 - u.cut.ctx, b = base + 32 * i;
     uint32_t bits;
-    if (!row) {
-        const int n = node - base + 1;
-        bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-    } else if (base < 0) {
-        bits = (static_cast<uint32_t>(__ldg(row)) << -base) | ((1u << -base) - 1u);
+    if (tree) {
+        bits = __funnelshift_r(w[i], w[i + 1], base & 31);
     } else {
-        const int w = base >> 5;
-        const uint32_t lo = w < a.W ? static_cast<uint32_t>(__ldg(row + w)) : 0u;
-        const uint32_t hi = w + 1 < a.W ? static_cast<uint32_t>(__ldg(row + w + 1)) : 0u;
-        bits = __funnelshift_r(lo, hi, base & 31);
+        const int n = node - b + 1;
+        bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
     }
-    const int left = u.cut.cnt - base;               // nodes from the first one on
+    const int left = u.cut.cnt - b;                  // nodes from the first position on
     if (left < 32) bits &= left <= 0 ? 0u : (1u << left) - 1u;
     return bits;
 }
 
-template <bool F16>
+// Sixteen e4m3 cells times 2^(e - 127), in the queries' type.
+template <bool F16> __device__ __forceinline__ void widen16(const uint4& raw, int e, uint32_t (&o)[8]) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    // a cell that is not a number takes its chunk with it
+    uint32_t bad = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    if (bad) e = 255;
+    if constexpr (F16) {
+        // 2^(e - 127) as the product of two fp16 powers (its range is smaller)
+        int h = e - 127;
+        h = h < -40 ? -40 : h > 24 ? 24 : h;
+        const int h1 = h / 2, h2 = h - h1;
+        uint32_t s1 = static_cast<uint32_t>(h1 + 15) << 10, s2 = static_cast<uint32_t>(h2 + 15) << 10;
+        if (h1 < -14) s1 = 0x0400u >> (-14 - h1);
+        if (h2 < -14) s2 = 0x0400u >> (-14 - h2);
+        if (e == 255) s1 = 0x7e00u;
+        s1 |= s1 << 16, s2 |= s2 << 16;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 t;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 t, lo;\n\t"
+                "mul.rn.f16x2 t, t, %2;\n\tmul.rn.f16x2 %0, t, %3;\n\t}"
+                : "=r"(o[i]) : "r"(w[i / 2] >> (16 * (i % 2))), "r"(s1), "r"(s2));
+        }
+    } else {
+        // the cell's exponent and digits in bf16's places are its value times 2^-120
+        uint32_t s = e == 255 ? 0x7fc0u : e == 0 ? 0x0040u : static_cast<uint32_t>(e) << 7;
+        s |= s << 16;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t t = __byte_perm(w[i / 2], 0, i % 2 ? 0x3424 : 0x1404);    // the bytes on top of 16 bits
+            const uint32_t v = (t & 0x80008000u) | ((t >> 4) & 0x07f007f0u);
+            asm("{\n\t.reg .b32 t;\n\tmul.rn.bf16x2 t, %1, %2;\n\tmul.rn.bf16x2 %0, t, %3;\n\t}"
+                : "=r"(o[i]) : "r"(v), "r"(0x7b807b80u), "r"(s));
+        }
+    }
+}
+
+template <bool E4, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) {
+    using M = Smem<E4>;
+    constexpr uint32_t S = M::kSlots;
+    constexpr int kFull = kRing, kEmpty = kRing + M::kSlots;
     extern __shared__ unsigned char raw[];
     unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    int64_t* s_row = reinterpret_cast<int64_t*>(smem + kOffRow);
-    uint32_t* s_flag = reinterpret_cast<uint32_t*>(smem + kOffFlag);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
-    __shared__ int64_t s_part[40];
-    __shared__ uint32_t s_tmem;
-    __shared__ int s_dead;
+    int64_t* s_row = reinterpret_cast<int64_t*>(smem + M::row);
+    uint32_t* s_flag = reinterpret_cast<uint32_t*>(smem + M::flag);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::bar);
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::word);
+    volatile int* s_dead = reinterpret_cast<volatile int*>(smem + M::word + 4);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int mts = (a.N * a.g + MT - 1) / MT;
     const int D = a.c.D;
-    const Sync sync{bars, &s_dead, a.status};
+    const Sync sync{bars, s_dead, a.status};
     if (tid == 0) {
-        s_dead = 0;
+        *s_dead = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bars + kKFull + i, 4);
-            mbar_init(bars + kKEmpty + i, 1);
-            mbar_init(bars + kVFull + i, 4);
-            mbar_init(bars + kVEmpty + i, 1);
             mbar_init(bars + kQFull + i, kRows);
             mbar_init(bars + kSFull + i, 1);
             mbar_init(bars + kPFull + i, kRows);
             mbar_init(bars + kOFull + i, 1);
         }
         mbar_init(bars + kEnd, 1);
+        for (int i = 0; i < M::kSlots; ++i) {
+            mbar_init(bars + kFull + i, kLoadWarps);
+            mbar_init(bars + kEmpty + i, 1);
+        }
         a.desc[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
     }
-    if (tid < 8) s_flag[tid] = 0;
-    if (warp == 12) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+    if (warp == 11) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(s_tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    const Part part = find_part<MT, BN, kThreads>(a, mts, s_part);      // holds barriers of the CTA
+    // the ring is not in use yet: its first bytes serve the search
+    const Part part = find_part<MT, BN, kThreads>(a, mts, reinterpret_cast<int64_t*>(smem));
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = *s_tmem;
     Walk<MT, BN> walk;
     walk.start(a, part, mts);
     Unit u;
@@ -210,7 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
         const int st = warp >> 2, r = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + st * 128, tO = tmem + lanes + 256 + st * 128;
-        const float c = fabsf(a.scale_log2);
+        // a negative scale turns the queries round; c > 0 so that -inf stays -inf
+        const float c = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
         const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
         uint32_t n = 0;                              // tiles of this stream so far
         uint32_t nv = 0;                             // tiles of the CTA so far
@@ -227,29 +302,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
             float m = -INFINITY, l = 0.0f;
             bool nan_row = false;
             if (run) {
-                unsigned char* qs = smem + kOffQ + st * kTile;
+                unsigned char* qs = smem + M::q + st * kTile;
                 const unsigned char* p = a.q + u.b * a.q_sb + node * a.q_sn +
                                          (static_cast<int64_t>(u.h) * a.g + row % a.g) * a.q_sh;
-                const bool aligned = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
-                for (int ch = 0; ch < D / 8; ++ch) {
-                    uint32_t v[4] = {0, 0, 0, 0};
-                    if (live && aligned) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(p + ch * 16);
-                        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-                    } else if (live) {
-                        const unsigned short* hp = reinterpret_cast<const unsigned short*>(p + ch * 16);
+                if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D / 8; c0 += 8) {
+                        uint4 v[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = hp[2 * i] | (static_cast<uint32_t>(hp[2 * i + 1]) << 16);
+                        for (int i = 0; i < 8; ++i)
+                            v[i] = live && c0 + i < D / 8 ? *reinterpret_cast<const uint4*>(p + (c0 + i) * 16) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4*>(qs + chunk_at(r, c0 + i)) =
+                                make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
                     }
-                    *reinterpret_cast<uint4*>(qs + chunk_at(r, ch)) = make_uint4(v[0] ^ flip, v[1] ^ flip, v[2] ^ flip, v[3] ^ flip);
+                } else {
+                    for (int i = 0; i < D; ++i)
+                        *reinterpret_cast<unsigned short*>(qs + chunk_at(r, i >> 3) + (i & 7) * 2) =
+                            live ? reinterpret_cast<const unsigned short*>(p)[i] ^ static_cast<unsigned short>(flip) : 0;
                 }
                 fence_async();
                 sync.arrive(kQFull + st);
                 // pages that are not the cache's: looked for once, a slow path if there are any
                 const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
-                const int pos_end = min(u.t1 * BN, u.len);
+                const int last_page = (min(u.t1 * BN, u.len) - 1) / a.c.P;
                 int bad = 0;
-                for (int pg = u.t0 * BN / a.c.P + r; pg <= (pos_end - 1) / a.c.P; pg += kRows) {
+                for (int pg = u.t0 * BN / a.c.P + r; pg <= last_page; pg += kRows) {
                     const int x = __ldg(table + pg);
                     bad |= x < 0 || x >= a.c.pages;
                 }
@@ -257,50 +336,63 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
                 asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.red.or.pred q, %2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
                              : "=r"(any_bad) : "r"(bad), "r"(2 + st) : "memory");
                 if (any_bad && r == 0 && a.status) atomicOr(a.status, kStatusBadPage);
-                const int32_t* mrow = a.mask && live ? a.mask + u.b * a.mask_sb + static_cast<int64_t>(node) * a.W : nullptr;
+                const int32_t* mrow = a.mask ? a.mask + u.b * a.mask_sb + static_cast<int64_t>(live ? node : 0) * a.W : nullptr;
+                uint32_t words[5];
+                // tiles from first_mixed on hold nodes, which some rows see and some do not
+                const int first_mixed = max(u.cut.ctx / BN - u.t0, 0);
+                if (mrow && first_mixed == 0) mask_words(a, mrow, u.t0 * BN - u.cut.ctx, words);
 
                 for (int t = 0; t < nt; ++t, ++n) {
                     const int pos0 = (u.t0 + t) * BN;
-                    const bool mixed = pos0 + BN > u.cut.ctx;       // some rows see a column and some do not
-                    uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-                    if (mixed) {
-                        sync.wait(kVFull + ((nv + t) & 1), (nv + t) >> 1 & 1);
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            see[i] = live ? sees(a, u, node, mrow, pos0 + 32 * i) : 0u;
-                            if (see[i] & s_flag[((nv + t) & 1) * 4 + i]) nan_row = true;
-                        }
-                    }
-                    if (any_bad) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            for (int y = 0; y < 32; ++y) {
-                                const int pos = pos0 + 32 * i + y;
-                                if (pos >= u.len || !(see[i] >> y & 1)) continue;
-                                const int pg = __ldg(table + pos / a.c.P);
-                                nan_row |= pg < 0 || pg >= a.c.pages;
-                            }
-                    }
+                    const bool mixed = t >= first_mixed;
                     sync.wait(kSFull + st, n & 1);
                     __syncwarp();
                     fence_after();
-                    float x[32];
-                    float top = -INFINITY;
+                    // the maximum over both halves of the columns; the second half stays
+                    // in registers, the first is read again
+                    float x[64];
+                    uint32_t see[4];
+                    if (mixed) {
+                        const uint32_t step = 2 * (nv + t) + 1;     // the values' place in the ring
+                        sync.wait(kFull + step % S, step / S & 1);
+                        __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        tmem_ld32(x, tS + 32 * i);
-                        if (mixed) {
-#pragma unroll
-                            for (int y = 0; y < 32; ++y)
-                                if (see[i] >> y & 1) top = fmaxf(top, x[y]);
-                        } else {
-                            float t4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                            for (int y = 4; y < 32; ++y) t4[y & 3] = fmaxf(t4[y & 3], x[y]);
-                            top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
+                        for (int i = 0; i < 4; ++i) {
+                            see[i] = live ? sees(u, mrow != nullptr, node, words, pos0, i) : 0u;
+                            const uint32_t* f = s_flag + ((nv + t) & 3) * (kLoadWarps * 4) + i;
+                            if (see[i] & (f[0] | f[4] | f[8])) nan_row = true;
+                            if (any_bad)
+                                for (int y = 0; y < 32; ++y) {
+                                    const int pos = pos0 + 32 * i + y;
+                                    if (pos >= u.len || !(see[i] >> y & 1)) continue;
+                                    const int pg = __ldg(table + pos / a.c.P);
+                                    nan_row |= pg < 0 || pg >= a.c.pages;
+                                }
+                        }
+                        __syncwarp();
+                    } else if (any_bad) {
+                        for (int pg = pos0 / a.c.P; pg <= (pos0 + BN - 1) / a.c.P; ++pg) {
+                            const int q = __ldg(table + pg);
+                            nan_row |= q < 0 || q >= a.c.pages;
                         }
                     }
+                    auto hide = [&](int h) {         // what the row does not see of half h
+                        if (mixed)
+#pragma unroll
+                            for (int y = 0; y < 64; ++y)
+                                x[y] = see[2 * h + (y >> 5)] >> (y & 31) & 1 ? x[y] : -INFINITY;
+                    };
+                    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        tmem_ld64(x, tS + 64 * h);
+                        hide(h);
+#pragma unroll
+                        for (int y = 0; y < 64; y += 8)
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) t4[z] = max3(t4[z], x[y + z], x[y + 4 + z]);
+                    }
+                    float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                     top = top == -INFINITY ? top : top * c;
                     // the reference moves when the scores pass it by far
                     const bool move = top > m + kSlack || (m == -INFINITY && top != -INFINITY);
@@ -310,40 +402,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
                         __syncwarp();
                         fence_after();
                         l *= by;
-                        for (int i = 0; i < D; i += 32) {           // columns past D hold nothing of use
-                            float o[32];
-                            tmem_ld32(o, tO + i);
+                        for (int i = 0; i < D; i += 16) {
+                            float o[16];
+                            tmem_ld16(o, tO + i);
 #pragma unroll
-                            for (int y = 0; y < 32; ++y) o[y] *= by;
-                            tmem_st32(tO + i, o);
+                            for (int y = 0; y < 16; ++y) o[y] *= by;
+                            tmem_st16(tO + i, o);
                         }
-                        tmem_wait_st();
                     }
                     if (move) m = top;
-                    const float sub = m == -INFINITY ? 0.0f : m;
+                    const float sub = m == -INFINITY ? 0.0f : -m;
+                    const F2 c2{c, c}, sub2{sub, sub};
+                    F2 s0{0.0f, 0.0f}, s1{0.0f, 0.0f};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        tmem_ld32(x, tS + 32 * i);
-                        uint32_t p2[16];
-                        float sum0 = 0.0f, sum1 = 0.0f;
-                        if (mixed) {
-#pragma unroll
-                            for (int y = 0; y < 32; ++y) x[y] = see[i] >> y & 1 ? ex2(fmaf(x[y], c, -sub)) : 0.0f;
-                        } else {
-#pragma unroll
-                            for (int y = 0; y < 32; ++y) x[y] = ex2(fmaf(x[y], c, -sub));
+                    for (int h = 1; h >= 0; --h) {
+                        if (h == 0) {
+                            tmem_ld64(x, tS);
+                            hide(0);
                         }
+                        uint32_t p2[32];
 #pragma unroll
-                        for (int y = 0; y < 16; ++y) {
-                            sum0 += x[2 * y], sum1 += x[2 * y + 1];
-                            p2[y] = pack2<F16>(x[2 * y], x[2 * y + 1]);
+                        for (int y = 0; y < 32; y += 2) {
+                            F2 v = fma2(F2{x[2 * y], x[2 * y + 1]}, c2, sub2);
+                            F2 w = fma2(F2{x[2 * y + 2], x[2 * y + 3]}, c2, sub2);
+                            v.x = ex2(v.x), v.y = ex2(v.y), w.x = ex2(w.x), w.y = ex2(w.y);
+                            s0 = add2(s0, v), s1 = add2(s1, w);
+                            p2[y] = pack2<F16>(v.x, v.y);
+                            p2[y + 1] = pack2<F16>(w.x, w.y);
                         }
-                        l += sum0 + sum1;
-                        tmem_st16(tS + 16 * i, p2);                  // over columns that have been read
+                        tmem_st32(tS + 64 * h, p2);          // over columns that have been read
                     }
+                    l += (s0.x + s0.y) + (s1.x + s1.y);
                     tmem_wait_st();
                     fence_before();
                     sync.arrive(kPFull + st);
+                    if (mrow && t + 1 >= first_mixed && t + 1 < nt) mask_words(a, mrow, pos0 + BN - u.cut.ctx, words);
                 }
                 sync.wait(kOFull + st, (n - 1) & 1);
                 __syncwarp();
@@ -389,105 +482,170 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
             __syncwarp();
             fence_before();
         }
-    } else if (warp < 12) {
+    } else if (warp < 11) {
         // ---------------- loads ----------------
-        const int p = tid - 256;                     // row of a tile, and thread of the copies
-        const int CH = D / 8;                        // 16-byte chunks of a row
-        uint32_t tiles = 0;                          // tiles of the CTA so far
-        const int pr = p / 16, pc = p % 16;          // chunk pc of rows pr, pr + 8, ...
-        // what the copies under way hold, for when they are in: is it V, its slot,
-        // and the first row that some rows do not see
-        bool pend_v = false;
-        int pend_slot = 0, pend_from = BN;
-        bool pending = false;
-        auto settle = [&]() {                        // the pending copies are in: look at them, hand them over
-            if (!pending) return;
-            if (pend_v && pend_from < BN) {          // values that are not numbers are kept out of the products
-                for (int i = 0; i < BN / 8; ++i) {
-                    const int r = pr + 8 * i;
-                    unsigned char* at = smem + kOffV + pend_slot * kTile + chunk_at(r, pc);
+        const int p = tid - 256, w = warp - 8;
+        const int cells = E4 ? 16 : 8;               // of a 16-byte chunk
+        const int CH = D / cells;                    // chunks of a row
+        const int LR = CH > 8 ? 16 : CH > 4 ? 8 : 4; // lanes of a row
+        const int RP = 32 / LR, lr = lane / LR, lc = lane % LR;     // rows of a warp's step
+        const bool copies = lc < CH;
+        constexpr uint32_t kPending = E4 ? 2 : 3;    // steps under way at most
+        uint32_t tiles = 0, slot = 0, phase = 0;     // the ring's next slot
+        uint32_t staged = 0;                         // e4m3: steps begun
+        // steps under way, the oldest first: slot, values or keys, tile, first
+        // row that some queries do not see
+        uint32_t pend[3] = {0, 0, 0}, pending = 0;
+        auto settle = [&]() {                        // the oldest step is in: finish it and hand it over
+            if (pending == 3)
+                asm volatile("cp.async.wait_group 2;" ::: "memory");
+            else if (pending == 2)
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            const uint32_t d = pend[0];
+            const int sl = d & 15, isv = d >> 4 & 1, tile = d >> 5 & 3, from = d >> 8;
+            unsigned char* base = smem + sl * kTile;
+            uint32_t* flags = s_flag + tile * (kLoadWarps * 4) + w * 4;
+            const bool check = isv && from < BN;     // values that are not numbers are kept out of the products
+            if (check) {
+                if (lane < 4) flags[lane] = 0;
+                __syncwarp();
+            }
+            if (E4 || check) {
+                const unsigned char* stage = smem + M::stage + ((staged - pending) & 1) * (BN * 128);
+                const unsigned char* ex = smem + M::exps + ((tile & 1) * 2 + isv) * BN;
+                for (int q = w; q < BN / RP; q += kLoadWarps) {
+                    const int r = q * RP + lr;
+                    uint32_t o[8];
                     bool bad = false;
-                    if (r >= pend_from && pc < CH) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(at);
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                        constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
+                    constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
+                    if (copies) {
+                        if constexpr (E4) {
+                            widen16<F16>(*reinterpret_cast<const uint4*>(stage + r * 128 + ((lc ^ (r & 7)) << 4)), ex[r], o);
+                        } else {
+                            const uint4 v = *reinterpret_cast<const uint4*>(base + chunk_at(r, lc));
+                            o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+                        }
+                        if (check && r >= from)
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) bad |= (w[y] & top) == top || (w[y] >> 16 & top) == top;
+                            for (int i = 0; i < (E4 ? 8 : 4); ++i)
+                                bad |= (o[i] & top) == top || (o[i] >> 16 & top) == top;
                     }
-                    const uint32_t who = __ballot_sync(0xffffffffu, bad) & (0xffffu << (lane & 16));
-                    if (who) {
-                        if (pc < CH) *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
-                        if (pc == 0) atomicOr(s_flag + pend_slot * 4 + (r >> 5), 1u << (r & 31));
+                    bool row_bad = false;
+                    if (check) {
+                        const uint32_t group = (LR == 32 ? 0xffffffffu : (1u << LR) - 1u) << (lr * LR);
+                        row_bad = (__ballot_sync(0xffffffffu, bad) & group) != 0;
+                        if (row_bad && lc == 0) atomicOr(flags + (r >> 5), 1u << (r & 31));
+                    }
+                    if (E4 ? copies : copies && row_bad) {
+#pragma unroll
+                        for (int i = 0; i < (E4 ? 8 : 4); i += 4)
+                            *reinterpret_cast<uint4*>(base + chunk_at(r, E4 ? 2 * lc + i / 4 : lc)) =
+                                row_bad ? make_uint4(0, 0, 0, 0) : make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                     }
                 }
             }
             fence_async();
             __syncwarp();
-            if (lane == 0) sync.arrive((pend_v ? kVFull : kKFull) + pend_slot);
-            pending = false;
+            if (lane == 0) sync.arrive(kFull + sl);
+            pend[0] = pend[1], pend[1] = pend[2];
+            --pending;
         };
         while (walk.next(a, part, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
             const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
-            auto fetch = [&](int t) {
-                const int pos = (u.t0 + t) * BN + p;
-                return t < nt && pos < u.len ? __ldg(table + pos / a.c.P) : -1;
+            // a thread looks after rows p and p + 96 of a tile: the page of the
+            // row is read two tiles ahead, and its exponents one tile ahead
+            auto page_at = [&](int t, int i) {
+                const int rr = p + i * kLoadThreads, pos = (u.t0 + t) * BN + rr;
+                return rr < BN && t < nt && pos < u.len ? __ldg(table + pos / a.c.P) : -1;
             };
-            int page = fetch(0);
+            auto cell_at = [&](int t, int i) {       // row within its page
+                return static_cast<int64_t>(u.h) * a.c.P + ((u.t0 + t) * BN + p + i * kLoadThreads) % a.c.P;
+            };
+            int page[2][2], ke[2] = {127, 127}, ve[2] = {127, 127};
+            auto exps_at = [&](int t, int i, int pg) {
+                ke[i] = ve[i] = 127;
+                if (pg >= 0 && pg < a.c.pages) {
+                    const int64_t o = pg * a.c.exp_page_stride + cell_at(t, i);
+                    ke[i] = a.c.ke[o];
+                    ve[i] = a.c.ve[o];
+                }
+            };
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                page[0][i] = page_at(0, i);
+                page[1][i] = page_at(1, i);
+                if constexpr (E4) exps_at(0, i, page[0][i]);
+            }
             for (int t = 0; t < nt; ++t, ++tiles) {
-                const int pos0 = (u.t0 + t) * BN, pos = pos0 + p, slot = tiles & 1;
-                s_row[slot * BN + p] =
-                    page >= 0 && page < a.c.pages
-                        ? page * a.c.page_stride + (static_cast<int64_t>(u.h) * a.c.P + pos % a.c.P) * D * 2 : -1;
-                page = fetch(t + 1);
-                bar_sync(1, 128);
+                const int pos0 = (u.t0 + t) * BN;
+                bar_sync(1, kLoadThreads);           // every copy of the tile before has been begun
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int rr = p + i * kLoadThreads, pg = page[0][i];
+                    if (rr < BN) {
+                        s_row[rr] = pg >= 0 && pg < a.c.pages
+                                        ? pg * a.c.page_stride + cell_at(t, i) * D * (E4 ? 1 : 2) : -1;
+                        if constexpr (E4) {
+                            smem[M::exps + (tiles & 1) * 2 * BN + rr] = static_cast<unsigned char>(ke[i]);
+                            smem[M::exps + (tiles & 1) * 2 * BN + BN + rr] = static_cast<unsigned char>(ve[i]);
+                        }
+                    }
+                    page[0][i] = page[1][i];
+                    page[1][i] = page_at(t + 2, i);
+                    if constexpr (E4) exps_at(t + 1, i, page[0][i]);
+                }
+                bar_sync(1, kLoadThreads);
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
-                    sync.wait((kv ? kVEmpty : kKEmpty) + slot, (tiles >> 1 & 1) ^ 1);
+                    if (pending == kPending) settle();
+                    // a slot that is still in use is time to finish what has come in
+                    while (pending > 0 && !__all_sync(0xffffffffu, sync.poll(kEmpty + slot, phase ^ 1))) settle();
+                    sync.wait(kEmpty + slot, phase ^ 1);
                     __syncwarp();
-                    if (kv && pos0 + BN > u.cut.ctx) {              // flags are looked at in such tiles only
-                        if (p < 4) s_flag[slot * 4 + p] = 0;
-                        bar_sync(1, 128);
-                    }
                     const unsigned char* src = kv ? a.c.v : a.c.k;
-                    const uint32_t dst = smem_u32(smem + (kv ? kOffV : kOffK) + slot * kTile);
-                    if (pc < CH) {
+                    const uint32_t dst = smem_u32(E4 ? smem + M::stage + (staged & 1) * (BN * 128) : smem + slot * kTile);
+                    if (copies) {
 #pragma unroll 4
-                        for (int i = 0; i < BN / 8; ++i) {
-                            const int r = pr + 8 * i;
-                            const int64_t off = s_row[slot * BN + r];
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + chunk_at(r, pc)),
-                                         "l"(src + (off < 0 ? 0 : off + pc * 16)), "r"(off < 0 ? 0 : 16) : "memory");
+                        for (int q = w; q < BN / RP; q += kLoadWarps) {
+                            const int r = q * RP + lr;
+                            const int64_t off = s_row[r];
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (E4 ? r * 128 + ((lc ^ (r & 7)) << 4) : chunk_at(r, lc))),
+                                         "l"(src + (off < 0 ? 0 : off + lc * 16)), "r"(off < 0 ? 0 : 16) : "memory");
                         }
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
-                    if (pending) {
-                        asm volatile("cp.async.wait_group 1;" ::: "memory");
-                        settle();
-                    }
-                    pending = true;
-                    pend_v = kv != 0;
-                    pend_slot = slot;
-                    pend_from = min(max(u.cut.ctx - pos0, 0), BN);
+                    const uint32_t from = static_cast<uint32_t>(min(max(u.cut.ctx - pos0, 0), BN));
+                    const uint32_t d = slot | static_cast<uint32_t>(kv) << 4 | (tiles & 3) << 5 | from << 8;
+                    if (pending == 0) pend[0] = d;
+                    else if (pending == 1) pend[1] = d;
+                    else pend[2] = d;
+                    ++pending;
+                    ++staged;
+                    if (++slot == S) slot = 0, phase ^= 1;
                 }
             }
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        settle();
+        while (pending > 0) settle();
     } else if (lane == 0) {
         // ---------------- products ----------------
         constexpr uint32_t type = F16 ? 0u : 1u;
         const uint32_t common = (1u << 4) | (type << 7) | (type << 10) | (8u << 24);    // fp32 += 16 bits, 128 rows
         const uint32_t idesc_s = common | (static_cast<uint32_t>(BN / 8) << 17);
         const uint32_t idesc_o = common | (1u << 16) | (static_cast<uint32_t>(D / 8) << 17);    // V is MN-major
-        const uint32_t k0 = smem_u32(smem + kOffK), v0 = smem_u32(smem + kOffV), q0 = smem_u32(smem + kOffQ);
+        const uint32_t ring_k = operand_lo(smem_u32(smem), 16), ring_v = operand_lo(smem_u32(smem), kBlock);
+        const uint32_t q0 = operand_lo(smem_u32(smem + M::q), 16);
+        const int nks = D / 16;
         uint32_t n[2] = {0, 0}, q[2] = {0, 0}, tiles = 0;
-        auto scores = [&](int s, uint32_t tile) {
+        auto scores = [&](int s, uint32_t key_slot) {
             if (*sync.dead) return;
-            for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t off = (ks >> 2) * kBlock + (ks & 3) * 32;
-                mma_ss(tmem + s * 128, operand(q0 + s * kTile + off, 16, 1024),
-                       operand(k0 + (tile & 1) * kTile + off, 16, 1024), idesc_s, ks > 0);
+            const uint32_t x = q0 + s * (kTile >> 4), y = ring_k + key_slot * (kTile >> 4), d = tmem + s * 128;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                const uint32_t off = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
+                if (ks < nks) mma_ss(d, x + off, y + off, idesc_s, ks > 0);
             }
         };
         while (walk.next(a, part, u)) {
@@ -495,37 +653,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
             if (nt == 0) continue;
             // stream s has a live row (stream 0 has one in every unit with tiles)
             const int streams = (u.mt * MT + kRows) / a.g < u.cut.cnt ? 2 : 1;
-            sync.wait(kKFull + (tiles & 1), tiles >> 1 & 1);
+            uint32_t step = 2 * tiles;               // keys' and values' places in the ring
+            sync.wait(kFull + step % S, step / S & 1);
             for (int s = 0; s < streams; ++s) {
                 sync.wait(kQFull + s, q[s]++ & 1);
                 fence_after();
-                scores(s, tiles);
+                scores(s, step % S);
                 sync.commit(kSFull + s);
             }
-            sync.commit(kKEmpty + (tiles & 1));
+            sync.commit(kEmpty + step % S);
             for (int t = 0; t < nt; ++t, ++tiles) {
                 const bool more = t + 1 < nt;
+                const uint32_t sv = 2 * tiles + 1, sk = sv + 1, slot_v = sv % S, slot_k = sk % S;
                 for (int s = 0; s < streams; ++s) {
                     sync.wait(kPFull + s, n[s]++ & 1);
-                    if (s == 0) sync.wait(kVFull + (tiles & 1), tiles >> 1 & 1);
+                    if (s == 0) sync.wait(kFull + slot_v, sv / S & 1);
                     fence_after();
                     if (!*sync.dead) {
+                        const uint32_t y = ring_v + slot_v * (kTile >> 4), d = tmem + 256 + s * 128, x = tmem + s * 128;
+#pragma unroll
                         for (int ks = 0; ks < BN / 16; ++ks)
-                            mma_ts(tmem + 256 + s * 128, tmem + s * 128 + ks * 8,
-                                   operand(v0 + (tiles & 1) * kTile + ks * 2048, kBlock, 1024), idesc_o, t > 0 || ks > 0);
+                            mma_ts(d, x + (ks >> 2) * 64 + (ks & 3) * 8, y + ks * (2048 >> 4), idesc_o, t > 0 || ks > 0);
                     }
                     sync.commit(kOFull + s);
                     if (more) {
                         if (s == 0) {
-                            sync.wait(kKFull + ((tiles + 1) & 1), (tiles + 1) >> 1 & 1);
+                            sync.wait(kFull + slot_k, sk / S & 1);
                             fence_after();
                         }
-                        scores(s, tiles + 1);
+                        scores(s, slot_k);
                         sync.commit(kSFull + s);
                     }
                 }
-                sync.commit(kVEmpty + (tiles & 1));
-                if (more) sync.commit(kKEmpty + ((tiles + 1) & 1));
+                sync.commit(kEmpty + slot_v);
+                if (more) sync.commit(kEmpty + slot_k);
             }
         }
         sync.commit(kEnd);                           // nothing is under way any more
@@ -534,25 +695,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
     __syncwarp();
     fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 11) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
 }
 
-template <bool F16> cudaError_t launch(AttnArgs a, int nsm, cudaStream_t s) {
-    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_tc_kernel<F16>), kSmem);
+template <bool E4, bool F16> cudaError_t launch(AttnArgs a, int nsm, cudaStream_t s) {
+    constexpr int bytes = Smem<E4>::bytes;
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_tc_kernel<E4, F16>), bytes);
     if (e != cudaSuccess) return e;
     a.ctas = nsm;
-    attn_tc_kernel<F16><<<static_cast<unsigned>(nsm), kThreads, kSmem, s>>>(a);
+    attn_tc_kernel<E4, F16><<<static_cast<unsigned>(nsm), kThreads, bytes, s>>>(a);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_attn_combine(a, F16, MT, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_tc(const AttnArgs& a, bool f16, int nsm, cudaStream_t s) {
-    return f16 ? launch<true>(a, nsm, s) : launch<false>(a, nsm, s);
+cudaError_t launch_attn_tc(const AttnArgs& a, bool f16, bool e4m3, int nsm, cudaStream_t s) {
+    if (e4m3) return f16 ? launch<true, true>(a, nsm, s) : launch<true, false>(a, nsm, s);
+    return f16 ? launch<false, true>(a, nsm, s) : launch<false, false>(a, nsm, s);
 }
 
 }  // namespace sdv
