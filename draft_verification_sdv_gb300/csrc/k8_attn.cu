@@ -78,7 +78,7 @@ cudaError_t launch_tree_attn(AttnArgs a, int type, bool e4m3, void* workspace, i
     a.part = reinterpret_cast<float*>(a.desc + 2 * kMaxCtasPerSm * nsm);
     const bool f16 = type == kTypeF16;
     const int rows = a.N * a.g;
-    if (a.c.D <= 128 && rows > kTcRows) return launch_attn_tc(a, f16, e4m3, nsm, s);
+    if (rows > kTcRows && attn_tc_takes(a)) return launch_attn_tc(a, f16, e4m3, nsm, s);
     if (a.c.D <= 64) return launch_attn_mma64(a, f16, e4m3, rows, nsm, s);
     if (a.c.D <= 128) return launch_attn_mma128(a, f16, e4m3, rows, nsm, s);
     return launch_attn_mma256(a, f16, e4m3, rows, nsm, s);

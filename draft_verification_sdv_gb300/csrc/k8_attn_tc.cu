@@ -20,15 +20,19 @@
 // that issues the products.  Tiles of 128 positions, keys and values in turn,
 // go through a ring of slots in shared memory, as rows of 128 bytes in the
 // 128-byte swizzle, [D / 64][128 rows]: the K operand is read K-major, and V,
-// whose contraction index is the row, MN-major.  Rows come from pages of any
-// size, so they are brought by 16-byte asynchronous copies rather than by tile
-// copies.  e4m3 rows are copied as they are into a second pair of tiles, and the
-// thread that copied a chunk brings it to the queries' type (times its row's
-// power of two) on its way to the ring.
+// whose contraction index is the row, MN-major.  Warp 8 brings a tile by tile
+// copies (TMA), one per page and column block, a lane to each, so that pages
+// may be of any size that is a multiple of 8 rows.  The three warps then hand
+// it over: after a look at the values of rows that some queries do not see
+// (what is not a number there must not meet a zero probability in a product),
+// or, for e4m3 rows, which are copied as they are into a second pair of tiles,
+// after bringing them to the queries' type, times their row's power of two.
 //
 // Every wait is bounded: a wait that gives up marks the CTA dead, after which
 // no wait waits, no product is issued, and every row that is still written is
 // not a number (SDV_STATUS_TIMEOUT).
+#include <cuda.h>
+
 #include "k8_attn.cuh"
 
 namespace sdv {
@@ -50,16 +54,16 @@ template <bool E4> struct Smem {
     static constexpr int kSlots = E4 ? 4 : 5;
     static constexpr int q = kSlots * kTile;
     static constexpr int stage = q + 2 * kTile;                 // two e4m3 tiles as they come
-    static constexpr int row = stage + (E4 ? 2 * BN * 128 : 0); // int64 [BN] byte offset of a row (-1: zeros)
-    static constexpr int exps = row + BN * 8;                   // bytes [2 tiles][keys, values][BN]
+    static constexpr int exps = stage + (E4 ? 2 * BN * 128 : 0);    // bytes [2 tiles][keys, values][BN]
     static constexpr int flag = exps + (E4 ? 4 * BN : 0);       // uint32 [4 tiles][3 warps][4] values that are not numbers
     static constexpr int bar = flag + 4 * kLoadWarps * 4 * 4;
-    static constexpr int word = bar + (2 * kSlots + 9) * 8;     // TMEM address, dead
+    static constexpr int word = bar + (3 * kSlots + 11) * 8;    // TMEM address, dead
     static constexpr int bytes = word + 8 + 1024;
 };
 static_assert(Smem<true>::bytes <= 227 * 1024 && Smem<false>::bytes <= 227 * 1024, "one CTA per SM");
 
-// Barriers: two per stream of each kind, one for the end, then the ring's.
+// Barriers: two per stream of each kind, one for the end, then the ring's (full,
+// empty, landed) and the e4m3 tiles' (empty; landed is the ring's first two).
 enum Bar { kQFull = 0, kSFull = 2, kPFull = 4, kOFull = 6, kEnd = 8, kRing = 9 };
 
 struct Sync {
@@ -92,6 +96,11 @@ struct Sync {
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// Tile copy of the box at (x, row, page) into shared memory.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int row, int page) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(row), "r"(page) : "memory");
+}
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
 #define SDV_R4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
@@ -234,13 +243,13 @@ template <bool F16> __device__ __forceinline__ void widen16(const uint4& raw, in
 }
 
 template <bool E4, bool F16>
-__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
+                                                              const __grid_constant__ CUtensorMap map_v, int run_rows) {
     using M = Smem<E4>;
     constexpr uint32_t S = M::kSlots;
-    constexpr int kFull = kRing, kEmpty = kRing + M::kSlots;
+    constexpr int kFull = kRing, kEmpty = kFull + M::kSlots, kLand = kEmpty + M::kSlots, kStage = kLand + M::kSlots;
     extern __shared__ unsigned char raw[];
     unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    int64_t* s_row = reinterpret_cast<int64_t*>(smem + M::row);
     uint32_t* s_flag = reinterpret_cast<uint32_t*>(smem + M::flag);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::bar);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::word);
@@ -262,7 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
         for (int i = 0; i < M::kSlots; ++i) {
             mbar_init(bars + kFull + i, kLoadWarps);
             mbar_init(bars + kEmpty + i, 1);
+            mbar_init(bars + kLand + i, 1);
         }
+        for (int i = 0; i < 2; ++i) mbar_init(bars + kStage + i, kLoadWarps);
         a.desc[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
     }
     if (warp == 11) {
@@ -485,150 +496,165 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
     } else if (warp < 11) {
         // ---------------- loads ----------------
         const int p = tid - 256, w = warp - 8;
-        const int cells = E4 ? 16 : 8;               // of a 16-byte chunk
-        const int CH = D / cells;                    // chunks of a row
+        const int CH = D / (E4 ? 16 : 8);            // 16-byte chunks of a row as it comes
         const int LR = CH > 8 ? 16 : CH > 4 ? 8 : 4; // lanes of a row
         const int RP = 32 / LR, lr = lane / LR, lc = lane % LR;     // rows of a warp's step
-        const bool copies = lc < CH;
-        constexpr uint32_t kPending = E4 ? 2 : 3;    // steps under way at most
-        uint32_t tiles = 0, slot = 0, phase = 0;     // the ring's next slot
-        uint32_t staged = 0;                         // e4m3: steps begun
-        // steps under way, the oldest first: slot, values or keys, tile, first
-        // row that some queries do not see
-        uint32_t pend[3] = {0, 0, 0}, pending = 0;
-        auto settle = [&]() {                        // the oldest step is in: finish it and hand it over
-            if (pending == 3)
-                asm volatile("cp.async.wait_group 2;" ::: "memory");
-            else if (pending == 2)
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-            else
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
-            const uint32_t d = pend[0];
-            const int sl = d & 15, isv = d >> 4 & 1, tile = d >> 5 & 3, from = d >> 8;
-            unsigned char* base = smem + sl * kTile;
-            uint32_t* flags = s_flag + tile * (kLoadWarps * 4) + w * 4;
-            const bool check = isv && from < BN;     // values that are not numbers are kept out of the products
-            if (check) {
-                if (lane < 4) flags[lane] = 0;
-                __syncwarp();
-            }
-            if (E4 || check) {
-                const unsigned char* stage = smem + M::stage + ((staged - pending) & 1) * (BN * 128);
-                const unsigned char* ex = smem + M::exps + ((tile & 1) * 2 + isv) * BN;
-                for (int q = w; q < BN / RP; q += kLoadWarps) {
-                    const int r = q * RP + lr;
-                    uint32_t o[8];
-                    bool bad = false;
-                    constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
-                    if (copies) {
-                        if constexpr (E4) {
-                            widen16<F16>(*reinterpret_cast<const uint4*>(stage + r * 128 + ((lc ^ (r & 7)) << 4)), ex[r], o);
-                        } else {
-                            const uint4 v = *reinterpret_cast<const uint4*>(base + chunk_at(r, lc));
-                            o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
-                        }
-                        if (check && r >= from)
-#pragma unroll
-                            for (int i = 0; i < (E4 ? 8 : 4); ++i)
-                                bad |= (o[i] & top) == top || (o[i] >> 16 & top) == top;
-                    }
-                    bool row_bad = false;
-                    if (check) {
-                        const uint32_t group = (LR == 32 ? 0xffffffffu : (1u << LR) - 1u) << (lr * LR);
-                        row_bad = (__ballot_sync(0xffffffffu, bad) & group) != 0;
-                        if (row_bad && lc == 0) atomicOr(flags + (r >> 5), 1u << (r & 31));
-                    }
-                    if (E4 ? copies : copies && row_bad) {
-#pragma unroll
-                        for (int i = 0; i < (E4 ? 8 : 4); i += 4)
-                            *reinterpret_cast<uint4*>(base + chunk_at(r, E4 ? 2 * lc + i / 4 : lc)) =
-                                row_bad ? make_uint4(0, 0, 0, 0) : make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                    }
-                }
-            }
-            fence_async();
-            __syncwarp();
-            if (lane == 0) sync.arrive(kFull + sl);
-            pend[0] = pend[1], pend[1] = pend[2];
-            --pending;
+        const uint32_t group = ((1u << LR) - 1u) << (lr * LR);
+        constexpr uint32_t kAhead = E4 ? 2 : 3;      // steps (tiles of keys or of values) under way
+
+        // warp 8: begins the copies of the next step; a walk of its own, ahead
+        Walk<MT, BN> lead;
+        Unit lu{};
+        lead.start(a, part, mts);
+        int lt = 0, lnt = 0, lpage = -1;
+        uint32_t lstep = 0;
+        bool more = w == 0;
+        const int blocks = !E4 && D > 64 ? 2 : 1;
+        const int copy = lane / blocks, block = lane % blocks;
+        auto lead_page = [&](int t) {                // the page of this lane's rows of tile t
+            const int pos = (lu.t0 + t) * BN + copy * run_rows;
+            const int pg = copy * run_rows < BN && t < lnt && pos < lu.len
+                               ? __ldg(a.table + static_cast<int64_t>(lu.b) * a.max_pages + pos / a.c.P) : -1;
+            return pg < a.c.pages ? pg : -1;
         };
+        auto begin = [&]() {
+            if (!more) return;
+            if ((lstep & 1) == 0 && lt == lnt) {     // the next unit with tiles
+                do {
+                    more = lead.next(a, part, lu);
+                    lnt = more && lu.len > 0 ? lu.t1 - lu.t0 : 0;
+                } while (more && lnt == 0);
+                if (!more) return;
+                lt = 0;
+                lpage = lead_page(0);
+            }
+            const bool isv = lstep & 1;
+            const uint32_t slot = E4 ? lstep & 1 : lstep % S, phase = E4 ? lstep >> 1 & 1 : lstep / S & 1;
+            sync.wait((E4 ? kStage : kEmpty) + slot, phase ^ 1);
+            __syncwarp();
+            more = !__any_sync(0xffffffffu, *sync.dead != 0);
+            if (!more) return;
+            const bool active = lpage >= 0;
+            const uint32_t n = __popc(__ballot_sync(0xffffffffu, active));
+            if (lane == 0) mbar_arrive_expect_tx(bars + kLand + slot, n * run_rows * 128);
+            __syncwarp();
+            if (active) {
+                const int pos = (lu.t0 + lt) * BN + copy * run_rows;
+                tma_load(smem_u32(smem + (E4 ? M::stage + slot * (BN * 128) : slot * kTile + block * kBlock) + copy * run_rows * 128),
+                         isv ? &map_v : &map_k, bars + kLand + slot, block * 64, lu.h * a.c.P + pos % a.c.P, lpage);
+            }
+            ++lstep;
+            if (isv) lpage = lead_page(++lt);
+        };
+        for (uint32_t i = 0; i < kAhead; ++i) begin();
+
+        uint32_t tiles = 0, step = 0;
         while (walk.next(a, part, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
+            // e4m3: a thread looks after the exponents of rows p and p + 96 of a
+            // tile; a row's page is read two tiles ahead, its exponents one
             const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
-            // a thread looks after rows p and p + 96 of a tile: the page of the
-            // row is read two tiles ahead, and its exponents one tile ahead
+            int page[2][2], ke[2] = {127, 127}, ve[2] = {127, 127};
             auto page_at = [&](int t, int i) {
                 const int rr = p + i * kLoadThreads, pos = (u.t0 + t) * BN + rr;
                 return rr < BN && t < nt && pos < u.len ? __ldg(table + pos / a.c.P) : -1;
             };
-            auto cell_at = [&](int t, int i) {       // row within its page
-                return static_cast<int64_t>(u.h) * a.c.P + ((u.t0 + t) * BN + p + i * kLoadThreads) % a.c.P;
-            };
-            int page[2][2], ke[2] = {127, 127}, ve[2] = {127, 127};
             auto exps_at = [&](int t, int i, int pg) {
                 ke[i] = ve[i] = 127;
                 if (pg >= 0 && pg < a.c.pages) {
-                    const int64_t o = pg * a.c.exp_page_stride + cell_at(t, i);
+                    const int64_t o = pg * a.c.exp_page_stride + static_cast<int64_t>(u.h) * a.c.P +
+                                      ((u.t0 + t) * BN + p + i * kLoadThreads) % a.c.P;
                     ke[i] = a.c.ke[o];
                     ve[i] = a.c.ve[o];
                 }
             };
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                page[0][i] = page_at(0, i);
-                page[1][i] = page_at(1, i);
-                if constexpr (E4) exps_at(0, i, page[0][i]);
-            }
-            for (int t = 0; t < nt; ++t, ++tiles) {
-                const int pos0 = (u.t0 + t) * BN;
-                bar_sync(1, kLoadThreads);           // every copy of the tile before has been begun
+            if constexpr (E4) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int rr = p + i * kLoadThreads, pg = page[0][i];
-                    if (rr < BN) {
-                        s_row[rr] = pg >= 0 && pg < a.c.pages
-                                        ? pg * a.c.page_stride + cell_at(t, i) * D * (E4 ? 1 : 2) : -1;
-                        if constexpr (E4) {
+                    page[0][i] = page_at(0, i);
+                    page[1][i] = page_at(1, i);
+                    exps_at(0, i, page[0][i]);
+                }
+            }
+            for (int t = 0; t < nt; ++t, ++tiles) {
+                const int from = min(max(u.cut.ctx - (u.t0 + t) * BN, 0), BN);   // first row that some do not see
+                if constexpr (E4) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int rr = p + i * kLoadThreads;
+                        if (rr < BN) {
                             smem[M::exps + (tiles & 1) * 2 * BN + rr] = static_cast<unsigned char>(ke[i]);
                             smem[M::exps + (tiles & 1) * 2 * BN + BN + rr] = static_cast<unsigned char>(ve[i]);
                         }
+                        page[0][i] = page[1][i];
+                        page[1][i] = page_at(t + 2, i);
+                        exps_at(t + 1, i, page[0][i]);
                     }
-                    page[0][i] = page[1][i];
-                    page[1][i] = page_at(t + 2, i);
-                    if constexpr (E4) exps_at(t + 1, i, page[0][i]);
+                    bar_sync(1, kLoadThreads);
                 }
-                bar_sync(1, kLoadThreads);
 #pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (pending == kPending) settle();
-                    // a slot that is still in use is time to finish what has come in
-                    while (pending > 0 && !__all_sync(0xffffffffu, sync.poll(kEmpty + slot, phase ^ 1))) settle();
-                    sync.wait(kEmpty + slot, phase ^ 1);
+                for (int kv = 0; kv < 2; ++kv, ++step) {
+                    const uint32_t slot = step % S, phase = step / S & 1;
+                    if constexpr (E4) {
+                        sync.wait(kLand + (step & 1), step >> 1 & 1);
+                        sync.wait(kEmpty + slot, phase ^ 1);
+                    } else {
+                        sync.wait(kLand + slot, phase);
+                    }
                     __syncwarp();
-                    const unsigned char* src = kv ? a.c.v : a.c.k;
-                    const uint32_t dst = smem_u32(E4 ? smem + M::stage + (staged & 1) * (BN * 128) : smem + slot * kTile);
-                    if (copies) {
-#pragma unroll 4
+                    unsigned char* base = smem + slot * kTile;
+                    const bool check = kv && from < BN;
+                    if (E4 || check) {
+                        uint32_t* flags = s_flag + (tiles & 3) * (kLoadWarps * 4) + w * 4;
+                        if (check) {
+                            if (lane < 4) flags[lane] = 0;
+                            __syncwarp();
+                        }
+                        const unsigned char* stage = smem + M::stage + (step & 1) * (BN * 128);
+                        const unsigned char* ex = smem + M::exps + ((tiles & 1) * 2 + kv) * BN;
                         for (int q = w; q < BN / RP; q += kLoadWarps) {
                             const int r = q * RP + lr;
-                            const int64_t off = s_row[r];
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (E4 ? r * 128 + ((lc ^ (r & 7)) << 4) : chunk_at(r, lc))),
-                                         "l"(src + (off < 0 ? 0 : off + lc * 16)), "r"(off < 0 ? 0 : 16) : "memory");
+                            uint32_t o[8];
+                            bool bad = false;
+                            constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
+                            if (lc < CH) {
+                                if constexpr (E4) {
+                                    widen16<F16>(*reinterpret_cast<const uint4*>(stage + r * 128 + lc * 16), ex[r], o);
+                                } else {
+                                    const uint4 v = *reinterpret_cast<const uint4*>(base + chunk_at(r, lc));
+                                    o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+                                }
+                                if (check && r >= from)
+#pragma unroll
+                                    for (int i = 0; i < (E4 ? 8 : 4); ++i)
+                                        bad |= (o[i] & top) == top || (o[i] >> 16 & top) == top;
+                            }
+                            bool row_bad = false;
+                            if (check) {
+                                row_bad = (__ballot_sync(0xffffffffu, bad) & group) != 0;
+                                if (row_bad && lc == 0) atomicOr(flags + (r >> 5), 1u << (r & 31));
+                            }
+                            if (lc < CH && (E4 || row_bad)) {
+#pragma unroll
+                                for (int i = 0; i < (E4 ? 8 : 4); i += 4)
+                                    *reinterpret_cast<uint4*>(base + chunk_at(r, E4 ? 2 * lc + i / 4 : lc)) =
+                                        row_bad ? make_uint4(0, 0, 0, 0) : make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                            }
                         }
                     }
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    const uint32_t from = static_cast<uint32_t>(min(max(u.cut.ctx - pos0, 0), BN));
-                    const uint32_t d = slot | static_cast<uint32_t>(kv) << 4 | (tiles & 3) << 5 | from << 8;
-                    if (pending == 0) pend[0] = d;
-                    else if (pending == 1) pend[1] = d;
-                    else pend[2] = d;
-                    ++pending;
-                    ++staged;
-                    if (++slot == S) slot = 0, phase ^= 1;
+                    fence_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        sync.arrive(kFull + slot);
+                        if constexpr (E4) sync.arrive(kStage + (step & 1));
+                    }
+                    begin();
                 }
             }
         }
-        while (pending > 0) settle();
+        if (w == 0)                                  // a dead CTA too waits for the copies it has begun
+            for (uint32_t i = lstep > kAhead ? lstep - kAhead : 0; i < lstep; ++i)
+                for (uint32_t n = 0; n < kPolls && !sync.poll(kLand + (E4 ? i & 1 : i % S), (E4 ? i >> 1 : i / S) & 1); ++n) {}
     } else if (lane == 0) {
         // ---------------- products ----------------
         constexpr uint32_t type = F16 ? 0u : 1u;
@@ -701,21 +727,61 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnArgs a) 
     }
 }
 
-template <bool E4, bool F16> cudaError_t launch(AttnArgs a, int nsm, cudaStream_t s) {
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled f = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return f;
+}
+
+// Cells as [pages][kv_heads * page_size][head_dim]; boxes of `rows` rows of 64
+// 16-bit cells (swizzled), or of 128 e4m3 cells; what lies past head_dim is 0.
+bool encode(CUtensorMap* map, const AttnArgs& a, unsigned char* cells, bool e4m3, int rows) {
+    const EncodeTiled f = encode_tiled();
+    if (!f) return false;
+    const int cell = e4m3 ? 1 : 2;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.c.D), static_cast<cuuint64_t>(a.c.H) * a.c.P,
+                                static_cast<cuuint64_t>(a.c.pages)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.c.D) * cell, static_cast<cuuint64_t>(a.c.page_stride)};
+    const cuuint32_t box[3] = {e4m3 ? 128u : 64u, static_cast<cuuint32_t>(rows), 1u}, one[3] = {1u, 1u, 1u};
+    return f(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, cells, dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool E4, bool F16>
+cudaError_t launch(AttnArgs a, const CUtensorMap& k, const CUtensorMap& v, int rows, int nsm, cudaStream_t s) {
     constexpr int bytes = Smem<E4>::bytes;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_tc_kernel<E4, F16>), bytes);
     if (e != cudaSuccess) return e;
     a.ctas = nsm;
-    attn_tc_kernel<E4, F16><<<static_cast<unsigned>(nsm), kThreads, bytes, s>>>(a);
+    attn_tc_kernel<E4, F16><<<static_cast<unsigned>(nsm), kThreads, bytes, s>>>(a, k, v, rows);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_attn_combine(a, F16, MT, s);
 }
 
 }  // namespace
 
+bool attn_tc_takes(const AttnArgs& a) { return a.c.D <= 128 && a.c.P % 8 == 0 && encode_tiled() != nullptr; }
+
 cudaError_t launch_attn_tc(const AttnArgs& a, bool f16, bool e4m3, int nsm, cudaStream_t s) {
-    if (e4m3) return f16 ? launch<true, true>(a, nsm, s) : launch<true, false>(a, nsm, s);
-    return f16 ? launch<false, true>(a, nsm, s) : launch<false, false>(a, nsm, s);
+    // rows of one copy: those of a tile that are sure to lie in one page
+    const int rows = min(a.c.P & -a.c.P, BN);
+    CUtensorMap k, v;
+    if (!encode(&k, a, a.c.k, e4m3, rows) || !encode(&v, a, a.c.v, e4m3, rows)) return cudaErrorInvalidValue;
+    if (e4m3) return f16 ? launch<true, true>(a, k, v, rows, nsm, s) : launch<true, false>(a, k, v, rows, nsm, s);
+    return f16 ? launch<false, true>(a, k, v, rows, nsm, s) : launch<false, false>(a, k, v, rows, nsm, s);
 }
 
 }  // namespace sdv
