@@ -123,66 +123,66 @@ struct Unit {
     int b, h, mt;
     Cut cut;
     int len;                 // positions it reads
-    int tiles, t0, t1;       // its tiles, and those of this CTA
-    int64_t first;           // place of tile 0 on the line
+    int t0, t1;              // this CTA's of its tiles
+    bool whole;              // that is all of them
 };
 
-// Walks the units of a CTA's part.
+// Walks the units of a CTA's part: the first is found by division, the others
+// follow one another.
 template <int MT, int BN> struct Walk {
-    int64_t at, seq0;
-    int b, mts;
+    int left, rest;          // tiles left of the part; tiles of the unit before it
+    int b, h, mt;
     Cut cut;
-    int64_t per_head;
-    __device__ __forceinline__ void start(const AttnArgs& a, const Part& p, int mts_) {
-        at = p.begin;
-        seq0 = p.seq0;
+    __device__ __forceinline__ void start(const AttnArgs& a, const Part& p, int mts) {
+        left = static_cast<int>(p.end - p.begin);
+        rest = 0;
         b = p.b;
-        mts = mts_;
-        if (b < a.B) {
-            cut = cut_of(a, b);
-            per_head = head_tiles<MT, BN>(a, cut, mts);
-        }
-    }
-    __device__ __forceinline__ bool next(const AttnArgs& a, const Part& p, Unit& u) {
-        if (at >= p.end) return false;
-        if (at - seq0 >= per_head * a.c.H) {
-            seq0 += per_head * a.c.H;
-            ++b;
-            cut = cut_of(a, b);
-            per_head = head_tiles<MT, BN>(a, cut, mts);
-        }
-        const int64_t in_seq = at - seq0;
-        u.b = b;
-        u.cut = cut;
-        u.h = static_cast<int>(in_seq / per_head);
-        int64_t rest = in_seq - u.h * per_head;
+        h = mt = 0;
+        if (b >= a.B) return;
+        cut = cut_of(a, b);
+        const int64_t in_seq = p.begin - p.seq0, per_head = head_tiles<MT, BN>(a, cut, mts);
+        h = static_cast<int>(in_seq / per_head);
+        int64_t before = in_seq - h * per_head;
         if (a.mask) {
             const int t = tiles_of<BN>(cut.ctx + cut.cnt);
             const int live = min(mts, (cut.cnt * a.g + MT - 1) / MT);
-            if (rest < static_cast<int64_t>(live) * t) {
-                u.mt = static_cast<int>(rest / t);
-                rest -= static_cast<int64_t>(u.mt) * t;
+            if (before < static_cast<int64_t>(live) * t) {
+                mt = static_cast<int>(before / t);
+                before -= static_cast<int64_t>(mt) * t;
             } else {
-                rest -= static_cast<int64_t>(live) * t;
-                u.mt = live + static_cast<int>(rest);
-                rest = 0;
+                mt = live + static_cast<int>(before - static_cast<int64_t>(live) * t);
+                before = 0;
             }
         } else {
-            u.mt = 0;
             while (true) {
-                const int t = tiles_of<BN>(tile_len<MT>(a, cut, u.mt));
-                if (rest < t) break;
-                rest -= t;
-                ++u.mt;
+                const int t = tiles_of<BN>(tile_len<MT>(a, cut, mt));
+                if (before < t) break;
+                before -= t;
+                ++mt;
             }
         }
-        u.len = tile_len<MT>(a, cut, u.mt);
-        u.tiles = tiles_of<BN>(u.len);
-        u.t0 = static_cast<int>(rest);
-        u.first = at - rest;
-        const int64_t left = p.end - u.first;
-        u.t1 = left < u.tiles ? static_cast<int>(left) : u.tiles;
-        at = u.first + u.t1;
+        rest = static_cast<int>(before);
+    }
+    __device__ __forceinline__ bool next(const AttnArgs& a, int mts, Unit& u) {
+        if (left <= 0) return false;
+        u.b = b;
+        u.h = h;
+        u.mt = mt;
+        u.cut = cut;
+        u.len = tile_len<MT>(a, cut, mt);
+        const int tiles = tiles_of<BN>(u.len);
+        u.t0 = rest;
+        u.t1 = min(tiles, rest + left);
+        u.whole = u.t0 == 0 && u.t1 == tiles;
+        left -= u.t1 - u.t0;
+        rest = 0;
+        if (++mt == mts) {
+            mt = 0;
+            if (++h == a.c.H) {
+                h = 0;
+                if (++b < a.B) cut = cut_of(a, b);
+            }
+        }
         return true;
     }
 };
@@ -193,13 +193,19 @@ __device__ __forceinline__ float* part_rows(const AttnArgs& a, int cta, int slot
 }
 
 // desc[2 i] = the unit that CTA i's part begins within, if CTA i is the first
-// to go on with it: (b, h, mt, first CTA); the last CTA in desc[2 i + 1].
-__device__ __forceinline__ void write_desc(const AttnArgs& a, const Part& p, const Unit& u) {
+// to go on with it: (b, h, mt, first CTA); the last CTA in desc[2 i + 1].  One
+// thread writes it, from a walk that has just started.
+template <int MT, int BN> __device__ __forceinline__ void write_desc(const AttnArgs& a, const Part& p, const Walk<MT, BN>& w) {
     const int i = blockIdx.x;
-    const int owner = part_owner(p.total, p.ctas, u.first);
-    const int last = part_owner(p.total, p.ctas, u.first + u.tiles - 1);
-    a.desc[2 * i] = make_int4(owner == i - 1 ? u.b : -1, u.h, u.mt, owner);
-    a.desc[2 * i + 1] = make_int4(last, 0, 0, 0);
+    int4 d = make_int4(-1, 0, 0, 0);
+    if (w.left > 0 && w.rest > 0) {
+        const int64_t first = p.begin - w.rest;
+        const int owner = part_owner(p.total, p.ctas, first);
+        const int tiles = tiles_of<BN>(tile_len<MT>(a, w.cut, w.mt));
+        if (owner == i - 1) d = make_int4(w.b, w.h, w.mt, owner);
+        a.desc[2 * i + 1] = make_int4(part_owner(p.total, p.ctas, first + tiles - 1), 0, 0, 0);
+    }
+    a.desc[2 * i] = d;
 }
 
 template <bool F16> __device__ __forceinline__ uint32_t pack2(float x, float y) {   // x in the low half

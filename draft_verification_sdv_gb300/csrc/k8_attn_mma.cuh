@@ -137,18 +137,14 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
     const int g4 = lane >> 2, t4 = lane & 3;
     const int mts = (a.N * a.g + MT - 1) / MT;
     const Part part = find_part<MT, BN, kThreads>(a, mts, s_part);
-    if (tid == 0) a.desc[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
 
     Walk<MT, BN> walk;
     walk.start(a, part, mts);
+    if (tid == 0) write_desc(a, part, walk);
     Unit u;
-    while (walk.next(a, part, u)) {
+    while (walk.next(a, mts, u)) {
         __syncthreads();                            // the unit before is done with shared memory
-        const bool whole = u.t0 == 0 && u.t1 == u.tiles;
-        if (tid == 0) {
-            if (u.t0 > 0) write_desc(a, part, u);
-            if (u.cut.bad && a.status) atomicOr(a.status, kStatusBadLength);
-        }
+        if (tid == 0 && u.cut.bad && a.status) atomicOr(a.status, kStatusBadLength);
         const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
         const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
 
@@ -516,7 +512,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
             const float log2sum = u.cut.bad ? nan : empty ? -INFINITY : mx + log2f(sum);
 #pragma unroll
             for (int x = 0; x < 4; ++x) acc[x] = empty ? 0.0f : acc[x] * inv;
-            if (whole) {
+            if (u.whole) {
                 const int64_t orow = (static_cast<int64_t>(u.b) * a.N + nd) * a.Hq + u.h * a.g + row % a.g;
                 unsigned short* dst = static_cast<unsigned short*>(a.out) + orow * a.c.D + d;
                 *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<F16>(acc[0], acc[1]), pack2<F16>(acc[2], acc[3]));

@@ -41,6 +41,7 @@ namespace {
 using namespace attn;
 
 constexpr int kThreads = 384;
+constexpr int kRegs = 168;               // per thread at launch
 constexpr int kRows = 128;               // rows of a stream
 constexpr int MT = 2 * kRows, BN = 128;
 constexpr int kBlock = BN * 128;         // bytes of 128 rows of 64 16-bit cells
@@ -57,14 +58,14 @@ template <bool E4> struct Smem {
     static constexpr int exps = stage + (E4 ? 2 * BN * 128 : 0);    // bytes [2 tiles][keys, values][BN]
     static constexpr int flag = exps + (E4 ? 4 * BN : 0);       // uint32 [4 tiles][3 warps][4] values that are not numbers
     static constexpr int bar = flag + 4 * kLoadWarps * 4 * 4;
-    static constexpr int word = bar + (3 * kSlots + 11) * 8;    // TMEM address, dead
+    static constexpr int word = bar + (3 * kSlots + 13) * 8;    // TMEM address, dead
     static constexpr int bytes = word + 8 + 1024;
 };
 static_assert(Smem<true>::bytes <= 227 * 1024 && Smem<false>::bytes <= 227 * 1024, "one CTA per SM");
 
 // Barriers: two per stream of each kind, one for the end, then the ring's (full,
 // empty, landed) and the e4m3 tiles' (empty; landed is the ring's first two).
-enum Bar { kQFull = 0, kSFull = 2, kPFull = 4, kOFull = 6, kEnd = 8, kRing = 9 };
+enum Bar { kQFull = 0, kSFull = 2, kPFull = 4, kOFull = 6, kQEmpty = 8, kEnd = 10, kRing = 11 };
 
 struct Sync {
     uint64_t* bar;
@@ -101,6 +102,10 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, u
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
                  "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(row), "r"(page) : "memory");
 }
+__device__ __forceinline__ void tma_load_q(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int head, int node, int b) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(head), "r"(node), "r"(b) : "memory");
+}
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
 #define SDV_R4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
@@ -125,14 +130,7 @@ __device__ __forceinline__ void tmem_ld16(float (&x)[16], uint32_t addr) {
         "tcgen05.wait::ld.sync.aligned;"
         : SDV_R16(r, 0) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        SDV_I16(r, 0), SDV_I16(r, 16) : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const float (&x)[16]) {
-    const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
         SDV_I16(r, 0) : "memory");
@@ -163,12 +161,6 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
         "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
         : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -244,7 +236,9 @@ template <bool F16> __device__ __forceinline__ void widen16(const uint4& raw, in
 
 template <bool E4, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
-                                                              const __grid_constant__ CUtensorMap map_v, int run_rows) {
+                                                              const __grid_constant__ CUtensorMap map_v,
+                                                              const __grid_constant__ CUtensorMap map_q, int run_rows,
+                                                              bool q_boxes) {
     using M = Smem<E4>;
     constexpr uint32_t S = M::kSlots;
     constexpr int kFull = kRing, kEmpty = kFull + M::kSlots, kLand = kEmpty + M::kSlots, kStage = kLand + M::kSlots;
@@ -262,7 +256,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     if (tid == 0) {
         *s_dead = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bars + kQFull + i, kRows);
+            mbar_init(bars + kQFull + i, q_boxes ? 1 : kLoadWarps);
+            mbar_init(bars + kQEmpty + i, 1);
             mbar_init(bars + kSFull + i, 1);
             mbar_init(bars + kPFull + i, kRows);
             mbar_init(bars + kOFull + i, 1);
@@ -274,7 +269,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             mbar_init(bars + kLand + i, 1);
         }
         for (int i = 0; i < 2; ++i) mbar_init(bars + kStage + i, kLoadWarps);
-        a.desc[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
     }
     if (warp == 11) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(s_tmem)) : "memory");
@@ -288,65 +282,49 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const uint32_t tmem = *s_tmem;
     Walk<MT, BN> walk;
     walk.start(a, part, mts);
+    if (tid == 0) write_desc(a, part, walk);
     Unit u;
 
+    // the softmax warps hold half a row of scores: they take registers that the
+    // others do not need (256 * 184 + 128 * 136 = 384 * 168, the launch's own)
+    if (warp < 8)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;" ::: "memory");
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 136;" ::: "memory");
     if (warp < 8) {
         // ---------------- softmax of one stream, a thread per row ----------------
         const int st = warp >> 2, r = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + st * 128, tO = tmem + lanes + 256 + st * 128;
-        // a negative scale turns the queries round; c > 0 so that -inf stays -inf
+        // a negative scale turns the scores round; c > 0 so that -inf stays -inf
         const float c = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
-        const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+        const bool flip = a.scale_log2 < 0.0f;
         uint32_t n = 0;                              // tiles of this stream so far
         uint32_t nv = 0;                             // tiles of the CTA so far
-        while (walk.next(a, part, u)) {
+        int seq = -1, any_bad = 0;
+        while (walk.next(a, mts, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
             const int first_row = u.mt * MT + st * kRows;
             const int row = first_row + r, node = row / a.g;
             const bool live = node < u.cut.cnt;
             const bool run = nt > 0 && first_row / a.g < u.cut.cnt;     // the stream has a live row
-            if (tid == 0) {
-                if (u.t0 > 0) write_desc(a, part, u);
-                if (u.cut.bad && a.status) atomicOr(a.status, kStatusBadLength);
-            }
+            if (tid == 0 && u.cut.bad && a.status) atomicOr(a.status, kStatusBadLength);
             float m = -INFINITY, l = 0.0f;
             bool nan_row = false;
             if (run) {
-                unsigned char* qs = smem + M::q + st * kTile;
-                const unsigned char* p = a.q + u.b * a.q_sb + node * a.q_sn +
-                                         (static_cast<int64_t>(u.h) * a.g + row % a.g) * a.q_sh;
-                if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D / 8; c0 += 8) {
-                        uint4 v[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            v[i] = live && c0 + i < D / 8 ? *reinterpret_cast<const uint4*>(p + (c0 + i) * 16) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<uint4*>(qs + chunk_at(r, c0 + i)) =
-                                make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
-                    }
-                } else {
-                    for (int i = 0; i < D; ++i)
-                        *reinterpret_cast<unsigned short*>(qs + chunk_at(r, i >> 3) + (i & 7) * 2) =
-                            live ? reinterpret_cast<const unsigned short*>(p)[i] ^ static_cast<unsigned short>(flip) : 0;
-                }
-                fence_async();
-                sync.arrive(kQFull + st);
-                // pages that are not the cache's: looked for once, a slow path if there are any
                 const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
-                const int last_page = (min(u.t1 * BN, u.len) - 1) / a.c.P;
-                int bad = 0;
-                for (int pg = u.t0 * BN / a.c.P + r; pg <= last_page; pg += kRows) {
-                    const int x = __ldg(table + pg);
-                    bad |= x < 0 || x >= a.c.pages;
+                if (u.b != seq) {                    // pages that are not the cache's: a slow path if there are any
+                    seq = u.b;
+                    const int last_page = (u.cut.ctx + u.cut.cnt - 1) / a.c.P;
+                    int bad = 0;
+                    for (int pg = r; pg <= last_page; pg += kRows) {
+                        const int x = __ldg(table + pg);
+                        bad |= x < 0 || x >= a.c.pages;
+                    }
+                    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.red.or.pred q, %2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+                                 : "=r"(any_bad) : "r"(bad), "r"(2 + st) : "memory");
+                    if (any_bad && r == 0 && a.status) atomicOr(a.status, kStatusBadPage);
                 }
-                int any_bad;
-                asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.red.or.pred q, %2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-                             : "=r"(any_bad) : "r"(bad), "r"(2 + st) : "memory");
-                if (any_bad && r == 0 && a.status) atomicOr(a.status, kStatusBadPage);
                 const int32_t* mrow = a.mask ? a.mask + u.b * a.mask_sb + static_cast<int64_t>(live ? node : 0) * a.W : nullptr;
                 uint32_t words[5];
                 // tiles from first_mixed on hold nodes, which some rows see and some do not
@@ -388,6 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         }
                     }
                     auto hide = [&](int h) {         // what the row does not see of half h
+                        if (flip)
+#pragma unroll
+                            for (int y = 0; y < 64; ++y) x[y] = -x[y];
                         if (mixed)
 #pragma unroll
                             for (int y = 0; y < 64; ++y)
@@ -413,12 +394,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         __syncwarp();
                         fence_after();
                         l *= by;
+#pragma unroll 1
                         for (int i = 0; i < D; i += 16) {
                             float o[16];
+                            uint32_t o2[16];
                             tmem_ld16(o, tO + i);
 #pragma unroll
-                            for (int y = 0; y < 16; ++y) o[y] *= by;
-                            tmem_st16(tO + i, o);
+                            for (int y = 0; y < 16; ++y) o2[y] = __float_as_uint(o[y] * by);
+                            tmem_st16(tO + i, o2);
                         }
                     }
                     if (move) m = top;
@@ -431,17 +414,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                             tmem_ld64(x, tS);
                             hide(0);
                         }
-                        uint32_t p2[32];
 #pragma unroll
-                        for (int y = 0; y < 32; y += 2) {
-                            F2 v = fma2(F2{x[2 * y], x[2 * y + 1]}, c2, sub2);
-                            F2 w = fma2(F2{x[2 * y + 2], x[2 * y + 3]}, c2, sub2);
-                            v.x = ex2(v.x), v.y = ex2(v.y), w.x = ex2(w.x), w.y = ex2(w.y);
-                            s0 = add2(s0, v), s1 = add2(s1, w);
-                            p2[y] = pack2<F16>(v.x, v.y);
-                            p2[y + 1] = pack2<F16>(w.x, w.y);
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t p2[16];
+#pragma unroll
+                            for (int y = 0; y < 16; y += 2) {
+                                const int z = 32 * e + 2 * y;
+                                F2 v = fma2(F2{x[z], x[z + 1]}, c2, sub2);
+                                F2 w = fma2(F2{x[z + 2], x[z + 3]}, c2, sub2);
+                                v.x = ex2(v.x), v.y = ex2(v.y), w.x = ex2(w.x), w.y = ex2(w.y);
+                                s0.x += v.x, s0.y += v.y, s1.x += w.x, s1.y += w.y;
+                                p2[y] = pack2<F16>(v.x, v.y);
+                                p2[y + 1] = pack2<F16>(w.x, w.y);
+                            }
+                            tmem_st16(tS + 64 * h + 16 * e, p2);    // over columns that have been read
                         }
-                        tmem_st32(tS + 64 * h, p2);          // over columns that have been read
                     }
                     l += (s0.x + s0.y) + (s1.x + s1.y);
                     tmem_wait_st();
@@ -462,11 +449,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const bool empty = l == 0.0f || (!live && !u.cut.bad);
             const float inv = empty ? 0.0f : 1.0f / l;
             const float log2sum = u.cut.bad ? nanv : empty ? -INFINITY : m + log2f(l);
-            const bool whole = u.t0 == 0 && u.t1 == u.tiles, mine = node < a.N;
+            const bool mine = node < a.N;
             const int64_t orow = (static_cast<int64_t>(u.b) * a.N + node) * a.Hq + u.h * a.g + row % a.g;
             float* prow = part_rows(a, blockIdx.x, u.t0 > 0 ? 0 : 1, MT);
-            if (mine && whole && a.lse) a.lse[orow] = log2sum * kLn2;
-            if (mine && !whole) prow[MT * D + st * kRows + r] = log2sum;
+            if (mine && u.whole && a.lse) a.lse[orow] = log2sum * kLn2;
+            if (mine && !u.whole) prow[MT * D + st * kRows + r] = log2sum;
             unsigned short* dst = static_cast<unsigned short*>(a.out) + orow * D;
             float* pdst = prow + (st * kRows + r) * D;
             for (int i = 0; i < D; i += 16) {
@@ -478,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 if (!mine) continue;
 #pragma unroll
                 for (int y = 0; y < 16; ++y) o[y] = empty ? 0.0f : o[y] * inv;
-                if (whole) {
+                if (u.whole) {
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
                         reinterpret_cast<uint4*>(dst + i)[y] =
@@ -521,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             if (!more) return;
             if ((lstep & 1) == 0 && lt == lnt) {     // the next unit with tiles
                 do {
-                    more = lead.next(a, part, lu);
+                    more = lead.next(a, mts, lu);
                     lnt = more && lu.len > 0 ? lu.t1 - lu.t0 : 0;
                 } while (more && lnt == 0);
                 if (!more) return;
@@ -548,9 +535,49 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         };
         for (uint32_t i = 0; i < kAhead; ++i) begin();
 
-        uint32_t tiles = 0, step = 0;
-        while (walk.next(a, part, u)) {
+        uint32_t tiles = 0, step = 0, nq[2] = {0, 0};
+        while (walk.next(a, mts, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
+            // the queries, once the scores of the unit before are done with theirs
+            const int streams = nt == 0 ? 0 : (u.mt * MT + kRows) / a.g < u.cut.cnt ? 2 : 1;
+            for (int s = 0; s < streams; ++s) {
+                if (q_boxes && w > 0) break;
+                sync.wait(kQEmpty + s, (nq[s]++ & 1) ^ 1);
+                __syncwarp();
+                if (__any_sync(0xffffffffu, *sync.dead != 0)) break;
+                unsigned char* qs = smem + M::q + s * kTile;
+                const int first = u.mt * MT + s * kRows;
+                if (q_boxes) {                       // the 128 rows are the group's heads of whole nodes
+                    const int q_blocks = D > 64 ? 2 : 1;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bars + kQFull + s, q_blocks * kBlock);
+                        for (int i = 0; i < q_blocks; ++i)
+                            tma_load_q(smem_u32(qs + i * kBlock), &map_q, bars + kQFull + s, i * 64, u.h * a.g, first / a.g, u.b);
+                    }
+                    continue;
+                }
+                const int lanes = D > 64 ? 16 : 8, rows = 32 / lanes, ch = lane % lanes;
+                for (int i = w; i < kRows / rows; i += kLoadWarps) {
+                    const int r = i * rows + lane / lanes, row = first + r, node = row / a.g;
+                    if (ch >= D / 8) continue;
+                    const unsigned char* src = a.q + u.b * a.q_sb + node * a.q_sn +
+                                               (static_cast<int64_t>(u.h) * a.g + row % a.g) * a.q_sh + ch * 16;
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (node < u.cut.cnt) {
+                        if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+                            v = *reinterpret_cast<const uint4*>(src);
+                        } else {
+                            const unsigned short* e = reinterpret_cast<const unsigned short*>(src);
+                            v = make_uint4(e[0] | static_cast<uint32_t>(e[1]) << 16, e[2] | static_cast<uint32_t>(e[3]) << 16,
+                                           e[4] | static_cast<uint32_t>(e[5]) << 16, e[6] | static_cast<uint32_t>(e[7]) << 16);
+                        }
+                    }
+                    *reinterpret_cast<uint4*>(qs + chunk_at(r, ch)) = v;
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) sync.arrive(kQFull + s);
+            }
             // e4m3: a thread looks after the exponents of rows p and p + 96 of a
             // tile; a row's page is read two tiles ahead, its exponents one
             const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
@@ -652,7 +679,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 }
             }
         }
-        if (w == 0)                                  // a dead CTA too waits for the copies it has begun
+        if (w == 0 && q_boxes)                       // a dead CTA too waits for the copies it has begun
+            for (int s = 0; s < 2; ++s)
+                for (uint32_t n = 0; nq[s] > 0 && n < kPolls && !sync.poll(kQFull + s, (nq[s] - 1) & 1) && !*sync.dead; ++n) {}
+        if (w == 0)
             for (uint32_t i = lstep > kAhead ? lstep - kAhead : 0; i < lstep; ++i)
                 for (uint32_t n = 0; n < kPolls && !sync.poll(kLand + (E4 ? i & 1 : i % S), (E4 ? i >> 1 : i / S) & 1); ++n) {}
     } else if (lane == 0) {
@@ -674,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 if (ks < nks) mma_ss(d, x + off, y + off, idesc_s, ks > 0);
             }
         };
-        while (walk.next(a, part, u)) {
+        while (walk.next(a, mts, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
             if (nt == 0) continue;
             // stream s has a live row (stream 0 has one in every unit with tiles)
@@ -686,6 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 fence_after();
                 scores(s, step % S);
                 sync.commit(kSFull + s);
+                if (nt == 1) sync.commit(kQEmpty + s);
             }
             sync.commit(kEmpty + step % S);
             for (int t = 0; t < nt; ++t, ++tiles) {
@@ -709,6 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         }
                         scores(s, slot_k);
                         sync.commit(kSFull + s);
+                        if (t + 2 == nt) sync.commit(kQEmpty + s);
                     }
                 }
                 sync.commit(kEmpty + slot_v);
@@ -760,13 +792,37 @@ bool encode(CUtensorMap* map, const AttnArgs& a, unsigned char* cells, bool e4m3
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Queries as [B][N][Hq][D]: a box is the group's heads of 128 / g nodes.  Not
+// for every group and stride: the kernel then copies the rows itself.
+bool encode_q(CUtensorMap* map, const AttnArgs& a) {
+    const EncodeTiled f = encode_tiled();
+    const int64_t strides_in[3] = {a.q_sh, a.q_sn, a.q_sb};
+    if (!f || kRows % a.g || (reinterpret_cast<uintptr_t>(a.q) & 15)) return false;
+    for (int i = 0; i < 3; ++i)
+        if (strides_in[i] <= 0 || strides_in[i] % 16 || strides_in[i] >= (int64_t(1) << 40)) return false;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.c.D), static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.N),
+                                static_cast<cuuint64_t>(a.B)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(a.q_sh), static_cast<cuuint64_t>(a.q_sn), static_cast<cuuint64_t>(a.q_sb)};
+    const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(a.g), static_cast<cuuint32_t>(kRows / a.g), 1u}, one[4] = {1u, 1u, 1u, 1u};
+    return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<unsigned char*>(a.q), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool E4, bool F16>
-cudaError_t launch(AttnArgs a, const CUtensorMap& k, const CUtensorMap& v, int rows, int nsm, cudaStream_t s) {
+cudaError_t launch(AttnArgs a, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, bool q_boxes, int rows, int nsm,
+                   cudaStream_t s) {
     constexpr int bytes = Smem<E4>::bytes;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_tc_kernel<E4, F16>), bytes);
     if (e != cudaSuccess) return e;
+    // the exchange of registers needs a launch that has them
+    static const int regs = [] {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(attn_tc_kernel<E4, F16>)) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs != kRegs) return cudaErrorInvalidKernelImage;
     a.ctas = nsm;
-    attn_tc_kernel<E4, F16><<<static_cast<unsigned>(nsm), kThreads, bytes, s>>>(a, k, v, rows);
+    attn_tc_kernel<E4, F16><<<static_cast<unsigned>(nsm), kThreads, bytes, s>>>(a, k, v, q, rows, q_boxes);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_attn_combine(a, F16, MT, s);
 }
@@ -778,10 +834,11 @@ bool attn_tc_takes(const AttnArgs& a) { return a.c.D <= 128 && a.c.P % 8 == 0 &&
 cudaError_t launch_attn_tc(const AttnArgs& a, bool f16, bool e4m3, int nsm, cudaStream_t s) {
     // rows of one copy: those of a tile that are sure to lie in one page
     const int rows = min(a.c.P & -a.c.P, BN);
-    CUtensorMap k, v;
+    CUtensorMap k, v, q = {};
     if (!encode(&k, a, a.c.k, e4m3, rows) || !encode(&v, a, a.c.v, e4m3, rows)) return cudaErrorInvalidValue;
-    if (e4m3) return f16 ? launch<true, true>(a, k, v, rows, nsm, s) : launch<true, false>(a, k, v, rows, nsm, s);
-    return f16 ? launch<false, true>(a, k, v, rows, nsm, s) : launch<false, false>(a, k, v, rows, nsm, s);
+    const bool boxes = encode_q(&q, a);
+    if (e4m3) return f16 ? launch<true, true>(a, k, v, q, boxes, rows, nsm, s) : launch<true, false>(a, k, v, q, boxes, rows, nsm, s);
+    return f16 ? launch<false, true>(a, k, v, q, boxes, rows, nsm, s) : launch<false, false>(a, k, v, q, boxes, rows, nsm, s);
 }
 
 }  // namespace sdv
