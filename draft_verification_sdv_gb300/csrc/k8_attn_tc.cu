@@ -5,12 +5,15 @@
 // the two contractions bound the step, not the cache's bytes.  A CTA works on
 // 256 rows as two streams of 128 (the rows of one tcgen05.mma), so that while
 // the softmax of one stream runs, the tensor cores multiply for the other:
-//   S_s = Q_s K^T        both operands in shared memory, accumulator in TMEM
-//   P_s = 2^(c S_s - m)  a thread per row reads S_s from TMEM and writes P_s,
-//                        16 bits wide, over S_s (each half of
-//                        the columns over the half it comes from)
-//   O_s += P_s V         P_s from TMEM, V from shared memory, O_s in TMEM
-// TMEM holds S_0, S_1, O_0, O_1: 4 x 128 columns, all 512.
+//   S_s = Q_s K^T        operands in shared memory, accumulator in TMEM
+//   P_s = 2^(c S_s - m)  a thread per row takes its 128 scores into registers,
+//                        which frees S_s for the next tile's product, and
+//                        writes P_s, 16 bits wide, to shared memory
+//   O_s += P_s V         operands in shared memory, accumulator in TMEM
+// TMEM holds S_0, S_1, O_0, O_1: 4 x 128 columns, all 512.  P goes through
+// shared memory rather than TMEM because a product of 128 x 128 x 16 took 65
+// clocks (the tensor cores' rate) with both operands there and 100 with the
+// first in TMEM, and because TMEM has no room for it beside S.
 //
 // O is not rescaled each time the maximum grows: the running reference m only
 // moves when a row's scores pass it by 2^8 (fp32 sums and 16-bit probabilities
@@ -25,7 +28,7 @@
 // may be of any size that is a multiple of 8 rows.  The three warps then hand
 // it over: after a look at the values of rows that some queries do not see
 // (what is not a number there must not meet a zero probability in a product),
-// or, for e4m3 rows, which are copied as they are into a second pair of tiles,
+// or, for e4m3 rows, which land as they are in the upper half of their slot,
 // after bringing them to the queries' type, times their row's power of two.
 //
 // Every wait is bounded: a wait that gives up marks the CTA dead, after which
@@ -51,46 +54,66 @@ constexpr uint32_t kPolls = 1u << 22;
 constexpr float kSlack = 8.0f;           // how far (log2) scores may pass the reference
 
 // Shared memory, bytes from its 1024-aligned start.
-template <bool E4> struct Smem {
-    static constexpr int kSlots = E4 ? 4 : 5;
-    static constexpr int q = kSlots * kTile;
-    static constexpr int stage = q + 2 * kTile;                 // two e4m3 tiles as they come
-    static constexpr int exps = stage + (E4 ? 2 * BN * 128 : 0);    // bytes [2 tiles][keys, values][BN]
-    static constexpr int flag = exps + (E4 ? 4 * BN : 0);       // uint32 [4 tiles][3 warps][4] values that are not numbers
-    static constexpr int bar = flag + 4 * kLoadWarps * 4 * 4;
-    static constexpr int word = bar + (3 * kSlots + 13) * 8;    // TMEM address, dead
-    static constexpr int bytes = word + 8 + 1024;
+constexpr int kSlots = 3;
+
+// Where a softmax warp is: kept in shared memory, its registers hold scores.
+struct SoftmaxState {
+    Walk<MT, BN> walk;
+    Unit u;
 };
-static_assert(Smem<true>::bytes <= 227 * 1024 && Smem<false>::bytes <= 227 * 1024, "one CTA per SM");
+
+struct Smem {
+    static constexpr int q = kSlots * kTile, p = q + 2 * kTile;
+    static constexpr int exps = p + 2 * kTile;                  // bytes [3 tiles][keys, values][BN] (e4m3)
+    static constexpr int flag = exps + 6 * BN;                  // uint32 [4 tiles][3 warps][4] values that are not numbers
+    static constexpr int bar = flag + 4 * kLoadWarps * 4 * 4;
+    static constexpr int word = bar + (3 * kSlots + 15) * 8;    // TMEM address, dead
+    static constexpr int state = word + 8;                      // SoftmaxState [8 warps]
+    static constexpr int bytes = state + 8 * static_cast<int>(sizeof(SoftmaxState)) + 1024;
+};
+static_assert(Smem::bytes <= 227 * 1024, "one CTA per SM");
 
 // Barriers: two per stream of each kind, one for the end, then the ring's (full,
-// empty, landed) and the e4m3 tiles' (empty; landed is the ring's first two).
-enum Bar { kQFull = 0, kSFull = 2, kPFull = 4, kOFull = 6, kQEmpty = 8, kEnd = 10, kRing = 11 };
+// empty, landed).
+enum Bar { kQFull = 0, kQEmpty = 2, kSFull = 4, kSFree = 6, kPFull = 8, kOFull = 10, kEnd = 12, kFull = 13,
+           kEmpty = kFull + kSlots, kLand = kEmpty + kSlots };
+
+// Tiles go through the ring in the order in which they are used: the scores of
+// tile t + 1 are under way before the outputs of tile t, so
+//   K0, K1, V0, K2, V1, ..., K(n-1), V(n-2), V(n-1)
+__device__ __forceinline__ uint32_t key_step(int t) { return t == 0 ? 0u : 2u * t - 1u; }
+__device__ __forceinline__ uint32_t value_step(int t, int n) { return t == n - 1 ? 2u * n - 1u : 2u * t + 2u; }
+__device__ __forceinline__ int step_tile(int j, int n, bool* isv) {
+    *isv = j > 0 && ((j & 1) == 0 || j == 2 * n - 1);
+    return j == 0 ? 0 : (j & 1) == 0 ? j / 2 - 1 : j == 2 * n - 1 ? n - 1 : (j + 1) / 2;
+}
 
 struct Sync {
-    uint64_t* bar;
-    volatile int* dead;
+    uint32_t bar, dead;      // shared-memory addresses
     unsigned* status;
+    __device__ __forceinline__ bool is_dead() const {
+        uint32_t d;
+        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(d) : "r"(dead) : "memory");
+        return d != 0;
+    }
     __device__ __forceinline__ bool poll(int i, uint32_t parity) const {
         uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done) : "r"(smem_u32(bar + i)), "r"(parity) : "memory");
+            : "=r"(done) : "r"(bar + i * 8), "r"(parity) : "memory");
         return done != 0;
     }
     __device__ __forceinline__ void wait(int i, uint32_t parity) const {
-        for (uint32_t n = 0; n < kPolls; ++n) {
-            if (poll(i, parity)) return;
-            if (*dead) return;
-        }
-        *dead = 1;
+        for (uint32_t n = 0; n < kPolls; ++n)
+            if (poll(i, parity) || is_dead()) return;
+        asm volatile("st.volatile.shared.u32 [%0], 1;" ::"r"(dead) : "memory");
         if (status) atomicOr(status, kStatusTimeout);
     }
     __device__ __forceinline__ void arrive(int i) const {
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar + i)) : "memory");
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar + i * 8) : "memory");
     }
     __device__ __forceinline__ void commit(int i) const {
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar + i)) : "memory");
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar + i * 8) : "memory");
     }
 };
 
@@ -113,15 +136,19 @@ __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync
 #define SDV_I4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
 #define SDV_I16(r, i) SDV_I4(r, i), SDV_I4(r, i + 4), SDV_I4(r, i + 8), SDV_I4(r, i + 12)
 
-// 64 columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld64(float* x, uint32_t addr) {
+// 128 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld128(float (&x)[128], uint32_t addr) {
     uint32_t* r = reinterpret_cast<uint32_t*>(x);
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
         "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%128];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,"
+        "%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,"
+        "%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%129];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : SDV_R16(r, 0), SDV_R16(r, 16), SDV_R16(r, 32), SDV_R16(r, 48) : "r"(addr) : "memory");
+        : SDV_R16(r, 0), SDV_R16(r, 16), SDV_R16(r, 32), SDV_R16(r, 48), SDV_R16(r, 64), SDV_R16(r, 80), SDV_R16(r, 96),
+          SDV_R16(r, 112) : "r"(addr), "r"(addr + 64) : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(float (&x)[16], uint32_t addr) {
     uint32_t* r = reinterpret_cast<uint32_t*>(x);
@@ -148,12 +175,6 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t x, uint32_t y, uint3
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(x), "r"(y), "r"(idesc), "r"(add),
                  "r"(kOperandHi) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t x, uint32_t y, uint32_t idesc, uint32_t add) {
-    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(x), "r"(y), "r"(idesc), "r"(add),
-                 "r"(kOperandHi) : "memory");
-}
-
 // Two fp32 operations at once.
 struct F2 { float x, y; };
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
@@ -194,6 +215,17 @@ __device__ __forceinline__ uint32_t sees(const Unit& u, bool tree, int node, con
     const int left = u.cut.cnt - b;                  // nodes from the first position on
     if (left < 32) bits &= left <= 0 ? 0u : (1u << left) - 1u;
     return bits;
+}
+
+// Whether a row sees a position on a page that is not the cache's.
+__device__ __noinline__ bool sees_bad_page(const int32_t* table, int pages, int P, uint4 see, int pos0, int len) {
+    bool bad = false;
+    for (int i = 0; i < BN && pos0 + i < len; ++i) {
+        const int pg = __ldg(table + (pos0 + i) / P);
+        const uint32_t w = i < 32 ? see.x : i < 64 ? see.y : i < 96 ? see.z : see.w;
+        bad |= (w >> (i & 31) & 1) && (pg < 0 || pg >= pages);
+    }
+    return bad;
 }
 
 // Sixteen e4m3 cells times 2^(e - 127), in the queries' type.
@@ -239,36 +271,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                                                               const __grid_constant__ CUtensorMap map_v,
                                                               const __grid_constant__ CUtensorMap map_q, int run_rows,
                                                               bool q_boxes) {
-    using M = Smem<E4>;
-    constexpr uint32_t S = M::kSlots;
-    constexpr int kFull = kRing, kEmpty = kFull + M::kSlots, kLand = kEmpty + M::kSlots, kStage = kLand + M::kSlots;
+    using M = Smem;
+    constexpr uint32_t S = kSlots;
     extern __shared__ unsigned char raw[];
     unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint32_t* s_flag = reinterpret_cast<uint32_t*>(smem + M::flag);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::bar);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::word);
-    volatile int* s_dead = reinterpret_cast<volatile int*>(smem + M::word + 4);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int mts = (a.N * a.g + MT - 1) / MT;
     const int D = a.c.D;
-    const Sync sync{bars, s_dead, a.status};
+    const Sync sync{smem_u32(bars), smem_u32(smem + M::word + 4), a.status};
     if (tid == 0) {
-        *s_dead = 0;
+        s_tmem[1] = 0;                               // dead
         for (int i = 0; i < 2; ++i) {
             mbar_init(bars + kQFull + i, q_boxes ? 1 : kLoadWarps);
             mbar_init(bars + kQEmpty + i, 1);
             mbar_init(bars + kSFull + i, 1);
+            mbar_init(bars + kSFree + i, kRows);
             mbar_init(bars + kPFull + i, kRows);
             mbar_init(bars + kOFull + i, 1);
         }
         mbar_init(bars + kEnd, 1);
-        for (int i = 0; i < M::kSlots; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
             mbar_init(bars + kFull + i, kLoadWarps);
             mbar_init(bars + kEmpty + i, 1);
             mbar_init(bars + kLand + i, 1);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(bars + kStage + i, kLoadWarps);
     }
     if (warp == 11) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(s_tmem)) : "memory");
@@ -283,7 +313,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     Walk<MT, BN> walk;
     walk.start(a, part, mts);
     if (tid == 0) write_desc(a, part, walk);
-    Unit u;
 
     // the softmax warps hold half a row of scores: they take registers that the
     // others do not need (256 * 184 + 128 * 136 = 384 * 168, the launch's own)
@@ -296,13 +325,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int st = warp >> 2, r = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + st * 128, tO = tmem + lanes + 256 + st * 128;
-        // a negative scale turns the scores round; c > 0 so that -inf stays -inf
+        // (a negative scale has turned the queries round); c > 0 so that -inf stays -inf
         const float c = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
-        const bool flip = a.scale_log2 < 0.0f;
         uint32_t n = 0;                              // tiles of this stream so far
         uint32_t nv = 0;                             // tiles of the CTA so far
         int seq = -1, any_bad = 0;
-        while (walk.next(a, mts, u)) {
+        SoftmaxState& state = reinterpret_cast<SoftmaxState*>(smem + M::state)[warp];
+        Unit& u = state.u;
+        if (lane == 0) state.walk = walk;
+        while (true) {
+            int more = 0;
+            if (lane == 0) more = state.walk.next(a, mts, u);
+            __syncwarp();
+            if (!__shfl_sync(0xffffffffu, more, 0)) break;
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
             const int first_row = u.mt * MT + st * kRows;
             const int row = first_row + r, node = row / a.g;
@@ -331,60 +366,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 const int first_mixed = max(u.cut.ctx / BN - u.t0, 0);
                 if (mrow && first_mixed == 0) mask_words(a, mrow, u.t0 * BN - u.cut.ctx, words);
 
+                unsigned char* ps = smem + M::p + st * kTile;
                 for (int t = 0; t < nt; ++t, ++n) {
                     const int pos0 = (u.t0 + t) * BN;
                     const bool mixed = t >= first_mixed;
                     sync.wait(kSFull + st, n & 1);
                     __syncwarp();
                     fence_after();
-                    // the maximum over both halves of the columns; the second half stays
-                    // in registers, the first is read again
-                    float x[64];
-                    uint32_t see[4];
-                    if (mixed) {
-                        const uint32_t step = 2 * (nv + t) + 1;     // the values' place in the ring
-                        sync.wait(kFull + step % S, step / S & 1);
-                        __syncwarp();
+                    float x[128];
+                    tmem_ld128(x, tS);
+                    fence_before();
+                    sync.arrive(kSFree + st);
+                    uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+                    if (mixed) {                     // what the row does not see
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             see[i] = live ? sees(u, mrow != nullptr, node, words, pos0, i) : 0u;
-                            const uint32_t* f = s_flag + ((nv + t) & 3) * (kLoadWarps * 4) + i;
-                            if (see[i] & (f[0] | f[4] | f[8])) nan_row = true;
-                            if (any_bad)
-                                for (int y = 0; y < 32; ++y) {
-                                    const int pos = pos0 + 32 * i + y;
-                                    if (pos >= u.len || !(see[i] >> y & 1)) continue;
-                                    const int pg = __ldg(table + pos / a.c.P);
-                                    nan_row |= pg < 0 || pg >= a.c.pages;
-                                }
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) x[32 * i + y] = see[i] >> y & 1 ? x[32 * i + y] : -INFINITY;
                         }
-                        __syncwarp();
-                    } else if (any_bad) {
-                        for (int pg = pos0 / a.c.P; pg <= (pos0 + BN - 1) / a.c.P; ++pg) {
-                            const int q = __ldg(table + pg);
-                            nan_row |= q < 0 || q >= a.c.pages;
-                        }
+                        if (mrow && t + 1 < nt) mask_words(a, mrow, pos0 + BN - u.cut.ctx, words);
+                    } else if (mrow && t + 1 == first_mixed && t + 1 < nt) {
+                        mask_words(a, mrow, pos0 + BN - u.cut.ctx, words);
                     }
-                    auto hide = [&](int h) {         // what the row does not see of half h
-                        if (flip)
+                    if (any_bad) nan_row |= sees_bad_page(table, a.c.pages, a.c.P, make_uint4(see[0], see[1], see[2], see[3]), pos0, u.len);
+                    float t4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                            for (int y = 0; y < 64; ++y) x[y] = -x[y];
-                        if (mixed)
+                    for (int y = 4; y < 124; y += 8)
 #pragma unroll
-                            for (int y = 0; y < 64; ++y)
-                                x[y] = see[2 * h + (y >> 5)] >> (y & 31) & 1 ? x[y] : -INFINITY;
-                    };
-                    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        tmem_ld64(x, tS + 64 * h);
-                        hide(h);
-#pragma unroll
-                        for (int y = 0; y < 64; y += 8)
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) t4[z] = max3(t4[z], x[y + z], x[y + 4 + z]);
-                    }
-                    float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                        for (int z = 0; z < 4; ++z) t4[z] = max3(t4[z], x[y + z], x[y + 4 + z]);
+                    float top = max3(max3(t4[0], x[124], x[125]), max3(t4[1], x[126], x[127]), fmaxf(t4[2], t4[3]));
                     top = top == -INFINITY ? top : top * c;
                     // the reference moves when the scores pass it by far
                     const bool move = top > m + kSlack || (m == -INFINITY && top != -INFINITY);
@@ -403,43 +414,43 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                             for (int y = 0; y < 16; ++y) o2[y] = __float_as_uint(o[y] * by);
                             tmem_st16(tO + i, o2);
                         }
+                        tmem_wait_st();
+                        fence_before();
                     }
                     if (move) m = top;
                     const float sub = m == -INFINITY ? 0.0f : -m;
                     const F2 c2{c, c}, sub2{sub, sub};
-                    F2 s0{0.0f, 0.0f}, s1{0.0f, 0.0f};
+                    float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    uint32_t pk[64];
 #pragma unroll
-                    for (int h = 1; h >= 0; --h) {
-                        if (h == 0) {
-                            tmem_ld64(x, tS);
-                            hide(0);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            uint32_t p2[16];
-#pragma unroll
-                            for (int y = 0; y < 16; y += 2) {
-                                const int z = 32 * e + 2 * y;
-                                F2 v = fma2(F2{x[z], x[z + 1]}, c2, sub2);
-                                F2 w = fma2(F2{x[z + 2], x[z + 3]}, c2, sub2);
-                                v.x = ex2(v.x), v.y = ex2(v.y), w.x = ex2(w.x), w.y = ex2(w.y);
-                                s0.x += v.x, s0.y += v.y, s1.x += w.x, s1.y += w.y;
-                                p2[y] = pack2<F16>(v.x, v.y);
-                                p2[y + 1] = pack2<F16>(w.x, w.y);
-                            }
-                            tmem_st16(tS + 64 * h + 16 * e, p2);    // over columns that have been read
-                        }
+                    for (int y = 0; y < 64; y += 2) {
+                        F2 v = fma2(F2{x[2 * y], x[2 * y + 1]}, c2, sub2);
+                        F2 w = fma2(F2{x[2 * y + 2], x[2 * y + 3]}, c2, sub2);
+                        v.x = ex2(v.x), v.y = ex2(v.y), w.x = ex2(w.x), w.y = ex2(w.y);
+                        s4[0] += v.x, s4[1] += v.y, s4[2] += w.x, s4[3] += w.y;
+                        pk[y] = pack2<F16>(v.x, v.y);
+                        pk[y + 1] = pack2<F16>(w.x, w.y);
                     }
-                    l += (s0.x + s0.y) + (s1.x + s1.y);
-                    tmem_wait_st();
-                    fence_before();
+                    l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                    if (t > 0) sync.wait(kOFull + st, (n - 1) & 1);     // the product before has read its P
+#pragma unroll
+                    for (int ch = 0; ch < 16; ++ch)
+                        *reinterpret_cast<uint4*>(ps + chunk_at(r, ch)) = make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
+                    fence_async();
+                    if (mixed) {                     // values that are not numbers, among those that the row sees
+                        const uint32_t step = 2 * nv + value_step(t, nt);
+                        sync.wait(kFull + step % S, step / S & 1);
+                        const uint32_t* f = s_flag + ((nv + t) & 3) * (kLoadWarps * 4);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (see[i] & (f[i] | f[4 + i] | f[8 + i])) nan_row = true;
+                    }
                     sync.arrive(kPFull + st);
-                    if (mrow && t + 1 >= first_mixed && t + 1 < nt) mask_words(a, mrow, pos0 + BN - u.cut.ctx, words);
                 }
                 sync.wait(kOFull + st, (n - 1) & 1);
                 __syncwarp();
                 fence_after();
-                if (*sync.dead) nan_row = true;
+                if (sync.is_dead()) nan_row = true;
             }
             nv += nt;
 
@@ -487,54 +498,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int LR = CH > 8 ? 16 : CH > 4 ? 8 : 4; // lanes of a row
         const int RP = 32 / LR, lr = lane / LR, lc = lane % LR;     // rows of a warp's step
         const uint32_t group = ((1u << LR) - 1u) << (lr * LR);
-        constexpr uint32_t kAhead = E4 ? 2 : 3;      // steps (tiles of keys or of values) under way
+        constexpr uint32_t kAhead = kSlots - 1;      // steps (tiles of keys or of values) under way
 
         // warp 8: begins the copies of the next step; a walk of its own, ahead
         Walk<MT, BN> lead;
         Unit lu{};
         lead.start(a, part, mts);
-        int lt = 0, lnt = 0, lpage = -1;
+        int lj = 0, lnt = 0, lpage = -1;             // step of the unit, its tiles
         uint32_t lstep = 0;
         bool more = w == 0;
         const int blocks = !E4 && D > 64 ? 2 : 1;
         const int copy = lane / blocks, block = lane % blocks;
-        auto lead_page = [&](int t) {                // the page of this lane's rows of tile t
-            const int pos = (lu.t0 + t) * BN + copy * run_rows;
-            const int pg = copy * run_rows < BN && t < lnt && pos < lu.len
+        auto lead_page = [&]() {                     // the page of this lane's rows at the unit's step
+            bool isv;
+            const int pos = (lu.t0 + step_tile(lj, lnt, &isv)) * BN + copy * run_rows;
+            const int pg = copy * run_rows < BN && lj < 2 * lnt && pos < lu.len
                                ? __ldg(a.table + static_cast<int64_t>(lu.b) * a.max_pages + pos / a.c.P) : -1;
             return pg < a.c.pages ? pg : -1;
         };
         auto begin = [&]() {
             if (!more) return;
-            if ((lstep & 1) == 0 && lt == lnt) {     // the next unit with tiles
+            if (lj == 2 * lnt) {                     // the next unit with tiles
                 do {
                     more = lead.next(a, mts, lu);
                     lnt = more && lu.len > 0 ? lu.t1 - lu.t0 : 0;
                 } while (more && lnt == 0);
                 if (!more) return;
-                lt = 0;
-                lpage = lead_page(0);
+                lj = 0;
+                lpage = lead_page();
             }
-            const bool isv = lstep & 1;
-            const uint32_t slot = E4 ? lstep & 1 : lstep % S, phase = E4 ? lstep >> 1 & 1 : lstep / S & 1;
-            sync.wait((E4 ? kStage : kEmpty) + slot, phase ^ 1);
+            bool isv;
+            const int pos = (lu.t0 + step_tile(lj, lnt, &isv)) * BN + copy * run_rows;
+            const uint32_t slot = lstep % S;
+            sync.wait(kEmpty + slot, (lstep / S & 1) ^ 1);
             __syncwarp();
-            more = !__any_sync(0xffffffffu, *sync.dead != 0);
+            more = !__any_sync(0xffffffffu, sync.is_dead());
             if (!more) return;
             const bool active = lpage >= 0;
             const uint32_t n = __popc(__ballot_sync(0xffffffffu, active));
             if (lane == 0) mbar_arrive_expect_tx(bars + kLand + slot, n * run_rows * 128);
             __syncwarp();
-            if (active) {
-                const int pos = (lu.t0 + lt) * BN + copy * run_rows;
-                tma_load(smem_u32(smem + (E4 ? M::stage + slot * (BN * 128) : slot * kTile + block * kBlock) + copy * run_rows * 128),
-                         isv ? &map_v : &map_k, bars + kLand + slot, block * 64, lu.h * a.c.P + pos % a.c.P, lpage);
-            }
+            if (active)                              // e4m3 lands in the slot's upper half
+                tma_load(smem_u32(smem + slot * kTile + (E4 ? kBlock : block * kBlock) + copy * run_rows * 128), isv ? &map_v : &map_k,
+                         bars + kLand + slot, block * 64, lu.h * a.c.P + pos % a.c.P, lpage);
             ++lstep;
-            if (isv) lpage = lead_page(++lt);
+            ++lj;
+            lpage = lead_page();
         };
         for (uint32_t i = 0; i < kAhead; ++i) begin();
 
+        Unit u;
         uint32_t tiles = 0, step = 0, nq[2] = {0, 0};
         while (walk.next(a, mts, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
@@ -544,9 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 if (q_boxes && w > 0) break;
                 sync.wait(kQEmpty + s, (nq[s]++ & 1) ^ 1);
                 __syncwarp();
-                if (__any_sync(0xffffffffu, *sync.dead != 0)) break;
+                if (__any_sync(0xffffffffu, sync.is_dead())) break;
                 unsigned char* qs = smem + M::q + s * kTile;
                 const int first = u.mt * MT + s * kRows;
+                const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
                 if (q_boxes) {                       // the 128 rows are the group's heads of whole nodes
                     const int q_blocks = D > 64 ? 2 : 1;
                     if (lane == 0) {
@@ -572,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                                            e[4] | static_cast<uint32_t>(e[5]) << 16, e[6] | static_cast<uint32_t>(e[7]) << 16);
                         }
                     }
-                    *reinterpret_cast<uint4*>(qs + chunk_at(r, ch)) = v;
+                    *reinterpret_cast<uint4*>(qs + chunk_at(r, ch)) = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
                 }
                 fence_async();
                 __syncwarp();
@@ -603,15 +617,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     exps_at(0, i, page[0][i]);
                 }
             }
-            for (int t = 0; t < nt; ++t, ++tiles) {
+#pragma unroll 1
+            for (int j = 0; j < 2 * nt; ++j, ++step) {
+                bool isv;
+                const int t = step_tile(j, nt, &isv);
+                const uint32_t tile = tiles + t, slot = step % S;
                 const int from = min(max(u.cut.ctx - (u.t0 + t) * BN, 0), BN);   // first row that some do not see
-                if constexpr (E4) {
+                if (E4 && !isv) {                    // the exponents of tile t
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int rr = p + i * kLoadThreads;
                         if (rr < BN) {
-                            smem[M::exps + (tiles & 1) * 2 * BN + rr] = static_cast<unsigned char>(ke[i]);
-                            smem[M::exps + (tiles & 1) * 2 * BN + BN + rr] = static_cast<unsigned char>(ve[i]);
+                            smem[M::exps + tile % 3 * 2 * BN + rr] = static_cast<unsigned char>(ke[i]);
+                            smem[M::exps + tile % 3 * 2 * BN + BN + rr] = static_cast<unsigned char>(ve[i]);
                         }
                         page[0][i] = page[1][i];
                         page[1][i] = page_at(t + 2, i);
@@ -619,72 +637,61 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     }
                     bar_sync(1, kLoadThreads);
                 }
-#pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv, ++step) {
-                    const uint32_t slot = step % S, phase = step / S & 1;
-                    if constexpr (E4) {
-                        sync.wait(kLand + (step & 1), step >> 1 & 1);
-                        sync.wait(kEmpty + slot, phase ^ 1);
-                    } else {
-                        sync.wait(kLand + slot, phase);
+                sync.wait(kLand + slot, step / S & 1);
+                __syncwarp();
+                unsigned char* base = smem + slot * kTile;
+                const bool check = isv && from < BN;
+                if (E4 || check) {
+                    uint32_t* flags = s_flag + (tile & 3) * (kLoadWarps * 4) + w * 4;
+                    if (check) {
+                        if (lane < 4) flags[lane] = 0;
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    unsigned char* base = smem + slot * kTile;
-                    const bool check = kv && from < BN;
-                    if (E4 || check) {
-                        uint32_t* flags = s_flag + (tiles & 3) * (kLoadWarps * 4) + w * 4;
+                    const unsigned char* ex = smem + M::exps + (tile % 3 * 2 + isv) * BN;
+                    for (int q = w; q < BN / RP; q += kLoadWarps) {
+                        const int r = q * RP + lr;
+                        uint32_t o[8];
+                        bool bad = false;
+                        constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
+                        if (lc < CH) {
+                            if constexpr (E4) {
+                                widen16<F16>(*reinterpret_cast<const uint4*>(base + kBlock + r * 128 + lc * 16), ex[r], o);
+                            } else {
+                                const uint4 v = *reinterpret_cast<const uint4*>(base + chunk_at(r, lc));
+                                o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+                            }
+                            if (check && r >= from)
+#pragma unroll
+                                for (int i = 0; i < (E4 ? 8 : 4); ++i)
+                                    bad |= (o[i] & top) == top || (o[i] >> 16 & top) == top;
+                        }
+                        bool row_bad = false;
                         if (check) {
-                            if (lane < 4) flags[lane] = 0;
-                            __syncwarp();
+                            row_bad = (__ballot_sync(0xffffffffu, bad) & group) != 0;
+                            if (row_bad && lc == 0) atomicOr(flags + (r >> 5), 1u << (r & 31));
                         }
-                        const unsigned char* stage = smem + M::stage + (step & 1) * (BN * 128);
-                        const unsigned char* ex = smem + M::exps + ((tiles & 1) * 2 + kv) * BN;
-                        for (int q = w; q < BN / RP; q += kLoadWarps) {
-                            const int r = q * RP + lr;
-                            uint32_t o[8];
-                            bool bad = false;
-                            constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
-                            if (lc < CH) {
-                                if constexpr (E4) {
-                                    widen16<F16>(*reinterpret_cast<const uint4*>(stage + r * 128 + lc * 16), ex[r], o);
-                                } else {
-                                    const uint4 v = *reinterpret_cast<const uint4*>(base + chunk_at(r, lc));
-                                    o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
-                                }
-                                if (check && r >= from)
+                        __syncwarp();                // a row's lanes have read it before it is written over
+                        if (lc < CH && (E4 || row_bad)) {
 #pragma unroll
-                                    for (int i = 0; i < (E4 ? 8 : 4); ++i)
-                                        bad |= (o[i] & top) == top || (o[i] >> 16 & top) == top;
-                            }
-                            bool row_bad = false;
-                            if (check) {
-                                row_bad = (__ballot_sync(0xffffffffu, bad) & group) != 0;
-                                if (row_bad && lc == 0) atomicOr(flags + (r >> 5), 1u << (r & 31));
-                            }
-                            if (lc < CH && (E4 || row_bad)) {
-#pragma unroll
-                                for (int i = 0; i < (E4 ? 8 : 4); i += 4)
-                                    *reinterpret_cast<uint4*>(base + chunk_at(r, E4 ? 2 * lc + i / 4 : lc)) =
-                                        row_bad ? make_uint4(0, 0, 0, 0) : make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                            }
+                            for (int i = 0; i < (E4 ? 8 : 4); i += 4)
+                                *reinterpret_cast<uint4*>(base + chunk_at(r, E4 ? 2 * lc + i / 4 : lc)) =
+                                    row_bad ? make_uint4(0, 0, 0, 0) : make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                         }
                     }
-                    fence_async();
-                    __syncwarp();
-                    if (lane == 0) {
-                        sync.arrive(kFull + slot);
-                        if constexpr (E4) sync.arrive(kStage + (step & 1));
-                    }
-                    begin();
                 }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) sync.arrive(kFull + slot);
+                begin();
             }
+            tiles += nt;
         }
         if (w == 0 && q_boxes)                       // a dead CTA too waits for the copies it has begun
             for (int s = 0; s < 2; ++s)
-                for (uint32_t n = 0; nq[s] > 0 && n < kPolls && !sync.poll(kQFull + s, (nq[s] - 1) & 1) && !*sync.dead; ++n) {}
+                for (uint32_t n = 0; nq[s] > 0 && n < kPolls && !sync.poll(kQFull + s, (nq[s] - 1) & 1) && !sync.is_dead(); ++n) {}
         if (w == 0)
             for (uint32_t i = lstep > kAhead ? lstep - kAhead : 0; i < lstep; ++i)
-                for (uint32_t n = 0; n < kPolls && !sync.poll(kLand + (E4 ? i & 1 : i % S), (E4 ? i >> 1 : i / S) & 1); ++n) {}
+                for (uint32_t n = 0; n < kPolls && !sync.poll(kLand + i % S, i / S & 1); ++n) {}
     } else if (lane == 0) {
         // ---------------- products ----------------
         constexpr uint32_t type = F16 ? 0u : 1u;
@@ -694,58 +701,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const uint32_t ring_k = operand_lo(smem_u32(smem), 16), ring_v = operand_lo(smem_u32(smem), kBlock);
         const uint32_t q0 = operand_lo(smem_u32(smem + M::q), 16);
         const int nks = D / 16;
-        uint32_t n[2] = {0, 0}, q[2] = {0, 0}, tiles = 0;
-        auto scores = [&](int s, uint32_t key_slot) {
-            if (*sync.dead) return;
-            const uint32_t x = q0 + s * (kTile >> 4), y = ring_k + key_slot * (kTile >> 4), d = tmem + s * 128;
+        const uint32_t p0 = operand_lo(smem_u32(smem + M::p), 16);
+        Unit u;
+        uint32_t n[2] = {0, 0}, np[2] = {0, 0}, q[2] = {0, 0}, tiles = 0;      // scores, outputs and queries so far
+        auto scores = [&](int s, uint32_t slot, bool last) {
+            if (n[s] > 0) sync.wait(kSFree + s, (n[s] - 1) & 1);
+            ++n[s];
+            fence_after();
+            if (!sync.is_dead()) {
+                const uint32_t x = q0 + s * (kTile >> 4), y = ring_k + slot * (kTile >> 4), d = tmem + s * 128;
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-                const uint32_t off = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
-                if (ks < nks) mma_ss(d, x + off, y + off, idesc_s, ks > 0);
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint32_t off = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
+                    if (ks < nks) mma_ss(d, x + off, y + off, idesc_s, ks > 0);
+                }
             }
+            sync.commit(kSFull + s);
+            if (last) sync.commit(kQEmpty + s);
         };
         while (walk.next(a, mts, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
             if (nt == 0) continue;
             // stream s has a live row (stream 0 has one in every unit with tiles)
             const int streams = (u.mt * MT + kRows) / a.g < u.cut.cnt ? 2 : 1;
-            uint32_t step = 2 * tiles;               // keys' and values' places in the ring
-            sync.wait(kFull + step % S, step / S & 1);
+            const uint32_t base = 2 * tiles;
+            sync.wait(kFull + base % S, base / S & 1);
             for (int s = 0; s < streams; ++s) {
                 sync.wait(kQFull + s, q[s]++ & 1);
-                fence_after();
-                scores(s, step % S);
-                sync.commit(kSFull + s);
-                if (nt == 1) sync.commit(kQEmpty + s);
+                scores(s, base % S, nt == 1);
             }
-            sync.commit(kEmpty + step % S);
-            for (int t = 0; t < nt; ++t, ++tiles) {
-                const bool more = t + 1 < nt;
-                const uint32_t sv = 2 * tiles + 1, sk = sv + 1, slot_v = sv % S, slot_k = sk % S;
+            sync.commit(kEmpty + base % S);
+            for (int t = 0; t < nt; ++t) {
+                if (t + 1 < nt) {
+                    const uint32_t sk = base + key_step(t + 1);
+                    sync.wait(kFull + sk % S, sk / S & 1);
+                    for (int s = 0; s < streams; ++s) scores(s, sk % S, t + 2 == nt);
+                    sync.commit(kEmpty + sk % S);
+                }
+                const uint32_t sv = base + value_step(t, nt), slot_v = sv % S;
                 for (int s = 0; s < streams; ++s) {
-                    sync.wait(kPFull + s, n[s]++ & 1);
+                    sync.wait(kPFull + s, np[s]++ & 1);
                     if (s == 0) sync.wait(kFull + slot_v, sv / S & 1);
                     fence_after();
-                    if (!*sync.dead) {
-                        const uint32_t y = ring_v + slot_v * (kTile >> 4), d = tmem + 256 + s * 128, x = tmem + s * 128;
+                    if (!sync.is_dead()) {
+                        const uint32_t x = p0 + s * (kTile >> 4), y = ring_v + slot_v * (kTile >> 4), d = tmem + 256 + s * 128;
 #pragma unroll
                         for (int ks = 0; ks < BN / 16; ++ks)
-                            mma_ts(d, x + (ks >> 2) * 64 + (ks & 3) * 8, y + ks * (2048 >> 4), idesc_o, t > 0 || ks > 0);
+                            mma_ss(d, x + (((ks >> 2) * kBlock + (ks & 3) * 32) >> 4), y + ks * (2048 >> 4), idesc_o, t > 0 || ks > 0);
                     }
                     sync.commit(kOFull + s);
-                    if (more) {
-                        if (s == 0) {
-                            sync.wait(kFull + slot_k, sk / S & 1);
-                            fence_after();
-                        }
-                        scores(s, slot_k);
-                        sync.commit(kSFull + s);
-                        if (t + 2 == nt) sync.commit(kQEmpty + s);
-                    }
                 }
                 sync.commit(kEmpty + slot_v);
-                if (more) sync.commit(kEmpty + slot_k);
             }
+            tiles += nt;
         }
         sync.commit(kEnd);                           // nothing is under way any more
         sync.wait(kEnd, 0);
@@ -812,7 +820,7 @@ bool encode_q(CUtensorMap* map, const AttnArgs& a) {
 template <bool E4, bool F16>
 cudaError_t launch(AttnArgs a, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, bool q_boxes, int rows, int nsm,
                    cudaStream_t s) {
-    constexpr int bytes = Smem<E4>::bytes;
+    constexpr int bytes = Smem::bytes;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_tc_kernel<E4, F16>), bytes);
     if (e != cudaSuccess) return e;
     // the exchange of registers needs a launch that has them
@@ -836,7 +844,8 @@ cudaError_t launch_attn_tc(const AttnArgs& a, bool f16, bool e4m3, int nsm, cuda
     const int rows = min(a.c.P & -a.c.P, BN);
     CUtensorMap k, v, q = {};
     if (!encode(&k, a, a.c.k, e4m3, rows) || !encode(&v, a, a.c.v, e4m3, rows)) return cudaErrorInvalidValue;
-    const bool boxes = encode_q(&q, a);
+    // (a negative scale is the queries' sign, which a copy by boxes leaves alone)
+    const bool boxes = a.scale_log2 >= 0.0f && encode_q(&q, a);
     if (e4m3) return f16 ? launch<true, true>(a, k, v, q, boxes, rows, nsm, s) : launch<true, false>(a, k, v, q, boxes, rows, nsm, s);
     return f16 ? launch<false, true>(a, k, v, q, boxes, rows, nsm, s) : launch<false, false>(a, k, v, q, boxes, rows, nsm, s);
 }
