@@ -50,7 +50,7 @@ constexpr int MT = 2 * kRows, BN = 128;
 constexpr int kBlock = BN * 128;         // bytes of 128 rows of 64 16-bit cells
 constexpr int kTile = 2 * kBlock;        // ... of 128
 constexpr int kLoadWarps = 3, kLoadThreads = 32 * kLoadWarps;
-constexpr uint32_t kPolls = 1u << 22;
+constexpr uint32_t kPolls = 1u << 17, kPollNs = 20000;     // a wait's limit: so many polls, each sleeping that long at most
 constexpr float kSlack = 8.0f;           // how far (log2) scores may pass the reference
 
 // Shared memory, bytes from its 1024-aligned start.
@@ -96,11 +96,13 @@ struct Sync {
         asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(d) : "r"(dead) : "memory");
         return d != 0;
     }
+    // sleeps until the phase is over or for some time: a warp that keeps asking
+    // holds up the shared-memory accesses of the others
     __device__ __forceinline__ bool poll(int i, uint32_t parity) const {
         uint32_t done;
         asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done) : "r"(bar + i * 8), "r"(parity) : "memory");
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done) : "r"(bar + i * 8), "r"(parity), "r"(kPollNs) : "memory");
         return done != 0;
     }
     __device__ __forceinline__ void wait(int i, uint32_t parity) const {
@@ -175,6 +177,14 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t x, uint32_t y, uint3
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(x), "r"(y), "r"(idesc), "r"(add),
                  "r"(kOperandHi) : "memory");
 }
+// One thread of a converged warp, and a value that is the same in all of them.
+__device__ __forceinline__ bool elected() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // Two fp32 operations at once.
 struct F2 { float x, y; };
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
@@ -289,8 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             mbar_init(bars + kQFull + i, q_boxes ? 1 : kLoadWarps);
             mbar_init(bars + kQEmpty + i, 1);
             mbar_init(bars + kSFull + i, 1);
-            mbar_init(bars + kSFree + i, kRows);
-            mbar_init(bars + kPFull + i, kRows);
+            mbar_init(bars + kSFree + i, kRows / 32);    // a warp arrives once: 32 arrivals take turns
+            mbar_init(bars + kPFull + i, kRows / 32);
             mbar_init(bars + kOFull + i, 1);
         }
         mbar_init(bars + kEnd, 1);
@@ -376,7 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     float x[128];
                     tmem_ld128(x, tS);
                     fence_before();
-                    sync.arrive(kSFree + st);
+                    __syncwarp();
+                    if (lane == 0) sync.arrive(kSFree + st);
                     uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
                     if (mixed) {                     // what the row does not see
 #pragma unroll
@@ -445,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         for (int i = 0; i < 4; ++i)
                             if (see[i] & (f[i] | f[4 + i] | f[8 + i])) nan_row = true;
                     }
-                    sync.arrive(kPFull + st);
+                    __syncwarp();
+                    if (lane == 0) sync.arrive(kPFull + st);
                 }
                 sync.wait(kOFull + st, (n - 1) & 1);
                 __syncwarp();
@@ -553,8 +565,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
             // the queries, once the scores of the unit before are done with theirs
             const int streams = nt == 0 ? 0 : (u.mt * MT + kRows) / a.g < u.cut.cnt ? 2 : 1;
-            for (int s = 0; s < streams; ++s) {
-                if (q_boxes && w > 0) break;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (s >= streams || (q_boxes && w > 0)) break;
                 sync.wait(kQEmpty + s, (nq[s]++ & 1) ^ 1);
                 __syncwarp();
                 if (__any_sync(0xffffffffu, sync.is_dead())) break;
@@ -687,37 +700,51 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             tiles += nt;
         }
         if (w == 0 && q_boxes)                       // a dead CTA too waits for the copies it has begun
+#pragma unroll
             for (int s = 0; s < 2; ++s)
                 for (uint32_t n = 0; nq[s] > 0 && n < kPolls && !sync.poll(kQFull + s, (nq[s] - 1) & 1) && !sync.is_dead(); ++n) {}
         if (w == 0)
             for (uint32_t i = lstep > kAhead ? lstep - kAhead : 0; i < lstep; ++i)
                 for (uint32_t n = 0; n < kPolls && !sync.poll(kLand + i % S, i / S & 1); ++n) {}
-    } else if (lane == 0) {
+    } else {
         // ---------------- products ----------------
+        // The whole warp walks and waits, so that the operands stay uniform; one
+        // elected thread issues.
         constexpr uint32_t type = F16 ? 0u : 1u;
         const uint32_t common = (1u << 4) | (type << 7) | (type << 10) | (8u << 24);    // fp32 += 16 bits, 128 rows
         const uint32_t idesc_s = common | (static_cast<uint32_t>(BN / 8) << 17);
         const uint32_t idesc_o = common | (1u << 16) | (static_cast<uint32_t>(D / 8) << 17);    // V is MN-major
         const uint32_t ring_k = operand_lo(smem_u32(smem), 16), ring_v = operand_lo(smem_u32(smem), kBlock);
-        const uint32_t q0 = operand_lo(smem_u32(smem + M::q), 16);
+        const uint32_t q0 = operand_lo(smem_u32(smem + M::q), 16), p0 = operand_lo(smem_u32(smem + M::p), 16);
         const int nks = D / 16;
-        const uint32_t p0 = operand_lo(smem_u32(smem + M::p), 16);
         Unit u;
         uint32_t n[2] = {0, 0}, np[2] = {0, 0}, q[2] = {0, 0}, tiles = 0;      // scores, outputs and queries so far
         auto scores = [&](int s, uint32_t slot, bool last) {
             if (n[s] > 0) sync.wait(kSFree + s, (n[s] - 1) & 1);
             ++n[s];
+            __syncwarp();
             fence_after();
-            if (!sync.is_dead()) {
-                const uint32_t x = q0 + s * (kTile >> 4), y = ring_k + slot * (kTile >> 4), d = tmem + s * 128;
+            const bool dead = sync.is_dead();
+            const uint32_t x = uniform(q0 + s * (kTile >> 4)), y = uniform(ring_k + slot * (kTile >> 4)), d = uniform(tmem + s * 128);
+            if (elected()) {
+                if (!dead) {
+                    if (nks == 8) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint32_t off = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
-                    if (ks < nks) mma_ss(d, x + off, y + off, idesc_s, ks > 0);
+                        for (int ks = 0; ks < 8; ++ks) {
+                            const uint32_t off = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
+                            mma_ss(d, x + off, y + off, idesc_s, ks > 0);
+                        }
+                    } else {
+                        for (int ks = 0; ks < nks; ++ks) {
+                            const uint32_t off = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
+                            mma_ss(d, x + off, y + off, idesc_s, ks > 0);
+                        }
+                    }
                 }
+                sync.commit(kSFull + s);
+                if (last) sync.commit(kQEmpty + s);
             }
-            sync.commit(kSFull + s);
-            if (last) sync.commit(kQEmpty + s);
+            __syncwarp();
         };
         while (walk.next(a, mts, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
@@ -726,36 +753,52 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const int streams = (u.mt * MT + kRows) / a.g < u.cut.cnt ? 2 : 1;
             const uint32_t base = 2 * tiles;
             sync.wait(kFull + base % S, base / S & 1);
-            for (int s = 0; s < streams; ++s) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (s >= streams) break;
                 sync.wait(kQFull + s, q[s]++ & 1);
                 scores(s, base % S, nt == 1);
             }
-            sync.commit(kEmpty + base % S);
+            if (elected()) sync.commit(kEmpty + base % S);
+            __syncwarp();
             for (int t = 0; t < nt; ++t) {
                 if (t + 1 < nt) {
                     const uint32_t sk = base + key_step(t + 1);
                     sync.wait(kFull + sk % S, sk / S & 1);
-                    for (int s = 0; s < streams; ++s) scores(s, sk % S, t + 2 == nt);
-                    sync.commit(kEmpty + sk % S);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+                        if (s < streams) scores(s, sk % S, t + 2 == nt);
+                    if (elected()) sync.commit(kEmpty + sk % S);
+                    __syncwarp();
                 }
                 const uint32_t sv = base + value_step(t, nt), slot_v = sv % S;
-                for (int s = 0; s < streams; ++s) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (s >= streams) break;
                     sync.wait(kPFull + s, np[s]++ & 1);
                     if (s == 0) sync.wait(kFull + slot_v, sv / S & 1);
+                    __syncwarp();
                     fence_after();
-                    if (!sync.is_dead()) {
-                        const uint32_t x = p0 + s * (kTile >> 4), y = ring_v + slot_v * (kTile >> 4), d = tmem + 256 + s * 128;
+                    const bool dead = sync.is_dead();
+                    const uint32_t x = uniform(p0 + s * (kTile >> 4)), y = uniform(ring_v + slot_v * (kTile >> 4));
+                    const uint32_t d = uniform(tmem + 256 + s * 128), first = uniform(t > 0);
+                    if (elected()) {
+                        if (!dead) {
 #pragma unroll
-                        for (int ks = 0; ks < BN / 16; ++ks)
-                            mma_ss(d, x + (((ks >> 2) * kBlock + (ks & 3) * 32) >> 4), y + ks * (2048 >> 4), idesc_o, t > 0 || ks > 0);
+                            for (int ks = 0; ks < BN / 16; ++ks)
+                                mma_ss(d, x + (((ks >> 2) * kBlock + (ks & 3) * 32) >> 4), y + ks * (2048 >> 4), idesc_o, ks > 0 ? 1u : first);
+                        }
+                        sync.commit(kOFull + s);
                     }
-                    sync.commit(kOFull + s);
+                    __syncwarp();
                 }
-                sync.commit(kEmpty + slot_v);
+                if (elected()) sync.commit(kEmpty + slot_v);
+                __syncwarp();
             }
             tiles += nt;
         }
-        sync.commit(kEnd);                           // nothing is under way any more
+        if (elected()) sync.commit(kEnd);            // nothing is under way any more
+        __syncwarp();
         sync.wait(kEnd, 0);
     }
     __syncwarp();
