@@ -6,14 +6,13 @@
 // 256 rows as two streams of 128 (the rows of one tcgen05.mma), so that while
 // the softmax of one stream runs, the tensor cores multiply for the other:
 //   S_s = Q_s K^T        operands in shared memory, accumulator in TMEM
-//   P_s = 2^(c S_s - m)  a thread per row takes its 128 scores into registers,
-//                        which frees S_s for the next tile's product, and
-//                        writes P_s, 16 bits wide, to shared memory
-//   O_s += P_s V         operands in shared memory, accumulator in TMEM
-// TMEM holds S_0, S_1, O_0, O_1: 4 x 128 columns, all 512.  P goes through
-// shared memory rather than TMEM because a product of 128 x 128 x 16 took 65
-// clocks (the tensor cores' rate) with both operands there and 100 with the
-// first in TMEM, and because TMEM has no room for it beside S.
+//   P_s = 2^(c S_s - m)  a thread per row takes its 128 scores into registers
+//                        and writes P_s, 16 bits wide, over S_s
+//   O_s += P_s V         P_s from TMEM, V from shared memory, O_s in TMEM
+// TMEM holds S_0, S_1, O_0, O_1: 4 x 128 columns, all 512.  P could go through
+// shared memory, where a product takes 65 clocks instead of 100; but two
+// operands there use all of the shared memory's bandwidth, and every barrier
+// and store of the other warps then waits (measured slower by half).
 //
 // O is not rescaled each time the maximum grows: the running reference m only
 // moves when a row's scores pass it by 2^8 (fp32 sums and 16-bit probabilities
@@ -54,7 +53,7 @@ constexpr uint32_t kPolls = 1u << 17, kPollNs = 20000;     // a wait's limit: so
 constexpr float kSlack = 8.0f;           // how far (log2) scores may pass the reference
 
 // Shared memory, bytes from its 1024-aligned start.
-constexpr int kSlots = 3;
+constexpr int kSlots = 5;
 
 // Where a softmax warp is: kept in shared memory, its registers hold scores.
 struct SoftmaxState {
@@ -63,11 +62,11 @@ struct SoftmaxState {
 };
 
 struct Smem {
-    static constexpr int q = kSlots * kTile, p = q + 2 * kTile;
-    static constexpr int exps = p + 2 * kTile;                  // bytes [3 tiles][keys, values][BN] (e4m3)
+    static constexpr int q = kSlots * kTile;
+    static constexpr int exps = q + 2 * kTile;                  // bytes [3 tiles][keys, values][BN] (e4m3)
     static constexpr int flag = exps + 6 * BN;                  // uint32 [4 tiles][3 warps][4] values that are not numbers
     static constexpr int bar = flag + 4 * kLoadWarps * 4 * 4;
-    static constexpr int word = bar + (3 * kSlots + 15) * 8;    // TMEM address, dead
+    static constexpr int word = bar + (3 * kSlots + 11) * 8;    // TMEM address, dead
     static constexpr int state = word + 8;                      // SoftmaxState [8 warps]
     static constexpr int bytes = state + 8 * static_cast<int>(sizeof(SoftmaxState)) + 1024;
 };
@@ -75,18 +74,8 @@ static_assert(Smem::bytes <= 227 * 1024, "one CTA per SM");
 
 // Barriers: two per stream of each kind, one for the end, then the ring's (full,
 // empty, landed).
-enum Bar { kQFull = 0, kQEmpty = 2, kSFull = 4, kSFree = 6, kPFull = 8, kOFull = 10, kEnd = 12, kFull = 13,
-           kEmpty = kFull + kSlots, kLand = kEmpty + kSlots };
-
-// Tiles go through the ring in the order in which they are used: the scores of
-// tile t + 1 are under way before the outputs of tile t, so
-//   K0, K1, V0, K2, V1, ..., K(n-1), V(n-2), V(n-1)
-__device__ __forceinline__ uint32_t key_step(int t) { return t == 0 ? 0u : 2u * t - 1u; }
-__device__ __forceinline__ uint32_t value_step(int t, int n) { return t == n - 1 ? 2u * n - 1u : 2u * t + 2u; }
-__device__ __forceinline__ int step_tile(int j, int n, bool* isv) {
-    *isv = j > 0 && ((j & 1) == 0 || j == 2 * n - 1);
-    return j == 0 ? 0 : (j & 1) == 0 ? j / 2 - 1 : j == 2 * n - 1 ? n - 1 : (j + 1) / 2;
-}
+enum Bar { kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6, kOFull = 8, kEnd = 10, kFull = 11, kEmpty = kFull + kSlots,
+           kLand = kEmpty + kSlots };
 
 struct Sync {
     uint32_t bar, dead;      // shared-memory addresses
@@ -177,6 +166,12 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t x, uint32_t y, uint3
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(x), "r"(y), "r"(idesc), "r"(add),
                  "r"(kOperandHi) : "memory");
 }
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t x, uint32_t y, uint32_t idesc, uint32_t add) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(x), "r"(y), "r"(idesc), "r"(add),
+                 "r"(kOperandHi) : "memory");
+}
+
 // One thread of a converged warp, and a value that is the same in all of them.
 __device__ __forceinline__ bool elected() {
     uint32_t e;
@@ -299,8 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             mbar_init(bars + kQFull + i, q_boxes ? 1 : kLoadWarps);
             mbar_init(bars + kQEmpty + i, 1);
             mbar_init(bars + kSFull + i, 1);
-            mbar_init(bars + kSFree + i, kRows / 32);    // a warp arrives once: 32 arrivals take turns
-            mbar_init(bars + kPFull + i, kRows / 32);
+            mbar_init(bars + kPFull + i, kRows / 32);    // a warp arrives once: 32 arrivals take turns
             mbar_init(bars + kOFull + i, 1);
         }
         mbar_init(bars + kEnd, 1);
@@ -325,11 +319,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     if (tid == 0) write_desc(a, part, walk);
 
     // the softmax warps hold half a row of scores: they take registers that the
-    // others do not need (256 * 184 + 128 * 136 = 384 * 168, the launch's own)
+    // others do not need (256 * 200 + 128 * 104 = 384 * 168, the launch's own)
     if (warp < 8)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;" ::: "memory");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;" ::: "memory");
     else
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 136;" ::: "memory");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;" ::: "memory");
     if (warp < 8) {
         // ---------------- softmax of one stream, a thread per row ----------------
         const int st = warp >> 2, r = tid & 127;
@@ -376,7 +370,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 const int first_mixed = max(u.cut.ctx / BN - u.t0, 0);
                 if (mrow && first_mixed == 0) mask_words(a, mrow, u.t0 * BN - u.cut.ctx, words);
 
-                unsigned char* ps = smem + M::p + st * kTile;
                 for (int t = 0; t < nt; ++t, ++n) {
                     const int pos0 = (u.t0 + t) * BN;
                     const bool mixed = t >= first_mixed;
@@ -385,9 +378,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     fence_after();
                     float x[128];
                     tmem_ld128(x, tS);
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) sync.arrive(kSFree + st);
                     uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
                     if (mixed) {                     // what the row does not see
 #pragma unroll
@@ -432,30 +422,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     const float sub = m == -INFINITY ? 0.0f : -m;
                     const F2 c2{c, c}, sub2{sub, sub};
                     float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    uint32_t pk[64];
 #pragma unroll
-                    for (int y = 0; y < 64; y += 2) {
-                        F2 v = fma2(F2{x[2 * y], x[2 * y + 1]}, c2, sub2);
-                        F2 w = fma2(F2{x[2 * y + 2], x[2 * y + 3]}, c2, sub2);
-                        v.x = ex2(v.x), v.y = ex2(v.y), w.x = ex2(w.x), w.y = ex2(w.y);
-                        s4[0] += v.x, s4[1] += v.y, s4[2] += w.x, s4[3] += w.y;
-                        pk[y] = pack2<F16>(v.x, v.y);
-                        pk[y + 1] = pack2<F16>(w.x, w.y);
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int y = 0; y < 16; y += 2) {
+                            const int z = 32 * h + 2 * y;
+                            F2 v = fma2(F2{x[z], x[z + 1]}, c2, sub2);
+                            F2 w = fma2(F2{x[z + 2], x[z + 3]}, c2, sub2);
+                            v.x = ex2(v.x), v.y = ex2(v.y), w.x = ex2(w.x), w.y = ex2(w.y);
+                            s4[0] += v.x, s4[1] += v.y, s4[2] += w.x, s4[3] += w.y;
+                            pk[y] = pack2<F16>(v.x, v.y);
+                            pk[y + 1] = pack2<F16>(w.x, w.y);
+                        }
+                        tmem_st16(tS + 16 * h, pk);
                     }
                     l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                    if (t > 0) sync.wait(kOFull + st, (n - 1) & 1);     // the product before has read its P
-#pragma unroll
-                    for (int ch = 0; ch < 16; ++ch)
-                        *reinterpret_cast<uint4*>(ps + chunk_at(r, ch)) = make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
-                    fence_async();
                     if (mixed) {                     // values that are not numbers, among those that the row sees
-                        const uint32_t step = 2 * nv + value_step(t, nt);
+                        const uint32_t step = 2 * (nv + t) + 1;
                         sync.wait(kFull + step % S, step / S & 1);
                         const uint32_t* f = s_flag + ((nv + t) & 3) * (kLoadWarps * 4);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             if (see[i] & (f[i] | f[4 + i] | f[8 + i])) nan_row = true;
+                        __syncwarp();
                     }
+                    tmem_wait_st();
+                    fence_before();
                     __syncwarp();
                     if (lane == 0) sync.arrive(kPFull + st);
                 }
@@ -510,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int LR = CH > 8 ? 16 : CH > 4 ? 8 : 4; // lanes of a row
         const int RP = 32 / LR, lr = lane / LR, lc = lane % LR;     // rows of a warp's step
         const uint32_t group = ((1u << LR) - 1u) << (lr * LR);
-        constexpr uint32_t kAhead = kSlots - 1;      // steps (tiles of keys or of values) under way
+        constexpr uint32_t kAhead = kSlots - 2;      // steps (tiles of keys or of values) under way
 
         // warp 8: begins the copies of the next step; a walk of its own, ahead
         Walk<MT, BN> lead;
@@ -522,8 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int blocks = !E4 && D > 64 ? 2 : 1;
         const int copy = lane / blocks, block = lane % blocks;
         auto lead_page = [&]() {                     // the page of this lane's rows at the unit's step
-            bool isv;
-            const int pos = (lu.t0 + step_tile(lj, lnt, &isv)) * BN + copy * run_rows;
+            const int pos = (lu.t0 + (lj >> 1)) * BN + copy * run_rows;
             const int pg = copy * run_rows < BN && lj < 2 * lnt && pos < lu.len
                                ? __ldg(a.table + static_cast<int64_t>(lu.b) * a.max_pages + pos / a.c.P) : -1;
             return pg < a.c.pages ? pg : -1;
@@ -539,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 lj = 0;
                 lpage = lead_page();
             }
-            bool isv;
-            const int pos = (lu.t0 + step_tile(lj, lnt, &isv)) * BN + copy * run_rows;
+            const bool isv = lj & 1;
+            const int pos = (lu.t0 + (lj >> 1)) * BN + copy * run_rows;
             const uint32_t slot = lstep % S;
             sync.wait(kEmpty + slot, (lstep / S & 1) ^ 1);
             __syncwarp();
@@ -632,8 +624,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             }
 #pragma unroll 1
             for (int j = 0; j < 2 * nt; ++j, ++step) {
-                bool isv;
-                const int t = step_tile(j, nt, &isv);
+                const bool isv = j & 1;
+                const int t = j >> 1;
                 const uint32_t tile = tiles + t, slot = step % S;
                 const int from = min(max(u.cut.ctx - (u.t0 + t) * BN, 0), BN);   // first row that some do not see
                 if (E4 && !isv) {                    // the exponents of tile t
@@ -715,17 +707,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const uint32_t idesc_s = common | (static_cast<uint32_t>(BN / 8) << 17);
         const uint32_t idesc_o = common | (1u << 16) | (static_cast<uint32_t>(D / 8) << 17);    // V is MN-major
         const uint32_t ring_k = operand_lo(smem_u32(smem), 16), ring_v = operand_lo(smem_u32(smem), kBlock);
-        const uint32_t q0 = operand_lo(smem_u32(smem + M::q), 16), p0 = operand_lo(smem_u32(smem + M::p), 16);
+        const uint32_t q0 = operand_lo(smem_u32(smem + M::q), 16);
         const int nks = D / 16;
         Unit u;
-        uint32_t n[2] = {0, 0}, np[2] = {0, 0}, q[2] = {0, 0}, tiles = 0;      // scores, outputs and queries so far
+        uint32_t n[2] = {0, 0}, q[2] = {0, 0}, tiles = 0;       // tiles and queries of each stream, tiles of the CTA
         auto scores = [&](int s, uint32_t slot, bool last) {
-            if (n[s] > 0) sync.wait(kSFree + s, (n[s] - 1) & 1);
-            ++n[s];
-            __syncwarp();
-            fence_after();
-            const bool dead = sync.is_dead();
             const uint32_t x = uniform(q0 + s * (kTile >> 4)), y = uniform(ring_k + slot * (kTile >> 4)), d = uniform(tmem + s * 128);
+            const bool dead = sync.is_dead();
             if (elected()) {
                 if (!dead) {
                     if (nks == 8) {
@@ -751,48 +739,48 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             if (nt == 0) continue;
             // stream s has a live row (stream 0 has one in every unit with tiles)
             const int streams = (u.mt * MT + kRows) / a.g < u.cut.cnt ? 2 : 1;
-            const uint32_t base = 2 * tiles;
-            sync.wait(kFull + base % S, base / S & 1);
+            const uint32_t first = 2 * tiles;        // the ring's step of the unit's first keys
+            sync.wait(kFull + first % S, first / S & 1);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 if (s >= streams) break;
                 sync.wait(kQFull + s, q[s]++ & 1);
-                scores(s, base % S, nt == 1);
+                __syncwarp();
+                fence_after();
+                scores(s, first % S, nt == 1);
             }
-            if (elected()) sync.commit(kEmpty + base % S);
+            if (elected()) sync.commit(kEmpty + first % S);
             __syncwarp();
             for (int t = 0; t < nt; ++t) {
-                if (t + 1 < nt) {
-                    const uint32_t sk = base + key_step(t + 1);
-                    sync.wait(kFull + sk % S, sk / S & 1);
-#pragma unroll
-                    for (int s = 0; s < 2; ++s)
-                        if (s < streams) scores(s, sk % S, t + 2 == nt);
-                    if (elected()) sync.commit(kEmpty + sk % S);
-                    __syncwarp();
-                }
-                const uint32_t sv = base + value_step(t, nt), slot_v = sv % S;
+                const bool more = t + 1 < nt;
+                const uint32_t sv = first + 2 * t + 1, sk = sv + 1, slot_v = sv % S, slot_k = sk % S;
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     if (s >= streams) break;
-                    sync.wait(kPFull + s, np[s]++ & 1);
-                    if (s == 0) sync.wait(kFull + slot_v, sv / S & 1);
+                    if (s == 0) {
+                        sync.wait(kFull + slot_v, sv / S & 1);
+                        if (more) sync.wait(kFull + slot_k, sk / S & 1);
+                    }
+                    sync.wait(kPFull + s, n[s]++ & 1);
                     __syncwarp();
                     fence_after();
+                    const uint32_t x = uniform(tmem + s * 128), y = uniform(ring_v + slot_v * (kTile >> 4));
+                    const uint32_t d = uniform(tmem + 256 + s * 128), add = uniform(t > 0);
                     const bool dead = sync.is_dead();
-                    const uint32_t x = uniform(p0 + s * (kTile >> 4)), y = uniform(ring_v + slot_v * (kTile >> 4));
-                    const uint32_t d = uniform(tmem + 256 + s * 128), first = uniform(t > 0);
                     if (elected()) {
                         if (!dead) {
 #pragma unroll
-                            for (int ks = 0; ks < BN / 16; ++ks)
-                                mma_ss(d, x + (((ks >> 2) * kBlock + (ks & 3) * 32) >> 4), y + ks * (2048 >> 4), idesc_o, ks > 0 ? 1u : first);
+                            for (int ks = 0; ks < BN / 16; ++ks) mma_ts(d, x + ks * 8, y + ks * (2048 >> 4), idesc_o, ks > 0 ? 1u : add);
                         }
                         sync.commit(kOFull + s);
                     }
                     __syncwarp();
+                    if (more) scores(s, slot_k, t + 2 == nt);
                 }
-                if (elected()) sync.commit(kEmpty + slot_v);
+                if (elected()) {
+                    sync.commit(kEmpty + slot_v);
+                    if (more) sync.commit(kEmpty + slot_k);
+                }
                 __syncwarp();
             }
             tiles += nt;
