@@ -3,13 +3,20 @@
 //
 // A unit is (sequence b, kv head h, row tile mt): MT of the N * g query rows
 // that read kv head h (row = node * g + head within the group), against all
-// positions that the tile's nodes can see, BN positions at a time.  All units'
-// key tiles form one long line, b outermost, and CTA i of n takes the i-th n-th
-// of it (so ragged lengths need no tuning: every CTA streams the same number of
-// tiles).  A unit cut by the end of a CTA's part gives partial results, one per
-// CTA: normalised fp32 outputs and the base-2 log of their sum, joined by
-// combine_kernel.  A CTA has at most two: a unit begun before it (slot 0) and
-// one that goes on after it (slot 1).
+// positions that the tile's nodes can see, BN positions at a time.  Units are
+// numbered b outermost, mt innermost.
+//
+// Where several row tiles read the same keys and values (mts > 1), CTA i first
+// takes units i, i + n, i + 2 n, ... for `rounds` rounds, so that the row tiles
+// of one head run side by side and its keys and values come from HBM once (all
+// heads at once would not fit the L2: 1.28 ms against 0.75 ms on 16 trees of
+// 513 nodes, 466 MB of cache).  The key tiles of the other units (of all, where
+// there is one row tile) form one line, cut into one part per CTA, longer for
+// those whose rounds were shorter: ragged lengths need no tuning.  A unit cut
+// by the end of a part gives partial results, one per CTA: normalised fp32
+// outputs and the base-2 log of their sum, joined by combine_kernel.  A CTA has
+// at most two: a unit begun before it (slot 0) and one that goes on after it
+// (slot 1).
 #pragma once
 
 #include "sdv_device.cuh"
@@ -60,55 +67,113 @@ __device__ __forceinline__ int64_t head_tiles(const AttnArgs& a, const Cut& c, i
 }
 
 struct Part {                // a CTA's part of the line
-    int64_t begin, end, total;
+    int64_t begin, end;      // tiles, counted from the line's first unit
+    int64_t total;
     int ctas;                // CTAs that have a part
-    int b;                   // sequence of `begin`, and where its tiles begin
+    int b;                   // sequence of `begin`, and where its first unit would be
     int64_t seq0;
+    const int64_t* begins;   // rounds > 0: every CTA's begin (valid until shared memory is reused)
 };
 
-__device__ __forceinline__ int64_t part_begin(int64_t total, int n, int i) { return total * i / n; }
-__device__ __forceinline__ int part_owner(int64_t total, int n, int64_t tile) {
-    return static_cast<int>(((tile + 1) * n - 1) / total);
+// Tiles of the units of a sequence that come before its unit j.
+template <int MT, int BN>
+__device__ __forceinline__ int64_t tiles_before(const AttnArgs& a, const Cut& c, int mts, int j) {
+    const int h = j / mts;
+    int64_t n = h > 0 ? head_tiles<MT, BN>(a, c, mts) * h : 0;
+    for (int mt = 0; mt < j - h * mts; ++mt) n += tiles_of<BN>(tile_len<MT>(a, c, mt));
+    return n;
 }
 
-// Every thread of the CTA calls this; `sm` holds 40 int64.
+// Where CTA i's part begins: every CTA has a tile at least.
+__device__ __forceinline__ int64_t part_begin(const Part& p, int i) {
+    if (p.begins) return p.begins[i];
+    return i + (p.total - p.ctas) * i / p.ctas;
+}
+
+// Every thread of the CTA calls this; `sm` holds 48 + 3 * ctas int64.
 template <int MT, int BN, int THREADS>
 __device__ __forceinline__ Part find_part(const AttnArgs& a, int mts, int64_t* sm) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per_seq = a.c.H * mts, n = a.ctas;
+    const int first = a.rounds * n;                  // the line's first unit
+    const int b0 = first / per_seq, j0 = first - b0 * per_seq;
     int64_t mine = 0;
-    for (int b = tid; b < a.B; b += THREADS)
-        mine += head_tiles<MT, BN>(a, cut_of(a, b), mts) * a.c.H;
+    for (int b = b0 + tid; b < a.B; b += THREADS) {
+        const Cut c = cut_of(a, b);
+        mine += head_tiles<MT, BN>(a, c, mts) * a.c.H;
+        if (b == b0) mine -= tiles_before<MT, BN>(a, c, mts, j0);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     if (lane == 0) sm[warp] = mine;
+    int64_t* begins = sm + 48;
+    int64_t* done = begins + n + 1;
+    if (a.rounds > 0)
+        for (int i = tid; i < n; i += THREADS) {     // the tiles of each CTA's rounds
+            int64_t s = 0;
+            for (int k = 0; k < a.rounds; ++k) {
+                const int j = i + k * n, b = j / per_seq;
+                s += tiles_of<BN>(tile_len<MT>(a, cut_of(a, b), (j - b * per_seq) % mts));
+            }
+            done[i] = s;
+        }
     __syncthreads();
     Part p;
     p.total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) p.total += sm[w];
-    p.ctas = static_cast<int>(p.total < a.ctas ? p.total : a.ctas);
+    p.ctas = static_cast<int>(p.total < n ? p.total : n);
+    p.begins = nullptr;
+    if (a.rounds > 0) {
+        // shares of the line: what a CTA's rounds lack of the mean
+        if (warp == 0) {
+            int64_t sum = 0;
+            for (int i = lane; i < n; i += 32) sum += done[i];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const int64_t mean = (sum + p.total) / n + 1;
+            int64_t base = 0;
+            for (int i0 = 0; i0 < p.ctas; i0 += 32) {
+                const int i = i0 + lane;
+                const int64_t w = i < p.ctas ? (mean > done[i] ? mean - done[i] : 0) : 0;
+                int64_t upto = w;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += x;
+                }
+                if (i < p.ctas) begins[i] = base + upto - w;
+                base += __shfl_sync(0xffffffffu, upto, 31);
+            }
+            __syncwarp();
+            for (int i = lane; i <= p.ctas; i += 32)
+                begins[i] = i == p.ctas ? p.total
+                                        : i + (base > 0 ? static_cast<int64_t>(static_cast<double>(p.total - p.ctas) * begins[i] / base) : 0);
+        }
+        p.begins = begins;
+        __syncthreads();
+    }
     const int i = blockIdx.x;
+    p.b = a.B;
     if (i >= p.ctas) {
-        p.begin = p.end = p.total;
-        p.b = a.B;
-        p.seq0 = p.total;
+        p.begin = p.end = p.seq0 = p.total;
         return p;
     }
-    p.begin = part_begin(p.total, p.ctas, i);
-    p.end = part_begin(p.total, p.ctas, i + 1);
+    p.begin = part_begin(p, i);
+    p.end = i + 1 == p.ctas ? p.total : part_begin(p, i + 1);
     if (warp == 0) {
-        int64_t base = 0;
-        for (int b0 = 0; b0 < a.B; b0 += 32) {
-            const int b = b0 + lane;
-            const int64_t n = b < a.B ? head_tiles<MT, BN>(a, cut_of(a, b), mts) * a.c.H : 0;
-            int64_t upto = n;
+        int64_t base = b0 < a.B ? -tiles_before<MT, BN>(a, cut_of(a, b0), mts, j0) : 0;
+        for (int bb = b0; bb < a.B; bb += 32) {
+            const int b = bb + lane;
+            const int64_t n_b = b < a.B ? head_tiles<MT, BN>(a, cut_of(a, b), mts) * a.c.H : 0;
+            int64_t upto = n_b;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
                 if (lane >= o) upto += x;
             }
-            const bool here = b < a.B && base + upto > p.begin && base + upto - n <= p.begin;
-            if (here) sm[32] = b, sm[33] = base + upto - n;
+            const bool here = b < a.B && base + upto > p.begin && base + upto - n_b <= p.begin;
+            if (here) sm[32] = b, sm[33] = base + upto - n_b;
             if (__ballot_sync(0xffffffffu, here)) break;
             base += __shfl_sync(0xffffffffu, upto, 31);
         }
@@ -127,12 +192,17 @@ struct Unit {
     bool whole;              // that is all of them
 };
 
-// Walks the units of a CTA's part: the first is found by division, the others
-// follow one another.
+// Walks a CTA's units: those of its rounds, then those of its part, of which the
+// first is found by division and the others follow one another.
 template <int MT, int BN> struct Walk {
+    int round;               // the next one
     int left, rest;          // tiles left of the part; tiles of the unit before it
     int b, h, mt;
     Cut cut;
+    __device__ __forceinline__ void begin(const AttnArgs& a, const Part& p, int mts) {
+        round = 0;
+        if (a.rounds == 0) start(a, p, mts);
+    }
     __device__ __forceinline__ void start(const AttnArgs& a, const Part& p, int mts) {
         left = static_cast<int>(p.end - p.begin);
         rest = 0;
@@ -163,7 +233,20 @@ template <int MT, int BN> struct Walk {
         }
         rest = static_cast<int>(before);
     }
-    __device__ __forceinline__ bool next(const AttnArgs& a, int mts, Unit& u) {
+    __device__ __forceinline__ bool next(const AttnArgs& a, const Part& p, int mts, Unit& u) {
+        if (round < a.rounds) {
+            const int j = blockIdx.x + round * a.ctas, per_seq = a.c.H * mts;
+            u.b = j / per_seq;
+            u.h = (j - u.b * per_seq) / mts;
+            u.mt = (j - u.b * per_seq) - u.h * mts;
+            u.cut = cut_of(a, u.b);
+            u.len = tile_len<MT>(a, u.cut, u.mt);
+            u.t0 = 0;
+            u.t1 = tiles_of<BN>(u.len);
+            u.whole = true;
+            if (++round == a.rounds) start(a, p, mts);
+            return true;
+        }
         if (left <= 0) return false;
         u.b = b;
         u.h = h;
@@ -194,16 +277,18 @@ __device__ __forceinline__ float* part_rows(const AttnArgs& a, int cta, int slot
 
 // desc[2 i] = the unit that CTA i's part begins within, if CTA i is the first
 // to go on with it: (b, h, mt, first CTA); the last CTA in desc[2 i + 1].  One
-// thread writes it, from a walk that has just started.
-template <int MT, int BN> __device__ __forceinline__ void write_desc(const AttnArgs& a, const Part& p, const Walk<MT, BN>& w) {
+// thread writes it.
+template <int MT, int BN> __device__ __forceinline__ void write_desc(const AttnArgs& a, const Part& p, int mts) {
     const int i = blockIdx.x;
+    Walk<MT, BN> w;
+    w.start(a, p, mts);
     int4 d = make_int4(-1, 0, 0, 0);
     if (w.left > 0 && w.rest > 0) {
-        const int64_t first = p.begin - w.rest;
-        const int owner = part_owner(p.total, p.ctas, first);
-        const int tiles = tiles_of<BN>(tile_len<MT>(a, w.cut, w.mt));
-        if (owner == i - 1) d = make_int4(w.b, w.h, w.mt, owner);
-        a.desc[2 * i + 1] = make_int4(part_owner(p.total, p.ctas, first + tiles - 1), 0, 0, 0);
+        const int64_t first = p.begin - w.rest, end = first + tiles_of<BN>(tile_len<MT>(a, w.cut, w.mt));
+        if (part_begin(p, i - 1) <= first) d = make_int4(w.b, w.h, w.mt, i - 1);
+        int last = i;
+        while (last + 1 < p.ctas && part_begin(p, last + 1) < end) ++last;
+        a.desc[2 * i + 1] = make_int4(last, 0, 0, 0);
     }
     a.desc[2 * i] = d;
 }

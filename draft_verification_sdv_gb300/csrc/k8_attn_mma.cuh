@@ -139,10 +139,10 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
     const Part part = find_part<MT, BN, kThreads>(a, mts, s_part);
 
     Walk<MT, BN> walk;
-    walk.start(a, part, mts);
-    if (tid == 0) write_desc(a, part, walk);
+    walk.begin(a, part, mts);
+    if (tid == 0) write_desc<MT, BN>(a, part, mts);
     Unit u;
-    while (walk.next(a, mts, u)) {
+    while (walk.next(a, part, mts, u)) {
         __syncthreads();                            // the unit before is done with shared memory
         if (tid == 0 && u.cut.bad && a.status) atomicOr(a.status, kStatusBadLength);
         const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
@@ -531,6 +531,7 @@ cudaError_t launch_one(AttnArgs a, int nsm, cudaStream_t s) {
     const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_mma_kernel<DP, E4, F16, WM>), smem);
     if (e != cudaSuccess) return e;
     a.ctas = nsm * (smem > 112 * 1024 ? 1 : 2);
+    a.rounds = 0;
     attn_mma_kernel<DP, E4, F16, WM><<<static_cast<unsigned>(a.ctas), kThreads, smem, s>>>(a);
     const cudaError_t e2 = cudaGetLastError();
     return e2 != cudaSuccess ? e2 : launch_attn_combine(a, F16, 16 * WM, s);

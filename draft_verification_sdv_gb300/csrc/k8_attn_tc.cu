@@ -315,8 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     fence_after();
     const uint32_t tmem = *s_tmem;
     Walk<MT, BN> walk;
-    walk.start(a, part, mts);
-    if (tid == 0) write_desc(a, part, walk);
+    walk.begin(a, part, mts);
+    if (tid == 0) write_desc<MT, BN>(a, part, mts);
+    __syncthreads();                                 // the ring may be used
 
     // the softmax warps hold half a row of scores: they take registers that the
     // others do not need (256 * 200 + 128 * 104 = 384 * 168, the launch's own)
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         if (lane == 0) state.walk = walk;
         while (true) {
             int more = 0;
-            if (lane == 0) more = state.walk.next(a, mts, u);
+            if (lane == 0) more = state.walk.next(a, part, mts, u);
             __syncwarp();
             if (!__shfl_sync(0xffffffffu, more, 0)) break;
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         // warp 8: begins the copies of the next step; a walk of its own, ahead
         Walk<MT, BN> lead;
         Unit lu{};
-        lead.start(a, part, mts);
+        lead.begin(a, part, mts);
         int lj = 0, lnt = 0, lpage = -1;             // step of the unit, its tiles
         uint32_t lstep = 0;
         bool more = w == 0;
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             if (!more) return;
             if (lj == 2 * lnt) {                     // the next unit with tiles
                 do {
-                    more = lead.next(a, mts, lu);
+                    more = lead.next(a, part, mts, lu);
                     lnt = more && lu.len > 0 ? lu.t1 - lu.t0 : 0;
                 } while (more && lnt == 0);
                 if (!more) return;
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 
         Unit u;
         uint32_t tiles = 0, step = 0, nq[2] = {0, 0};
-        while (walk.next(a, mts, u)) {
+        while (walk.next(a, part, mts, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
             // the queries, once the scores of the unit before are done with theirs
             const int streams = nt == 0 ? 0 : (u.mt * MT + kRows) / a.g < u.cut.cnt ? 2 : 1;
@@ -734,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             }
             __syncwarp();
         };
-        while (walk.next(a, mts, u)) {
+        while (walk.next(a, part, mts, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
             if (nt == 0) continue;
             // stream s has a live row (stream 0 has one in every unit with tiles)
@@ -861,6 +862,9 @@ cudaError_t launch(AttnArgs a, const CUtensorMap& k, const CUtensorMap& v, const
     }();
     if (regs != kRegs) return cudaErrorInvalidKernelImage;
     a.ctas = nsm;
+    const int mts = (a.N * a.g + MT - 1) / MT;
+    const int64_t units = static_cast<int64_t>(a.B) * a.c.H * mts;
+    a.rounds = mts > 1 && units >= 2 * nsm ? static_cast<int>(units / nsm - 1) : 0;
     attn_tc_kernel<E4, F16><<<static_cast<unsigned>(nsm), kThreads, bytes, s>>>(a, k, v, q, rows, q_boxes);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_attn_combine(a, F16, MT, s);

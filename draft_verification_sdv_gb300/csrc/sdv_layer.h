@@ -81,7 +81,7 @@ struct AttnArgs {
     int4* desc;                       // two per CTA: the unit that its start splits
     int B, N, Hq, g, W, max_pages;
     float scale_log2;                 // scale * log2(e)
-    int ctas;
+    int ctas, rounds;                 // see k8_attn.cuh
 };
 size_t attn_workspace_bytes(int nsm);
 cudaError_t launch_tree_attn(AttnArgs a, int type, bool e4m3, void* workspace, int nsm,

@@ -340,6 +340,40 @@ def test_attn_large_tree(B, K, G, Hq, Hk, D, ctx, dtype, cdtype):
     _check_attn(*case, ctx, count=t["count"].tolist(), mask=t["mask"])
 
 
+@pytest.mark.parametrize("dtype,cdtype", [(BF, BF), (HF, F8)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_attn_more_units_than_the_machine_holds(dtype, cdtype, tree):
+    """Row tiles enough for whole rounds and a line cut into unequal parts; the
+    reference is each sequence by itself (which few CTAs share)."""
+    B, K, G, Hq, Hk, D, P = 9, 10, 32, 16, 8, 64, 16
+    N = 1 + K * G
+    ctx = [700, 3, 0, 1500, 130, 90, 2100, 40, 513]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    drafts = torch.randint(0, 9, (B, K, G), generator=g, device="cuda", dtype=torch.int32)
+    t = bd.sdv_tree_build(_i32([0] * B), drafts)
+    mask = t["mask"] if tree else None
+    q, kc, vc, ke, ve, table = _attn_case(B, N, Hq, Hk, D, P, ctx, dtype, cdtype, seed=31)
+    out, lse = bd.sdv_tree_attn(q, kc, vc, table, _i32(ctx), count=t["count"], mask=mask, k_exp=ke, v_exp=ve, lse=True)
+    half = ref.HALF_STEP[dtype]
+    for b in range(B):
+        o, x = bd.sdv_tree_attn(q[b:b + 1], kc, vc, table[b:b + 1].contiguous(), _i32(ctx[b:b + 1]),
+                                count=t["count"][b:b + 1].contiguous(), k_exp=ke, v_exp=ve, lse=True,
+                                mask=None if mask is None else mask[b:b + 1].contiguous())
+        # the same probabilities, their references and their order of summing apart
+        err = (out[b].double() - o[0].double()).abs()
+        assert (err <= 2 * half * o[0].double().abs() + 2 * half * 4).all()
+        assert float(err.square().mean().sqrt()) <= half * float(o[0].double().square().mean().sqrt())
+        fin = x[0] > -math.inf
+        assert torch.equal(fin, lse[b] > -math.inf) and (lse[b] - x[0])[fin].abs().max() <= 2.0 ** -16
+    # and one sequence against the definition
+    few = [2, 40, 77]
+    cpu = lambda t: None if t is None else t.cpu()  # noqa: E731
+    want, wl, tol, tl = ref.attn(q[1:2].cpu(), cpu(kc), cpu(vc), table[1:2].cpu(), ctx[1:2], [78], cpu(mask[1:2]) if tree else None,
+                                 D ** -0.5, cpu(ke), cpu(ve))
+    got = out[1:2, few].double().cpu()
+    assert ((got - want[:, few]).abs() <= tol[:, few]).all()
+
+
 @pytest.mark.parametrize("dtype,cdtype", TYPES)
 def test_attn_growing_scores(dtype, cdtype):
     """Scores that grow along the positions, so that the running maximum moves
