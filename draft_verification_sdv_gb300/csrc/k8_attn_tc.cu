@@ -23,9 +23,9 @@
 // go through a ring of slots in shared memory, as rows of 128 bytes in the
 // 128-byte swizzle, [D / 64][128 rows]: the K operand is read K-major, and V,
 // whose contraction index is the row, MN-major.  Warp 8 brings a tile by tile
-// copies (TMA), one per page and column block, a lane to each, so that pages
-// may be of any size that is a multiple of 8 rows.  The three warps then hand
-// it over: after a look at the values of rows that some queries do not see
+// copies (TMA), one per page and column block, so that pages may be of any size
+// that is a multiple of 8 rows.  Warps 9 and 10 then hand it over (warp 8 helps
+// them with e4m3 rows): after a look at the values of rows that some queries do not see
 // (what is not a number there must not meet a zero probability in a product),
 // or, for e4m3 rows, which land as they are in the upper half of their slot,
 // after bringing them to the queries' type, times their row's power of two.
@@ -290,8 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const Sync sync{smem_u32(bars), smem_u32(smem + M::word + 4), a.status};
     if (tid == 0) {
         s_tmem[1] = 0;                               // dead
+        for (int i = 0; i < 4 * kLoadWarps * 4; ++i) s_flag[i] = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bars + kQFull + i, q_boxes ? 1 : kLoadWarps);
+            mbar_init(bars + kQFull + i, q_boxes ? 1 : E4 ? kLoadWarps : kLoadWarps - 1);
             mbar_init(bars + kQEmpty + i, 1);
             mbar_init(bars + kSFull + i, 1);
             mbar_init(bars + kPFull + i, kRows / 32);    // a warp arrives once: 32 arrivals take turns
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
         mbar_init(bars + kEnd, 1);
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(bars + kFull + i, kLoadWarps);
+            mbar_init(bars + kFull + i, E4 ? kLoadWarps : kLoadWarps - 1);
             mbar_init(bars + kEmpty + i, 1);
             mbar_init(bars + kLand + i, 1);
         }
@@ -500,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     } else if (warp < 11) {
         // ---------------- loads ----------------
         const int p = tid - 256, w = warp - 8;
+        constexpr int kFirst = E4 ? 0 : 1, kSettle = kLoadWarps - kFirst;   // warps that hand tiles over
         const int CH = D / (E4 ? 16 : 8);            // 16-byte chunks of a row as it comes
         const int LR = CH > 8 ? 16 : CH > 4 ? 8 : 4; // lanes of a row
         const int RP = 32 / LR, lr = lane / LR, lc = lane % LR;     // rows of a warp's step
@@ -510,57 +512,70 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         Walk<MT, BN> lead;
         Unit lu{};
         lead.begin(a, part, mts);
-        int lj = 0, lnt = 0, lpage = -1;             // step of the unit, its tiles
+        int lt = 0, lnt = 0;                         // tile of the unit, its tiles
+        int lpage = -1, loff = 0, npage = -1, noff = 0;     // this lane's rows of the tile and of the next one
         uint32_t lstep = 0;
         bool more = w == 0;
-        const int blocks = !E4 && D > 64 ? 2 : 1;
-        const int copy = lane / blocks, block = lane % blocks;
-        auto lead_page = [&]() {                     // the page of this lane's rows at the unit's step
-            const int pos = (lu.t0 + (lj >> 1)) * BN + copy * run_rows;
-            const int pg = copy * run_rows < BN && lj < 2 * lnt && pos < lu.len
-                               ? __ldg(a.table + static_cast<int64_t>(lu.b) * a.max_pages + pos / a.c.P) : -1;
-            return pg < a.c.pages ? pg : -1;
+        const int blocks = !E4 && D > 64 ? 2 : 1, copies = BN / run_rows;
+        auto lead_page = [&](int t, int& off) {
+            const int pos = (lu.t0 + t) * BN + lane * run_rows;
+            if (lane >= copies || t >= lnt || pos >= lu.len) return -1;
+            const int i = pos / a.c.P;
+            off = lu.h * a.c.P + pos - i * a.c.P;
+            return __ldg(a.table + static_cast<int64_t>(lu.b) * a.max_pages + i);
         };
         auto begin = [&]() {
             if (!more) return;
-            if (lj == 2 * lnt) {                     // the next unit with tiles
+            const bool isv = lstep & 1;
+            if (!isv && lt == lnt) {                 // the next unit with tiles
                 do {
                     more = lead.next(a, part, mts, lu);
                     lnt = more && lu.len > 0 ? lu.t1 - lu.t0 : 0;
                 } while (more && lnt == 0);
                 if (!more) return;
-                lj = 0;
-                lpage = lead_page();
+                lt = 0;
+                npage = lead_page(0, noff);
             }
-            const bool isv = lj & 1;
-            const int pos = (lu.t0 + (lj >> 1)) * BN + copy * run_rows;
+            if (!isv) {
+                lpage = npage, loff = noff;
+                npage = lead_page(lt + 1, noff);
+            }
             const uint32_t slot = lstep % S;
             sync.wait(kEmpty + slot, (lstep / S & 1) ^ 1);
             __syncwarp();
-            more = !__any_sync(0xffffffffu, sync.is_dead());
-            if (!more) return;
-            const bool active = lpage >= 0;
-            const uint32_t n = __popc(__ballot_sync(0xffffffffu, active));
-            if (lane == 0) mbar_arrive_expect_tx(bars + kLand + slot, n * run_rows * 128);
+            if (sync.is_dead()) {
+                more = false;
+                return;
+            }
+            const uint32_t good = __ballot_sync(0xffffffffu, lpage >= 0 && lpage < a.c.pages);
+            const uint32_t dst = uniform(smem_u32(smem + slot * kTile + (E4 ? kBlock : 0)));    // e4m3 lands in the upper half
+            const CUtensorMap* map = isv ? &map_v : &map_k;
+            if (elected()) mbar_arrive_expect_tx(bars + kLand + slot, __popc(good) * run_rows * 128 * blocks);
             __syncwarp();
-            if (active)                              // e4m3 lands in the slot's upper half
-                tma_load(smem_u32(smem + slot * kTile + (E4 ? kBlock : block * kBlock) + copy * run_rows * 128), isv ? &map_v : &map_k,
-                         bars + kLand + slot, block * 64, lu.h * a.c.P + pos % a.c.P, lpage);
+            for (int c = 0; c < copies; ++c) {
+                const int page = __shfl_sync(0xffffffffu, lpage, c), row = __shfl_sync(0xffffffffu, loff, c);
+                if ((good >> c & 1) && elected()) {
+                    tma_load(dst + c * run_rows * 128, map, bars + kLand + slot, 0, row, page);
+                    if (blocks == 2) tma_load(dst + kBlock + c * run_rows * 128, map, bars + kLand + slot, 64, row, page);
+                }
+                __syncwarp();
+            }
             ++lstep;
-            ++lj;
-            lpage = lead_page();
+            if (isv) ++lt;
         };
         for (uint32_t i = 0; i < kAhead; ++i) begin();
+        if (!E4 && w == 0)
+            while (more) begin();                    // nothing else to do
 
         Unit u;
         uint32_t tiles = 0, step = 0, nq[2] = {0, 0};
-        while (walk.next(a, part, mts, u)) {
+        while ((E4 || w > 0) && walk.next(a, part, mts, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
             // the queries, once the scores of the unit before are done with theirs
             const int streams = nt == 0 ? 0 : (u.mt * MT + kRows) / a.g < u.cut.cnt ? 2 : 1;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                if (s >= streams || (q_boxes && w > 0)) break;
+                if (s >= streams || (q_boxes && w != kFirst)) break;
                 sync.wait(kQEmpty + s, (nq[s]++ & 1) ^ 1);
                 __syncwarp();
                 if (__any_sync(0xffffffffu, sync.is_dead())) break;
@@ -577,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     continue;
                 }
                 const int lanes = D > 64 ? 16 : 8, rows = 32 / lanes, ch = lane % lanes;
-                for (int i = w; i < kRows / rows; i += kLoadWarps) {
+                for (int i = w - kFirst; i < kRows / rows; i += kSettle) {
                     const int r = i * rows + lane / lanes, row = first + r, node = row / a.g;
                     if (ch >= D / 8) continue;
                     const unsigned char* src = a.q + u.b * a.q_sb + node * a.q_sn +
@@ -654,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         __syncwarp();
                     }
                     const unsigned char* ex = smem + M::exps + (tile % 3 * 2 + isv) * BN;
-                    for (int q = w; q < BN / RP; q += kLoadWarps) {
+                    for (int q = w - kFirst; q < BN / RP; q += kSettle) {
                         const int r = q * RP + lr;
                         uint32_t o[8];
                         bool bad = false;
@@ -688,16 +703,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 fence_async();
                 __syncwarp();
                 if (lane == 0) sync.arrive(kFull + slot);
-                begin();
+                if constexpr (E4) begin();
             }
             tiles += nt;
         }
-        if (w == 0 && q_boxes)                       // a dead CTA too waits for the copies it has begun
+        if (w == kFirst && q_boxes)                  // a dead CTA too waits for the copies it has begun
 #pragma unroll
             for (int s = 0; s < 2; ++s)
                 for (uint32_t n = 0; nq[s] > 0 && n < kPolls && !sync.poll(kQFull + s, (nq[s] - 1) & 1) && !sync.is_dead(); ++n) {}
         if (w == 0)
-            for (uint32_t i = lstep > kAhead ? lstep - kAhead : 0; i < lstep; ++i)
+            for (uint32_t i = lstep > S ? lstep - S : 0; i < lstep; ++i)
                 for (uint32_t n = 0; n < kPolls && !sync.poll(kLand + i % S, i / S & 1); ++n) {}
     } else {
         // ---------------- products ----------------
