@@ -53,7 +53,7 @@ constexpr uint32_t kPolls = 1u << 17, kPollNs = 20000;     // a wait's limit: so
 constexpr float kSlack = 8.0f;           // how far (log2) scores may pass the reference
 
 // Shared memory, bytes from its 1024-aligned start.
-constexpr int kSlots = 5;
+constexpr int kKeySlots = 3, kValueSlots = 2, kSlots = kKeySlots + kValueSlots;
 
 // Where a softmax warp is: kept in shared memory, its registers hold scores.
 struct SoftmaxState {
@@ -66,16 +66,23 @@ struct Smem {
     static constexpr int exps = q + 2 * kTile;                  // bytes [3 tiles][keys, values][BN] (e4m3)
     static constexpr int flag = exps + 6 * BN;                  // uint32 [4 tiles][3 warps][4] values that are not numbers
     static constexpr int bar = flag + 4 * kLoadWarps * 4 * 4;
-    static constexpr int word = bar + (3 * kSlots + 11) * 8;    // TMEM address, dead
+    static constexpr int word = bar + 20 * 8;                   // TMEM address, dead
     static constexpr int state = word + 8;                      // SoftmaxState [8 warps]
     static constexpr int bytes = state + 8 * static_cast<int>(sizeof(SoftmaxState)) + 1024;
 };
 static_assert(Smem::bytes <= 227 * 1024, "one CTA per SM");
 
-// Barriers: two per stream of each kind, one for the end, then the ring's (full,
-// empty, landed).
-enum Bar { kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6, kOFull = 8, kEnd = 10, kFull = 11, kEmpty = kFull + kSlots,
-           kLand = kEmpty + kSlots };
+// Barriers: two per stream of each kind, one for the end, and the tiles'.  Tile T
+// (of the CTA's, through all its units) has its keys in slot T % 3 and its
+// values in slot 3 + T % 2.  The values of a tile and the keys of the next one
+// are used and freed together: full(T) says that K(T) and V(T - 1) are there,
+// free(T) that S(T + 1) and the outputs of tile T are done, so that V(T + 2) and
+// K(T + 3) may come.  Few barriers, because each is a round trip through a
+// shared memory that the products keep busy (200 clocks and more).
+enum Bar { kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6, kOFull = 8, kEnd = 10, kFull = 11, kFree = 13, kLand = 15,
+           kBars = kLand + kSlots };
+
+static_assert(Smem::word == Smem::bar + kBars * 8, "a place for each barrier");
 
 struct Sync {
     uint32_t bar, dead;      // shared-memory addresses
@@ -84,6 +91,13 @@ struct Sync {
         uint32_t d;
         asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(d) : "r"(dead) : "memory");
         return d != 0;
+    }
+    __device__ __forceinline__ bool test(int i, uint32_t parity) const {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done) : "r"(bar + i * 8), "r"(parity) : "memory");
+        return done != 0;
     }
     // sleeps until the phase is over or for some time: a warp that keeps asking
     // holds up the shared-memory accesses of the others
@@ -94,11 +108,15 @@ struct Sync {
             : "=r"(done) : "r"(bar + i * 8), "r"(parity), "r"(kPollNs) : "memory");
         return done != 0;
     }
-    __device__ __forceinline__ void wait(int i, uint32_t parity) const {
-        for (uint32_t n = 0; n < kPolls; ++n)
-            if (poll(i, parity) || is_dead()) return;
+    // false: the CTA is dead
+    __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
+        for (uint32_t n = 0; n < kPolls; ++n) {
+            if (poll(i, parity)) return true;
+            if (is_dead()) return false;
+        }
         asm volatile("st.volatile.shared.u32 [%0], 1;" ::"r"(dead) : "memory");
         if (status) atomicOr(status, kStatusTimeout);
+        return false;
     }
     __device__ __forceinline__ void arrive(int i) const {
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar + i * 8) : "memory");
@@ -198,6 +216,14 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // Byte offset of 16-byte chunk c of row r in a tile.
 __device__ __forceinline__ int chunk_at(int r, int c) { return (c >> 3) * kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
 
+// A whole sector at once: the rows of a warp lie apart, and each store of it
+// takes a turn per row at a memory pipe that the products keep busy.
+__device__ __forceinline__ void store32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f, uint32_t g,
+                                        uint32_t h) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f),
+                 "r"(g), "r"(h) : "memory");
+}
+
 // The mask words that hold nodes base .. base + 127 of a row.
 __device__ __forceinline__ void mask_words(const AttnArgs& a, const int32_t* row, int base, uint32_t (&w)[5]) {
     const int w0 = base >> 5;                        // floor
@@ -271,13 +297,31 @@ template <bool F16> __device__ __forceinline__ void widen16(const uint4& raw, in
     }
 }
 
+// Whether a warp's share of a tile's 16-bit rows holds what is not a number in
+// rows from `from` on: rows q * RP + lr for q = first, first + step, ..., of which
+// the lane has chunk lc.
+template <bool F16>
+__device__ __forceinline__ bool odd_values(const unsigned char* base, int from, int first, int step, int RP, int lr, int lc, int chunks) {
+    // all ones in an exponent carry into the sign's place
+    constexpr uint32_t ones = F16 ? 0x7c007c00u : 0x7f807f80u, unit = F16 ? 0x04000400u : 0x00800080u;
+    uint32_t bad = 0;
+    if (lc < chunks)
+#pragma unroll 8
+        for (int q = first + from / RP / step * step; q < BN / RP; q += step) {
+            const int r = q * RP + lr;
+            const uint4 v = *reinterpret_cast<const uint4*>(base + chunk_at(r, lc));
+            const uint32_t b = ((v.x & ones) + unit) | ((v.y & ones) + unit) | ((v.z & ones) + unit) | ((v.w & ones) + unit);
+            bad |= r >= from ? b : 0u;
+        }
+    return __any_sync(0xffffffffu, (bad & 0x80008000u) != 0);
+}
+
 template <bool E4, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                                                               const __grid_constant__ CUtensorMap map_v,
                                                               const __grid_constant__ CUtensorMap map_q, int run_rows,
                                                               bool q_boxes) {
     using M = Smem;
-    constexpr uint32_t S = kSlots;
     extern __shared__ unsigned char raw[];
     unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint32_t* s_flag = reinterpret_cast<uint32_t*>(smem + M::flag);
@@ -299,11 +343,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             mbar_init(bars + kOFull + i, 1);
         }
         mbar_init(bars + kEnd, 1);
-        for (int i = 0; i < kSlots; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(bars + kFull + i, E4 ? kLoadWarps : kLoadWarps - 1);
-            mbar_init(bars + kEmpty + i, 1);
-            mbar_init(bars + kLand + i, 1);
+            mbar_init(bars + kFree + i, 1);
         }
+        for (int i = 0; i < kSlots; ++i) mbar_init(bars + kLand + i, 1);
     }
     if (warp == 11) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(s_tmem)) : "memory");
@@ -320,12 +364,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     if (tid == 0) write_desc<MT, BN>(a, part, mts);
     __syncthreads();                                 // the ring may be used
 
-    // the softmax warps hold half a row of scores: they take registers that the
-    // others do not need (256 * 200 + 128 * 104 = 384 * 168, the launch's own)
+    // the softmax warps hold a row of scores: they take registers that the others
+    // do not need (256 * kMore + 128 * kLess = 384 * 168, the launch's own; the
+    // warps that bring e4m3 rows to 16 bits need some themselves)
+    constexpr int kMore = E4 ? 184 : 200, kLess = E4 ? 136 : 104;
+    static_assert(256 * kMore + 128 * kLess == kThreads * kRegs, "no more than the launch has");
     if (warp < 8)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;" ::: "memory");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMore) : "memory");
     else
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;" ::: "memory");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLess) : "memory");
     if (warp < 8) {
         // ---------------- softmax of one stream, a thread per row ----------------
         const int st = warp >> 2, r = tid & 127;
@@ -334,16 +381,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         // (a negative scale has turned the queries round); c > 0 so that -inf stays -inf
         const float c = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
         uint32_t n = 0;                              // tiles of this stream so far
-        uint32_t nv = 0;                             // tiles of the CTA so far
+        uint32_t nv = 0, units = 0;                  // tiles of the CTA, units of this stream so far
         int seq = -1, any_bad = 0;
         SoftmaxState& state = reinterpret_cast<SoftmaxState*>(smem + M::state)[warp];
         Unit& u = state.u;
         if (lane == 0) state.walk = walk;
-        while (true) {
+        // the next unit; and for a new sequence a look for pages that are not the
+        // cache's: a slow path if there are any
+        auto prepare = [&]() {
             int more = 0;
             if (lane == 0) more = state.walk.next(a, part, mts, u);
             __syncwarp();
-            if (!__shfl_sync(0xffffffffu, more, 0)) break;
+            if (!__shfl_sync(0xffffffffu, more, 0)) return false;
+            if (u.b != seq) {
+                seq = u.b;
+                const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
+                const int pages = (u.cut.ctx + u.cut.cnt + a.c.P - 1) / a.c.P;
+                int bad = 0;
+                for (int pg = r; pg < pages; pg += kRows) {
+                    const int x = __ldg(table + pg);
+                    bad |= x < 0 || x >= a.c.pages;
+                }
+                asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.red.or.pred q, %2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+                             : "=r"(any_bad) : "r"(bad), "r"(2 + st) : "memory");
+                if (any_bad && r == 0 && a.status) atomicOr(a.status, kStatusBadPage);
+            }
+            return true;
+        };
+        bool more = prepare();
+        while (more) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
             const int first_row = u.mt * MT + st * kRows;
             const int row = first_row + r, node = row / a.g;
@@ -354,73 +420,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             bool nan_row = false;
             if (run) {
                 const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
-                if (u.b != seq) {                    // pages that are not the cache's: a slow path if there are any
-                    seq = u.b;
-                    const int last_page = (u.cut.ctx + u.cut.cnt - 1) / a.c.P;
-                    int bad = 0;
-                    for (int pg = r; pg <= last_page; pg += kRows) {
-                        const int x = __ldg(table + pg);
-                        bad |= x < 0 || x >= a.c.pages;
-                    }
-                    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.red.or.pred q, %2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-                                 : "=r"(any_bad) : "r"(bad), "r"(2 + st) : "memory");
-                    if (any_bad && r == 0 && a.status) atomicOr(a.status, kStatusBadPage);
-                }
                 const int32_t* mrow = a.mask ? a.mask + u.b * a.mask_sb + static_cast<int64_t>(live ? node : 0) * a.W : nullptr;
-                uint32_t words[5];
-                // tiles from first_mixed on hold nodes, which some rows see and some do not
-                const int first_mixed = max(u.cut.ctx / BN - u.t0, 0);
-                if (mrow && first_mixed == 0) mask_words(a, mrow, u.t0 * BN - u.cut.ctx, words);
-
-                for (int t = 0; t < nt; ++t, ++n) {
-                    const int pos0 = (u.t0 + t) * BN;
-                    const bool mixed = t >= first_mixed;
-                    sync.wait(kSFull + st, n & 1);
-                    __syncwarp();
-                    fence_after();
-                    float x[128];
-                    tmem_ld128(x, tS);
-                    uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-                    if (mixed) {                     // what the row does not see
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            see[i] = live ? sees(u, mrow != nullptr, node, words, pos0, i) : 0u;
-#pragma unroll
-                            for (int y = 0; y < 32; ++y) x[32 * i + y] = see[i] >> y & 1 ? x[32 * i + y] : -INFINITY;
-                        }
-                        if (mrow && t + 1 < nt) mask_words(a, mrow, pos0 + BN - u.cut.ctx, words);
-                    } else if (mrow && t + 1 == first_mixed && t + 1 < nt) {
-                        mask_words(a, mrow, pos0 + BN - u.cut.ctx, words);
-                    }
-                    if (any_bad) nan_row |= sees_bad_page(table, a.c.pages, a.c.P, make_uint4(see[0], see[1], see[2], see[3]), pos0, u.len);
+                uint32_t words[5] = {0, 0, 0, 0, 0};
+                // tiles from `plain` on hold nodes, which some rows see and some do not
+                // (all of them go the long way where a page is bad)
+                const int plain = any_bad ? 0 : min(max(u.cut.ctx / BN - u.t0, 0), nt);
+                if (mrow && plain == 0) mask_words(a, mrow, u.t0 * BN - u.cut.ctx, words);
+                // scores to probabilities: the running maximum and sum, P over S
+                auto weigh = [&](const float (&x)[128], bool first) {
                     float t4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
                     for (int y = 4; y < 124; y += 8)
 #pragma unroll
                         for (int z = 0; z < 4; ++z) t4[z] = max3(t4[z], x[y + z], x[y + 4 + z]);
                     float top = max3(max3(t4[0], x[124], x[125]), max3(t4[1], x[126], x[127]), fmaxf(t4[2], t4[3]));
-                    top = top == -INFINITY ? top : top * c;
+                    top *= c;                        // (c > 0: -inf stays)
                     // the reference moves when the scores pass it by far
                     const bool move = top > m + kSlack || (m == -INFINITY && top != -INFINITY);
-                    if (t > 0 && __any_sync(0xffffffffu, move)) {
-                        const float by = move ? ex2(m - top) : 1.0f;
-                        sync.wait(kOFull + st, (n - 1) & 1);        // the product before has been added
-                        __syncwarp();
-                        fence_after();
-                        l *= by;
+                    if (__any_sync(0xffffffffu, move)) {
+                        if (!first) {
+                            // (these scores were multiplied after the outputs of the tile before: both are done)
+                            const float by = move ? ex2(m - top) : 1.0f;
+                            l *= by;
 #pragma unroll 1
-                        for (int i = 0; i < D; i += 16) {
-                            float o[16];
-                            uint32_t o2[16];
-                            tmem_ld16(o, tO + i);
+                            for (int i = 0; i < D; i += 16) {
+                                float o[16];
+                                uint32_t o2[16];
+                                tmem_ld16(o, tO + i);
 #pragma unroll
-                            for (int y = 0; y < 16; ++y) o2[y] = __float_as_uint(o[y] * by);
-                            tmem_st16(tO + i, o2);
+                                for (int y = 0; y < 16; ++y) o2[y] = __float_as_uint(o[y] * by);
+                                tmem_st16(tO + i, o2);
+                            }
                         }
-                        tmem_wait_st();
-                        fence_before();
+                        if (move) m = top;
                     }
-                    if (move) m = top;
                     const float sub = m == -INFINITY ? 0.0f : -m;
                     const F2 c2{c, c}, sub2{sub, sub};
                     float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -440,38 +473,75 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         tmem_st16(tS + 16 * h, pk);
                     }
                     l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                    if (mixed) {                     // values that are not numbers, among those that the row sees
-                        const uint32_t step = 2 * (nv + t) + 1;
-                        sync.wait(kFull + step % S, step / S & 1);
-                        const uint32_t* f = s_flag + ((nv + t) & 3) * (kLoadWarps * 4);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (see[i] & (f[i] | f[4 + i] | f[8 + i])) nan_row = true;
-                        __syncwarp();
-                    }
+                };
+                auto hand_over = [&]() {
                     tmem_wait_st();
                     fence_before();
                     __syncwarp();
                     if (lane == 0) sync.arrive(kPFull + st);
+                };
+#pragma unroll 1
+                for (int t = 0; t < plain; ++t, ++n) {
+                    sync.wait(kSFull + st, n & 1);
+                    __syncwarp();
+                    fence_after();
+                    float x[128];
+                    tmem_ld128(x, tS);
+                    weigh(x, t == 0);
+                    hand_over();
+                    if (mrow && t + 1 == plain && t + 1 < nt) mask_words(a, mrow, (u.t0 + t + 1) * BN - u.cut.ctx, words);
                 }
-                sync.wait(kOFull + st, (n - 1) & 1);
-                __syncwarp();
-                fence_after();
-                if (sync.is_dead()) nan_row = true;
+#pragma unroll 1
+                for (int t = plain; t < nt; ++t, ++n) {
+                    const int pos0 = (u.t0 + t) * BN;
+                    uint32_t see[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) see[i] = live ? sees(u, mrow != nullptr, node, words, pos0, i) : 0u;
+                    if (mrow && t + 1 < nt) mask_words(a, mrow, pos0 + BN - u.cut.ctx, words);
+                    if (any_bad) nan_row |= sees_bad_page(table, a.c.pages, a.c.P, make_uint4(see[0], see[1], see[2], see[3]), pos0, u.len);
+                    sync.wait(kSFull + st, n & 1);
+                    __syncwarp();
+                    fence_after();
+                    float x[128];
+                    tmem_ld128(x, tS);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) x[32 * i + y] = see[i] >> y & 1 ? x[32 * i + y] : -INFINITY;
+                    weigh(x, t == 0);
+                    // values that are not numbers, among those that the row sees
+                    const uint32_t T = nv + t;
+                    sync.wait(kFull + ((T + 1) & 1), (T + 1) >> 1 & 1);
+                    const uint32_t* f = s_flag + (T & 3) * (kLoadWarps * 4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (see[i] & (f[i] | f[4 + i] | f[8 + i])) nan_row = true;
+                    __syncwarp();
+                    hand_over();
+                }
             }
             nv += nt;
 
-            // the row: its output, or its part of one (the TMEM reads are the warp's)
+            // the row: its output, or its part of one.  What comes next is looked up
+            // while the last products run; the TMEM reads are the warp's.
             const float nanv = __int_as_float(0x7fc00000);
-            if (nan_row || u.cut.bad) l = nanv;
-            const bool empty = l == 0.0f || (!live && !u.cut.bad);
-            const float inv = empty ? 0.0f : 1.0f / l;
-            const float log2sum = u.cut.bad ? nanv : empty ? -INFINITY : m + log2f(l);
-            const bool mine = node < a.N;
+            const bool whole = u.whole, ubad = u.cut.bad, mine = node < a.N;
             const int64_t orow = (static_cast<int64_t>(u.b) * a.N + node) * a.Hq + u.h * a.g + row % a.g;
             float* prow = part_rows(a, blockIdx.x, u.t0 > 0 ? 0 : 1, MT);
-            if (mine && u.whole && a.lse) a.lse[orow] = log2sum * kLn2;
-            if (mine && !u.whole) prow[MT * D + st * kRows + r] = log2sum;
+            __syncwarp();                            // every lane has read the unit
+            more = prepare();
+            if (run) {
+                const bool done = sync.wait(kOFull + st, units++ & 1);
+                __syncwarp();
+                fence_after();
+                if (!done) nan_row = true;
+            }
+            if (nan_row || ubad) l = nanv;
+            const bool empty = l == 0.0f || (!live && !ubad);
+            const float inv = empty ? 0.0f : 1.0f / l;
+            const float log2sum = ubad ? nanv : empty ? -INFINITY : m + log2f(l);
+            if (mine && whole && a.lse) a.lse[orow] = log2sum * kLn2;
+            if (mine && !whole) prow[MT * D + st * kRows + r] = log2sum;
             unsigned short* dst = static_cast<unsigned short*>(a.out) + orow * D;
             float* pdst = prow + (st * kRows + r) * D;
             for (int i = 0; i < D; i += 16) {
@@ -483,16 +553,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 if (!mine) continue;
 #pragma unroll
                 for (int y = 0; y < 16; ++y) o[y] = empty ? 0.0f : o[y] * inv;
-                if (u.whole) {
-#pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        reinterpret_cast<uint4*>(dst + i)[y] =
-                            make_uint4(pack2<F16>(o[8 * y], o[8 * y + 1]), pack2<F16>(o[8 * y + 2], o[8 * y + 3]),
-                                       pack2<F16>(o[8 * y + 4], o[8 * y + 5]), pack2<F16>(o[8 * y + 6], o[8 * y + 7]));
+                if (whole) {
+                    store32(dst + i, pack2<F16>(o[0], o[1]), pack2<F16>(o[2], o[3]), pack2<F16>(o[4], o[5]), pack2<F16>(o[6], o[7]),
+                            pack2<F16>(o[8], o[9]), pack2<F16>(o[10], o[11]), pack2<F16>(o[12], o[13]), pack2<F16>(o[14], o[15]));
                 } else {
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        reinterpret_cast<float4*>(pdst + i)[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                    const uint32_t* q = reinterpret_cast<const uint32_t*>(o);
+                    store32(pdst + i, q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]);
+                    store32(pdst + i + 8, q[8], q[9], q[10], q[11], q[12], q[13], q[14], q[15]);
                 }
             }
             __syncwarp();
@@ -506,7 +573,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int LR = CH > 8 ? 16 : CH > 4 ? 8 : 4; // lanes of a row
         const int RP = 32 / LR, lr = lane / LR, lc = lane % LR;     // rows of a warp's step
         const uint32_t group = ((1u << LR) - 1u) << (lr * LR);
-        constexpr uint32_t kAhead = kSlots - 2;      // steps (tiles of keys or of values) under way
 
         // warp 8: begins the copies of the next step; a walk of its own, ahead
         Walk<MT, BN> lead;
@@ -524,15 +590,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             off = lu.h * a.c.P + pos - i * a.c.P;
             return __ldg(a.table + static_cast<int64_t>(lu.b) * a.max_pages + i);
         };
-        auto begin = [&]() {
-            if (!more) return;
+        // step 2 T: the keys of tile T, 2 T + 1: its values; false: not yet
+        auto begin = [&](bool block) {
+            if (!more) return false;
             const bool isv = lstep & 1;
+            const uint32_t T = lstep >> 1;
+            if (isv && T >= 2) {                     // (which frees the keys' place of the step after, too)
+                const int bar = kFree + (T & 1);
+                const uint32_t parity = (T - 2) >> 1 & 1;
+                if (block) {
+                    more = sync.wait(bar, parity);
+                    more = __all_sync(0xffffffffu, more);
+                    if (!more) return false;
+                } else if (!__all_sync(0xffffffffu, sync.test(bar, parity))) {
+                    return false;
+                }
+            }
             if (!isv && lt == lnt) {                 // the next unit with tiles
                 do {
                     more = lead.next(a, part, mts, lu);
                     lnt = more && lu.len > 0 ? lu.t1 - lu.t0 : 0;
                 } while (more && lnt == 0);
-                if (!more) return;
+                if (!more) return false;
                 lt = 0;
                 npage = lead_page(0, noff);
             }
@@ -540,13 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 lpage = npage, loff = noff;
                 npage = lead_page(lt + 1, noff);
             }
-            const uint32_t slot = lstep % S;
-            sync.wait(kEmpty + slot, (lstep / S & 1) ^ 1);
-            __syncwarp();
-            if (sync.is_dead()) {
-                more = false;
-                return;
-            }
+            const uint32_t slot = isv ? kKeySlots + (T & 1) : T % kKeySlots;
             const uint32_t good = __ballot_sync(0xffffffffu, lpage >= 0 && lpage < a.c.pages);
             const uint32_t dst = uniform(smem_u32(smem + slot * kTile + (E4 ? kBlock : 0)));    // e4m3 lands in the upper half
             const CUtensorMap* map = isv ? &map_v : &map_k;
@@ -562,57 +635,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             }
             ++lstep;
             if (isv) ++lt;
+            return true;
         };
-        for (uint32_t i = 0; i < kAhead; ++i) begin();
         if (!E4 && w == 0)
-            while (more) begin();                    // nothing else to do
+            while (begin(true)) {}                   // nothing else to do
 
         Unit u;
         uint32_t tiles = 0, step = 0, nq[2] = {0, 0};
         while ((E4 || w > 0) && walk.next(a, part, mts, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
-            // the queries, once the scores of the unit before are done with theirs
-            const int streams = nt == 0 ? 0 : (u.mt * MT + kRows) / a.g < u.cut.cnt ? 2 : 1;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (s >= streams || (q_boxes && w != kFirst)) break;
-                sync.wait(kQEmpty + s, (nq[s]++ & 1) ^ 1);
-                __syncwarp();
-                if (__any_sync(0xffffffffu, sync.is_dead())) break;
-                unsigned char* qs = smem + M::q + s * kTile;
-                const int first = u.mt * MT + s * kRows;
-                const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-                if (q_boxes) {                       // the 128 rows are the group's heads of whole nodes
-                    const int q_blocks = D > 64 ? 2 : 1;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(bars + kQFull + s, q_blocks * kBlock);
-                        for (int i = 0; i < q_blocks; ++i)
-                            tma_load_q(smem_u32(qs + i * kBlock), &map_q, bars + kQFull + s, i * 64, u.h * a.g, first / a.g, u.b);
-                    }
-                    continue;
-                }
-                const int lanes = D > 64 ? 16 : 8, rows = 32 / lanes, ch = lane % lanes;
-                for (int i = w - kFirst; i < kRows / rows; i += kSettle) {
-                    const int r = i * rows + lane / lanes, row = first + r, node = row / a.g;
-                    if (ch >= D / 8) continue;
-                    const unsigned char* src = a.q + u.b * a.q_sb + node * a.q_sn +
-                                               (static_cast<int64_t>(u.h) * a.g + row % a.g) * a.q_sh + ch * 16;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (node < u.cut.cnt) {
-                        if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-                            v = *reinterpret_cast<const uint4*>(src);
-                        } else {
-                            const unsigned short* e = reinterpret_cast<const unsigned short*>(src);
-                            v = make_uint4(e[0] | static_cast<uint32_t>(e[1]) << 16, e[2] | static_cast<uint32_t>(e[3]) << 16,
-                                           e[4] | static_cast<uint32_t>(e[5]) << 16, e[6] | static_cast<uint32_t>(e[7]) << 16);
-                        }
-                    }
-                    *reinterpret_cast<uint4*>(qs + chunk_at(r, ch)) = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
-                }
-                fence_async();
-                __syncwarp();
-                if (lane == 0) sync.arrive(kQFull + s);
-            }
             // e4m3: a thread looks after the exponents of rows p and p + 96 of a
             // tile; a row's page is read two tiles ahead, its exponents one
             const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
@@ -642,7 +673,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             for (int j = 0; j < 2 * nt; ++j, ++step) {
                 const bool isv = j & 1;
                 const int t = j >> 1;
-                const uint32_t tile = tiles + t, slot = step % S;
+                const uint32_t tile = tiles + t, slot = isv ? kKeySlots + (tile & 1) : tile % kKeySlots;
+                if constexpr (E4) {                  // copies as far ahead as there is room
+                    if (w == 0) {
+                        while (begin(false)) {}
+                        while (lstep <= step && begin(true)) {}
+                    }
+                }
                 const int from = min(max(u.cut.ctx - (u.t0 + t) * BN, 0), BN);   // first row that some do not see
                 if (E4 && !isv) {                    // the exponents of tile t
 #pragma unroll
@@ -658,16 +695,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     }
                     bar_sync(1, kLoadThreads);
                 }
-                sync.wait(kLand + slot, step / S & 1);
+                sync.wait(kLand + slot, (isv ? tile >> 1 : tile / kKeySlots) & 1);
                 __syncwarp();
                 unsigned char* base = smem + slot * kTile;
                 const bool check = isv && from < BN;
-                if (E4 || check) {
+                if (check) {
+                    if (lane < 4) s_flag[(tile & 3) * (kLoadWarps * 4) + w * 4 + lane] = 0;
+                    __syncwarp();
+                }
+                if (E4 || (check && odd_values<F16>(base, from, w - kFirst, kSettle, RP, lr, lc, CH))) {
                     uint32_t* flags = s_flag + (tile & 3) * (kLoadWarps * 4) + w * 4;
-                    if (check) {
-                        if (lane < 4) flags[lane] = 0;
-                        __syncwarp();
-                    }
                     const unsigned char* ex = smem + M::exps + (tile % 3 * 2 + isv) * BN;
                     for (int q = w - kFirst; q < BN / RP; q += kSettle) {
                         const int r = q * RP + lr;
@@ -702,18 +739,66 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 }
                 fence_async();
                 __syncwarp();
-                if (lane == 0) sync.arrive(kFull + slot);
-                if constexpr (E4) begin();
+                if (!isv && lane == 0) sync.arrive(kFull + (tile & 1));
+                if (j == 0) {
+                    // the queries, once the scores of the unit before are done with theirs
+                    const int streams = nt == 0 ? 0 : (u.mt * MT + kRows) / a.g < u.cut.cnt ? 2 : 1;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if (s >= streams || (q_boxes && w != kFirst)) break;
+                        sync.wait(kQEmpty + s, (nq[s]++ & 1) ^ 1);
+                        __syncwarp();
+                        if (__any_sync(0xffffffffu, sync.is_dead())) break;
+                        unsigned char* qs = smem + M::q + s * kTile;
+                        const int first = u.mt * MT + s * kRows;
+                        const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+                        if (q_boxes) {                       // the 128 rows are the group's heads of whole nodes
+                            const int q_blocks = D > 64 ? 2 : 1;
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(bars + kQFull + s, q_blocks * kBlock);
+                                for (int i = 0; i < q_blocks; ++i)
+                                    tma_load_q(smem_u32(qs + i * kBlock), &map_q, bars + kQFull + s, i * 64, u.h * a.g, first / a.g, u.b);
+                            }
+                            continue;
+                        }
+                        const int lanes = D > 64 ? 16 : 8, rows = 32 / lanes, ch = lane % lanes;
+                        for (int i = w - kFirst; i < kRows / rows; i += kSettle) {
+                            const int r = i * rows + lane / lanes, row = first + r, node = row / a.g;
+                            if (ch >= D / 8) continue;
+                            const unsigned char* src = a.q + u.b * a.q_sb + node * a.q_sn +
+                                                       (static_cast<int64_t>(u.h) * a.g + row % a.g) * a.q_sh + ch * 16;
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            if (node < u.cut.cnt) {
+                                if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+                                    v = *reinterpret_cast<const uint4*>(src);
+                                } else {
+                                    const unsigned short* e = reinterpret_cast<const unsigned short*>(src);
+                                    v = make_uint4(e[0] | static_cast<uint32_t>(e[1]) << 16, e[2] | static_cast<uint32_t>(e[3]) << 16,
+                                                   e[4] | static_cast<uint32_t>(e[5]) << 16, e[6] | static_cast<uint32_t>(e[7]) << 16);
+                                }
+                            }
+                            *reinterpret_cast<uint4*>(qs + chunk_at(r, ch)) = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+                        }
+                        fence_async();
+                        __syncwarp();
+                        if (lane == 0) sync.arrive(kQFull + s);
+                    }
+                }
             }
             tiles += nt;
         }
+        if ((E4 || w > 0) && lane == 0) sync.arrive(kFull + (tiles & 1));       // the last values
         if (w == kFirst && q_boxes)                  // a dead CTA too waits for the copies it has begun
 #pragma unroll
             for (int s = 0; s < 2; ++s)
                 for (uint32_t n = 0; nq[s] > 0 && n < kPolls && !sync.poll(kQFull + s, (nq[s] - 1) & 1) && !sync.is_dead(); ++n) {}
         if (w == 0)
-            for (uint32_t i = lstep > S ? lstep - S : 0; i < lstep; ++i)
-                for (uint32_t n = 0; n < kPolls && !sync.poll(kLand + i % S, i / S & 1); ++n) {}
+            // (two tiles' values and the keys of three at most; those before have been used)
+            for (uint32_t i = lstep > 5 ? lstep - 4 - (lstep & 1) : 0; i < lstep; ++i) {
+                const uint32_t T = i >> 1;
+                const int bar = kLand + (i & 1 ? kKeySlots + (T & 1) : T % kKeySlots);
+                for (uint32_t n = 0; n < kPolls && !sync.poll(bar, (i & 1 ? T >> 1 : T / kKeySlots) & 1); ++n) {}
+            }
     } else {
         // ---------------- products ----------------
         // The whole warp walks and waits, so that the operands stay uniform; one
@@ -726,12 +811,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const uint32_t q0 = operand_lo(smem_u32(smem + M::q), 16);
         const int nks = D / 16;
         Unit u;
-        uint32_t n[2] = {0, 0}, q[2] = {0, 0}, tiles = 0;       // tiles and queries of each stream, tiles of the CTA
-        auto scores = [&](int s, uint32_t slot, bool last) {
-            const uint32_t x = uniform(q0 + s * (kTile >> 4)), y = uniform(ring_k + slot * (kTile >> 4)), d = uniform(tmem + s * 128);
-            const bool dead = sync.is_dead();
+        uint32_t n[2] = {0, 0}, q[2] = {0, 0}, T = 0;           // tiles and queries of each stream, tiles of the CTA
+        bool ok = true;                              // while no wait has given up
+        const uint32_t tm = uniform(tmem);
+        auto scores = [&](int s, uint32_t key_slot, bool last) {
             if (elected()) {
-                if (!dead) {
+                if (ok) {
+                    const uint32_t x = q0 + s * (kTile >> 4), y = ring_k + key_slot * (kTile >> 4), d = tm + s * 128;
                     if (nks == 8) {
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks) {
@@ -748,58 +834,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 sync.commit(kSFull + s);
                 if (last) sync.commit(kQEmpty + s);
             }
-            __syncwarp();
         };
         while (walk.next(a, part, mts, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
             if (nt == 0) continue;
             // stream s has a live row (stream 0 has one in every unit with tiles)
             const int streams = (u.mt * MT + kRows) / a.g < u.cut.cnt ? 2 : 1;
-            const uint32_t first = 2 * tiles;        // the ring's step of the unit's first keys
-            sync.wait(kFull + first % S, first / S & 1);
+            // (the unit before has waited for these keys with its last values)
+            if (T == 0) ok = sync.wait(kFull, 0) && ok;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 if (s >= streams) break;
-                sync.wait(kQFull + s, q[s]++ & 1);
+                ok = sync.wait(kQFull + s, q[s]++ & 1) && ok;
                 __syncwarp();
                 fence_after();
-                scores(s, first % S, nt == 1);
+                scores(s, T % kKeySlots, nt == 1);
             }
-            if (elected()) sync.commit(kEmpty + first % S);
-            __syncwarp();
-            for (int t = 0; t < nt; ++t) {
+            if (T > 0 && elected()) sync.commit(kFree + ((T - 1) & 1));
+            uint32_t key_slot = T % kKeySlots;
+            for (int t = 0; t < nt; ++t, ++T) {
                 const bool more = t + 1 < nt;
-                const uint32_t sv = first + 2 * t + 1, sk = sv + 1, slot_v = sv % S, slot_k = sk % S;
+                key_slot = key_slot + 1 == kKeySlots ? 0 : key_slot + 1;
+                ok = sync.wait(kFull + ((T + 1) & 1), (T + 1) >> 1 & 1) && ok;
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     if (s >= streams) break;
-                    if (s == 0) {
-                        sync.wait(kFull + slot_v, sv / S & 1);
-                        if (more) sync.wait(kFull + slot_k, sk / S & 1);
-                    }
-                    sync.wait(kPFull + s, n[s]++ & 1);
+                    ok = sync.wait(kPFull + s, n[s]++ & 1) && ok;
                     __syncwarp();
                     fence_after();
-                    const uint32_t x = uniform(tmem + s * 128), y = uniform(ring_v + slot_v * (kTile >> 4));
-                    const uint32_t d = uniform(tmem + 256 + s * 128), add = uniform(t > 0);
-                    const bool dead = sync.is_dead();
                     if (elected()) {
-                        if (!dead) {
+                        if (ok) {
+                            const uint32_t x = tm + s * 128, y = ring_v + (kKeySlots + (T & 1)) * (kTile >> 4), d = tm + 256 + s * 128;
 #pragma unroll
-                            for (int ks = 0; ks < BN / 16; ++ks) mma_ts(d, x + ks * 8, y + ks * (2048 >> 4), idesc_o, ks > 0 ? 1u : add);
+                            for (int ks = 0; ks < BN / 16; ++ks) mma_ts(d, x + ks * 8, y + ks * (2048 >> 4), idesc_o, t > 0 || ks > 0);
                         }
-                        sync.commit(kOFull + s);
+                        if (!more) sync.commit(kOFull + s);
                     }
-                    __syncwarp();
-                    if (more) scores(s, slot_k, t + 2 == nt);
+                    if (more) scores(s, key_slot, t + 2 == nt);
                 }
-                if (elected()) {
-                    sync.commit(kEmpty + slot_v);
-                    if (more) sync.commit(kEmpty + slot_k);
-                }
+                if (more && elected()) sync.commit(kFree + (T & 1));
                 __syncwarp();
             }
-            tiles += nt;
         }
         if (elected()) sync.commit(kEnd);            // nothing is under way any more
         __syncwarp();

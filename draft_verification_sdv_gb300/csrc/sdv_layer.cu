@@ -296,7 +296,7 @@ sdv_status sdv_tree_attn(const sdv_kv_cache* cache, int B, int N, int Hq, sdv_dt
     a.g = Hq / a.c.H;
     if (static_cast<int64_t>(N) * a.g > (int64_t(1) << 28)) return SDV_ERR_ARG;
     if (!q || !ctx_len || !out || !workspace) return SDV_ERR_ARG;
-    if (misaligned(q, 2) || misaligned(out, 16) || misaligned(workspace, 16)) return SDV_ERR_ARG;
+    if (misaligned(q, 2) || misaligned(out, 32) || misaligned(workspace, 32)) return SDV_ERR_ARG;
     const void* ptrs[9] = {ctx_len, count, mask, lse, status, block_table, q, out, workspace};
     for (int i = 0; i < 6; ++i)
         if (misaligned(ptrs[i], 4)) return SDV_ERR_ARG;

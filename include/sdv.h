@@ -648,10 +648,10 @@ sdv_status sdv_kv_commit(const sdv_kv_cache* cache, int B, int K, int gamma, voi
  *          h / (Hq / kv_heads)
  *   mask   device int32, rows of ceil(N / 32) words, one row per node;
  *          mask_sb words from one sequence's to the next (0: all have the same)
- *   out    device [B][N][Hq][D] of `dtype`, contiguous, 16-byte aligned
+ *   out    device [B][N][Hq][D] of `dtype`, contiguous, 32-byte aligned
  *   lse    device float [B][N][Hq] contiguous, or NULL
  *   workspace  device memory of at least sdv_tree_attn_workspace(...) bytes,
- *          16-byte aligned, that no other call uses until this one is done
+ *          32-byte aligned, that no other call uses until this one is done
  * Probabilities are rounded to 16 bits for their product with the values; all
  * sums are fp32.  What a node does not see has no influence on it, whatever it
  * holds; a NaN or an infinity that it does see makes its output not finite

@@ -353,7 +353,10 @@ def test_attn_more_units_than_the_machine_holds(dtype, cdtype, tree):
     t = bd.sdv_tree_build(_i32([0] * B), drafts)
     mask = t["mask"] if tree else None
     q, kc, vc, ke, ve, table = _attn_case(B, N, Hq, Hk, D, P, ctx, dtype, cdtype, seed=31)
-    out, lse = bd.sdv_tree_attn(q, kc, vc, table, _i32(ctx), count=t["count"], mask=mask, k_exp=ke, v_exp=ve, lse=True)
+    st = _status()
+    out, lse = bd.sdv_tree_attn(q, kc, vc, table, _i32(ctx), count=t["count"], mask=mask, k_exp=ke, v_exp=ve, lse=True,
+                                status=st)
+    assert int(st) == 0
     half = ref.HALF_STEP[dtype]
     for b in range(B):
         o, x = bd.sdv_tree_attn(q[b:b + 1], kc, vc, table[b:b + 1].contiguous(), _i32(ctx[b:b + 1]),
