@@ -547,6 +547,8 @@ def _array(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, name: str) -> 
     """Address of a contiguous device array of n entries (None stays None)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.is_cuda and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_cuda:
@@ -558,14 +560,22 @@ def _array(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, name: str) -> 
 
 def _rows_of(t: torch.Tensor, dims: int, name: str):
     """(shape, strides) of a device tensor whose innermost dimension is contiguous."""
-    if t.dim() != dims:
-        raise ValueError("%s must have %d dimensions, got %s" % (name, dims, tuple(t.shape)))
+    shape, stride = t.shape, t.stride()
+    if len(stride) != dims:
+        raise ValueError("%s must have %d dimensions, got %s" % (name, dims, tuple(shape)))
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    stride = t.stride()
-    if stride[-1] != 1 and t.shape[-1] != 1:
+    if stride[-1] != 1 and shape[-1] != 1:
         raise ValueError("%s must be contiguous in its last dimension" % name)
-    return t.shape, stride
+    return shape, stride
+
+
+def _stream_of(t: torch.Tensor, stream) -> int:
+    """Handle of `stream`, or of the current stream of t's device (asked for
+    without building a Stream object: these calls come once per layer)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return _stream_handle(stream)
 
 
 def _type_of(types: dict, dtype: torch.dtype, name: str) -> int:
@@ -577,12 +587,11 @@ def _type_of(types: dict, dtype: torch.dtype, name: str) -> int:
 
 def _cache_of(k_cache, v_cache, k_exp, v_exp) -> _KVCache:
     shape, ks = _rows_of(k_cache, 4, "k_cache")
-    vshape, vs = _rows_of(v_cache, 4, "v_cache")
     pages, heads, place, dim = shape
-    code = _type_of(_CELL_TYPES, k_cache.dtype, "the cache")
-    inner = (place * dim, dim, 1)
-    if vshape != shape or v_cache.dtype != k_cache.dtype or vs[0] != ks[0] \
-            or tuple(ks[1:]) != inner or tuple(vs[1:]) != inner:
+    dtype = k_cache.dtype
+    code = _type_of(_CELL_TYPES, dtype, "the cache")
+    if v_cache.shape != shape or v_cache.dtype != dtype or v_cache.stride() != ks or not v_cache.is_cuda \
+            or ks[1] != place * dim or ks[2] != dim:
         raise ValueError("k_cache and v_cache must be [pages, kv_heads, page_size, head_dim] of one "
                          "type and page stride, each page contiguous")
     exp_stride, ke, ve = 0, None, None
@@ -594,8 +603,8 @@ def _cache_of(k_cache, v_cache, k_exp, v_exp) -> _KVCache:
             if t.dtype != torch.uint8 or eshape != shape[:3] or es[1] != place:
                 raise ValueError("%s must be uint8 [pages, kv_heads, page_size], each page contiguous"
                                  % name)
-        exp_stride = k_exp.stride(0)
-        if v_exp.stride(0) != exp_stride:
+        exp_stride = es[0]
+        if k_exp.stride(0) != exp_stride:
             raise ValueError("k_exp and v_exp must have one page stride")
         ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
     elif k_exp is not None or v_exp is not None:
@@ -605,8 +614,9 @@ def _cache_of(k_cache, v_cache, k_exp, v_exp) -> _KVCache:
 
 
 def _table_of(block_table: torch.Tensor, B: int) -> int:
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [%d, max_pages], got %s" % (B, tuple(block_table.shape)))
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != B:
+        raise ValueError("block_table must be [%d, max_pages], got %s" % (B, tuple(shape)))
     return _array(block_table, block_table.numel(), torch.int32, "block_table")
 
 
@@ -670,9 +680,11 @@ def sdv_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor
     code = _type_of(_ROPE_TYPES, q.dtype, "q")
     if out_q is None:
         out_q = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    oshape, os_ = _rows_of(out_q, 3, "out_q")
-    if oshape != q.shape or out_q.dtype != q.dtype:
-        raise ValueError("out_q must have q's shape and type")
+        os_ = (Hq * D, D)
+    else:
+        oshape, os_ = _rows_of(out_q, 3, "out_q")
+        if oshape != q.shape or out_q.dtype != q.dtype:
+            raise ValueError("out_q must have q's shape and type")
     Hk, kp, ks, okp, oks = 0, None, (0, 0), None, (0, 0)
     if k is not None:
         kshape, ks = _rows_of(k, 3, "k")
@@ -681,15 +693,17 @@ def sdv_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor
             raise ValueError("k must be [%d, Hk, %d] of q's type" % (T, D))
         if out_k is None:
             out_k = torch.empty(kshape, dtype=k.dtype, device=k.device)
-        okshape, oks = _rows_of(out_k, 3, "out_k")
-        if okshape != kshape or out_k.dtype != k.dtype:
-            raise ValueError("out_k must have k's shape and type")
+            oks = (Hk * D, D)
+        else:
+            okshape, oks = _rows_of(out_k, 3, "out_k")
+            if okshape != kshape or out_k.dtype != k.dtype:
+                raise ValueError("out_k must have k's shape and type")
         kp, okp = k.data_ptr(), out_k.data_ptr()
     elif out_k is not None:
         raise ValueError("out_k without k")
     half = inv_freq.numel()
     st = load().sdv_rope(T, Hq, Hk, D, 2 * half, 1 if interleaved else 0, code,
-                         _stream_handle(stream), q.data_ptr(), qs[0], qs[1], kp, ks[0], ks[1],
+                         _stream_of(q, stream), q.data_ptr(), qs[0], qs[1], kp, ks[0], ks[1],
                          _array(positions, T, torch.int32, "positions"),
                          _array(inv_freq, half, torch.float32, "inv_freq"), factor,
                          out_q.data_ptr(), os_[0], os_[1], okp, oks[0], oks[1])
@@ -713,7 +727,7 @@ def sdv_kv_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     if vshape != k.shape or v.dtype != k.dtype or H != cache.kv_heads or D != cache.head_dim:
         raise ValueError("k and v must be [B, N, %d, %d] of one type" % (cache.kv_heads, cache.head_dim))
     code = _type_of(_HALF_TYPES, k.dtype, "k")
-    st = load().sdv_kv_write(cache, B, N, code, _stream_handle(stream), k.data_ptr(), ks[0], ks[1],
+    st = load().sdv_kv_write(cache, B, N, code, _stream_of(k, stream), k.data_ptr(), ks[0], ks[1],
                              ks[2], v.data_ptr(), vs[0], vs[1], vs[2], _table_of(block_table, B),
                              block_table.shape[1], _array(start, B, torch.int32, "start"),
                              _array(count, B, torch.int32, "count"), _status_of(status))
@@ -735,7 +749,7 @@ def sdv_kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch
     code = _type_of(_HALF_TYPES, dtype, "dtype")
     B = start.numel()
     out = torch.empty((2, B, N, cache.kv_heads, cache.head_dim), dtype=dtype, device=k_cache.device)
-    st = load().sdv_kv_read(cache, B, N, code, _stream_handle(stream), out[0].data_ptr(),
+    st = load().sdv_kv_read(cache, B, N, code, _stream_of(k_cache, stream), out[0].data_ptr(),
                             out[1].data_ptr(), _table_of(block_table, B), block_table.shape[1],
                             _array(start, B, torch.int32, "start"),
                             _array(count, B, torch.int32, "count"), _status_of(status))
@@ -756,7 +770,7 @@ def sdv_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: tor
     B, K, G = nodes.shape
     if out_len is None:
         out_len = torch.empty(B, dtype=torch.int32, device=nodes.device)
-    st = load().sdv_kv_commit(cache, B, K, G, _stream_handle(stream), _table_of(block_table, B),
+    st = load().sdv_kv_commit(cache, B, K, G, _stream_of(k_cache, stream), _table_of(block_table, B),
                               block_table.shape[1], _array(start, B, torch.int32, "start"),
                               _array(nodes, B * K * G, torch.int32, "nodes"),
                               _array(sel, B, torch.int32, "sel"),
@@ -788,17 +802,19 @@ def sdv_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     if D != cache.head_dim:
         raise ValueError("q must be [B, N, Hq, %d]" % cache.head_dim)
     lib = load()
-    handle = _stream_handle(stream)
+    handle = _stream_of(q, stream)
     mask_sb, W = 0, (N + 31) // 32
     if mask is not None:
         shape = tuple(mask.shape)
         if shape != (N, W) and shape != (B, N, W):
             raise ValueError("mask must be [%d, %d] or [%d, %d, %d]" % (N, W, B, N, W))
         mask_sb = N * W if len(shape) == 3 else 0
+    out_p = _array(out, B * N * Hq * D, q.dtype, "out")
     if out is None:
         out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
+        out_p = out.data_ptr()
     logs = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device) if lse else None
-    ws_bytes = lib.sdv_tree_attn_workspace()
+    ws_bytes = lib.sdv_tree_attn_workspace() if workspace is None else 0
     if workspace is None:
         if stream is None:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
@@ -814,7 +830,7 @@ def sdv_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         _array(count, B, torch.int32, "count"),
         None if mask is None else _array(mask, mask.numel(), torch.int32, "mask"), mask_sb,
         D ** -0.5 if scale is None else scale,
-        _array(out, B * N * Hq * D, q.dtype, "out"), None if logs is None else logs.data_ptr(),
+        out_p, None if logs is None else logs.data_ptr(),
         workspace.data_ptr(), workspace.numel(), _status_of(status))
     if st != SDV_OK:
         raise SdvError(st, "sdv_tree_attn")
@@ -855,7 +871,7 @@ def sdv_logits_process(logits: torch.Tensor, drafts: torch.Tensor,
         out = torch.empty((B, K, G + 1, V), dtype=logits.dtype, device=logits.device)
     i32, f32 = torch.int32, torch.float32
     st = load().sdv_logits_process(
-        B, K, G, V, code, _stream_handle(stream), _array(logits, logits.numel(), logits.dtype, "logits"),
+        B, K, G, V, code, _stream_of(logits, stream), _array(logits, logits.numel(), logits.dtype, "logits"),
         nsrc, _array(rows, B * K * (G + 1), i32, "rows"), _array(drafts, B * K * G, i32, "drafts"),
         _array(counts, B * V, i32, "counts"), _array(prompt, B * W, i32, "prompt"),
         _array(repetition, B, f32, "repetition"), _array(frequency, B, f32, "frequency"),
@@ -876,7 +892,7 @@ def sdv_counts_commit(counts: torch.Tensor, drafts: torch.Tensor, sel: torch.Ten
     B, K, G = drafts.shape
     V = counts.shape[-1]
     i32 = torch.int32
-    st = load().sdv_counts_commit(B, K, G, V, _stream_handle(stream),
+    st = load().sdv_counts_commit(B, K, G, V, _stream_of(counts, stream),
                                   _array(drafts, B * K * G, i32, "drafts"), _array(sel, B, i32, "sel"),
                                   _array(accept_len, B, i32, "accept_len"),
                                   _array(next_token, B, i32, "next_token"),

@@ -66,151 +66,165 @@ template <bool VEC> __device__ __forceinline__ uint4 load8(const unsigned char* 
     }
 }
 
-// The page of position `pos` of sequence b, or -1 with the status set.
-__device__ __forceinline__ int page_of(const CellsArgs& a, int b, int64_t pos, unsigned* st) {
-    if (pos < 0 || pos >= static_cast<int64_t>(a.max_pages) * a.c.P) {
-        *st = kStatusBadLength;
+// A thread's work: R positions from n on, one head of the keys or the values.
+struct Rows {
+    int b, n, h, cnt, start;
+    bool isv, live;
+};
+
+// Item w of the grid: (b, block of R positions, k or v, h), heads fastest.
+template <int R> __device__ __forceinline__ Rows rows_of(const CellsArgs& a, int64_t w) {
+    Rows r;
+    const unsigned hv = 2u * a.c.H, blocks = static_cast<unsigned>((a.N + R - 1) / R);
+    r.live = w < static_cast<int64_t>(a.B) * blocks * hv;
+    if (!r.live) w = 0;
+    const unsigned long long bn = static_cast<unsigned long long>(w) / hv;
+    const int x = static_cast<int>(static_cast<unsigned long long>(w) - bn * hv);
+    r.isv = x >= a.c.H;
+    r.h = r.isv ? x - a.c.H : x;
+    r.b = static_cast<int>(bn / blocks);
+    r.n = static_cast<int>(bn - static_cast<unsigned long long>(r.b) * blocks) * R;
+    r.cnt = a.count ? __ldg(a.count + r.b) : a.N;
+    r.start = __ldg(a.start + r.b);
+    return r;
+}
+
+// Where position n of the item sits: its page (or -1, with the status set, or
+// -2: there is no such row) and its row within the page.
+__device__ __forceinline__ int place_of(const CellsArgs& a, const Rows& r, int n, int64_t* cell, unsigned* st) {
+    if (!r.live || n >= a.N) return -2;
+    if (r.cnt < 0 || r.cnt > a.N) {
+        *st |= kStatusBadLength;
         return -1;
     }
-    const int page = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + pos / a.c.P);
+    if (n >= r.cnt) return -2;
+    const int64_t pos = static_cast<int64_t>(r.start) + n;
+    if (pos < 0 || pos >= static_cast<int64_t>(a.max_pages) * a.c.P) {
+        *st |= kStatusBadLength;
+        return -1;
+    }
+    const int p = static_cast<int>(pos), i = p / a.c.P;          // at most 2^30 positions
+    *cell = static_cast<int64_t>(r.h) * a.c.P + (p - i * a.c.P);
+    const int page = __ldg(a.table + static_cast<int64_t>(r.b) * a.max_pages + i);
     if (page < 0 || page >= a.c.pages) {
-        *st = kStatusBadPage;
+        *st |= kStatusBadPage;
         return -1;
     }
     return page;
 }
 
-struct Row {
-    int b, n, h;
-    bool isv, live;
-    int cnt;
-};
-
-// Item w of the grid: (b, n, k or v, h), heads fastest.
-__device__ __forceinline__ Row row_of(const CellsArgs& a, int64_t w) {
-    Row r;
-    const int hv = 2 * a.c.H;
-    r.live = w < static_cast<int64_t>(a.B) * a.N * hv;
-    if (!r.live) w = 0;
-    const int64_t bn = w / hv;
-    const int x = static_cast<int>(w - bn * hv);
-    r.isv = x >= a.c.H;
-    r.h = r.isv ? x - a.c.H : x;
-    r.b = static_cast<int>(bn / a.N);
-    r.n = static_cast<int>(bn - static_cast<int64_t>(r.b) * a.N);
-    r.cnt = a.count ? __ldg(a.count + r.b) : a.N;
-    return r;
-}
-
-template <int TYPE, bool E4M3, bool VEC, int LANES>
+template <int TYPE, bool E4M3, bool VEC, int LANES, int R>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CellsArgs a) {
     const int lane = threadIdx.x % LANES;
-    const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / LANES;
-    const Row r = row_of(a, w);
+    const Rows r = rows_of<R>(a, (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / LANES);
+    const bool mine = lane * 8 < a.c.D;
+    const unsigned char* src = (r.isv ? a.v + r.b * a.v_sb + r.h * a.v_sh : a.k + r.b * a.k_sb + r.h * a.k_sh) + lane * 16;
+    const int64_t sn = r.isv ? a.v_sn : a.k_sn;
+    uint4 x[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i)                     // whatever becomes of a row, it may be read
+        x[i] = r.live && mine && r.n + i < a.N ? load8<VEC>(src + (r.n + i) * sn) : make_uint4(0, 0, 0, 0);
     unsigned st = 0;
-    bool go = r.live;
-    if (r.cnt < 0 || r.cnt > a.N) st = kStatusBadLength, go = false;
-    if (r.n >= r.cnt) go = false;
-    const int64_t pos = static_cast<int64_t>(__ldg(a.start + r.b)) + r.n;
-    int page = 0;
-    if (go) {
-        page = page_of(a, r.b, pos, &st);
-        go = page >= 0;
-    }
-    if (st && r.live && lane == 0 && a.status) atomicOr(a.status, st);
-    const bool mine = go && lane * 8 < a.c.D;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (mine)
-        x = load8<VEC>((r.isv ? a.v + r.b * a.v_sb + r.n * a.v_sn + r.h * a.v_sh
-                              : a.k + r.b * a.k_sb + r.n * a.k_sn + r.h * a.k_sh) + lane * 16);
-    const int64_t cell = static_cast<int64_t>(r.h) * a.c.P + pos % a.c.P;   // row within the page
-    unsigned char* dst = (r.isv ? a.c.v : a.c.k) + page * a.c.page_stride;
-    if constexpr (!E4M3) {
-        if (mine) *reinterpret_cast<uint4*>(dst + cell * a.c.D * 2 + lane * 16) = x;
-    } else {
-        float f[8], top = 0.0f;
-        int bad = 0;
-        widen<TYPE>(x, f);
+    int page[R];
+    int64_t cell[R];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            top = fmaxf(top, fabsf(f[i]));
-            bad |= !(fabsf(f[i]) < INFINITY);
-        }
+    for (int i = 0; i < R; ++i) page[i] = place_of(a, r, r.n + i, &cell[i], &st);
+    if (st && lane == 0 && a.status) atomicOr(a.status, st);
 #pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-        }
-        // top = 1.m 2^x <= 448 2^e: e = x - 8 while 1.m <= 1.75, else x - 7
-        // (a subnormal or zero top has x = -127 and ends at the floor as well)
-        const int bits = __float_as_int(top);
-        int e = (bits >> 23) - 127 - ((bits & 0x7fffff) <= 0x600000 ? 8 : 7);
-        e = e < -126 ? -126 : e;
-        const float inv = pow2f(-e);
-        uint32_t o[2];
+    for (int i = 0; i < R; ++i) {
+        const bool go = page[i] >= 0;
+        unsigned char* dst = (r.isv ? a.c.v : a.c.k) + (go ? page[i] * a.c.page_stride : 0);
+        if constexpr (!E4M3) {
+            if (go && mine) *reinterpret_cast<uint4*>(dst + cell[i] * a.c.D * 2 + lane * 16) = x[i];
+        } else {
+            float f[8], top = 0.0f;
+            int bad = 0;
+            widen<TYPE>(x[i], f);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
-                make_float2(f[4 * i] * inv, f[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-            const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
-                make_float2(f[4 * i + 2] * inv, f[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-            o[i] = bad ? 0x7f7f7f7fu : static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
-        }
-        if (mine) {
-            *reinterpret_cast<uint2*>(dst + cell * a.c.D + lane * 8) = make_uint2(o[0], o[1]);
-            if (lane == 0)
-                (r.isv ? a.c.ve : a.c.ke)[page * a.c.exp_page_stride + cell] =
-                    static_cast<unsigned char>(bad ? 255 : e + 127);
+            for (int e = 0; e < 8; ++e) {
+                top = fmaxf(top, fabsf(f[e]));
+                bad |= !(fabsf(f[e]) < INFINITY);
+            }
+            // the largest magnitude's bits; all ones where something is not a number
+            unsigned bits = bad ? 0x7fffffffu : __float_as_uint(top);
+#pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+            bad = bits == 0x7fffffffu;
+            // top = 1.m 2^x <= 448 2^e: e = x - 8 while 1.m <= 1.75, else x - 7
+            // (a subnormal or zero top has x = -127 and ends at the floor as well)
+            int e = static_cast<int>(bits >> 23) - 127 - ((bits & 0x7fffff) <= 0x600000 ? 8 : 7);
+            e = e < -126 ? -126 : e;
+            const float inv = pow2f(-e);
+            uint32_t o[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
+                    make_float2(f[4 * y] * inv, f[4 * y + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+                const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
+                    make_float2(f[4 * y + 2] * inv, f[4 * y + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+                o[y] = bad ? 0x7f7f7f7fu : static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+            }
+            if (go && mine) {
+                *reinterpret_cast<uint2*>(dst + cell[i] * a.c.D + lane * 8) = make_uint2(o[0], o[1]);
+                if (lane == 0)
+                    (r.isv ? a.c.ve : a.c.ke)[page[i] * a.c.exp_page_stride + cell[i]] =
+                        static_cast<unsigned char>(bad ? 255 : e + 127);
+            }
         }
     }
 }
 
-template <int TYPE, bool E4M3, int LANES>
+template <int TYPE, bool E4M3, int LANES, int R>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CellsArgs a) {
     const int lane = threadIdx.x % LANES;
-    const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / LANES;
-    const Row r = row_of(a, w);
+    const Rows r = rows_of<R>(a, (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / LANES);
     if (!r.live || lane * 8 >= a.c.D) return;
     unsigned st = 0;
-    int page = -1;
-    bool zero = false;
-    const int64_t pos = static_cast<int64_t>(__ldg(a.start + r.b)) + r.n;
-    if (r.cnt < 0 || r.cnt > a.N)
-        st = kStatusBadLength;
-    else if (r.n >= r.cnt)
-        zero = true;
-    else
-        page = page_of(a, r.b, pos, &st);
+    int page[R], ex[R];
+    uint4 x[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        int64_t cell = 0;
+        page[i] = place_of(a, r, r.n + i, &cell, &st);
+        ex[i] = 127;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (page[i] >= 0) {
+            const unsigned char* src = (r.isv ? a.c.v : a.c.k) + page[i] * a.c.page_stride;
+            if constexpr (E4M3) {
+                const uint2 q = __ldcs(reinterpret_cast<const uint2*>(src + cell * a.c.D + lane * 8));
+                x[i].x = q.x, x[i].y = q.y;
+                ex[i] = __ldg((r.isv ? a.c.ve : a.c.ke) + page[i] * a.c.exp_page_stride + cell);
+            } else {
+                x[i] = __ldcs(reinterpret_cast<const uint4*>(src + cell * a.c.D * 2 + lane * 16));
+            }
+        }
+    }
     if (st && lane == 0 && a.status) atomicOr(a.status, st);
-    uint4 o = make_uint4(0, 0, 0, 0);
-    if (page >= 0) {
-        const int64_t cell = static_cast<int64_t>(r.h) * a.c.P + pos % a.c.P;
-        const unsigned char* src = (r.isv ? a.c.v : a.c.k) + page * a.c.page_stride;
-        if constexpr (!E4M3) {
-            o = __ldcs(reinterpret_cast<const uint4*>(src + cell * a.c.D * 2 + lane * 16));
-        } else {
-            const uint2 q = __ldcs(reinterpret_cast<const uint2*>(src + cell * a.c.D + lane * 8));
-            const int ex = (r.isv ? a.c.ve : a.c.ke)[page * a.c.exp_page_stride + cell];
+    unsigned char* dst = static_cast<unsigned char*>(r.isv ? a.ov : a.ok);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (r.n + i >= a.N) break;
+        uint4 o = x[i];
+        if (page[i] == -1) {
+            o = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);   // NaN in either type
+        } else if constexpr (E4M3) {
             // 2^(ex - 127) (0 stands for 2^-127, a subnormal), 255: not a number
-            const float unit = ex == 255 ? __int_as_float(0x7fc00000)
-                               : ex == 0 ? __int_as_float(0x00400000) : __int_as_float(ex << 23);
-            const uint32_t ww[2] = {q.x, q.y};
+            const float unit = ex[i] == 255 ? __int_as_float(0x7fc00000)
+                               : ex[i] == 0 ? __int_as_float(0x00400000) : __int_as_float(ex[i] << 23);
+            const uint32_t w[2] = {x[i].x, x[i].y};
             uint32_t out[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int y = 0; y < 4; ++y) {
                 const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-                    static_cast<__nv_fp8x2_storage_t>(ww[i / 2] >> (16 * (i % 2))), __NV_E4M3);
+                    static_cast<__nv_fp8x2_storage_t>(w[y / 2] >> (16 * (y % 2))), __NV_E4M3);
                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                out[i] = narrow2<TYPE>(f.x * unit, f.y * unit);
+                out[y] = narrow2<TYPE>(f.x * unit, f.y * unit);
             }
             o = make_uint4(out[0], out[1], out[2], out[3]);
         }
-    } else if (!zero) {
-        o = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);   // NaN in either type
+        const int64_t row = (static_cast<int64_t>(r.b) * a.N + r.n + i) * a.c.H + r.h;
+        __stcs(reinterpret_cast<uint4*>(dst + row * a.c.D * 2 + lane * 16), o);
     }
-    unsigned char* dst = static_cast<unsigned char*>(r.isv ? a.ov : a.ok);
-    const int64_t row = (static_cast<int64_t>(r.b) * a.N + r.n) * a.c.H + r.h;
-    __stcs(reinterpret_cast<uint4*>(dst + row * a.c.D * 2 + lane * 16), o);
 }
 
 // One CTA per sequence; a thread moves one piece of a row (or one exponent) of
@@ -276,18 +290,26 @@ __global__ void __launch_bounds__(kThreads) kv_commit_kernel(const CommitArgs a)
     }
 }
 
-template <int LANES> dim3 grid_of(const CellsArgs& a) {
-    const int64_t rows = static_cast<int64_t>(a.B) * a.N * 2 * a.c.H;
-    return dim3(static_cast<unsigned>((rows * LANES + kThreads - 1) / kThreads));
+// Positions a thread takes: several where there are many, for loads in flight.
+constexpr int kMany = 4, kManyFrom = 32;
+
+template <int LANES, int R> dim3 grid_of(const CellsArgs& a) {
+    const int64_t items = static_cast<int64_t>(a.B) * ((a.N + R - 1) / R) * 2 * a.c.H;
+    return dim3(static_cast<unsigned>((items * LANES + kThreads - 1) / kThreads));
+}
+
+template <int TYPE, bool E4M3, int LANES, int R>
+cudaError_t write_rows(const CellsArgs& a, bool vec, cudaStream_t s) {
+    if (vec)
+        kv_write_kernel<TYPE, E4M3, true, LANES, R><<<grid_of<LANES, R>(a), kThreads, 0, s>>>(a);
+    else
+        kv_write_kernel<TYPE, E4M3, false, LANES, R><<<grid_of<LANES, R>(a), kThreads, 0, s>>>(a);
+    return cudaGetLastError();
 }
 
 template <int TYPE, bool E4M3, int LANES>
 cudaError_t write_lanes(const CellsArgs& a, bool vec, cudaStream_t s) {
-    if (vec)
-        kv_write_kernel<TYPE, E4M3, true, LANES><<<grid_of<LANES>(a), kThreads, 0, s>>>(a);
-    else
-        kv_write_kernel<TYPE, E4M3, false, LANES><<<grid_of<LANES>(a), kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return a.N >= kManyFrom ? write_rows<TYPE, E4M3, LANES, kMany>(a, vec, s) : write_rows<TYPE, E4M3, LANES, 1>(a, vec, s);
 }
 
 template <int TYPE, bool E4M3>
@@ -297,15 +319,19 @@ cudaError_t write_typed(const CellsArgs& a, bool vec, cudaStream_t s) {
     return write_lanes<TYPE, E4M3, 32>(a, vec, s);
 }
 
+template <int TYPE, bool E4M3, int LANES> cudaError_t read_lanes(const CellsArgs& a, cudaStream_t s) {
+    if (a.N >= kManyFrom)
+        kv_read_kernel<TYPE, E4M3, LANES, kMany><<<grid_of<LANES, kMany>(a), kThreads, 0, s>>>(a);
+    else
+        kv_read_kernel<TYPE, E4M3, LANES, 1><<<grid_of<LANES, 1>(a), kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
 template <int TYPE, bool E4M3>
 cudaError_t read_typed(const CellsArgs& a, cudaStream_t s) {
-    if (a.c.D <= 64)
-        kv_read_kernel<TYPE, E4M3, 8><<<grid_of<8>(a), kThreads, 0, s>>>(a);
-    else if (a.c.D <= 128)
-        kv_read_kernel<TYPE, E4M3, 16><<<grid_of<16>(a), kThreads, 0, s>>>(a);
-    else
-        kv_read_kernel<TYPE, E4M3, 32><<<grid_of<32>(a), kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    if (a.c.D <= 64) return read_lanes<TYPE, E4M3, 8>(a, s);
+    if (a.c.D <= 128) return read_lanes<TYPE, E4M3, 16>(a, s);
+    return read_lanes<TYPE, E4M3, 32>(a, s);
 }
 
 }  // namespace

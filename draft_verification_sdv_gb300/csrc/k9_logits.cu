@@ -5,8 +5,9 @@
 // Row (b, k, j) counts the history of sequence b and the first j tokens of
 // draft k, so the rows of one draft differ by one token from one to the next.
 // A CTA therefore owns a slice of the vocabulary and walks the rows of one
-// draft: the counts, prompt bits and biases of its slice are read once and stay
-// in registers, and the thread that owns draft token j counts it after row j.
+// sequence, draft by draft: the counts, prompt bits and biases of its slice are
+// in registers (the counts are read again at each draft's start), and the thread
+// that owns draft token j counts it after row j.
 //
 // Bound by HBM: each logit is read and written once (2 + 2 bytes in bf16, and a
 // bit of the grammar mask).  Four rows are in flight per thread.
@@ -31,34 +32,24 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs a) {
     __shared__ int2 s_raw[kBiasPass];               // (place in the list, id)
     __shared__ int2 s_bias[kBiasPass];              // (id, value) in the list's order
     const unsigned slices = (static_cast<unsigned>(a.V) + kSlice - 1) / kSlice;
-    const int bk = static_cast<int>(blockIdx.x / slices);
-    const int b = bk / a.K, k = bk % a.K;
+    const int b = static_cast<int>(blockIdx.x / slices);
     const int slice0 = static_cast<int>(blockIdx.x % slices) * kSlice;
     const int v0 = slice0 + threadIdx.x * E;        // this thread's first token
     const bool live = v0 < a.V;                     // V is a multiple of E
-    const int rows = a.G + 1;
-    const int j0 = static_cast<int>(static_cast<int64_t>(blockIdx.y) * rows / a.row_splits);
-    const int j1 = static_cast<int>(static_cast<int64_t>(blockIdx.y + 1) * rows / a.row_splits);
+    const int rows = a.G + 1;                       // of a draft
+    const int64_t all = static_cast<int64_t>(a.K) * rows;
+    const int r0 = static_cast<int>(blockIdx.y * all / a.row_splits);
+    const int r1 = static_cast<int>((blockIdx.y + 1) * all / a.row_splits);
 
-    const float rep = a.rep ? a.rep[b] : 1.0f;
+    const float rep = a.rep ? a.rep[b] : 1.0f, inv = 1.0f / rep;
     const float freq = a.freq ? a.freq[b] : 0.0f, pres = a.pres ? a.pres[b] : 0.0f;
     int c[E];
     float bias[E], add[E];
-    unsigned seen = 0;                              // bit e: the repetition penalty applies
+    unsigned prompt = 0, seen = 0;                  // bit e: in the prompt; the repetition penalty applies
 #pragma unroll
-    for (int e = 0; e < E; ++e) c[e] = 0, bias[e] = 0.0f;
-    if (live) {
-        if (a.counts) {
-            const int4* p = reinterpret_cast<const int4*>(a.counts + static_cast<int64_t>(b) * a.V + v0);
-#pragma unroll
-            for (int u = 0; u < E / 4; ++u) {
-                const int4 x = __ldg(p + u);
-                c[4 * u] = x.x, c[4 * u + 1] = x.y, c[4 * u + 2] = x.z, c[4 * u + 3] = x.w;
-            }
-        }
-        if (a.prompt)
-            seen = static_cast<unsigned>(__ldg(a.prompt + static_cast<int64_t>(b) * a.W + (v0 >> 5))) >> (v0 & 31);
-    }
+    for (int e = 0; e < E; ++e) bias[e] = 0.0f;
+    if (live && a.prompt)
+        prompt = static_cast<unsigned>(__ldg(a.prompt + static_cast<int64_t>(b) * a.W + (v0 >> 5))) >> (v0 & 31);
     for (int m0 = 0; m0 < a.M; m0 += kBiasPass) {   // the biases that fall into the slice
         if (threadIdx.x == 0) s_n = 0;
         __syncthreads();
@@ -88,46 +79,59 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs a) {
     }
     if (!live) return;
 
-    const int32_t* dr = a.drafts + (static_cast<int64_t>(b) * a.K + k) * a.G;
-    auto count_token = [&](int tok) {
-        const int off = tok - v0;
-        if (tok >= 0 && off >= 0 && off < E) {
+    auto history = [&] {                            // the counts before a draft's first token
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (e == off) ++c[e];
+        for (int e = 0; e < E; ++e) c[e] = 0;
+        if (a.counts) {
+            const int4* p = reinterpret_cast<const int4*>(a.counts + static_cast<int64_t>(b) * a.V + v0);
+#pragma unroll
+            for (int u = 0; u < E / 4; ++u) {
+                const int4 x = __ldg(p + u);
+                c[4 * u] = x.x, c[4 * u + 1] = x.y, c[4 * u + 2] = x.z, c[4 * u + 3] = x.w;
+            }
         }
     };
+    auto count_token = [&](int tok) {
+        if (tok < v0 || tok >= v0 + E) return false;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (e == tok - v0) ++c[e];
+        return true;
+    };
     auto settle = [&] {                             // what the counts come to
+        seen = prompt;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             if (c[e] > 0) seen |= 1u << e;
             add[e] = (bias[e] - freq * static_cast<float>(c[e])) - (c[e] > 0 ? pres : 0.0f);
         }
     };
-    for (int i = 0; i < j0; ++i) count_token(dr[i]);
+    const int32_t* dr = a.drafts + static_cast<int64_t>(b) * a.K * a.G;
+    int k = r0 / rows, j = r0 - k * rows;           // the next row
+    history();
+    for (int i = 0; i < j; ++i) count_token(dr[k * a.G + i]);
     settle();
 
-    const int64_t row0 = (static_cast<int64_t>(b) * a.K + k) * rows;
-    const int64_t nvec = a.V / E;
+    const int64_t row0 = b * all, nvec = a.V / E;
     const uint4* in = static_cast<const uint4*>(a.logits);
     uint4* out = static_cast<uint4*>(a.out) + row0 * nvec + v0 / E;
     const int32_t* allow = a.allow ? a.allow + row0 * a.W + (v0 >> 5) : nullptr;
 
-    for (int j = j0; j < j1; j += kFlight) {
+    for (int r = r0; r < r1; r += kFlight) {
         uint4 x[kFlight];
         unsigned ok[kFlight];
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            if (j + u >= j1) break;
-            int64_t src = row0 + j + u;
+            if (r + u >= r1) break;
+            int64_t src = row0 + r + u;
             bool good = true;
             if (a.rows) {
-                const int r = __ldg(a.rows + row0 + j + u);
-                good = r >= 0 && r < a.nsrc;
-                src = static_cast<int64_t>(b) * a.nsrc + (good ? r : 0);
+                const int s = __ldg(a.rows + row0 + r + u);
+                good = s >= 0 && s < a.nsrc;
+                src = static_cast<int64_t>(b) * a.nsrc + (good ? s : 0);
                 if (!good && a.status) atomicOr(a.status, kStatusBadLength);
             }
-            ok[u] = allow ? static_cast<unsigned>(__ldg(allow + static_cast<int64_t>(j + u) * a.W)) >> (v0 & 31)
+            ok[u] = allow ? static_cast<unsigned>(__ldg(allow + static_cast<int64_t>(r + u) * a.W)) >> (v0 & 31)
                           : 0xffffffffu;
             if (good)
                 x[u] = __ldcs(in + src * nvec + v0 / E);
@@ -136,36 +140,36 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs a) {
         }
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            if (j + u >= j1) break;
-            float f[E];
+            if (r + u >= r1) break;
+            if (j == rows) {                        // the next draft
+                j = 0;
+                ++k;
+                history();
+                settle();
+            }
             const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                f[e] = BF16 ? ((e & 1) ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2])) : __uint_as_float(w[e % 4]);
+            float f[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                if (seen >> e & 1) f[e] = f[e] > 0.0f ? f[e] / rep : f[e] * rep;
+                f[e] = BF16 ? ((e & 1) ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2])) : __uint_as_float(w[e % 4]);
+                // x / rep as x * (1 / rep): a rounding more in fp32
+                if (seen >> e & 1) f[e] *= f[e] > 0.0f ? inv : rep;
                 f[e] += add[e];
                 if (!(ok[u] >> e & 1)) f[e] = -INFINITY;
             }
-            uint32_t r[4];
+            uint32_t o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if constexpr (BF16) {
                     const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-                    r[i] = *reinterpret_cast<const uint32_t*>(&h);
+                    o[i] = *reinterpret_cast<const uint32_t*>(&h);
                 } else {
-                    r[i] = __float_as_uint(f[i]);
+                    o[i] = __float_as_uint(f[i]);
                 }
             }
-            __stcs(out + static_cast<int64_t>(j + u) * nvec, make_uint4(r[0], r[1], r[2], r[3]));
-            if (j + u < a.G) {
-                const int tok = __ldg(dr + j + u);
-                if (tok >= v0 && tok < v0 + E) {
-                    count_token(tok);
-                    settle();
-                }
-            }
+            __stcs(out + static_cast<int64_t>(r + u) * nvec, make_uint4(o[0], o[1], o[2], o[3]));
+            if (j < a.G && count_token(__ldg(dr + k * a.G + j))) settle();
+            ++j;
         }
     }
 }
@@ -192,11 +196,12 @@ __global__ void __launch_bounds__(128) counts_kernel(const CountsArgs a) {
 cudaError_t launch_logits(const LogitsArgs& args, bool bf16, int nsm, cudaStream_t s) {
     LogitsArgs a = args;
     const int slice = kThreads * (bf16 ? 8 : 4);
-    const int64_t base = static_cast<int64_t>((a.V + slice - 1) / slice) * a.B * a.K;
-    // Few drafts: their rows are shared out until every SM has about eight CTAs,
-    // a CTA keeping four rows at least (its counts are then read for those).
+    const int64_t base = static_cast<int64_t>((a.V + slice - 1) / slice) * a.B;
+    // Few sequences: their rows are shared out until every SM has about eight
+    // CTAs, a CTA keeping four rows at least (its counts and biases serve those).
+    const int64_t all = static_cast<int64_t>(a.K) * (a.G + 1);
     int64_t split = (static_cast<int64_t>(nsm) * 8 + base - 1) / base;
-    const int64_t most = (a.G + kFlight) / kFlight;
+    const int64_t most = (all + kFlight - 1) / kFlight;
     a.row_splits = static_cast<int>(split < 1 ? 1 : split > most ? most : split);
     const dim3 grid(static_cast<unsigned>(base), static_cast<unsigned>(a.row_splits));
     if (bf16)
