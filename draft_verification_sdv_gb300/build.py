@@ -17,9 +17,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsdv.so")
 SOURCES = ["k1_rowpass.cu", "k2_select.cu", "k3_sample.cu", "k4_cps.cu", "k5_adl.cu", "k6_rope.cu", "k7_kvcache.cu",
-           "k8_attn.cu", "k8_attn_tc.cu", "k8_attn_mma64.cu", "k8_attn_mma128.cu", "k8_attn_mma256.cu", "k9_logits.cu", "k10_tree.cu",
+           "k8_attn.cu", "k8_attn_tc.cu", "k8_attn_dec.cu", "k8_attn_mma64.cu", "k8_attn_mma128.cu", "k8_attn_mma256.cu", "k9_logits.cu", "k10_tree.cu",
            "sdv_api.cu", "sdv_layer.cu", "sdv_static.cu"]
-HEADERS = ["sdv_device.cuh", "sdv_plan.h", "sdv_layer.h", "k8_attn.cuh", "k8_attn_mma.cuh"]
+HEADERS = ["sdv_device.cuh", "sdv_plan.h", "sdv_layer.h", "k8_attn.cuh", "k8_attn_mma.cuh", "k8_attn_tma.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

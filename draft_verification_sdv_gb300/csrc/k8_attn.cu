@@ -6,8 +6,7 @@ namespace sdv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxRows = 256;        // of the largest row tile
-constexpr int kMaxCtasPerSm = 2;
+constexpr int kMaxCtasPerSm = 3;
 constexpr int kTcRows = 64;          // query rows per kv head above which the tensor-core kernel runs
 
 // out = sum_i 2^(L_i - L) out_i with L = log2 sum_i 2^(L_i), over the CTAs that
@@ -69,8 +68,11 @@ cudaError_t launch_attn_combine(const AttnArgs& a, bool f16, int MT, cudaStream_
 }
 
 size_t attn_workspace_bytes(int nsm) {
-    const size_t ctas = static_cast<size_t>(nsm) * kMaxCtasPerSm;
-    return ctas * (2 * sizeof(int4) + 2 * static_cast<size_t>(kMaxRows) * (kCacheMaxDim + 1) * sizeof(float));
+    // two partial results per CTA: 256 rows of up to 128 (one CTA per SM), 64
+    // rows of up to 256 (two) or 16 rows of up to 128 (three)
+    const size_t tc = size_t(1) * 256 * (128 + 1), mma = size_t(2) * 64 * (kCacheMaxDim + 1), dec = size_t(3) * 16 * (128 + 1);
+    const size_t most = tc > mma ? (tc > dec ? tc : dec) : (mma > dec ? mma : dec);
+    return nsm * (kMaxCtasPerSm * 2 * sizeof(int4) + 2 * most * sizeof(float));
 }
 
 cudaError_t launch_tree_attn(AttnArgs a, int type, bool e4m3, void* workspace, int nsm, cudaStream_t s) {
@@ -78,7 +80,10 @@ cudaError_t launch_tree_attn(AttnArgs a, int type, bool e4m3, void* workspace, i
     a.part = reinterpret_cast<float*>(a.desc + 2 * kMaxCtasPerSm * nsm);
     const bool f16 = type == kTypeF16;
     const int rows = a.N * a.g;
-    if (rows > kTcRows && attn_tc_takes(a)) return launch_attn_tc(a, f16, e4m3, nsm, s);
+    if (attn_tma_takes(a)) {
+        if (rows <= 16) return launch_attn_dec(a, f16, e4m3, nsm, s);
+        if (rows > kTcRows) return launch_attn_tc(a, f16, e4m3, nsm, s);
+    }
     if (a.c.D <= 64) return launch_attn_mma64(a, f16, e4m3, rows, nsm, s);
     if (a.c.D <= 128) return launch_attn_mma128(a, f16, e4m3, rows, nsm, s);
     return launch_attn_mma256(a, f16, e4m3, rows, nsm, s);

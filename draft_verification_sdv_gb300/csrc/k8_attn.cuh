@@ -309,8 +309,10 @@ template <bool F16> __device__ __forceinline__ uint32_t pack2(float x, float y) 
 cudaError_t launch_attn_mma64(const AttnArgs& a, bool f16, bool e4m3, int rows, int nsm, cudaStream_t s);
 cudaError_t launch_attn_mma128(const AttnArgs& a, bool f16, bool e4m3, int rows, int nsm, cudaStream_t s);
 cudaError_t launch_attn_mma256(const AttnArgs& a, bool f16, bool e4m3, int rows, int nsm, cudaStream_t s);
-// tcgen05 kernel, and whether it takes this head dimension and page size.
-bool attn_tc_takes(const AttnArgs& a);
+// Kernels whose tiles come by tile copies, for up to 16 rows per kv head and for
+// more (tcgen05), and whether they take this head dimension and page size.
+bool attn_tma_takes(const AttnArgs& a);
+cudaError_t launch_attn_dec(const AttnArgs& a, bool f16, bool e4m3, int nsm, cudaStream_t s);
 cudaError_t launch_attn_tc(const AttnArgs& a, bool f16, bool e4m3, int nsm, cudaStream_t s);
 // Joins the partial results of the kernel just launched with row tiles of MT.
 cudaError_t launch_attn_combine(const AttnArgs& a, bool f16, int MT, cudaStream_t s);

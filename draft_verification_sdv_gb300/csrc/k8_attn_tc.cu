@@ -33,9 +33,7 @@
 // Every wait is bounded: a wait that gives up marks the CTA dead, after which
 // no wait waits, no product is issued, and every row that is still written is
 // not a number (SDV_STATUS_TIMEOUT).
-#include <cuda.h>
-
-#include "k8_attn.cuh"
+#include "k8_attn_tma.cuh"
 
 namespace sdv {
 namespace {
@@ -49,7 +47,6 @@ constexpr int MT = 2 * kRows, BN = 128;
 constexpr int kBlock = BN * 128;         // bytes of 128 rows of 64 16-bit cells
 constexpr int kTile = 2 * kBlock;        // ... of 128
 constexpr int kLoadWarps = 3, kLoadThreads = 32 * kLoadWarps;
-constexpr uint32_t kPolls = 1u << 17, kPollNs = 20000;     // a wait's limit: so many polls, each sleeping that long at most
 constexpr float kSlack = 8.0f;           // how far (log2) scores may pass the reference
 
 // Shared memory, bytes from its 1024-aligned start.
@@ -84,61 +81,13 @@ enum Bar { kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6, kOFull = 8, kEnd = 1
 
 static_assert(Smem::word == Smem::bar + kBars * 8, "a place for each barrier");
 
-struct Sync {
-    uint32_t bar, dead;      // shared-memory addresses
-    unsigned* status;
-    __device__ __forceinline__ bool is_dead() const {
-        uint32_t d;
-        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(d) : "r"(dead) : "memory");
-        return d != 0;
-    }
-    __device__ __forceinline__ bool test(int i, uint32_t parity) const {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done) : "r"(bar + i * 8), "r"(parity) : "memory");
-        return done != 0;
-    }
-    // sleeps until the phase is over or for some time: a warp that keeps asking
-    // holds up the shared-memory accesses of the others
-    __device__ __forceinline__ bool poll(int i, uint32_t parity) const {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done) : "r"(bar + i * 8), "r"(parity), "r"(kPollNs) : "memory");
-        return done != 0;
-    }
-    // false: the CTA is dead
-    __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
-        for (uint32_t n = 0; n < kPolls; ++n) {
-            if (poll(i, parity)) return true;
-            if (is_dead()) return false;
-        }
-        asm volatile("st.volatile.shared.u32 [%0], 1;" ::"r"(dead) : "memory");
-        if (status) atomicOr(status, kStatusTimeout);
-        return false;
-    }
-    __device__ __forceinline__ void arrive(int i) const {
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar + i * 8) : "memory");
-    }
-    __device__ __forceinline__ void commit(int i) const {
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar + i * 8) : "memory");
-    }
-};
-
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// Tile copy of the box at (x, row, page) into shared memory.
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int row, int page) {
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(row), "r"(page) : "memory");
-}
 __device__ __forceinline__ void tma_load_q(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int head, int node, int b) {
     asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
                  "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(head), "r"(node), "r"(b) : "memory");
 }
-__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
 #define SDV_R4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
 #define SDV_R16(r, i) SDV_R4(r, i), SDV_R4(r, i + 4), SDV_R4(r, i + 8), SDV_R4(r, i + 12)
@@ -189,14 +138,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t x, uint32_t y, uint3
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(x), "r"(y), "r"(idesc), "r"(add),
                  "r"(kOperandHi) : "memory");
 }
-
-// One thread of a converged warp, and a value that is the same in all of them.
-__device__ __forceinline__ bool elected() {
-    uint32_t e;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-    return e != 0;
-}
-__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // Two fp32 operations at once.
 struct F2 { float x, y; };
@@ -889,39 +830,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-    static const EncodeTiled f = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            p = nullptr;
-        }
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return f;
-}
-
-// Cells as [pages][kv_heads * page_size][head_dim]; boxes of `rows` rows of 64
-// 16-bit cells (swizzled), or of 128 e4m3 cells; what lies past head_dim is 0.
-bool encode(CUtensorMap* map, const AttnArgs& a, unsigned char* cells, bool e4m3, int rows) {
-    const EncodeTiled f = encode_tiled();
-    if (!f) return false;
-    const int cell = e4m3 ? 1 : 2;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.c.D), static_cast<cuuint64_t>(a.c.H) * a.c.P,
-                                static_cast<cuuint64_t>(a.c.pages)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.c.D) * cell, static_cast<cuuint64_t>(a.c.page_stride)};
-    const cuuint32_t box[3] = {e4m3 ? 128u : 64u, static_cast<cuuint32_t>(rows), 1u}, one[3] = {1u, 1u, 1u};
-    return f(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, cells, dims, strides, box, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Queries as [B][N][Hq][D]: a box is the group's heads of 128 / g nodes.  Not
 // for every group and stride: the kernel then copies the rows itself.
 bool encode_q(CUtensorMap* map, const AttnArgs& a) {
@@ -962,13 +870,13 @@ cudaError_t launch(AttnArgs a, const CUtensorMap& k, const CUtensorMap& v, const
 
 }  // namespace
 
-bool attn_tc_takes(const AttnArgs& a) { return a.c.D <= 128 && a.c.P % 8 == 0 && encode_tiled() != nullptr; }
+bool attn_tma_takes(const AttnArgs& a) { return a.c.D <= 128 && a.c.P % 8 == 0 && encode_tiled() != nullptr; }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, bool f16, bool e4m3, int nsm, cudaStream_t s) {
     // rows of one copy: those of a tile that are sure to lie in one page
     const int rows = min(a.c.P & -a.c.P, BN);
     CUtensorMap k, v, q = {};
-    if (!encode(&k, a, a.c.k, e4m3, rows) || !encode(&v, a, a.c.v, e4m3, rows)) return cudaErrorInvalidValue;
+    if (!encode_cells(&k, a, a.c.k, e4m3, rows, !e4m3) || !encode_cells(&v, a, a.c.v, e4m3, rows, !e4m3)) return cudaErrorInvalidValue;
     // (a negative scale is the queries' sign, which a copy by boxes leaves alone)
     const bool boxes = a.scale_log2 >= 0.0f && encode_q(&q, a);
     if (e4m3) return f16 ? launch<true, true>(a, k, v, q, boxes, rows, nsm, s) : launch<true, false>(a, k, v, q, boxes, rows, nsm, s);
