@@ -6,7 +6,7 @@ namespace sdv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxCtasPerSm = 3;
+constexpr int kMaxCtasPerSm = 2;
 constexpr int kTcRows = 64;          // query rows per kv head above which the tensor-core kernel runs
 
 // out = sum_i 2^(L_i - L) out_i with L = log2 sum_i 2^(L_i), over the CTAs that
@@ -69,9 +69,9 @@ cudaError_t launch_attn_combine(const AttnArgs& a, bool f16, int MT, cudaStream_
 
 size_t attn_workspace_bytes(int nsm) {
     // two partial results per CTA: 256 rows of up to 128 (one CTA per SM), 64
-    // rows of up to 256 (two) or 16 rows of up to 128 (three)
-    const size_t tc = size_t(1) * 256 * (128 + 1), mma = size_t(2) * 64 * (kCacheMaxDim + 1), dec = size_t(3) * 16 * (128 + 1);
-    const size_t most = tc > mma ? (tc > dec ? tc : dec) : (mma > dec ? mma : dec);
+    // rows of up to 256 (two), which covers 16 rows of up to 128 (two)
+    const size_t tc = size_t(1) * 256 * (128 + 1), mma = size_t(2) * 64 * (kCacheMaxDim + 1);
+    const size_t most = tc > mma ? tc : mma;
     return nsm * (kMaxCtasPerSm * 2 * sizeof(int4) + 2 * most * sizeof(float));
 }
 

@@ -3,7 +3,7 @@
 //
 // The whole cache is read for a handful of rows, so HBM bounds the step, and the
 // work per byte has to be small: a producer warp brings tiles of 32 KB (keys and
-// values of BN positions) by tile copies, two or three ahead, and four warps
+// values of BN positions) by tile copies, two ahead, and four warps
 // split each tile's positions.  Each keeps its own running maximum, sum and
 // output, so no warp waits for another until the unit's end; the products run on
 // mma.sync m16n8k16, whose 16 rows waste less on 8 query heads than a
@@ -36,24 +36,25 @@ template <int DP, bool E4> struct DecShape {
 };
 
 template <int DP, bool E4, int H> struct DecSmem {
-    static constexpr int kStages = H == 1 ? 2 : 3;          // three CTAs or two per SM
+    static constexpr int kStages = 3;                       // two CTAs per SM
     static constexpr int q = kStages * 2 * kDecTile;        // [16][DP] 16-bit, swizzled
     static constexpr int join = q + 16 * DP * 2;            // float [8 H][DP]
-    static constexpr int ke = join + 8 * H * DP * 4;        // float [4 warps][NW] keys' powers of two, then values' exponents
+    static constexpr int ke = join + 8 * H * DP * 4;        // float [warps][2][NW] keys' powers of two, values' exponents
     static constexpr int qe = ke + (E4 ? 2 * DecShape<DP, E4>::BN * 4 : 0);
-    static constexpr int ml = qe + 16 * 4;                  // float [2][4 warps][16] maxima and sums
-    static constexpr int bar = ml + 2 * 4 * 16 * 4;         // full, empty [kStages]
+    static constexpr int ml = qe + 16 * 4;                  // float [2][warps][16] maxima and sums
+    static constexpr int bar = ml + 2 * kDecWarps * 16 * 4;         // full, empty [kStages]
     static constexpr int dead = bar + 2 * kStages * 8;
     static constexpr int bytes = (dead + 4 + 15) / 16 * 16 + 1024;
 };
 
 template <int DP, bool E4, bool F16, int H>
-__global__ void __launch_bounds__(kDecThreads, H == 1 ? 3 : 2) attn_dec_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
+__global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                                                                const __grid_constant__ CUtensorMap map_v, int run_rows) {
     using S = DecShape<DP, E4>;
     using M = DecSmem<DP, E4, H>;
     constexpr int BN = S::BN, NW = S::NW, NT = S::NT, NB = S::NB, MT = 16, kStages = M::kStages;
     constexpr bool M16 = F16 || E4;                  // the products' type is fp16
+    static_assert(NT % 2 == 0 && NW <= 32, "a warp takes pairs of column tiles, a lane one position");
     extern __shared__ unsigned char raw[];
     unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::bar);
@@ -516,7 +517,7 @@ cudaError_t dec_one(AttnArgs a, int nsm, cudaStream_t s) {
     if (!encode_cells(&k, a, a.c.k, E4, rows, true) || !encode_cells(&v, a, a.c.v, E4, rows, true)) return cudaErrorInvalidValue;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_dec_kernel<DP, E4, F16, H>), bytes);
     if (e != cudaSuccess) return e;
-    a.ctas = nsm * (H == 1 ? 3 : 2);
+    a.ctas = nsm * 2;
     a.rounds = 0;
     attn_dec_kernel<DP, E4, F16, H><<<static_cast<unsigned>(a.ctas), kDecThreads, bytes, s>>>(a, k, v, rows);
     e = cudaGetLastError();
