@@ -113,6 +113,21 @@ __device__ __forceinline__ int place_of(const CellsArgs& a, const Rows& r, int n
     return page;
 }
 
+// The places of an item's R rows, one lane of it looking up each; the status is
+// set for those that have none.
+template <int LANES, int R>
+__device__ __forceinline__ void places_of(const CellsArgs& a, const Rows& r, int lane, int (&page)[R], int64_t (&cell)[R]) {
+    unsigned st = 0;
+    int64_t c = 0;
+    const int p = lane < R ? place_of(a, r, r.n + lane, &c, &st) : -2;
+    if (st && a.status) atomicOr(a.status, st);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        page[i] = __shfl_sync(0xffffffffu, p, i, LANES);
+        cell[i] = __shfl_sync(0xffffffffu, static_cast<int>(c), i, LANES);      // rows of a page: fewer than 2^30
+    }
+}
+
 template <int TYPE, bool E4M3, bool VEC, int LANES, int R>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CellsArgs a) {
     const int lane = threadIdx.x % LANES;
@@ -124,12 +139,9 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CellsArgs a) {
 #pragma unroll
     for (int i = 0; i < R; ++i)                     // whatever becomes of a row, it may be read
         x[i] = r.live && mine && r.n + i < a.N ? load8<VEC>(src + (r.n + i) * sn) : make_uint4(0, 0, 0, 0);
-    unsigned st = 0;
     int page[R];
     int64_t cell[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) page[i] = place_of(a, r, r.n + i, &cell[i], &st);
-    if (st && lane == 0 && a.status) atomicOr(a.status, st);
+    places_of<LANES, R>(a, r, lane, page, cell);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const bool go = page[i] >= 0;
@@ -137,24 +149,21 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const CellsArgs a) {
         if constexpr (!E4M3) {
             if (go && mine) *reinterpret_cast<uint4*>(dst + cell[i] * a.c.D * 2 + lane * 16) = x[i];
         } else {
-            float f[8], top = 0.0f;
-            int bad = 0;
-            widen<TYPE>(x[i], f);
+            // magnitudes order as their bits do, infinities and NaN last
+            unsigned top = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                    __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+            top = max(top >> 16, top & 0xffffu);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                top = fmaxf(top, fabsf(f[e]));
-                bad |= !(fabsf(f[e]) < INFINITY);
-            }
-            // the largest magnitude's bits; all ones where something is not a number
-            unsigned bits = bad ? 0x7fffffffu : __float_as_uint(top);
-#pragma unroll
-            for (int o = LANES / 2; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
-            bad = bits == 0x7fffffffu;
+            for (int o = LANES / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const bool bad = top >= (TYPE == kTypeBf16 ? 0x7f80u : 0x7c00u);
+            const unsigned bits = TYPE == kTypeBf16 ? top << 16 : __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
             // top = 1.m 2^x <= 448 2^e: e = x - 8 while 1.m <= 1.75, else x - 7
             // (a subnormal or zero top has x = -127 and ends at the floor as well)
             int e = static_cast<int>(bits >> 23) - 127 - ((bits & 0x7fffff) <= 0x600000 ? 8 : 7);
-            e = e < -126 ? -126 : e;
+            e = bad ? 0 : e < -126 ? -126 : e;
             const float inv = pow2f(-e);
+            float f[8];
+            widen<TYPE>(x[i], f);
             uint32_t o[2];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
@@ -178,28 +187,26 @@ template <int TYPE, bool E4M3, int LANES, int R>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CellsArgs a) {
     const int lane = threadIdx.x % LANES;
     const Rows r = rows_of<R>(a, (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / LANES);
-    if (!r.live || lane * 8 >= a.c.D) return;
-    unsigned st = 0;
     int page[R], ex[R];
+    int64_t cell[R];
+    places_of<LANES, R>(a, r, lane, page, cell);
+    if (!r.live || lane * 8 >= a.c.D) return;
     uint4 x[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        int64_t cell = 0;
-        page[i] = place_of(a, r, r.n + i, &cell, &st);
         ex[i] = 127;
         x[i] = make_uint4(0, 0, 0, 0);
         if (page[i] >= 0) {
             const unsigned char* src = (r.isv ? a.c.v : a.c.k) + page[i] * a.c.page_stride;
             if constexpr (E4M3) {
-                const uint2 q = __ldcs(reinterpret_cast<const uint2*>(src + cell * a.c.D + lane * 8));
+                const uint2 q = __ldcs(reinterpret_cast<const uint2*>(src + cell[i] * a.c.D + lane * 8));
                 x[i].x = q.x, x[i].y = q.y;
-                ex[i] = __ldg((r.isv ? a.c.ve : a.c.ke) + page[i] * a.c.exp_page_stride + cell);
+                ex[i] = __ldg((r.isv ? a.c.ve : a.c.ke) + page[i] * a.c.exp_page_stride + cell[i]);
             } else {
-                x[i] = __ldcs(reinterpret_cast<const uint4*>(src + cell * a.c.D * 2 + lane * 16));
+                x[i] = __ldcs(reinterpret_cast<const uint4*>(src + cell[i] * a.c.D * 2 + lane * 16));
             }
         }
     }
-    if (st && lane == 0 && a.status) atomicOr(a.status, st);
     unsigned char* dst = static_cast<unsigned char*>(r.isv ? a.ov : a.ok);
 #pragma unroll
     for (int i = 0; i < R; ++i) {

@@ -26,6 +26,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, int
         if (node >= a.N) continue;
         float top = -INFINITY;
         bool nan = false;
+#pragma unroll 8
         for (int i = first; i <= last; ++i) {
             const float L = attn::part_rows(a, i, i == first, MT)[MT * D + r];
             nan |= L != L;
@@ -33,6 +34,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, int
         }
         const float base = top == -INFINITY ? 0.0f : top;
         float sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
         for (int i = first; i <= last; ++i) {
             const float* p = attn::part_rows(a, i, i == first, MT);
             const float f = ex2(p[MT * D + r] - base);

@@ -23,6 +23,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kFlight = 4;            // rows in flight per thread
 constexpr int kBiasPass = 1024;       // biases sorted at a time
+constexpr int kRowsMost = 1024;       // rows of a CTA
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs a) {
@@ -31,6 +32,7 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs a) {
     __shared__ int s_n;
     __shared__ int2 s_raw[kBiasPass];               // (place in the list, id)
     __shared__ int2 s_bias[kBiasPass];              // (id, value) in the list's order
+    __shared__ int2 s_row[kRowsMost];               // source row, the draft token after it (-1: none)
     const unsigned slices = (static_cast<unsigned>(a.V) + kSlice - 1) / kSlice;
     const int b = static_cast<int>(blockIdx.x / slices);
     const int slice0 = static_cast<int>(blockIdx.x % slices) * kSlice;
@@ -41,6 +43,20 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs a) {
     const int r0 = static_cast<int>(blockIdx.y * all / a.row_splits);
     const int r1 = static_cast<int>((blockIdx.y + 1) * all / a.row_splits);
 
+    for (int i = threadIdx.x; i < r1 - r0; i += kThreads) {
+        const int r = r0 + i, k = r / rows, j = r - k * rows;
+        const int64_t at = b * all + r;
+        int src = r;
+        if (a.rows) {
+            src = a.rows[at];
+            if (src < 0 || src >= a.nsrc) {
+                src = -1;
+                if (slice0 == 0 && a.status) atomicOr(a.status, kStatusBadLength);
+            }
+        }
+        s_row[i] = make_int2(src, j < a.G ? a.drafts[(static_cast<int64_t>(b) * a.K + k) * a.G + j] : -1);
+    }
+    __syncthreads();
     const float rep = a.rep ? a.rep[b] : 1.0f, inv = 1.0f / rep;
     const float freq = a.freq ? a.freq[b] : 0.0f, pres = a.pres ? a.pres[b] : 0.0f;
     int c[E];
@@ -107,13 +123,14 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs a) {
         }
     };
     const int32_t* dr = a.drafts + static_cast<int64_t>(b) * a.K * a.G;
-    int k = r0 / rows, j = r0 - k * rows;           // the next row
+    const int k0 = r0 / rows;
+    int j = r0 - k0 * rows;                         // the next row's place in its draft
     history();
-    for (int i = 0; i < j; ++i) count_token(dr[k * a.G + i]);
+    for (int i = 0; i < j; ++i) count_token(dr[k0 * a.G + i]);
     settle();
 
     const int64_t row0 = b * all, nvec = a.V / E;
-    const uint4* in = static_cast<const uint4*>(a.logits);
+    const uint4* in = static_cast<const uint4*>(a.logits) + (a.rows ? static_cast<int64_t>(b) * a.nsrc : row0) * nvec + v0 / E;
     uint4* out = static_cast<uint4*>(a.out) + row0 * nvec + v0 / E;
     const int32_t* allow = a.allow ? a.allow + row0 * a.W + (v0 >> 5) : nullptr;
 
@@ -123,18 +140,11 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs a) {
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
             if (r + u >= r1) break;
-            int64_t src = row0 + r + u;
-            bool good = true;
-            if (a.rows) {
-                const int s = __ldg(a.rows + row0 + r + u);
-                good = s >= 0 && s < a.nsrc;
-                src = static_cast<int64_t>(b) * a.nsrc + (good ? s : 0);
-                if (!good && a.status) atomicOr(a.status, kStatusBadLength);
-            }
+            const int src = s_row[r + u - r0].x;
             ok[u] = allow ? static_cast<unsigned>(__ldg(allow + static_cast<int64_t>(r + u) * a.W)) >> (v0 & 31)
                           : 0xffffffffu;
-            if (good)
-                x[u] = __ldcs(in + src * nvec + v0 / E);
+            if (src >= 0)
+                x[u] = __ldcs(in + src * nvec);
             else                                    // NaN in either type
                 x[u] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u), ok[u] = ~0u;
         }
@@ -143,7 +153,6 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs a) {
             if (r + u >= r1) break;
             if (j == rows) {                        // the next draft
                 j = 0;
-                ++k;
                 history();
                 settle();
             }
@@ -168,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs a) {
                 }
             }
             __stcs(out + static_cast<int64_t>(r + u) * nvec, make_uint4(o[0], o[1], o[2], o[3]));
-            if (j < a.G && count_token(__ldg(dr + k * a.G + j))) settle();
+            if (count_token(s_row[r + u - r0].y)) settle();
             ++j;
         }
     }
@@ -202,7 +211,9 @@ cudaError_t launch_logits(const LogitsArgs& args, bool bf16, int nsm, cudaStream
     const int64_t all = static_cast<int64_t>(a.K) * (a.G + 1);
     int64_t split = (static_cast<int64_t>(nsm) * 8 + base - 1) / base;
     const int64_t most = (all + kFlight - 1) / kFlight;
-    a.row_splits = static_cast<int>(split < 1 ? 1 : split > most ? most : split);
+    split = split > most ? most : split;
+    const int64_t least = (all + kRowsMost - 1) / kRowsMost;
+    a.row_splits = static_cast<int>(split < least ? least : split);
     const dim3 grid(static_cast<unsigned>(base), static_cast<unsigned>(a.row_splits));
     if (bf16)
         logits_kernel<true><<<grid, kThreads, 0, s>>>(a);

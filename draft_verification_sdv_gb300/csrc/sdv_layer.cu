@@ -243,7 +243,9 @@ sdv_status sdv_logits_process(int B, int K, int gamma, int V, sdv_dtype dtype, v
     const int elt = dtype == SDV_BF16 ? 2 : 4;
     if ((static_cast<int64_t>(V) * elt) % 16 || V > (1 << 28)) return SDV_ERR_ARG;
     if (static_cast<int64_t>(B) * K * (gamma + 1) > (int64_t(1) << 27)) return SDV_ERR_ARG;
-    if (static_cast<int64_t>(B) * K * (V / 1024 + 1) >= (int64_t(1) << 31) || gamma > 65535) return SDV_ERR_ARG;
+    if (static_cast<int64_t>(B) * K * (V / 1024 + 1) >= (int64_t(1) << 31) || gamma > 65535 ||
+        static_cast<int64_t>(K) * (gamma + 1) > (int64_t(1) << 25))
+        return SDV_ERR_ARG;
     if (!logits || !drafts || !out || misaligned(logits, 16) || misaligned(out, 16) || misaligned(counts, 16))
         return SDV_ERR_ARG;
     if (rows ? nsrc < 1 || out == logits : false) return SDV_ERR_ARG;
