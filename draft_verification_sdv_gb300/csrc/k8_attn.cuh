@@ -50,8 +50,29 @@ template <int MT> __device__ __forceinline__ int tile_len(const AttnArgs& a, con
     return c.ctx + min(c.cnt, last + 1);
 }
 
+// Positions, from the first on, that every row of the tile sees (if it has any).
+template <int MT> __device__ __forceinline__ int seen_by_all(const AttnArgs& a, const Cut& c, int mt) {
+    return a.mask ? c.ctx : c.ctx + mt * MT / a.g + 1;
+}
+
 template <int BN> __device__ __forceinline__ int tiles_of(int len) {
     return len > 0 ? (len + BN - 1) / BN : 1;       // an empty unit still writes its rows
+}
+
+// Tiles of the first mts row tiles of one head of a causal chain: a tile's last
+// node, (mt * MT + MT - 1) / g, is carried along rather than divided for.
+template <int MT, int BN> __device__ __forceinline__ int64_t chain_tiles(const AttnArgs& a, const Cut& c, int mts) {
+    const int dq = MT / a.g, dr = MT - dq * a.g;
+    int first = 0, fr = 0;                           // the tile's first node, and its row's head
+    int64_t n = 0;
+    for (int mt = 0; mt < mts; ++mt) {
+        int next = first + dq, nr = fr + dr;
+        if (nr >= a.g) nr -= a.g, ++next;
+        const int last = nr == 0 ? next - 1 : next;
+        n += first >= c.cnt ? 1 : tiles_of<BN>(c.ctx + min(c.cnt, last + 1));
+        first = next, fr = nr;
+    }
+    return n;
 }
 
 // Tiles of all row tiles of one head of a sequence.
@@ -61,9 +82,7 @@ __device__ __forceinline__ int64_t head_tiles(const AttnArgs& a, const Cut& c, i
         const int live = min(mts, (c.cnt * a.g + MT - 1) / MT);
         return static_cast<int64_t>(live) * tiles_of<BN>(c.ctx + c.cnt) + (mts - live);
     }
-    int64_t n = 0;
-    for (int mt = 0; mt < mts; ++mt) n += tiles_of<BN>(tile_len<MT>(a, c, mt));
-    return n;
+    return chain_tiles<MT, BN>(a, c, mts);
 }
 
 struct Part {                // a CTA's part of the line
@@ -80,7 +99,7 @@ template <int MT, int BN>
 __device__ __forceinline__ int64_t tiles_before(const AttnArgs& a, const Cut& c, int mts, int j) {
     const int h = j / mts;
     int64_t n = h > 0 ? head_tiles<MT, BN>(a, c, mts) * h : 0;
-    for (int mt = 0; mt < j - h * mts; ++mt) n += tiles_of<BN>(tile_len<MT>(a, c, mt));
+    if (j > h * mts) n += a.mask ? head_tiles<MT, BN>(a, c, j - h * mts) : chain_tiles<MT, BN>(a, c, j - h * mts);
     return n;
 }
 

@@ -363,9 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
                 const int32_t* mrow = a.mask ? a.mask + u.b * a.mask_sb + static_cast<int64_t>(live ? node : 0) * a.W : nullptr;
                 uint32_t words[5] = {0, 0, 0, 0, 0};
-                // tiles from `plain` on hold nodes, which some rows see and some do not
+                // tiles from `plain` on hold positions that some rows see and some do not
                 // (all of them go the long way where a page is bad)
-                const int plain = any_bad ? 0 : min(max(u.cut.ctx / BN - u.t0, 0), nt);
+                const int plain = any_bad ? 0 : min(max(min(seen_by_all<MT>(a, u.cut, u.mt), u.cut.ctx + u.cut.cnt) / BN - u.t0, 0), nt);
                 if (mrow && plain == 0) mask_words(a, mrow, u.t0 * BN - u.cut.ctx, words);
                 // scores to probabilities: the running maximum and sum, P over S
                 auto weigh = [&](const float (&x)[128], bool first) {
@@ -585,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         uint32_t tiles = 0, step = 0, nq[2] = {0, 0};
         while ((E4 || w > 0) && walk.next(a, part, mts, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
+            const int all_see = min(seen_by_all<MT>(a, u.cut, u.mt), u.cut.ctx + u.cut.cnt);
             // e4m3: a thread looks after the exponents of rows p and p + 96 of a
             // tile; a row's page is read two tiles ahead, its exponents one
             const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
@@ -621,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         while (lstep <= step && begin(true)) {}
                     }
                 }
-                const int from = min(max(u.cut.ctx - (u.t0 + t) * BN, 0), BN);   // first row that some do not see
+                const int from = min(max(all_see - (u.t0 + t) * BN, 0), BN);    // first row that some do not see
                 if (E4 && !isv) {                    // the exponents of tile t
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 __syncwarp();
                 unsigned char* base = smem + slot * kTile;
                 const bool check = isv && from < BN;
-                if (check) {
+                if (isv) {                           // (read for other tiles too, where a page is bad)
                     if (lane < 4) s_flag[(tile & 3) * (kLoadWarps * 4) + w * 4 + lane] = 0;
                     __syncwarp();
                 }

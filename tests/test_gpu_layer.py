@@ -446,6 +446,27 @@ def test_attn_zero_values_and_tiny_ones_in_e4m3():
     assert ((out.double() * 2.0 ** 100 - 1).abs() <= 2.0 ** -8).all()
 
 
+def test_attn_bad_page_does_not_spread():
+    """A bad page after tiles with flagged values: only rows that see one of the two are not numbers."""
+    N, ctx = 300, [600]
+    q, kc, vc, ke, ve, table = _attn_case(1, N, 2, 1, 64, 16, ctx, BF, BF, seed=16)
+    x = torch.full((1, 1, 1, 64), math.nan, device="cuda", dtype=BF)
+    bd.sdv_kv_write(x, x, kc, vc, table, _i32([600 + 40]))
+    bad = table.clone()
+    bad[0, 53] = 10 ** 6                                      # positions 848 .. 863: nodes 248 .. 263
+    out = bd.sdv_tree_attn(q, kc, vc, bad, _i32(ctx))
+    fin = out.isfinite().all(-1).all(-1)[0].cpu()
+    assert fin[:40].all() and not fin[40:].any()
+    st = _status()
+    bd.sdv_kv_write(torch.zeros_like(x), torch.zeros_like(x), kc, vc, table, _i32([600 + 40]))
+    good = bd.sdv_tree_attn(q, kc, vc, table, _i32(ctx))
+    out = bd.sdv_tree_attn(q, kc, vc, bad, _i32(ctx), status=st)
+    assert int(st) == bd.SDV_STATUS_BAD_PAGE
+    fin = out.isfinite().all(-1).all(-1)[0].cpu()
+    assert fin[:248].all() and not fin[248:].any()
+    assert torch.equal(out[0, :248], good[0, :248])
+
+
 @pytest.mark.parametrize("N", [5, 50])
 def test_attn_large_scores(N):
     q, kc, vc, ke, ve, table = _attn_case(1, N, 4, 2, 64, 16, [150], BF, BF, seed=8)
