@@ -77,15 +77,16 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
 
     if (warp == kDecWarps) {
         // ---------------- loads ----------------
-        const int copies = BN / run_rows;
+        // a lane to each copy of a tile's keys or values (32 at most), in turn
+        const int copies = BN / run_rows, copy = lane / NB, block = lane - copy * NB;
         bool ok = true;
         while (ok && walk.next(a, part, 1, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
             const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
             int off = 0, noff = 0;
             auto page_at = [&](int t, int& o) {
-                const int pos = (u.t0 + t) * BN + lane * run_rows;
-                if (lane >= copies || t >= nt || pos >= u.len) return -1;
+                const int pos = (u.t0 + t) * BN + copy * run_rows;
+                if (copy >= copies || t >= nt || pos >= u.len) return -1;
                 const int i = pos / a.c.P;
                 o = u.h * a.c.P + pos - i * a.c.P;
                 return __ldg(table + i);
@@ -97,21 +98,16 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
                 const uint32_t st = n % kStages;
                 ok = __all_sync(0xffffffffu, sync.wait(kStages + st, (n / kStages & 1) ^ 1));
                 if (!ok) break;
-                const uint32_t good = __ballot_sync(0xffffffffu, page >= 0 && page < a.c.pages);
-                const uint32_t dst = smem_u32(smem + st * 2 * kDecTile);
-                if (elected()) mbar_arrive_expect_tx(bars + st, __popc(good) * run_rows * 128 * NB * 2);
+                const bool good = page >= 0 && page < a.c.pages;
+                const uint32_t many = __popc(__ballot_sync(0xffffffffu, good));
+                const uint32_t dst = smem_u32(smem + st * 2 * kDecTile) + block * BN * 128 + copy * run_rows * 128;
+                if (elected()) mbar_arrive_expect_tx(bars + st, many * run_rows * 128 * 2);
                 __syncwarp();
-                for (int c = 0; c < copies; ++c) {
-                    const int pg = __shfl_sync(0xffffffffu, page, c), row = __shfl_sync(0xffffffffu, off, c);
-                    if ((good >> c & 1) && elected()) {
-#pragma unroll
-                        for (int i = 0; i < NB; ++i) {
-                            tma_load(dst + i * BN * 128 + c * run_rows * 128, &map_k, bars + st, i * 64, row, pg);
-                            tma_load(dst + kDecTile + i * BN * 128 + c * run_rows * 128, &map_v, bars + st, i * 64, row, pg);
-                        }
-                    }
-                    __syncwarp();
+                if (good) {
+                    tma_load(dst, &map_k, bars + st, block * 64, off, page);
+                    tma_load(dst + kDecTile, &map_v, bars + st, block * 64, off, page);
                 }
+                __syncwarp();
             }
         }
         // what is still under way lands before the CTA goes (a dead one's too)

@@ -523,10 +523,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         int lpage = -1, loff = 0, npage = -1, noff = 0;     // this lane's rows of the tile and of the next one
         uint32_t lstep = 0;
         bool more = w == 0;
-        const int blocks = !E4 && D > 64 ? 2 : 1, copies = BN / run_rows;
+        const int blocks = !E4 && D > 64 ? 2 : 1, copies = BN / run_rows;      // 32 at most, a lane to each
+        const int copy = lane / blocks, column = lane - copy * blocks;
         auto lead_page = [&](int t, int& off) {
-            const int pos = (lu.t0 + t) * BN + lane * run_rows;
-            if (lane >= copies || t >= lnt || pos >= lu.len) return -1;
+            const int pos = (lu.t0 + t) * BN + copy * run_rows;
+            if (copy >= copies || t >= lnt || pos >= lu.len) return -1;
             const int i = pos / a.c.P;
             off = lu.h * a.c.P + pos - i * a.c.P;
             return __ldg(a.table + static_cast<int64_t>(lu.b) * a.max_pages + i);
@@ -561,19 +562,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 npage = lead_page(lt + 1, noff);
             }
             const uint32_t slot = isv ? kKeySlots + (T & 1) : T % kKeySlots;
-            const uint32_t good = __ballot_sync(0xffffffffu, lpage >= 0 && lpage < a.c.pages);
-            const uint32_t dst = uniform(smem_u32(smem + slot * kTile + (E4 ? kBlock : 0)));    // e4m3 lands in the upper half
-            const CUtensorMap* map = isv ? &map_v : &map_k;
-            if (elected()) mbar_arrive_expect_tx(bars + kLand + slot, __popc(good) * run_rows * 128 * blocks);
+            const bool good = lpage >= 0 && lpage < a.c.pages;
+            const uint32_t n = __popc(__ballot_sync(0xffffffffu, good));
+            if (elected()) mbar_arrive_expect_tx(bars + kLand + slot, n * run_rows * 128);
             __syncwarp();
-            for (int c = 0; c < copies; ++c) {
-                const int page = __shfl_sync(0xffffffffu, lpage, c), row = __shfl_sync(0xffffffffu, loff, c);
-                if ((good >> c & 1) && elected()) {
-                    tma_load(dst + c * run_rows * 128, map, bars + kLand + slot, 0, row, page);
-                    if (blocks == 2) tma_load(dst + kBlock + c * run_rows * 128, map, bars + kLand + slot, 64, row, page);
-                }
-                __syncwarp();
-            }
+            if (good)                                // e4m3 lands in the slot's upper half
+                tma_load(smem_u32(smem + slot * kTile + (E4 ? kBlock : column * kBlock) + copy * run_rows * 128), isv ? &map_v : &map_k,
+                         bars + kLand + slot, column * 64, loff, lpage);
+            __syncwarp();
             ++lstep;
             if (isv) ++lt;
             return true;
