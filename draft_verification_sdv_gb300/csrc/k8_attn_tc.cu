@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         s_tmem[1] = 0;                               // dead
         for (int i = 0; i < 4 * kLoadWarps * 4; ++i) s_flag[i] = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bars + kQFull + i, q_boxes ? 1 : E4 ? kLoadWarps : kLoadWarps - 1);
+            mbar_init(bars + kQFull + i, q_boxes ? 1 : E4 ? kLoadWarps : 1);
             mbar_init(bars + kQEmpty + i, 1);
             mbar_init(bars + kSFull + i, 1);
             mbar_init(bars + kPFull + i, kRows / 32);    // a warp arrives once: 32 arrivals take turns
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
         mbar_init(bars + kEnd, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bars + kFull + i, E4 ? kLoadWarps : kLoadWarps - 1);
+            mbar_init(bars + kFull + i, E4 ? kLoadWarps : 1);
             mbar_init(bars + kFree + i, 1);
         }
         for (int i = 0; i < kSlots; ++i) mbar_init(bars + kLand + i, 1);
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     } else if (warp < 11) {
         // ---------------- loads ----------------
         const int p = tid - 256, w = warp - 8;
-        constexpr int kFirst = E4 ? 0 : 1, kSettle = kLoadWarps - kFirst;   // warps that hand tiles over
+        constexpr int kFirst = E4 ? 0 : 2, kSettle = kLoadWarps - kFirst;   // warps that hand tiles over
         const int CH = D / (E4 ? 16 : 8);            // 16-byte chunks of a row as it comes
         const int LR = CH > 8 ? 16 : CH > 4 ? 8 : 4; // lanes of a row
         const int RP = 32 / LR, lr = lane / LR, lc = lane % LR;     // rows of a warp's step
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         int lt = 0, lnt = 0;                         // tile of the unit, its tiles
         int lpage = -1, loff = 0, npage = -1, noff = 0;     // this lane's rows of the tile and of the next one
         uint32_t lstep = 0;
-        bool more = w == 0;
+        bool more = w < (E4 ? 1 : 2);
         const int blocks = !E4 && D > 64 ? 2 : 1, copies = BN / run_rows;      // 32 at most, a lane to each
         const int copy = lane / blocks, column = lane - copy * blocks;
         auto lead_page = [&](int t, int& off) {
@@ -537,7 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             if (!more) return false;
             const bool isv = lstep & 1;
             const uint32_t T = lstep >> 1;
-            if (isv && T >= 2) {                     // (which frees the keys' place of the step after, too)
+            // (values wait for free(T - 2); with it the keys of tile T + 1 may come)
+            const bool mine = E4 || isv == (w == 1);
+            if (isv && T >= 2) {
                 const int bar = kFree + (T & 1);
                 const uint32_t parity = (T - 2) >> 1 & 1;
                 if (block) {
@@ -564,9 +566,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const uint32_t slot = isv ? kKeySlots + (T & 1) : T % kKeySlots;
             const bool good = lpage >= 0 && lpage < a.c.pages;
             const uint32_t n = __popc(__ballot_sync(0xffffffffu, good));
-            if (elected()) mbar_arrive_expect_tx(bars + kLand + slot, n * run_rows * 128);
+            if (mine && elected()) mbar_arrive_expect_tx(bars + kLand + slot, n * run_rows * 128);
             __syncwarp();
-            if (good)                                // e4m3 lands in the slot's upper half
+            if (mine && good)                                // e4m3 lands in the slot's upper half
                 tma_load(smem_u32(smem + slot * kTile + (E4 ? kBlock : column * kBlock) + copy * run_rows * 128), isv ? &map_v : &map_k,
                          bars + kLand + slot, column * 64, loff, lpage);
             __syncwarp();
@@ -574,12 +576,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             if (isv) ++lt;
             return true;
         };
-        if (!E4 && w == 0)
+        if (!E4 && w < kFirst)
             while (begin(true)) {}                   // nothing else to do
 
         Unit u;
         uint32_t tiles = 0, step = 0, nq[2] = {0, 0};
-        while ((E4 || w > 0) && walk.next(a, part, mts, u)) {
+        while (w >= kFirst && walk.next(a, part, mts, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
             const int all_see = min(seen_by_all<MT>(a, u.cut, u.mt), u.cut.ctx + u.cut.cnt);
             // e4m3: a thread looks after the exponents of rows p and p + 96 of a
@@ -725,12 +727,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             }
             tiles += nt;
         }
-        if ((E4 || w > 0) && lane == 0) sync.arrive(kFull + (tiles & 1));       // the last values
+        if (w >= kFirst && lane == 0) sync.arrive(kFull + (tiles & 1));       // the last values
         if (w == kFirst && q_boxes)                  // a dead CTA too waits for the copies it has begun
 #pragma unroll
             for (int s = 0; s < 2; ++s)
                 for (uint32_t n = 0; nq[s] > 0 && n < kPolls && !sync.poll(kQFull + s, (nq[s] - 1) & 1) && !sync.is_dead(); ++n) {}
-        if (w == 0)
+        if (w == 0 || (!E4 && w == 1))
             // (two tiles' values and the keys of three at most; those before have been used)
             for (uint32_t i = lstep > 5 ? lstep - 4 - (lstep & 1) : 0; i < lstep; ++i) {
                 const uint32_t T = i >> 1;
