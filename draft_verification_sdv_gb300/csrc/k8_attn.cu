@@ -7,7 +7,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxCtasPerSm = 2;
-constexpr int kTcRows = 64;          // query rows per kv head above which the tensor-core kernel runs
+
+// Query rows per kv head up to which k8_attn_dec.cu runs, in units of 16 rows;
+// above, k8_attn_tc.cu, whose time hardly depends on the rows up to 256.  Times
+// for 32 sequences of 4000 positions, 8 kv heads of 128: 16-bit caches, 16 rows
+// 101 and 124 us, 24 rows 178 and 129 us; e4m3 caches, which the second has to
+// widen in shared memory first, 48 rows 221 and 338 us, 64 rows 288 and 340, 80
+// rows 358 and 341.  (Heads of 64, 16 bits: 60 and 105 us, 32 rows 102 and 107,
+// 48 rows 139 and 108.)
+constexpr int kDecRows = 16, kDecRowsE4m3 = 64;
 
 // out = sum_i 2^(L_i - L) out_i with L = log2 sum_i 2^(L_i), over the CTAs that
 // share a unit.  One column of the grid per CTA of the kernel before, most of
@@ -83,8 +91,8 @@ cudaError_t launch_tree_attn(AttnArgs a, int type, bool e4m3, void* workspace, i
     const bool f16 = type == kTypeF16;
     const int rows = a.N * a.g;
     if (attn_tma_takes(a)) {
-        if (rows <= 16) return launch_attn_dec(a, f16, e4m3, nsm, s);
-        if (rows > kTcRows) return launch_attn_tc(a, f16, e4m3, nsm, s);
+        if (rows <= (e4m3 ? kDecRowsE4m3 : kDecRows)) return launch_attn_dec(a, f16, e4m3, nsm, s);
+        return launch_attn_tc(a, f16, e4m3, nsm, s);
     }
     if (a.c.D <= 64) return launch_attn_mma64(a, f16, e4m3, rows, nsm, s);
     if (a.c.D <= 128) return launch_attn_mma128(a, f16, e4m3, rows, nsm, s);

@@ -328,8 +328,8 @@ template <bool F16> __device__ __forceinline__ uint32_t pack2(float x, float y) 
 cudaError_t launch_attn_mma64(const AttnArgs& a, bool f16, bool e4m3, int rows, int nsm, cudaStream_t s);
 cudaError_t launch_attn_mma128(const AttnArgs& a, bool f16, bool e4m3, int rows, int nsm, cudaStream_t s);
 cudaError_t launch_attn_mma256(const AttnArgs& a, bool f16, bool e4m3, int rows, int nsm, cudaStream_t s);
-// Kernels whose tiles come by tile copies, for up to 16 rows per kv head and for
-// more (tcgen05), and whether they take this head dimension and page size.
+// Kernels whose tiles come by tile copies, for few rows per kv head and for
+// many (tcgen05), and whether they take this head dimension and page size.
 bool attn_tma_takes(const AttnArgs& a);
 cudaError_t launch_attn_dec(const AttnArgs& a, bool f16, bool e4m3, int nsm, cudaStream_t s);
 cudaError_t launch_attn_tc(const AttnArgs& a, bool f16, bool e4m3, int nsm, cudaStream_t s);

@@ -1,5 +1,5 @@
-// k8_attn_dec.cu -- tree attention for up to 16 query rows per kv head, such as
-// one new token's (sdv_tree_attn).
+// k8_attn_dec.cu -- tree attention for few query rows per kv head, such as one new
+// token's (sdv_tree_attn), in units of 16 rows.
 //
 // The whole cache is read for a handful of rows, so HBM bounds the step, and the
 // work per byte has to be small: a producer warp brings tiles of 32 KB (keys and
@@ -68,10 +68,11 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
             mbar_init(bars + kStages + i, kDecWarps);
         }
     }
-    const Part part = find_part<MT, BN, kDecThreads>(a, 1, s_part);     // holds barriers of the CTA
+    const int mts = (a.N * a.g + MT - 1) / MT;
+    const Part part = find_part<MT, BN, kDecThreads>(a, mts, s_part);     // holds barriers of the CTA
     Walk<MT, BN> walk;
-    walk.begin(a, part, 1);
-    if (tid == 0) write_desc<MT, BN>(a, part, 1);
+    walk.begin(a, part, mts);
+    if (tid == 0) write_desc<MT, BN>(a, part, mts);
     Unit u;
     uint32_t n = 0;                                  // tiles so far
 
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
         // a lane to each copy of a tile's keys or values (32 at most), in turn
         const int copies = BN / run_rows, copy = lane / NB, block = lane - copy * NB;
         bool ok = true;
-        while (ok && walk.next(a, part, 1, u)) {
+        while (ok && walk.next(a, part, mts, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
             const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
             int off = 0, noff = 0;
@@ -129,20 +130,21 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
     auto chunk_of = [](int r, int c) { return (c >> 3) * (BN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
     constexpr int kAll = 32 * kDecWarps;
 
-    while (walk.next(a, part, 1, u)) {
+    while (walk.next(a, part, mts, u)) {
         if (tid == 0 && u.cut.bad && a.status) atomicOr(a.status, kStatusBadLength);
         const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
         const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
         bool alive = true;
+        const int first = u.mt * MT;                 // of the unit's rows
 
         // ---- queries ----
         for (int w = tid; w < 16 * (DP / 8); w += kAll) {
             const int r = w / (DP / 8), c = w % (DP / 8);
-            const int node = r / a.g;
+            const int row = first + r, node = row / a.g;
             uint32_t v[4] = {0, 0, 0, 0};
             if (node < u.cut.cnt && c * 8 < a.c.D) {
                 const unsigned char* p = a.q + u.b * a.q_sb + node * a.q_sn +
-                                         (static_cast<int64_t>(u.h) * a.g + r % a.g) * a.q_sh + c * 16;
+                                         (static_cast<int64_t>(u.h) * a.g + row % a.g) * a.q_sh + c * 16;
                 if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
                     const uint4 x = *reinterpret_cast<const uint4*>(p);
                     v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
         for (int r = 0; r < H; ++r) {
             m[r] = mv[r] = -INFINITY, l[r] = 0.0f;
             rowf[r] = s_qe[g4 + 8 * r];
-            node[r] = (g4 + 8 * r) / a.g;
+            node[r] = (first + g4 + 8 * r) / a.g;
         }
 
         // a lane looks after one of the warp's positions: its page is read two
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
         float* prow = part_rows(a, blockIdx.x, u.t0 > 0 ? 0 : 1, MT);
         for (int w = tid; w < 8 * H * (DP / 4); w += kAll) {
             const int r = w / (DP / 4), d = (w % (DP / 4)) * 4;
-            const int nd = r / a.g;
+            const int nd = (first + r) / a.g;
             if (nd >= a.N || d >= a.c.D) continue;
             float mx = -INFINITY, sum = 0.0f;
 #pragma unroll
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
             const float log2sum = u.cut.bad ? nan : empty ? -INFINITY : b0 + log2f(sum);
             const float acc[4] = {empty ? 0.0f : v.x * inv, empty ? 0.0f : v.y * inv, empty ? 0.0f : v.z * inv, empty ? 0.0f : v.w * inv};
             if (u.whole) {
-                const int64_t orow = (static_cast<int64_t>(u.b) * a.N + nd) * a.Hq + u.h * a.g + r % a.g;
+                const int64_t orow = (static_cast<int64_t>(u.b) * a.N + nd) * a.Hq + u.h * a.g + (first + r) % a.g;
                 unsigned short* dst = static_cast<unsigned short*>(a.out) + orow * a.c.D + d;
                 *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<F16>(acc[0], acc[1]), pack2<F16>(acc[2], acc[3]));
                 if (d == 0 && a.lse) a.lse[orow] = log2sum * kLn2;

@@ -12,7 +12,8 @@
 // TMEM holds S_0, S_1, O_0, O_1: 4 x 128 columns, all 512.  P could go through
 // shared memory, where a product takes 65 clocks instead of 100; but two
 // operands there use all of the shared memory's bandwidth, and every barrier
-// and store of the other warps then waits (measured slower by half).
+// and store of the other warps then waits (1547 us against 1276 us for 16 trees
+// of 513 nodes, when both were built).
 //
 // O is not rescaled each time the maximum grows: the running reference m only
 // moves when a row's scores pass it by 2^8 (fp32 sums and 16-bit probabilities
@@ -22,13 +23,22 @@
 // that issues the products.  Tiles of 128 positions, keys and values in turn,
 // go through a ring of slots in shared memory, as rows of 128 bytes in the
 // 128-byte swizzle, [D / 64][128 rows]: the K operand is read K-major, and V,
-// whose contraction index is the row, MN-major.  Warp 8 brings a tile by tile
-// copies (TMA), one per page and column block, so that pages may be of any size
-// that is a multiple of 8 rows.  Warps 9 and 10 then hand it over (warp 8 helps
-// them with e4m3 rows): after a look at the values of rows that some queries do not see
-// (what is not a number there must not meet a zero probability in a product),
-// or, for e4m3 rows, which land as they are in the upper half of their slot,
-// after bringing them to the queries' type, times their row's power of two.
+// whose contraction index is the row, MN-major.  They come by tile copies (TMA),
+// one per page and column block and a lane to each, so that pages may be of any
+// size that is a multiple of 8 rows: warp 8 brings the keys and warp 9 the
+// values, and warp 10 hands a tile over, after a look at the values of rows that
+// some queries do not see (what is not a number there must not meet a zero
+// probability in a product).  e4m3 rows land as they are in the upper half of
+// their slot; then warp 8 brings both, and all three hand over, after widening
+// the rows in place to the queries' type, times their power of two.
+//
+// What bounds it: the chain of one stream's step, softmax (2230 clocks for two
+// streams' tiles, a third of them the 2^x), P V (430) and S (640) and the waits
+// between them (440), 3740 clocks for two tiles where the products alone take
+// 2100.  16 trees of 513 nodes over 1500 to 3500 positions, 8 x 8 heads of 128:
+// 876 us, 760 TFLOP/s; 3 chunks of 1900 tokens, 8 x 4 heads of 64: 262 us.  e4m3
+// rows: 2700 clocks to widen a tile, which bounds units of one stream (338 us
+// against 139 us for 32 sequences of 4000 positions).
 //
 // Every wait is bounded: a wait that gives up marks the CTA dead, after which
 // no wait waits, no product is issued, and every row that is still written is
@@ -234,6 +244,31 @@ template <bool F16> __device__ __forceinline__ void widen16(const uint4& raw, in
             const uint32_t v = (t & 0x80008000u) | ((t >> 4) & 0x07f007f0u);
             asm("{\n\t.reg .b32 t;\n\tmul.rn.bf16x2 t, %1, %2;\n\tmul.rn.bf16x2 %0, t, %3;\n\t}"
                 : "=r"(o[i]) : "r"(v), "r"(0x7b807b80u), "r"(s));
+        }
+    }
+}
+
+// The same for the usual powers, those that one 16-bit factor holds: half the work.
+template <bool F16> __device__ __forceinline__ bool usual_power(int e) { return F16 ? e >= 113 && e <= 142 : e <= 134; }
+template <bool F16> __device__ __forceinline__ void widen16_usual(const uint4& raw, int e, uint32_t (&o)[8]) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t bad = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    uint32_t s = F16 ? static_cast<uint32_t>(e - 112) << 10 : static_cast<uint32_t>(e + 120) << 7;
+    if (bad) s = F16 ? 0x7e00u : 0x7fc0u;
+    s = __byte_perm(s, 0, 0x1010);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (F16) {
+            asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 t, u;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 t, lo;\n\t"
+                "cvt.rn.f16x2.e4m3x2 u, hi;\n\tmul.rn.f16x2 %0, t, %3;\n\tmul.rn.f16x2 %1, u, %3;\n\t}"
+                : "=r"(o[2 * i]), "=r"(o[2 * i + 1]) : "r"(w[i]), "r"(s));
+        } else {
+            // high and low bytes of the cells' bits in bf16's places
+            const uint32_t hi = (w[i] & 0x80808080u) | ((w[i] >> 4) & 0x07070707u), lo = (w[i] << 4) & 0xf0f0f0f0u;
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[2 * i]) : "r"(__byte_perm(lo, hi, 0x5140)), "r"(s));
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[2 * i + 1]) : "r"(__byte_perm(lo, hi, 0x7362)), "r"(s));
         }
     }
 }
@@ -510,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         // ---------------- loads ----------------
         const int p = tid - 256, w = warp - 8;
         constexpr int kFirst = E4 ? 0 : 2, kSettle = kLoadWarps - kFirst;   // warps that hand tiles over
+        constexpr int kBatch = E4 ? 6 : 1;
         const int CH = D / (E4 ? 16 : 8);            // 16-byte chunks of a row as it comes
         const int LR = CH > 8 ? 16 : CH > 4 ? 8 : 4; // lanes of a row
         const int RP = 32 / LR, lr = lane / LR, lc = lane % LR;     // rows of a warp's step
@@ -646,34 +682,67 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 if (E4 || (check && odd_values<F16>(base, from, w - kFirst, kSettle, RP, lr, lc, CH))) {
                     uint32_t* flags = s_flag + (tile & 3) * (kLoadWarps * 4) + w * 4;
                     const unsigned char* ex = smem + M::exps + (tile % 3 * 2 + isv) * BN;
-                    for (int q = w - kFirst; q < BN / RP; q += kSettle) {
-                        const int r = q * RP + lr;
-                        uint32_t o[8];
-                        bool bad = false;
-                        constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
-                        if (lc < CH) {
-                            if constexpr (E4) {
-                                widen16<F16>(*reinterpret_cast<const uint4*>(base + kBlock + r * 128 + lc * 16), ex[r], o);
-                            } else {
-                                const uint4 v = *reinterpret_cast<const uint4*>(base + chunk_at(r, lc));
-                                o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
-                            }
-                            if (check && r >= from)
+                    // several of its rows read before the first is written: a read
+                    // waits hundreds of clocks behind the products' operands
+                    for (int q0 = w - kFirst; q0 < BN / RP; q0 += kBatch * kSettle) {
+                        uint4 in[kBatch];
+                        int e[kBatch];
 #pragma unroll
-                                for (int i = 0; i < (E4 ? 8 : 4); ++i)
-                                    bad |= (o[i] & top) == top || (o[i] >> 16 & top) == top;
-                        }
-                        bool row_bad = false;
-                        if (check) {
-                            row_bad = (__ballot_sync(0xffffffffu, bad) & group) != 0;
-                            if (row_bad && lc == 0) atomicOr(flags + (r >> 5), 1u << (r & 31));
+                        for (int i = 0; i < kBatch; ++i) {
+                            const int q = q0 + i * kSettle, r = q * RP + lr;
+                            in[i] = make_uint4(0, 0, 0, 0), e[i] = 127;
+                            if (q < BN / RP && lc < CH) {
+                                in[i] = *reinterpret_cast<const uint4*>(base + (E4 ? kBlock + r * 128 + lc * 16 : chunk_at(r, lc)));
+                                e[i] = E4 ? ex[r] : 127;
+                            }
                         }
                         __syncwarp();                // a row's lanes have read it before it is written over
-                        if (lc < CH && (E4 || row_bad)) {
+                        if constexpr (E4) {
+                            bool usual = !check;
 #pragma unroll
-                            for (int i = 0; i < (E4 ? 8 : 4); i += 4)
-                                *reinterpret_cast<uint4*>(base + chunk_at(r, E4 ? 2 * lc + i / 4 : lc)) =
-                                    row_bad ? make_uint4(0, 0, 0, 0) : make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                            for (int i = 0; i < kBatch; ++i) usual = usual && usual_power<F16>(e[i]);
+                            if (__all_sync(0xffffffffu, usual)) {
+                                // (no branch between the rows: their steps overlap)
+#pragma unroll
+                                for (int i = 0; i < kBatch; ++i) {
+                                    const int q = q0 + i * kSettle, r = q * RP + lr;
+                                    uint32_t o[8];
+                                    widen16_usual<F16>(in[i], e[i], o);
+                                    if (q < BN / RP && lc < CH) {
+                                        *reinterpret_cast<uint4*>(base + chunk_at(r, 2 * lc)) = make_uint4(o[0], o[1], o[2], o[3]);
+                                        *reinterpret_cast<uint4*>(base + chunk_at(r, 2 * lc + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                                    }
+                                }
+                                continue;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) {
+                            const int q = q0 + i * kSettle, r = q * RP + lr;
+                            if (q >= BN / RP) break;
+                            uint32_t o[8];
+                            if constexpr (E4) {
+                                widen16<F16>(in[i], e[i], o);
+                            } else {
+                                o[0] = in[i].x, o[1] = in[i].y, o[2] = in[i].z, o[3] = in[i].w;
+                            }
+                            bool row_bad = false;
+                            if (check) {
+                                constexpr uint32_t top = F16 ? 0x7c00u : 0x7f80u;
+                                bool bad = false;
+                                if (lc < CH && r >= from)
+#pragma unroll
+                                    for (int y = 0; y < (E4 ? 8 : 4); ++y)
+                                        bad |= (o[y] & top) == top || (o[y] >> 16 & top) == top;
+                                row_bad = (__ballot_sync(0xffffffffu, bad) & group) != 0;
+                                if (row_bad && lc == 0) atomicOr(flags + (r >> 5), 1u << (r & 31));
+                            }
+                            if (lc < CH && (E4 || row_bad)) {
+#pragma unroll
+                                for (int y = 0; y < (E4 ? 8 : 4); y += 4)
+                                    *reinterpret_cast<uint4*>(base + chunk_at(r, E4 ? 2 * lc + y / 4 : lc)) =
+                                        row_bad ? make_uint4(0, 0, 0, 0) : make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+                            }
                         }
                     }
                 }
