@@ -1,12 +1,15 @@
-// k8_attn_mma.cuh -- tree attention for few query rows (sdv_tree_attn); one
-// translation unit per head dimension includes this.
+// k8_attn_mma.cuh -- tree attention for head dimensions above 128 and for pages
+// of any size (sdv_tree_attn), where the kernels that load by tile copies do not
+// go; one translation unit per head dimension includes this.
 //
-// One decode step reads a sequence's whole cache for a handful of query rows,
-// so it is bound by HBM, and what matters is bytes in flight: tiles of BN
-// positions come in by 16-byte asynchronous copies, several tiles ahead, into
-// rows swizzled so that the fragments are read without bank conflicts.  The
-// contractions run on mma.sync m16n8k16, whose 16 rows waste less on 8 query
-// heads than a 128-row instruction would.
+// A tile of BN positions may begin and end anywhere in a page, so its rows come
+// in by 16-byte asynchronous copies, each with an address of its own, several
+// tiles ahead, swizzled so that the fragments are read without bank conflicts.
+// The contractions run on mma.sync m16n8k16, whose 16 rows waste less on 8 query
+// heads than a 128-row instruction would.  For few rows the cache's bytes and
+// the copies' instructions bound it (32 sequences of 4000 positions, 8 kv heads,
+// 8 rows each: heads of 256, 327 us, 3.2 TB/s; heads of 128 on pages of 12, 130
+// us, 4.0 TB/s), for many the matrix instructions.
 //
 // MT = 16 WM rows; the WN = 4 / WM warps that share rows split each tile's
 // positions and keep their own running maximum, sum and output, which are
@@ -537,8 +540,13 @@ cudaError_t launch_one(AttnArgs a, int nsm, cudaStream_t s) {
     return e2 != cudaSuccess ? e2 : launch_attn_combine(a, F16, 16 * WM, s);
 }
 
+// Units of 16 rows read the cache once per 16 rows, units of 64 compute for 64
+// however many there are.  32 sequences of 4000 positions, 8 kv heads of 128 on
+// pages of 12, 16-bit cache: 16 rows 132 and 370 us, 32 rows 245 and 378, 48 rows
+// 359 and 385; e4m3: 16 rows 120 and 554 us, 48 rows 318 and 560, 64 rows 411
+// and 562.  (Heads of 64, e4m3: 48 rows 231 and 262 us, 64 rows 296 and 270.)
 template <int DP, bool E4, bool F16> cudaError_t launch_rows(const AttnArgs& a, int rows, int nsm, cudaStream_t s) {
-    return rows <= 16 ? launch_one<DP, E4, F16, 1>(a, nsm, s) : launch_one<DP, E4, F16, 4>(a, nsm, s);
+    return rows <= (E4 ? 48 : 32) ? launch_one<DP, E4, F16, 1>(a, nsm, s) : launch_one<DP, E4, F16, 4>(a, nsm, s);
 }
 
 template <int DP>

@@ -10,7 +10,9 @@
 // that owns draft token j counts it after row j.
 //
 // Bound by HBM: each logit is read and written once (2 + 2 bytes in bf16, and a
-// bit of the grammar mask).  Four rows are in flight per thread.
+// bit of the grammar mask).  Four rows are in flight per thread.  32 sequences of
+// 8 drafts of 16 tokens, 152064 logits a row under a grammar: 558 us, 4.8 TB/s
+// (what is left is the instructions of a logit: unpacking, counts, rounding).
 #include <cuda_bf16.h>
 
 #include "sdv_device.cuh"
@@ -208,6 +210,8 @@ cudaError_t launch_logits(const LogitsArgs& args, bool bf16, int nsm, cudaStream
     const int64_t base = static_cast<int64_t>((a.V + slice - 1) / slice) * a.B;
     // Few sequences: their rows are shared out until every SM has about eight
     // CTAs, a CTA keeping four rows at least (its counts and biases serve those).
+    // One sequence of 4 x 17 rows: 31 us against 43 us in one share; two of 8 x 17:
+    // 51 against 72; eight of 4 x 17: 78 against 74.
     const int64_t all = static_cast<int64_t>(a.K) * (a.G + 1);
     int64_t split = (static_cast<int64_t>(nsm) * 8 + base - 1) / base;
     const int64_t most = (all + kFlight - 1) / kFlight;
