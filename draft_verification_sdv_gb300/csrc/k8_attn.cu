@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, int
 cudaError_t launch_attn_combine(const AttnArgs& a, bool f16, int MT, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     const int blocks = (MT * (a.c.D / 4) + kThreads - 1) / kThreads;        // 16 rows of 128: two
-    cfg.gridDim = dim3(static_cast<unsigned>(a.ctas), static_cast<unsigned>(blocks < 8 ? blocks : 8));
+    cfg.gridDim = dim3(static_cast<unsigned>(a.ctas), static_cast<unsigned>(blocks < 16 ? blocks : 16));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

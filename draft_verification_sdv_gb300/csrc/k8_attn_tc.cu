@@ -99,6 +99,10 @@ __device__ __forceinline__ void tma_load_q(uint32_t dst, const CUtensorMap* map,
                  "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(head), "r"(node), "r"(b) : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 #define SDV_R4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
 #define SDV_R16(r, i) SDV_R4(r, i), SDV_R4(r, i + 4), SDV_R4(r, i + 8), SDV_R4(r, i + 12)
 #define SDV_I4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
@@ -197,6 +201,31 @@ __device__ __forceinline__ uint32_t sees(const Unit& u, bool tree, int node, con
     const int left = u.cut.cnt - b;                  // nodes from the first position on
     if (left < 32) bits &= left <= 0 ? 0u : (1u << left) - 1u;
     return bits;
+}
+
+// Rows first .. first + 127 of a unit of `nodes` nodes, by warp `at` of `of`; all copies are under
+// way at once where queries lie on 16 bytes and their signs stay.
+__device__ __noinline__ void copy_queries(const unsigned char* q, int64_t q_sn, int64_t q_sh, int g, int nodes, int chunks, int first, int at,
+                                          int of, unsigned char* qs, uint32_t flip) {
+    const int lane = threadIdx.x & 31, lanes = chunks > 8 ? 16 : 8, rows = 32 / lanes, ch = lane % lanes;
+    if (ch < chunks) {
+        for (int i = at; i < kRows / rows; i += of) {
+            const int r = i * rows + lane / lanes, row = first + r, node = row / g;
+            const unsigned char* src = q + node * q_sn + (row - node * g) * q_sh + ch * 16;
+            unsigned char* dst = qs + chunk_at(r, ch);
+            if (node >= nodes) {
+                *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+            } else if (flip == 0 && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+            } else {
+                const unsigned short* e = reinterpret_cast<const unsigned short*>(src);
+                *reinterpret_cast<uint4*>(dst) =
+                    make_uint4((e[0] | static_cast<uint32_t>(e[1]) << 16) ^ flip, (e[2] | static_cast<uint32_t>(e[3]) << 16) ^ flip,
+                               (e[4] | static_cast<uint32_t>(e[5]) << 16) ^ flip, (e[6] | static_cast<uint32_t>(e[7]) << 16) ^ flip);
+            }
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Whether a row sees a position on a page that is not the cache's.
@@ -324,6 +353,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             mbar_init(bars + kFree + i, 1);
         }
         for (int i = 0; i < kSlots; ++i) mbar_init(bars + kLand + i, 1);
+    }
+    if (tid == 32) {                                 // on its way while the work is shared out
+        prefetch_map(&map_k);
+        prefetch_map(&map_v);
+        if (q_boxes) prefetch_map(&map_q);
     }
     if (warp == 11) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(s_tmem)) : "memory");
@@ -770,24 +804,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                             }
                             continue;
                         }
-                        const int lanes = D > 64 ? 16 : 8, rows = 32 / lanes, ch = lane % lanes;
-                        for (int i = w - kFirst; i < kRows / rows; i += kSettle) {
-                            const int r = i * rows + lane / lanes, row = first + r, node = row / a.g;
-                            if (ch >= D / 8) continue;
-                            const unsigned char* src = a.q + u.b * a.q_sb + node * a.q_sn +
-                                                       (static_cast<int64_t>(u.h) * a.g + row % a.g) * a.q_sh + ch * 16;
-                            uint4 v = make_uint4(0, 0, 0, 0);
-                            if (node < u.cut.cnt) {
-                                if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-                                    v = *reinterpret_cast<const uint4*>(src);
-                                } else {
-                                    const unsigned short* e = reinterpret_cast<const unsigned short*>(src);
-                                    v = make_uint4(e[0] | static_cast<uint32_t>(e[1]) << 16, e[2] | static_cast<uint32_t>(e[3]) << 16,
-                                                   e[4] | static_cast<uint32_t>(e[5]) << 16, e[6] | static_cast<uint32_t>(e[7]) << 16);
-                                }
-                            }
-                            *reinterpret_cast<uint4*>(qs + chunk_at(r, ch)) = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
-                        }
+                        copy_queries(a.q + u.b * a.q_sb + static_cast<int64_t>(u.h) * a.g * a.q_sh, a.q_sn, a.q_sh, a.g, u.cut.cnt, D / 8, first,
+                                     w - kFirst, kSettle, qs, flip);
                         fence_async();
                         __syncwarp();
                         if (lane == 0) sync.arrive(kQFull + s);
