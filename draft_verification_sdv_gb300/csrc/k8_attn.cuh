@@ -85,28 +85,42 @@ __device__ __forceinline__ int64_t head_tiles(const AttnArgs& a, const Cut& c, i
     return chain_tiles<MT, BN>(a, c, mts);
 }
 
+// a / b of numbers that are not negative: 64 bits only where they are needed.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return (a | b) >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
+
 struct Part {                // a CTA's part of the line
     int64_t begin, end;      // tiles, counted from the line's first unit
     int64_t total;
+    int64_t each;            // (total - ctas) / ctas, and what is left of it
+    int rest;
     int ctas;                // CTAs that have a part
     int b;                   // sequence of `begin`, and where its first unit would be
     int64_t seq0;
     const int64_t* begins;   // rounds > 0: every CTA's begin (valid until shared memory is reused)
 };
 
-// Tiles of the units of a sequence that come before its unit j.
-template <int MT, int BN>
-__device__ __forceinline__ int64_t tiles_before(const AttnArgs& a, const Cut& c, int mts, int j) {
-    const int h = j / mts;
-    int64_t n = h > 0 ? head_tiles<MT, BN>(a, c, mts) * h : 0;
-    if (j > h * mts) n += a.mask ? head_tiles<MT, BN>(a, c, j - h * mts) : chain_tiles<MT, BN>(a, c, j - h * mts);
-    return n;
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// How many of the units j .. (all heads, of a sequence) are row tile mt's.
+__device__ __forceinline__ int units_from(int heads, int mts, int j, int mt) {
+    return heads - (j > mt ? (j - mt + mts - 1) / mts : 0);
+}
+
+// Tiles of row tile mt of a sequence.
+template <int MT, int BN> __device__ __forceinline__ int unit_tiles(const AttnArgs& a, const Cut& c, int mt) {
+    return tiles_of<BN>(tile_len<MT>(a, c, mt));
 }
 
 // Where CTA i's part begins: every CTA has a tile at least.
 __device__ __forceinline__ int64_t part_begin(const Part& p, int i) {
     if (p.begins) return p.begins[i];
-    return i + (p.total - p.ctas) * i / p.ctas;
+    return i + p.each * i + static_cast<uint32_t>(p.rest) * static_cast<uint32_t>(i) / static_cast<uint32_t>(p.ctas);
 }
 
 // Every thread of the CTA calls this; `sm` holds 48 + 3 * ctas int64.
@@ -116,26 +130,27 @@ __device__ __forceinline__ Part find_part(const AttnArgs& a, int mts, int64_t* s
     const int per_seq = a.c.H * mts, n = a.ctas;
     const int first = a.rounds * n;                  // the line's first unit
     const int b0 = first / per_seq, j0 = first - b0 * per_seq;
-    int64_t mine = 0;
-    for (int b = b0 + tid; b < a.B; b += THREADS) {
-        const Cut c = cut_of(a, b);
-        mine += head_tiles<MT, BN>(a, c, mts) * a.c.H;
-        if (b == b0) mine -= tiles_before<MT, BN>(a, c, mts, j0);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) sm[warp] = mine;
     int64_t* begins = sm + 48;
     int64_t* done = begins + n + 1;
     if (a.rounds > 0)
-        for (int i = tid; i < n; i += THREADS) {     // the tiles of each CTA's rounds
-            int64_t s = 0;
-            for (int k = 0; k < a.rounds; ++k) {
-                const int j = i + k * n, b = j / per_seq;
-                s += tiles_of<BN>(tile_len<MT>(a, cut_of(a, b), (j - b * per_seq) % mts));
-            }
-            done[i] = s;
+        for (int i = tid; i < n; i += THREADS) done[i] = 0;
+    // a thread takes row tiles of the line's sequences
+    int64_t mine = 0;
+    const int64_t pairs = static_cast<int64_t>(a.B - b0) * mts;
+    for (int64_t i = tid; i < pairs; i += THREADS) {
+        const int b = static_cast<int>(quotient(i, mts)), mt = static_cast<int>(i - static_cast<int64_t>(b) * mts);
+        mine += static_cast<int64_t>(unit_tiles<MT, BN>(a, cut_of(a, b0 + b), mt)) * units_from(a.c.H, mts, b == 0 ? j0 : 0, mt);
+    }
+    mine = warp_sum(mine);
+    if (lane == 0) sm[warp] = mine;
+    if (a.rounds > 0) {
+        __syncthreads();
+        for (int j = tid; j < first; j += THREADS) { // the tiles of each CTA's rounds
+            const int b = j / per_seq;
+            const int tiles = unit_tiles<MT, BN>(a, cut_of(a, b), (j - b * per_seq) % mts);
+            atomicAdd(reinterpret_cast<unsigned long long*>(done + j % n), static_cast<unsigned long long>(tiles));
         }
+    }
     __syncthreads();
     Part p;
     p.total = 0;
@@ -143,14 +158,15 @@ __device__ __forceinline__ Part find_part(const AttnArgs& a, int mts, int64_t* s
     for (int w = 0; w < THREADS / 32; ++w) p.total += sm[w];
     p.ctas = static_cast<int>(p.total < n ? p.total : n);
     p.begins = nullptr;
+    p.each = quotient(p.total - p.ctas, p.ctas > 0 ? p.ctas : 1);
+    p.rest = static_cast<int>(p.total - p.ctas - p.each * p.ctas);
     if (a.rounds > 0) {
         // shares of the line: what a CTA's rounds lack of the mean
         if (warp == 0) {
             int64_t sum = 0;
             for (int i = lane; i < n; i += 32) sum += done[i];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const int64_t mean = (sum + p.total) / n + 1;
+            sum = warp_sum(sum);
+            const int64_t mean = quotient(sum + p.total, n) + 1;
             int64_t base = 0;
             for (int i0 = 0; i0 < p.ctas; i0 += 32) {
                 const int i = i0 + lane;
@@ -181,7 +197,11 @@ __device__ __forceinline__ Part find_part(const AttnArgs& a, int mts, int64_t* s
     p.begin = part_begin(p, i);
     p.end = i + 1 == p.ctas ? p.total : part_begin(p, i + 1);
     if (warp == 0) {
-        int64_t base = b0 < a.B ? -tiles_before<MT, BN>(a, cut_of(a, b0), mts, j0) : 0;
+        int64_t base = 0;                            // tiles of sequence b0 that come before the line
+        if (j0 > 0 && b0 < a.B)
+            for (int mt = lane; mt < mts; mt += 32)
+                base -= static_cast<int64_t>(unit_tiles<MT, BN>(a, cut_of(a, b0), mt)) * (a.c.H - units_from(a.c.H, mts, j0, mt));
+        base = warp_sum(base);
         for (int bb = b0; bb < a.B; bb += 32) {
             const int b = bb + lane;
             const int64_t n_b = b < a.B ? head_tiles<MT, BN>(a, cut_of(a, b), mts) * a.c.H : 0;
@@ -212,7 +232,8 @@ struct Unit {
 };
 
 // Walks a CTA's units: those of its rounds, then those of its part, of which the
-// first is found by division and the others follow one another.
+// first is found by division and the others follow one another.  Whole warps
+// begin together; what goes on from a copy may be a single thread.
 template <int MT, int BN> struct Walk {
     int round;               // the next one
     int left, rest;          // tiles left of the part; tiles of the unit before it
@@ -220,37 +241,53 @@ template <int MT, int BN> struct Walk {
     Cut cut;
     __device__ __forceinline__ void begin(const AttnArgs& a, const Part& p, int mts) {
         round = 0;
-        if (a.rounds == 0) start(a, p, mts);
-    }
-    __device__ __forceinline__ void start(const AttnArgs& a, const Part& p, int mts) {
         left = static_cast<int>(p.end - p.begin);
         rest = 0;
         b = p.b;
         h = mt = 0;
         if (b >= a.B) return;
         cut = cut_of(a, b);
-        const int64_t in_seq = p.begin - p.seq0, per_head = head_tiles<MT, BN>(a, cut, mts);
-        h = static_cast<int>(in_seq / per_head);
-        int64_t before = in_seq - h * per_head;
+        const int lane = threadIdx.x & 31;
+        const int64_t in_seq = p.begin - p.seq0;
         if (a.mask) {
+            const int64_t per_head = head_tiles<MT, BN>(a, cut, mts);
+            h = static_cast<int>(quotient(in_seq, per_head));
+            int64_t before = in_seq - h * per_head;
             const int t = tiles_of<BN>(cut.ctx + cut.cnt);
             const int live = min(mts, (cut.cnt * a.g + MT - 1) / MT);
             if (before < static_cast<int64_t>(live) * t) {
-                mt = static_cast<int>(before / t);
+                mt = static_cast<int>(quotient(before, t));
                 before -= static_cast<int64_t>(mt) * t;
             } else {
                 mt = live + static_cast<int>(before - static_cast<int64_t>(live) * t);
                 before = 0;
             }
+            rest = static_cast<int>(before);
         } else {
-            while (true) {
-                const int t = tiles_of<BN>(tile_len<MT>(a, cut, mt));
-                if (before < t) break;
-                before -= t;
-                ++mt;
+            // a lane to a row tile, 32 at a time
+            int64_t per_head = 0;
+            for (int i = lane; i < mts; i += 32) per_head += unit_tiles<MT, BN>(a, cut, i);
+            per_head = warp_sum(per_head);
+            h = static_cast<int>(quotient(in_seq, per_head));
+            int64_t before = in_seq - h * per_head;
+            for (int i0 = 0; i0 < mts; i0 += 32) {
+                const int own = i0 + lane < mts ? unit_tiles<MT, BN>(a, cut, i0 + lane) : 0;
+                int upto = own;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += x;
+                }
+                const uint32_t past = __ballot_sync(0xffffffffu, upto > before);
+                if (past) {
+                    const int at = __ffs(past) - 1;
+                    mt = i0 + at;
+                    rest = static_cast<int>(before - __shfl_sync(0xffffffffu, upto - own, at));
+                    break;
+                }
+                before -= __shfl_sync(0xffffffffu, upto, 31);
             }
         }
-        rest = static_cast<int>(before);
     }
     __device__ __forceinline__ bool next(const AttnArgs& a, const Part& p, int mts, Unit& u) {
         if (round < a.rounds) {
@@ -263,7 +300,7 @@ template <int MT, int BN> struct Walk {
             u.t0 = 0;
             u.t1 = tiles_of<BN>(u.len);
             u.whole = true;
-            if (++round == a.rounds) start(a, p, mts);
+            ++round;
             return true;
         }
         if (left <= 0) return false;
@@ -297,10 +334,9 @@ __device__ __forceinline__ float* part_rows(const AttnArgs& a, int cta, int slot
 // desc[2 i] = the unit that CTA i's part begins within, if CTA i is the first
 // to go on with it: (b, h, mt, first CTA); the last CTA in desc[2 i + 1].  One
 // thread writes it.
-template <int MT, int BN> __device__ __forceinline__ void write_desc(const AttnArgs& a, const Part& p, int mts) {
+template <int MT, int BN>
+__device__ __forceinline__ void write_desc(const AttnArgs& a, const Part& p, const Walk<MT, BN>& w) {    // w: begun, not gone on
     const int i = blockIdx.x;
-    Walk<MT, BN> w;
-    w.start(a, p, mts);
     int4 d = make_int4(-1, 0, 0, 0);
     if (w.left > 0 && w.rest > 0) {
         const int64_t first = p.begin - w.rest, end = first + tiles_of<BN>(tile_len<MT>(a, w.cut, w.mt));

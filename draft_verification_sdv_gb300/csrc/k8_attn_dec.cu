@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
     const Part part = find_part<MT, BN, kDecThreads>(a, mts, s_part);     // holds barriers of the CTA
     Walk<MT, BN> walk;
     walk.begin(a, part, mts);
-    if (tid == 0) write_desc<MT, BN>(a, part, mts);
+    if (tid == 0) write_desc(a, part, walk);
     Unit u;
     uint32_t n = 0;                                  // tiles so far
 

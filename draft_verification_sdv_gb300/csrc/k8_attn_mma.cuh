@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
 
     Walk<MT, BN> walk;
     walk.begin(a, part, mts);
-    if (tid == 0) write_desc<MT, BN>(a, part, mts);
+    if (tid == 0) write_desc(a, part, walk);
     Unit u;
     while (walk.next(a, part, mts, u)) {
         __syncthreads();                            // the unit before is done with shared memory

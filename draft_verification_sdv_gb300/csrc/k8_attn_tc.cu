@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const uint32_t tmem = *s_tmem;
     Walk<MT, BN> walk;
     walk.begin(a, part, mts);
-    if (tid == 0) write_desc<MT, BN>(a, part, mts);
+    if (a.rounds > 0 && tid == 0) write_desc(a, part, walk);    // (its begins are in the ring)
     __syncthreads();                                 // the ring may be used
 
     // the softmax warps hold a row of scores: they take registers that the others
@@ -396,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         SoftmaxState& state = reinterpret_cast<SoftmaxState*>(smem + M::state)[warp];
         Unit& u = state.u;
         if (lane == 0) state.walk = walk;
+        if (a.rounds == 0 && tid == 0) write_desc(a, part, walk);
         // the next unit; and for a new sequence a look for pages that are not the
         // cache's: a slow path if there are any
         auto prepare = [&]() {
@@ -586,9 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const uint32_t group = ((1u << LR) - 1u) << (lr * LR);
 
         // warp 8: begins the copies of the next step; a walk of its own, ahead
-        Walk<MT, BN> lead;
+        Walk<MT, BN> lead = walk;
         Unit lu{};
-        lead.begin(a, part, mts);
         int lt = 0, lnt = 0;                         // tile of the unit, its tiles
         int lpage = -1, loff = 0, npage = -1, noff = 0;     // this lane's rows of the tile and of the next one
         uint32_t lstep = 0;
