@@ -492,42 +492,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     if (lane == 0) sync.arrive(kPFull + st);
                 };
 #pragma unroll 1
-                for (int t = 0; t < plain; ++t, ++n) {
-                    sync.wait(kSFull + st, n & 1);
-                    __syncwarp();
-                    fence_after();
-                    float x[128];
-                    tmem_ld128(x, tS);
-                    weigh(x, t == 0);
-                    hand_over();
-                    if (mrow && t + 1 == plain && t + 1 < nt) mask_words(a, mrow, (u.t0 + t + 1) * BN - u.cut.ctx, words);
-                }
-#pragma unroll 1
-                for (int t = plain; t < nt; ++t, ++n) {
+                for (int t = 0; t < nt; ++t, ++n) {
+                    const bool mixed = t >= plain;
                     const int pos0 = (u.t0 + t) * BN;
-                    uint32_t see[4];
+                    uint32_t see[4] = {0, 0, 0, 0};
+                    if (mixed) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) see[i] = live ? sees(u, mrow != nullptr, node, words, pos0, i) : 0u;
-                    if (mrow && t + 1 < nt) mask_words(a, mrow, pos0 + BN - u.cut.ctx, words);
-                    if (any_bad) nan_row |= sees_bad_page(table, a.c.pages, a.c.P, make_uint4(see[0], see[1], see[2], see[3]), pos0, u.len);
+                        for (int i = 0; i < 4; ++i) see[i] = live ? sees(u, mrow != nullptr, node, words, pos0, i) : 0u;
+                        if (any_bad) nan_row |= sees_bad_page(table, a.c.pages, a.c.P, make_uint4(see[0], see[1], see[2], see[3]), pos0, u.len);
+                    }
+                    if (mrow && t + 1 >= plain && t + 1 < nt) mask_words(a, mrow, pos0 + BN - u.cut.ctx, words);
                     sync.wait(kSFull + st, n & 1);
                     __syncwarp();
                     fence_after();
                     float x[128];
                     tmem_ld128(x, tS);
+                    if (mixed) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) x[32 * i + y] = see[i] >> y & 1 ? x[32 * i + y] : -INFINITY;
+                            for (int y = 0; y < 32; ++y) x[32 * i + y] = see[i] >> y & 1 ? x[32 * i + y] : -INFINITY;
+                    }
                     weigh(x, t == 0);
-                    // values that are not numbers, among those that the row sees
-                    const uint32_t T = nv + t;
-                    sync.wait(kFull + ((T + 1) & 1), (T + 1) >> 1 & 1);
-                    const uint32_t* f = s_flag + (T & 3) * (kLoadWarps * 4);
+                    if (mixed) {                     // values that are not numbers, among those that the row sees
+                        const uint32_t T = nv + t;
+                        sync.wait(kFull + ((T + 1) & 1), (T + 1) >> 1 & 1);
+                        const uint32_t* f = s_flag + (T & 3) * (kLoadWarps * 4);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (see[i] & (f[i] | f[4 + i] | f[8 + i])) nan_row = true;
-                    __syncwarp();
+                        for (int i = 0; i < 4; ++i)
+                            if (see[i] & (f[i] | f[4 + i] | f[8 + i])) nan_row = true;
+                        __syncwarp();
+                    }
                     hand_over();
                 }
             }
