@@ -203,29 +203,23 @@ __device__ __forceinline__ uint32_t sees(const Unit& u, bool tree, int node, con
     return bits;
 }
 
-// Rows first .. first + 127 of a unit of `nodes` nodes, by warp `at` of `of`; all copies are under
-// way at once where queries lie on 16 bytes and their signs stay.
-__device__ __noinline__ void copy_queries(const unsigned char* q, int64_t q_sn, int64_t q_sh, int g, int nodes, int chunks, int first, int at,
-                                          int of, unsigned char* qs, uint32_t flip) {
-    const int lane = threadIdx.x & 31, lanes = chunks > 8 ? 16 : 8, rows = 32 / lanes, ch = lane % lanes;
-    if (ch < chunks) {
-        for (int i = at; i < kRows / rows; i += of) {
-            const int r = i * rows + lane / lanes, row = first + r, node = row / g;
-            const unsigned char* src = q + node * q_sn + (row - node * g) * q_sh + ch * 16;
-            unsigned char* dst = qs + chunk_at(r, ch);
-            if (node >= nodes) {
-                *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
-            } else if (flip == 0 && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-            } else {
-                const unsigned short* e = reinterpret_cast<const unsigned short*>(src);
-                *reinterpret_cast<uint4*>(dst) =
-                    make_uint4((e[0] | static_cast<uint32_t>(e[1]) << 16) ^ flip, (e[2] | static_cast<uint32_t>(e[3]) << 16) ^ flip,
-                               (e[4] | static_cast<uint32_t>(e[5]) << 16) ^ flip, (e[6] | static_cast<uint32_t>(e[7]) << 16) ^ flip);
-            }
+// A thread's row of queries into its place, with the sign turned where flip is
+// set: copies that are still under way if it lies on 16 bytes.
+__device__ __noinline__ void copy_row(const unsigned char* src, bool there, uint32_t flip, unsigned char* qs, int r, int chunks) {
+    const bool plain = flip == 0 && (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+    for (int c = 0; c < chunks; ++c, src += 16) {
+        unsigned char* dst = qs + chunk_at(r, c);
+        if (!there) {
+            *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+        } else if (plain) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+        } else {
+            const unsigned short* e = reinterpret_cast<const unsigned short*>(src);
+            *reinterpret_cast<uint4*>(dst) =
+                make_uint4((e[0] | static_cast<uint32_t>(e[1]) << 16) ^ flip, (e[2] | static_cast<uint32_t>(e[3]) << 16) ^ flip,
+                           (e[4] | static_cast<uint32_t>(e[5]) << 16) ^ flip, (e[6] | static_cast<uint32_t>(e[7]) << 16) ^ flip);
         }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Whether a row sees a position on a page that is not the cache's.
@@ -278,7 +272,11 @@ template <bool F16> __device__ __forceinline__ void widen16(const uint4& raw, in
 }
 
 // The same for the usual powers, those that one 16-bit factor holds: half the work.
-template <bool F16> __device__ __forceinline__ bool usual_power(int e) { return F16 ? e >= 113 && e <= 142 : e <= 134; }
+template <bool F16> __device__ __forceinline__ bool usual_power(int e) { return F16 ? e >= 113 && e <= 134 : e <= 134; }
+__device__ __forceinline__ bool has_nan(const uint4& v) {
+    return ((((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) | ((v.z & 0x7f7f7f7fu) + 0x01010101u) |
+             ((v.w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u) != 0;
+}
 template <bool F16> __device__ __forceinline__ void widen16_usual(const uint4& raw, int e, uint32_t (&o)[8]) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     uint32_t bad = 0;
@@ -302,30 +300,36 @@ template <bool F16> __device__ __forceinline__ void widen16_usual(const uint4& r
     }
 }
 
-// Whether a warp's share of a tile's 16-bit rows holds what is not a number in
-// rows from `from` on: rows q * RP + lr for q = first, first + step, ..., of which
-// the lane has chunk lc.
-template <bool F16>
-__device__ __forceinline__ bool odd_values(const unsigned char* base, int from, int first, int step, int RP, int lr, int lc, int chunks) {
-    // all ones in an exponent carry into the sign's place
-    constexpr uint32_t ones = F16 ? 0x7c007c00u : 0x7f807f80u, unit = F16 ? 0x04000400u : 0x00800080u;
-    uint32_t bad = 0;
-    if (lc < chunks)
+// Whether rows from `from` on of a tile of 16-bit cells hold what is not a number:
+// times zero, it adds one that stays.  A warp reads the rows as they lie: the
+// swizzle keeps a row's chunks in the row, and columns past D are zeros.
+template <bool F16> __device__ __forceinline__ bool odd_values(const unsigned char* base, int from, int blocks, int lane) {
+    uint32_t acc[4] = {0, 0, 0, 0};
+    for (int b = 0; b < blocks; ++b) {
+        const unsigned char* at = base + b * kBlock + lane * 16;
 #pragma unroll 8
-        for (int q = first + from / RP / step * step; q < BN / RP; q += step) {
-            const int r = q * RP + lr;
-            const uint4 v = *reinterpret_cast<const uint4*>(base + chunk_at(r, lc));
-            const uint32_t b = ((v.x & ones) + unit) | ((v.y & ones) + unit) | ((v.z & ones) + unit) | ((v.w & ones) + unit);
-            bad |= r >= from ? b : 0u;
+        for (int i = from >> 2; i < BN / 4; ++i) {
+            uint4 v = *reinterpret_cast<const uint4*>(at + i * 512);
+            if (4 * i + (lane >> 3) < from) v = make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                if constexpr (F16)
+                    asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc[y]) : "r"(w[y]), "r"(0));
+                else
+                    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[y]) : "r"(w[y]), "r"(0));
+            }
         }
-    return __any_sync(0xffffffffu, (bad & 0x80008000u) != 0);
+    }
+    // (zeros of either sign otherwise)
+    return __any_sync(0xffffffffu, ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0);
 }
 
-template <bool E4, bool F16>
+// BOXES: queries come by tile copies.
+template <bool E4, bool F16, bool BOXES>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                                                               const __grid_constant__ CUtensorMap map_v,
-                                                              const __grid_constant__ CUtensorMap map_q, int run_rows,
-                                                              bool q_boxes) {
+                                                              const __grid_constant__ CUtensorMap map_q, int run_rows) {
     using M = Smem;
     extern __shared__ unsigned char raw[];
     unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -341,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         s_tmem[1] = 0;                               // dead
         for (int i = 0; i < 4 * kLoadWarps * 4; ++i) s_flag[i] = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bars + kQFull + i, q_boxes ? 1 : E4 ? kLoadWarps : 1);
+            mbar_init(bars + kQFull + i, BOXES ? 1 : kRows / 32);
             mbar_init(bars + kQEmpty + i, 1);
             mbar_init(bars + kSFull + i, 1);
             mbar_init(bars + kPFull + i, kRows / 32);    // a warp arrives once: 32 arrivals take turns
@@ -357,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     if (tid == 32) {                                 // on its way while the work is shared out
         prefetch_map(&map_k);
         prefetch_map(&map_v);
-        if (q_boxes) prefetch_map(&map_q);
+        if (BOXES) prefetch_map(&map_q);
     }
     if (warp == 11) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(s_tmem)) : "memory");
@@ -419,7 +423,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             }
             return true;
         };
+        // queries that no box takes: each thread brings its row of the next unit (the
+        // scores of the one before are done with theirs: their last tile was read)
+        auto begin_queries = [&]() {
+            const int first_row = u.mt * MT + st * kRows, row = first_row + r, node = row / a.g;
+            if (u.len <= 0 || u.t1 <= u.t0 || first_row / a.g >= u.cut.cnt) return false;
+            copy_row(a.q + u.b * a.q_sb + node * a.q_sn + (static_cast<int64_t>(u.h) * a.g + row - node * a.g) * a.q_sh, node < u.cut.cnt,
+                     a.scale_log2 < 0.0f ? 0x80008000u : 0u, smem + M::q + st * kTile, r, D / 8);
+            return true;
+        };
+        auto end_queries = [&]() {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_async();
+            __syncwarp();
+            if (lane == 0) sync.arrive(kQFull + st);
+        };
         bool more = prepare();
+        if constexpr (!BOXES) {
+            if (more && begin_queries()) end_queries();
+        }
         while (more) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
             const int first_row = u.mt * MT + st * kRows;
@@ -536,12 +558,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             float* prow = part_rows(a, blockIdx.x, u.t0 > 0 ? 0 : 1, MT);
             __syncwarp();                            // every lane has read the unit
             more = prepare();
+            bool coming = false;
+            if constexpr (!BOXES) coming = more && begin_queries();
             if (run) {
                 const bool done = sync.wait(kOFull + st, units++ & 1);
                 __syncwarp();
                 fence_after();
                 if (!done) nan_row = true;
             }
+            if (coming) end_queries();
             if (nan_row || ubad) l = nanv;
             const bool empty = l == 0.0f || (!live && !ubad);
             const float inv = empty ? 0.0f : 1.0f / l;
@@ -708,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     if (lane < 4) s_flag[(tile & 3) * (kLoadWarps * 4) + w * 4 + lane] = 0;
                     __syncwarp();
                 }
-                if (E4 || (check && odd_values<F16>(base, from, w - kFirst, kSettle, RP, lr, lc, CH))) {
+                if (E4 || (check && odd_values<F16>(base, from, D > 64 ? 2 : 1, lane))) {
                     uint32_t* flags = s_flag + (tile & 3) * (kLoadWarps * 4) + w * 4;
                     const unsigned char* ex = smem + M::exps + (tile % 3 * 2 + isv) * BN;
                     // several of its rows read before the first is written: a read
@@ -727,9 +752,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         }
                         __syncwarp();                // a row's lanes have read it before it is written over
                         if constexpr (E4) {
-                            bool usual = !check;
+                            // (the usual powers make no infinity)
+                            bool usual = true;
 #pragma unroll
-                            for (int i = 0; i < kBatch; ++i) usual = usual && usual_power<F16>(e[i]);
+                            for (int i = 0; i < kBatch; ++i) usual = usual && usual_power<F16>(e[i]) && !(check && has_nan(in[i]));
                             if (__all_sync(0xffffffffu, usual)) {
                                 // (no branch between the rows: their steps overlap)
 #pragma unroll
@@ -778,39 +804,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 fence_async();
                 __syncwarp();
                 if (!isv && lane == 0) sync.arrive(kFull + (tile & 1));
-                if (j == 0) {
+                if (BOXES && j == 0 && w == kFirst) {
                     // the queries, once the scores of the unit before are done with theirs
                     const int streams = nt == 0 ? 0 : (u.mt * MT + kRows) / a.g < u.cut.cnt ? 2 : 1;
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        if (s >= streams || (q_boxes && w != kFirst)) break;
+                        if (s >= streams) break;
                         sync.wait(kQEmpty + s, (nq[s]++ & 1) ^ 1);
                         __syncwarp();
                         if (__any_sync(0xffffffffu, sync.is_dead())) break;
+                        // the 128 rows are the group's heads of whole nodes
                         unsigned char* qs = smem + M::q + s * kTile;
-                        const int first = u.mt * MT + s * kRows;
-                        const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-                        if (q_boxes) {                       // the 128 rows are the group's heads of whole nodes
-                            const int q_blocks = D > 64 ? 2 : 1;
-                            if (lane == 0) {
-                                mbar_arrive_expect_tx(bars + kQFull + s, q_blocks * kBlock);
-                                for (int i = 0; i < q_blocks; ++i)
-                                    tma_load_q(smem_u32(qs + i * kBlock), &map_q, bars + kQFull + s, i * 64, u.h * a.g, first / a.g, u.b);
-                            }
-                            continue;
+                        const int q_blocks = D > 64 ? 2 : 1;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(bars + kQFull + s, q_blocks * kBlock);
+                            for (int i = 0; i < q_blocks; ++i)
+                                tma_load_q(smem_u32(qs + i * kBlock), &map_q, bars + kQFull + s, i * 64, u.h * a.g, (u.mt * MT + s * kRows) / a.g, u.b);
                         }
-                        copy_queries(a.q + u.b * a.q_sb + static_cast<int64_t>(u.h) * a.g * a.q_sh, a.q_sn, a.q_sh, a.g, u.cut.cnt, D / 8, first,
-                                     w - kFirst, kSettle, qs, flip);
-                        fence_async();
-                        __syncwarp();
-                        if (lane == 0) sync.arrive(kQFull + s);
                     }
                 }
             }
             tiles += nt;
         }
         if (w >= kFirst && lane == 0) sync.arrive(kFull + (tiles & 1));       // the last values
-        if (w == kFirst && q_boxes)                  // a dead CTA too waits for the copies it has begun
+        if (BOXES && w == kFirst)                  // a dead CTA too waits for the copies it has begun
 #pragma unroll
             for (int s = 0; s < 2; ++s)
                 for (uint32_t n = 0; nq[s] > 0 && n < kPolls && !sync.poll(kQFull + s, (nq[s] - 1) & 1) && !sync.is_dead(); ++n) {}
@@ -928,25 +945,30 @@ bool encode_q(CUtensorMap* map, const AttnArgs& a) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool E4, bool F16>
-cudaError_t launch(AttnArgs a, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, bool q_boxes, int rows, int nsm,
-                   cudaStream_t s) {
+template <bool E4, bool F16, bool BOXES>
+cudaError_t launch_one(AttnArgs a, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, int rows, int nsm, cudaStream_t s) {
     constexpr int bytes = Smem::bytes;
-    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_tc_kernel<E4, F16>), bytes);
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_tc_kernel<E4, F16, BOXES>), bytes);
     if (e != cudaSuccess) return e;
     // the exchange of registers needs a launch that has them
     static const int regs = [] {
         cudaFuncAttributes at;
-        return cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(attn_tc_kernel<E4, F16>)) == cudaSuccess ? at.numRegs : 0;
+        return cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(attn_tc_kernel<E4, F16, BOXES>)) == cudaSuccess ? at.numRegs : 0;
     }();
     if (regs != kRegs) return cudaErrorInvalidKernelImage;
     a.ctas = nsm;
     const int mts = (a.N * a.g + MT - 1) / MT;
     const int64_t units = static_cast<int64_t>(a.B) * a.c.H * mts;
     a.rounds = mts > 1 && units >= 2 * nsm ? static_cast<int>(units / nsm - 1) : 0;
-    attn_tc_kernel<E4, F16><<<static_cast<unsigned>(nsm), kThreads, bytes, s>>>(a, k, v, q, rows, q_boxes);
+    attn_tc_kernel<E4, F16, BOXES><<<static_cast<unsigned>(nsm), kThreads, bytes, s>>>(a, k, v, q, rows);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_attn_combine(a, F16, MT, s);
+}
+
+template <bool E4, bool F16>
+cudaError_t launch(const AttnArgs& a, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, bool boxes, int rows, int nsm,
+                   cudaStream_t s) {
+    return boxes ? launch_one<E4, F16, true>(a, k, v, q, rows, nsm, s) : launch_one<E4, F16, false>(a, k, v, q, rows, nsm, s);
 }
 
 }  // namespace
