@@ -32,23 +32,32 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, int
         const int r = w / vec, d = (w % vec) * 4;
         const int row = mt * MT + r, node = row / a.g;
         if (node >= a.N) continue;
-        float top = -INFINITY;
+        // eight parts' loads at once, their sum in units of the largest so far
+        float top = -INFINITY, sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         bool nan = false;
-#pragma unroll 8
-        for (int i = first; i <= last; ++i) {
-            const float L = attn::part_rows(a, i, i == first, MT)[MT * D + r];
-            nan |= L != L;
-            top = fmaxf(top, L);
-        }
-        const float base = top == -INFINITY ? 0.0f : top;
-        float sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-        for (int i = first; i <= last; ++i) {
-            const float* p = attn::part_rows(a, i, i == first, MT);
-            const float f = ex2(p[MT * D + r] - base);
-            const float4 v = *reinterpret_cast<const float4*>(p + r * D + d);
-            sum += f;
-            acc[0] += v.x * f, acc[1] += v.y * f, acc[2] += v.z * f, acc[3] += v.w * f;
+        for (int i0 = first; i0 <= last; i0 += 8) {
+            float L[8];
+            float4 v[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                L[y] = -INFINITY, v[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (i0 + y > last) continue;
+                const float* p = attn::part_rows(a, i0 + y, i0 + y == first, MT);
+                L[y] = p[MT * D + r];
+                v[y] = *reinterpret_cast<const float4*>(p + r * D + d);
+            }
+            float to = top;
+#pragma unroll
+            for (int y = 0; y < 8; ++y) to = fmaxf(to, L[y]), nan |= L[y] != L[y];
+            const float base = to == -INFINITY ? 0.0f : to, by = ex2(top - base);
+            top = to;
+            sum *= by, acc[0] *= by, acc[1] *= by, acc[2] *= by, acc[3] *= by;
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                const float f = ex2(L[y] - base);
+                sum += f;
+                acc[0] += v[y].x * f, acc[1] += v[y].y * f, acc[2] += v[y].z * f, acc[3] += v[y].w * f;
+            }
         }
         const float inv = nan ? nan_value : sum == 0.0f ? 0.0f : 1.0f / sum;
         const int64_t orow = (static_cast<int64_t>(b) * a.N + node) * a.Hq + h * a.g + row % a.g;

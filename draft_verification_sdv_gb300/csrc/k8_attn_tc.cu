@@ -307,7 +307,7 @@ template <bool F16> __device__ __forceinline__ bool odd_values(const unsigned ch
     uint32_t acc[4] = {0, 0, 0, 0};
     for (int b = 0; b < blocks; ++b) {
         const unsigned char* at = base + b * kBlock + lane * 16;
-#pragma unroll 8
+#pragma unroll 4
         for (int i = from >> 2; i < BN / 4; ++i) {
             uint4 v = *reinterpret_cast<const uint4*>(at + i * 512);
             if (4 * i + (lane >> 3) < from) v = make_uint4(0, 0, 0, 0);
@@ -668,6 +668,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         };
         if (!E4 && w < kFirst)
             while (begin(true)) {}                   // nothing else to do
+        if (E4 && w == 0)
+            while (begin(false)) {}                  // the first tiles, before anything is waited for
 
         Unit u;
         uint32_t tiles = 0, step = 0, nq[2] = {0, 0};
