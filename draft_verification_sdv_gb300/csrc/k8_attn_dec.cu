@@ -52,7 +52,8 @@ template <int DP, bool E4, int H> struct DecSmem {
     static constexpr int bytes = (dead + 4 + 15) / 16 * 16 + 1024;
 };
 
-template <int DP, bool E4, bool F16, int H>
+// ONE: a kv head has one unit (16 rows at most).
+template <int DP, bool E4, bool F16, int H, bool ONE>
 __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                                                                const __grid_constant__ CUtensorMap map_v, int run_rows) {
     using S = DecShape<DP, E4>;
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
             mbar_init(bars + kStages + i, kDecWarps);
         }
     }
-    const int mts = (a.N * a.g + MT - 1) / MT;
+    const int mts = ONE ? 1 : (a.N * a.g + MT - 1) / MT;
     const Part part = find_part<MT, BN, kDecThreads>(a, mts, s_part);     // holds barriers of the CTA
     Walk<MT, BN> walk;
     walk.begin(a, part, mts);
@@ -135,12 +136,25 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
     auto chunk_of = [](int r, int c) { return (c >> 3) * (BN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
     constexpr int kAll = 32 * kDecWarps;
 
-    while (walk.next(a, part, mts, u)) {
+    // where the warp is among its units waits in shared memory: registers are short
+    __shared__ Walk<MT, BN> s_walk[kDecWarps];
+    if (lane == 0) s_walk[warp] = walk;
+    __syncwarp();
+    auto next = [&]() {
+        Walk<MT, BN> w = s_walk[warp];
+        __syncwarp();
+        const bool more = w.next(a, part, mts, u);
+        if (lane == 0) s_walk[warp] = w;
+        __syncwarp();
+        return more;
+    };
+
+    while (next()) {
         if (tid == 0 && u.cut.bad && a.status) atomicOr(a.status, kStatusBadLength);
         const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
         const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
         bool alive = true;
-        const int first = u.mt * MT;                 // of the unit's rows
+        const int first = ONE ? 0 : u.mt * MT;       // of the unit's rows
 
         // ---- queries ----
         for (int w = tid; w < 16 * (DP / 8); w += kAll) {
@@ -512,17 +526,17 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
     }
 }
 
-template <int DP, bool E4, bool F16, int H>
+template <int DP, bool E4, bool F16, int H, bool ONE>
 cudaError_t dec_one(AttnArgs a, int nsm, cudaStream_t s) {
     constexpr int bytes = DecSmem<DP, E4, H>::bytes, BN = DecShape<DP, E4>::BN;
     const int rows = min(a.c.P & -a.c.P, BN);        // of one copy: sure to lie in one page
     CUtensorMap k, v;
     if (!encode_cells(&k, a, a.c.k, E4, rows, true) || !encode_cells(&v, a, a.c.v, E4, rows, true)) return cudaErrorInvalidValue;
-    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_dec_kernel<DP, E4, F16, H>), bytes);
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_dec_kernel<DP, E4, F16, H, ONE>), bytes);
     if (e != cudaSuccess) return e;
     a.ctas = nsm * 2;
     a.rounds = 0;
-    attn_dec_kernel<DP, E4, F16, H><<<static_cast<unsigned>(a.ctas), kDecThreads, bytes, s>>>(a, k, v, rows);
+    attn_dec_kernel<DP, E4, F16, H, ONE><<<static_cast<unsigned>(a.ctas), kDecThreads, bytes, s>>>(a, k, v, rows);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_attn_combine(a, F16, 16, s);
 }
@@ -530,7 +544,12 @@ cudaError_t dec_one(AttnArgs a, int nsm, cudaStream_t s) {
 // With 8 rows or fewer the other half of the instructions' 16 is not carried
 // along: 64 ragged sequences of 8 rows, e4m3, 485 us against 557 us.
 template <int DP, bool E4, bool F16> cudaError_t dec_rows(const AttnArgs& a, int nsm, cudaStream_t s) {
-    return a.N * a.g <= 8 ? dec_one<DP, E4, F16, 1>(a, nsm, s) : dec_one<DP, E4, F16, 2>(a, nsm, s);
+    const int rows = a.N * a.g;
+    if (rows <= 8) return dec_one<DP, E4, F16, 1, true>(a, nsm, s);
+    if (rows <= 16) return dec_one<DP, E4, F16, 2, true>(a, nsm, s);
+    // (e4m3 alone comes here with more rows)
+    if constexpr (E4) return dec_one<DP, E4, F16, 2, false>(a, nsm, s);
+    return cudaErrorInvalidValue;
 }
 
 template <int DP> cudaError_t dec_types(const AttnArgs& a, bool f16, bool e4m3, int nsm, cudaStream_t s) {
