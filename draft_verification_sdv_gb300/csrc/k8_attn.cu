@@ -11,15 +11,17 @@ constexpr int kMaxCtasPerSm = 2;
 // Query rows per kv head up to which k8_attn_dec.cu runs, in units of 16 rows;
 // above, k8_attn_tc.cu, whose time hardly depends on the rows up to 256.  Times
 // for 32 sequences of 4000 positions, 8 kv heads of 128: 16-bit caches, 16 rows
-// 101 and 124 us, 24 rows 178 and 129 us; e4m3 caches, which the second has to
-// widen in shared memory first, 48 rows 221 and 338 us, 64 rows 288 and 340, 80
-// rows 358 and 341.  (Heads of 64, 16 bits: 60 and 105 us, 32 rows 102 and 107,
-// 48 rows 139 and 108.)
-constexpr int kDecRows = 16, kDecRowsE4m3 = 64;
+// 100 and 120 us, 24 rows 178 and 121 us; e4m3 caches, which the second has to
+// widen in shared memory first, 48 rows 211 and 357 us, 80 rows 331 and 364, 128
+// rows 501 and 373.  (Heads of 64, 16 bits: 16 rows 59 and 106 us, 48 rows 139
+// and 107; e4m3: 80 rows 217 and 283 us, 128 rows 333 and 285.)
+constexpr int kDecRows = 16, kDecRowsE4m3 = 80;
 
 // out = sum_i 2^(L_i - L) out_i with L = log2 sum_i 2^(L_i), over the CTAs that
-// share a unit.  One column of the grid per CTA of the kernel before, most of
-// which find nothing to do.
+// share a unit, in the CTAs' order.  One column of the grid per CTA of the kernel
+// before, most of which find nothing to do; up to 16 blocks deep, so that the
+// round trips of a unit's parts are shared (2 chains of 177 nodes, 13 parts a
+// unit: 21 us in 16, 38 us in 8 that read twice; 32 gain nothing more).
 template <bool F16>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, int MT) {
     asm volatile("griddepcontrol.wait;" ::: "memory");

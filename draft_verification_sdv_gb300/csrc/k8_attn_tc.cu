@@ -7,7 +7,9 @@
 // the softmax of one stream runs, the tensor cores multiply for the other:
 //   S_s = Q_s K^T        operands in shared memory, accumulator in TMEM
 //   P_s = 2^(c S_s - m)  a thread per row takes its 128 scores into registers
-//                        and writes P_s, 16 bits wide, over S_s
+//                        and writes P_s over S_s, 16 bits wide as the products
+//                        want it (half a step of that type off, relative; the sum
+//                        of the row adds them up in fp32 as they were)
 //   O_s += P_s V         P_s from TMEM, V from shared memory, O_s in TMEM
 // TMEM holds S_0, S_1, O_0, O_1: 4 x 128 columns, all 512.  P could go through
 // shared memory, where a product takes 65 clocks instead of 100; but two
@@ -36,9 +38,12 @@
 // streams' tiles, a third of them the 2^x), P V (430) and S (640) and the waits
 // between them (440), 3740 clocks for two tiles where the products alone take
 // 2100.  16 trees of 513 nodes over 1500 to 3500 positions, 8 x 8 heads of 128:
-// 876 us, 760 TFLOP/s; 3 chunks of 1900 tokens, 8 x 4 heads of 64: 262 us.  e4m3
-// rows: 2700 clocks to widen a tile, which bounds units of one stream (338 us
-// against 139 us for 32 sequences of 4000 positions).
+// 840 us, 795 TFLOP/s; 3 chunks of 1900 tokens, 8 x 4 heads of 64: 239 us.  e4m3
+// rows: 2700 clocks and more to widen a tile (741 us against 290 us for 4 chains
+// of 513 nodes behind 4000 positions).  Seven warps for it have too few registers,
+// and rows that land beside their slots leave too few slots: both were slower.
+// Short units: some 11000 clocks from one to the next, of which the rows' way to
+// memory is 4000.
 //
 // Every wait is bounded: a wait that gives up marks the CTA dead, after which
 // no wait waits, no product is issued, and every row that is still written is
@@ -668,8 +673,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         };
         if (!E4 && w < kFirst)
             while (begin(true)) {}                   // nothing else to do
-        if (E4 && w == 0)
-            while (begin(false)) {}                  // the first tiles, before anything is waited for
 
         Unit u;
         uint32_t tiles = 0, step = 0, nq[2] = {0, 0};
@@ -757,7 +760,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                             // (the usual powers make no infinity)
                             bool usual = true;
 #pragma unroll
-                            for (int i = 0; i < kBatch; ++i) usual = usual && usual_power<F16>(e[i]) && !(check && has_nan(in[i]));
+                            for (int i = 0; i < kBatch; ++i) usual = usual && usual_power<F16>(e[i]);
+                            if (check)
+#pragma unroll
+                                for (int i = 0; i < kBatch; ++i) usual = usual && !has_nan(in[i]);
                             if (__all_sync(0xffffffffu, usual)) {
                                 // (no branch between the rows: their steps overlap)
 #pragma unroll
