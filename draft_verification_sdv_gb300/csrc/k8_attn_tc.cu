@@ -39,7 +39,7 @@
 // between them (440), 3740 clocks for two tiles where the products alone take
 // 2100.  16 trees of 513 nodes over 1500 to 3500 positions, 8 x 8 heads of 128:
 // 840 us, 795 TFLOP/s; 3 chunks of 1900 tokens, 8 x 4 heads of 64: 239 us.  e4m3
-// rows: 2700 clocks and more to widen a tile (741 us against 290 us for 4 chains
+// rows: 2700 clocks and more to widen a tile (671 us against 305 us for 4 chains
 // of 513 nodes behind 4000 positions).  Seven warps for it have too few registers,
 // and rows that land beside their slots leave too few slots: both were slower.
 // Short units: some 11000 clocks from one to the next, of which the rows' way to

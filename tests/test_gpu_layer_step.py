@@ -205,7 +205,7 @@ def test_layer_in_a_graph(cdtype):
 
 @pytest.mark.parametrize("dtype,cdtype", [(BF, BF), (HF, HF), (BF, F8), (HF, F8)])
 @pytest.mark.parametrize("D,P", [(128, 16), (64, 8), (128, 12), (160, 16)])
-@pytest.mark.parametrize("N,g", [(16, 1), (17, 1), (11, 3), (33, 1), (7, 7), (10, 5), (13, 5), (65, 1)])
+@pytest.mark.parametrize("N,g", [(16, 1), (17, 1), (11, 3), (33, 1), (7, 7), (10, 5), (13, 5), (65, 1), (16, 5), (27, 3)])
 def test_attn_row_counts(N, g, D, P, dtype, cdtype):
     case = _attn_case(2, N, 2 * g, 2, D, P, [150, 3], dtype, cdtype, seed=N * g)
     _check_attn(*case, [150, 3], count=[N, N - 1])
