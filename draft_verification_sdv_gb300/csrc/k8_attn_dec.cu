@@ -278,7 +278,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
                     const uint32_t who = __ballot_sync(0xffffffffu, bad);
                     if (who) {
                         const bool row_bad = (who >> (lane / LR * LR) & (LR == 32 ? ~0u : (1u << LR) - 1u)) != 0;
-                        if (row_bad) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v0 + chunk_of(r, c)), "r"(0) : "memory");
+                        if (row_bad) {
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v0 + chunk_of(r, c)), "r"(0) : "memory");
+                            fence_async();           // before the copy that takes the slot next
+                        }
 #pragma unroll
                         for (int i = 0; i < 32 / LR; ++i)
                             if (who >> (i * LR) & (LR == 32 ? ~0u : (1u << LR) - 1u)) flags |= 1u << (r0 + i);

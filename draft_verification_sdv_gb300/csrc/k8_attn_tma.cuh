@@ -58,6 +58,9 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, u
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
                  "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(row), "r"(page) : "memory");
 }
+// This thread's ordinary accesses to shared memory come before the copies (and
+// products) that a barrier after this lets begin.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 // One thread of a converged warp, and a value that is the same in all of them.
 __device__ __forceinline__ bool elected() {
