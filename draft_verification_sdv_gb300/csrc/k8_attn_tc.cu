@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     Walk<MT, BN> walk;
     walk.begin(a, part, mts);
     if (a.rounds > 0 && tid == 0) write_desc(a, part, walk);    // (its begins are in the ring)
+    fence_async();                                   // what the search kept there comes before the tiles
     __syncthreads();                                 // the ring may be used
 
     // the softmax warps hold a row of scores: they take registers that the others

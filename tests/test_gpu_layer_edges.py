@@ -33,7 +33,7 @@ def _words(see):
 # ---- shared memory that is used again ----
 
 @pytest.mark.parametrize("dtype,cdtype", [(BF, BF), (HF, HF), (BF, F8), (HF, F8)])
-@pytest.mark.parametrize("B,N,g,D", [(96, 12, 1, 128), (96, 8, 2, 64)])
+@pytest.mark.parametrize("B,N,g,D", [(96, 12, 1, 128), (96, 8, 2, 64), (96, 100, 2, 64), (40, 70, 4, 128)])
 def test_attn_values_kept_out_do_not_reach_later_tiles(B, N, g, D, dtype, cdtype):
     """Values that are not numbers are zeroed in the slots of the ring, which later
     tiles of the same CTA use: with them, the outputs are those without."""
