@@ -32,6 +32,7 @@ SDV_STATUS_BAD_LENGTH = 16
 SDV_STATUS_BAD_PAGE = 64
 SDV_ROPE_PLAIN, SDV_ROPE_LINEAR, SDV_ROPE_BASE, SDV_ROPE_PARTS = 0, 1, 2, 3
 SDV_HOOK_SAMPLE_NO_COPY = 1
+SDV_HOOK_ATTN_NO_COPY = 2
 
 # Every entry point of include/sdv.h, with its ctypes signature.
 _VP, _I, _I64, _U64, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
@@ -85,6 +86,7 @@ SIGNATURES = {
     "sdv_tree_attn_workspace": (ctypes.c_size_t, []),
     "sdv_tree_attn": (_I, [_KVP, _I, _I, _I, _I, _VP, _VP, _I64, _I64, _I64, _VP, _I, _VP, _VP, _VP,
                            _I64, _F, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
+    "sdv_set_attn_test_hooks": (_I, [ctypes.c_uint]),
     "sdv_logits_process": (_I, [_I, _I, _I, _I, _I, _VP, _VP, _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                 _I, _VP, _VP, _VP, _VP, _VP]),
     "sdv_counts_commit": (_I, [_I, _I, _I, _I] + [_VP] * 7),
@@ -835,6 +837,12 @@ def sdv_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     if st != SDV_OK:
         raise SdvError(st, "sdv_tree_attn")
     return (out, logs) if lse else out
+
+
+def sdv_set_attn_test_hooks(hooks: int) -> int:
+    """Fault-path test hooks of later sdv_tree_attn calls (SDV_HOOK_ATTN_NO_COPY
+    or 0)."""
+    return load().sdv_set_attn_test_hooks(int(hooks))
 
 
 def sdv_logits_process(logits: torch.Tensor, drafts: torch.Tensor,

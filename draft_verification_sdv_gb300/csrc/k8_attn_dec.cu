@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::bar);
     __shared__ int64_t s_part[40];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Sync sync{smem_u32(bars), smem_u32(smem + M::dead), a.status};
+    const Sync sync{smem_u32(bars), smem_u32(smem + M::dead), a.status, a.hooks ? kHookPolls : kPolls};
     if (tid == 0) {
         *reinterpret_cast<int*>(smem + M::dead) = 0;
         for (int i = 0; i < kStages; ++i) {
@@ -103,8 +103,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
                 page = npage, off = noff;
                 npage = page_at(t + 1, noff);
                 const uint32_t st = n % kStages;
-                ok = __all_sync(0xffffffffu, sync.wait(kStages + st, (n / kStages & 1) ^ 1));
+                ok = sync.wait(kStages + st, (n / kStages & 1) ^ 1) && !sync.is_dead();
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
+                if ((a.hooks & kHookAttnNoCopy) && blockIdx.x == 0 && n == 1) continue;     // a test: a tile that never comes
                 const bool good = page >= 0 && page < a.c.pages;
                 const uint32_t many = __popc(__ballot_sync(0xffffffffu, good));
                 const uint32_t dst = smem_u32(smem + st * 2 * kDecTile) + block * BN * 128 + copy * run_rows * 128;
@@ -118,8 +120,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
             }
         }
         // what is still under way lands before the CTA goes (a dead one's too)
-        for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
-            for (uint32_t p = 0; p < kPolls && !sync.poll(i % kStages, i / kStages & 1); ++p) {}
+        for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i) sync.landed(i % kStages, i / kStages & 1);
         return;
     }
 
@@ -462,12 +463,13 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
         }
 
         // ---- the unit's rows: the warps' outputs join one after another ----
+        const bool dead = !alive || sync.is_dead();
         float base[H];
 #pragma unroll
         for (int r = 0; r < H; ++r) {
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-            if (!alive) l[r] = __int_as_float(0x7fc00000);
+            if (dead) l[r] = __int_as_float(0x7fc00000);
             if (t4 == 0) s_m[warp * 16 + g4 + 8 * r] = m[r], s_l[warp * 16 + g4 + 8 * r] = l[r];
         }
         bar_sync(1, kAll);

@@ -10,10 +10,17 @@ namespace sdv {
 namespace {
 
 constexpr uint32_t kPolls = 1u << 17, kPollNs = 20000;     // a wait's limit: so many polls, each sleeping that long at most
+constexpr uint32_t kHookPolls = 1u << 12;                  // ... under the test hook
 
+// A wait that gives up marks its CTA dead.  From then on no wait waits and no
+// copy is begun.  Phases may then be out of step, so that a later wait finds its
+// phase over although nothing came: whatever is handed on is only good if the
+// CTA is not dead when it is written, which `is_dead` is asked then.  (The mark is
+// set before the arrivals that what was not waited for leads to.)
 struct Sync {
     uint32_t bar, dead;      // shared-memory addresses
     unsigned* status;
+    uint32_t polls;
     __device__ __forceinline__ bool is_dead() const {
         uint32_t d;
         asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(d) : "r"(dead) : "memory");
@@ -37,13 +44,17 @@ struct Sync {
     }
     // false: the CTA is dead
     __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
-        for (uint32_t n = 0; n < kPolls; ++n) {
+        for (uint32_t n = 0; n < polls; ++n) {
             if (poll(i, parity)) return true;
             if (is_dead()) return false;
         }
         asm volatile("st.volatile.shared.u32 [%0], 1;" ::"r"(dead) : "memory");
         if (status) atomicOr(status, kStatusTimeout);
         return false;
+    }
+    // The copies that complete phase `parity` have landed (or the limit is over).
+    __device__ __forceinline__ void landed(int i, uint32_t parity) const {
+        for (uint32_t n = 0; n < polls && !poll(i, parity); ++n) {}
     }
     __device__ __forceinline__ void arrive(int i) const {
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar + i * 8) : "memory");

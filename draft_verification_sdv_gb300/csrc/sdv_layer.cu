@@ -13,6 +13,7 @@ static_assert(SDV_BF16 == kTypeBf16 && SDV_F32 == kTypeF32 && SDV_F16 == kTypeF1
 static_assert(SDV_STATUS_BAD_TOKEN == kStatusBadDraft && SDV_STATUS_TIMEOUT == kStatusTimeout &&
                   SDV_STATUS_BAD_PAGE == kStatusBadPage && SDV_STATUS_BAD_LENGTH == kStatusBadLength,
               "public and kernel status bits must agree");
+static_assert(SDV_HOOK_ATTN_NO_COPY == kHookAttnNoCopy, "public test hooks and kernel hooks must agree");
 
 namespace {
 
@@ -25,6 +26,8 @@ template <int N> bool all_device(const void* const (&p)[N]) {
 bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
 sdv_status done(cudaError_t e) { return e == cudaSuccess ? SDV_OK : SDV_ERR_CUDA; }
+
+unsigned test_hooks = 0;      // sdv_set_attn_test_hooks
 
 cudaStream_t stream_of(void* s) { return static_cast<cudaStream_t>(s); }
 
@@ -281,6 +284,12 @@ sdv_status sdv_counts_commit(int B, int K, int gamma, int V, void* stream, const
     return done(launch_counts_commit(a, stream_of(stream)));
 }
 
+sdv_status sdv_set_attn_test_hooks(unsigned hooks) {
+    if (hooks & ~kHookAttnNoCopy) return SDV_ERR_ARG;
+    __atomic_store_n(&test_hooks, hooks, __ATOMIC_RELAXED);
+    return SDV_OK;
+}
+
 size_t sdv_tree_attn_workspace(void) {
     const int nsm = sm_count();
     return nsm > 0 ? attn_workspace_bytes(nsm) : 0;
@@ -313,6 +322,7 @@ sdv_status sdv_tree_attn(const sdv_kv_cache* cache, int B, int N, int Hq, sdv_dt
     a.status = reinterpret_cast<unsigned*>(status);
     a.B = B, a.N = N, a.Hq = Hq, a.W = (N + 31) / 32, a.max_pages = max_pages;
     a.scale_log2 = scale * 1.4426950408889634f;
+    a.hooks = __atomic_load_n(&test_hooks, __ATOMIC_RELAXED);
     return done(launch_tree_attn(a, dtype, cache->dtype == SDV_E4M3, workspace, nsm, stream_of(stream)));
 }
 

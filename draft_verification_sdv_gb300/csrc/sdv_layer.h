@@ -82,7 +82,11 @@ struct AttnArgs {
     int B, N, Hq, g, W, max_pages;
     float scale_log2;                 // scale * log2(e)
     int ctas, rounds;                 // see k8_attn.cuh
+    unsigned hooks;                   // kHook* bits (tests of the waits)
 };
+// The first CTA's second tile (its values) never comes, and waits give up soon:
+// nothing is in flight for the wait that runs out (the public SDV_HOOK_ATTN_NO_COPY).
+constexpr unsigned kHookAttnNoCopy = 2u;
 size_t attn_workspace_bytes(int nsm);
 cudaError_t launch_tree_attn(AttnArgs a, int type, bool e4m3, void* workspace, int nsm,
                              cudaStream_t s);

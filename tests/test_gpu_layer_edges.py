@@ -50,3 +50,45 @@ def test_attn_values_kept_out_do_not_reach_later_tiles(B, N, g, D, dtype, cdtype
         out.append(bd.sdv_tree_attn(q, kc, vc, table, _i32(ctx), mask=mask, k_exp=ke, v_exp=ve, lse=True))
     for o, lse in out[1:]:
         assert o.isfinite().all() and torch.equal(o, out[0][0]) and torch.equal(lse, out[0][1])
+
+
+# ---- waits that run out ----
+
+@pytest.mark.parametrize("dtype,cdtype", [(BF, BF), (HF, HF), (BF, F8), (HF, F8)])
+@pytest.mark.parametrize("B,N,g,D,ctx", [
+    (8, 1, 8, 128, 6000), (100, 2, 8, 64, 300), (8, 40, 4, 128, 6000), (8, 40, 3, 64, 6000), (100, 40, 4, 64, 300),
+    (40, 80, 8, 128, 200), (400, 2, 8, 64, 300), (400, 40, 4, 64, 300)])
+def test_attn_waits_that_run_out(B, N, g, D, ctx, dtype, cdtype):
+    """A tile of the first block never comes: nothing of what the block writes after
+    that is taken for a result, and the next call is right again."""
+    Hk, lens = 4, [ctx - b % 7 for b in range(B)]
+    case = _attn_case(B, N, Hk * g, Hk, D, 16, lens, dtype, cdtype, seed=N)
+    q, kc, vc, ke, ve, table = case
+    kw = dict(k_exp=ke, v_exp=ve, lse=True)
+    good, good_lse = bd.sdv_tree_attn(q, kc, vc, table, _i32(lens), **kw)
+    st = _status()
+    torch.cuda.synchronize()
+    assert bd.sdv_set_attn_test_hooks(bd.SDV_HOOK_ATTN_NO_COPY) == bd.SDV_OK
+    try:
+        out, lse = bd.sdv_tree_attn(q, kc, vc, table, _i32(lens), status=st, **kw)
+        torch.cuda.synchronize()
+    finally:
+        assert bd.sdv_set_attn_test_hooks(0) == bd.SDV_OK
+    assert int(st) == bd.SDV_STATUS_TIMEOUT
+    bad = out.isnan().all(-1)
+    assert torch.equal(bad, lse.isnan()) and torch.equal(bad, out.isnan().any(-1))
+    assert torch.equal(out[~bad], good[~bad]) and torch.equal(lse[~bad], good_lse[~bad])
+    rows = bad.view(B, N, Hk, g).transpose(1, 2).reshape(B * Hk, N * g)     # of each (sequence, head)
+    assert rows[0, :256].all() and not rows.all()
+    if N * g <= 256:                                            # a head's rows share their fate; later units too
+        units = rows.all(1)
+        assert torch.equal(rows.any(1), units)
+        n = int(units.sum())
+        assert units[:n].all() and (n > 1 or B < 300)
+    again, again_lse = bd.sdv_tree_attn(q, kc, vc, table, _i32(lens), status=_status(), **kw)
+    assert torch.equal(again, good) and torch.equal(again_lse, good_lse)
+
+
+def test_attn_hooks_refused():
+    assert bd.sdv_set_attn_test_hooks(1) == bd.SDV_ERR_ARG
+    assert bd.sdv_set_attn_test_hooks(4) == bd.SDV_ERR_ARG
