@@ -17,8 +17,12 @@
 // 128-byte swizzle neither has a bank conflict.  The rows' powers of two stay
 // out of the products: a key's multiplies its score; a value's is added to the
 // exponent, x' = x + e_v, with a running reference of x' for the outputs beside
-// the one of x for the sum, so that neither can overflow or vanish.  bf16
-// queries are brought to fp16 in units of a power of two per row.
+// the one of x for the sum, so that neither can overflow.  These weights of the
+// values have digits down to 2^-14, and some down to 2^-25; so the largest is kept
+// within 2^6 .. 2^14: a row of values up to 2^-20 of the largest in probability
+// times power counts with all its digits, one below 2^-31 not at all (with the
+// largest at 1, channels beside one of 65000 were off by 2^-9).  bf16 queries are
+// brought to fp16 in units of a power of two per row.
 //
 // 64 ragged sequences of up to 32000 positions, 8 kv heads of 128, e4m3: 453 us,
 // 5.3 TB/s (the widening and the products then take the warps' time); 32 of 4000,
@@ -33,6 +37,7 @@ namespace {
 constexpr int kDecWarps = 4, kDecThreads = 32 * (kDecWarps + 1);
 constexpr int kDecTile = 16 * 1024;          // of keys or of values
 constexpr float kDecSlack = 8.0f;            // how far (log2) scores may pass their reference
+constexpr float kDecUp = 14.0f - kDecSlack;  // e4m3: weights of values may reach 2^14
 
 // DP: head dimension's room, 64 or 128; H: halves of the 16 rows in use.
 template <int DP, bool E4> struct DecShape {
@@ -402,7 +407,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
 #pragma unroll
             for (int r = 0; r < H; ++r) {
                 sub[r] = m[r] == -INFINITY ? 0.0f : m[r];    // nothing seen yet: 2^-inf = 0
-                subv[r] = mv[r] == -INFINITY ? 0.0f : mv[r];
+                subv[r] = mv[r] == -INFINITY ? 0.0f : mv[r] - kDecUp;
             }
 
             // ---- probabilities (fp32 into the sum, 16 bits into the product) and outputs ----
@@ -480,7 +485,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
             for (int x = 0; x < kDecWarps; ++x) mx = fmaxf(mx, s_m[x * 16 + g4 + 8 * r]);
             base[r] = mx == -INFINITY ? 0.0f : mx;
             // in units of 2^base: o * 2^(mv - base)
-            const float up = mv[r] == -INFINITY ? 0.0f : ex2(mv[r] - base[r]);
+            const float up = mv[r] == -INFINITY ? 0.0f : ex2(mv[r] - (E4 ? kDecUp : 0.0f) - base[r]);
 #pragma unroll
             for (int i = 0; i < DP / 8; ++i) o[i][2 * r] *= up, o[i][2 * r + 1] *= up;
         }

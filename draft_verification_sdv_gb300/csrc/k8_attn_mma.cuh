@@ -22,8 +22,11 @@
 // share of four output columns, transposed by byte permutes.  The rows' powers
 // of two stay out of the products: a key's multiplies its score; a value's is
 // added to the exponent, x' = x + e_v, with a running maximum of x' for the
-// outputs beside the one of x for the sum, so that neither can overflow or
-// vanish.  bf16 queries are brought to fp16 in units of a power of two per row.
+// outputs beside the one of x for the sum, so that neither can overflow.  These
+// weights of the values have digits down to 2^-14, and some down to 2^-25, so the
+// largest so far is 2^14: a row of values up to 2^-28 of the largest in probability
+// times power counts with all its digits, one below 2^-39 not at all.  bf16 queries
+// are brought to fp16 in units of a power of two per row.
 #pragma once
 
 #include "k8_attn.cuh"
@@ -34,6 +37,7 @@ namespace {
 using namespace attn;
 
 constexpr int kThreads = 128;
+constexpr float kUp = 14.0f;             // e4m3: log2 of the largest weight of a value
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
@@ -429,7 +433,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
                     l[r] += e0 + e1;
                     if constexpr (E4) {
                         const float2 ev = *reinterpret_cast<const float2*>(s_ve + st * BN + wn * NW + i * 8 + 2 * t4);
-                        p[y] = pack2<true>(ex2(x0 + ev.x - subv[r]), ex2(x1 + ev.y - subv[r]));
+                        p[y] = pack2<true>(ex2(x0 + ev.x - (subv[r] - kUp)), ex2(x1 + ev.y - (subv[r] - kUp)));
                     } else {
                         p[y] = pack2<F16>(e0, e1);
                     }
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_kernel(const AttnArgs a) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             // the warp's own outputs in units of 2^m: o * 2^(mv - m)
-            const float up = E4 ? (m[r] == -INFINITY ? 0.0f : ex2(mv[r] - m[r])) : 1.0f;
+            const float up = E4 ? (m[r] == -INFINITY ? 0.0f : ex2(mv[r] - kUp - m[r])) : 1.0f;
             if (t4 == 0) s_m[warp][g4 + 8 * r] = m[r], s_l[warp][g4 + 8 * r] = l[r];
             float* dst = s_o + (warp * 16 + g4 + 8 * r) * DP;
 #pragma unroll

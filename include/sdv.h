@@ -653,7 +653,10 @@ sdv_status sdv_kv_commit(const sdv_kv_cache* cache, int B, int K, int gamma, voi
  *   workspace  device memory of at least sdv_tree_attn_workspace(...) bytes,
  *          32-byte aligned, that no other call uses until this one is done
  * Probabilities are rounded to 16 bits for their product with the values; all
- * sums are fp32.  What a node does not see has no influence on it, whatever it
+ * sums are fp32.  Over an e4m3 cache that product may be taken in fp16 of the
+ * probability times the value row's power of two: a row where this is below
+ * 2^-20 of the node's largest counts with fewer digits, below 2^-31 not at all.
+ * What a node does not see has no influence on it, whatever it
  * holds; a NaN or an infinity that it does see makes its output not finite
  * (which elements, and NaN or infinite, is not fixed).  A sequence whose
  * ctx_len, count or ctx_len + count is out of range gets NaN in out and lse;

@@ -92,3 +92,20 @@ def test_attn_waits_that_run_out(B, N, g, D, ctx, dtype, cdtype):
 def test_attn_hooks_refused():
     assert bd.sdv_set_attn_test_hooks(1) == bd.SDV_ERR_ARG
     assert bd.sdv_set_attn_test_hooks(4) == bd.SDV_ERR_ARG
+
+
+# ---- values of one channel that are far larger than the others ----
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("N,g,D,P", [(12, 1, 64, 16), (1, 8, 128, 16), (60, 1, 96, 8), (12, 1, 128, 12), (60, 1, 64, 4),
+                                     (9, 2, 192, 16)])
+def test_attn_channels_beside_a_large_one(N, g, D, P, dtype):
+    """Rows of e4m3 values in units of very different powers of two: what the small
+    ones add keeps its digits."""
+    B, Hk, ctx = 2, 2, [300, 40]
+    q, kc, vc, ke, ve, table = _attn_case(B, N, Hk * g, Hk, D, P, ctx, dtype, F8, seed=N + D)
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    k, v = (torch.randn((B, max(ctx) + N, Hk, D), generator=gen, device="cuda") for _ in range(2))
+    v[:, 9::50, :, 3] = -65000.0
+    bd.sdv_kv_write(k.to(dtype), v.to(dtype), kc, vc, table, _i32([0] * B), k_exp=ke, v_exp=ve)
+    _check_attn(q, kc, vc, ke, ve, table, ctx)
