@@ -93,17 +93,19 @@ size_t attn_workspace_bytes(int nsm) {
     // rows of up to 256 (two), which covers 16 rows of up to 128 (two)
     const size_t tc = size_t(1) * 256 * (128 + 1), mma = size_t(2) * 64 * (kCacheMaxDim + 1);
     const size_t most = tc > mma ? tc : mma;
-    return nsm * (kMaxCtasPerSm * 2 * sizeof(int4) + 2 * most * sizeof(float));
+    return nsm * (kMaxCtasPerSm * 2 * sizeof(int4) + 2 * most * sizeof(float) + sizeof(unsigned));
 }
 
 cudaError_t launch_tree_attn(AttnArgs a, int type, bool e4m3, void* workspace, int nsm, cudaStream_t s) {
     a.desc = static_cast<int4*>(workspace);
     a.part = reinterpret_cast<float*>(a.desc + 2 * kMaxCtasPerSm * nsm);
+    a.beyond = reinterpret_cast<unsigned*>(static_cast<unsigned char*>(workspace) + attn_workspace_bytes(nsm)) - nsm;
     const bool f16 = type == kTypeF16;
     const int rows = a.N * a.g;
     if (attn_tma_takes(a)) {
         if (rows <= (e4m3 ? kDecRowsE4m3 : kDecRows)) return launch_attn_dec(a, f16, e4m3, nsm, s);
-        return launch_attn_tc(a, f16, e4m3, nsm, s);
+        const cudaError_t e = launch_attn_tc(a, f16, e4m3, nsm, s);
+        return e == cudaSuccess && f16 && e4m3 ? launch_attn_redo(a, nsm, s) : e;
     }
     if (a.c.D <= 64) return launch_attn_mma64(a, f16, e4m3, rows, nsm, s);
     if (a.c.D <= 128) return launch_attn_mma128(a, f16, e4m3, rows, nsm, s);

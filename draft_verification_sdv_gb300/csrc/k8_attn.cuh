@@ -369,6 +369,11 @@ cudaError_t launch_attn_mma256(const AttnArgs& a, bool f16, bool e4m3, int rows,
 bool attn_tma_takes(const AttnArgs& a);
 cudaError_t launch_attn_dec(const AttnArgs& a, bool f16, bool e4m3, int nsm, cudaStream_t s);
 cudaError_t launch_attn_tc(const AttnArgs& a, bool f16, bool e4m3, int nsm, cudaStream_t s);
+// After launch_attn_tc with fp16 queries on an e4m3 cache: does the call again, in
+// units of 16 rows, if a block has met rows that fp16 does not hold (a.beyond);
+// otherwise its blocks end at once, 3 us later.  8 trees of 65 nodes behind 4000
+// positions, 8 x 8 heads of 128: 258 us, and 754 us with such a row in each.
+cudaError_t launch_attn_redo(const AttnArgs& a, int nsm, cudaStream_t s);
 // Joins the partial results of the kernel just launched with row tiles of MT.
 cudaError_t launch_attn_combine(const AttnArgs& a, bool f16, int MT, cudaStream_t s);
 

@@ -57,8 +57,9 @@ template <int DP, bool E4, int H> struct DecSmem {
     static constexpr int bytes = (dead + 4 + 15) / 16 * 16 + 1024;
 };
 
-// ONE: a kv head has one unit (16 rows at most).
-template <int DP, bool E4, bool F16, int H, bool ONE>
+// ONE: a kv head has one unit (16 rows at most).  REDO: launch_attn_redo; whole
+// units, dealt out in turn.
+template <int DP, bool E4, bool F16, int H, bool ONE, bool REDO>
 __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                                                                const __grid_constant__ CUtensorMap map_v, int run_rows) {
     using S = DecShape<DP, E4>;
@@ -80,10 +81,23 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
         }
     }
     const int mts = ONE ? 1 : (a.N * a.g + MT - 1) / MT;
-    const Part part = find_part<MT, BN, kDecThreads>(a, mts, s_part);     // holds barriers of the CTA
-    Walk<MT, BN> walk;
-    walk.begin(a, part, mts);
-    if (tid == 0) write_desc(a, part, walk);
+    Part part{};
+    Walk<MT, BN> walk{};
+    if constexpr (REDO) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        unsigned beyond = 0;
+        for (int i = tid; i < static_cast<int>(gridDim.x) / 2; i += kDecThreads) beyond |= a.beyond[i];
+        if (!__syncthreads_or(beyond != 0)) return;
+    } else {
+        part = find_part<MT, BN, kDecThreads>(a, mts, s_part);            // holds barriers of the CTA
+        walk.begin(a, part, mts);
+        if (tid == 0) write_desc(a, part, walk);
+    }
+    auto next_unit = [&](Walk<MT, BN>& w, Unit& u) {
+        if constexpr (REDO)
+            if (static_cast<int>(blockIdx.x) + w.round * a.ctas >= a.B * a.c.H * mts) return false;
+        return w.next(a, part, mts, u);
+    };
     Unit u;
     uint32_t n = 0;                                  // tiles so far
 
@@ -92,7 +106,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
         // a lane to each copy of a tile's keys or values (32 at most), in turn
         const int copies = BN / run_rows, copy = lane / NB, block = lane - copy * NB;
         bool ok = true;
-        while (ok && walk.next(a, part, mts, u)) {
+        while (ok && next_unit(walk, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
             const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
             int off = 0, noff = 0;
@@ -149,7 +163,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
     auto next = [&]() {
         Walk<MT, BN> w = s_walk[warp];
         __syncwarp();
-        const bool more = w.next(a, part, mts, u);
+        const bool more = next_unit(w, u);
         if (lane == 0) s_walk[warp] = w;
         __syncwarp();
         return more;
@@ -536,17 +550,30 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
     }
 }
 
-template <int DP, bool E4, bool F16, int H, bool ONE>
+template <int DP, bool E4, bool F16, int H, bool ONE, bool REDO = false>
 cudaError_t dec_one(AttnArgs a, int nsm, cudaStream_t s) {
     constexpr int bytes = DecSmem<DP, E4, H>::bytes, BN = DecShape<DP, E4>::BN;
     const int rows = min(a.c.P & -a.c.P, BN);        // of one copy: sure to lie in one page
     CUtensorMap k, v;
     if (!encode_cells(&k, a, a.c.k, E4, rows, true) || !encode_cells(&v, a, a.c.v, E4, rows, true)) return cudaErrorInvalidValue;
-    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_dec_kernel<DP, E4, F16, H, ONE>), bytes);
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_dec_kernel<DP, E4, F16, H, ONE, REDO>), bytes);
     if (e != cudaSuccess) return e;
     a.ctas = nsm * 2;
-    a.rounds = 0;
-    attn_dec_kernel<DP, E4, F16, H, ONE><<<static_cast<unsigned>(a.ctas), kDecThreads, bytes, s>>>(a, k, v, rows);
+    a.rounds = REDO ? 1 << 30 : 0;
+    if constexpr (REDO) {                            // its launch is on its way while the kernel before ends
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
+        cfg.blockDim = dim3(kDecThreads);
+        cfg.dynamicSmemBytes = bytes;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, attn_dec_kernel<DP, E4, F16, H, ONE, REDO>, a, k, v, rows);
+    }
+    attn_dec_kernel<DP, E4, F16, H, ONE, REDO><<<static_cast<unsigned>(a.ctas), kDecThreads, bytes, s>>>(a, k, v, rows);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_attn_combine(a, F16, 16, s);
 }
@@ -571,6 +598,10 @@ template <int DP> cudaError_t dec_types(const AttnArgs& a, bool f16, bool e4m3, 
 
 cudaError_t launch_attn_dec(const AttnArgs& a, bool f16, bool e4m3, int nsm, cudaStream_t s) {
     return a.c.D <= 64 ? dec_types<64>(a, f16, e4m3, nsm, s) : dec_types<128>(a, f16, e4m3, nsm, s);
+}
+
+cudaError_t launch_attn_redo(const AttnArgs& a, int nsm, cudaStream_t s) {
+    return a.c.D <= 64 ? dec_one<64, true, true, 2, false, true>(a, nsm, s) : dec_one<128, true, true, 2, false, true>(a, nsm, s);
 }
 
 }  // namespace sdv

@@ -32,7 +32,10 @@
 // some queries do not see (what is not a number there must not meet a zero
 // probability in a product).  e4m3 rows land as they are in the upper half of
 // their slot; then warp 8 brings both, and all three hand over, after widening
-// the rows in place to the queries' type, times their power of two.
+// the rows in place to the queries' type, times their power of two.  bf16 holds that
+// as it is; fp16 does not where a power is far from 1.  A block that meets such a
+// row says so, and launch_attn_redo then takes the call's place, with the powers
+// outside the products.
 //
 // What bounds it: the chain of one stream's step, softmax (2230 clocks for two
 // streams' tiles, a third of them the 2^x), P V (430) and S (640) and the waits
@@ -78,8 +81,8 @@ struct Smem {
     static constexpr int exps = q + 2 * kTile;                  // bytes [3 tiles][keys, values][BN] (e4m3)
     static constexpr int flag = exps + 6 * BN;                  // uint32 [4 tiles][3 warps][4] values that are not numbers
     static constexpr int bar = flag + 4 * kLoadWarps * 4 * 4;
-    static constexpr int word = bar + 20 * 8;                   // TMEM address, dead
-    static constexpr int state = word + 8;                      // SoftmaxState [8 warps]
+    static constexpr int word = bar + 20 * 8;                   // TMEM address, dead, rows that fp16 does not hold
+    static constexpr int state = word + 16;                     // SoftmaxState [8 warps]
     static constexpr int bytes = state + 8 * static_cast<int>(sizeof(SoftmaxState)) + 1024;
 };
 static_assert(Smem::bytes <= 227 * 1024, "one CTA per SM");
@@ -237,8 +240,9 @@ __device__ __noinline__ bool sees_bad_page(const int32_t* table, int pages, int 
     return bad;
 }
 
-// Sixteen e4m3 cells times 2^(e - 127), in the queries' type.
-template <bool F16> __device__ __forceinline__ void widen16(const uint4& raw, int e, uint32_t (&o)[8]) {
+// Sixteen e4m3 cells times 2^(e - 127), in the queries' type; `beyond` is set where
+// that is fp16, which does not hold them as they are.
+template <bool F16> __device__ __forceinline__ void widen16(const uint4& raw, int e, uint32_t (&o)[8], bool& beyond) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     // a cell that is not a number takes its chunk with it
     uint32_t bad = 0;
@@ -248,19 +252,28 @@ template <bool F16> __device__ __forceinline__ void widen16(const uint4& raw, in
     if constexpr (F16) {
         // 2^(e - 127) as the product of two fp16 powers (its range is smaller)
         int h = e - 127;
-        h = h < -40 ? -40 : h > 24 ? 24 : h;
+        // (beyond 2^30 every cell but zero is infinite, below 2^-34 none is left)
+        h = h < -34 ? -34 : h > 30 ? 30 : h;
         const int h1 = h / 2, h2 = h - h1;
         uint32_t s1 = static_cast<uint32_t>(h1 + 15) << 10, s2 = static_cast<uint32_t>(h2 + 15) << 10;
         if (h1 < -14) s1 = 0x0400u >> (-14 - h1);
         if (h2 < -14) s2 = 0x0400u >> (-14 - h2);
         if (e == 255) s1 = 0x7e00u;
         s1 |= s1 << 16, s2 |= s2 << 16;
+        // the way back (to 2^15 a step) gives the cells, unless digits went missing
+        const uint32_t r1 = (h1 < -15 ? 30u : 15u - h1) << 10, r2 = (h2 < -15 ? 30u : 15u - h2) << 10;
+        uint32_t off = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 t;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 t, lo;\n\t"
-                "mul.rn.f16x2 t, t, %2;\n\tmul.rn.f16x2 %0, t, %3;\n\t}"
-                : "=r"(o[i]) : "r"(w[i / 2] >> (16 * (i % 2))), "r"(s1), "r"(s2));
+            uint32_t lost;
+            asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 t, u;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 t, lo;\n\t"
+                "mul.rn.f16x2 u, t, %3;\n\tmul.rn.f16x2 %0, u, %4;\n\t"
+                "mul.rn.f16x2 u, %0, %5;\n\tmul.rn.f16x2 u, u, %6;\n\txor.b32 %1, t, u;\n\t}"
+                : "=&r"(o[i]), "=r"(lost)
+                : "r"(w[i / 2] >> (16 * (i % 2))), "r"(s1), "r"(s2), "r"(r1 | r1 << 16), "r"(r2 | r2 << 16));
+            off |= lost;
         }
+        beyond |= e != 255 && off != 0;
     } else {
         // the cell's exponent and digits in bf16's places are its value times 2^-120
         uint32_t s = e == 255 ? 0x7fc0u : e == 0 ? 0x0040u : static_cast<uint32_t>(e) << 7;
@@ -346,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const int D = a.c.D;
     const Sync sync{smem_u32(bars), smem_u32(smem + M::word + 4), a.status, a.hooks ? kHookPolls : kPolls};
     if (tid == 0) {
-        s_tmem[1] = 0;                               // dead
+        s_tmem[1] = s_tmem[2] = 0;                   // not dead, no such row
         for (int i = 0; i < 4 * kLoadWarps * 4; ++i) s_flag[i] = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(bars + kQFull + i, BOXES ? 1 : kRows / 32);
@@ -788,7 +801,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                             if (q >= BN / RP) break;
                             uint32_t o[8];
                             if constexpr (E4) {
-                                widen16<F16>(in[i], e[i], o);
+                                bool beyond = false;
+                                widen16<F16>(in[i], e[i], o, beyond);
+                                if (F16 && beyond) s_tmem[2] = 1;
                             } else {
                                 o[0] = in[i].x, o[1] = in[i].y, o[2] = in[i].z, o[3] = in[i].w;
                             }
@@ -934,6 +949,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     __syncwarp();
     fence_before();
     __syncthreads();
+    if constexpr (E4 && F16)
+        if (tid == 0) a.beyond[blockIdx.x] = s_tmem[2];
     if (warp == 11) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");

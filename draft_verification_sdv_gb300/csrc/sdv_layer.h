@@ -79,6 +79,7 @@ struct AttnArgs {
     unsigned* status;
     float* part;                      // partial outputs (see part_rows)
     int4* desc;                       // two per CTA: the unit that its start splits
+    unsigned* beyond;                 // one per SM: see launch_attn_redo
     int B, N, Hq, g, W, max_pages;
     float scale_log2;                 // scale * log2(e)
     int ctas, rounds;                 // see k8_attn.cuh

@@ -565,7 +565,8 @@ sdv_status sdv_rope(int64_t T, int Hq, int Hk, int D, int R, int interleaved, sd
  * of a power of two of its own, 2^(exp - 127), with exp in k_exp / v_exp,
  * uint8 [pages][kv_heads][page_size], exp_page_stride after one another
  * (a row holds the smallest power, no less than 2^-126, that brings its
- * largest magnitude to at most 448; exp 255: the row is not a number).
+ * largest magnitude to at most 448; exp 255: the row is not a number).  A
+ * magnitude of 2^128 - 2^123 and more rounds to 2^128, which may count as infinite.
  * head_dim is a multiple of 16, at most 256; page_size >= 1.
  */
 typedef struct sdv_kv_cache {

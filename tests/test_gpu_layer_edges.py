@@ -109,3 +109,51 @@ def test_attn_channels_beside_a_large_one(N, g, D, P, dtype):
     v[:, 9::50, :, 3] = -65000.0
     bd.sdv_kv_write(k.to(dtype), v.to(dtype), kc, vc, table, _i32([0] * B), k_exp=ke, v_exp=ve)
     _check_attn(q, kc, vc, ke, ve, table, ctx)
+
+
+# ---- powers of two of e4m3 rows that fp16 does not hold ----
+
+@pytest.mark.parametrize("kind", ["large keys", "large values", "tiny keys", "top of fp16"])
+@pytest.mark.parametrize("N,g,D,P", [(12, 1, 64, 16), (100, 1, 128, 16), (34, 3, 64, 8), (100, 1, 96, 12), (150, 2, 128, 32)])
+def test_attn_fp16_queries_on_rows_beyond_fp16(N, g, D, P, kind):
+    """An e4m3 row stands for more than fp16 holds: whatever the number of query
+    rows, and so the kernel, finite rows give the finite answer."""
+    B, Hk, ctx = 2, 2, [300, 40]
+    write = HF if kind == "top of fp16" else BF
+    q, kc, vc, ke, ve, table = _attn_case(B, N, Hk * g, Hk, D, P, ctx, write, F8, seed=N + D)
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    k, v = (torch.randn((B, max(ctx) + N, Hk, D), generator=gen, device="cuda") for _ in range(2))
+    q, scale = q.to(HF), D ** -0.5
+    if kind == "large keys":                     # in a channel that the queries leave alone
+        k[:, 7::31, :, 0] = 3.0e5
+        q[..., 0] = 0.0
+    elif kind == "large values":
+        v[:, 5::61] *= 1.0e5
+        v[:, 41] *= 1.0e30
+        k[:, 41, :, 0], q[..., 0] = -1000.0, 16.0    # ... of a probability that is 0 even against that
+    elif kind == "tiny keys":
+        k *= 2.0 ** -18
+        q, scale = q * 2.0 ** 12, 16.0 * 8 / D ** 0.5
+    else:
+        k[:, 7::31, :, 0] = 65000.0
+        q[..., 0] = 0.0
+        v[:, 9::50, :, 3] = -65000.0
+    bd.sdv_kv_write(k.to(write), v.to(write), kc, vc, table, _i32([0] * B), k_exp=ke, v_exp=ve)
+    st = _status()
+    out, lse = bd.sdv_tree_attn(q, kc, vc, table, _i32(ctx), scale=scale, k_exp=ke, v_exp=ve, lse=True, status=st)
+    assert int(st) == 0
+    v0 = vc.cpu()
+    if kind == "large values":                   # the reference without what has no weight
+        for row in table.cpu():
+            v0.view(torch.uint8)[row[41 // P], :, 41 % P] = 0
+    want, wl, tol, tl = ref.attn(q.cpu(), kc.cpu(), v0, table.cpu(), ctx, None, None, scale, ke.cpu(), ve.cpu())
+    got, top = out.double().cpu(), 65504.0
+    over = want.abs() > top + tol                # more than fp16 holds: infinite, of its sign
+    assert torch.equal(got[over], want[over].sign() * math.inf) and not got.isnan().any()
+    fin = want.abs() < top - tol
+    assert ((got - want).abs()[fin] <= tol[fin]).all(), float(((got - want).abs()[fin] / tol[fin]).max())
+    assert fin.sum() > 0.9 * fin.numel() and ((lse.double().cpu() - wl).abs() <= tl).all()
+    # and from one call to the next: rows that fp16 holds again
+    one = torch.randn(k.shape, generator=gen, device="cuda").to(write)
+    bd.sdv_kv_write(one, one, kc, vc, table, _i32([0] * B), k_exp=ke, v_exp=ve)
+    _check_attn(q if kind != "tiny keys" else q * 2.0 ** -12, kc, vc, ke, ve, table, ctx)
