@@ -537,7 +537,8 @@ class Verifier:
 #
 # These run once per layer and step, so the checks here read what torch holds
 # and build no intermediate objects; whether a pointer is on the device is
-# checked by the library.
+# checked by the library.  With a `stream` of its own a call is ordered there: the
+# caller orders what it reads before it and what reads its outputs after it.
 # --------------------------------------------------------------------------
 
 _HALF_TYPES = {torch.bfloat16: SDV_BF16, torch.float16: SDV_F16}
@@ -578,6 +579,24 @@ def _stream_of(t: torch.Tensor, stream) -> int:
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(t.device.index)
     return _stream_handle(stream)
+
+
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """torch.empty for a call on `stream` (None: the current one).  Memory comes
+    from the pool of the stream that writes it: a block of the current stream's
+    may still be in use there.  And it goes back only when the current stream,
+    where the caller reads it, is done with it too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) else \
+            torch.cuda.default_stream(device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if stream != here:
+        t.record_stream(here)
+    return t
 
 
 def _type_of(types: dict, dtype: torch.dtype, name: str) -> int:
@@ -639,7 +658,7 @@ def sdv_tree_build(root: torch.Tensor, drafts: torch.Tensor,
     shapes = {"tokens": (B, N), "depth": (B, N), "mask": (B, N, W), "nodes": (B, K, G),
               "rows": (B, K, G + 1), "count": (B,)}
     if out is None:
-        out = {n: torch.empty(s, dtype=torch.int32, device=drafts.device) for n, s in shapes.items()}
+        out = {n: _empty(s, torch.int32, drafts.device, stream) for n, s in shapes.items()}
     at = []
     for n, s in shapes.items():
         size = 1
@@ -681,7 +700,7 @@ def sdv_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor
     (T, Hq, D), qs = _rows_of(q, 3, "q")
     code = _type_of(_ROPE_TYPES, q.dtype, "q")
     if out_q is None:
-        out_q = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        out_q = _empty((T, Hq, D), q.dtype, q.device, stream)
         os_ = (Hq * D, D)
     else:
         oshape, os_ = _rows_of(out_q, 3, "out_q")
@@ -694,7 +713,7 @@ def sdv_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor
         if kshape[0] != T or kshape[2] != D or k.dtype != q.dtype:
             raise ValueError("k must be [%d, Hk, %d] of q's type" % (T, D))
         if out_k is None:
-            out_k = torch.empty(kshape, dtype=k.dtype, device=k.device)
+            out_k = _empty(kshape, k.dtype, k.device, stream)
             oks = (Hk * D, D)
         else:
             okshape, oks = _rows_of(out_k, 3, "out_k")
@@ -750,7 +769,7 @@ def sdv_kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch
         dtype = torch.bfloat16 if cache.dtype == SDV_E4M3 else k_cache.dtype
     code = _type_of(_HALF_TYPES, dtype, "dtype")
     B = start.numel()
-    out = torch.empty((2, B, N, cache.kv_heads, cache.head_dim), dtype=dtype, device=k_cache.device)
+    out = _empty((2, B, N, cache.kv_heads, cache.head_dim), dtype, k_cache.device, stream)
     st = load().sdv_kv_read(cache, B, N, code, _stream_of(k_cache, stream), out[0].data_ptr(),
                             out[1].data_ptr(), _table_of(block_table, B), block_table.shape[1],
                             _array(start, B, torch.int32, "start"),
@@ -771,7 +790,7 @@ def sdv_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: tor
     cache = _cache_of(k_cache, v_cache, k_exp, v_exp)
     B, K, G = nodes.shape
     if out_len is None:
-        out_len = torch.empty(B, dtype=torch.int32, device=nodes.device)
+        out_len = _empty((B,), torch.int32, nodes.device, stream)
     st = load().sdv_kv_commit(cache, B, K, G, _stream_of(k_cache, stream), _table_of(block_table, B),
                               block_table.shape[1], _array(start, B, torch.int32, "start"),
                               _array(nodes, B * K * G, torch.int32, "nodes"),
@@ -796,8 +815,8 @@ def sdv_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     chain), whose keys and values are at positions ctx_len[b] + node.  scale
     defaults to 1 / sqrt(D).  Returns out [B, N, Hq, D], and with `lse` also the
     log-sum-exp [B, N, Hq].  `workspace` (uint8, sdv_tree_attn_workspace()
-    bytes) may be passed to reuse one; by default it is taken from torch's
-    allocator for the call."""
+    bytes, some 40 MB) may be passed to reuse one; by default it is taken from
+    torch's allocator for the call."""
     cache = _cache_of(k_cache, v_cache, k_exp, v_exp)
     (B, N, Hq, D), qs = _rows_of(q, 4, "q")
     code = _type_of(_HALF_TYPES, q.dtype, "q")
@@ -813,17 +832,11 @@ def sdv_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         mask_sb = N * W if len(shape) == 3 else 0
     out_p = _array(out, B * N * Hq * D, q.dtype, "out")
     if out is None:
-        out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
+        out = _empty((B, N, Hq, D), q.dtype, q.device, stream)
         out_p = out.data_ptr()
-    logs = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device) if lse else None
-    ws_bytes = lib.sdv_tree_attn_workspace() if workspace is None else 0
+    logs = _empty((B, N, Hq), torch.float32, q.device, stream) if lse else None
     if workspace is None:
-        if stream is None:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-        else:       # the allocator hands memory out again in its stream's order
-            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-            with torch.cuda.stream(s):
-                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        workspace = _empty((lib.sdv_tree_attn_workspace(),), torch.uint8, q.device, stream)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous uint8")
     st = lib.sdv_tree_attn(
@@ -876,7 +889,7 @@ def sdv_logits_process(logits: torch.Tensor, drafts: torch.Tensor,
         nsrc = logits.shape[1]
     M = 0 if bias_ids is None else bias_ids.numel() // B
     if out is None:
-        out = torch.empty((B, K, G + 1, V), dtype=logits.dtype, device=logits.device)
+        out = _empty((B, K, G + 1, V), logits.dtype, logits.device, stream)
     i32, f32 = torch.int32, torch.float32
     st = load().sdv_logits_process(
         B, K, G, V, code, _stream_of(logits, stream), _array(logits, logits.numel(), logits.dtype, "logits"),

@@ -157,3 +157,67 @@ def test_attn_fp16_queries_on_rows_beyond_fp16(N, g, D, P, kind):
     one = torch.randn(k.shape, generator=gen, device="cuda").to(write)
     bd.sdv_kv_write(one, one, kc, vc, table, _i32([0] * B), k_exp=ke, v_exp=ve)
     _check_attn(q if kind != "tiny keys" else q * 2.0 ** -12, kc, vc, ke, ve, table, ctx)
+
+
+# ---- outputs of calls on a named stream ----
+
+def _calls():
+    """Each call that makes its own outputs, as a function of the stream."""
+    B, K, G, Hq, Hk, D, V, P = 3, 2, 6, 8, 2, 64, 1000, 16
+    drafts, root = _i32([[[1] * G, [2] * G]] * B), _i32([1, 2, 3])
+    kc, vc, _, _ = _cache(40, Hk, P, D, BF)
+    table, start = _tables(B, 12, 40, 1), _i32([0, 50, 130])
+    q, k = torch.randn((30, Hq, D), device="cuda").to(BF), torch.randn((30, Hk, D), device="cuda").to(BF)
+    pos, (freq, factor) = torch.arange(30, dtype=torch.int32, device="cuda"), bd.sdv_rope_freqs(D)
+    tree = bd.sdv_tree_build(root, drafts)
+    logits = torch.randn((B, K, G + 1, V), device="cuda")
+    qt = torch.randn((B, 1 + K * G, Hq, D), device="cuda").to(BF)
+    sel = _i32([0, 1, 0])
+    torch.cuda.synchronize()
+    return {
+        "tree": lambda s: list(bd.sdv_tree_build(root, drafts, stream=s).values()),
+        "rope": lambda s: list(bd.sdv_rope(q, k, pos, freq, factor, stream=s)),
+        "read": lambda s: list(bd.sdv_kv_read(kc, vc, table, start, 20, stream=s)),
+        "commit": lambda s: [bd.sdv_kv_commit(kc, vc, table, start, tree["nodes"], sel, sel, stream=s)],
+        "attn": lambda s: list(bd.sdv_tree_attn(qt, kc, vc, table, start, mask=tree["mask"], lse=True, stream=s)),
+        "logits": lambda s: [bd.sdv_logits_process(logits, drafts, stream=s)],
+    }
+
+
+def _wait():
+    torch.cuda._sleep(200_000_000)          # about 0.1 s on the current stream
+
+
+@pytest.mark.parametrize("named", ["object", "handle", "default"])
+@pytest.mark.parametrize("name", ["tree", "rope", "read", "commit", "attn", "logits"])
+def test_outputs_on_a_named_stream(name, named):
+    """Neither is a block that the current stream still uses written by the call's
+    stream, nor one of the call's handed out again while the current stream reads it."""
+    call = _calls()[name]
+    side = torch.cuda.Stream()
+    stream = {"object": side, "handle": side.cuda_stream, "default": 0}[named]
+    here = torch.cuda.current_stream() if named != "default" else torch.cuda.Stream()
+    want = [x.clone() for x in call(None)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(here):
+        blocks = [torch.full_like(x, 7) for x in want for _ in range(3)]
+        _wait()
+        copies = [x.clone() for x in blocks]        # still to come when the blocks go
+        used = {x.untyped_storage().data_ptr() for x in blocks}
+        del blocks
+        out = call(stream)
+        assert not used & {x.untyped_storage().data_ptr() for x in out}
+        torch.cuda.synchronize()
+        assert all((x == 7).all() for x in copies)
+        for x, y in zip(out, want):
+            assert torch.equal(x, y)
+        _wait()
+        reads = [x.clone() for x in out]            # the caller's reads, on its stream
+        used = {x.untyped_storage().data_ptr() for x in out}
+        x = y = None
+        del out
+        again = call(stream)
+        assert not used & {x.untyped_storage().data_ptr() for x in again}
+        torch.cuda.synchronize()
+        for x, y in zip(reads, want):
+            assert torch.equal(x, y)
