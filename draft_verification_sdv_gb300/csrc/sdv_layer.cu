@@ -17,9 +17,22 @@ static_assert(SDV_HOOK_ATTN_NO_COPY == kHookAttnNoCopy, "public test hooks and k
 
 namespace {
 
+// Whether each is NULL or memory of the current device, which the call runs on.
 template <int N> bool all_device(const void* const (&p)[N]) {
-    for (const void* x : p)
-        if (x && !is_device_ptr(x)) return false;
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    for (const void* x : p) {
+        cudaPointerAttributes at;
+        if (!x) continue;
+        if (cudaPointerGetAttributes(&at, x) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        if (!memory_of(at, device)) return false;
+    }
     return true;
 }
 

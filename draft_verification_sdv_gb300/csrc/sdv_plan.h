@@ -243,6 +243,12 @@ cudaError_t setup_sample(size_t smem);
 // a larger shape.  Thread-safe (one lock around the per-device record).
 cudaError_t raise_smem_limit(const void* func, size_t bytes);
 
+// Whether memory with these attributes is the device's own (or managed): another
+// device's address is no address here.
+inline bool memory_of(const cudaPointerAttributes& at, int device) {
+    return (at.type == cudaMemoryTypeDevice && at.device == device) || at.type == cudaMemoryTypeManaged;
+}
+
 // True when `p` is device (or managed) memory of some device.
 inline bool is_device_ptr(const void* p) {
     cudaPointerAttributes at;

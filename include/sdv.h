@@ -468,7 +468,8 @@ sdv_status sdv_verify_static(int B, int K, int gamma, int V, sdv_dtype dtype, vo
  * below are this library's.
  *
  * All entry points here are stateless: they check their arguments on the host
- * (SDV_ERR_ARG: nothing was enqueued), allocate nothing, only enqueue on
+ * (SDV_ERR_ARG: nothing was enqueued; pointers that are not memory of the
+ * current device among them), allocate nothing, only enqueue on
  * `stream`, and can be captured into a CUDA graph (after one uncaptured call of
  * each shape).  Strides are in elements, and the innermost one is 1.  Data
  * errors that only the device can see (a page id outside the cache, a length
