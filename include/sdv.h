@@ -659,8 +659,11 @@ sdv_status sdv_kv_commit(const sdv_kv_cache* cache, int B, int K, int gamma, voi
  * probability times the value row's power of two: a row where this is below
  * 2^-20 of the node's largest counts with fewer digits, below 2^-31 not at all.
  * What a node does not see has no influence on it, whatever it
- * holds; a NaN or an infinity that it does see makes its output not finite
- * (which elements, and NaN or infinite, is not fixed).  A sequence whose
+ * holds.  A NaN, an infinite value and a score of +infinity that it does see make
+ * its output not finite (which elements, and NaN or infinite, is not fixed).  A
+ * score of -infinity (an infinite key in a 16-bit cache; an e4m3 row with an
+ * infinity is not a number) has weight 0, and a node that sees no other score has
+ * out = 0, lse = -inf as if it saw nothing.  A sequence whose
  * ctx_len, count or ctx_len + count is out of range gets NaN in out and lse;
  * the cells of a bad page count as not a number; both set the status bits of
  * sdv_kv_write.

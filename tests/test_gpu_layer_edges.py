@@ -221,3 +221,35 @@ def test_outputs_on_a_named_stream(name, named):
         torch.cuda.synchronize()
         for x, y in zip(reads, want):
             assert torch.equal(x, y)
+
+
+# ---- infinite keys ----
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("N,g,D,P", [(1, 8, 128, 16), (12, 1, 64, 16), (40, 4, 64, 16), (60, 3, 128, 16), (12, 1, 64, 12),
+                                     (60, 1, 192, 16)])
+def test_attn_infinite_keys(N, g, D, P, dtype):
+    """A score of -infinity has weight 0, +infinity is not a number, and nodes whose
+    scores are all -infinity have nothing."""
+    Hk, ctx = 2, [200]
+    q, kc, vc, ke, ve, table = _attn_case(1, N, Hk * g, Hk, D, P, ctx, dtype, dtype, seed=N)
+    q = q.clone()
+    q[..., 0] = 2.0
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    k = torch.randn((1, ctx[0] + N, Hk, D), generator=gen, device="cuda").to(dtype)
+    at = torch.zeros(ctx[0] + N, dtype=torch.bool)
+    at[3::17] = True
+    at[ctx[0]] = False                          # (the first node sees itself)
+
+    def run(fill, where):
+        kk = k.clone()
+        kk[0, where, :, 0] = fill
+        bd.sdv_kv_write(kk, k.flip(1), kc, vc, table, _i32([0]))
+        return bd.sdv_tree_attn(q, kc, vc, table, _i32(ctx), lse=True)
+
+    want, got = run(-6.0e4, at), run(-math.inf, at)
+    assert want[0].isfinite().all() and torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    out, lse = run(math.inf, at)
+    assert not out.isfinite().all(-1).any()
+    none, lse = run(-math.inf, torch.ones_like(at))
+    assert not none.any() and (lse == -math.inf).all()
