@@ -700,7 +700,8 @@ sdv_status sdv_set_attn_test_hooks(unsigned hooks);
  *                                                       the prompt
  *   x = x - frequency[b] * c - presence[b] * [c > 0] + sum of v's biases
  *   x = -inf                                            where v is not allowed
- * rounded once to the logits' type.
+ * rounded once to the logits' type.  (For bf16 logits the quotient may be the
+ * product with the rounded reciprocal: one rounding of fp32 more.)
  *   logits     device [B][K][gamma + 1][V], or with `rows`
  *              [B][nsrc][V] (a tree's logits), 16-byte aligned
  *   rows       device int32 [B][K][gamma + 1] source row within the sequence's

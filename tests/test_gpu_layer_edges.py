@@ -253,3 +253,29 @@ def test_attn_infinite_keys(N, g, D, P, dtype):
     assert not out.isfinite().all(-1).any()
     none, lse = run(-math.inf, torch.ones_like(at))
     assert not none.any() and (lse == -math.inf).all()
+
+
+# ---- sampling parameters ----
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_logits_repetition_is_a_quotient(dtype):
+    """x / repetition, rounded once (bf16: from a quotient two roundings of fp32 off at
+    most), for factors whose reciprocal is rounded, infinite or next to zero too."""
+    reps = [1.3, 3.0, 0.7, 1.0e-39, 3.0e38, 49.0]
+    B, V = len(reps), 4096
+    gen = torch.Generator().manual_seed(2)
+    x = torch.randn((B, 1, 2, V), generator=gen) * torch.exp2(torch.randint(-60, 20, (B, 1, 2, V), generator=gen).float())
+    x, rep = x.to(dtype), torch.tensor(reps)
+    counts = torch.ones((B, V), dtype=torch.int32, device="cuda")
+    drafts = torch.zeros((B, 1, 1), dtype=torch.int32, device="cuda")
+    out = bd.sdv_logits_process(x.cuda(), drafts, counts=counts, repetition=rep.cuda()).cpu()
+    r = rep.view(B, 1, 1, 1).double()
+    want = torch.where(x > 0, x.double() / r, x.double() * r)
+    if dtype == F32:
+        assert torch.equal(out, want.float())
+        return
+    over = want.abs() > 3.395e38                                # past bf16's largest by half a step
+    assert torch.equal(out[over], (want[over].sign() * math.inf).to(BF))
+    fin = want.abs() < 3.38e38
+    tol = (2.0 ** -8 + 2.0 ** -22) * want.abs() + 2.0 ** -133
+    assert ((out.double() - want).abs()[fin] <= tol[fin]).all()
