@@ -3,9 +3,11 @@
 // Pair i of token t turns by pos_t * f_i.  In fp32 that product loses the
 // angle at far positions, and fp64 is slow here, so the angle is kept as a
 // 64-bit fraction of a turn: F_i = f_i / 2 pi mod 1 in units of 2^-64, and
-// pos * F mod 2^64 is the angle's fraction exactly (integer products wrap by
-// themselves).  F comes from one fp64 product per pair and thread; sine and
-// cosine are taken of the top 32 bits.
+// pos * F mod 2^64 is the angle's fraction (integer products wrap by themselves),
+// off by pos units at most: 2^-33 of a turn.  F needs more digits than one fp64
+// product has (2^-55 of a turn off, times 2^31), so it is the sum of a product, of
+// what that lost (one fma) and of f times the next digits of 1 / 2 pi.  Sine and
+// cosine are taken of the top 32 bits, rounded to fp32: 2^-26 of a turn.
 //
 // Bound by HBM: every element is read and written once.  A CTA takes a few
 // tokens at a time, computes their R / 2 sines and cosines once for all heads
@@ -49,9 +51,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
         const int nt = static_cast<int>(a.T - t0 < kTokens ? a.T - t0 : kTokens);
         for (int i = threadIdx.x; i < half; i += kThreads) {
             const float f = a.freq[i];
-            double turns = static_cast<double>(f) * 0.15915494309189533577;     // 1 / (2 pi)
-            turns -= floor(turns);
-            const unsigned long long F = __double2ull_rn(turns * 18446744073709551616.0);
+            constexpr double kInv = 0.15915494309189535, kInvLow = -9.839338337591243e-18;   // 1 / (2 pi)
+            constexpr double kUnits = 18446744073709551616.0;
+            const double d = f, turns = d * kInv, low = fma(d, kInv, -turns) + d * kInvLow;
+            const unsigned long long F = static_cast<unsigned long long>(__double2ll_rn((turns - rint(turns)) * kUnits)) +
+                                         static_cast<unsigned long long>(__double2ll_rn(low * kUnits));
             for (int t = 0; t < nt; ++t) {
                 const long long p = a.pos[t0 + t];
                 const int frac = static_cast<int>((static_cast<unsigned long long>(p) * F) >> 32);

@@ -537,8 +537,9 @@ sdv_status sdv_rope_freqs(int R, double base, int scaling, double factor, double
  * Pair i < R / 2 of token t's head, (x_i, x_{i + R/2}) or with `interleaved`
  * (x_{2i}, x_{2i + 1}), turns by the angle positions[t] * inv_freq[i]:
  *   (a, b) -> factor * (a cos - b sin, b cos + a sin)
- * and elements R..D-1 are copied.  Angles are exact to about 2^-32 of a turn
- * at any int32 position; arithmetic is fp32 with one rounding at the end.
+ * and elements R..D-1 are copied.  Angles are off by 2^-26 of a turn at most, at
+ * any int32 position (for |inv_freq| up to 2^40); arithmetic is fp32 with one
+ * rounding at the end.
  *   dtype      SDV_BF16, SDV_F16 or SDV_F32
  *   q_st, q_sh strides of a token and of a head (k_*, oq_*, ok_* alike)
  *   k, out_k   NULL with Hk = 0: queries alone

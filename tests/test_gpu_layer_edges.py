@@ -2,6 +2,7 @@
 shared memory that are used again, waits that run out, powers of two that 16 bits
 do not hold, streams, infinities, far positions, schedules of many units."""
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -279,3 +280,25 @@ def test_logits_repetition_is_a_quotient(dtype):
     fin = want.abs() < 3.38e38
     tol = (2.0 ** -8 + 2.0 ** -22) * want.abs() + 2.0 ** -133
     assert ((out.double() - want).abs()[fin] <= tol[fin]).all()
+
+
+# ---- rotary positions far away ----
+
+def test_rope_angles_at_any_position():
+    """Angles to 2^-26 of a turn, by whole-number arithmetic on frequency and position
+    with 1 / (2 pi) to 50 digits."""
+    turn = Fraction(10 ** 50, 2 * 314159265358979323846264338327950288419716939937511)
+    freq = torch.tensor([1.0, 0.7598, 100.3, 1.0e-4, 0.1, 6.0e5, -3.7, 0.0], dtype=torch.float32)
+    pos = [2 ** 31 - 1, -2 ** 31, 1234567891, 16777217, -7, 0]
+    half = len(freq)
+    q = torch.zeros((len(pos), 1, 2 * half), device="cuda")
+    q[..., :half] = 1.0                                  # (1, 0) turns to (cos, sin)
+    out = bd.sdv_rope(q, None, _i32(pos), freq.cuda())[0].double().cpu()[:, 0]
+    # the angle, and sine and cosine to two units of fp32
+    tol = 2 * math.pi * (2.0 ** -26 + 2.0 ** -32) + 2 * 2.0 ** -24
+    for i, p in enumerate(pos):
+        for j, f in enumerate(freq.tolist()):
+            part = p * Fraction(f) * turn
+            angle = 2 * math.pi * float(part - round(part))
+            assert abs(float(out[i, j]) - math.cos(angle)) <= tol, (p, f)
+            assert abs(float(out[i, half + j]) - math.sin(angle)) <= tol, (p, f)
