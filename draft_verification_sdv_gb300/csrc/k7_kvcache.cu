@@ -343,8 +343,10 @@ cudaError_t write_lanes(const CellsArgs& a, bool vec, cudaStream_t s) {
     if (a.N < kManyFrom) return write_rows<TYPE, E4M3, LANES, 1, 1>(a, vec, s);
     // quantising is bound by instructions: two vectors a lane share a row's maximum,
     // its power of two and its place (8 prompts of 4099: 37 us against 45 us)
-    if constexpr (E4M3) return write_rows<TYPE, E4M3, LANES / 2, kMany, 2>(a, vec, s);
-    return write_rows<TYPE, E4M3, LANES, kMany, 1>(a, vec, s);
+    if constexpr (E4M3)
+        return write_rows<TYPE, E4M3, LANES / 2, kMany, 2>(a, vec, s);
+    else
+        return write_rows<TYPE, E4M3, LANES, kMany, 1>(a, vec, s);
 }
 
 template <int TYPE, bool E4M3>
