@@ -302,3 +302,105 @@ def test_rope_angles_at_any_position():
             angle = 2 * math.pi * float(part - round(part))
             assert abs(float(out[i, j]) - math.cos(angle)) <= tol, (p, f)
             assert abs(float(out[i, half + j]) - math.sin(angle)) <= tol, (p, f)
+
+
+# ---- schedules: more units than blocks, in rounds and a line of unequal parts ----
+
+def _definition(q, kc, vc, ke, ve, table, ctx, count, mask, scale):
+    """ref.attn's results and tolerances for whole sequences at once, in 64 bits on
+    the device, sequence by sequence: (out, lse, tol_out, tol_lse)."""
+    B, N, Hq, D = q.shape
+    Hk, half = kc.shape[1], ref.HALF_STEP[q.dtype]
+    g = Hq // Hk
+    for b in range(B):
+        c, n = ctx[b], count[b]
+        see = torch.ones((n, c + n), dtype=torch.bool, device="cuda")
+        i = torch.arange(n, device="cuda")
+        if mask is None:
+            see[:, c:] = i[None, :] <= i[:, None]
+        else:
+            see[:, c:] = (mask[b, :n][:, i // 32] >> (i % 32).int() & 1).bool()
+        out = torch.zeros((N, Hq, D), dtype=torch.float64, device="cuda")
+        lse = torch.full((N, Hq), -math.inf, dtype=torch.float64, device="cuda")
+        tol, tol_l = torch.zeros_like(out), torch.zeros_like(lse)
+        k, v = (ref.sequence(t, e, table[b], c + n) for t, e in ((kc, ke), (vc, ve)))
+        for h in range(Hq):
+            x, kh, vh = q[b, :n, h].double(), k[:, h // g], v[:, h // g]
+            s = (x @ kh.T * scale).masked_fill(~see, -math.inf)
+            size = (x.abs() @ kh.abs().T).masked_fill(~see, 0.0).amax(1) * abs(scale)
+            ds = (D + 8) * 2.0 ** -24 * size + 4 * 2.0 ** -24 * s.masked_fill(~see, 0.0).abs().amax(1) + 2.0 ** -20
+            p = s.softmax(1)
+            out[:n, h], lse[:n, h] = p @ vh, s.logsumexp(1)
+            tol[:n, h] = half * out[:n, h].abs() + (half + 2 * ds)[:, None] * (p @ vh.abs()) * 1.01 + 2 * ref.FLOOR[q.dtype]
+            if q.dtype == HF:
+                tol[:n, h] += 2.0 ** -24 * (see.double() @ vh.abs())
+            tol_l[:n, h] = ds + 2.0 ** -23 * lse[:n, h].abs()
+        yield out, lse, tol, tol_l
+
+
+@pytest.mark.parametrize("dtype,cdtype", [(BF, BF), (HF, HF), (BF, F8), (HF, F8)])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("B,K,G,Hq,Hk,D", [(24, 10, 32, 16, 8, 64), (13, 20, 30, 12, 6, 128)])
+def test_attn_in_rounds(B, K, G, Hq, Hk, D, tree, dtype, cdtype):
+    gen = torch.Generator(device="cuda").manual_seed(B)
+    N, ctx = 1 + K * G, [(b * 977) % 1900 if b % 5 else 3 * b for b in range(B)]
+    drafts = torch.randint(0, 9, (B, K, G), generator=gen, device="cuda", dtype=torch.int32)
+    t = bd.sdv_tree_build(_i32([0] * B), drafts, _i32([G - b % 3 for b in range(B)]))
+    count = t["count"].tolist()
+    tiles = -(-N * (Hq // Hk) // 256)
+    assert tiles > 1 and B * Hk * tiles >= 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    q, kc, vc, ke, ve, table = _attn_case(B, N, Hq, Hk, D, 16, ctx, dtype, cdtype, seed=B)
+    mask, st = (t["mask"] if tree else None), _status()
+    out, lse = bd.sdv_tree_attn(q, kc, vc, table, _i32(ctx), count=t["count"], mask=mask, k_exp=ke, v_exp=ve, lse=True,
+                                status=st)
+    assert int(st) == 0
+    for b, (want, wl, tol, tl) in enumerate(_definition(q, kc, vc, ke, ve, table, ctx, count, mask, D ** -0.5)):
+        assert ((out[b].double() - want).abs() <= tol).all(), b
+        fin = wl > -math.inf
+        assert torch.equal(lse[b] > -math.inf, fin) and ((lse[b].double() - wl).abs()[fin] <= tl[fin]).all(), b
+
+
+# ---- rows that are not written ----
+
+@pytest.mark.parametrize("cdtype", [BF, F8])
+@pytest.mark.parametrize("N", [3, 40])
+def test_kv_rows_that_are_refused_leave_the_cells(N, cdtype):
+    """Every byte of a cache after writes of which some are refused is that of the
+    cache with the others alone."""
+    H, D, P, per = 2, 32, 4, 12
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    x = torch.randn((2, N, H, D), generator=gen, device="cuda").to(BF)
+    y = -2.0 * x
+    table = _tables(2, per, 2 * per, 1)
+    off = table.clone()
+    off[1, 0], off[0, 1] = 2 * per, -1
+    places = per * P
+    bits = bd.SDV_STATUS_BAD_LENGTH
+    for start, count, pages, want in (([-1, 0], [N, N], table, bits), ([places - 2, 0], [N, 2], table, bits),
+                                      ([0, 0], [N + 1, 2], table, bits), ([0, 5], [-1, N], table, bits),
+                                      ([-2 ** 31, 2 ** 31 - 1], [N, N], table, bits),
+                                      ([2, 2], [N, N], off, bd.SDV_STATUS_BAD_PAGE)):
+        caches = []
+        for alone in (False, True):
+            kc, vc, ke, ve = _cache(2 * per, H, P, D, cdtype)
+            for t in (kc, vc):
+                t.view(torch.uint8).fill_(0x11)
+            for t in (ke, ve):
+                if t is not None:
+                    t.fill_(99)
+            if not alone:
+                st = _status()
+                bd.sdv_kv_write(x, y, kc, vc, pages, _i32(start), count=_i32(count), k_exp=ke, v_exp=ve, status=st)
+                assert int(st) == want
+            else:                                # the good rows one by one
+                for b in range(2):
+                    for n in range(N):
+                        pos = start[b] + n
+                        if not 0 <= count[b] <= N or n >= count[b] or not 0 <= pos < places:
+                            continue
+                        if 0 <= int(pages[b, pos // P]) < 2 * per:
+                            bd.sdv_kv_write(x[b:b + 1, n:n + 1], y[b:b + 1, n:n + 1], kc, vc, pages[b:b + 1].contiguous(),
+                                            _i32([pos]), k_exp=ke, v_exp=ve)
+            caches.append([t.contiguous().view(torch.uint8) for t in (kc, vc, ke, ve) if t is not None])
+        for a, b in zip(*caches):
+            assert torch.equal(a, b), (start, count)
