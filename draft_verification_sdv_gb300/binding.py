@@ -606,13 +606,30 @@ def _type_of(types: dict, dtype: torch.dtype, name: str) -> int:
     return code
 
 
+def _page_stride(shape, stride) -> Optional[int]:
+    """Elements from one page to the next (None: a page is not contiguous).  The
+    stride of a dimension of one entry means nothing."""
+    whole = 1
+    for n, s in zip(shape[:0:-1], stride[:0:-1]):
+        if n != 1 and s != whole:
+            return None
+        whole *= n
+    return stride[0] if shape[0] != 1 else whole
+
+
 def _cache_of(k_cache, v_cache, k_exp, v_exp) -> _KVCache:
     shape, ks = _rows_of(k_cache, 4, "k_cache")
     pages, heads, place, dim = shape
     dtype = k_cache.dtype
     code = _type_of(_CELL_TYPES, dtype, "the cache")
-    if v_cache.shape != shape or v_cache.dtype != dtype or v_cache.stride() != ks or not v_cache.is_cuda \
-            or ks[1] != place * dim or ks[2] != dim:
+    vs = v_cache.stride()
+    if pages > 1 and vs == ks and ks[1] == place * dim and ks[2] == dim:
+        page = ks[0]
+    else:
+        page = _page_stride(shape, ks)
+        if page != _page_stride(shape, vs):
+            page = None
+    if v_cache.shape != shape or v_cache.dtype != dtype or not v_cache.is_cuda or page is None:
         raise ValueError("k_cache and v_cache must be [pages, kv_heads, page_size, head_dim] of one "
                          "type and page stride, each page contiguous")
     exp_stride, ke, ve = 0, None, None
@@ -621,16 +638,16 @@ def _cache_of(k_cache, v_cache, k_exp, v_exp) -> _KVCache:
             raise ValueError("an e4m3 cache needs k_exp and v_exp")
         for t, name in ((k_exp, "k_exp"), (v_exp, "v_exp")):
             eshape, es = _rows_of(t, 3, name)
-            if t.dtype != torch.uint8 or eshape != shape[:3] or es[1] != place:
+            exp_stride = es[0] if pages > 1 and es[1] == place else _page_stride(eshape, es)
+            if t.dtype != torch.uint8 or eshape != shape[:3] or exp_stride is None:
                 raise ValueError("%s must be uint8 [pages, kv_heads, page_size], each page contiguous"
                                  % name)
-        exp_stride = es[0]
-        if k_exp.stride(0) != exp_stride:
+        if k_exp.stride(0) != es[0] and _page_stride(shape[:3], k_exp.stride()) != exp_stride:
             raise ValueError("k_exp and v_exp must have one page stride")
         ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
     elif k_exp is not None or v_exp is not None:
         raise ValueError("k_exp and v_exp belong to an e4m3 cache")
-    return _KVCache(k_cache.data_ptr(), v_cache.data_ptr(), ke, ve, ks[0], exp_stride, pages, place,
+    return _KVCache(k_cache.data_ptr(), v_cache.data_ptr(), ke, ve, page, exp_stride, pages, place,
                     heads, dim, code)
 
 

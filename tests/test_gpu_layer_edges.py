@@ -404,3 +404,33 @@ def test_kv_rows_that_are_refused_leave_the_cells(N, cdtype):
             caches.append([t.contiguous().view(torch.uint8) for t in (kc, vc, ke, ve) if t is not None])
         for a, b in zip(*caches):
             assert torch.equal(a, b), (start, count)
+
+
+# ---- caches whose strides are those of dimensions of one entry ----
+
+@pytest.mark.parametrize("cdtype", [BF, F8])
+@pytest.mark.parametrize("pages,H,P", [(9, 1, 16), (60, 2, 1), (60, 1, 1), (1, 2, 64), (1, 1, 64)])
+def test_cache_strides_that_mean_nothing(pages, H, P, cdtype):
+    D, N, ctx = 64, 9, 40
+    views = [t if t is None else t.as_strided(t.shape, [7 if n == 1 else x for n, x in zip(t.shape, t.stride())])
+             for t in _cache(pages, H, P, D, cdtype)]
+    plain = _cache(pages, H, P, D, cdtype)
+    assert any(a is not None and a.stride() != b.stride() for a, b in zip(views, plain))
+    x = torch.randn((1, ctx + N, H, D), device="cuda").to(BF)
+    q = torch.randn((1, N, 3 * H, D), device="cuda").to(BF)
+    table = torch.arange(-(-(ctx + N) // P), dtype=torch.int32, device="cuda")[None]
+    res = []
+    for kc, vc, ke, ve in (views, plain):
+        kw = dict(k_exp=ke, v_exp=ve)
+        bd.sdv_kv_write(x, -x, kc, vc, table, _i32([0]), **kw)
+        bd.sdv_kv_commit(kc, vc, table, _i32([ctx]), _i32([[[3, 5]]]), _i32([0]), _i32([2]), **kw)
+        res.append(bd.sdv_kv_read(kc, vc, table, _i32([0]), ctx + N, **kw) +
+                   (bd.sdv_tree_attn(q, kc, vc, table, _i32([ctx]), **kw),))
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+    good = _cache(4, 2, 8, D, cdtype)
+    for i in (0, 1) if cdtype == BF else (0, 1, 2, 3):       # what is not contiguous is refused
+        bad = list(good)
+        bad[i] = bad[i].transpose(1, 2).contiguous().transpose(1, 2)
+        with pytest.raises(ValueError):
+            bd.sdv_kv_read(bad[0], bad[1], _i32([[0]]), _i32([0]), 1, k_exp=bad[2], v_exp=bad[3])
