@@ -904,7 +904,11 @@ def sdv_logits_process(logits: torch.Tensor, drafts: torch.Tensor,
         if logits.dim() != 3 or logits.shape[0] != B:
             raise ValueError("logits must be [%d, nodes, V]" % B)
         nsrc = logits.shape[1]
-    M = 0 if bias_ids is None else bias_ids.numel() // B
+    M = 0
+    if bias_ids is not None or bias is not None:
+        if bias_ids is None or bias is None or bias_ids.numel() != bias.numel() or bias_ids.numel() % B:
+            raise ValueError("bias_ids and bias must be [%d, M] both" % B)
+        M = bias_ids.numel() // B
     if out is None:
         out = _empty((B, K, G + 1, V), logits.dtype, logits.device, stream)
     i32, f32 = torch.int32, torch.float32

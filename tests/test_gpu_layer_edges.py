@@ -434,3 +434,53 @@ def test_cache_strides_that_mean_nothing(pages, H, P, cdtype):
         bad[i] = bad[i].transpose(1, 2).contiguous().transpose(1, 2)
         with pytest.raises(ValueError):
             bd.sdv_kv_read(bad[0], bad[1], _i32([[0]]), _i32([0]), 1, k_exp=bad[2], v_exp=bad[3])
+
+
+# ---- biases that would be passed over ----
+
+def test_logits_biases_of_the_wrong_size_are_refused():
+    x = torch.randn((2, 1, 3, 64), device="cuda").to(BF)
+    d = _i32([[[1, 2]], [[3, 4]]])
+    one, f = _i32([5]), torch.ones(1, device="cuda")
+    for ids, bias in ((one, f), (None, f), (one, None), (_i32([1, 2, 3]), torch.ones(3, device="cuda")),
+                      (_i32([[1], [2]]), torch.ones((2, 2), device="cuda"))):
+        with pytest.raises(ValueError):
+            bd.sdv_logits_process(x, d, bias_ids=ids, bias=bias)
+    none = torch.empty((2, 0), device="cuda")
+    assert torch.equal(bd.sdv_logits_process(x, d, bias_ids=none.int(), bias=none), x)
+
+
+# ---- captured calls ----
+
+@pytest.mark.parametrize("large", [False, True])
+def test_attn_redo_in_a_graph(large):
+    """fp16 queries on an e4m3 cache: what a replay finds in the cache decides, not
+    what was there when the call was captured."""
+    B, N, Hk, g, D, ctx = 2, 50, 2, 3, 64, [100, 170]
+    q, kc, vc, ke, ve, table = _attn_case(B, N, Hk * g, Hk, D, 16, ctx, HF, F8, seed=4)
+    lens = _i32(ctx)
+    kw = dict(k_exp=ke, v_exp=ve, lse=True)
+
+    def fill(big):
+        gen = torch.Generator(device="cuda").manual_seed(5 + big)
+        v = torch.randn((B, max(ctx) + N, Hk, D), generator=gen, device="cuda").to(BF)
+        if big:
+            v[:, 20] *= 1.0e5
+        bd.sdv_kv_write(v / 4, v, kc, vc, table, _i32([0] * B), k_exp=ke, v_exp=ve)
+
+    fill(large)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        bd.sdv_tree_attn(q, kc, vc, table, lens, **kw)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = bd.sdv_tree_attn(q, kc, vc, table, lens, **kw)
+    for big in (not large, large, not large):
+        fill(big)
+        graph.replay()
+        want, wl = bd.sdv_tree_attn(q, kc, vc, table, lens, **kw)
+        # (a key of 25000 has all the weight of some rows, whose value of 1e5 fp16 does not hold)
+        assert torch.equal(out, want) and torch.equal(lse, wl) and not out.isnan().any()
+        assert big or out.isfinite().all()
