@@ -7,6 +7,7 @@ fast-math); ``-lineinfo`` for profiling.
 """
 import concurrent.futures
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -21,6 +22,9 @@ SOURCES = ["k1_rowpass.cu", "k2_select.cu", "k3_sample.cu", "k4_cps.cu", "k5_adl
            "sdv_api.cu", "sdv_layer.cu", "sdv_static.cu"]
 HEADERS = ["sdv_device.cuh", "sdv_plan.h", "sdv_layer.h", "k8_attn.cuh", "k8_attn_mma.cuh", "k8_attn_tma.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
+# Kernels that exchange registers between their warps need a launch with just this
+# many per thread (kRegs of the source): with another count every call is refused.
+REGISTERS = {"k8_attn_tc.cu": ("attn_tc_kernel", 168)}
 
 
 def nvcc() -> str:
@@ -42,6 +46,17 @@ def _run(cmd):
     return r.stdout + r.stderr
 
 
+def check_registers(src: str, report: str) -> None:
+    """Raise unless the compiler's report (-Xptxas -v) of `src` gives each kernel
+    of REGISTERS its count."""
+    kernel, want = REGISTERS[src]
+    found = re.findall(r"Compiling entry function '(\S*)'.*?Used (\d+) registers", report, re.S)
+    counts = [int(n) for name, n in found if kernel in name]
+    if not counts or set(counts) != {want}:
+        raise RuntimeError("%s: %s must have %d registers per thread, the compiler gave %s"
+                           % (src, kernel, want, counts))
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     """Compile libsdv.so if any source is newer than it; return its path."""
     if not force and os.path.exists(LIB) and all(
@@ -56,7 +71,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
 
     def compile_one(src):
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
-        out = _run([nv] + flags + ["-c", os.path.join(CSRC, src), "-o", obj])
+        report = ["-Xptxas", "-v"] if src in REGISTERS and not verbose_ptxas else []
+        out = _run([nv] + flags + report + ["-c", os.path.join(CSRC, src), "-o", obj])
+        if src in REGISTERS:
+            check_registers(src, out)
         return obj, out
 
     with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as ex:
