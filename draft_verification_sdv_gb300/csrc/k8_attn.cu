@@ -11,10 +11,12 @@ constexpr int kMaxCtasPerSm = 2;
 // Query rows per kv head up to which k8_attn_dec.cu runs, in units of 16 rows;
 // above, k8_attn_tc.cu, whose time hardly depends on the rows up to 256.  Times
 // for 32 sequences of 4000 positions, 8 kv heads of 128: 16-bit caches, 16 rows
-// 100 and 120 us, 24 rows 178 and 121 us; e4m3 caches, which the second has to
-// widen in shared memory first, 48 rows 211 and 357 us, 80 rows 331 and 364, 128
-// rows 501 and 373.  (Heads of 64, 16 bits: 16 rows 59 and 106 us, 48 rows 139
-// and 107; e4m3: 80 rows 217 and 283 us, 128 rows 333 and 285.)
+// 100 and 117 us, 24 rows 178 (when the first took them) and 118 us; e4m3 caches,
+// which the second has to widen in shared memory first, 48 rows 207 and 322 us, 80
+// rows 326 and 330, 128 rows 495 and 342.  (Heads of 64, 16 bits: 16 rows 59 and 96
+// us, 48 rows 139 and 97; e4m3: 80 rows 220 and 262 us, 128 rows 339 and 265.)  Two
+// sequences of 100000: 16 bits, 16 rows 143 and 161 us; e4m3, 80 rows 405 and 476 us,
+// 128 rows 626 and 478; one of 20000: e4m3, 80 rows 70 and 68 us, 128 rows 91 and 68.
 constexpr int kDecRows = 16, kDecRowsE4m3 = 80;
 
 // out = sum_i 2^(L_i - L) out_i with L = log2 sum_i 2^(L_i), over the CTAs that

@@ -9,8 +9,8 @@
 // Where several row tiles read the same keys and values (mts > 1), CTA i first
 // takes units i, i + n, i + 2 n, ... for `rounds` rounds, so that the row tiles
 // of one head run side by side and its keys and values come from HBM once (all
-// heads at once would not fit the L2: 840 us against 948 us on 16 trees of 513
-// nodes and some 200 MB of cache, 239 against 267 us on 3 chunks of 1900 tokens).  The key tiles of the other units (of all, where
+// heads at once would not fit the L2: 784 us against 869 us on 16 trees of 513
+// nodes and some 200 MB of cache, 232 against 260 us on 3 chunks of 1900 tokens).  The key tiles of the other units (of all, where
 // there is one row tile) form one line, cut into one part per CTA, longer for
 // those whose rounds were shorter: ragged lengths need no tuning.  A unit cut
 // by the end of a part gives partial results, one per CTA: normalised fp32

@@ -24,10 +24,11 @@
 // largest at 1, channels beside one of 65000 were off by 2^-9).  bf16 queries are
 // brought to fp16 in units of a power of two per row.
 //
-// 64 ragged sequences of up to 32000 positions, 8 kv heads of 128, e4m3: 453 us,
+// 64 ragged sequences of up to 32000 positions, 8 kv heads of 128, e4m3: 457 us,
 // 5.3 TB/s (the widening and the products then take the warps' time); 32 of 4000,
-// 16 bits: 95 us, 5.6 TB/s.  Two CTAs of three stages per SM: with three CTAs of
-// two the registers spill (657 us).
+// 16 bits: 95 us, 5.6 TB/s.  Two CTAs of three stages per SM, where e4m3 heads of
+// 128 spill 30 to 60 bytes a thread; with three CTAs of two stages it is far more
+// (657 us).
 #include "k8_attn_mma.cuh"
 #include "k8_attn_tma.cuh"
 
@@ -579,7 +580,7 @@ cudaError_t dec_one(AttnArgs a, int nsm, cudaStream_t s) {
 }
 
 // With 8 rows or fewer the other half of the instructions' 16 is not carried
-// along: 64 ragged sequences of 8 rows, e4m3, 453 us against 528 us.
+// along: 64 ragged sequences of 8 rows, e4m3, 457 us against 533 us.
 template <int DP, bool E4, bool F16> cudaError_t dec_rows(const AttnArgs& a, int nsm, cudaStream_t s) {
     const int rows = a.N * a.g;
     if (rows <= 8) return dec_one<DP, E4, F16, 1, true>(a, nsm, s);

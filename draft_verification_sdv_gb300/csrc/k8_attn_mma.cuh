@@ -545,10 +545,11 @@ cudaError_t launch_one(AttnArgs a, int nsm, cudaStream_t s) {
 }
 
 // Units of 16 rows read the cache once per 16 rows, units of 64 compute for 64
-// however many there are.  32 sequences of 4000 positions, 8 kv heads of 128 on
-// pages of 12, 16-bit cache: 16 rows 132 and 370 us, 32 rows 245 and 378, 48 rows
-// 359 and 385; e4m3: 16 rows 120 and 554 us, 48 rows 318 and 560, 64 rows 411
-// and 562.  (Heads of 64, e4m3: 48 rows 231 and 262 us, 64 rows 296 and 270.)
+// however many there are.  32 sequences of 4000 positions, 8 kv heads, 16-bit cache:
+// heads of 256, 16 rows 328 and 658 us, 32 rows 636 and 673, 40 rows 936 and 677
+// (heads of 128 on pages of 12: 32 rows 243 and 425, 48 rows 355 and 432, 56 rows 465
+// and 433); e4m3: heads of 128, 48 rows 308 and 646, heads of 64, 48 rows 228 and
+// 267, 64 rows 295 and 269.
 template <int DP, bool E4, bool F16> cudaError_t launch_rows(const AttnArgs& a, int rows, int nsm, cudaStream_t s) {
     return rows <= (E4 ? 48 : 32) ? launch_one<DP, E4, F16, 1>(a, nsm, s) : launch_one<DP, E4, F16, 4>(a, nsm, s);
 }

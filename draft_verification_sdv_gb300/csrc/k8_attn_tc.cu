@@ -40,10 +40,10 @@
 // What bounds it: the chain of one stream's step, softmax (2230 clocks for two
 // streams' tiles, a third of them the 2^x), P V (430) and S (640) and the waits
 // between them (440), 3740 clocks for two tiles where the products alone take
-// 2100.  16 trees of 513 nodes over 1500 to 3500 positions, 8 x 8 heads of 128:
-// 840 us, 795 TFLOP/s; 3 chunks of 1900 tokens, 8 x 4 heads of 64: 239 us.  e4m3
-// rows: 2700 clocks and more to widen a tile (671 us against 305 us for 4 chains
-// of 513 nodes behind 4000 positions).  Seven warps for it have too few registers,
+// 2100 (counted when 16 trees took 840 us).  16 trees of 513 nodes over 1500 to
+// 3500 positions, 8 x 8 heads of 128: 780 us, 855 TFLOP/s; 3 chunks of 1900 tokens,
+// 8 x 4 heads of 64: 232 us.  e4m3 rows: 2700 clocks and more to widen a tile (682 us
+// against 280 us for 4 chains of 513 nodes behind 4000 positions).  Seven warps for it have too few registers,
 // and rows that land beside their slots leave too few slots: both were slower.
 // Short units: some 11000 clocks from one to the next, of which the rows' way to
 // memory is 4000.
