@@ -8,8 +8,8 @@
 // The contractions run on mma.sync m16n8k16, whose 16 rows waste less on 8 query
 // heads than a 128-row instruction would.  For few rows the cache's bytes and
 // the copies' instructions bound it (32 sequences of 4000 positions, 8 kv heads,
-// 8 rows each: heads of 256, 327 us, 3.2 TB/s; heads of 128 on pages of 12, 130
-// us, 4.0 TB/s), for many the matrix instructions.
+// 8 rows each: heads of 256, 321 us, 3.3 TB/s; heads of 128 on pages of 12, 128
+// us, 4.1 TB/s), for many the matrix instructions.
 //
 // MT = 16 WM rows; the WN = 4 / WM warps that share rows split each tile's
 // positions and keep their own running maximum, sum and output, which are
