@@ -573,10 +573,11 @@ cudaError_t dec_one(AttnArgs a, int nsm, cudaStream_t s) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         return cudaLaunchKernelEx(&cfg, attn_dec_kernel<DP, E4, F16, H, ONE, REDO>, a, k, v, rows);
+    } else {
+        attn_dec_kernel<DP, E4, F16, H, ONE, REDO><<<static_cast<unsigned>(a.ctas), kDecThreads, bytes, s>>>(a, k, v, rows);
+        e = cudaGetLastError();
+        return e != cudaSuccess ? e : launch_attn_combine(a, F16, 16, s);
     }
-    attn_dec_kernel<DP, E4, F16, H, ONE, REDO><<<static_cast<unsigned>(a.ctas), kDecThreads, bytes, s>>>(a, k, v, rows);
-    e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_attn_combine(a, F16, 16, s);
 }
 
 // With 8 rows or fewer the other half of the instructions' 16 is not carried

@@ -43,10 +43,10 @@
 // 2100 (counted when 16 trees took 840 us).  16 trees of 513 nodes over 1500 to
 // 3500 positions, 8 x 8 heads of 128: 780 us, 855 TFLOP/s; 3 chunks of 1900 tokens,
 // 8 x 4 heads of 64: 232 us.  e4m3 rows: 2700 clocks and more to widen a tile (682 us
-// against 280 us for 4 chains of 513 nodes behind 4000 positions).  Seven warps for it have too few registers,
-// and rows that land beside their slots leave too few slots: both were slower.
-// Short units: some 11000 clocks from one to the next, of which the rows' way to
-// memory is 4000.
+// against 280 us for 4 chains of 513 nodes behind 4000 positions).  Seven warps for
+// it have too few registers, and rows that land beside their slots leave too few
+// slots: both were slower.  Short units: some 11000 clocks from one to the next, of
+// which the rows' way to memory is 4000.
 //
 // Every wait is bounded: a wait that gives up marks the CTA dead, after which
 // no wait waits, no copy is begun, and every row with something to see that is
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const bool skip = (a.hooks & kHookAttnNoCopy) && blockIdx.x == 0 && lstep == 3;
             if (mine && !skip && elected()) mbar_arrive_expect_tx(bars + kLand + slot, n * run_rows * 128);
             __syncwarp();
-            if (mine && good && !skip)                                // e4m3 lands in the slot's upper half
+            if (mine && good && !skip)                       // e4m3 lands in the slot's upper half
                 tma_load(smem_u32(smem + slot * kTile + (E4 ? kBlock : column * kBlock) + copy * run_rows * 128), isv ? &map_v : &map_k,
                          bars + kLand + slot, column * 64, loff, lpage);
             __syncwarp();
