@@ -28,8 +28,10 @@ STATUS_NAMES = {0: "SDV_OK", 1: "SDV_ERR_ARG", 2: "SDV_ERR_CUDA", 3: "SDV_ERR_OO
                 4: "SDV_ERR_DEVICE_DATA", 5: "SDV_ERR_SCRATCH"}
 STATIC_SCRATCH_BYTES = 8 << 20
 SDV_STATUS_BAD_TOKEN, SDV_STATUS_TIMEOUT = 1, 8
+SDV_STATUS_BAD_ROW, SDV_STATUS_BAD_PARAM = 2, 4
 SDV_STATUS_BAD_LENGTH = 16
 SDV_STATUS_BAD_PAGE = 64
+SDV_STATUS_NO_PAGES = 128
 SDV_ROPE_PLAIN, SDV_ROPE_LINEAR, SDV_ROPE_BASE, SDV_ROPE_PARTS = 0, 1, 2, 3
 SDV_HOOK_SAMPLE_NO_COPY = 1
 SDV_HOOK_ATTN_NO_COPY = 2
@@ -86,10 +88,18 @@ SIGNATURES = {
     "sdv_tree_attn_workspace": (ctypes.c_size_t, []),
     "sdv_tree_attn": (_I, [_KVP, _I, _I, _I, _I, _VP, _VP, _I64, _I64, _I64, _VP, _I, _VP, _VP, _VP,
                            _I64, _F, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
+    "sdv_prefix_attn_workspace": (ctypes.c_size_t, [_I, _I, _I, _I]),
+    "sdv_prefix_attn": (_I, [_KVP, _I, _I, _I, _I, _I, _VP, _VP, _I64, _I64, _I64, _VP, _I, _VP, _VP, _I,
+                             _VP, _VP, _VP, _I64, _F, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
     "sdv_set_attn_test_hooks": (_I, [ctypes.c_uint]),
     "sdv_logits_process": (_I, [_I, _I, _I, _I, _I, _VP, _VP, _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                 _I, _VP, _VP, _VP, _VP, _VP]),
     "sdv_counts_commit": (_I, [_I, _I, _I, _I] + [_VP] * 7),
+    "sdv_pages_extend": (_I, [_I] * 5 + [_VP] * 12),
+    "sdv_pages_release": (_I, [_I] * 4 + [_VP] * 7),
+    "sdv_sample": (_I, [_I64, _I, _I, _I, _VP, _VP, _I64] + [_VP] * 9),
+    "sdv_logits_truncate": (_I, [_I64, _I, _I, _I, _VP, _VP, _I64, _VP, _VP, _VP, _VP, _VP, _I64, _VP,
+                                 _VP]),
 }
 
 _lib = None
@@ -750,6 +760,55 @@ def sdv_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor
     return out_q, out_k
 
 
+def sdv_pages_extend(free_list: torch.Tensor, free_count: torch.Tensor, block_table: torch.Tensor,
+                     held: torch.Tensor, start: torch.Tensor, N: int, page_size: int,
+                     count: Optional[torch.Tensor] = None, depth: Optional[torch.Tensor] = None,
+                     base: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                     slots: Optional[torch.Tensor] = None, stream=None,
+                     status: Optional[torch.Tensor] = None):
+    """Pages for the tokens start[b] .. start[b] + count[b] - 1 (count None: N) of
+    each sequence, from the stack free_list[:free_count] into block_table [B,
+    max_pages] behind the held[b] that it has; free_count and held follow (all
+    int32, changed in place).  Returns (positions [B, N] int32, slots [B, N]
+    int64): base[b] + start[b] + depth[b, n] (depth None: n), as sdv_rope takes
+    them, and each token's place in the cache, page * page_size + place, or -1."""
+    B = held.numel()
+    i32 = torch.int32
+    held_p = _array(held, B, i32, "held")
+    if positions is None:
+        positions = _empty((B, N), i32, held.device, stream)
+    if slots is None:
+        slots = _empty((B, N), torch.int64, held.device, stream)
+    st = load().sdv_pages_extend(
+        B, N, free_list.numel(), page_size, block_table.shape[1], _stream_of(held, stream),
+        _array(free_list, free_list.numel(), i32, "free_list"), _array(free_count, 1, i32, "free_count"),
+        _table_of(block_table, B), held_p, _array(start, B, i32, "start"),
+        _array(count, B, i32, "count"), _array(depth, B * N, i32, "depth"), _array(base, B, i32, "base"),
+        _array(positions, B * N, i32, "positions"), _array(slots, B * N, torch.int64, "slots"),
+        _status_of(status))
+    if st != SDV_OK:
+        raise SdvError(st, "sdv_pages_extend")
+    return positions, slots
+
+
+def sdv_pages_release(free_list: torch.Tensor, free_count: torch.Tensor, block_table: torch.Tensor,
+                      held: torch.Tensor, keep: torch.Tensor, page_size: int, stream=None,
+                      status: Optional[torch.Tensor] = None) -> None:
+    """Give back the pages behind the first keep[b] positions of each sequence
+    (0: all that it holds): their entries of block_table become -1, free_list,
+    free_count and held follow."""
+    B = held.numel()
+    i32 = torch.int32
+    held_p = _array(held, B, i32, "held")
+    st = load().sdv_pages_release(
+        B, free_list.numel(), page_size, block_table.shape[1], _stream_of(held, stream),
+        _array(free_list, free_list.numel(), i32, "free_list"), _array(free_count, 1, i32, "free_count"),
+        _table_of(block_table, B), held_p, _array(keep, B, i32, "keep"),
+        _status_of(status))
+    if st != SDV_OK:
+        raise SdvError(st, "sdv_pages_release")
+
+
 def sdv_kv_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                  block_table: torch.Tensor, start: torch.Tensor,
                  count: Optional[torch.Tensor] = None, k_exp: Optional[torch.Tensor] = None,
@@ -869,6 +928,60 @@ def sdv_tree_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     return (out, logs) if lse else out
 
 
+def sdv_prefix_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    prefix_table: torch.Tensor, prefix_len: torch.Tensor, block_table: torch.Tensor,
+                    ctx_len: torch.Tensor, count: Optional[torch.Tensor] = None,
+                    mask: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                    k_exp: Optional[torch.Tensor] = None, v_exp: Optional[torch.Tensor] = None,
+                    lse: bool = False, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None,
+                    status: Optional[torch.Tensor] = None):
+    """sdv_tree_attn for sequences that share prefixes: prefix_table [groups,
+    max_prefix_pages] and prefix_len [groups] say where the prefix of each group of
+    B / groups sequences lies, block_table and ctx_len what each sequence has
+    added behind it, on pages of its own.  A prefix is read once for all its
+    sequences.  `workspace` (uint8) has sdv_prefix_attn_workspace(B, N, Hq, D)
+    bytes: some 40 MB and two fp32 rows for each row of out."""
+    cache = _cache_of(k_cache, v_cache, k_exp, v_exp)
+    (B, N, Hq, D), qs = _rows_of(q, 4, "q")
+    code = _type_of(_HALF_TYPES, q.dtype, "q")
+    if D != cache.head_dim:
+        raise ValueError("q must be [B, N, Hq, %d]" % cache.head_dim)
+    groups = prefix_len.numel()
+    if groups < 1 or B % groups:
+        raise ValueError("prefix_len must have a number of entries that divides %d, got %d" % (B, groups))
+    lib = load()
+    handle = _stream_of(q, stream)
+    mask_sb, W = 0, (N + 31) // 32
+    if mask is not None:
+        shape = tuple(mask.shape)
+        if shape != (N, W) and shape != (B, N, W):
+            raise ValueError("mask must be [%d, %d] or [%d, %d, %d]" % (N, W, B, N, W))
+        mask_sb = N * W if len(shape) == 3 else 0
+    out_p = _array(out, B * N * Hq * D, q.dtype, "out")
+    if out is None:
+        out = _empty((B, N, Hq, D), q.dtype, q.device, stream)
+        out_p = out.data_ptr()
+    logs = _empty((B, N, Hq), torch.float32, q.device, stream) if lse else None
+    if workspace is None:
+        workspace = _empty((lib.sdv_prefix_attn_workspace(B, N, Hq, D),), torch.uint8, q.device, stream)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous uint8")
+    st = lib.sdv_prefix_attn(
+        cache, B, groups, N, Hq, code, handle, q.data_ptr(), qs[0], qs[1], qs[2],
+        _table_of(prefix_table, groups), prefix_table.shape[1],
+        _array(prefix_len, groups, torch.int32, "prefix_len"), _table_of(block_table, B),
+        block_table.shape[1], _array(ctx_len, B, torch.int32, "ctx_len"),
+        _array(count, B, torch.int32, "count"),
+        None if mask is None else _array(mask, mask.numel(), torch.int32, "mask"), mask_sb,
+        D ** -0.5 if scale is None else scale,
+        out_p, None if logs is None else logs.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _status_of(status))
+    if st != SDV_OK:
+        raise SdvError(st, "sdv_prefix_attn")
+    return (out, logs) if lse else out
+
+
 def sdv_set_attn_test_hooks(hooks: int) -> int:
     """Fault-path test hooks of later sdv_tree_attn calls (SDV_HOOK_ATTN_NO_COPY
     or 0)."""
@@ -941,3 +1054,88 @@ def sdv_counts_commit(counts: torch.Tensor, drafts: torch.Tensor, sel: torch.Ten
                                   _array(counts, B * V, i32, "counts"), _status_of(status))
     if st != SDV_OK:
         raise SdvError(st, "sdv_counts_commit")
+
+
+def _logit_rows(t: torch.Tensor, name: str):
+    """(B, rows per entry of the first dimension, V, elements between rows) of
+    logits [B, ..., V] whose rows are evenly apart."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) < 2:
+        raise ValueError("%s must be [B, ..., V], got %s" % (name, tuple(shape)))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if stride[-1] != 1 and shape[-1] != 1:
+        raise ValueError("%s must be contiguous in its last dimension" % name)
+    rows, step = 1, None                 # of the dimensions from here on
+    for n, s in zip(shape[-2::-1], stride[-2::-1]):
+        if n == 1:
+            continue
+        if step is None:
+            step = s
+        elif s != rows * step:
+            raise ValueError("the rows of %s must be evenly apart" % name)
+        rows *= n
+    per = rows // shape[0] if shape[0] and rows else 1
+    return shape[0], per, shape[-1], shape[-1] if step is None else step
+
+
+def _cuts(B: int, temperature, top_k, top_p, min_p):
+    f32 = torch.float32
+    return (_array(temperature, B, f32, "temperature"), _array(top_k, B, torch.int32, "top_k"),
+            _array(top_p, B, f32, "top_p"), _array(min_p, B, f32, "min_p"))
+
+
+def sdv_sample(logits: torch.Tensor, uniform: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+               top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+               min_p: Optional[torch.Tensor] = None, logprob: bool = False,
+               tokens: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None, stream=None,
+               status: Optional[torch.Tensor] = None):
+    """A token for each row of logits [B, ..., V] (bfloat16 or float32) from the
+    random numbers uniform [B, ...] in [0, 1), under the parameters of its sequence
+    ([B] each; temperature 0 takes the best token): tokens [B, ...] int32, and with
+    `logprob` also their log-probabilities among what is kept.  `kept` (int32
+    [B, ...]) receives how many tokens that is."""
+    B, per, V, step = _logit_rows(logits, "logits")
+    code = _dtype_code(logits.dtype)
+    shape = logits.shape[:-1]
+    rows = B * per if logits.numel() else 0
+    if tokens is None:
+        tokens = _empty(shape, torch.int32, logits.device, stream)
+    logs = _empty(shape, torch.float32, logits.device, stream) if logprob else None
+    st = load().sdv_sample(rows, per, V, code, _stream_of(logits, stream), logits.data_ptr(), step,
+                           *_cuts(B, temperature, top_k, top_p, min_p),
+                           _array(uniform, rows, torch.float32, "uniform"),
+                           _array(tokens, rows, torch.int32, "tokens"),
+                           None if logs is None else logs.data_ptr(),
+                           _array(kept, rows, torch.int32, "kept"), _status_of(status))
+    if st != SDV_OK:
+        raise SdvError(st, "sdv_sample")
+    return (tokens, logs) if logprob else tokens
+
+
+def sdv_logits_truncate(logits: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+                        top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+                        min_p: Optional[torch.Tensor] = None, kept: bool = False,
+                        out: Optional[torch.Tensor] = None, stream=None,
+                        status: Optional[torch.Tensor] = None):
+    """logits [B, ..., V] with -inf in the place of every token that sdv_sample
+    under the same parameters would not draw (not scaled by the temperature), for a
+    Verifier call that is lossless for the truncated distribution; with `kept` also
+    how many are left [B, ...].  out=logits works in place."""
+    B, per, V, step = _logit_rows(logits, "logits")
+    code = _dtype_code(logits.dtype)
+    rows = B * per if logits.numel() else 0
+    if out is None:
+        out = _empty(logits.shape, logits.dtype, logits.device, stream)
+        out_step = V
+    else:
+        if out.shape != logits.shape or out.dtype != logits.dtype:
+            raise ValueError("out must have the shape and type of logits")
+        out_step = _logit_rows(out, "out")[3]
+    many = _empty(logits.shape[:-1], torch.int32, logits.device, stream) if kept else None
+    st = load().sdv_logits_truncate(rows, per, V, code, _stream_of(logits, stream), logits.data_ptr(), step,
+                                    *_cuts(B, temperature, top_k, top_p, min_p), out.data_ptr(), out_step,
+                                    None if many is None else many.data_ptr(), _status_of(status))
+    if st != SDV_OK:
+        raise SdvError(st, "sdv_logits_truncate")
+    return (out, many) if kept else out

@@ -65,11 +65,8 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, int
         }
         const float inv = nan ? nan_value : sum == 0.0f ? 0.0f : 1.0f / sum;
         const int64_t orow = (static_cast<int64_t>(b) * a.N + node) * a.Hq + h * a.g + row % a.g;
-        unsigned short* dst = static_cast<unsigned short*>(a.out) + orow * D + d;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(attn::pack2<F16>(acc[0] * inv, acc[1] * inv),
-                                                    attn::pack2<F16>(acc[2] * inv, acc[3] * inv));
-        if (d == 0 && a.lse)
-            a.lse[orow] = nan ? nan_value : sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        const float x[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
+        attn::store_row4<F16>(a, orow, d, x, nan ? nan_value : sum == 0.0f ? -INFINITY : top + log2f(sum));
     }
 }
 

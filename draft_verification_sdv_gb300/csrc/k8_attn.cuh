@@ -36,16 +36,30 @@ __device__ __forceinline__ Cut cut_of(const AttnArgs& a, int b) {
     c.ctx = __ldg(a.ctx + b);
     c.cnt = a.count ? __ldg(a.count + b) : a.N;
     c.bad = c.ctx < 0 || c.cnt < 0 || c.cnt > a.N ||
-            static_cast<int64_t>(c.ctx) + c.cnt > static_cast<int64_t>(a.max_pages) * a.c.P;
+            static_cast<int64_t>(c.ctx) + (a.W > 0 ? c.cnt : 0) > static_cast<int64_t>(a.max_pages) * a.c.P;
     if (c.bad) c.ctx = c.cnt = 0;
     return c;
+}
+
+// Positions of the sequence that hold keys: the committed ones and the nodes'.
+__device__ __forceinline__ int held_of(const AttnArgs& a, const Cut& c) { return c.ctx + (a.W > 0 ? c.cnt : 0); }
+
+// A node's queries (head 0).
+__device__ __forceinline__ const unsigned char* q_of(const AttnArgs& a, int b, int node) {
+    int64_t at = b * a.q_sb;
+    if (a.q_n > 0) {
+        const int s = node / a.q_n;
+        at += s * a.q_s2;
+        node -= s * a.q_n;
+    }
+    return a.q + at + node * a.q_sn;
 }
 
 // Positions that row tile mt of a sequence reads.
 template <int MT> __device__ __forceinline__ int tile_len(const AttnArgs& a, const Cut& c, int mt) {
     const int first = mt * MT / a.g;
     if (first >= c.cnt) return 0;
-    if (a.mask) return c.ctx + c.cnt;
+    if (a.mask) return held_of(a, c);
     const int last = (mt * MT + MT - 1) / a.g;
     return c.ctx + min(c.cnt, last + 1);
 }
@@ -80,7 +94,7 @@ template <int MT, int BN>
 __device__ __forceinline__ int64_t head_tiles(const AttnArgs& a, const Cut& c, int mts) {
     if (a.mask) {
         const int live = min(mts, (c.cnt * a.g + MT - 1) / MT);
-        return static_cast<int64_t>(live) * tiles_of<BN>(c.ctx + c.cnt) + (mts - live);
+        return static_cast<int64_t>(live) * tiles_of<BN>(held_of(a, c)) + (mts - live);
     }
     return chain_tiles<MT, BN>(a, c, mts);
 }
@@ -253,7 +267,7 @@ template <int MT, int BN> struct Walk {
             const int64_t per_head = head_tiles<MT, BN>(a, cut, mts);
             h = static_cast<int>(quotient(in_seq, per_head));
             int64_t before = in_seq - h * per_head;
-            const int t = tiles_of<BN>(cut.ctx + cut.cnt);
+            const int t = tiles_of<BN>(held_of(a, cut));
             const int live = min(mts, (cut.cnt * a.g + MT - 1) / MT);
             if (before < static_cast<int64_t>(live) * t) {
                 mt = static_cast<int>(quotient(before, t));
@@ -355,6 +369,19 @@ template <bool F16> __device__ __forceinline__ uint32_t pack2(float x, float y) 
     else
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
     return r;
+}
+
+// Four elements, from d on, of a finished row.
+template <bool F16>
+__device__ __forceinline__ void store_row4(const AttnArgs& a, int64_t orow, int d, const float (&x)[4], float log2sum) {
+    if (a.raw) {
+        *reinterpret_cast<float4*>(a.raw + orow * a.c.D + d) = make_float4(x[0], x[1], x[2], x[3]);
+        if (d == 0) a.raw_log[orow] = log2sum;
+    } else {
+        unsigned short* dst = static_cast<unsigned short*>(a.out) + orow * a.c.D + d;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<F16>(x[0], x[1]), pack2<F16>(x[2], x[3]));
+        if (d == 0 && a.lse) a.lse[orow] = log2sum * kLn2;
+    }
 }
 
 }  // namespace attn

@@ -183,8 +183,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
             const int row = first + r, node = row / a.g;
             uint32_t v[4] = {0, 0, 0, 0};
             if (node < u.cut.cnt && c * 8 < a.c.D) {
-                const unsigned char* p = a.q + u.b * a.q_sb + node * a.q_sn +
-                                         (static_cast<int64_t>(u.h) * a.g + row % a.g) * a.q_sh + c * 16;
+                const unsigned char* p = q_of(a, u.b, node) + (static_cast<int64_t>(u.h) * a.g + row % a.g) * a.q_sh + c * 16;
                 if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
                     const uint4 x = *reinterpret_cast<const uint4*>(p);
                     v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
@@ -539,9 +538,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_dec_kernel(const __grid_c
             const float acc[4] = {empty ? 0.0f : v.x * inv, empty ? 0.0f : v.y * inv, empty ? 0.0f : v.z * inv, empty ? 0.0f : v.w * inv};
             if (u.whole) {
                 const int64_t orow = (static_cast<int64_t>(u.b) * a.N + nd) * a.Hq + u.h * a.g + (first + r) % a.g;
-                unsigned short* dst = static_cast<unsigned short*>(a.out) + orow * a.c.D + d;
-                *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<F16>(acc[0], acc[1]), pack2<F16>(acc[2], acc[3]));
-                if (d == 0 && a.lse) a.lse[orow] = log2sum * kLn2;
+                store_row4<F16>(a, orow, d, acc, log2sum);
             } else {
                 *reinterpret_cast<float4*>(prow + r * a.c.D + d) = make_float4(acc[0], acc[1], acc[2], acc[3]);
                 if (d == 0) prow[MT * a.c.D + r] = log2sum;

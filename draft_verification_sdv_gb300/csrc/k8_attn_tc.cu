@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             if (u.b != seq) {
                 seq = u.b;
                 const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
-                const int pages = (u.cut.ctx + u.cut.cnt + a.c.P - 1) / a.c.P;
+                const int pages = (held_of(a, u.cut) + a.c.P - 1) / a.c.P;
                 int bad = 0;
                 for (int pg = r; pg < pages; pg += kRows) {
                     const int x = __ldg(table + pg);
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         auto begin_queries = [&]() {
             const int first_row = u.mt * MT + st * kRows, row = first_row + r, node = row / a.g;
             if (u.len <= 0 || u.t1 <= u.t0 || first_row / a.g >= u.cut.cnt) return false;
-            copy_row(a.q + u.b * a.q_sb + node * a.q_sn + (static_cast<int64_t>(u.h) * a.g + row - node * a.g) * a.q_sh, node < u.cut.cnt,
+            copy_row(q_of(a, u.b, node) + (static_cast<int64_t>(u.h) * a.g + row - node * a.g) * a.q_sh, node < u.cut.cnt,
                      a.scale_log2 < 0.0f ? 0x80008000u : 0u, smem + M::q + st * kTile, r, D / 8);
             return true;
         };
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 uint32_t words[5] = {0, 0, 0, 0, 0};
                 // tiles from `plain` on hold positions that some rows see and some do not
                 // (all of them go the long way where a page is bad)
-                const int plain = any_bad ? 0 : min(max(min(seen_by_all<MT>(a, u.cut, u.mt), u.cut.ctx + u.cut.cnt) / BN - u.t0, 0), nt);
+                const int plain = any_bad ? 0 : min(max(min(seen_by_all<MT>(a, u.cut, u.mt), held_of(a, u.cut)) / BN - u.t0, 0), nt);
                 if (mrow && plain == 0) mask_words(a, mrow, u.t0 * BN - u.cut.ctx, words);
                 // scores to probabilities: the running maximum and sum, P over S
                 auto weigh = [&](const float (&x)[128], bool first) {
@@ -589,10 +589,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const bool empty = l == 0.0f || (!live && !ubad);
             const float inv = empty ? 0.0f : 1.0f / l;
             const float log2sum = ubad ? nanv : empty ? -INFINITY : m + log2f(l);
-            if (mine && whole && a.lse) a.lse[orow] = log2sum * kLn2;
+            const bool half = whole && !a.raw;      // 16-bit outputs
+            if (mine && half && a.lse) a.lse[orow] = log2sum * kLn2;
+            if (mine && whole && a.raw) a.raw_log[orow] = log2sum;
             if (mine && !whole) prow[MT * D + st * kRows + r] = log2sum;
             unsigned short* dst = static_cast<unsigned short*>(a.out) + orow * D;
-            float* pdst = prow + (st * kRows + r) * D;
+            float* pdst = whole ? a.raw + orow * D : prow + (st * kRows + r) * D;
             for (int i = 0; i < D; i += 16) {
                 float o[16];
 #pragma unroll
@@ -602,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 if (!mine) continue;
 #pragma unroll
                 for (int y = 0; y < 16; ++y) o[y] = empty ? 0.0f : o[y] * inv;
-                if (whole) {
+                if (half) {
                     store32(dst + i, pack2<F16>(o[0], o[1]), pack2<F16>(o[2], o[3]), pack2<F16>(o[4], o[5]), pack2<F16>(o[6], o[7]),
                             pack2<F16>(o[8], o[9]), pack2<F16>(o[10], o[11]), pack2<F16>(o[12], o[13]), pack2<F16>(o[14], o[15]));
                 } else {
@@ -694,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         uint32_t tiles = 0, step = 0, nq[2] = {0, 0};
         while (w >= kFirst && walk.next(a, part, mts, u)) {
             const int nt = u.len > 0 ? u.t1 - u.t0 : 0;
-            const int all_see = min(seen_by_all<MT>(a, u.cut, u.mt), u.cut.ctx + u.cut.cnt);
+            const int all_see = min(seen_by_all<MT>(a, u.cut, u.mt), held_of(a, u.cut));
             // e4m3: a thread looks after the exponents of rows p and p + 96 of a
             // tile; a row's page is read two tiles ahead, its exponents one
             const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
@@ -962,7 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 bool encode_q(CUtensorMap* map, const AttnArgs& a) {
     const EncodeTiled f = encode_tiled();
     const int64_t strides_in[3] = {a.q_sh, a.q_sn, a.q_sb};
-    if (!f || kRows % a.g || (reinterpret_cast<uintptr_t>(a.q) & 15)) return false;
+    if (!f || kRows % a.g || a.q_n > 0 || (reinterpret_cast<uintptr_t>(a.q) & 15)) return false;
     for (int i = 0; i < 3; ++i)
         if (strides_in[i] <= 0 || strides_in[i] % 16 || strides_in[i] >= (int64_t(1) << 40)) return false;
     const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.c.D), static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.N),

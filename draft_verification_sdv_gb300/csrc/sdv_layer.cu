@@ -11,7 +11,9 @@ using namespace sdv;
 static_assert(SDV_BF16 == kTypeBf16 && SDV_F32 == kTypeF32 && SDV_F16 == kTypeF16 && SDV_E4M3 == kTypeE4m3,
               "public and kernel types must agree");
 static_assert(SDV_STATUS_BAD_TOKEN == kStatusBadDraft && SDV_STATUS_TIMEOUT == kStatusTimeout &&
-                  SDV_STATUS_BAD_PAGE == kStatusBadPage && SDV_STATUS_BAD_LENGTH == kStatusBadLength,
+                  SDV_STATUS_BAD_PAGE == kStatusBadPage && SDV_STATUS_BAD_LENGTH == kStatusBadLength &&
+                  SDV_STATUS_BAD_ROW == kStatusBadRow && SDV_STATUS_BAD_PARAM == kStatusBadTemp &&
+                  SDV_STATUS_NO_PAGES == kStatusNoPages,
               "public and kernel status bits must agree");
 static_assert(SDV_HOOK_ATTN_NO_COPY == kHookAttnNoCopy, "public test hooks and kernel hooks must agree");
 
@@ -101,6 +103,62 @@ bool spans_ok(const CacheView& v, int B, int N, const int32_t* table, int max_pa
     if (B < 1 || N < 1 || max_pages < 1 || !table || misaligned(table, 4)) return false;
     if (static_cast<int64_t>(max_pages) * v.P > (int64_t(1) << 30)) return false;
     return static_cast<int64_t>(B) * N <= (int64_t(1) << 36) / (2 * v.H * 32);
+}
+
+// The arguments that the two kinds of attention share.
+sdv_status attn_args(const sdv_kv_cache* cache, int B, int N, int Hq, sdv_dtype dtype, const void* q, int64_t q_sb, int64_t q_sn,
+                     int64_t q_sh, const int32_t* block_table, int max_pages, const int32_t* ctx_len, const int32_t* count,
+                     const int32_t* mask, int64_t mask_sb, float scale, void* out, float* lse, void* workspace, int32_t* status,
+                     AttnArgs* a) {
+    if (!cache_ok(cache, dtype, false, &a->c) || !spans_ok(a->c, B, N, block_table, max_pages)) return SDV_ERR_ARG;
+    if (Hq < 1 || Hq % a->c.H || N > (1 << 20) || !std::isfinite(scale)) return SDV_ERR_ARG;
+    a->g = Hq / a->c.H;
+    if (static_cast<int64_t>(N) * a->g > (int64_t(1) << 28)) return SDV_ERR_ARG;
+    if (!q || !ctx_len || !out || !workspace) return SDV_ERR_ARG;
+    if (misaligned(q, 2) || misaligned(out, 32) || misaligned(workspace, 32)) return SDV_ERR_ARG;
+    const void* ptrs[9] = {ctx_len, count, mask, lse, status, block_table, q, out, workspace};
+    for (int i = 0; i < 6; ++i)
+        if (misaligned(ptrs[i], 4)) return SDV_ERR_ARG;
+    if (!all_device(ptrs)) return SDV_ERR_ARG;
+    a->q = static_cast<const unsigned char*>(q);
+    a->q_sb = q_sb * 2, a->q_sn = q_sn * 2, a->q_sh = q_sh * 2;
+    a->table = block_table, a->ctx = ctx_len, a->count = count, a->mask = mask, a->mask_sb = mask_sb;
+    a->out = out, a->lse = lse;
+    a->status = reinterpret_cast<unsigned*>(status);
+    a->B = B, a->N = N, a->Hq = Hq, a->W = (N + 31) / 32, a->max_pages = max_pages;
+    a->scale_log2 = scale * 1.4426950408889634f;
+    a->hooks = __atomic_load_n(&test_hooks, __ATOMIC_RELAXED);
+    return SDV_OK;
+}
+
+// Rows of B sequences of N nodes each: the join takes a grid of them.
+bool prefix_shape_ok(int B, int N, int Hq) {
+    return B >= 1 && N >= 1 && Hq >= 1 && N <= (1 << 20) && static_cast<int64_t>(B) * N <= (int64_t(1) << 31) / Hq;
+}
+
+bool pages_ok(int B, int pages, int page_size, int max_pages) {
+    if (B < 1 || B > (1 << 20) || pages < 1 || page_size < 1 || max_pages < 1) return false;
+    return static_cast<int64_t>(max_pages) * page_size <= (int64_t(1) << 30);
+}
+
+// The arguments that a draw and a truncation share.
+sdv_status rows_args(int64_t rows, int per, int V, sdv_dtype dtype, const void* logits, int64_t row_stride, const float* temperature,
+                     const int32_t* top_k, const float* top_p, const float* min_p, int32_t* kept, int32_t* status, RowsArgs* a) {
+    if (dtype != SDV_BF16 && dtype != SDV_F32) return SDV_ERR_ARG;
+    if (rows < 0 || rows > (int64_t(1) << 31) || per < 1 || rows % per || V < 1 || V > kRowsMaxVocab) return SDV_ERR_ARG;
+    if (rows == 0) return SDV_OK;
+    const int elt = dtype == SDV_BF16 ? 2 : 4;
+    if (!logits || misaligned(logits, elt) || row_stride < 0 || row_stride > (int64_t(1) << 40)) return SDV_ERR_ARG;
+    const void* ptrs[7] = {temperature, top_k, top_p, min_p, kept, status, logits};
+    for (int i = 0; i < 6; ++i)
+        if (misaligned(ptrs[i], 4)) return SDV_ERR_ARG;
+    if (!all_device(ptrs)) return SDV_ERR_ARG;
+    a->logits = logits, a->in_stride = row_stride * elt;
+    a->temperature = temperature, a->top_k = top_k, a->top_p = top_p, a->min_p = min_p;
+    a->kept = kept;
+    a->status = reinterpret_cast<unsigned*>(status);
+    a->rows = rows, a->per = per, a->V = V;
+    return SDV_OK;
 }
 
 }  // namespace
@@ -315,28 +373,118 @@ sdv_status sdv_tree_attn(const sdv_kv_cache* cache, int B, int N, int Hq, sdv_dt
                          void* out, float* lse, void* workspace, size_t workspace_bytes,
                          int32_t* status) {
     AttnArgs a{};
-    if (!cache_ok(cache, dtype, false, &a.c) || !spans_ok(a.c, B, N, block_table, max_pages)) return SDV_ERR_ARG;
-    if (Hq < 1 || Hq % a.c.H || N > (1 << 20) || !std::isfinite(scale)) return SDV_ERR_ARG;
-    a.g = Hq / a.c.H;
-    if (static_cast<int64_t>(N) * a.g > (int64_t(1) << 28)) return SDV_ERR_ARG;
-    if (!q || !ctx_len || !out || !workspace) return SDV_ERR_ARG;
-    if (misaligned(q, 2) || misaligned(out, 32) || misaligned(workspace, 32)) return SDV_ERR_ARG;
-    const void* ptrs[9] = {ctx_len, count, mask, lse, status, block_table, q, out, workspace};
-    for (int i = 0; i < 6; ++i)
-        if (misaligned(ptrs[i], 4)) return SDV_ERR_ARG;
-    if (!all_device(ptrs)) return SDV_ERR_ARG;
+    const sdv_status st = attn_args(cache, B, N, Hq, dtype, q, q_sb, q_sn, q_sh, block_table, max_pages, ctx_len, count, mask,
+                                    mask_sb, scale, out, lse, workspace, status, &a);
+    if (st != SDV_OK) return st;
     const int nsm = sm_count();
     if (nsm < 1) return SDV_ERR_CUDA;
     if (workspace_bytes < attn_workspace_bytes(nsm)) return SDV_ERR_SCRATCH;
-    a.q = static_cast<const unsigned char*>(q);
-    a.q_sb = q_sb * 2, a.q_sn = q_sn * 2, a.q_sh = q_sh * 2;
-    a.table = block_table, a.ctx = ctx_len, a.count = count, a.mask = mask, a.mask_sb = mask_sb;
-    a.out = out, a.lse = lse;
-    a.status = reinterpret_cast<unsigned*>(status);
-    a.B = B, a.N = N, a.Hq = Hq, a.W = (N + 31) / 32, a.max_pages = max_pages;
-    a.scale_log2 = scale * 1.4426950408889634f;
-    a.hooks = __atomic_load_n(&test_hooks, __ATOMIC_RELAXED);
     return done(launch_tree_attn(a, dtype, cache->dtype == SDV_E4M3, workspace, nsm, stream_of(stream)));
+}
+
+size_t sdv_prefix_attn_workspace(int B, int N, int Hq, int head_dim) {
+    if (!prefix_shape_ok(B, N, Hq) || head_dim < 16 || head_dim > kCacheMaxDim || head_dim % 16) return 0;
+    const int nsm = sm_count();
+    return nsm > 0 ? prefix_workspace_bytes(static_cast<int64_t>(B) * N * Hq, head_dim, nsm) : 0;
+}
+
+sdv_status sdv_prefix_attn(const sdv_kv_cache* cache, int B, int groups, int N, int Hq, sdv_dtype dtype,
+                           void* stream, const void* q, int64_t q_sb, int64_t q_sn, int64_t q_sh,
+                           const int32_t* prefix_table, int max_prefix_pages,
+                           const int32_t* prefix_len, const int32_t* block_table, int max_pages,
+                           const int32_t* ctx_len, const int32_t* count, const int32_t* mask,
+                           int64_t mask_sb, float scale, void* out, float* lse, void* workspace,
+                           size_t workspace_bytes, int32_t* status) {
+    AttnArgs a{};
+    const sdv_status st = attn_args(cache, B, N, Hq, dtype, q, q_sb, q_sn, q_sh, block_table, max_pages, ctx_len, count, mask,
+                                    mask_sb, scale, out, lse, workspace, status, &a);
+    if (st != SDV_OK) return st;
+    if (groups < 1 || B % groups || !prefix_shape_ok(B, N, Hq) || !prefix_len || misaligned(prefix_len, 4)) return SDV_ERR_ARG;
+    if (!spans_ok(a.c, groups, 1, prefix_table, max_prefix_pages)) return SDV_ERR_ARG;
+    if (static_cast<int64_t>(B / groups) * N * a.g > (int64_t(1) << 28)) return SDV_ERR_ARG;
+    const void* ptrs[2] = {prefix_table, prefix_len};
+    if (!all_device(ptrs)) return SDV_ERR_ARG;
+    const int nsm = sm_count();
+    if (nsm < 1) return SDV_ERR_CUDA;
+    if (workspace_bytes < prefix_workspace_bytes(static_cast<int64_t>(B) * N * Hq, a.c.D, nsm)) return SDV_ERR_SCRATCH;
+    const PrefixArgs p{prefix_table, prefix_len, max_prefix_pages, groups};
+    return done(launch_prefix_attn(a, p, dtype, cache->dtype == SDV_E4M3, workspace, nsm, stream_of(stream)));
+}
+
+sdv_status sdv_pages_extend(int B, int N, int pages, int page_size, int max_pages, void* stream,
+                            int32_t* free_list, int32_t* free_count, int32_t* block_table,
+                            int32_t* held, const int32_t* start, const int32_t* count,
+                            const int32_t* depth, const int32_t* base, int32_t* positions,
+                            int64_t* slots, int32_t* status) {
+    if (!pages_ok(B, pages, page_size, max_pages) || N < 1 || N > (1 << 20)) return SDV_ERR_ARG;
+    if (static_cast<int64_t>(B) * N > (int64_t(1) << 36)) return SDV_ERR_ARG;
+    if (!free_list || !free_count || !block_table || !held || !start || misaligned(slots, 8)) return SDV_ERR_ARG;
+    const void* ptrs[11] = {free_list, free_count, block_table, held, start, count, depth, base, positions, slots, status};
+    for (const void* p : ptrs)
+        if (misaligned(p, 4)) return SDV_ERR_ARG;
+    if (!all_device(ptrs)) return SDV_ERR_ARG;
+    const int nsm = sm_count();
+    if (nsm < 1) return SDV_ERR_CUDA;
+    PagesArgs a{};
+    a.list = free_list, a.free_count = free_count, a.table = block_table, a.held = held;
+    a.start = start, a.count = count, a.depth = depth, a.base = base, a.positions = positions, a.slots = slots;
+    a.status = reinterpret_cast<unsigned*>(status);
+    a.B = B, a.N = N, a.pages = pages, a.P = page_size, a.max_pages = max_pages;
+    return done(launch_pages_extend(a, nsm, stream_of(stream)));
+}
+
+sdv_status sdv_pages_release(int B, int pages, int page_size, int max_pages, void* stream,
+                             int32_t* free_list, int32_t* free_count, int32_t* block_table,
+                             int32_t* held, const int32_t* keep, int32_t* status) {
+    if (!pages_ok(B, pages, page_size, max_pages)) return SDV_ERR_ARG;
+    if (!free_list || !free_count || !block_table || !held || !keep) return SDV_ERR_ARG;
+    const void* ptrs[6] = {free_list, free_count, block_table, held, keep, status};
+    for (const void* p : ptrs)
+        if (misaligned(p, 4)) return SDV_ERR_ARG;
+    if (!all_device(ptrs)) return SDV_ERR_ARG;
+    const int nsm = sm_count();
+    if (nsm < 1) return SDV_ERR_CUDA;
+    PagesArgs a{};
+    a.list = free_list, a.free_count = free_count, a.table = block_table, a.held = held, a.start = keep;
+    a.status = reinterpret_cast<unsigned*>(status);
+    a.B = B, a.pages = pages, a.P = page_size, a.max_pages = max_pages;
+    return done(launch_pages_release(a, nsm, stream_of(stream)));
+}
+
+sdv_status sdv_sample(int64_t rows, int per, int V, sdv_dtype dtype, void* stream, const void* logits,
+                      int64_t row_stride, const float* temperature, const int32_t* top_k,
+                      const float* top_p, const float* min_p, const float* uniform, int32_t* tokens,
+                      float* logprob, int32_t* kept, int32_t* status) {
+    RowsArgs a{};
+    const sdv_status st = rows_args(rows, per, V, dtype, logits, row_stride, temperature, top_k, top_p, min_p, kept, status, &a);
+    if (st != SDV_OK || rows == 0) return st;
+    if (!uniform || !tokens) return SDV_ERR_ARG;
+    const void* ptrs[3] = {uniform, tokens, logprob};
+    for (const void* p : ptrs)
+        if (misaligned(p, 4)) return SDV_ERR_ARG;
+    if (!all_device(ptrs)) return SDV_ERR_ARG;
+    const int nsm = sm_count();
+    if (nsm < 1) return SDV_ERR_CUDA;
+    a.uniform = uniform, a.tokens = tokens, a.logprob = logprob;
+    return done(launch_rows(a, dtype == SDV_BF16, true, nsm, stream_of(stream)));
+}
+
+sdv_status sdv_logits_truncate(int64_t rows, int per, int V, sdv_dtype dtype, void* stream,
+                               const void* logits, int64_t row_stride, const float* temperature,
+                               const int32_t* top_k, const float* top_p, const float* min_p, void* out,
+                               int64_t out_stride, int32_t* kept, int32_t* status) {
+    RowsArgs a{};
+    const sdv_status st = rows_args(rows, per, V, dtype, logits, row_stride, temperature, top_k, top_p, min_p, kept, status, &a);
+    if (st != SDV_OK || rows == 0) return st;
+    const int elt = dtype == SDV_BF16 ? 2 : 4;
+    if (!out || misaligned(out, elt) || (rows > 1 && out_stride < V) || out_stride > (int64_t(1) << 40)) return SDV_ERR_ARG;
+    if (out == logits && rows > 1 && out_stride != row_stride) return SDV_ERR_ARG;
+    const void* ptrs[1] = {out};
+    if (!all_device(ptrs)) return SDV_ERR_ARG;
+    const int nsm = sm_count();
+    if (nsm < 1) return SDV_ERR_CUDA;
+    a.out = out, a.out_stride = out_stride * elt;
+    return done(launch_rows(a, dtype == SDV_BF16, false, nsm, stream_of(stream)));
 }
 
 }  // extern "C"

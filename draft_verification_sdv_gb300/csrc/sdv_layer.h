@@ -11,6 +11,7 @@ namespace sdv {
 
 constexpr int kTypeBf16 = 0, kTypeF32 = 1, kTypeF16 = 2, kTypeE4m3 = 3;
 constexpr unsigned kStatusBadPage = 64u;     // a page id outside the cache
+constexpr unsigned kStatusNoPages = 128u;    // the free pages ran out
 
 constexpr int kTreeMaxDrafts = 64;
 constexpr int kTreeMaxGamma = 128;
@@ -72,15 +73,19 @@ struct AttnArgs {
     CacheView c;
     const unsigned char* q;
     int64_t q_sb, q_sn, q_sh;         // bytes
+    int q_n;                          // > 0: nodes q_n apart are q_s2 bytes apart, those between q_sn
+    int64_t q_s2;
     const int32_t *table, *ctx, *count, *mask;
     int64_t mask_sb;                  // words
     void* out;
     float* lse;
+    float *raw, *raw_log;             // not NULL: rows go here as fp32, with the base-2 logs of their sums
     unsigned* status;
     float* part;                      // partial outputs (see part_rows)
     int4* desc;                       // two per CTA: the unit that its start splits
     unsigned* beyond;                 // one per SM: see launch_attn_redo
-    int B, N, Hq, g, W, max_pages;
+    int B, N, Hq, g, max_pages;
+    int W;                            // words of a mask row; 0: no node's keys are in the cache (mask is then not read)
     float scale_log2;                 // scale * log2(e)
     int ctas, rounds;                 // see k8_attn.cuh
     unsigned hooks;                   // kHook* bits (tests of the waits)
@@ -91,6 +96,15 @@ constexpr unsigned kHookAttnNoCopy = 2u;
 size_t attn_workspace_bytes(int nsm);
 cudaError_t launch_tree_attn(AttnArgs a, int type, bool e4m3, void* workspace, int nsm,
                              cudaStream_t s);
+
+// The prefixes of `groups` groups of sequences (the groups' sequences are a.B / groups).
+struct PrefixArgs {
+    const int32_t *table, *len;
+    int max_pages, groups;
+};
+size_t prefix_workspace_bytes(int64_t rows, int D, int nsm);      // rows: B * N * Hq
+cudaError_t launch_prefix_attn(const AttnArgs& a, const PrefixArgs& p, int type, bool e4m3, void* workspace, int nsm,
+                               cudaStream_t s);
 
 struct LogitsArgs {
     const void* logits;
@@ -110,5 +124,31 @@ struct CountsArgs {
     int B, K, G, V;
 };
 cudaError_t launch_counts_commit(const CountsArgs& a, cudaStream_t s);
+
+struct PagesArgs {
+    int32_t *list, *free_count, *table, *held;
+    const int32_t *start, *count, *depth, *base;      // (release: start is what is kept)
+    int32_t* positions;
+    int64_t* slots;
+    unsigned* status;
+    int B, N, pages, P, max_pages;
+};
+cudaError_t launch_pages_extend(const PagesArgs& a, int nsm, cudaStream_t s);
+cudaError_t launch_pages_release(const PagesArgs& a, int nsm, cudaStream_t s);
+
+constexpr int kRowsMaxVocab = 1 << 19;       // sums of that many weights fit 64 bits
+struct RowsArgs {
+    const void* logits;
+    int64_t in_stride, out_stride;            // bytes
+    const float *temperature, *top_p, *min_p, *uniform;
+    const int32_t* top_k;
+    void* out;
+    int32_t *tokens, *kept;
+    float* logprob;
+    unsigned* status;
+    int64_t rows;
+    int per, V;
+};
+cudaError_t launch_rows(const RowsArgs& a, bool bf16, bool draw, int nsm, cudaStream_t s);
 
 }  // namespace sdv

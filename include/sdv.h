@@ -478,8 +478,11 @@ sdv_status sdv_verify_static(int B, int K, int gamma, int V, sdv_dtype dtype, vo
  * at each call, and no memory outside the caller's buffers is touched.
  * --------------------------------------------------------------------- */
 #define SDV_STATUS_BAD_TOKEN 1      /* a token id outside [0, V)                      */
+#define SDV_STATUS_BAD_ROW 2        /* a row with a NaN or +infinity, or nothing finite */
+#define SDV_STATUS_BAD_PARAM 4      /* a sampling parameter outside its range         */
 #define SDV_STATUS_TIMEOUT 8        /* a bounded device wait gave up                  */
 #define SDV_STATUS_BAD_PAGE 64      /* a page id outside [0, pages)                   */
+#define SDV_STATUS_NO_PAGES 128     /* the free pages ran out                         */
 
 /*
  * The tree of K drafts.  Node 0 is the sequence's last committed token (the
@@ -586,6 +589,53 @@ typedef struct sdv_kv_cache {
 } sdv_kv_cache;
 
 /*
+ * Pages for new tokens, from request lengths.  The free pages are a stack,
+ * free_list[0 .. *free_count - 1], and sequence b holds the first held[b] pages
+ * of its row of block_table.  For positions start[b] .. start[b] + count[b] - 1
+ * (count NULL: N) it needs ceil((start[b] + count[b]) / page_size) pages; those
+ * it lacks are taken from the stack's top, sequence by sequence in order, and
+ * go to its row, and held and *free_count follow.  Where the stack does not last,
+ * a sequence for which it no longer does takes nothing (SDV_STATUS_NO_PAGES), nor
+ * does any after it that lacks a page.
+ *   free_list  device int32 [pages]
+ *   free_count device int32 [1], held device int32 [B]
+ *   block_table device int32 [B][max_pages]
+ *   depth      device int32 [B][N] (sdv_tree_build's) or NULL: n
+ *   base       device int32 [B] or NULL: 0 (a shared prefix's length)
+ *   positions  device int32 [B][N] or NULL: base[b] + start[b] + depth[b][n], as
+ *              sdv_rope takes them; 0 from count[b] on
+ *   slots      device int64 [B][N] or NULL: place (start[b] + n) of the cache,
+ *              page * page_size + place in the page; -1 from count[b] on and
+ *              where there is no page (or a bad one)
+ * A held outside [0, max_pages], a negative start, a count outside [0, N], or a
+ * sum beyond max_pages * page_size sets SDV_STATUS_BAD_LENGTH, and the sequence
+ * takes nothing and has no slots; *free_count outside [0, pages] sets it too, and
+ * no sequence takes anything.  An entry of the list outside [0, pages) sets
+ * SDV_STATUS_BAD_PAGE and is handed out as it is (the cache's entry points refuse
+ * it).  N <= 2^20, B <= 2^20, max_pages * page_size <= 2^30.
+ */
+sdv_status sdv_pages_extend(int B, int N, int pages, int page_size, int max_pages, void* stream,
+                            int32_t* free_list, int32_t* free_count, int32_t* block_table,
+                            int32_t* held, const int32_t* start, const int32_t* count,
+                            const int32_t* depth, const int32_t* base, int32_t* positions,
+                            int64_t* slots, int32_t* status);
+
+/*
+ * Give back the pages behind the first keep[b] positions of each sequence (0:
+ * all it holds): its entries of block_table from place ceil(keep[b] / page_size)
+ * on go to the stack and become -1, and held and *free_count follow.  A keep
+ * beyond what is held changes nothing.  They go back in the order that returns the
+ * stack to what it was when they were just taken by sdv_pages_extend.  A negative
+ * keep or a held outside [0, max_pages] sets SDV_STATUS_BAD_LENGTH, and the
+ * sequence keeps all; so does a *free_count that is out of range or would exceed
+ * `pages`, and all keep all.  An entry outside [0, pages) sets SDV_STATUS_BAD_PAGE
+ * and goes back as it is.
+ */
+sdv_status sdv_pages_release(int B, int pages, int page_size, int max_pages, void* stream,
+                             int32_t* free_list, int32_t* free_count, int32_t* block_table,
+                             int32_t* held, const int32_t* keep, int32_t* status);
+
+/*
  * Write the keys and values of up to N new positions per sequence: row n of
  * sequence b goes to position start[b] + n, for n < count[b] (NULL: N).
  *   k, v       device [B][N][kv_heads][D] of `dtype` (SDV_BF16 or SDV_F16; the
@@ -680,6 +730,36 @@ sdv_status sdv_tree_attn(const sdv_kv_cache* cache, int B, int N, int Hq, sdv_dt
                          int32_t* status);
 
 /*
+ * The same attention for sequences that share prefixes, each prefix read once
+ * for all of its sequences.  The B sequences form `groups` groups of B / groups
+ * (a whole number), in order; those of group j follow a prefix of prefix_len[j]
+ * positions whose keys and values are on pages of their own, position t at place
+ * t % page_size of page prefix_table[j][t / page_size].  What a sequence adds
+ * begins on a new page: node i of sequence b sees the whole prefix of its group,
+ * then what it sees in sdv_tree_attn, which all other arguments are as for.
+ * (sdv_kv_write and sdv_kv_commit take block_table and ctx_len; a node's position
+ * for sdv_rope is prefix_len + ctx_len + depth.)
+ *   prefix_table  device int32 [groups][max_prefix_pages]
+ *   prefix_len    device int32 [groups], 0 <= prefix_len <= max_prefix_pages * page_size
+ *   workspace     at least sdv_prefix_attn_workspace(B, N, Hq, head_dim) bytes,
+ *                 32-byte aligned, that no other call uses until this one is done
+ * The nodes of a group whose prefix_len is out of range get NaN in out and lse
+ * (nodes from count[b] on stay 0 and -inf); the other failures are those of
+ * sdv_tree_attn.  B * N * Hq <= 2^31, and (B / groups) * N query rows of a kv head
+ * at most 2^28.  Results of the two parts are joined in fp32.
+ * sdv_prefix_attn_workspace: 0 for a bad shape, or when the device cannot be
+ * asked.
+ */
+size_t sdv_prefix_attn_workspace(int B, int N, int Hq, int head_dim);
+sdv_status sdv_prefix_attn(const sdv_kv_cache* cache, int B, int groups, int N, int Hq, sdv_dtype dtype,
+                           void* stream, const void* q, int64_t q_sb, int64_t q_sn, int64_t q_sh,
+                           const int32_t* prefix_table, int max_prefix_pages,
+                           const int32_t* prefix_len, const int32_t* block_table, int max_pages,
+                           const int32_t* ctx_len, const int32_t* count, const int32_t* mask,
+                           int64_t mask_sb, float scale, void* out, float* lse, void* workspace,
+                           size_t workspace_bytes, int32_t* status);
+
+/*
  * Fault-path test hook of later sdv_tree_attn calls of the process (not part of
  * the method).  With SDV_HOOK_ATTN_NO_COPY the kernels that load by tile copies
  * (head_dim <= 128, page_size a multiple of 8) leave the copies of the first
@@ -739,6 +819,54 @@ sdv_status sdv_logits_process(int B, int K, int gamma, int V, sdv_dtype dtype, v
 sdv_status sdv_counts_commit(int B, int K, int gamma, int V, void* stream, const int32_t* drafts,
                              const int32_t* sel, const int32_t* accept_len,
                              const int32_t* next_token, int32_t* counts, int32_t* status);
+
+/*
+ * Draws from rows of logits, and their truncation.  Rows r / per share one entry
+ * of the parameters.  A row's tokens are ordered by falling logit, equal ones by
+ * index, and token i weighs
+ *   w_i = round(2^44 e^((x_i - max x) / temperature))       (whole numbers)
+ * Of that order a row keeps a first part, cut in turn by
+ *   min_p  to the tokens with x_i >= max x + temperature * ln(min_p)
+ *   top_k  to the first top_k
+ *   top_p  to those before which less than top_p * W lies, W being the weight of
+ *          what the others keep
+ * and a logit of -infinity is never kept.  temperature 0 keeps the first token
+ * alone.  Since weights are whole numbers, what is kept and drawn does not depend
+ * on how a row is shared out; the two products with W are rounded to 64-bit
+ * floating point, as is W.
+ *   logits     device [rows] of V logits, row_stride elements apart (0 with one
+ *              row, or to draw from one row several times)
+ *   temperature  device float [rows / per], 0 or 2^-64 .. 2^64, or NULL: 1
+ *   top_k      device int32 [rows / per], >= 0 (0: all), or NULL
+ *   top_p      device float [rows / per], in (0, 1], or NULL: 1
+ *   min_p      device float [rows / per], in [0, 1], or NULL: 0
+ *   kept       device int32 [rows] or NULL: how many tokens the row keeps
+ * dtype SDV_BF16 or SDV_F32; any V <= 2^19, aligned to an element; rows a multiple
+ * of per, at most 2^31.  A row that holds a NaN or +infinity, or nothing finite,
+ * sets SDV_STATUS_BAD_ROW; a parameter outside its range sets
+ * SDV_STATUS_BAD_PARAM: kept is then 0, and the outputs what is said below.
+ *
+ * sdv_sample: the token of each row where the running sum of kept weights passes
+ * u * (their sum).
+ *   uniform    device float [rows], u in [0, 1)
+ *   tokens     device int32 [rows]; -1 for a bad row
+ *   logprob    device float [rows] or NULL: ln(w / (sum of kept weights)); NaN for
+ *              a bad row
+ *
+ * sdv_logits_truncate: the logits, -infinity where a token is not kept (a bad
+ * row: NaN), unscaled: sdv_verify on such rows, with the same temperatures, is
+ * lossless for the truncated distribution.
+ *   out        device [rows] of V, out_stride elements apart; it may be logits
+ *              with the same stride (in place), and must not overlap it otherwise
+ */
+sdv_status sdv_sample(int64_t rows, int per, int V, sdv_dtype dtype, void* stream, const void* logits,
+                      int64_t row_stride, const float* temperature, const int32_t* top_k,
+                      const float* top_p, const float* min_p, const float* uniform, int32_t* tokens,
+                      float* logprob, int32_t* kept, int32_t* status);
+sdv_status sdv_logits_truncate(int64_t rows, int per, int V, sdv_dtype dtype, void* stream,
+                               const void* logits, int64_t row_stride, const float* temperature,
+                               const int32_t* top_k, const float* top_p, const float* min_p, void* out,
+                               int64_t out_stride, int32_t* kept, int32_t* status);
 
 #ifdef __cplusplus
 }
