@@ -352,6 +352,28 @@ def test_rows_of_a_vocabulary(V, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_with_very_many_of_one_value(dtype):
+    """More equal logits than 16 bits count: of either sign, zeros of both, and
+    places that a grammar masks."""
+    V = 140000
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.randn((6, 1, V), generator=g, device="cuda")
+    many = torch.rand(V, generator=g, device="cuda") < 0.6
+    x[0, 0, many], x[1, 0, many], x[2, 0, many] = 1.5, -1.5, -math.inf
+    x[3, 0, many] = 0.0
+    x[3, 0, ::2] *= -1.0                             # half of the zeros are negative
+    x[4, 0] = torch.where(many, 2.0, -math.inf)
+    x[5, 0, many], x[5, 0, ~many] = -math.inf, 0.25
+    cut = dict(temperature=[1.0, 0.7, 1.0, 2.0, 1.0, 0.0], top_k=[0, 100000, 0, 90000, 70001, 0],
+               top_p=[0.5, 1.0, 0.9, 0.7, 1.0, 1.0], min_p=[0.0, 0.0, 0.1, 0.0, 0.0, 0.0])
+    _check_rows(x.to(dtype), cut, 3)
+    x[0, 0, 5], x[1, 0, 77], x[2, 0, :70000] = math.nan, math.inf, math.inf
+    st = _status()
+    got = bd.sdv_sample(x[:3].to(dtype), torch.zeros((3, 1), device="cuda"), status=st)
+    assert int(st) == bd.SDV_STATUS_BAD_ROW and (got == -1).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_row_strides_alignment_and_places(dtype):
     """Rows that begin anywhere, apart by more than their length, in place, and
     several draws of one row; nothing beside the rows is written."""
