@@ -13,20 +13,20 @@ namespace {
 
 using namespace rows;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 512, kBins = 4096;
 
-template <bool DRAW> __global__ void __launch_bounds__(kThreads) rows_f32_kernel(const RowsArgs a) {
+template <bool DRAW> __global__ void __launch_bounds__(kThreads, 2) rows_f32_kernel(const RowsArgs a) {
     extern __shared__ __align__(16) unsigned char raw[];
-    PassSmem<kThreads>& sm = *reinterpret_cast<PassSmem<kThreads>*>(raw);
+    PassSmem<kThreads, kBins>& sm = *reinterpret_cast<PassSmem<kThreads, kBins>*>(raw);
     load_tables(sm.tables, threadIdx.x, kThreads);
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        row_in_passes<false, DRAW, kThreads>(a, r, sm);
+        row_in_passes<false, DRAW, kThreads, kBins>(a, r, sm);
         __syncthreads();
     }
 }
 
 template <bool DRAW> cudaError_t launch(const RowsArgs& a, int nsm, cudaStream_t s) {
-    constexpr size_t bytes = sizeof(PassSmem<kThreads>);
+    constexpr size_t bytes = sizeof(PassSmem<kThreads, kBins>);
     const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(rows_f32_kernel<DRAW>), bytes);
     if (e != cudaSuccess) return e;
     const int64_t ctas = a.rows < 2 * nsm ? a.rows : 2 * nsm;

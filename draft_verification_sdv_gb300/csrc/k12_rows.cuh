@@ -12,7 +12,7 @@
 // 2^44 e^(-d / T) is computed in pairs of fp32 numbers: p = d log2(e) / T to 2^-47
 // of itself, 2^(frac p) as a product of two table entries (7 bits each) and
 // 1 + z + z^2 / 2 + z^3 / 6 with |z| < 2^-15, in 62-bit fixed point.  It is off
-// by well under a unit below 2^42 and by 2^-44 of itself above.
+// by less than a unit.
 #pragma once
 
 #include "sdv_device.cuh"
@@ -58,14 +58,21 @@ struct Scale {
     float hi, lo;            // 2 log2(e) / T
 };
 
-__device__ __forceinline__ Scale scale_of(float top, float T) {
-    Scale s;
+// What one thread works out in 64 bits, of which an SM has few lanes: the factor,
+// and how far below the largest logit min-p reaches (T ln(min_p)).
+struct Factors {
+    float hi, lo;
+    double reach;
+};
+__device__ __forceinline__ Factors factors_of(float T, float min_p) {
+    Factors f;
     const double c = 2.8853900817779268147 / static_cast<double>(T);
-    s.top = top;
-    s.hi = static_cast<float>(c);
-    s.lo = static_cast<float>(c - static_cast<double>(s.hi));
-    return s;
+    f.hi = static_cast<float>(c);
+    f.lo = static_cast<float>(c - static_cast<double>(f.hi));
+    f.reach = min_p > 0.0f ? static_cast<double>(T) * log(static_cast<double>(min_p)) : 0.0;
+    return f;
 }
+__device__ __forceinline__ float floor_of(float top, double reach) { return __double2float_ru(static_cast<double>(top) + reach); }
 
 // How far x lies below the largest, in halvings of the weight, as an fp32
 // number; `low` is what it lacks.
@@ -83,7 +90,7 @@ __device__ __forceinline__ float fall_of(const Scale& s, float x, float& low) {
 __device__ __forceinline__ uint64_t weight_of(const Scale& s, float x, const Tables& t) {
     if (x == s.top) return uint64_t(1) << kOneBits;
     float low;
-    const float p = fall_of(s, x, low);
+    const float p = fmaxf(fall_of(s, x, low), 0.0f);
     if (!(p < kFallMost)) return 0;
     const float k = rintf(p), f = k - p;                         // exact; 2^-p = 2^-k 2^f
     const int i = __float2int_rn(f * 128.0f);
@@ -94,12 +101,41 @@ __device__ __forceinline__ uint64_t weight_of(const Scale& s, float x, const Tab
     const float y = __fmul_rn(z, 0.693147182f);                  // z ln 2, and what that lacks
     const float yl = __fmaf_rn(z, 0.693147182f, -y) + __fmaf_rn(z, -1.90465421e-9f, __fmul_rn(zl, 0.693147182f));
     const float more = yl + __fmul_rn(__fmul_rn(y, y), __fmaf_rn(y, 0.166666667f, 0.5f));
-    const int64_t one = int64_t(1) << 62;
-    const uint64_t q = static_cast<uint64_t>(one + __float2ll_rn(y * 0x1p62f) + __float2ll_rn(more * 0x1p62f));
+    // (32-bit conversions: 64-bit ones share the few 64-bit lanes)
+    const int32_t frac = __float2int_rn(y * 0x1p46f) + __float2int_rn(more * 0x1p46f);
+    const uint64_t q = static_cast<uint64_t>((int64_t(1) << 62) + (static_cast<int64_t>(frac) << 16));
     const uint64_t ab = __umul64hi(t.coarse[i + 64], t.fine[j + 64]) << 2;
     const uint64_t w = __umul64hi(ab, q) << 2;                   // 2^f in units of 2^-62
     const int shift = 62 - kOneBits + static_cast<int>(k);       // 18 .. 63
     return ((w >> (shift - 1)) + 1) >> 1;
+}
+
+// u * w and p * w for an fp32 number in [0, 1), exact but for the last step: rounded
+// down, or up.
+__device__ __forceinline__ uint64_t times_down(float u, uint64_t w) {
+    const int e = static_cast<int>(__float_as_uint(u) >> 23);                  // u = m 2^(max(e, 1) - 150)
+    const uint64_t m = (__float_as_uint(u) & 0x7fffffu) | (e > 0 ? 0x800000u : 0u);
+    const int shift = 150 - (e > 0 ? e : 1);                     // 24 .. 149
+    const uint64_t lo = m * w, hi = __umul64hi(m, w);
+    if (shift >= 128) return 0;
+    return shift >= 64 ? hi >> (shift - 64) : (lo >> shift) | (hi << (64 - shift));
+}
+__device__ __forceinline__ uint64_t times_up(float p, uint64_t w) {
+    const int e = static_cast<int>(__float_as_uint(p) >> 23);
+    const uint64_t m = (__float_as_uint(p) & 0x7fffffu) | (e > 0 ? 0x800000u : 0u);
+    const int shift = 150 - (e > 0 ? e : 1);
+    const uint64_t lo = m * w, hi = __umul64hi(m, w);
+    if (shift >= 128) return 1;                                  // (neither is 0)
+    const uint64_t down = shift >= 64 ? hi >> (shift - 64) : (lo >> shift) | (hi << (64 - shift));
+    const bool left = shift >= 64 ? lo != 0 || (hi & ((uint64_t(1) << (shift - 64)) - 1)) != 0 : (lo & ((uint64_t(1) << shift) - 1)) != 0;
+    return down + left;
+}
+
+// ln(unit / weight), a quotient of whole weights.
+__device__ __forceinline__ float log_share(uint64_t unit, uint64_t weight) {
+    const uint64_t rest = weight - unit;
+    const float f = __ull2float_rn(rest < unit ? rest : unit) / __ull2float_rn(weight);
+    return rest < unit ? log1pf(-f) : logf(f);
 }
 
 // Logits in order: a larger one has a larger key, and both zeros the same.
@@ -111,19 +147,19 @@ __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k &
 constexpr uint32_t kKeyLow = 0x007fffffu;    // -infinity
 constexpr uint32_t kKeyHigh = 0xff800000u;   // +infinity; keys outside the two are not numbers
 
-constexpr int kBins = 4096;
-constexpr float kBinsPerHalving = 64.0f;
 
-struct Hist {
-    uint64_t mass[kBins];
-    uint32_t count[kBins];
+template <int BINS> struct Hist {
+    uint64_t mass[BINS];
+    uint32_t count[BINS];
 };
 
-template <int THREADS> struct PassSmem {
+template <int THREADS, int BINS> struct PassSmem {
     Tables tables;
-    Hist first, next;
+    Hist<BINS> first, next;
     uint64_t sum[2][THREADS / 32];
     uint32_t word[THREADS / 32];
+    Factors factors;
+    float floor;
     // what `locate` has found
     uint64_t before_w, at_w;
     uint32_t before_n, at_n;
@@ -195,8 +231,9 @@ template <int THREADS> __device__ __forceinline__ uint32_t block_sum(uint32_t x,
 
 // The bin of a histogram where the running count (or weight) passes `target`:
 // into sm.bin and what comes before it and lies in it.
-template <int THREADS> __device__ __forceinline__ void pick(PassSmem<THREADS>& sm, const Hist& h, bool by_weight, uint64_t target) {
-    constexpr int kPerThread = kBins / THREADS;
+template <int THREADS, int BINS>
+__device__ __forceinline__ void pick(PassSmem<THREADS, BINS>& sm, const Hist<BINS>& h, bool by_weight, uint64_t target) {
+    constexpr int kPerThread = BINS / THREADS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t n = 0, w = 0;
     for (int i = 0; i < kPerThread; ++i) n += h.count[tid * kPerThread + i], w += h.mass[tid * kPerThread + i];
@@ -228,7 +265,7 @@ template <int THREADS> __device__ __forceinline__ void pick(PassSmem<THREADS>& s
     __syncthreads();
 }
 
-template <bool BF16, int THREADS> struct Row {
+template <bool BF16, int THREADS, int BINS> struct Row {
     const unsigned char* at;
     int V;
     bool vec;
@@ -236,7 +273,7 @@ template <bool BF16, int THREADS> struct Row {
     float bins;                      // per unit of logit
     uint32_t low;                    // key of the smallest finite logit
     __device__ __forceinline__ int bin_of(float x) const {
-        return static_cast<int>(fminf((scale.top - x) * bins, static_cast<float>(kBins - 1)));
+        return static_cast<int>(fminf((scale.top - x) * bins, static_cast<float>(BINS - 1)));
     }
     template <class F> __device__ __forceinline__ void each(F f) const {
         constexpr int E = kStep<BF16>;
@@ -249,7 +286,7 @@ template <bool BF16, int THREADS> struct Row {
     }
     // The place where the running count (weight) of the order passes `target`
     // (which lies below its total).
-    __device__ Place locate(PassSmem<THREADS>& sm, bool by_weight, uint64_t target) const {
+    __device__ Place locate(PassSmem<THREADS, BINS>& sm, bool by_weight, uint64_t target) const {
         pick(sm, sm.first, by_weight, target);
         Place p{0, sm.before_n, sm.at_n, sm.before_w};
         const int bin = sm.bin;
@@ -271,11 +308,11 @@ template <bool BF16, int THREADS> struct Row {
                 b = m - 1;
             hi = a;
         }
-        for (int level = 0; level < 3 && lo != hi; ++level) {    // (a level settles 12 bits)
+        for (int level = 0; level < 4 && lo != hi; ++level) {    // (a level settles 10 bits or more)
             int shift = 0;
-            while ((hi - lo) >> shift >= kBins) ++shift;
+            while ((hi - lo) >> shift >= BINS) ++shift;
             __syncthreads();
-            for (int i = threadIdx.x; i < kBins; i += THREADS) sm.next.count[i] = 0, sm.next.mass[i] = 0;
+            for (int i = threadIdx.x; i < BINS; i += THREADS) sm.next.count[i] = 0, sm.next.mass[i] = 0;
             __syncthreads();
             each([&](float x) {
                 const uint32_t k = key_of(x);
@@ -304,7 +341,7 @@ struct Ask {
 };
 
 __device__ __forceinline__ Ask ask_of(const RowsArgs& a, int64_t row) {
-    const int64_t g = row / a.per;
+    const uint32_t g = a.per == 1 ? static_cast<uint32_t>(row) : static_cast<uint32_t>(row) / static_cast<uint32_t>(a.per);
     Ask q;
     q.T = a.temperature ? a.temperature[g] : 1.0f;
     q.top_k = a.top_k ? a.top_k[g] : 0;
@@ -318,13 +355,13 @@ __device__ __forceinline__ Ask ask_of(const RowsArgs& a, int64_t row) {
 
 // One row, in passes: for rows in 32 bits, and for those in 16 whose counts do not fit
 // k12_rows_bf16.cu's.  All threads of the CTA; sm.tables is filled.
-template <bool BF16, bool DRAW, int THREADS>
-__device__ __noinline__ void row_in_passes(const RowsArgs& a, int64_t r, PassSmem<THREADS>& sm) {
+template <bool BF16, bool DRAW, int THREADS, int BINS>
+__device__ __noinline__ void row_in_passes(const RowsArgs& a, int64_t r, PassSmem<THREADS, BINS>& sm) {
     constexpr int E = kStep<BF16>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float nan = __int_as_float(0x7fc00000);
     const Ask q = ask_of(a, r);
-    Row<BF16, THREADS> row;
+    Row<BF16, THREADS, BINS> row;
     row.at = static_cast<const unsigned char*>(a.logits) + r * a.in_stride;
     row.V = a.V;
     row.vec = (reinterpret_cast<uintptr_t>(row.at) & 15) == 0;
@@ -342,7 +379,7 @@ __device__ __noinline__ void row_in_passes(const RowsArgs& a, int64_t r, PassSme
     high = __reduce_max_sync(0xffffffffu, high);
     low = __reduce_min_sync(0xffffffffu, low);
     if (lane == 0) sm.sum[0][warp] = high, sm.sum[1][warp] = low;
-    for (int i = tid; i < kBins; i += THREADS) sm.first.count[i] = 0, sm.first.mass[i] = 0;
+    for (int i = tid; i < BINS; i += THREADS) sm.first.count[i] = 0, sm.first.mass[i] = 0;
     odd = __syncthreads_or(odd);
     for (int i = 0; i < (THREADS / 32); ++i) high = max(high, static_cast<uint32_t>(sm.sum[0][i])), low = min(low, static_cast<uint32_t>(sm.sum[1][i]));
     finite = block_sum<THREADS>(finite, sm.word);
@@ -375,10 +412,14 @@ __device__ __noinline__ void row_in_passes(const RowsArgs& a, int64_t r, PassSme
         kept = 1, share = 1, last.key = high;
         weight = unit = uint64_t(1) << kOneBits;
     } else {
-        row.scale = scale_of(top, q.T);
-        row.bins = kBinsPerHalving * 0.5f * row.scale.hi;
-        const float floor = q.min_p > 0.0f ? __double2float_ru(static_cast<double>(top) + static_cast<double>(q.T) * log(static_cast<double>(q.min_p)))
-                                           : -INFINITY;
+        if (tid == 0) {
+            sm.factors = factors_of(q.T, q.min_p);
+            sm.floor = q.min_p > 0.0f ? floor_of(top, sm.factors.reach) : -INFINITY;
+        }
+        __syncthreads();
+        row.scale = Scale{top, sm.factors.hi, sm.factors.lo};
+        row.bins = (BINS / 64) * 0.5f * row.scale.hi;
+        const float floor = sm.floor;
         uint32_t over = 0;
         uint64_t sum = 0;
         row.each([&](float x) {
@@ -411,12 +452,12 @@ __device__ __noinline__ void row_in_passes(const RowsArgs& a, int64_t r, PassSme
         }
         if (q.top_p < 1.0f) {
             // tokens while what comes before them weighs less than this
-            const uint64_t need = __double2ull_ru(static_cast<double>(q.top_p) * static_cast<double>(weight));
+            const uint64_t need = times_up(q.top_p, weight);
             const Place p = row.locate(sm, true, need - 1);
             cut(p, static_cast<uint32_t>((need - 1 - p.before_w) / weight_of(row.scale, of_key(p.key), sm.tables)) + 1);
         }
         if (DRAW) {
-            aim = static_cast<uint64_t>(static_cast<double>(q.u) * static_cast<double>(weight));
+            aim = times_down(q.u, weight);
             drawn = row.locate(sm, true, aim);
             unit = weight_of(row.scale, of_key(drawn.key), sm.tables);
         }
@@ -469,12 +510,7 @@ __device__ __noinline__ void row_in_passes(const RowsArgs& a, int64_t r, PassSme
                     if (m >> y & 1) {
                         if (at == rank) {
                             a.tokens[r] = (s * 32 + lane) * E + y;
-                            if (a.logprob) {
-                                const uint64_t rest = weight - unit;
-                                const double part = rest < unit ? static_cast<double>(rest) : static_cast<double>(unit);
-                                const float f = static_cast<float>(part / static_cast<double>(weight));
-                                a.logprob[r] = rest < unit ? log1pf(-f) : logf(f);
-                            }
+                            if (a.logprob) a.logprob[r] = log_share(unit, weight);
                         }
                         ++at;
                     }

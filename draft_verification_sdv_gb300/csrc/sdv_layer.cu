@@ -145,7 +145,7 @@ bool pages_ok(int B, int pages, int page_size, int max_pages) {
 sdv_status rows_args(int64_t rows, int per, int V, sdv_dtype dtype, const void* logits, int64_t row_stride, const float* temperature,
                      const int32_t* top_k, const float* top_p, const float* min_p, int32_t* kept, int32_t* status, RowsArgs* a) {
     if (dtype != SDV_BF16 && dtype != SDV_F32) return SDV_ERR_ARG;
-    if (rows < 0 || rows > (int64_t(1) << 31) || per < 1 || rows % per || V < 1 || V > kRowsMaxVocab) return SDV_ERR_ARG;
+    if (rows < 0 || rows >= (int64_t(1) << 31) || per < 1 || rows % per || V < 1 || V > kRowsMaxVocab) return SDV_ERR_ARG;
     if (rows == 0) return SDV_OK;
     const int elt = dtype == SDV_BF16 ? 2 : 4;
     if (!logits || misaligned(logits, elt) || row_stride < 0 || row_stride > (int64_t(1) << 40)) return SDV_ERR_ARG;

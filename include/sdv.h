@@ -842,7 +842,7 @@ sdv_status sdv_counts_commit(int B, int K, int gamma, int V, void* stream, const
  *   min_p      device float [rows / per], in [0, 1], or NULL: 0
  *   kept       device int32 [rows] or NULL: how many tokens the row keeps
  * dtype SDV_BF16 or SDV_F32; any V <= 2^19, aligned to an element; rows a multiple
- * of per, at most 2^31.  A row that holds a NaN or +infinity, or nothing finite,
+ * of per, below 2^31.  A row that holds a NaN or +infinity, or nothing finite,
  * sets SDV_STATUS_BAD_ROW; a parameter outside its range sets
  * SDV_STATUS_BAD_PARAM: kept is then 0, and the outputs what is said below.
  *
