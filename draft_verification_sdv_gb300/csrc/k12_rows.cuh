@@ -88,10 +88,9 @@ __device__ __forceinline__ float fall_of(const Scale& s, float x, float& low) {
 
 // The whole weight of a logit that is at most the largest.
 __device__ __forceinline__ uint64_t weight_of(const Scale& s, float x, const Tables& t) {
-    if (x == s.top) return uint64_t(1) << kOneBits;
     float low;
-    const float p = fmaxf(fall_of(s, x, low), 0.0f);
-    if (!(p < kFallMost)) return 0;
+    const float far = fmaxf(fall_of(s, x, low), 0.0f);
+    const float p = fminf(far, kFallMost);
     const float k = rintf(p), f = k - p;                         // exact; 2^-p = 2^-k 2^f
     const int i = __float2int_rn(f * 128.0f);
     const float g = __fmaf_rn(static_cast<float>(i), -0x1p-7f, f);
@@ -103,11 +102,19 @@ __device__ __forceinline__ uint64_t weight_of(const Scale& s, float x, const Tab
     const float more = yl + __fmul_rn(__fmul_rn(y, y), __fmaf_rn(y, 0.166666667f, 0.5f));
     // (32-bit conversions: 64-bit ones share the few 64-bit lanes)
     const int32_t frac = __float2int_rn(y * 0x1p46f) + __float2int_rn(more * 0x1p46f);
-    const uint64_t q = static_cast<uint64_t>((int64_t(1) << 62) + (static_cast<int64_t>(frac) << 16));
     const uint64_t ab = __umul64hi(t.coarse[i + 64], t.fine[j + 64]) << 2;
-    const uint64_t w = __umul64hi(ab, q) << 2;                   // 2^f in units of 2^-62
+    const uint64_t w = ab + static_cast<uint64_t>((static_cast<int64_t>(static_cast<uint32_t>(ab >> 31)) * frac) >> 15);   // 2^f in units of 2^-62
     const int shift = 62 - kOneBits + static_cast<int>(k);       // 18 .. 63
-    return ((w >> (shift - 1)) + 1) >> 1;
+    const uint64_t rounded = ((w >> (shift - 1)) + 1) >> 1;
+    return x == s.top ? uint64_t(1) << kOneBits : far < kFallMost ? rounded : 0;
+}
+
+// a / b, less than 2^20: off by one at most in fp32.
+__device__ __forceinline__ uint32_t quotient(uint64_t a, uint64_t b) {
+    uint32_t q = __float2uint_rz(__fdividef(__ull2float_rn(a), __ull2float_rn(b)));
+    while (q * b > a) --q;
+    while ((q + 1) * b <= a) ++q;
+    return q;
 }
 
 // u * w and p * w for an fp32 number in [0, 1), exact but for the last step: rounded
@@ -454,7 +461,7 @@ __device__ __noinline__ void row_in_passes(const RowsArgs& a, int64_t r, PassSme
             // tokens while what comes before them weighs less than this
             const uint64_t need = times_up(q.top_p, weight);
             const Place p = row.locate(sm, true, need - 1);
-            cut(p, static_cast<uint32_t>((need - 1 - p.before_w) / weight_of(row.scale, of_key(p.key), sm.tables)) + 1);
+            cut(p, quotient(need - 1 - p.before_w, weight_of(row.scale, of_key(p.key), sm.tables)) + 1);
         }
         if (DRAW) {
             aim = times_down(q.u, weight);
@@ -467,7 +474,7 @@ __device__ __noinline__ void row_in_passes(const RowsArgs& a, int64_t r, PassSme
     // ---- tokens of one logit, counted in the order of their index ----
     // A warp looks after a run of the row, so that counts of runs place it.
     const uint32_t key = DRAW ? drawn.key : last.key;
-    const uint32_t rank = DRAW ? static_cast<uint32_t>((aim - drawn.before_w) / unit) : share;
+    const uint32_t rank = DRAW ? quotient(aim - drawn.before_w, unit) : share;
     const int steps = (a.V + 32 * E - 1) / (32 * E), run = (steps + (THREADS / 32) - 1) / (THREADS / 32);
     const int s0 = min(warp * run, steps), s1 = min(s0 + run, steps);
     auto equals = [&](int s, float (&x)[E]) {    // of this lane's logits of step s

@@ -7,17 +7,18 @@
 // that top-k, min-p and top-p keep, the one that a draw meets.  Only which token of
 // that value it is takes a second look at the row, which is in L2 by then.
 //
-// The histogram has a word for each magnitude from 2^-40 to 2^24, 64 octaves of 128
-// (32 KB, so that two CTAs share an SM and one counts while the other looks for
-// its places); its low half counts positive logits, its high half negative ones.
-// Zeros and -infinity are counted in registers.  A row that holds something else, or
-// more of one value than a half can count (which shows in the sum of all counts)
-// goes the long way, row_in_passes.
+// The histogram has a word for each value whose magnitude lies from 2^-39 to 2^23,
+// 62 octaves of 128 of either sign (64 KB: two CTAs share an SM, and one counts
+// while the other looks for its places).  Smaller and larger magnitudes go to a word
+// at either end, -infinity nowhere; a row where the sum of the counts shows such
+// logits is looked through once more for zeros and infinities, and one that holds
+// other ones goes the long way (row_in_passes).  What bounds the count is the
+// words' banks: 32 lanes hit one of them 3.5 times.
 //
 // Few rows are shared by a cluster of C CTAs, each of which counts a C-th of the
 // row; octave o is looked after by CTA o % C, which adds up the C counts.  A warp
 // takes an octave at a time and sums its counts and weights; warp 0 of the first CTA
-// adds up the 129 sums (octaves of either sign, zeros between them) in the order
+// adds up the 125 sums (octaves of either sign, zeros between them) in the order
 // of the logits and finds places in them, octave first.
 #include <cuda_bf16.h>
 
@@ -28,16 +29,22 @@ namespace {
 
 using namespace rows;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kPassBins = 1024;
-constexpr int kOctaves = 64, kFirstOctave = 127 - 40, kWords = kOctaves * 128, kBase = kFirstOctave * 128;
-constexpr int kZeroStep = kOctaves, kSteps = 2 * kOctaves + 1;   // step s < 64: positive octave 63 - s; s > 64: negative octave s - 65
-constexpr int kChunk = 5, kPadded = 32 * kChunk;                 // steps of a lane of warp 0
-static_assert(kPadded >= kSteps, "a lane holds five steps");
+constexpr int kThreads = 512, kCtas = 1024 / kThreads, kWarps = kThreads / 32, kPassBins = 1024;
+constexpr int kOctaves = 62, kFirstOctave = 127 - 39, kBase = kFirstOctave * 128, kAbove = kBase + kOctaves * 128;
+// words: a magnitude m stands at m - kBase + 128, smaller ones at 127, larger ones at kLarge; negative ones kHalf further
+constexpr int kHalf = 8192, kLarge = 128 + kOctaves * 128, kWords = 2 * kHalf;
+static_assert(kLarge < kHalf, "a sign's words and the two at their ends");
+constexpr int kZeroStep = kOctaves, kSteps = 2 * kOctaves + 1;   // step s < 62: positive octave 61 - s; s > 62: negative octave s - 63
+constexpr int kChunk = 4, kPadded = 32 * kChunk;                 // steps of a lane of warp 0
+static_assert(kPadded >= kSteps, "a lane holds four steps");
 constexpr int kListed = 256;             // tokens of one value that are kept in a list
 
-// What a CTA says of its part of a row, or of its octaves.
+// What a CTA says of its part of a row and of its octaves.
 struct Note {
-    uint32_t total, zeros, infinities, odd, high;
+    uint32_t total, high;                // logits in the octaves, the largest
+};
+struct Rest {
+    uint32_t zeros, infinities, odd;
 };
 enum : uint32_t { kOddNan = 1u, kOddFar = 2u };
 
@@ -47,7 +54,8 @@ struct Smem {
     uint32_t steps[kPadded];             // counts
     Tables tables;
     Factors factors;
-    Note part[8], whole[8];              // of each CTA of the cluster
+    Note note[8];                        // of each CTA of the cluster
+    Rest rest[8];
     uint32_t word[8 * kWarps];
     // what warp 0 has found
     uint32_t kept, key, share, at_n, rank;       // key: bits of a bf16
@@ -55,7 +63,7 @@ struct Smem {
     uint32_t list[kListed];
 };
 static_assert(sizeof(PassSmem<kThreads, kPassBins>) <= sizeof(uint32_t) * kWords, "the long way uses the histogram's place");
-static_assert(2 * (sizeof(Smem) + 1024) <= 227 * 1024, "two CTAs per SM");
+static_assert(kCtas * (sizeof(Smem) + 1024) <= 227 * 1024, "two CTAs per SM");
 
 // The same place in another CTA of the cluster.
 template <int C, class T> __device__ __forceinline__ T* of_rank(T* p, uint32_t rank) {
@@ -73,6 +81,26 @@ template <int C> __device__ __forceinline__ void sync_all() {
     }
 }
 
+// The first look at a row keeps it in L2 if it can, the last one and the results do not.
+__device__ __forceinline__ uint64_t keep_policy() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint64_t drop_policy() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint4 ld_hint(const unsigned char* p, uint64_t policy) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p), "l"(policy));
+    return v;
+}
+__device__ __forceinline__ void st_hint(unsigned char* p, const uint4& v, uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "l"(policy) : "memory");
+}
 __device__ __forceinline__ uint4 ld_row(const unsigned char* p) {
     uint4 v;
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
@@ -81,26 +109,29 @@ __device__ __forceinline__ uint4 ld_row(const unsigned char* p) {
 
 __device__ __forceinline__ float value_of(uint32_t bits) { return __uint_as_float(bits << 16); }
 
-// A thread's counts of what has no word.
-struct Rest {
-    uint32_t zeros, infinities, odd;
-};
-
-// Counts a logit, given as its magnitude's distance from the first word and its sign's half.
-__device__ __forceinline__ void count_one(uint32_t* h, Rest& rest, uint32_t mag, uint32_t one) {
-    const uint32_t at = mag - kBase;
-    if (at < kWords) {
-        atomicAdd(h + at, one);
-    } else {
-        const bool zero = mag == 0, inf = mag == 0x7f80u && one != 1u;
-        rest.zeros += zero;
-        rest.infinities += inf;
-        rest.odd |= zero || inf ? 0u : mag >= 0x7f80u ? kOddNan : kOddFar;
-    }
+// Counts a word's two logits.  Both halves at once: the magnitude, kept within the
+// octaves and the words at their ends, as a byte offset; the sign on top of it.
+__device__ __forceinline__ void count_two(uint32_t* h, uint32_t w) {
+    constexpr uint32_t kTwo = 0x00010001u, kSkip = (kLarge << 2) | 0x8000u;
+    const uint32_t m = __vminu2(__vmaxu2(w & 0x7fff7fffu, (kBase - 1) * kTwo), static_cast<uint32_t>(kAbove) * kTwo);
+    const uint32_t p = ((m - (kBase - 128) * kTwo) << 2) | (w & 0x80008000u);
+    unsigned char* at = reinterpret_cast<unsigned char*>(h);
+    const uint32_t lo = p & 0xffffu, hi = p >> 16;
+    if (lo != kSkip) atomicAdd(reinterpret_cast<uint32_t*>(at + lo), 1u);
+    if (hi != kSkip) atomicAdd(reinterpret_cast<uint32_t*>(at + hi), 1u);
 }
-__device__ __forceinline__ void count_two(uint32_t* h, Rest& rest, uint32_t w) {
-    count_one(h, rest, w & 0x7fffu, 1u << ((w >> 11) & 16u));
-    count_one(h, rest, (w >> 16) & 0x7fffu, 1u << ((w >> 27) & 16u));
+__device__ __forceinline__ void count_one(uint32_t* h, uint32_t bits) {
+    const uint32_t m = min(max(bits & 0x7fffu, static_cast<uint32_t>(kBase - 1)), static_cast<uint32_t>(kAbove));
+    const uint32_t at = m - (kBase - 128) + (bits & 0x8000u ? kHalf : 0);
+    if (at != kLarge + kHalf) atomicAdd(h + at, 1u);
+}
+__device__ __forceinline__ void look_at(Rest& rest, uint32_t bits) {
+    const uint32_t m = bits & 0x7fffu;
+    if (m - kBase < static_cast<uint32_t>(kAbove - kBase)) return;
+    const bool zero = m == 0, inf = bits == 0xff80u;
+    rest.zeros += zero;
+    rest.infinities += inf;
+    rest.odd |= zero || inf ? 0u : m >= 0x7f80u ? kOddNan : kOddFar;
 }
 
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t x) {
@@ -112,7 +143,7 @@ __device__ __forceinline__ uint64_t warp_sum64(uint64_t x) {
 // Four values of a step (not the zeros'), in the order of the logits, that a lane looks after.
 struct Four {
     uint32_t bits[4], count[4];
-    uint64_t mass[4];
+    uint64_t weight[4];                  // of one
 };
 template <int C> __device__ __forceinline__ Four four_of(const uint32_t* h, int step, int lane) {
     Four f;
@@ -125,19 +156,16 @@ template <int C> __device__ __forceinline__ Four four_of(const uint32_t* h, int 
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const uint4 v = *reinterpret_cast<const uint4*>(of_rank<C>(h + first, c));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f.count[i] += neg ? w[i] >> 16 : w[3 - i] & 0xffffu;
+        const uint4 v = *reinterpret_cast<const uint4*>(of_rank<C>(h + (neg ? kHalf : 0) + 128 + first, c));
+        f.count[0] += neg ? v.x : v.w, f.count[1] += neg ? v.y : v.z;
+        f.count[2] += neg ? v.z : v.y, f.count[3] += neg ? v.w : v.x;
     }
     return f;
 }
 __device__ __forceinline__ void weigh(Four& f, const Scale& scale, const Tables& t) {
+    // (no branch between them: their steps overlap)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f.mass[i] = 0;
-        if (__any_sync(0xffffffffu, f.count[i] != 0)) f.mass[i] = f.count[i] * weight_of(scale, value_of(f.bits[i]), t);
-    }
+    for (int i = 0; i < 4; ++i) f.weight[i] = weight_of(scale, value_of(f.bits[i]), t);
 }
 
 // A lane's steps: what comes before them, and what they hold.
@@ -148,12 +176,20 @@ struct Chunk {
 
 struct Found {
     uint32_t bits, at_n, before_n;
-    uint64_t before_w;
+    uint64_t before_w, weight;           // weight: of one of them
+};
+
+// The step that was looked into last.
+struct Look {
+    int step;
+    Four f;
+    uint32_t n;                          // counts and weights of the lanes before, within it
+    uint64_t w;
 };
 
 // The value where the running count (weight) of the order passes `target`.  Warp 0.
 template <int C>
-__device__ __forceinline__ Found find(const Smem& sm, const Chunk& c, const Scale& scale, bool by_weight, uint64_t target) {
+__device__ __forceinline__ Found find(const Smem& sm, const Chunk& c, Look& look, const Scale& scale, bool by_weight, uint64_t target) {
     const int lane = threadIdx.x & 31;
     // the chunk, the step in it, the value in that
     const uint64_t at = by_weight ? c.before_w : c.before_n, own = by_weight ? c.own_w : c.own_n;
@@ -169,34 +205,41 @@ __device__ __forceinline__ Found find(const Smem& sm, const Chunk& c, const Scal
         bw += w, bn += n, ++step;
     }
     step = min(step, kSteps - 1);
-    if (step == kZeroStep) return Found{0, sm.steps[step], bn, bw};
-    Four f = four_of<C>(sm.count, step, lane);
-    weigh(f, scale, sm.tables);
-    const uint64_t fw = (f.mass[0] + f.mass[1]) + (f.mass[2] + f.mass[3]);
-    const uint32_t fn = (f.count[0] + f.count[1]) + (f.count[2] + f.count[3]);
-    uint64_t aw = fw;
-    uint32_t an = fn;
+    if (step == kZeroStep) return Found{0, sm.steps[step], bn, bw, weight_of(scale, 0.0f, sm.tables)};
+    if (look.step != step) {
+        look.step = step;
+        look.f = four_of<C>(sm.count, step, lane);
+        weigh(look.f, scale, sm.tables);
+        uint64_t own_w = 0;
+        uint32_t own_n = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t x = __shfl_up_sync(0xffffffffu, aw, o);
-        const uint32_t y = __shfl_up_sync(0xffffffffu, an, o);
-        if (lane >= o) aw += x, an += y;
+        for (int i = 0; i < 4; ++i) own_w += look.f.count[i] * look.f.weight[i], own_n += look.f.count[i];
+        look.w = own_w, look.n = own_n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t x = __shfl_up_sync(0xffffffffu, look.w, o);
+            const uint32_t y = __shfl_up_sync(0xffffffffu, look.n, o);
+            if (lane >= o) look.w += x, look.n += y;
+        }
+        look.w -= own_w, look.n -= own_n;
     }
-    const int who = __ffs(__ballot_sync(0xffffffffu, target < (by_weight ? bw + aw : static_cast<uint64_t>(bn) + an)) | 0x80000000u) - 1;
-    bw += aw - fw;                                   // before this lane's four
-    bn += an - fn;
-    Found r{0, 0, 0, 0};
-    bool done = false;
+    bw += look.w;                                    // before this lane's four
+    bn += look.n;
+    // the lane and the value where it is passed: the first past the target
+    Found r{0, 0, 0, 0, 0};
+    bool passed = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (!done) r = Found{f.bits[i], f.count[i], bn, bw};
-        bw += f.mass[i], bn += f.count[i];
-        done = done || target < (by_weight ? bw : static_cast<uint64_t>(bn));
+        if (!passed) r = Found{look.f.bits[i], look.f.count[i], bn, bw, look.f.weight[i]};
+        bw += look.f.count[i] * look.f.weight[i], bn += look.f.count[i];
+        passed = passed || target < (by_weight ? bw : static_cast<uint64_t>(bn));
     }
+    const int who = __ffs(__ballot_sync(0xffffffffu, passed) | 0x80000000u) - 1;
     r.bits = __shfl_sync(0xffffffffu, r.bits, who);
     r.at_n = __shfl_sync(0xffffffffu, r.at_n, who);
     r.before_n = __shfl_sync(0xffffffffu, r.before_n, who);
     r.before_w = __shfl_sync(0xffffffffu, r.before_w, who);
+    r.weight = __shfl_sync(0xffffffffu, r.weight, who);
     return r;
 }
 
@@ -231,7 +274,7 @@ __device__ __forceinline__ uint32_t halves_of(uint32_t w, uint32_t pair, uint32_
     return (t & 0xffffu ? 0u : 1u) | (t >> 16 ? 0u : 2u);
 }
 
-template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_bf16_kernel(const RowsArgs a) {
+template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) rows_bf16_kernel(const RowsArgs a) {
     extern __shared__ __align__(16) unsigned char raw[];
     Smem& sm = *reinterpret_cast<Smem*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -240,6 +283,7 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
     constexpr int kAll = C * kThreads;
     const float nan = __int_as_float(0x7fc00000);
     Smem* const lead = of_rank<C>(&sm, 0);
+    const uint64_t keep = keep_policy(), drop = drop_policy();
     load_tables(sm.tables, tid, kThreads);
     for (int i = tid; i < kWords / 4; i += kThreads) reinterpret_cast<uint4*>(sm.count)[i] = make_uint4(0, 0, 0, 0);
     for (int i = tid; i < kPadded; i += kThreads) sm.mass[i] = 0, sm.steps[i] = 0;
@@ -255,83 +299,86 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
         if (tid == kThreads - 1) sm.factors = factors_of(q.T, q.min_p);
 
         // ---- every logit is counted ----
-        Rest rest{0, 0, 0};
         constexpr int U = 4;
         int i = me;
         for (; i + (U - 1) * kAll < vectors; i += U * kAll) {
             uint4 v[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = ld_row(row + static_cast<int64_t>(i + u * kAll) * 16);
+            for (int u = 0; u < U; ++u) v[u] = ld_hint(row + static_cast<int64_t>(i + u * kAll) * 16, keep);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                count_two(sm.count, rest, v[u].x), count_two(sm.count, rest, v[u].y);
-                count_two(sm.count, rest, v[u].z), count_two(sm.count, rest, v[u].w);
-            }
+            for (int u = 0; u < U; ++u) count_two(sm.count, v[u].x), count_two(sm.count, v[u].y), count_two(sm.count, v[u].z), count_two(sm.count, v[u].w);
         }
         for (; i < vectors; i += kAll) {
             const uint4 v = ld_row(row + static_cast<int64_t>(i) * 16);
-            count_two(sm.count, rest, v.x), count_two(sm.count, rest, v.y);
-            count_two(sm.count, rest, v.z), count_two(sm.count, rest, v.w);
+            count_two(sm.count, v.x), count_two(sm.count, v.y), count_two(sm.count, v.z), count_two(sm.count, v.w);
         }
-        for (int y = vectors * 8 + me; y < a.V; y += kAll) count_one(sm.count, rest, cells[y] & 0x7fffu, 1u << ((cells[y] >> 11) & 16u));
-        rest.zeros = __reduce_add_sync(0xffffffffu, rest.zeros);
-        rest.infinities = __reduce_add_sync(0xffffffffu, rest.infinities);
-        rest.odd = __reduce_or_sync(0xffffffffu, rest.odd);
-        if (lane == 0) sm.list[warp] = rest.zeros, sm.list[kWarps + warp] = rest.infinities, sm.list[2 * kWarps + warp] = rest.odd;
+        for (int y = vectors * 8 + me; y < a.V; y += kAll) count_one(sm.count, cells[y]);
         sync_all<C>();
 
         // ---- which octaves hold something, how much in all, the largest ----
         // (octaves of this CTA, a warp to each, a lane to four magnitudes)
-        constexpr int kMine = kOctaves / (C * kWarps) > 0 ? kOctaves / (C * kWarps) : 1;
+        constexpr int kMine = (kOctaves + C * kWarps - 1) / (C * kWarps);
         uint32_t some[2] = {0, 0}, total = 0, high = 0;      // high: 0x8000 and how far the largest lies above zero
 #pragma unroll
-        for (int x = 0; x < kMine; ++x) {
-            const int o = (x * kWarps + warp) * C + rank;
+        for (int x = 0; x < 2 * kMine; ++x) {
+            const int o = ((x >> 1) * kWarps + warp) * C + rank;
             if (o >= kOctaves) break;
-            uint32_t any = 0, top[2] = {0, 0};
+            uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const uint4 v = reinterpret_cast<const uint4*>(of_rank<C>(sm.count, c))[o * 32 + lane];
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    total += (w[y] & 0xffffu) + (w[y] >> 16);
-                    any |= w[y];
-                    if (w[y] & 0xffffu) top[0] = max(top[0], static_cast<uint32_t>(y));
-                    if (w[y] >> 16) top[1] = max(top[1], static_cast<uint32_t>(3 - y));
-                }
+                const uint4 v = reinterpret_cast<const uint4*>(of_rank<C>(sm.count, c))[((x & 1) * kHalf + 128) / 4 + o * 32 + lane];
+                w[0] += v.x, w[1] += v.y, w[2] += v.z, w[3] += v.w;
             }
-            if (any & 0xffffu) high = max(high, 0x8000u + kBase + o * 128 + lane * 4 + top[0]);
-            if (any >> 16) high = max(high, 0x8000u - (kBase + o * 128 + lane * 4 + 3 - top[1]));
-            some[0] |= (__ballot_sync(0xffffffffu, (any & 0xffffu) != 0) != 0 ? 1u : 0u) << x;
-            some[1] |= (__ballot_sync(0xffffffffu, (any >> 16) != 0) != 0 ? 1u : 0u) << x;
+            const uint32_t n = (w[0] + w[1]) + (w[2] + w[3]);
+            total += n;
+            if (!__any_sync(0xffffffffu, n != 0)) continue;
+            some[x & 1] |= 1u << (x >> 1);
+            const uint32_t at = kBase + o * 128 + lane * 4;
+            if (n) high = max(high, x & 1 ? 0x8000u - (at + (w[0] ? 0 : w[1] ? 1 : w[2] ? 2 : 3)) : 0x8000u + at + (w[3] ? 3 : w[2] ? 2 : w[1] ? 1 : 0));
         }
         high = __reduce_max_sync(0xffffffffu, high);
         total = __reduce_add_sync(0xffffffffu, total);
         if (lane == 0) sm.word[warp] = high, sm.word[kWarps + warp] = total;
         __syncthreads();
         if (warp == 0) {
-            const int w = lane % kWarps;
             Note n;
-            n.high = __reduce_max_sync(0xffffffffu, sm.word[w]);
-            n.odd = __reduce_or_sync(0xffffffffu, sm.list[2 * kWarps + w]);
-            n.total = __reduce_add_sync(0xffffffffu, lane < kWarps ? sm.word[kWarps + w] : 0u);
-            n.zeros = __reduce_add_sync(0xffffffffu, lane < kWarps ? sm.list[w] : 0u);
-            n.infinities = __reduce_add_sync(0xffffffffu, lane < kWarps ? sm.list[kWarps + w] : 0u);
-            if (lane < C) *of_rank<C>(&sm.part[rank], lane) = n;
+            n.high = __reduce_max_sync(0xffffffffu, sm.word[lane % kWarps]);
+            n.total = __reduce_add_sync(0xffffffffu, lane < kWarps ? sm.word[kWarps + lane] : 0u);
+            if (lane < C) *of_rank<C>(&sm.note[rank], lane) = n;
         }
         sync_all<C>();
-        Note all = sm.part[0];
+        Note all = sm.note[0];
 #pragma unroll
         for (int c = 1; c < C; ++c) {
-            const Note n = sm.part[c];
-            all.total += n.total, all.zeros += n.zeros, all.infinities += n.infinities;
-            all.odd |= n.odd, all.high = max(all.high, n.high);
+            const Note n = sm.note[c];
+            all.total += n.total, all.high = max(all.high, n.high);
         }
-        if (all.zeros) all.high = max(all.high, 0x8000u);
-        total = all.total + all.zeros;               // finite logits
-        const bool over = (all.odd & kOddFar) || total + all.infinities != static_cast<uint32_t>(a.V);
-        const bool bad = q.bad || (all.odd & kOddNan) || (!over && total == 0);
+        Rest rest{0, 0, 0};
+        if (all.total != static_cast<uint32_t>(a.V)) {           // some logits are not in the octaves: which
+            for (int x = me; x < vectors; x += kAll) {
+                const uint4 v = ld_row(row + static_cast<int64_t>(x) * 16);
+                look_at(rest, v.x & 0xffffu), look_at(rest, v.x >> 16), look_at(rest, v.y & 0xffffu), look_at(rest, v.y >> 16);
+                look_at(rest, v.z & 0xffffu), look_at(rest, v.z >> 16), look_at(rest, v.w & 0xffffu), look_at(rest, v.w >> 16);
+            }
+            for (int y = vectors * 8 + me; y < a.V; y += kAll) look_at(rest, cells[y]);
+            rest.zeros = __reduce_add_sync(0xffffffffu, rest.zeros);
+            rest.odd = __reduce_or_sync(0xffffffffu, rest.odd);
+            if (lane == 0) sm.word[warp] = rest.zeros, sm.word[kWarps + warp] = rest.odd;
+            __syncthreads();
+            if (warp == 0) {
+                rest.zeros = __reduce_add_sync(0xffffffffu, lane < kWarps ? sm.word[lane] : 0u);
+                rest.odd = __reduce_or_sync(0xffffffffu, sm.word[kWarps + lane % kWarps]);
+                if (lane < C) *of_rank<C>(&sm.rest[rank], lane) = rest;
+            }
+            sync_all<C>();
+            rest = sm.rest[0];
+#pragma unroll
+            for (int c = 1; c < C; ++c) rest.zeros += sm.rest[c].zeros, rest.odd |= sm.rest[c].odd;
+            if (rest.zeros) all.high = max(all.high, 0x8000u);
+        }
+        total = all.total + rest.zeros;              // finite logits
+        const bool over = rest.odd & kOddFar;
+        const bool bad = q.bad || (rest.odd & kOddNan) || (!over && total == 0);
         if (bad || over) {
             sync_all<C>();                           // (nobody reads another's counts any more)
             if (!bad) {
@@ -373,7 +420,7 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
                 if (some[x & 1] >> (x >> 1) & 1) {
                     Four f = four_of<C>(sm.count, step, lane);
                     weigh(f, scale, sm.tables);
-                    mass = warp_sum64((f.mass[0] + f.mass[1]) + (f.mass[2] + f.mass[3]));
+                    mass = warp_sum64((f.count[0] * f.weight[0] + f.count[1] * f.weight[1]) + (f.count[2] * f.weight[2] + f.count[3] * f.weight[3]));
                     n = __reduce_add_sync(0xffffffffu, (f.count[0] + f.count[1]) + (f.count[2] + f.count[3]));
                 }
                 if (lane == 0) lead->mass[step] = mass, lead->steps[step] = n;
@@ -386,17 +433,15 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
             uint32_t kept = 1, share = 1, key = best, at_n = 0, place = 0;
             uint64_t weight = uint64_t(1) << kOneBits, unit = weight;
             if (q.T == 0.0f) {
-                at_n = best == 0 ? all.zeros : 0;
+                at_n = best == 0 ? rest.zeros : 0;
                 if (best != 0)
 #pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        const uint32_t w = *of_rank<C>(&sm.count[(best & 0x7fffu) - kBase], c);
-                        at_n += best & 0x8000u ? w >> 16 : w & 0xffffu;
-                    }
+                    for (int c = 0; c < C; ++c)
+                        at_n += *of_rank<C>(&sm.count[(best & 0x7fffu) - kBase + 128 + (best & 0x8000u ? kHalf : 0)], c);
             } else {
                 if (lane == 0) {
-                    sm.steps[kZeroStep] = all.zeros;
-                    sm.mass[kZeroStep] = all.zeros ? all.zeros * weight_of(scale, 0.0f, sm.tables) : 0;
+                    sm.steps[kZeroStep] = rest.zeros;
+                    sm.mass[kZeroStep] = rest.zeros ? rest.zeros * weight_of(scale, 0.0f, sm.tables) : 0;
                 }
                 __syncwarp();
                 Chunk c{0, 0, 0, 0};
@@ -411,30 +456,29 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
                 }
                 weight = __shfl_sync(0xffffffffu, c.before_w, 31);
                 c.before_w -= c.own_w, c.before_n -= c.own_n;
+                Look look;
+                look.step = -1;
                 uint32_t most = total;
                 if (q.min_p > 0.0f) most = count_from<C>(sm, floor_of(scale.top, sm.factors.reach));
                 if (q.top_k > 0) most = min(most, static_cast<uint32_t>(q.top_k));
                 kept = total, share = 0;
-                if (most < total) {
-                    const Found f = find<C>(sm, c, scale, false, most - 1);
-                    key = f.bits, at_n = f.at_n, share = most - f.before_n, kept = most;
-                    weight = f.before_w + share * weight_of(scale, value_of(key), sm.tables);
-                }
-                if (q.top_p < 1.0f) {
-                    // tokens while what comes before them weighs less than this
-                    const uint64_t need = times_up(q.top_p, weight);
-                    const Found f = find<C>(sm, c, scale, true, need - 1);
-                    const uint64_t w = weight_of(scale, value_of(f.bits), sm.tables);
-                    key = f.bits, at_n = f.at_n, share = static_cast<uint32_t>((need - 1 - f.before_w) / w) + 1;
-                    kept = f.before_n + share;
-                    weight = f.before_w + share * w;
-                }
-                if (DRAW) {
-                    const uint64_t aim = times_down(q.u, weight);
-                    const Found f = find<C>(sm, c, scale, true, aim);
+                // the last of the first `most`; the last before which less than top_p of their
+                // weight lies; the one that is drawn
+#pragma unroll 1
+                for (int ask = 0; ask < 3; ++ask) {
+                    if (ask == 0 ? most >= total : ask == 1 ? !(q.top_p < 1.0f) : !DRAW) continue;
+                    const uint64_t target = ask == 0 ? most - 1 : ask == 1 ? times_up(q.top_p, weight) - 1 : times_down(q.u, weight);
+                    const Found f = find<C>(sm, c, look, scale, ask != 0, target);
                     key = f.bits, at_n = f.at_n;
-                    unit = weight_of(scale, value_of(key), sm.tables);
-                    place = static_cast<uint32_t>((aim - f.before_w) / unit);
+                    const uint32_t nth = ask == 0 ? most - 1 - f.before_n : quotient(target - f.before_w, f.weight);
+                    if (ask < 2) {
+                        share = nth + 1;
+                        kept = f.before_n + share;
+                        weight = f.before_w + share * f.weight;
+                    } else {
+                        place = nth;
+                        unit = f.weight;
+                    }
                 }
             }
             if (lane < C) {
@@ -459,8 +503,7 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
         const bool by_list = (DRAW || some_stay) && at_n <= kListed, by_index = (DRAW || some_stay) && !by_list;
         auto put = [&](uint32_t token) { lead->list[atomicAdd(&lead->listed, 1u)] = token; };
         if (DRAW && by_list) {
-            for (int v0 = me; v0 < vectors; v0 += kAll) {
-                const uint4 v = ld_row(row + static_cast<int64_t>(v0) * 16);
+            auto look_for = [&](const uint4& v, int v0) {
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
@@ -468,8 +511,17 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
                     if (m & 1) put(v0 * 8 + 2 * y);
                     if (m & 2) put(v0 * 8 + 2 * y + 1);
                 }
+            };
+            int v0 = me;
+            for (; v0 + (U - 1) * kAll < vectors; v0 += U * kAll) {
+                uint4 v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) v[u] = ld_row(row + static_cast<int64_t>(v0 + u * kAll) * 16);
+#pragma unroll
+                for (int u = 0; u < U; ++u) look_for(v[u], v0 + u * kAll);
                 if (C == 1 && *reinterpret_cast<volatile uint32_t*>(&sm.listed) >= at_n) break;      // that was all of them
             }
+            for (; v0 < vectors; v0 += kAll) look_for(ld_row(row + static_cast<int64_t>(v0) * 16), v0);
             for (int y = vectors * 8 + me; y < a.V; y += kAll)
                 if (halves_of(cells[y] | other, pair, sign) & 1) put(y);
         }
@@ -477,10 +529,29 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
         if (by_index) {
             // by runs of the row, a warp to each: counted, then the one that holds it
             constexpr int kRuns = C * kWarps;
-            const int run = (a.V + kRuns - 1) / kRuns, mine = rank * kWarps + warp, y0 = min(mine * run, a.V), y1 = min(y0 + run, a.V);
-            auto is = [&](int y) { return y < y1 && (halves_of(cells[y] | other, pair, sign) & 1); };
+            const int steps = (a.V + 255) / 256, run = (steps + kRuns - 1) / kRuns, mine = rank * kWarps + warp;
+            const int s0 = min(mine * run, steps), s1 = min(s0 + run, steps);
+            auto load = [&](int s, uint4 (&v)[U]) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if ((s + u) * 32 + lane < vectors) v[u] = ld_row(row + static_cast<int64_t>((s + u) * 32 + lane) * 16);
+            };
+            auto matches = [&](int s, const uint4& v) {          // among the lane's eight logits of step s, as bits
+                const int at = (s * 32 + lane) * 8;
+                if (s >= s1 || at >= a.V) return 0u;
+                if (s * 32 + lane < vectors)
+                    return halves_of(v.x, pair, sign) | halves_of(v.y, pair, sign) << 2 | halves_of(v.z, pair, sign) << 4 | halves_of(v.w, pair, sign) << 6;
+                uint32_t m = 0;
+                for (int y = 0; y < 8 && at + y < a.V; ++y) m |= (halves_of(cells[at + y] | other, pair, sign) & 1u) << y;
+                return m;
+            };
             uint32_t n = 0;
-            for (int y = y0 + lane; y < y1; y += 32) n += is(y);
+            for (int s = s0; s < s1; s += U) {
+                uint4 v[U];
+                load(s, v);
+#pragma unroll
+                for (int u = 0; u < U; ++u) n += __popc(matches(s + u, v[u]));
+            }
             n = __reduce_add_sync(0xffffffffu, n);
             if (lane < C) of_rank<C>(&sm, lane)->word[mine] = n;
             sync_all<C>();
@@ -488,14 +559,28 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
             for (int x = lane; x < mine; x += 32) before += sm.word[x];
             before = __reduce_add_sync(0xffffffffu, before);
             if (before <= place && place < before + n) {
-                for (int y = y0; y < y1; y += 32) {
-                    const uint32_t m = __ballot_sync(0xffffffffu, is(y + lane)), here = __popc(m);
-                    if (place < before + here) {
-                        if ((m >> lane & 1) && before + __popc(m & ((1u << lane) - 1u)) == place)
-                            for (int c = 0; c < C; ++c) of_rank<C>(&sm, c)->found = y + lane;
-                        break;
+                bool done = false;
+                for (int s = s0; s < s1 && !done; s += U) {
+                    uint4 v[U];
+                    load(s, v);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const uint32_t m = matches(s + u, v[u]), own = __popc(m), here = __reduce_add_sync(0xffffffffu, own);
+                        if (!done && place < before + here) {
+                            done = true;
+                            uint32_t upto = own;
+#pragma unroll
+                            for (int o = 1; o < 32; o <<= 1) {
+                                const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                                if (lane >= o) upto += x;
+                            }
+                            const uint32_t first = before + upto - own;
+                            if (first <= place && place < first + own)
+                                for (int c = 0; c < C; ++c)
+                                    of_rank<C>(&sm, c)->found = ((s + u) * 32 + lane) * 8 + __fns(m, 0, static_cast<int>(place - first) + 1);
+                        }
+                        before += here;
                     }
-                    before += here;
                 }
             }
             sync_all<C>();
@@ -522,12 +607,21 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
                 }
                 return (w & stay) | (~stay & 0xff80ff80u);
             };
-            if (out_vec)
-                for (int v0 = me; v0 < vectors; v0 += kAll) {
-                    const uint4 v = ld_row(row + static_cast<int64_t>(v0) * 16);
-                    *reinterpret_cast<uint4*>(out + static_cast<int64_t>(v0) * 16) =
-                        make_uint4(cut(v.x, v0 * 8), cut(v.y, v0 * 8 + 2), cut(v.z, v0 * 8 + 4), cut(v.w, v0 * 8 + 6));
+            auto write = [&](const uint4& v, int v0) {
+                st_hint(out + static_cast<int64_t>(v0) * 16,
+                        make_uint4(cut(v.x, v0 * 8), cut(v.y, v0 * 8 + 2), cut(v.z, v0 * 8 + 4), cut(v.w, v0 * 8 + 6)), drop);
+            };
+            if (out_vec) {
+                int v0 = me;
+                for (; v0 + (U - 1) * kAll < vectors; v0 += U * kAll) {
+                    uint4 v[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) v[u] = ld_hint(row + static_cast<int64_t>(v0 + u * kAll) * 16, drop);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) write(v[u], v0 + u * kAll);
                 }
+                for (; v0 < vectors; v0 += kAll) write(ld_hint(row + static_cast<int64_t>(v0) * 16, drop), v0);
+            }
             for (int y = (out_vec ? vectors * 8 : 0) + me; y < a.V; y += kAll)
                 reinterpret_cast<unsigned short*>(out)[y] = static_cast<unsigned short>(cut(cells[y] | other, y));
         }
@@ -573,7 +667,7 @@ template <bool DRAW, int C> cudaError_t launch_one(const RowsArgs& a, int slots,
 
 template <bool DRAW> cudaError_t launch(const RowsArgs& a, int nsm, cudaStream_t s) {
     // a row to a cluster, of as many CTAs as the machine has places for
-    const int slots = 2 * nsm;
+        const int slots = kCtas * nsm;
     if (a.rows * 8 <= slots) return launch_one<DRAW, 8>(a, slots, s);
     if (a.rows * 4 <= slots) return launch_one<DRAW, 4>(a, slots, s);
     if (a.rows * 2 <= slots) return launch_one<DRAW, 2>(a, slots, s);
