@@ -10,7 +10,7 @@
 // The histogram has a word for each value whose magnitude lies from 2^-39 to 2^23,
 // 62 octaves of 128 of either sign (64 KB: two CTAs share an SM, and one counts
 // while the other looks for its places).  Smaller and larger magnitudes go to a word
-// at either end, -infinity nowhere; a row where the sum of the counts shows such
+// at either end; a row where the sum of the counts shows such
 // logits is looked through once more for zeros and infinities, and one that holds
 // other ones goes the long way (row_in_passes).  What bounds the count is the
 // words' banks: 32 lanes hit one of them 3.5 times.
@@ -32,16 +32,20 @@ using namespace rows;
 constexpr int kThreads = 512, kCtas = 1024 / kThreads, kWarps = kThreads / 32, kPassBins = 1024;
 constexpr int kOctaves = 62, kFirstOctave = 127 - 39, kBase = kFirstOctave * 128, kAbove = kBase + kOctaves * 128;
 // words: a magnitude m stands at m - kBase + 128, smaller ones at 127, larger ones at kLarge; negative ones kHalf further
-constexpr int kHalf = 8192, kLarge = 128 + kOctaves * 128, kWords = 2 * kHalf;
+constexpr int kHalf = 8192, kSmall = 127, kLarge = 128 + kOctaves * 128, kWords = 2 * kHalf;
 static_assert(kLarge < kHalf, "a sign's words and the two at their ends");
 constexpr int kZeroStep = kOctaves, kSteps = 2 * kOctaves + 1;   // step s < 62: positive octave 61 - s; s > 62: negative octave s - 63
 constexpr int kChunk = 4, kPadded = 32 * kChunk;                 // steps of a lane of warp 0
 static_assert(kPadded >= kSteps, "a lane holds four steps");
 constexpr int kListed = 256;             // tokens of one value that are kept in a list
+constexpr int kHeads = 2048;             // vectors that hold a logit of the head
+constexpr int kHeadK = 256;              // top-k up to which a row is first looked through for its head alone
+constexpr int kManyLogits = 1 << 16;     // from here on the head's bound is the least of 16 maxima of 512, else of 32 of 256
 
 // What a CTA says of its part of a row and of its octaves.
 struct Note {
     uint32_t total, high;                // logits in the octaves, the largest
+    uint32_t head, heads, odd, beyond;   // the head's bound (a key), its vectors; kOdd* bits; counts beyond the octaves
 };
 struct Rest {
     uint32_t zeros, infinities, odd;
@@ -59,11 +63,18 @@ struct Smem {
     uint32_t word[8 * kWarps];
     // what warp 0 has found
     uint32_t kept, key, share, at_n, rank;       // key: bits of a bf16
-    uint32_t listed, found;
-    uint32_t list[kListed];
+    uint32_t listed, found, heads, odd;
+    uint32_t list[kListed], head[kHeads];
 };
 static_assert(sizeof(PassSmem<kThreads, kPassBins>) <= sizeof(uint32_t) * kWords, "the long way uses the histogram's place");
 static_assert(kCtas * (sizeof(Smem) + 1024) <= 227 * 1024, "two CTAs per SM");
+
+// (Functions that are called find it for themselves: the compiler then knows that it
+// is shared memory.)
+__device__ __forceinline__ Smem& smem() {
+    extern __shared__ __align__(16) unsigned char raw[];
+    return *reinterpret_cast<Smem*>(raw);
+}
 
 // The same place in another CTA of the cluster.
 template <int C, class T> __device__ __forceinline__ T* of_rank(T* p, uint32_t rank) {
@@ -111,19 +122,17 @@ __device__ __forceinline__ float value_of(uint32_t bits) { return __uint_as_floa
 
 // Counts a word's two logits.  Both halves at once: the magnitude, kept within the
 // octaves and the words at their ends, as a byte offset; the sign on top of it.
-__device__ __forceinline__ void count_two(uint32_t* h, uint32_t w) {
-    constexpr uint32_t kTwo = 0x00010001u, kSkip = (kLarge << 2) | 0x8000u;
+// (Lanes that hit one word cost one pass: masked rows are no slower.)
+__device__ __forceinline__ void count_two(uint32_t counts, uint32_t w) {
+    constexpr uint32_t kTwo = 0x00010001u;
     const uint32_t m = __vminu2(__vmaxu2(w & 0x7fff7fffu, (kBase - 1) * kTwo), static_cast<uint32_t>(kAbove) * kTwo);
-    const uint32_t p = ((m - (kBase - 128) * kTwo) << 2) | (w & 0x80008000u);
-    unsigned char* at = reinterpret_cast<unsigned char*>(h);
-    const uint32_t lo = p & 0xffffu, hi = p >> 16;
-    if (lo != kSkip) atomicAdd(reinterpret_cast<uint32_t*>(at + lo), 1u);
-    if (hi != kSkip) atomicAdd(reinterpret_cast<uint32_t*>(at + hi), 1u);
+    const uint32_t p = (m * 4 - (kBase - 128) * 4 * kTwo) | (w & 0x80008000u);
+    asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(counts + (p & 0xffffu)) : "memory");
+    asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(counts + (p >> 16)) : "memory");
 }
 __device__ __forceinline__ void count_one(uint32_t* h, uint32_t bits) {
     const uint32_t m = min(max(bits & 0x7fffu, static_cast<uint32_t>(kBase - 1)), static_cast<uint32_t>(kAbove));
-    const uint32_t at = m - (kBase - 128) + (bits & 0x8000u ? kHalf : 0);
-    if (at != kLarge + kHalf) atomicAdd(h + at, 1u);
+    atomicAdd(h + (m - (kBase - 128) + (bits & 0x8000u ? kHalf : 0)), 1u);
 }
 __device__ __forceinline__ void look_at(Rest& rest, uint32_t bits) {
     const uint32_t m = bits & 0x7fffu;
@@ -132,6 +141,30 @@ __device__ __forceinline__ void look_at(Rest& rest, uint32_t bits) {
     rest.zeros += zero;
     rest.infinities += inf;
     rest.odd |= zero || inf ? 0u : m >= 0x7f80u ? kOddNan : kOddFar;
+}
+
+// Key of the largest of eight logits (0: none above -infinity).
+__device__ __forceinline__ uint32_t largest_of(const uint4& v) {
+    const uint32_t m = bf16x2_max(bf16x2_max(v.x, v.y), bf16x2_max(v.z, v.w));
+    const float f = fmaxf(bf16_lo(m), bf16_hi(m));
+    return f > -INFINITY ? key_of(f) : 0u;
+}
+__device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ void count_above(uint32_t* h, uint32_t w, float least) {
+    if (bf16_lo(w) >= least) count_one(h, w & 0xffffu);
+    if (bf16_hi(w) >= least) count_one(h, w >> 16);
+}
+// Whether one of them is at least `above`.
+__device__ __forceinline__ bool at_least(const uint4& v, __nv_bfloat162 above) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) m |= __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[y]), above);
+    return m != 0;
 }
 
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t x) {
@@ -274,20 +307,273 @@ __device__ __forceinline__ uint32_t halves_of(uint32_t w, uint32_t pair, uint32_
     return (t & 0xffffu ? 0u : 1u) | (t >> 16 ? 0u : 2u);
 }
 
+// Counts and weights of this CTA's octaves, a warp to each: some[x] tells which of the
+// positive (negative) ones are not empty.
+template <int C> constexpr int kMine = (kOctaves + C * kWarps - 1) / (C * kWarps);
+template <int C> __device__ __noinline__ void weigh_octaves(const Scale scale, uint32_t positive, uint32_t negative, int rank) {
+    Smem& sm = smem();
+    Smem* const lead = of_rank<C>(&sm, 0);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll 1
+    for (int x = 0; x < 2 * kMine<C>; ++x) {
+        const int o = ((x >> 1) * kWarps + warp) * C + rank, step = x & 1 ? kZeroStep + 1 + o : kOctaves - 1 - o;
+        if (o >= kOctaves) break;
+        uint64_t mass = 0;
+        uint32_t n = 0;
+        if ((x & 1 ? negative : positive) >> (x >> 1) & 1) {
+            Four f = four_of<C>(sm.count, step, lane);
+            weigh(f, scale, sm.tables);
+            mass = warp_sum64((f.count[0] * f.weight[0] + f.count[1] * f.weight[1]) + (f.count[2] * f.weight[2] + f.count[3] * f.weight[3]));
+            n = __reduce_add_sync(0xffffffffu, (f.count[0] + f.count[1]) + (f.count[2] + f.count[3]));
+        }
+        if (lane == 0) lead->mass[step] = mass, lead->steps[step] = n;
+    }
+}
+
+// What a row keeps and what is drawn (total: logits counted, finite: of how many): told to every CTA of the cluster.  Warp 0 of the first.
+template <bool DRAW, int C>
+__device__ __noinline__ void settle(const RowsArgs& a, int r, const Ask q, const Scale scale, uint32_t best, uint32_t total, uint32_t finite, uint32_t zeros) {
+    Smem& sm = smem();
+    const int lane = threadIdx.x & 31;
+    uint32_t kept = 1, share = 1, key = best, at_n = 0, place = 0;
+    uint64_t weight = uint64_t(1) << kOneBits, unit = weight;
+    if (q.T == 0.0f) {
+        at_n = best == 0 ? zeros : 0;
+        if (best != 0)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                at_n += *of_rank<C>(&sm.count[(best & 0x7fffu) - kBase + 128 + (best & 0x8000u ? kHalf : 0)], c);
+    } else {
+        if (lane == 0) {
+            sm.steps[kZeroStep] = zeros;
+            sm.mass[kZeroStep] = zeros ? zeros * weight_of(scale, 0.0f, sm.tables) : 0;
+        }
+        __syncwarp();
+        Chunk c{0, 0, 0, 0};
+#pragma unroll
+        for (int x = 0; x < kChunk; ++x) c.own_w += sm.mass[lane * kChunk + x], c.own_n += sm.steps[lane * kChunk + x];
+        c.before_w = c.own_w, c.before_n = c.own_n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t y = __shfl_up_sync(0xffffffffu, c.before_w, o);
+            const uint32_t z = __shfl_up_sync(0xffffffffu, c.before_n, o);
+            if (lane >= o) c.before_w += y, c.before_n += z;
+        }
+        weight = __shfl_sync(0xffffffffu, c.before_w, 31);
+        c.before_w -= c.own_w, c.before_n -= c.own_n;
+        Look look;
+        look.step = -1;
+        uint32_t most = total;
+        if (q.min_p > 0.0f) most = count_from<C>(sm, floor_of(scale.top, sm.factors.reach));
+        if (q.top_k > 0) most = min(most, static_cast<uint32_t>(q.top_k));
+        kept = total, share = 0;
+        // the last of the first `most`; the last before which less than top_p of their
+        // weight lies; the one that is drawn
+#pragma unroll 1
+        for (int ask = 0; ask < 3; ++ask) {
+            if (ask == 0 ? most >= finite : ask == 1 ? !(q.top_p < 1.0f) : !DRAW) continue;
+            const uint64_t target = ask == 0 ? most - 1 : ask == 1 ? times_up(q.top_p, weight) - 1 : times_down(q.u, weight);
+            const Found f = find<C>(sm, c, look, scale, ask != 0, target);
+            key = f.bits, at_n = f.at_n;
+            const uint32_t nth = ask == 0 ? most - 1 - f.before_n : quotient(target - f.before_w, f.weight);
+            if (ask < 2) {
+                share = nth + 1;
+                kept = f.before_n + share;
+                weight = f.before_w + share * f.weight;
+            } else {
+                place = nth;
+                unit = f.weight;
+            }
+        }
+    }
+    if (lane < C) {
+        Smem* to = of_rank<C>(&sm, lane);
+        to->kept = kept, to->key = key, to->share = share, to->at_n = at_n, to->rank = place;
+    }
+    if (lane == 0) {
+        if (a.kept) a.kept[r] = static_cast<int32_t>(kept);
+        if (DRAW && a.logprob) a.logprob[r] = log_share(unit, weight);
+    }
+}
+
+// Counts this CTA's vectors of a row.  A sample, 32 vectors here and there, gives a bound
+// that some hundred logits of the row reach; vectors with such a one, the head, are
+// written down; without COUNT only those are counted.  Returns the bound, a key.  (A function of its own, as the other steps
+// are: a row's other numbers would take the registers of its loads.)
+template <int C, bool COUNT> __device__ __noinline__ uint32_t count_row(const unsigned char* row, int V, int vectors, int rank) {
+    constexpr int U = 4, kAll = C * kThreads, kSamples = C * kWarps * 2;
+    Smem& sm = smem();
+    const uint32_t counts = smem_u32(sm.count);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint64_t keep = keep_policy();
+    const int chunks = (vectors + 31) / 32;
+    uint32_t least = 0xffffffffu, most = 0;
+    {
+        uint4 v[2];
+        bool there[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int n = (rank * kWarps + warp) * 2 + u;
+            const int at = (chunks >= kSamples ? static_cast<int>(static_cast<uint32_t>(n) * chunks / kSamples) : n) * 32 + lane;
+            there[u] = at < vectors;
+            if (there[u]) v[u] = ld_hint(row + static_cast<int64_t>(at) * 16, keep);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const uint32_t top = __reduce_max_sync(0xffffffffu, there[u] ? largest_of(v[u]) : 0u);
+            if (top) least = min(least, top);
+            most = max(most, top);
+        }
+    }
+    if (lane < C) of_rank<C>(&sm, lane)->word[rank * kWarps + warp] = V < kManyLogits || most == 0 ? least : most;
+    int i = rank * kThreads + threadIdx.x;
+    uint4 v[U];
+    const bool full = i + (U - 1) * kAll < vectors;
+    if (full)                                        // (on their way while the bound is agreed upon)
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = ld_hint(row + static_cast<int64_t>(i + u * kAll) * 16, keep);
+    sync_all<C>();
+    uint32_t bound = kKeyLow + 1;                    // (a short row is head as a whole)
+    if (vectors > kHeads) {
+        // the fourth smallest: the smallest ones of 16 differ much
+        uint32_t mine[(C * kWarps + 31) / 32];
+#pragma unroll
+        for (int x = 0; x < (C * kWarps + 31) / 32; ++x) mine[x] = x * 32 + lane < C * kWarps ? sm.word[x * 32 + lane] : 0xffffffffu;
+#pragma unroll
+        for (int turn = 0; turn < 4; ++turn) {
+            uint32_t m = 0xffffffffu;
+#pragma unroll
+            for (int x = 0; x < (C * kWarps + 31) / 32; ++x) m = min(m, mine[x]);
+            bound = __reduce_min_sync(0xffffffffu, m);
+#pragma unroll
+            for (int x = 0; x < (C * kWarps + 31) / 32; ++x) mine[x] = mine[x] == bound ? 0xffffffffu : mine[x];
+        }
+        bound = min(bound, kKeyHigh);
+    }
+    const float f = of_key(bound);
+    const __nv_bfloat162 above = __floats2bfloat162_rn(f, f);
+    uint32_t most2 = 0xff80ff80u;                    // of both halves; a NaN stays
+    auto take = [&](const uint4& x, int index) {
+        if constexpr (COUNT)
+            count_two(counts, x.x), count_two(counts, x.y), count_two(counts, x.z), count_two(counts, x.w);
+        else
+            most2 = max_nan(most2, max_nan(max_nan(x.x, x.y), max_nan(x.z, x.w)));
+        if (at_least(x, above)) {
+            const uint32_t n = atomicAdd(&sm.heads, 1u);
+            if (n < kHeads) sm.head[n] = index;
+        }
+    };
+    if (full) {
+        for (;;) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) take(v[u], i + u * kAll);
+            i += U * kAll;
+            if (i + (U - 1) * kAll >= vectors) break;
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = ld_hint(row + static_cast<int64_t>(i + u * kAll) * 16, keep);
+        }
+    }
+    for (; i < vectors; i += kAll) take(ld_hint(row + static_cast<int64_t>(i) * 16, keep), i);
+    if constexpr (!COUNT) {
+        const bool odd = !(fmaxf(bf16_lo(most2), bf16_hi(most2)) < INFINITY) || bf16_lo(most2) != bf16_lo(most2) || bf16_hi(most2) != bf16_hi(most2);
+        if (odd) atomicOr(&sm.odd, kOddNan);
+        // of the vectors written down, what reaches the bound is counted
+        __syncthreads();
+        if (sm.heads <= kHeads)
+            for (uint32_t x = threadIdx.x; x < sm.heads; x += kThreads) {
+                const uint4 w = ld_hint(row + static_cast<int64_t>(sm.head[x]) * 16, keep);
+                count_above(sm.count, w.x, f), count_above(sm.count, w.y, f), count_above(sm.count, w.z, f), count_above(sm.count, w.w, f);
+            }
+        const unsigned short* cells = reinterpret_cast<const unsigned short*>(row);
+        for (int y = vectors * 8 + rank * kThreads + threadIdx.x; y < V; y += kAll) {
+            const uint32_t x = cells[y];
+            if (value_of(x) >= f) count_one(sm.count, x);
+            if (!(value_of(x) < INFINITY)) atomicOr(&sm.odd, kOddNan);
+        }
+    }
+    return bound;
+}
+
+// The index of the token of one value that stands at `place` among them, into sm.found of
+// every CTA of the cluster.
+template <int C>
+__device__ __noinline__ void find_by_index(const unsigned short* cells, int V, int vectors, int rank, uint32_t pair, uint32_t sign, uint32_t place) {
+    constexpr int U = 4;
+    Smem& sm = smem();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t other = ~pair << 16;
+    // by runs of the row, a warp to each: counted, then the one that holds it
+    constexpr int kRuns = C * kWarps;
+    const int steps = (V + 255) / 256, run = (steps + kRuns - 1) / kRuns, mine = rank * kWarps + warp;
+    const int s0 = min(mine * run, steps), s1 = min(s0 + run, steps);
+    auto load = [&](int s, uint4 (&v)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if ((s + u) * 32 + lane < vectors) v[u] = ld_row(reinterpret_cast<const unsigned char*>(cells) + static_cast<int64_t>((s + u) * 32 + lane) * 16);
+    };
+    auto matches = [&](int s, const uint4& v) {          // among the lane's eight logits of step s, as bits
+        const int at = (s * 32 + lane) * 8;
+        if (s >= s1 || at >= V) return 0u;
+        if (s * 32 + lane < vectors)
+            return halves_of(v.x, pair, sign) | halves_of(v.y, pair, sign) << 2 | halves_of(v.z, pair, sign) << 4 | halves_of(v.w, pair, sign) << 6;
+        uint32_t m = 0;
+        for (int y = 0; y < 8 && at + y < V; ++y) m |= (halves_of(cells[at + y] | other, pair, sign) & 1u) << y;
+        return m;
+    };
+    uint32_t n = 0;
+    for (int s = s0; s < s1; s += U) {
+        uint4 v[U];
+        load(s, v);
+#pragma unroll
+        for (int u = 0; u < U; ++u) n += __popc(matches(s + u, v[u]));
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane < C) of_rank<C>(&sm, lane)->word[mine] = n;
+    sync_all<C>();
+    uint32_t before = 0;
+    for (int x = lane; x < mine; x += 32) before += sm.word[x];
+    before = __reduce_add_sync(0xffffffffu, before);
+    if (before <= place && place < before + n) {
+        bool done = false;
+        for (int s = s0; s < s1 && !done; s += U) {
+            uint4 v[U];
+            load(s, v);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t m = matches(s + u, v[u]), own = __popc(m), here = __reduce_add_sync(0xffffffffu, own);
+                if (!done && place < before + here) {
+                    done = true;
+                    uint32_t upto = own;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                        if (lane >= o) upto += x;
+                    }
+                    const uint32_t first = before + upto - own;
+                    if (first <= place && place < first + own)
+                        for (int c = 0; c < C; ++c)
+                            of_rank<C>(&sm, c)->found = ((s + u) * 32 + lane) * 8 + __fns(m, 0, static_cast<int>(place - first) + 1);
+                }
+                before += here;
+            }
+        }
+    }
+    sync_all<C>();
+}
+
 template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) rows_bf16_kernel(const RowsArgs a) {
-    extern __shared__ __align__(16) unsigned char raw[];
-    Smem& sm = *reinterpret_cast<Smem*>(raw);
+    Smem& sm = smem();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
     const int me = rank * kThreads + tid;            // among the cluster's threads
     constexpr int kAll = C * kThreads;
     const float nan = __int_as_float(0x7fc00000);
     Smem* const lead = of_rank<C>(&sm, 0);
-    const uint64_t keep = keep_policy(), drop = drop_policy();
+    const uint64_t drop = drop_policy();
     load_tables(sm.tables, tid, kThreads);
     for (int i = tid; i < kWords / 4; i += kThreads) reinterpret_cast<uint4*>(sm.count)[i] = make_uint4(0, 0, 0, 0);
     for (int i = tid; i < kPadded; i += kThreads) sm.mass[i] = 0, sm.steps[i] = 0;
-    if (tid == 0) sm.listed = 0;
+    if (tid == 0) sm.listed = sm.heads = sm.odd = 0;
     for (int64_t r = blockIdx.x / C; r < a.rows; r += gridDim.x / C) {
         const Ask q = ask_of(a, r);
         const unsigned char* row = static_cast<const unsigned char*>(a.logits) + r * a.in_stride;
@@ -300,61 +586,78 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
 
         // ---- every logit is counted ----
         constexpr int U = 4;
-        int i = me;
-        for (; i + (U - 1) * kAll < vectors; i += U * kAll) {
-            uint4 v[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = ld_hint(row + static_cast<int64_t>(i + u * kAll) * 16, keep);
-#pragma unroll
-            for (int u = 0; u < U; ++u) count_two(sm.count, v[u].x), count_two(sm.count, v[u].y), count_two(sm.count, v[u].z), count_two(sm.count, v[u].w);
-        }
-        for (; i < vectors; i += kAll) {
-            const uint4 v = ld_row(row + static_cast<int64_t>(i) * 16);
-            count_two(sm.count, v.x), count_two(sm.count, v.y), count_two(sm.count, v.z), count_two(sm.count, v.w);
-        }
-        for (int y = vectors * 8 + me; y < a.V; y += kAll) count_one(sm.count, cells[y]);
-        sync_all<C>();
+        // Where few tokens are asked for, they are in the head as a rule: the first look is for
+        // that alone, at HBM's rate, and a second one counts all where it does not do.
+        const bool brief = vectors > 0 && (q.T == 0.0f || (q.top_k > 0 && q.top_k <= kHeadK) || q.min_p >= 0x1p-10f);
+        uint32_t some[2] = {0, 0}, total = 0;
+        Note all;
+        bool whole = !brief;                         // all logits are counted
+#pragma unroll 1
+        for (;; whole = true) {
+            uint32_t bound = kKeyHigh;
+            if (vectors > 0) bound = whole ? count_row<C, true>(row, a.V, vectors, rank) : count_row<C, false>(row, a.V, vectors, rank);
+            if (whole)
+                for (int y = vectors * 8 + me; y < a.V; y += kAll) count_one(sm.count, cells[y]);
+            sync_all<C>();
 
-        // ---- which octaves hold something, how much in all, the largest ----
-        // (octaves of this CTA, a warp to each, a lane to four magnitudes)
-        constexpr int kMine = (kOctaves + C * kWarps - 1) / (C * kWarps);
-        uint32_t some[2] = {0, 0}, total = 0, high = 0;      // high: 0x8000 and how far the largest lies above zero
+            // ---- which octaves hold something, how much in all, the largest ----
+            // (octaves of this CTA, a warp to each, a lane to four magnitudes)
+            some[0] = some[1] = 0;
+            total = 0;
+            uint32_t high = 0;                       // high: 0x8000 and how far the largest lies above zero
 #pragma unroll
-        for (int x = 0; x < 2 * kMine; ++x) {
-            const int o = ((x >> 1) * kWarps + warp) * C + rank;
-            if (o >= kOctaves) break;
-            uint32_t w[4] = {0, 0, 0, 0};
+            for (int x = 0; x < 2 * kMine<C>; ++x) {
+                const int o = ((x >> 1) * kWarps + warp) * C + rank;
+                if (o >= kOctaves) break;
+                uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const uint4 v = reinterpret_cast<const uint4*>(of_rank<C>(sm.count, c))[((x & 1) * kHalf + 128) / 4 + o * 32 + lane];
-                w[0] += v.x, w[1] += v.y, w[2] += v.z, w[3] += v.w;
+                for (int c = 0; c < C; ++c) {
+                    const uint4 v = reinterpret_cast<const uint4*>(of_rank<C>(sm.count, c))[((x & 1) * kHalf + 128) / 4 + o * 32 + lane];
+                    w[0] += v.x, w[1] += v.y, w[2] += v.z, w[3] += v.w;
+                }
+                const uint32_t n = (w[0] + w[1]) + (w[2] + w[3]);
+                total += n;
+                if (!__any_sync(0xffffffffu, n != 0)) continue;
+                some[x & 1] |= 1u << (x >> 1);
+                const uint32_t at = kBase + o * 128 + lane * 4;
+                if (n) high = max(high, x & 1 ? 0x8000u - (at + (w[0] ? 0 : w[1] ? 1 : w[2] ? 2 : 3)) : 0x8000u + at + (w[3] ? 3 : w[2] ? 2 : w[1] ? 1 : 0));
             }
-            const uint32_t n = (w[0] + w[1]) + (w[2] + w[3]);
-            total += n;
-            if (!__any_sync(0xffffffffu, n != 0)) continue;
-            some[x & 1] |= 1u << (x >> 1);
-            const uint32_t at = kBase + o * 128 + lane * 4;
-            if (n) high = max(high, x & 1 ? 0x8000u - (at + (w[0] ? 0 : w[1] ? 1 : w[2] ? 2 : 3)) : 0x8000u + at + (w[3] ? 3 : w[2] ? 2 : w[1] ? 1 : 0));
-        }
-        high = __reduce_max_sync(0xffffffffu, high);
-        total = __reduce_add_sync(0xffffffffu, total);
-        if (lane == 0) sm.word[warp] = high, sm.word[kWarps + warp] = total;
-        __syncthreads();
-        if (warp == 0) {
-            Note n;
-            n.high = __reduce_max_sync(0xffffffffu, sm.word[lane % kWarps]);
-            n.total = __reduce_add_sync(0xffffffffu, lane < kWarps ? sm.word[kWarps + lane] : 0u);
-            if (lane < C) *of_rank<C>(&sm.note[rank], lane) = n;
-        }
-        sync_all<C>();
-        Note all = sm.note[0];
+            high = __reduce_max_sync(0xffffffffu, high);
+            total = __reduce_add_sync(0xffffffffu, total);
+            if (lane == 0) sm.word[warp] = high, sm.word[kWarps + warp] = total;
+            __syncthreads();
+            if (warp == 0) {
+                Note n;
+                n.high = __reduce_max_sync(0xffffffffu, sm.word[lane % kWarps]);
+                n.total = __reduce_add_sync(0xffffffffu, lane < kWarps ? sm.word[kWarps + lane] : 0u);
+                n.head = bound, n.heads = sm.heads, n.odd = sm.odd;
+                n.beyond = sm.count[kSmall] + sm.count[kLarge] + sm.count[kHalf + kSmall] + sm.count[kHalf + kLarge];
+                if (lane < C) *of_rank<C>(&sm.note[rank], lane) = n;
+            }
+            sync_all<C>();
+            all = sm.note[0];
 #pragma unroll
-        for (int c = 1; c < C; ++c) {
-            const Note n = sm.note[c];
-            all.total += n.total, all.high = max(all.high, n.high);
+            for (int c = 1; c < C; ++c) {
+                const Note n = sm.note[c];
+                all.total += n.total, all.high = max(all.high, n.high);
+                all.head = max(all.head, n.head), all.heads = max(all.heads, n.heads);
+                all.odd |= n.odd, all.beyond += n.beyond;
+            }
+            if (whole || q.bad) break;
+            // does the head hold all that is asked for?
+            const float top = value_of(all.high >= 0x8000u ? all.high - 0x8000u : 0x8000u | (0x8000u - all.high));
+            const float reach = q.min_p > 0.0f ? top + q.T * __logf(q.min_p) : INFINITY;         // (with room for what it is off by)
+            const bool first = q.T == 0.0f || (q.top_k > 0 && static_cast<uint32_t>(q.top_k) <= all.total);
+            const bool enough = all.total > 0 && all.heads <= kHeads && all.beyond == 0 &&
+                                (first || (q.min_p > 0.0f && reach - fabsf(reach) * 1e-4f - 1e-30f >= of_key(all.head)));
+            if (enough || (all.odd & kOddNan)) break;
+            sync_all<C>();                           // (nobody reads another's counts any more)
+            for (int x = tid; x < kWords / 4; x += kThreads) reinterpret_cast<uint4*>(sm.count)[x] = make_uint4(0, 0, 0, 0);
+            if (tid == 0) sm.heads = 0;
+            sync_all<C>();
         }
         Rest rest{0, 0, 0};
-        if (all.total != static_cast<uint32_t>(a.V)) {           // some logits are not in the octaves: which
+        if (whole && all.total != static_cast<uint32_t>(a.V)) {  // some logits are not in the octaves: which
             for (int x = me; x < vectors; x += kAll) {
                 const uint4 v = ld_row(row + static_cast<int64_t>(x) * 16);
                 look_at(rest, v.x & 0xffffu), look_at(rest, v.x >> 16), look_at(rest, v.y & 0xffffu), look_at(rest, v.y >> 16);
@@ -378,12 +681,12 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
         }
         total = all.total + rest.zeros;              // finite logits
         const bool over = rest.odd & kOddFar;
-        const bool bad = q.bad || (rest.odd & kOddNan) || (!over && total == 0);
+        const bool bad = q.bad || ((rest.odd | all.odd) & kOddNan) || (!over && total == 0);
         if (bad || over) {
             sync_all<C>();                           // (nobody reads another's counts any more)
             if (!bad) {
                 if (rank == 0) {
-                    PassSmem<kThreads, kPassBins>& ps = *reinterpret_cast<PassSmem<kThreads, kPassBins>*>(raw);
+                    PassSmem<kThreads, kPassBins>& ps = *reinterpret_cast<PassSmem<kThreads, kPassBins>*>(sm.count);
                     load_tables(ps.tables, tid, kThreads);
                     __syncthreads();
                     row_in_passes<true, DRAW, kThreads, kPassBins>(a, r, ps);
@@ -404,6 +707,7 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
                 }
             }
             for (int x = tid; x < kWords / 4; x += kThreads) reinterpret_cast<uint4*>(sm.count)[x] = make_uint4(0, 0, 0, 0);
+            if (tid == 0) sm.heads = sm.odd = 0;
             continue;
         }
 
@@ -411,84 +715,13 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
         const uint32_t best = all.high >= 0x8000u ? all.high - 0x8000u : 0x8000u | (0x8000u - all.high);
         const Scale scale{value_of(best), sm.factors.hi, sm.factors.lo};
         if (q.T != 0.0f) {
-#pragma unroll 1
-            for (int x = 0; x < 2 * kMine; ++x) {
-                const int o = ((x >> 1) * kWarps + warp) * C + rank, step = x & 1 ? kZeroStep + 1 + o : kOctaves - 1 - o;
-                if (o >= kOctaves) break;
-                uint64_t mass = 0;
-                uint32_t n = 0;
-                if (some[x & 1] >> (x >> 1) & 1) {
-                    Four f = four_of<C>(sm.count, step, lane);
-                    weigh(f, scale, sm.tables);
-                    mass = warp_sum64((f.count[0] * f.weight[0] + f.count[1] * f.weight[1]) + (f.count[2] * f.weight[2] + f.count[3] * f.weight[3]));
-                    n = __reduce_add_sync(0xffffffffu, (f.count[0] + f.count[1]) + (f.count[2] + f.count[3]));
-                }
-                if (lane == 0) lead->mass[step] = mass, lead->steps[step] = n;
-            }
+            weigh_octaves<C>(scale, some[0], some[1], rank);
         }
         sync_all<C>();
 
         // ---- what is kept, what is drawn ----
         if (rank == 0 && warp == 0) {
-            uint32_t kept = 1, share = 1, key = best, at_n = 0, place = 0;
-            uint64_t weight = uint64_t(1) << kOneBits, unit = weight;
-            if (q.T == 0.0f) {
-                at_n = best == 0 ? rest.zeros : 0;
-                if (best != 0)
-#pragma unroll
-                    for (int c = 0; c < C; ++c)
-                        at_n += *of_rank<C>(&sm.count[(best & 0x7fffu) - kBase + 128 + (best & 0x8000u ? kHalf : 0)], c);
-            } else {
-                if (lane == 0) {
-                    sm.steps[kZeroStep] = rest.zeros;
-                    sm.mass[kZeroStep] = rest.zeros ? rest.zeros * weight_of(scale, 0.0f, sm.tables) : 0;
-                }
-                __syncwarp();
-                Chunk c{0, 0, 0, 0};
-#pragma unroll
-                for (int x = 0; x < kChunk; ++x) c.own_w += sm.mass[lane * kChunk + x], c.own_n += sm.steps[lane * kChunk + x];
-                c.before_w = c.own_w, c.before_n = c.own_n;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint64_t y = __shfl_up_sync(0xffffffffu, c.before_w, o);
-                    const uint32_t z = __shfl_up_sync(0xffffffffu, c.before_n, o);
-                    if (lane >= o) c.before_w += y, c.before_n += z;
-                }
-                weight = __shfl_sync(0xffffffffu, c.before_w, 31);
-                c.before_w -= c.own_w, c.before_n -= c.own_n;
-                Look look;
-                look.step = -1;
-                uint32_t most = total;
-                if (q.min_p > 0.0f) most = count_from<C>(sm, floor_of(scale.top, sm.factors.reach));
-                if (q.top_k > 0) most = min(most, static_cast<uint32_t>(q.top_k));
-                kept = total, share = 0;
-                // the last of the first `most`; the last before which less than top_p of their
-                // weight lies; the one that is drawn
-#pragma unroll 1
-                for (int ask = 0; ask < 3; ++ask) {
-                    if (ask == 0 ? most >= total : ask == 1 ? !(q.top_p < 1.0f) : !DRAW) continue;
-                    const uint64_t target = ask == 0 ? most - 1 : ask == 1 ? times_up(q.top_p, weight) - 1 : times_down(q.u, weight);
-                    const Found f = find<C>(sm, c, look, scale, ask != 0, target);
-                    key = f.bits, at_n = f.at_n;
-                    const uint32_t nth = ask == 0 ? most - 1 - f.before_n : quotient(target - f.before_w, f.weight);
-                    if (ask < 2) {
-                        share = nth + 1;
-                        kept = f.before_n + share;
-                        weight = f.before_w + share * f.weight;
-                    } else {
-                        place = nth;
-                        unit = f.weight;
-                    }
-                }
-            }
-            if (lane < C) {
-                Smem* to = of_rank<C>(&sm, lane);
-                to->kept = kept, to->key = key, to->share = share, to->at_n = at_n, to->rank = place;
-            }
-            if (lane == 0) {
-                if (a.kept) a.kept[r] = static_cast<int32_t>(kept);
-                if (DRAW && a.logprob) a.logprob[r] = log_share(unit, weight);
-            }
+            settle<DRAW, C>(a, static_cast<int>(r), q, scale, best, total, whole ? total : 0xffffffffu, rest.zeros);
         }
         sync_all<C>();
         // the histogram is done with
@@ -496,11 +729,14 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
 
         // ---- the tokens of one value, by index ----
         const uint32_t key = sm.key, at_n = sm.at_n, place = DRAW ? sm.rank : sm.share;
-        const bool uncut = !DRAW && sm.kept == total;                // nothing goes
+        const bool uncut = !DRAW && whole && sm.kept == total;       // nothing goes
         const uint32_t sign = (key & 0x7fffu) == 0 ? 0x80008000u : 0u, pair = (key & ~sign & 0xffffu) * 0x10001u;
         const uint32_t other = ~pair << 16;                          // beside a logit alone: not that value
         const bool some_stay = !DRAW && place < at_n && !uncut;      // of the last value, the first `place` stay
         const bool by_list = (DRAW || some_stay) && at_n <= kListed, by_index = (DRAW || some_stay) && !by_list;
+        // the head holds every logit from the last value on
+        const bool by_head = vectors > 0 && !uncut && !by_index && all.heads <= kHeads && key_of(value_of(key)) >= all.head;
+        const uint32_t heads = min(sm.heads, static_cast<uint32_t>(kHeads));
         auto put = [&](uint32_t token) { lead->list[atomicAdd(&lead->listed, 1u)] = token; };
         if (DRAW && by_list) {
             auto look_for = [&](const uint4& v, int v0) {
@@ -512,7 +748,9 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
                     if (m & 2) put(v0 * 8 + 2 * y + 1);
                 }
             };
-            int v0 = me;
+            if (by_head)
+                for (uint32_t x = tid; x < heads; x += kThreads) look_for(ld_row(row + static_cast<int64_t>(sm.head[x]) * 16), sm.head[x]);
+            int v0 = by_head ? vectors : me;
             for (; v0 + (U - 1) * kAll < vectors; v0 += U * kAll) {
                 uint4 v[U];
 #pragma unroll
@@ -527,63 +765,7 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
         }
         uint32_t last = 0;                                           // index of the token of that place (a truncation: the first that goes)
         if (by_index) {
-            // by runs of the row, a warp to each: counted, then the one that holds it
-            constexpr int kRuns = C * kWarps;
-            const int steps = (a.V + 255) / 256, run = (steps + kRuns - 1) / kRuns, mine = rank * kWarps + warp;
-            const int s0 = min(mine * run, steps), s1 = min(s0 + run, steps);
-            auto load = [&](int s, uint4 (&v)[U]) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if ((s + u) * 32 + lane < vectors) v[u] = ld_row(row + static_cast<int64_t>((s + u) * 32 + lane) * 16);
-            };
-            auto matches = [&](int s, const uint4& v) {          // among the lane's eight logits of step s, as bits
-                const int at = (s * 32 + lane) * 8;
-                if (s >= s1 || at >= a.V) return 0u;
-                if (s * 32 + lane < vectors)
-                    return halves_of(v.x, pair, sign) | halves_of(v.y, pair, sign) << 2 | halves_of(v.z, pair, sign) << 4 | halves_of(v.w, pair, sign) << 6;
-                uint32_t m = 0;
-                for (int y = 0; y < 8 && at + y < a.V; ++y) m |= (halves_of(cells[at + y] | other, pair, sign) & 1u) << y;
-                return m;
-            };
-            uint32_t n = 0;
-            for (int s = s0; s < s1; s += U) {
-                uint4 v[U];
-                load(s, v);
-#pragma unroll
-                for (int u = 0; u < U; ++u) n += __popc(matches(s + u, v[u]));
-            }
-            n = __reduce_add_sync(0xffffffffu, n);
-            if (lane < C) of_rank<C>(&sm, lane)->word[mine] = n;
-            sync_all<C>();
-            uint32_t before = 0;
-            for (int x = lane; x < mine; x += 32) before += sm.word[x];
-            before = __reduce_add_sync(0xffffffffu, before);
-            if (before <= place && place < before + n) {
-                bool done = false;
-                for (int s = s0; s < s1 && !done; s += U) {
-                    uint4 v[U];
-                    load(s, v);
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const uint32_t m = matches(s + u, v[u]), own = __popc(m), here = __reduce_add_sync(0xffffffffu, own);
-                        if (!done && place < before + here) {
-                            done = true;
-                            uint32_t upto = own;
-#pragma unroll
-                            for (int o = 1; o < 32; o <<= 1) {
-                                const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
-                                if (lane >= o) upto += x;
-                            }
-                            const uint32_t first = before + upto - own;
-                            if (first <= place && place < first + own)
-                                for (int c = 0; c < C; ++c)
-                                    of_rank<C>(&sm, c)->found = ((s + u) * 32 + lane) * 8 + __fns(m, 0, static_cast<int>(place - first) + 1);
-                        }
-                        before += here;
-                    }
-                }
-            }
-            sync_all<C>();
+            find_by_index<C>(cells, a.V, vectors, rank, pair, sign, place);
             last = sm.found;
             if (DRAW && me == 0) a.tokens[r] = static_cast<int32_t>(last);
         }
@@ -611,7 +793,35 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
                 st_hint(out + static_cast<int64_t>(v0) * 16,
                         make_uint4(cut(v.x, v0 * 8), cut(v.y, v0 * 8 + 2), cut(v.z, v0 * 8 + 4), cut(v.w, v0 * 8 + 6)), drop);
             };
-            if (out_vec) {
+            if (by_head) {
+                // the head is taken up, all becomes -infinity, and what the head keeps comes back
+                constexpr int kOwn = kHeads / kThreads;
+                uint4 v[kOwn];
+#pragma unroll
+                for (int x = 0; x < kOwn; ++x)
+                    if (tid + x * kThreads < heads) v[x] = ld_row(row + static_cast<int64_t>(sm.head[tid + x * kThreads]) * 16);
+                sync_all<C>();
+                const uint4 none = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+                for (int v0 = me; v0 < vectors; v0 += kAll) {
+                    if (out_vec)
+                        st_hint(out + static_cast<int64_t>(v0) * 16, none, drop);
+                    else
+                        for (int y = 0; y < 8; ++y) reinterpret_cast<unsigned short*>(out)[v0 * 8 + y] = 0xff80u;
+                }
+                sync_all<C>();
+#pragma unroll
+                for (int x = 0; x < kOwn; ++x)
+                    if (tid + x * kThreads < heads) {
+                        const int at = static_cast<int>(sm.head[tid + x * kThreads]);
+                        const uint32_t w[4] = {cut(v[x].x, at * 8), cut(v[x].y, at * 8 + 2), cut(v[x].z, at * 8 + 4), cut(v[x].w, at * 8 + 6)};
+                        if (out_vec)
+                            *reinterpret_cast<uint4*>(out + static_cast<int64_t>(at) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                        else
+#pragma unroll
+                            for (int y = 0; y < 8; ++y)
+                                reinterpret_cast<unsigned short*>(out)[at * 8 + y] = static_cast<unsigned short>(w[y / 2] >> (16 * (y % 2)));
+                    }
+            } else if (out_vec) {
                 int v0 = me;
                 for (; v0 + (U - 1) * kAll < vectors; v0 += U * kAll) {
                     uint4 v[U];
@@ -622,7 +832,7 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
                 }
                 for (; v0 < vectors; v0 += kAll) write(ld_hint(row + static_cast<int64_t>(v0) * 16, drop), v0);
             }
-            for (int y = (out_vec ? vectors * 8 : 0) + me; y < a.V; y += kAll)
+            for (int y = (out_vec || by_head ? vectors * 8 : 0) + me; y < a.V; y += kAll)
                 reinterpret_cast<unsigned short*>(out)[y] = static_cast<unsigned short>(cut(cells[y] | other, y));
         }
         if (by_list) {
@@ -642,6 +852,8 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
                 if (tid == 0) sm.listed = 0;
             }
         }
+        __syncthreads();
+        if (tid == 0) sm.heads = 0;
     }
     sync_all<C>();                                   // no CTA goes while another may still write to it
 }
