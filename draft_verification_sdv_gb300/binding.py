@@ -941,7 +941,7 @@ def sdv_prefix_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     B / groups sequences lies, block_table and ctx_len what each sequence has
     added behind it, on pages of its own.  A prefix is read once for all its
     sequences.  `workspace` (uint8) has sdv_prefix_attn_workspace(B, N, Hq, D)
-    bytes: some 40 MB and two fp32 rows for each row of out."""
+    bytes: some 40 MB and two or more fp32 rows for each row of out."""
     cache = _cache_of(k_cache, v_cache, k_exp, v_exp)
     (B, N, Hq, D), qs = _rows_of(q, 4, "q")
     code = _type_of(_HALF_TYPES, q.dtype, "q")

@@ -19,7 +19,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsdv.so")
 SOURCES = ["k1_rowpass.cu", "k2_select.cu", "k3_sample.cu", "k4_cps.cu", "k5_adl.cu", "k6_rope.cu", "k7_kvcache.cu",
            "k8_attn.cu", "k8_attn_tc.cu", "k8_attn_dec.cu", "k8_attn_mma64.cu", "k8_attn_mma128.cu", "k8_attn_mma256.cu",
-           "k8_attn_prefix.cu", "k9_logits.cu", "k10_tree.cu",
+           "k8_attn_prefix.cu", "k8_attn_one.cu", "k9_logits.cu", "k10_tree.cu",
            "k11_pages.cu", "k12_rows.cu", "k12_rows_bf16.cu",
            "sdv_api.cu", "sdv_layer.cu", "sdv_static.cu"]
 HEADERS = ["sdv_device.cuh", "sdv_plan.h", "sdv_layer.h", "k8_attn.cuh", "k8_attn_mma.cuh", "k8_attn_tma.cuh", "k12_rows.cuh"]

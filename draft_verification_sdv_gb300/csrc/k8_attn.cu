@@ -26,6 +26,7 @@ constexpr int kDecRows = 16, kDecRowsE4m3 = 80;
 // unit: 21 us in 16, 38 us in 8 that read twice; 32 gain nothing more).
 template <bool F16>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, int MT) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 d0 = a.desc[2 * blockIdx.x];
     if (d0.x < 0) return;

@@ -401,6 +401,12 @@ cudaError_t launch_attn_tc(const AttnArgs& a, bool f16, bool e4m3, int nsm, cuda
 // otherwise its blocks end at once, 3 us later.  8 trees of 65 nodes behind 4000
 // positions, 8 x 8 heads of 128: 258 us, and 754 us with such a row in each.
 cudaError_t launch_attn_redo(const AttnArgs& a, int nsm, cudaStream_t s);
+// Single tokens (N = 1) over their sequences' own positions, joined with the rows
+// `far` and their logs that the kernel before leaves; or, with splits > 1, the parts
+// a.raw [splits][B * Hq][D] and a.raw_log, where a log of -infinity has no row.
+// Whether it takes these heads.
+bool attn_one_takes(const AttnArgs& a);
+cudaError_t launch_attn_one(const AttnArgs& a, bool f16, bool e4m3, const float* far, const float* far_log, int splits, cudaStream_t s);
 // Joins the partial results of the kernel just launched with row tiles of MT.
 cudaError_t launch_attn_combine(const AttnArgs& a, bool f16, int MT, cudaStream_t s);
 

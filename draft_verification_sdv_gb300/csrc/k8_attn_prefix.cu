@@ -3,11 +3,13 @@
 //
 // The nodes of a group's sequences are to its prefix what the nodes of one
 // sequence are to theirs: one batch of S * N nodes that all see the prefix and
-// nothing of one another.  So the attention kernels run twice, over the prefixes
-// with a group for a sequence, which reads a prefix once for all its sequences,
-// and over the sequences' own pages; each time they leave normalised fp32 rows
-// and the base-2 logs L of their sums.  A row's two results join as
-//   out = (2^(L1 - L) o1 + 2^(L2 - L) o2),   L = log2(2^L1 + 2^L2).
+// nothing of one another.  So the attention kernels run over the prefixes with a
+// group for a sequence, which reads a prefix once for all its sequences, and leave
+// normalised fp32 rows and the base-2 logs L of their sums.  What the sequences have
+// added comes from the same kernels, or for single tokens from k8_attn_one.cu.  A
+// row's results join as
+//   out = sum_i 2^(L_i - L) o_i,   L = log2 sum_i 2^(L_i),
+// in the kernel of single tokens, or in one of its own.
 #include "k8_attn.cuh"
 
 namespace sdv {
@@ -15,48 +17,88 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Four elements of a row to a thread.
+// Parts of single tokens' own positions, where there are few heads to share out.
+constexpr int kMaxSplits = 8;
+int splits_of(int64_t rows, int N) {
+    const int64_t n = N > 1 ? 1 : 8192 / rows;       // 64 heads: one part from 128 sequences on
+    return static_cast<int>(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
+}
+
+// Four elements of a row to a thread; near: `parts` of [rows][D], whose rows are only
+// there where their log is not -infinity.
 template <bool F16>
 __global__ void __launch_bounds__(kThreads) join_kernel(const AttnArgs a, const float* far, const float* far_log, const float* near,
-                                                        const float* near_log, int64_t rows) {
+                                                        const float* near_log, int parts, int64_t rows) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int vec = a.c.D / 4;
     const int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
     const int64_t row = i / vec;
     if (row >= rows) return;
     const int d = static_cast<int>(i - row * vec) * 4;
     const float nan = __int_as_float(0x7fc00000);
-    const float L1 = far_log[row], L2 = near_log[row];
-    const float4 x = *reinterpret_cast<const float4*>(far + row * a.c.D + d);
-    const float4 y = *reinterpret_cast<const float4*>(near + row * a.c.D + d);
+    float L[kMaxSplits + 1];
+    L[0] = far_log[row];
+#pragma unroll
+    for (int p = 0; p < kMaxSplits; ++p) L[p + 1] = p < parts ? near_log[p * rows + row] : -INFINITY;
     const int64_t node = row / a.Hq;
     const int b = static_cast<int>(node / a.N);
-    // (a bad sequence's second result is not a number; nodes that are not there see nothing)
-    const bool there = !a.count || node - static_cast<int64_t>(b) * a.N < a.count[b] || L2 != L2;
-    const float top = fmaxf(L1, L2), base = top == -INFINITY ? 0.0f : top;
-    const float f1 = ex2(L1 - base), f2 = ex2(L2 - base), sum = f1 + f2;
-    const bool bad = L1 != L1 || L2 != L2, empty = !there || (!bad && top == -INFINITY);
-    const float g1 = empty ? 0.0f : bad ? nan : f1 / sum, g2 = empty ? 0.0f : bad ? nan : f2 / sum;
-    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (!empty) {
-        // (an empty side's row is 0, and its factor too)
-        o[0] = x.x * g1 + y.x * g2, o[1] = x.y * g1 + y.y * g2;
-        o[2] = x.z * g1 + y.z * g2, o[3] = x.w * g1 + y.w * g2;
+    float top = -INFINITY;
+    bool bad = false, bad_near = false;
+#pragma unroll
+    for (int p = 0; p <= kMaxSplits; ++p) {
+        top = fmaxf(top, L[p]);
+        bad |= L[p] != L[p];
+        bad_near |= p > 0 && L[p] != L[p];
     }
+    // (a bad sequence's own result is not a number; nodes that are not there see nothing)
+    const bool there = !a.count || node - static_cast<int64_t>(b) * a.N < a.count[b] || bad_near;
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int p = 0; p <= kMaxSplits; ++p) {
+        if (L[p] == -INFINITY) continue;
+        const float4 x = *reinterpret_cast<const float4*>((p == 0 ? far : near + (p - 1) * rows * a.c.D) + row * a.c.D + d);
+        const float f = ex2(L[p] - base);
+        sum += f;
+        o[0] += x.x * f, o[1] += x.y * f, o[2] += x.z * f, o[3] += x.w * f;
+    }
+    const bool empty = !there || (!bad && sum == 0.0f);
+    const float inv = empty ? 0.0f : bad ? nan : 1.0f / sum;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[x] = empty ? 0.0f : o[x] * inv;
     attn::store_row4<F16>(a, row, d, o, empty ? -INFINITY : bad ? nan : base + log2f(sum));
+}
+
+template <bool F16>
+cudaError_t launch_join(const AttnArgs& a, const float* far, const float* far_log, const float* near, const float* near_log, int parts,
+                        int64_t rows, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((rows * (a.c.D / 4) + kThreads - 1) / kThreads));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<F16>, a, far, far_log, near, near_log, parts, rows);
 }
 
 }  // namespace
 
-size_t prefix_workspace_bytes(int64_t rows, int D, int nsm) {
+size_t prefix_workspace_bytes(int B, int N, int Hq, int D, int nsm) {
+    const int64_t rows = static_cast<int64_t>(B) * N * Hq;
     const size_t one = static_cast<size_t>(rows) * (D + 1) * sizeof(float);
-    return (attn_workspace_bytes(nsm) + 31) / 32 * 32 + 2 * ((one + 31) / 32 * 32);
+    return (attn_workspace_bytes(nsm) + 31) / 32 * 32 + (1 + splits_of(rows, N)) * ((one + 31) / 32 * 32);
 }
 
 cudaError_t launch_prefix_attn(const AttnArgs& a, const PrefixArgs& p, int type, bool e4m3, void* workspace, int nsm, cudaStream_t s) {
-    const int64_t rows = static_cast<int64_t>(a.B) * a.N * a.Hq;
-    unsigned char* at = static_cast<unsigned char*>(workspace) + (attn_workspace_bytes(nsm) + 31) / 32 * 32;
-    const size_t one = (static_cast<size_t>(rows) * (a.c.D + 1) * sizeof(float) + 31) / 32 * 32;
-    float* raw[2] = {reinterpret_cast<float*>(at), reinterpret_cast<float*>(at + one)};
+    const int64_t rows = static_cast<int64_t>(a.B) * a.N * a.Hq, cells = rows * a.c.D;
+    const bool f16 = type == kTypeF16;
+    float* far_rows = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + (attn_workspace_bytes(nsm) + 31) / 32 * 32);
+    float* near_rows = far_rows + (cells + rows + 7) / 8 * 8;
+    const bool single = attn_one_takes(a);
+    const int parts = single ? splits_of(rows, a.N) : 1;
 
     AttnArgs far = a, near = a;
     const int each = a.B / p.groups;
@@ -72,17 +114,14 @@ cudaError_t launch_prefix_attn(const AttnArgs& a, const PrefixArgs& p, int type,
     far.table = p.table, far.max_pages = p.max_pages, far.ctx = p.len;
     far.count = nullptr;
     far.mask = p.table, far.mask_sb = 0, far.W = 0;  // (a mask without words: no node sees another)
-    far.raw = raw[0], far.raw_log = raw[0] + rows * a.c.D;
-    near.raw = raw[1], near.raw_log = raw[1] + rows * a.c.D;
+    far.raw = far_rows, far.raw_log = far_rows + cells;
+    near.raw = near_rows, near.raw_log = near_rows + parts * cells;
     cudaError_t e = launch_tree_attn(far, type, e4m3, workspace, nsm, s);
-    if (e == cudaSuccess) e = launch_tree_attn(near, type, e4m3, workspace, nsm, s);
-    if (e != cudaSuccess) return e;
-    const int64_t blocks = (rows * (a.c.D / 4) + kThreads - 1) / kThreads;
-    if (type == kTypeF16)
-        join_kernel<true><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a, far.raw, far.raw_log, near.raw, near.raw_log, rows);
-    else
-        join_kernel<false><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a, far.raw, far.raw_log, near.raw, near.raw_log, rows);
-    return cudaGetLastError();
+    if (e == cudaSuccess)
+        e = single ? launch_attn_one(near, f16, e4m3, far.raw, far.raw_log, parts, s) : launch_tree_attn(near, type, e4m3, workspace, nsm, s);
+    if (e != cudaSuccess || (single && parts == 1)) return e;
+    return f16 ? launch_join<true>(a, far.raw, far.raw_log, near.raw, near.raw_log, parts, rows, s)
+               : launch_join<false>(a, far.raw, far.raw_log, near.raw, near.raw_log, parts, rows, s);
 }
 
 }  // namespace sdv

@@ -385,7 +385,7 @@ sdv_status sdv_tree_attn(const sdv_kv_cache* cache, int B, int N, int Hq, sdv_dt
 size_t sdv_prefix_attn_workspace(int B, int N, int Hq, int head_dim) {
     if (!prefix_shape_ok(B, N, Hq) || head_dim < 16 || head_dim > kCacheMaxDim || head_dim % 16) return 0;
     const int nsm = sm_count();
-    return nsm > 0 ? prefix_workspace_bytes(static_cast<int64_t>(B) * N * Hq, head_dim, nsm) : 0;
+    return nsm > 0 ? prefix_workspace_bytes(B, N, Hq, head_dim, nsm) : 0;
 }
 
 sdv_status sdv_prefix_attn(const sdv_kv_cache* cache, int B, int groups, int N, int Hq, sdv_dtype dtype,
@@ -406,7 +406,7 @@ sdv_status sdv_prefix_attn(const sdv_kv_cache* cache, int B, int groups, int N, 
     if (!all_device(ptrs)) return SDV_ERR_ARG;
     const int nsm = sm_count();
     if (nsm < 1) return SDV_ERR_CUDA;
-    if (workspace_bytes < prefix_workspace_bytes(static_cast<int64_t>(B) * N * Hq, a.c.D, nsm)) return SDV_ERR_SCRATCH;
+    if (workspace_bytes < prefix_workspace_bytes(B, N, Hq, a.c.D, nsm)) return SDV_ERR_SCRATCH;
     const PrefixArgs p{prefix_table, prefix_len, max_prefix_pages, groups};
     return done(launch_prefix_attn(a, p, dtype, cache->dtype == SDV_E4M3, workspace, nsm, stream_of(stream)));
 }

@@ -102,7 +102,7 @@ struct PrefixArgs {
     const int32_t *table, *len;
     int max_pages, groups;
 };
-size_t prefix_workspace_bytes(int64_t rows, int D, int nsm);      // rows: B * N * Hq
+size_t prefix_workspace_bytes(int B, int N, int Hq, int D, int nsm);
 cudaError_t launch_prefix_attn(const AttnArgs& a, const PrefixArgs& p, int type, bool e4m3, void* workspace, int nsm,
                                cudaStream_t s);
 
