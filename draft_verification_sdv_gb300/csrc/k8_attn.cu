@@ -96,6 +96,10 @@ size_t attn_workspace_bytes(int nsm) {
     return nsm * (kMaxCtasPerSm * 2 * sizeof(int4) + 2 * most * sizeof(float) + sizeof(unsigned));
 }
 
+bool attn_goes_on(const AttnArgs& a, bool f16, bool e4m3) {
+    return attn_tma_takes(a) && a.N * a.g > (e4m3 ? kDecRowsE4m3 : kDecRows) && !(f16 && e4m3);
+}
+
 cudaError_t launch_tree_attn(AttnArgs a, int type, bool e4m3, void* workspace, int nsm, cudaStream_t s) {
     a.desc = static_cast<int4*>(workspace);
     a.part = reinterpret_cast<float*>(a.desc + 2 * kMaxCtasPerSm * nsm);

@@ -396,6 +396,8 @@ cudaError_t launch_attn_mma256(const AttnArgs& a, bool f16, bool e4m3, int rows,
 bool attn_tma_takes(const AttnArgs& a);
 cudaError_t launch_attn_dec(const AttnArgs& a, bool f16, bool e4m3, int nsm, cudaStream_t s);
 cudaError_t launch_attn_tc(const AttnArgs& a, bool f16, bool e4m3, int nsm, cudaStream_t s);
+// Whether launch_tree_attn takes a.far for these rows.
+bool attn_goes_on(const AttnArgs& a, bool f16, bool e4m3);
 // After launch_attn_tc with fp16 queries on an e4m3 cache: does the call again, in
 // units of 16 rows, if a block has met rows that fp16 does not hold (a.beyond);
 // otherwise its blocks end at once, 3 us later.  8 trees of 65 nodes behind 4000

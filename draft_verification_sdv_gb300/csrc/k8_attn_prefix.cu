@@ -9,7 +9,8 @@
 // added comes from the same kernels, or for single tokens from k8_attn_one.cu.  A
 // row's results join as
 //   out = sum_i 2^(L_i - L) o_i,   L = log2 sum_i 2^(L_i),
-// in the kernel of single tokens, or in one of its own.
+// in the kernel of single tokens; in the kernel of many rows, which goes on from the
+// prefix's; or in one of its own.
 #include "k8_attn.cuh"
 
 namespace sdv {
@@ -26,7 +27,7 @@ int splits_of(int64_t rows, int N) {
 
 // Four elements of a row to a thread; near: `parts` of [rows][D], whose rows are only
 // there where their log is not -infinity.
-template <bool F16>
+template <bool F16, int MOST>
 __global__ void __launch_bounds__(kThreads) join_kernel(const AttnArgs a, const float* far, const float* far_log, const float* near,
                                                         const float* near_log, int parts, int64_t rows) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -36,16 +37,16 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const AttnArgs a, const 
     if (row >= rows) return;
     const int d = static_cast<int>(i - row * vec) * 4;
     const float nan = __int_as_float(0x7fc00000);
-    float L[kMaxSplits + 1];
+    float L[MOST + 1];
     L[0] = far_log[row];
 #pragma unroll
-    for (int p = 0; p < kMaxSplits; ++p) L[p + 1] = p < parts ? near_log[p * rows + row] : -INFINITY;
+    for (int p = 0; p < MOST; ++p) L[p + 1] = p < parts ? near_log[p * rows + row] : -INFINITY;
     const int64_t node = row / a.Hq;
     const int b = static_cast<int>(node / a.N);
     float top = -INFINITY;
     bool bad = false, bad_near = false;
 #pragma unroll
-    for (int p = 0; p <= kMaxSplits; ++p) {
+    for (int p = 0; p <= MOST; ++p) {
         top = fmaxf(top, L[p]);
         bad |= L[p] != L[p];
         bad_near |= p > 0 && L[p] != L[p];
@@ -55,7 +56,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const AttnArgs a, const 
     const float base = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int p = 0; p <= kMaxSplits; ++p) {
+    for (int p = 0; p <= MOST; ++p) {
         if (L[p] == -INFINITY) continue;
         const float4 x = *reinterpret_cast<const float4*>((p == 0 ? far : near + (p - 1) * rows * a.c.D) + row * a.c.D + d);
         const float f = ex2(L[p] - base);
@@ -69,9 +70,9 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const AttnArgs a, const 
     attn::store_row4<F16>(a, row, d, o, empty ? -INFINITY : bad ? nan : base + log2f(sum));
 }
 
-template <bool F16>
-cudaError_t launch_join(const AttnArgs& a, const float* far, const float* far_log, const float* near, const float* near_log, int parts,
-                        int64_t rows, cudaStream_t s) {
+// from: rows and logs of the prefix, rows and logs of the parts.
+template <bool F16, int MOST>
+cudaError_t launch_join(const AttnArgs& a, const float* const (&from)[4], int64_t rows, cudaStream_t s, int parts = 1) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((rows * (a.c.D / 4) + kThreads - 1) / kThreads));
     cfg.blockDim = dim3(kThreads);
@@ -81,7 +82,7 @@ cudaError_t launch_join(const AttnArgs& a, const float* far, const float* far_lo
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<F16>, a, far, far_log, near, near_log, parts, rows);
+    return cudaLaunchKernelEx(&cfg, join_kernel<F16, MOST>, a, from[0], from[1], from[2], from[3], parts, rows);
 }
 
 }  // namespace
@@ -115,13 +116,20 @@ cudaError_t launch_prefix_attn(const AttnArgs& a, const PrefixArgs& p, int type,
     far.count = nullptr;
     far.mask = p.table, far.mask_sb = 0, far.W = 0;  // (a mask without words: no node sees another)
     far.raw = far_rows, far.raw_log = far_rows + cells;
-    near.raw = near_rows, near.raw_log = near_rows + parts * cells;
     cudaError_t e = launch_tree_attn(far, type, e4m3, workspace, nsm, s);
-    if (e == cudaSuccess)
-        e = single ? launch_attn_one(near, f16, e4m3, far.raw, far.raw_log, parts, s) : launch_tree_attn(near, type, e4m3, workspace, nsm, s);
+    if (e != cudaSuccess) return e;
+    // many rows go on from the prefix's outputs themselves (trees of 257 nodes: no join of
+    // 270 MB; not where fp16 queries may make them be done again)
+    if (attn_goes_on(near, f16, e4m3)) {
+        near.far = far.raw, near.far_log = far.raw_log;
+        return launch_tree_attn(near, type, e4m3, workspace, nsm, s);
+    }
+    near.raw = near_rows, near.raw_log = near_rows + parts * cells;
+    e = single ? launch_attn_one(near, f16, e4m3, far.raw, far.raw_log, parts, s) : launch_tree_attn(near, type, e4m3, workspace, nsm, s);
     if (e != cudaSuccess || (single && parts == 1)) return e;
-    return f16 ? launch_join<true>(a, far.raw, far.raw_log, near.raw, near.raw_log, parts, rows, s)
-               : launch_join<false>(a, far.raw, far.raw_log, near.raw, near.raw_log, parts, rows, s);
+    const float* rows_of[4] = {far.raw, far.raw_log, near.raw, near.raw_log};
+    if (parts == 1) return f16 ? launch_join<true, 1>(a, rows_of, rows, s) : launch_join<false, 1>(a, rows_of, rows, s);
+    return f16 ? launch_join<true, kMaxSplits>(a, rows_of, rows, s, parts) : launch_join<false, kMaxSplits>(a, rows_of, rows, s, parts);
 }
 
 }  // namespace sdv

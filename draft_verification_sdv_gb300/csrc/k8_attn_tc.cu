@@ -469,6 +469,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             if (tid == 0 && u.cut.bad && a.status) atomicOr(a.status, kStatusBadLength);
             float m = -INFINITY, l = 0.0f;
             bool nan_row = false;
+            const bool begun = a.far != nullptr && u.t0 == 0;    // rows go on from others' outputs
+            if (run && begun) {
+                const int64_t from = (static_cast<int64_t>(u.b) * a.N + (live ? node : 0)) * a.Hq + u.h * a.g + row % a.g;
+                const float L = live ? a.far_log[from] : -INFINITY;
+                nan_row = L != L;
+                const bool some = L > -INFINITY;     // (normalised: of a sum of 1 in units of 2^L)
+                if (some) m = L, l = 1.0f;
+                const float* src = a.far + from * D;
+#pragma unroll 1
+                for (int i = 0; i < D; i += 16) {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int y = 0; y < 16; y += 4) {
+                        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (some) x = *reinterpret_cast<const float4*>(src + i + y);
+                        o[y] = __float_as_uint(x.x), o[y + 1] = __float_as_uint(x.y), o[y + 2] = __float_as_uint(x.z), o[y + 3] = __float_as_uint(x.w);
+                    }
+                    __syncwarp();
+                    tmem_st16(tO + i, o);
+                }
+                tmem_wait_st();
+            }
             if (run) {
                 const int32_t* table = a.table + static_cast<int64_t>(u.b) * a.max_pages;
                 const int32_t* mrow = a.mask ? a.mask + u.b * a.mask_sb + static_cast<int64_t>(live ? node : 0) * a.W : nullptr;
@@ -553,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
                             for (int y = 0; y < 32; ++y) x[32 * i + y] = see[i] >> y & 1 ? x[32 * i + y] : -INFINITY;
                     }
-                    weigh(x, t == 0);
+                    weigh(x, t == 0 && !begun);
                     if (mixed) {                     // values that are not numbers, among those that the row sees
                         const uint32_t T = nv + t;
                         sync.wait(kFull + ((T + 1) & 1), (T + 1) >> 1 & 1);
@@ -908,6 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             if (nt == 0) continue;
             // stream s has a live row (stream 0 has one in every unit with tiles)
             const int streams = (u.mt * MT + kRows) / a.g < u.cut.cnt ? 2 : 1;
+            const bool begun = a.far != nullptr && u.t0 == 0;    // the softmax warps have set the outputs
             // (the unit before has waited for these keys with its last values)
             if (T == 0) ok = sync.wait(kFull, 0) && ok;
 #pragma unroll
@@ -934,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         if (ok) {
                             const uint32_t x = tm + s * 128, y = ring_v + (kKeySlots + (T & 1)) * (kTile >> 4), d = tm + 256 + s * 128;
 #pragma unroll
-                            for (int ks = 0; ks < BN / 16; ++ks) mma_ts(d, x + ks * 8, y + ks * (2048 >> 4), idesc_o, t > 0 || ks > 0);
+                            for (int ks = 0; ks < BN / 16; ++ks) mma_ts(d, x + ks * 8, y + ks * (2048 >> 4), idesc_o, t > 0 || ks > 0 || begun);
                         }
                         if (!more) sync.commit(kOFull + s);
                     }

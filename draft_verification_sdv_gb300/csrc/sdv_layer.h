@@ -80,6 +80,7 @@ struct AttnArgs {
     void* out;
     float* lse;
     float *raw, *raw_log;             // not NULL: rows go here as fp32, with the base-2 logs of their sums
+    const float *far, *far_log;       // not NULL: rows to go on from (launch_attn_tc alone, without a raw)
     unsigned* status;
     float* part;                      // partial outputs (see part_rows)
     int4* desc;                       // two per CTA: the unit that its start splits
