@@ -1,11 +1,17 @@
 // k12_rows.cu -- draws from rows of logits and their truncation (sdv_sample,
 // sdv_logits_truncate): rows in 32 bits.
 //
-// A CTA takes a row at a time and reads it in passes (row_in_passes): the largest
-// logit; a histogram of counts and weights over 4096 bins of equal width in
-// (max - x) / T, which keeps the order; then, for each of the places that are asked
-// for (the last token that min-p and top-k keep, the last that top-p keeps, the one
-// that is drawn), the bin that holds it is split by keys until one logit is left.
+// What a row keeps or draws is nearly always among the few hundred largest logits.  A
+// sample gives a bound that so many reach; one look at the row writes those, the
+// head, into a list, which is sorted by logit and index.  There top-k, min-p, top-p
+// and the draw are places of running sums.  Where only top-p or the draw limits the
+// row, a second look adds up all weights (whole numbers: the sum is the one that
+// any other order gives), and the head's share of them tells whether the place lies in
+// it.  Other rows go the long way, in passes over histograms (row_in_passes).
+//
+// A row is shared by a cluster of C CTAs where there are few; the first one has the list.
+// What bounds it: for the first look the row's bytes, for the second the
+// instructions of a weight.
 #include "k12_rows.cuh"
 
 namespace sdv {
@@ -13,25 +19,391 @@ namespace {
 
 using namespace rows;
 
-constexpr int kThreads = 512, kBins = 4096;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = 4096;
+constexpr int kList = 2048, kOwn = kList / kThreads;
+constexpr uint32_t kOddNan = 1u;
 
-template <bool DRAW> __global__ void __launch_bounds__(kThreads, 2) rows_f32_kernel(const RowsArgs a) {
+struct Head {
+    uint64_t list[kList];                // key << 32 | ~index, 0: none
+    uint64_t before[kList];              // weight of those before
+    Tables tables;
+    Factors factors;
+    float floor;
+    uint64_t sum[kWarps], total;
+    uint32_t word[8 * kWarps];
+    uint32_t listed, odd, finite, over, at;
+    uint64_t part[8];                    // weights and counts of the CTAs' parts
+    uint32_t count[8], strange[8];
+    // what the first CTA has found
+    uint32_t verdict, kept;
+};
+union Smem {
+    Head head;
+    PassSmem<kThreads, kBins> passes;
+};
+static_assert(2 * (sizeof(Smem) + 1024) <= 227 * 1024, "two CTAs per SM");
+enum : uint32_t { kDone, kCopy, kBad, kLongWay };        // verdicts: kept ones are the list's first; all are kept
+
+__device__ __forceinline__ Smem& smem() {
     extern __shared__ __align__(16) unsigned char raw[];
-    PassSmem<kThreads, kBins>& sm = *reinterpret_cast<PassSmem<kThreads, kBins>*>(raw);
-    load_tables(sm.tables, threadIdx.x, kThreads);
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        row_in_passes<false, DRAW, kThreads, kBins>(a, r, sm);
-        __syncthreads();
+    return *reinterpret_cast<Smem*>(raw);
+}
+
+__device__ __forceinline__ float largest_of(const uint4& v) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+
+// Writes the logits of this CTA's part of a row that reach the bound into the first CTA's
+// list; whether there is a NaN or +infinity into `odd`.  Returns the bound, a key.
+template <int C> __device__ __noinline__ uint32_t list_head(const unsigned char* row, int V, int vectors, int rank) {
+    constexpr int U = 4, kAll = C * kThreads, kSamples = C * kWarps * 2;
+    Head& sm = smem().head;
+    Head* const lead = of_rank<C>(&sm, 0);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = rank * kThreads + threadIdx.x;
+    const uint64_t keep = keep_policy();
+    uint32_t bound = kKeyLow + 1;                    // (a short row is head as a whole)
+    if (V > kList) {
+        const int chunks = (V / 4 + 31) / 32;        // (as if it were aligned)
+        uint32_t least = 0xffffffffu, most = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int n = (rank * kWarps + warp) * 2 + u;
+            const int at = (chunks >= kSamples ? static_cast<int>(static_cast<uint32_t>(n) * chunks / kSamples) : n) * 32 + lane;
+            float x = -INFINITY;
+            if (at < vectors)
+                x = largest_of(ld_hint(row + static_cast<int64_t>(at) * 16, keep));
+            else if (at < V / 4)
+                for (int y = 0; y < 4; ++y) x = fmaxf(x, reinterpret_cast<const float*>(row)[at * 4 + y]);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, x > -INFINITY ? key_of(x) : 0u);
+            if (top) least = min(least, top);
+            most = max(most, top);
+        }
+        if (lane < C) of_rank<C>(&sm, lane)->word[rank * kWarps + warp] = V < kManyLogits || most == 0 ? least : most;
+        sync_all<C>();
+        bound = min(fourth_smallest<C * kWarps>(sm.word), kKeyHigh);
+    }
+    const float f = of_key(bound);
+    float most = -INFINITY;
+    bool odd = false;
+    auto put = [&](float x, int index) {
+        if (!(x >= f)) return;
+        const uint32_t n = atomicAdd(&lead->listed, 1u);
+        if (n < kList) lead->list[n] = static_cast<uint64_t>(key_of(x)) << 32 | static_cast<uint32_t>(~index);
+    };
+    auto take = [&](const uint4& v, int index) {
+        const float x = __uint_as_float(v.x), y = __uint_as_float(v.y), z = __uint_as_float(v.z), w = __uint_as_float(v.w);
+        const float top = fmaxf(fmaxf(x, y), fmaxf(z, w));
+        most = fmaxf(most, top);
+        odd |= !((x + y) + (z + w) < INFINITY) && (x != x || y != y || z != z || w != w);
+        if (top >= f) put(x, index * 4), put(y, index * 4 + 1), put(z, index * 4 + 2), put(w, index * 4 + 3);
+    };
+    int i = me;
+    for (; i + (U - 1) * kAll < vectors; i += U * kAll) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = ld_hint(row + static_cast<int64_t>(i + u * kAll) * 16, keep);
+#pragma unroll
+        for (int u = 0; u < U; ++u) take(v[u], i + u * kAll);
+    }
+    for (; i < vectors; i += kAll) take(ld_hint(row + static_cast<int64_t>(i) * 16, keep), i);
+    for (int y = vectors * 4 + me; y < V; y += kAll) {
+        const float x = reinterpret_cast<const float*>(row)[y];
+        odd |= x != x;
+        most = fmaxf(most, x);
+        put(x, y);
+    }
+    odd |= most == INFINITY;
+    if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(&sm.odd, kOddNan);
+    return bound;
+}
+
+// Weights and number of the finite logits of this CTA's part, told to every CTA.
+template <int C> __device__ __noinline__ void sum_all(const unsigned char* row, int V, int vectors, int rank, const Scale scale) {
+    constexpr int U = 2, kAll = C * kThreads;
+    Head& sm = smem().head;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = rank * kThreads + threadIdx.x;
+    uint64_t sum = 0;
+    uint32_t n = 0;
+    auto add = [&](float x) {
+        sum += weight_of(scale, x, sm.tables);
+        n += x > -INFINITY;
+    };
+    auto take = [&](const uint4& v) {
+        add(__uint_as_float(v.x)), add(__uint_as_float(v.y)), add(__uint_as_float(v.z)), add(__uint_as_float(v.w));
+    };
+    int i = me;
+    for (; i + (U - 1) * kAll < vectors; i += U * kAll) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = ld_row(row + static_cast<int64_t>(i + u * kAll) * 16);
+#pragma unroll
+        for (int u = 0; u < U; ++u) take(v[u]);
+    }
+    for (; i < vectors; i += kAll) take(ld_row(row + static_cast<int64_t>(i) * 16));
+    for (int y = vectors * 4 + me; y < V; y += kAll) add(reinterpret_cast<const float*>(row)[y]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    n = __reduce_add_sync(0xffffffffu, n);
+    __syncthreads();
+    if (lane == 0) sm.sum[warp] = sum, sm.word[warp] = n;
+    __syncthreads();
+    if (threadIdx.x < C) {
+        uint64_t s = 0;
+        uint32_t c = 0;
+        for (int w = 0; w < kWarps; ++w) s += sm.sum[w], c += sm.word[w];
+        Head* to = of_rank<C>(&sm, threadIdx.x);
+        to->part[rank] = s, to->count[rank] = c;
     }
 }
 
-template <bool DRAW> cudaError_t launch(const RowsArgs& a, int nsm, cudaStream_t s) {
-    constexpr size_t bytes = sizeof(PassSmem<kThreads, kBins>);
-    const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(rows_f32_kernel<DRAW>), bytes);
+// The list's first `n` entries in falling order (n at most a power of two `size`, the rest 0).
+__device__ __noinline__ void sort_list(int size) {
+    Head& sm = smem().head;
+    for (int k = 2; k <= size; k <<= 1)
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            __syncthreads();
+            for (int x = threadIdx.x; x < size / 2; x += kThreads) {
+                const int lo = 2 * x - (x & (j - 1)), hi = lo + j;   // pairs j apart
+                const uint64_t a = sm.list[lo], b = sm.list[hi];
+                if ((a < b) == ((lo & k) == 0)) sm.list[lo] = b, sm.list[hi] = a;
+            }
+        }
+    __syncthreads();
+}
+
+// The weights before each of the list's n entries, and their total.
+__device__ __noinline__ void sum_list(int n, const Scale scale) {
+    Head& sm = smem().head;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint64_t w[kOwn], own = 0;
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x) {
+        const int i = tid * kOwn + x;
+        w[x] = i < n ? weight_of(scale, of_key(static_cast<uint32_t>(sm.list[i] >> 32)), sm.tables) : 0;
+        own += w[x];
+    }
+    uint64_t upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    if (lane == 31) sm.sum[warp] = upto;
+    __syncthreads();
+    uint64_t before = upto - own;
+    for (int x = 0; x < warp; ++x) before += sm.sum[x];
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x) {
+        sm.before[tid * kOwn + x] = before;
+        before += w[x];
+    }
+    if (tid == kThreads - 1) sm.total = before;
+    __syncthreads();
+}
+
+// The entry where the running weight passes `target` (less than the total): into sm.at.
+__device__ __forceinline__ int find(Head& sm, int n, uint64_t target) {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint64_t end = i + 1 < n ? sm.before[i + 1] : sm.total;
+        if (sm.before[i] <= target && target < end) sm.at = i;
+    }
+    __syncthreads();
+    const int at = static_cast<int>(sm.at);
+    __syncthreads();
+    return at;
+}
+
+template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_f32_kernel(const RowsArgs a) {
+    Head& sm = smem().head;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int me = rank * kThreads + tid;
+    constexpr int kAll = C * kThreads;
+    const float nan = __int_as_float(0x7fc00000);
+    bool tables = false;
+    for (int64_t r = blockIdx.x / C; r < a.rows; r += gridDim.x / C) {
+        const Ask q = ask_of(a, r);
+        const unsigned char* row = static_cast<const unsigned char*>(a.logits) + r * a.in_stride;
+        float* out = reinterpret_cast<float*>(static_cast<unsigned char*>(a.out) + r * a.out_stride);
+        const int vectors = (reinterpret_cast<uintptr_t>(row) & 15) == 0 ? a.V / 4 : 0;
+        sync_all<C>();                               // (the row before is done with shared memory)
+        if (!tables) load_tables(sm.tables, tid, kThreads);
+        tables = true;
+        if (tid == 0) sm.listed = sm.odd = 0;
+        if (tid == kThreads - 1) sm.factors = factors_of(q.T, q.min_p);
+        sync_all<C>();
+        const uint32_t bound = list_head<C>(row, a.V, vectors, rank);
+        __syncthreads();
+        if (tid < C) of_rank<C>(&sm, tid)->strange[rank] = sm.odd;
+        sync_all<C>();
+        uint32_t odd = 0;
+        for (int c = 0; c < C; ++c) odd |= sm.strange[c];
+        const uint32_t listed = of_rank<C>(&sm, 0)->listed;
+
+        // ---- the head, sorted ----
+        const int n = static_cast<int>(min(listed, static_cast<uint32_t>(kList)));
+        const bool usable = !q.bad && !odd && listed > 0 && listed <= kList;
+        int size = 32;
+        while (size < n) size <<= 1;
+        if (rank == 0 && usable) {
+            for (int i = n + tid; i < size; i += kThreads) sm.list[i] = 0;
+            sort_list(size);
+        }
+        sync_all<C>();
+        const float top = usable ? of_key(static_cast<uint32_t>(of_rank<C>(&sm, 0)->list[0] >> 32)) : 0.0f;
+        const Scale scale{top, sm.factors.hi, sm.factors.lo};
+        // does it hold what top-k and min-p keep, or do all weights have to be known?
+        if (tid == 0) sm.floor = usable && q.min_p > 0.0f ? floor_of(top, sm.factors.reach) : -INFINITY;
+        __syncthreads();
+        const float floor = sm.floor;
+        const bool by_floor = q.min_p > 0.0f && floor >= of_key(bound), by_k = q.top_k > 0 && q.top_k <= n;
+        const bool limited = q.T == 0.0f || by_floor || by_k;
+        const bool whole = bound == kKeyLow + 1;     // the list holds every finite logit
+        const bool sums = usable && !limited && !whole && q.top_k == 0 && q.min_p == 0.0f && (DRAW || q.top_p < 1.0f || a.kept);
+        if (sums) {
+            sum_all<C>(row, a.V, vectors, rank, scale);
+            sync_all<C>();
+        }
+        if (rank == 0) {
+            uint32_t verdict = kDone;
+            uint64_t weight = uint64_t(1) << kOneBits, unit = weight;
+            int kept = 1, drawn = 0, all = 0;        // all: finite logits, where they are known
+            if (q.bad || odd) {
+                verdict = kBad;
+            } else if (!usable) {
+                verdict = kLongWay;                  // (a row without finite logits too)
+            } else if (q.T != 0.0f) {
+                sum_list(n, scale);
+                kept = n, weight = sm.total;
+                if (whole) all = n;
+                if (sums) {
+                    weight = 0;
+                    for (int c = 0; c < C; ++c) weight += sm.part[c], all += static_cast<int>(sm.count[c]);
+                    kept = all;
+                } else if (!limited && !whole) {
+                    verdict = !DRAW && q.top_k == 0 && q.min_p == 0.0f ? kCopy : kLongWay;       // (the former: nothing cuts it)
+                }
+                if (by_floor || (whole && q.min_p > 0.0f)) {
+                    if (tid == 0) sm.over = 0;
+                    __syncthreads();
+                    uint32_t c = 0;
+                    for (int i = tid; i < n; i += kThreads) c += of_key(static_cast<uint32_t>(sm.list[i] >> 32)) >= floor;
+                    c = __reduce_add_sync(0xffffffffu, c);
+                    if (lane == 0) atomicAdd(&sm.over, c);
+                    __syncthreads();
+                    kept = min(kept, static_cast<int>(sm.over));
+                }
+                if (q.top_k > 0) kept = min(kept, q.top_k);
+                if (!sums && kept < n) weight = sm.before[kept];
+                if (verdict == kDone && q.top_p < 1.0f) {
+                    // tokens while what comes before them weighs less than this
+                    const uint64_t need = times_up(q.top_p, weight);
+                    if (need > sm.total) {
+                        verdict = kLongWay;
+                    } else {
+                        kept = find(sm, n, need - 1) + 1;
+                        weight = kept < n ? sm.before[kept] : sm.total;
+                    }
+                }
+                if (verdict == kDone && DRAW) {
+                    const uint64_t aim = times_down(q.u, weight);
+                    if (aim >= sm.total) {
+                        verdict = kLongWay;
+                    } else {
+                        drawn = find(sm, n, aim);
+                        unit = (drawn + 1 < n ? sm.before[drawn + 1] : sm.total) - sm.before[drawn];
+                    }
+                }
+                if (verdict == kDone && !DRAW && kept > n) verdict = kCopy;
+            }
+            if (tid == 0) {
+                if (verdict == kBad) {
+                    if (a.status) atomicOr(a.status, q.bad ? kStatusBadTemp : kStatusBadRow);
+                    if (DRAW) a.tokens[r] = -1;
+                    if (DRAW && a.logprob) a.logprob[r] = nan;
+                } else if (DRAW && verdict == kDone) {
+                    a.tokens[r] = static_cast<int32_t>(~static_cast<uint32_t>(sm.list[drawn]));
+                    if (a.logprob) a.logprob[r] = log_share(unit, weight);
+                }
+                if (a.kept && verdict != kLongWay) a.kept[r] = verdict == kBad ? 0 : kept;
+            }
+            __syncthreads();
+            if (tid < C) {
+                Head* to = of_rank<C>(&sm, tid);
+                to->verdict = verdict, to->kept = static_cast<uint32_t>(kept);
+            }
+        }
+        sync_all<C>();
+        const uint32_t verdict = sm.verdict;
+        if (verdict == kLongWay) {
+            if (rank == 0) {
+                PassSmem<kThreads, kBins>& ps = smem().passes;
+                __syncthreads();
+                load_tables(ps.tables, tid, kThreads);
+                __syncthreads();
+                row_in_passes<false, DRAW, kThreads, kBins>(a, r, ps);
+                tables = false;
+            }
+        } else if constexpr (!DRAW) {
+            if (verdict == kCopy) {
+                const float* from = reinterpret_cast<const float*>(row);
+                if (from != out)
+                    for (int y = me; y < a.V; y += kAll) out[y] = from[y];
+            } else {
+                // all becomes -infinity (or NaN), and what is kept comes back
+                const float none = verdict == kBad ? nan : -INFINITY;
+                float mine[kOwn];                    // (with their signs, if they are zeros)
+                uint32_t index[kOwn];
+                if (rank == 0)
+#pragma unroll
+                    for (int x = 0; x < kOwn; ++x) {
+                        const uint32_t i = tid + x * kThreads;
+                        index[x] = verdict == kDone && i < sm.kept ? ~static_cast<uint32_t>(sm.list[i]) : 0xffffffffu;
+                        if (index[x] != 0xffffffffu) mine[x] = reinterpret_cast<const float*>(row)[index[x]];
+                    }
+                sync_all<C>();
+                const bool out_vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+                const int wide = out_vec ? a.V / 4 : 0;
+                const uint32_t bits = __float_as_uint(none);
+                const uint64_t drop = drop_policy();
+                for (int y = me; y < wide; y += kAll) st_hint(reinterpret_cast<unsigned char*>(out) + static_cast<int64_t>(y) * 16, make_uint4(bits, bits, bits, bits), drop);
+                for (int y = wide * 4 + me; y < a.V; y += kAll) out[y] = none;
+                sync_all<C>();
+                if (rank == 0)
+#pragma unroll
+                    for (int x = 0; x < kOwn; ++x)
+                        if (index[x] != 0xffffffffu) out[index[x]] = mine[x];
+            }
+        }
+    }
+    sync_all<C>();                                   // no CTA goes while another may still write to it
+}
+
+template <bool DRAW, int C> cudaError_t launch_one(const RowsArgs& a, int slots, cudaStream_t s) {
+    const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(rows_f32_kernel<DRAW, C>), sizeof(Smem));
     if (e != cudaSuccess) return e;
-    const int64_t ctas = a.rows < 2 * nsm ? a.rows : 2 * nsm;
-    rows_f32_kernel<DRAW><<<static_cast<unsigned>(ctas), kThreads, bytes, s>>>(a);
-    return cudaGetLastError();
+    const int64_t rows = a.rows < slots / C ? a.rows : slots / C;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * C));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Smem);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = C > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, rows_f32_kernel<DRAW, C>, a);
+}
+
+template <bool DRAW> cudaError_t launch(const RowsArgs& a, int nsm, cudaStream_t s) {
+    // a row to a cluster, of as many CTAs as the machine has places for
+    const int slots = 2 * nsm;
+    if (a.rows * 8 <= slots) return launch_one<DRAW, 8>(a, slots, s);
+    if (a.rows * 4 <= slots) return launch_one<DRAW, 4>(a, slots, s);
+    if (a.rows * 2 <= slots) return launch_one<DRAW, 2>(a, slots, s);
+    return launch_one<DRAW, 1>(a, slots, s);
 }
 
 }  // namespace

@@ -22,8 +22,10 @@
 namespace sdv {
 namespace rows {
 
+constexpr int kManyLogits = 1 << 16;         // from here on the bound of a head is taken from maxima of more logits
 constexpr int kOneBits = 44;                 // the largest weight is 2^44
 constexpr float kFallMost = 45.5f;           // a fall (in halvings) from which on a weight is 0
+constexpr float kFallLight = 24.0f;          // ... and from which on fp32 gives it
 
 // 2^(i / 128) and 2^(i / 2^14) for i = -64 .. 64, in units of 2^-62.
 constexpr double exp_series(double x) {
@@ -86,11 +88,13 @@ __device__ __forceinline__ float fall_of(const Scale& s, float x, float& low) {
     return p;
 }
 
-// The whole weight of a logit that is at most the largest.
+// The whole weight of a logit that is at most the largest.  Most logits of a row weigh
+// less than 2^20, which fp32 gives to a unit.
 __device__ __forceinline__ uint64_t weight_of(const Scale& s, float x, const Tables& t) {
     float low;
-    const float far = fmaxf(fall_of(s, x, low), 0.0f);
-    const float p = fminf(far, kFallMost);
+    const float p = fmaxf(fall_of(s, x, low), 0.0f);
+    if (p >= kFallLight) return p < kFallMost ? __float2uint_rn(ex2((static_cast<float>(kOneBits) - p) - low)) : 0u;
+    if (x == s.top) return uint64_t(1) << kOneBits;
     const float k = rintf(p), f = k - p;                         // exact; 2^-p = 2^-k 2^f
     const int i = __float2int_rn(f * 128.0f);
     const float g = __fmaf_rn(static_cast<float>(i), -0x1p-7f, f);
@@ -104,9 +108,8 @@ __device__ __forceinline__ uint64_t weight_of(const Scale& s, float x, const Tab
     const int32_t frac = __float2int_rn(y * 0x1p46f) + __float2int_rn(more * 0x1p46f);
     const uint64_t ab = __umul64hi(t.coarse[i + 64], t.fine[j + 64]) << 2;
     const uint64_t w = ab + static_cast<uint64_t>((static_cast<int64_t>(static_cast<uint32_t>(ab >> 31)) * frac) >> 15);   // 2^f in units of 2^-62
-    const int shift = 62 - kOneBits + static_cast<int>(k);       // 18 .. 63
-    const uint64_t rounded = ((w >> (shift - 1)) + 1) >> 1;
-    return x == s.top ? uint64_t(1) << kOneBits : far < kFallMost ? rounded : 0;
+    const int shift = 62 - kOneBits + static_cast<int>(k);       // 18 .. 42
+    return ((w >> (shift - 1)) + 1) >> 1;
 }
 
 // a / b, less than 2^20: off by one at most in fp32.
@@ -115,6 +118,67 @@ __device__ __forceinline__ uint32_t quotient(uint64_t a, uint64_t b) {
     while (q * b > a) --q;
     while ((q + 1) * b <= a) ++q;
     return q;
+}
+
+// The same place in another CTA of the cluster.
+template <int C, class T> __device__ __forceinline__ T* of_rank(T* p, uint32_t rank) {
+    if constexpr (C == 1) return p;
+    T* r;
+    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
+    return r;
+}
+template <int C> __device__ __forceinline__ void sync_all() {
+    if constexpr (C == 1) {
+        __syncthreads();
+    } else {
+        __syncwarp();
+        cluster_sync();
+    }
+}
+
+// The first look at a row keeps it in L2 if it can, the last one and the results do not.
+__device__ __forceinline__ uint64_t keep_policy() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint64_t drop_policy() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint4 ld_hint(const unsigned char* p, uint64_t policy) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p), "l"(policy));
+    return v;
+}
+__device__ __forceinline__ void st_hint(unsigned char* p, const uint4& v, uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "l"(policy) : "memory");
+}
+__device__ __forceinline__ uint4 ld_row(const unsigned char* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// The fourth smallest of N numbers in shared memory, equal ones taken as one (the smallest
+// of 16 differ much).  A whole warp.
+template <int N> __device__ __forceinline__ uint32_t fourth_smallest(const uint32_t* words) {
+    const int lane = threadIdx.x & 31;
+    uint32_t mine[(N + 31) / 32], found = 0;
+#pragma unroll
+    for (int x = 0; x < (N + 31) / 32; ++x) mine[x] = x * 32 + lane < N ? words[x * 32 + lane] : 0xffffffffu;
+#pragma unroll
+    for (int turn = 0; turn < 4; ++turn) {
+        uint32_t m = 0xffffffffu;
+#pragma unroll
+        for (int x = 0; x < (N + 31) / 32; ++x) m = min(m, mine[x]);
+        found = __reduce_min_sync(0xffffffffu, m);
+#pragma unroll
+        for (int x = 0; x < (N + 31) / 32; ++x) mine[x] = mine[x] == found ? 0xffffffffu : mine[x];
+    }
+    return found;
 }
 
 // u * w and p * w for an fp32 number in [0, 1), exact but for the last step: rounded

@@ -40,7 +40,6 @@ static_assert(kPadded >= kSteps, "a lane holds four steps");
 constexpr int kListed = 256;             // tokens of one value that are kept in a list
 constexpr int kHeads = 2048;             // vectors that hold a logit of the head
 constexpr int kHeadK = 256;              // top-k up to which a row is first looked through for its head alone
-constexpr int kManyLogits = 1 << 16;     // from here on the head's bound is the least of 16 maxima of 512, else of 32 of 256
 
 // What a CTA says of its part of a row and of its octaves.
 struct Note {
@@ -74,48 +73,6 @@ static_assert(kCtas * (sizeof(Smem) + 1024) <= 227 * 1024, "two CTAs per SM");
 __device__ __forceinline__ Smem& smem() {
     extern __shared__ __align__(16) unsigned char raw[];
     return *reinterpret_cast<Smem*>(raw);
-}
-
-// The same place in another CTA of the cluster.
-template <int C, class T> __device__ __forceinline__ T* of_rank(T* p, uint32_t rank) {
-    if constexpr (C == 1) return p;
-    T* r;
-    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
-    return r;
-}
-template <int C> __device__ __forceinline__ void sync_all() {
-    if constexpr (C == 1) {
-        __syncthreads();
-    } else {
-        __syncwarp();
-        cluster_sync();
-    }
-}
-
-// The first look at a row keeps it in L2 if it can, the last one and the results do not.
-__device__ __forceinline__ uint64_t keep_policy() {
-    uint64_t p;
-    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-__device__ __forceinline__ uint64_t drop_policy() {
-    uint64_t p;
-    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-__device__ __forceinline__ uint4 ld_hint(const unsigned char* p, uint64_t policy) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p), "l"(policy));
-    return v;
-}
-__device__ __forceinline__ void st_hint(unsigned char* p, const uint4& v, uint64_t policy) {
-    asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "l"(policy) : "memory");
-}
-__device__ __forceinline__ uint4 ld_row(const unsigned char* p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
 }
 
 __device__ __forceinline__ float value_of(uint32_t bits) { return __uint_as_float(bits << 16); }
@@ -196,7 +153,6 @@ template <int C> __device__ __forceinline__ Four four_of(const uint32_t* h, int 
     return f;
 }
 __device__ __forceinline__ void weigh(Four& f, const Scale& scale, const Tables& t) {
-    // (no branch between them: their steps overlap)
 #pragma unroll
     for (int i = 0; i < 4; ++i) f.weight[i] = weight_of(scale, value_of(f.bits[i]), t);
 }
@@ -434,22 +390,7 @@ template <int C, bool COUNT> __device__ __noinline__ uint32_t count_row(const un
         for (int u = 0; u < U; ++u) v[u] = ld_hint(row + static_cast<int64_t>(i + u * kAll) * 16, keep);
     sync_all<C>();
     uint32_t bound = kKeyLow + 1;                    // (a short row is head as a whole)
-    if (vectors > kHeads) {
-        // the fourth smallest: the smallest ones of 16 differ much
-        uint32_t mine[(C * kWarps + 31) / 32];
-#pragma unroll
-        for (int x = 0; x < (C * kWarps + 31) / 32; ++x) mine[x] = x * 32 + lane < C * kWarps ? sm.word[x * 32 + lane] : 0xffffffffu;
-#pragma unroll
-        for (int turn = 0; turn < 4; ++turn) {
-            uint32_t m = 0xffffffffu;
-#pragma unroll
-            for (int x = 0; x < (C * kWarps + 31) / 32; ++x) m = min(m, mine[x]);
-            bound = __reduce_min_sync(0xffffffffu, m);
-#pragma unroll
-            for (int x = 0; x < (C * kWarps + 31) / 32; ++x) mine[x] = mine[x] == bound ? 0xffffffffu : mine[x];
-        }
-        bound = min(bound, kKeyHigh);
-    }
+    if (vectors > kHeads) bound = min(fourth_smallest<C * kWarps>(sm.word), kKeyHigh);
     const float f = of_key(bound);
     const __nv_bfloat162 above = __floats2bfloat162_rn(f, f);
     uint32_t most2 = 0xff80ff80u;                    // of both halves; a NaN stays
