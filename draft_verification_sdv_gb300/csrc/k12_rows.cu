@@ -7,7 +7,10 @@
 // and the draw are places of running sums.  Where only top-p or the draw limits the
 // row, a second look adds up all weights (whole numbers: the sum is the one that
 // any other order gives), and the head's share of them tells whether the place lies in
-// it.  Other rows go the long way, in passes over histograms (row_in_passes).
+// it.  Other rows are counted and weighed into bins of equal width in (max - x) / T,
+// which keep the order, and the bin that holds a place is listed and sorted in turn
+// (row_by_bins); rows with too many logits in one bin go the long way, in passes over
+// histograms of keys (row_in_passes).
 //
 // A row is shared by a cluster of C CTAs where there are few; the first one has the list.
 // What bounds it: for the first look the row's bytes, for the second the
@@ -37,8 +40,14 @@ struct Head {
     // what the first CTA has found
     uint32_t verdict, kept;
 };
+struct Bins {
+    Head head;
+    Hist<kBins> hist;
+    Picked<kThreads> picked;
+};
 union Smem {
     Head head;
+    Bins bins;
     PassSmem<kThreads, kBins> passes;
 };
 static_assert(2 * (sizeof(Smem) + 1024) <= 227 * 1024, "two CTAs per SM");
@@ -55,25 +64,23 @@ __device__ __forceinline__ float largest_of(const uint4& v) {
 
 // Writes the logits of this CTA's part of a row that reach the bound into the first CTA's
 // list; whether there is a NaN or +infinity into `odd`.  Returns the bound, a key.
-template <int C> __device__ __noinline__ uint32_t list_head(const unsigned char* row, int V, int vectors, int rank) {
+template <int C> __device__ __noinline__ uint32_t list_head(const unsigned char* row, int V, const Span span, int rank) {
     constexpr int U = 4, kAll = C * kThreads, kSamples = C * kWarps * 2;
     Head& sm = smem().head;
     Head* const lead = of_rank<C>(&sm, 0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = rank * kThreads + threadIdx.x;
     const uint64_t keep = keep_policy();
+    const unsigned char* first = row + span.head * 4;
     uint32_t bound = kKeyLow + 1;                    // (a short row is head as a whole)
     if (V > kList) {
-        const int chunks = (V / 4 + 31) / 32;        // (as if it were aligned)
+        const int chunks = (span.vectors + 31) / 32;
         uint32_t least = 0xffffffffu, most = 0;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int n = (rank * kWarps + warp) * 2 + u;
             const int at = (chunks >= kSamples ? static_cast<int>(static_cast<uint32_t>(n) * chunks / kSamples) : n) * 32 + lane;
             float x = -INFINITY;
-            if (at < vectors)
-                x = largest_of(ld_hint(row + static_cast<int64_t>(at) * 16, keep));
-            else if (at < V / 4)
-                for (int y = 0; y < 4; ++y) x = fmaxf(x, reinterpret_cast<const float*>(row)[at * 4 + y]);
+            if (at < span.vectors) x = largest_of(ld_hint(first + static_cast<int64_t>(at) * 16, keep));
             const uint32_t top = __reduce_max_sync(0xffffffffu, x > -INFINITY ? key_of(x) : 0u);
             if (top) least = min(least, top);
             most = max(most, top);
@@ -95,18 +102,19 @@ template <int C> __device__ __noinline__ uint32_t list_head(const unsigned char*
         const float top = fmaxf(fmaxf(x, y), fmaxf(z, w));
         most = fmaxf(most, top);
         odd |= !((x + y) + (z + w) < INFINITY) && (x != x || y != y || z != z || w != w);
-        if (top >= f) put(x, index * 4), put(y, index * 4 + 1), put(z, index * 4 + 2), put(w, index * 4 + 3);
+        if (top >= f) put(x, index), put(y, index + 1), put(z, index + 2), put(w, index + 3);
     };
     int i = me;
-    for (; i + (U - 1) * kAll < vectors; i += U * kAll) {
+    for (; i + (U - 1) * kAll < span.vectors; i += U * kAll) {
         uint4 v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = ld_hint(row + static_cast<int64_t>(i + u * kAll) * 16, keep);
+        for (int u = 0; u < U; ++u) v[u] = ld_hint(first + static_cast<int64_t>(i + u * kAll) * 16, keep);
 #pragma unroll
-        for (int u = 0; u < U; ++u) take(v[u], i + u * kAll);
+        for (int u = 0; u < U; ++u) take(v[u], span.index_of(i + u * kAll));
     }
-    for (; i < vectors; i += kAll) take(ld_hint(row + static_cast<int64_t>(i) * 16, keep), i);
-    for (int y = vectors * 4 + me; y < V; y += kAll) {
+    for (; i < span.vectors; i += kAll) take(ld_hint(first + static_cast<int64_t>(i) * 16, keep), span.index_of(i));
+    if (me < span.loose) {                           // (six at most)
+        const int y = span.loose_at(me);
         const float x = reinterpret_cast<const float*>(row)[y];
         odd |= x != x;
         most = fmaxf(most, x);
@@ -118,7 +126,7 @@ template <int C> __device__ __noinline__ uint32_t list_head(const unsigned char*
 }
 
 // Weights and number of the finite logits of this CTA's part, told to every CTA.
-template <int C> __device__ __noinline__ void sum_all(const unsigned char* row, int V, int vectors, int rank, const Scale scale) {
+template <int C> __device__ __noinline__ void sum_all(const unsigned char* row, const Span span, int rank, const Scale scale) {
     constexpr int U = 2, kAll = C * kThreads;
     Head& sm = smem().head;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = rank * kThreads + threadIdx.x;
@@ -131,16 +139,17 @@ template <int C> __device__ __noinline__ void sum_all(const unsigned char* row, 
     auto take = [&](const uint4& v) {
         add(__uint_as_float(v.x)), add(__uint_as_float(v.y)), add(__uint_as_float(v.z)), add(__uint_as_float(v.w));
     };
+    const unsigned char* first = row + span.head * 4;
     int i = me;
-    for (; i + (U - 1) * kAll < vectors; i += U * kAll) {
+    for (; i + (U - 1) * kAll < span.vectors; i += U * kAll) {
         uint4 v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = ld_row(row + static_cast<int64_t>(i + u * kAll) * 16);
+        for (int u = 0; u < U; ++u) v[u] = ld_row(first + static_cast<int64_t>(i + u * kAll) * 16);
 #pragma unroll
         for (int u = 0; u < U; ++u) take(v[u]);
     }
-    for (; i < vectors; i += kAll) take(ld_row(row + static_cast<int64_t>(i) * 16));
-    for (int y = vectors * 4 + me; y < V; y += kAll) add(reinterpret_cast<const float*>(row)[y]);
+    for (; i < span.vectors; i += kAll) take(ld_row(first + static_cast<int64_t>(i) * 16));
+    if (me < span.loose) add(reinterpret_cast<const float*>(row)[span.loose_at(me)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     n = __reduce_add_sync(0xffffffffu, n);
@@ -156,11 +165,39 @@ template <int C> __device__ __noinline__ void sum_all(const unsigned char* row, 
     }
 }
 
-// The list's first `n` entries in falling order (n at most a power of two `size`, the rest 0).
+// The list's first `size` entries in falling order (a power of two, 64 at least).  Merges of
+// alternating runs; each warp holds 64 entries in registers, two to a lane (i and
+// i + 32), so that only exchanges over 64 entries and more go through shared memory.
 __device__ __noinline__ void sort_list(int size) {
     Head& sm = smem().head;
-    for (int k = 2; k <= size; k <<= 1)
-        for (int j = k >> 1; j > 0; j >>= 1) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto within = [&](int base, int k, int top) {    // the steps top, top / 2, ... 1 of merges to runs of k
+        uint64_t a = sm.list[base + lane], b = sm.list[base + 32 + lane];
+        if (top == 32) {
+            if ((a < b) == (((base + lane) & k) == 0)) {
+                const uint64_t x = a;
+                a = b, b = x;
+            }
+            top = 16;
+        }
+        for (int j = top; j > 0; j >>= 1) {
+            const uint64_t x = __shfl_xor_sync(0xffffffffu, a, j), y = __shfl_xor_sync(0xffffffffu, b, j);
+            const bool first = (lane & j) == 0;
+            // (a falling run keeps the larger one first)
+            const bool fa = ((base + lane) & k) == 0, fb = ((base + 32 + lane) & k) == 0;
+            a = (a > x) == (first == fa) ? a : x;
+            b = (b > y) == (first == fb) ? b : y;
+        }
+        sm.list[base + lane] = a, sm.list[base + 32 + lane] = b;
+    };
+    __syncthreads();
+    for (int base = warp * 64; base < size; base += kWarps * 64)
+        for (int k = 2; k <= 64; k <<= 1) {
+            within(base, k, k >> 1);
+            __syncwarp();
+        }
+    for (int k = 128; k <= size; k <<= 1) {
+        for (int j = k >> 1; j >= 64; j >>= 1) {
             __syncthreads();
             for (int x = threadIdx.x; x < size / 2; x += kThreads) {
                 const int lo = 2 * x - (x & (j - 1)), hi = lo + j;   // pairs j apart
@@ -168,6 +205,9 @@ __device__ __noinline__ void sort_list(int size) {
                 if ((a < b) == ((lo & k) == 0)) sm.list[lo] = b, sm.list[hi] = a;
             }
         }
+        __syncthreads();
+        for (int base = warp * 64; base < size; base += kWarps * 64) within(base, k, 32);
+    }
     __syncthreads();
 }
 
@@ -213,6 +253,111 @@ __device__ __forceinline__ int find(Head& sm, int n, uint64_t target) {
     return at;
 }
 
+// A row whose places do not lie in its head; the largest logit and the factors are known.
+// The first CTA; false: a bin does not fit the list, and nothing is written.
+template <bool DRAW> __device__ __noinline__ bool row_by_bins(const RowsArgs& a, int r, const Ask q, const Scale scale, float floor) {
+    constexpr int U = 2;
+    Bins& sm = smem().bins;
+    Head& head = sm.head;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const unsigned char* row = static_cast<const unsigned char*>(a.logits) + r * a.in_stride;
+    const float* cells = reinterpret_cast<const float*>(row);
+    const Span span = span_of(row, a.V, 4);
+    const float wide = (kBins / 64) * 0.5f * scale.hi;           // bins per unit of logit
+    auto bin_of = [&](float x) { return static_cast<int>(fminf((scale.top - x) * wide, static_cast<float>(kBins - 1))); };
+    auto each = [&](auto work) {                     // (x, index)
+        const unsigned char* first = row + span.head * 4;
+        auto four = [&](const uint4& v, int at) {
+            work(__uint_as_float(v.x), at), work(__uint_as_float(v.y), at + 1);
+            work(__uint_as_float(v.z), at + 2), work(__uint_as_float(v.w), at + 3);
+        };
+        int i = tid;
+        for (; i + (U - 1) * kThreads < span.vectors; i += U * kThreads) {
+            uint4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = ld_row(first + static_cast<int64_t>(i + u * kThreads) * 16);
+#pragma unroll
+            for (int u = 0; u < U; ++u) four(v[u], span.index_of(i + u * kThreads));
+        }
+        for (; i < span.vectors; i += kThreads) four(ld_row(first + static_cast<int64_t>(i) * 16), span.index_of(i));
+        if (tid < span.loose) work(cells[span.loose_at(tid)], span.loose_at(tid));
+    };
+    for (int x = tid; x < kBins; x += kThreads) sm.hist.count[x] = 0, sm.hist.mass[x] = 0;
+    if (tid == 0) head.over = 0;
+    __syncthreads();
+    uint64_t weight = 0;
+    uint32_t finite = 0, over = 0;
+    each([&](float x, int) {
+        if (!(x > -INFINITY)) return;
+        const uint64_t w = weight_of(scale, x, head.tables);
+        const int b = bin_of(x);
+        atomicAdd(&sm.hist.count[b], 1u);
+        add_weight(&sm.hist.mass[b], w);
+        weight += w;
+        ++finite;
+        over += x >= floor;
+    });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) weight += __shfl_xor_sync(0xffffffffu, weight, o);
+    finite = __reduce_add_sync(0xffffffffu, finite);
+    over = __reduce_add_sync(0xffffffffu, over);
+    if (lane == 0) head.sum[warp] = weight, head.word[warp] = finite, atomicAdd(&head.over, over);
+    __syncthreads();
+    weight = 0, finite = 0;
+    for (int w = 0; w < kWarps; ++w) weight += head.sum[w], finite += head.word[w];
+    __syncthreads();
+    uint32_t kept = finite, most = min(finite, head.over);
+    if (q.top_k > 0) most = min(most, static_cast<uint32_t>(q.top_k));
+    // the last of the first `most`; the last before which less than top_p of their weight
+    // lies; the one that is drawn
+    uint64_t last = 0, unit = 0;                     // (an entry, as the list has them: what is not less is kept)
+    int listed = -1;
+#pragma unroll 1
+    for (int ask = 0; ask < 3; ++ask) {
+        if (ask == 0 ? most >= finite : ask == 1 ? !(q.top_p < 1.0f) : !DRAW) continue;
+        const uint64_t target = ask == 0 ? most - 1 : ask == 1 ? times_up(q.top_p, weight) - 1 : times_down(q.u, weight);
+        pick<kThreads, kBins>(sm.picked, sm.hist, ask != 0, target);
+        const int bin = sm.picked.bin, n = static_cast<int>(sm.picked.at_n);
+        if (n > kList) return false;
+        if (bin != listed) {
+            listed = bin;
+            if (tid == 0) head.listed = 0;
+            int size = 64;
+            while (size < n) size <<= 1;
+            for (int x = n + tid; x < size; x += kThreads) head.list[x] = 0;
+            __syncthreads();
+            each([&](float x, int index) {
+                if (x > -INFINITY && bin_of(x) == bin)
+                    head.list[atomicAdd(&head.listed, 1u)] = static_cast<uint64_t>(key_of(x)) << 32 | static_cast<uint32_t>(~index);
+            });
+            sort_list(size);
+            sum_list(n, scale);
+        }
+        const int at = ask == 0 ? static_cast<int>(target) - static_cast<int>(sm.picked.before_n) : find(head, n, target - sm.picked.before_w);
+        const uint64_t end = sm.picked.before_w + (at + 1 < n ? head.before[at + 1] : head.total);
+        if (ask < 2) {
+            kept = sm.picked.before_n + at + 1;
+            weight = end;
+            last = head.list[at];
+        } else {
+            unit = end - sm.picked.before_w - head.before[at];
+            if (tid == 0) {
+                a.tokens[r] = static_cast<int32_t>(~static_cast<uint32_t>(head.list[at]));
+                if (a.logprob) a.logprob[r] = log_share(unit, weight);
+            }
+        }
+        __syncthreads();
+    }
+    if (tid == 0 && a.kept) a.kept[r] = static_cast<int32_t>(kept);
+    if constexpr (!DRAW) {
+        float* out = reinterpret_cast<float*>(static_cast<unsigned char*>(a.out) + r * a.out_stride);
+        each([&](float x, int index) {
+            out[index] = (static_cast<uint64_t>(key_of(x)) << 32 | static_cast<uint32_t>(~index)) >= last ? x : -INFINITY;
+        });
+    }
+    return true;
+}
+
 template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_f32_kernel(const RowsArgs a) {
     Head& sm = smem().head;
     const int tid = threadIdx.x, lane = tid & 31;
@@ -225,14 +370,14 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
         const Ask q = ask_of(a, r);
         const unsigned char* row = static_cast<const unsigned char*>(a.logits) + r * a.in_stride;
         float* out = reinterpret_cast<float*>(static_cast<unsigned char*>(a.out) + r * a.out_stride);
-        const int vectors = (reinterpret_cast<uintptr_t>(row) & 15) == 0 ? a.V / 4 : 0;
+        const Span span = span_of(row, a.V, 4);
         sync_all<C>();                               // (the row before is done with shared memory)
         if (!tables) load_tables(sm.tables, tid, kThreads);
         tables = true;
         if (tid == 0) sm.listed = sm.odd = 0;
         if (tid == kThreads - 1) sm.factors = factors_of(q.T, q.min_p);
         sync_all<C>();
-        const uint32_t bound = list_head<C>(row, a.V, vectors, rank);
+        const uint32_t bound = list_head<C>(row, a.V, span, rank);
         __syncthreads();
         if (tid < C) of_rank<C>(&sm, tid)->strange[rank] = sm.odd;
         sync_all<C>();
@@ -243,7 +388,7 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
         // ---- the head, sorted ----
         const int n = static_cast<int>(min(listed, static_cast<uint32_t>(kList)));
         const bool usable = !q.bad && !odd && listed > 0 && listed <= kList;
-        int size = 32;
+        int size = 64;
         while (size < n) size <<= 1;
         if (rank == 0 && usable) {
             for (int i = n + tid; i < size; i += kThreads) sm.list[i] = 0;
@@ -261,7 +406,7 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
         const bool whole = bound == kKeyLow + 1;     // the list holds every finite logit
         const bool sums = usable && !limited && !whole && q.top_k == 0 && q.min_p == 0.0f && (DRAW || q.top_p < 1.0f || a.kept);
         if (sums) {
-            sum_all<C>(row, a.V, vectors, rank, scale);
+            sum_all<C>(row, span, rank, scale);
             sync_all<C>();
         }
         if (rank == 0) {
@@ -336,7 +481,7 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
         sync_all<C>();
         const uint32_t verdict = sm.verdict;
         if (verdict == kLongWay) {
-            if (rank == 0) {
+            if (rank == 0 && !(usable && row_by_bins<DRAW>(a, static_cast<int>(r), q, scale, floor))) {
                 PassSmem<kThreads, kBins>& ps = smem().passes;
                 __syncthreads();
                 load_tables(ps.tables, tid, kThreads);
@@ -362,12 +507,12 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
                         if (index[x] != 0xffffffffu) mine[x] = reinterpret_cast<const float*>(row)[index[x]];
                     }
                 sync_all<C>();
-                const bool out_vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-                const int wide = out_vec ? a.V / 4 : 0;
+                const Span to = span_of(reinterpret_cast<const unsigned char*>(out), a.V, 4);
                 const uint32_t bits = __float_as_uint(none);
                 const uint64_t drop = drop_policy();
-                for (int y = me; y < wide; y += kAll) st_hint(reinterpret_cast<unsigned char*>(out) + static_cast<int64_t>(y) * 16, make_uint4(bits, bits, bits, bits), drop);
-                for (int y = wide * 4 + me; y < a.V; y += kAll) out[y] = none;
+                for (int y = me; y < to.vectors; y += kAll)
+                    st_hint(reinterpret_cast<unsigned char*>(out + to.index_of(y)), make_uint4(bits, bits, bits, bits), drop);
+                if (me < to.loose) out[to.loose_at(me)] = none;
                 sync_all<C>();
                 if (rank == 0)
 #pragma unroll

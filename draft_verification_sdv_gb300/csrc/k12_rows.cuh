@@ -224,17 +224,29 @@ template <int BINS> struct Hist {
     uint32_t count[BINS];
 };
 
-template <int THREADS, int BINS> struct PassSmem {
-    Tables tables;
-    Hist<BINS> first, next;
+// A weight into a shared sum, in 32-bit steps: 64-bit ones go round a loop.
+__device__ __forceinline__ void add_weight(uint64_t* sum, uint64_t w) {
+    uint32_t* at = reinterpret_cast<uint32_t*>(sum);
+    const uint32_t lo = static_cast<uint32_t>(w);
+    uint32_t hi = static_cast<uint32_t>(w >> 32);
+    if (lo && atomicAdd(at, lo) > ~lo) ++hi;         // (it ran over)
+    if (hi) atomicAdd(at + 1, hi);
+}
+
+// What `pick` finds, and its room.
+template <int THREADS> struct Picked {
     uint64_t sum[2][THREADS / 32];
-    uint32_t word[THREADS / 32];
-    Factors factors;
-    float floor;
-    // what `locate` has found
     uint64_t before_w, at_w;
     uint32_t before_n, at_n;
     int bin;
+};
+
+template <int THREADS, int BINS> struct PassSmem : Picked<THREADS> {
+    Tables tables;
+    Hist<BINS> first, next;
+    uint32_t word[THREADS / 32];
+    Factors factors;
+    float floor;
 };
 
 // Where in the order a place lies: the logit there, and what comes before it.
@@ -243,6 +255,23 @@ struct Place {
     uint32_t before_n, at_n;         // tokens of larger logits, and of this one
     uint64_t before_w;               // weight of the former
 };
+
+// A row in 16-byte vectors: the logits before the first that lies on 16 bytes, the
+// vectors, and those after the last.  Loose ones are counted through: first the former.
+struct Span {
+    int head, vectors, loose, width;
+    __device__ __forceinline__ int index_of(int v) const { return head + v * width; }
+    __device__ __forceinline__ int loose_at(int i) const { return i < head ? i : i + vectors * width; }
+};
+__device__ __forceinline__ Span span_of(const unsigned char* row, int V, int bytes) {
+    Span s;
+    s.width = 16 / bytes;
+    s.head = static_cast<int>((0u - static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row))) & 15u) / bytes;
+    s.head = s.head < V ? s.head : V;
+    s.vectors = (V - s.head) / s.width;
+    s.loose = V - s.vectors * s.width;
+    return s;
+}
 
 template <bool BF16> constexpr int kStep = BF16 ? 8 : 4;         // logits of 16 bytes
 
@@ -303,7 +332,7 @@ template <int THREADS> __device__ __forceinline__ uint32_t block_sum(uint32_t x,
 // The bin of a histogram where the running count (or weight) passes `target`:
 // into sm.bin and what comes before it and lies in it.
 template <int THREADS, int BINS>
-__device__ __forceinline__ void pick(PassSmem<THREADS, BINS>& sm, const Hist<BINS>& h, bool by_weight, uint64_t target) {
+__device__ __forceinline__ void pick(Picked<THREADS>& sm, const Hist<BINS>& h, bool by_weight, uint64_t target) {
     constexpr int kPerThread = BINS / THREADS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t n = 0, w = 0;
@@ -358,7 +387,7 @@ template <bool BF16, int THREADS, int BINS> struct Row {
     // The place where the running count (weight) of the order passes `target`
     // (which lies below its total).
     __device__ Place locate(PassSmem<THREADS, BINS>& sm, bool by_weight, uint64_t target) const {
-        pick(sm, sm.first, by_weight, target);
+        pick<THREADS, BINS>(sm, sm.first, by_weight, target);
         Place p{0, sm.before_n, sm.at_n, sm.before_w};
         const int bin = sm.bin;
         // keys of the bin: the order of bins is that of keys, turned round
@@ -389,11 +418,10 @@ template <bool BF16, int THREADS, int BINS> struct Row {
                 const uint32_t k = key_of(x);
                 if (k < lo || k > hi) return;
                 atomicAdd(&sm.next.count[(hi - k) >> shift], 1u);
-                atomicAdd(reinterpret_cast<unsigned long long*>(&sm.next.mass[(hi - k) >> shift]),
-                          static_cast<unsigned long long>(weight_of(scale, x, sm.tables)));
+                add_weight(&sm.next.mass[(hi - k) >> shift], weight_of(scale, x, sm.tables));
             });
             __syncthreads();
-            pick(sm, sm.next, by_weight, target - (by_weight ? p.before_w : p.before_n));
+            pick<THREADS, BINS>(sm, sm.next, by_weight, target - (by_weight ? p.before_w : p.before_n));
             p.before_n += sm.before_n, p.before_w += sm.before_w, p.at_n = sm.at_n;
             const uint32_t top = hi - (static_cast<uint32_t>(sm.bin) << shift), span = (1u << shift) - 1;
             lo = top - lo > span ? top - span : lo;
@@ -498,7 +526,7 @@ __device__ __noinline__ void row_in_passes(const RowsArgs& a, int64_t r, PassSme
             const uint64_t w = weight_of(row.scale, x, sm.tables);
             const int b = row.bin_of(x);
             atomicAdd(&sm.first.count[b], 1u);
-            atomicAdd(reinterpret_cast<unsigned long long*>(&sm.first.mass[b]), static_cast<unsigned long long>(w));
+            add_weight(&sm.first.mass[b], w);
             over += x >= floor;
             sum += w;
         });

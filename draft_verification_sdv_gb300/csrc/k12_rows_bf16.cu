@@ -356,7 +356,9 @@ __device__ __noinline__ void settle(const RowsArgs& a, int r, const Ask q, const
 // that some hundred logits of the row reach; vectors with such a one, the head, are
 // written down; without COUNT only those are counted.  Returns the bound, a key.  (A function of its own, as the other steps
 // are: a row's other numbers would take the registers of its loads.)
-template <int C, bool COUNT> __device__ __noinline__ uint32_t count_row(const unsigned char* row, int V, int vectors, int rank) {
+template <int C, bool COUNT> __device__ __noinline__ uint32_t count_row(const unsigned char* cells, int V, const Span span, int rank) {
+    const unsigned char* row = cells + span.head * 2;            // the first vector
+    const int vectors = span.vectors;
     constexpr int U = 4, kAll = C * kThreads, kSamples = C * kWarps * 2;
     Smem& sm = smem();
     const uint32_t counts = smem_u32(sm.count);
@@ -425,9 +427,8 @@ template <int C, bool COUNT> __device__ __noinline__ uint32_t count_row(const un
                 const uint4 w = ld_hint(row + static_cast<int64_t>(sm.head[x]) * 16, keep);
                 count_above(sm.count, w.x, f), count_above(sm.count, w.y, f), count_above(sm.count, w.z, f), count_above(sm.count, w.w, f);
             }
-        const unsigned short* cells = reinterpret_cast<const unsigned short*>(row);
-        for (int y = vectors * 8 + rank * kThreads + threadIdx.x; y < V; y += kAll) {
-            const uint32_t x = cells[y];
+        if (rank * kThreads + static_cast<int>(threadIdx.x) < span.loose) {
+            const uint32_t x = reinterpret_cast<const unsigned short*>(cells)[span.loose_at(rank * kThreads + threadIdx.x)];
             if (value_of(x) >= f) count_one(sm.count, x);
             if (!(value_of(x) < INFINITY)) atomicOr(&sm.odd, kOddNan);
         }
@@ -438,27 +439,33 @@ template <int C, bool COUNT> __device__ __noinline__ uint32_t count_row(const un
 // The index of the token of one value that stands at `place` among them, into sm.found of
 // every CTA of the cluster.
 template <int C>
-__device__ __noinline__ void find_by_index(const unsigned short* cells, int V, int vectors, int rank, uint32_t pair, uint32_t sign, uint32_t place) {
+__device__ __noinline__ void find_by_index(const unsigned short* cells, int V, const Span span, int rank, uint32_t pair, uint32_t sign, uint32_t place) {
     constexpr int U = 4;
     Smem& sm = smem();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t other = ~pair << 16;
     // by runs of the row, a warp to each: counted, then the one that holds it
     constexpr int kRuns = C * kWarps;
-    const int steps = (V + 255) / 256, run = (steps + kRuns - 1) / kRuns, mine = rank * kWarps + warp;
+    // eights of the row: whole vectors, but for the first (where a vector does not begin the
+    // row) and the last
+    const int shift = (8 - span.head) & 7;
+    auto eight_at = [&](int e) { return e * 8 - shift; };
+    auto is_vector = [&](int e) { const int v = e - (shift ? 1 : 0); return v >= 0 && v < span.vectors; };
+    const int steps = (V + shift + 255) / 256, run = (steps + kRuns - 1) / kRuns, mine = rank * kWarps + warp;
     const int s0 = min(mine * run, steps), s1 = min(s0 + run, steps);
     auto load = [&](int s, uint4 (&v)[U]) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if ((s + u) * 32 + lane < vectors) v[u] = ld_row(reinterpret_cast<const unsigned char*>(cells) + static_cast<int64_t>((s + u) * 32 + lane) * 16);
+            if (is_vector((s + u) * 32 + lane)) v[u] = ld_row(reinterpret_cast<const unsigned char*>(cells + eight_at((s + u) * 32 + lane)));
     };
     auto matches = [&](int s, const uint4& v) {          // among the lane's eight logits of step s, as bits
-        const int at = (s * 32 + lane) * 8;
+        const int at = eight_at(s * 32 + lane);
         if (s >= s1 || at >= V) return 0u;
-        if (s * 32 + lane < vectors)
+        if (is_vector(s * 32 + lane))
             return halves_of(v.x, pair, sign) | halves_of(v.y, pair, sign) << 2 | halves_of(v.z, pair, sign) << 4 | halves_of(v.w, pair, sign) << 6;
         uint32_t m = 0;
-        for (int y = 0; y < 8 && at + y < V; ++y) m |= (halves_of(cells[at + y] | other, pair, sign) & 1u) << y;
+        for (int y = 0; y < 8; ++y)
+            if (at + y >= 0 && at + y < V) m |= (halves_of(cells[at + y] | other, pair, sign) & 1u) << y;
         return m;
     };
     uint32_t n = 0;
@@ -493,7 +500,7 @@ __device__ __noinline__ void find_by_index(const unsigned short* cells, int V, i
                     const uint32_t first = before + upto - own;
                     if (first <= place && place < first + own)
                         for (int c = 0; c < C; ++c)
-                            of_rank<C>(&sm, c)->found = ((s + u) * 32 + lane) * 8 + __fns(m, 0, static_cast<int>(place - first) + 1);
+                            of_rank<C>(&sm, c)->found = eight_at((s + u) * 32 + lane) + __fns(m, 0, static_cast<int>(place - first) + 1);
                 }
                 before += here;
             }
@@ -519,8 +526,11 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
         const Ask q = ask_of(a, r);
         const unsigned char* row = static_cast<const unsigned char*>(a.logits) + r * a.in_stride;
         unsigned char* out = static_cast<unsigned char*>(a.out) + r * a.out_stride;
-        const bool vec = (reinterpret_cast<uintptr_t>(row) & 15) == 0, out_vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-        const int vectors = vec ? a.V / 8 : 0;
+        const Span span = span_of(row, a.V, 2);
+        const int vectors = span.vectors;
+        const unsigned char* first = row + span.head * 2;        // vector
+        unsigned char* out_first = out + span.head * 2;
+        const bool out_vec = (reinterpret_cast<uintptr_t>(out_first) & 15) == 0;
         const unsigned short* cells = reinterpret_cast<const unsigned short*>(row);
         sync_all<C>();                               // (the row before is done with shared memory)
         if (tid == kThreads - 1) sm.factors = factors_of(q.T, q.min_p);
@@ -536,9 +546,8 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
 #pragma unroll 1
         for (;; whole = true) {
             uint32_t bound = kKeyHigh;
-            if (vectors > 0) bound = whole ? count_row<C, true>(row, a.V, vectors, rank) : count_row<C, false>(row, a.V, vectors, rank);
-            if (whole)
-                for (int y = vectors * 8 + me; y < a.V; y += kAll) count_one(sm.count, cells[y]);
+            if (vectors > 0) bound = whole ? count_row<C, true>(row, a.V, span, rank) : count_row<C, false>(row, a.V, span, rank);
+            if (whole && me < span.loose) count_one(sm.count, cells[span.loose_at(me)]);
             sync_all<C>();
 
             // ---- which octaves hold something, how much in all, the largest ----
@@ -600,11 +609,11 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
         Rest rest{0, 0, 0};
         if (whole && all.total != static_cast<uint32_t>(a.V)) {  // some logits are not in the octaves: which
             for (int x = me; x < vectors; x += kAll) {
-                const uint4 v = ld_row(row + static_cast<int64_t>(x) * 16);
+                const uint4 v = ld_row(first + static_cast<int64_t>(x) * 16);
                 look_at(rest, v.x & 0xffffu), look_at(rest, v.x >> 16), look_at(rest, v.y & 0xffffu), look_at(rest, v.y >> 16);
                 look_at(rest, v.z & 0xffffu), look_at(rest, v.z >> 16), look_at(rest, v.w & 0xffffu), look_at(rest, v.w >> 16);
             }
-            for (int y = vectors * 8 + me; y < a.V; y += kAll) look_at(rest, cells[y]);
+            if (me < span.loose) look_at(rest, cells[span.loose_at(me)]);
             rest.zeros = __reduce_add_sync(0xffffffffu, rest.zeros);
             rest.odd = __reduce_or_sync(0xffffffffu, rest.odd);
             if (lane == 0) sm.word[warp] = rest.zeros, sm.word[kWarps + warp] = rest.odd;
@@ -644,7 +653,7 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
                     float x[8];
 #pragma unroll
                     for (int y = 0; y < 8; ++y) x[y] = nan;
-                    for (int i0 = me * 8; i0 < a.V; i0 += kAll * 8) store_step<true>(out, i0, a.V, out_vec, x);
+                    for (int i0 = me * 8; i0 < a.V; i0 += kAll * 8) store_step<true>(out, i0, a.V, (reinterpret_cast<uintptr_t>(out) & 15) == 0, x);
                 }
             }
             for (int x = tid; x < kWords / 4; x += kThreads) reinterpret_cast<uint4*>(sm.count)[x] = make_uint4(0, 0, 0, 0);
@@ -685,28 +694,27 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     const uint32_t m = halves_of(w[y], pair, sign);
-                    if (m & 1) put(v0 * 8 + 2 * y);
-                    if (m & 2) put(v0 * 8 + 2 * y + 1);
+                    if (m & 1) put(span.index_of(v0) + 2 * y);
+                    if (m & 2) put(span.index_of(v0) + 2 * y + 1);
                 }
             };
             if (by_head)
-                for (uint32_t x = tid; x < heads; x += kThreads) look_for(ld_row(row + static_cast<int64_t>(sm.head[x]) * 16), sm.head[x]);
+                for (uint32_t x = tid; x < heads; x += kThreads) look_for(ld_row(first + static_cast<int64_t>(sm.head[x]) * 16), sm.head[x]);
             int v0 = by_head ? vectors : me;
             for (; v0 + (U - 1) * kAll < vectors; v0 += U * kAll) {
                 uint4 v[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) v[u] = ld_row(row + static_cast<int64_t>(v0 + u * kAll) * 16);
+                for (int u = 0; u < U; ++u) v[u] = ld_row(first + static_cast<int64_t>(v0 + u * kAll) * 16);
 #pragma unroll
                 for (int u = 0; u < U; ++u) look_for(v[u], v0 + u * kAll);
                 if (C == 1 && *reinterpret_cast<volatile uint32_t*>(&sm.listed) >= at_n) break;      // that was all of them
             }
-            for (; v0 < vectors; v0 += kAll) look_for(ld_row(row + static_cast<int64_t>(v0) * 16), v0);
-            for (int y = vectors * 8 + me; y < a.V; y += kAll)
-                if (halves_of(cells[y] | other, pair, sign) & 1) put(y);
+            for (; v0 < vectors; v0 += kAll) look_for(ld_row(first + static_cast<int64_t>(v0) * 16), v0);
+            if (me < span.loose && (halves_of(cells[span.loose_at(me)] | other, pair, sign) & 1)) put(span.loose_at(me));
         }
         uint32_t last = 0;                                           // index of the token of that place (a truncation: the first that goes)
         if (by_index) {
-            find_by_index<C>(cells, a.V, vectors, rank, pair, sign, place);
+            find_by_index<C>(cells, a.V, span, rank, pair, sign, place);
             last = sm.found;
             if (DRAW && me == 0) a.tokens[r] = static_cast<int32_t>(last);
         }
@@ -731,8 +739,8 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
                 return (w & stay) | (~stay & 0xff80ff80u);
             };
             auto write = [&](const uint4& v, int v0) {
-                st_hint(out + static_cast<int64_t>(v0) * 16,
-                        make_uint4(cut(v.x, v0 * 8), cut(v.y, v0 * 8 + 2), cut(v.z, v0 * 8 + 4), cut(v.w, v0 * 8 + 6)), drop);
+                st_hint(out_first + static_cast<int64_t>(v0) * 16,
+                        make_uint4(cut(v.x, span.index_of(v0)), cut(v.y, span.index_of(v0) + 2), cut(v.z, span.index_of(v0) + 4), cut(v.w, span.index_of(v0) + 6)), drop);
             };
             if (by_head) {
                 // the head is taken up, all becomes -infinity, and what the head keeps comes back
@@ -740,41 +748,45 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
                 uint4 v[kOwn];
 #pragma unroll
                 for (int x = 0; x < kOwn; ++x)
-                    if (tid + x * kThreads < heads) v[x] = ld_row(row + static_cast<int64_t>(sm.head[tid + x * kThreads]) * 16);
+                    if (tid + x * kThreads < heads) v[x] = ld_row(first + static_cast<int64_t>(sm.head[tid + x * kThreads]) * 16);
                 sync_all<C>();
                 const uint4 none = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
                 for (int v0 = me; v0 < vectors; v0 += kAll) {
                     if (out_vec)
-                        st_hint(out + static_cast<int64_t>(v0) * 16, none, drop);
+                        st_hint(out_first + static_cast<int64_t>(v0) * 16, none, drop);
                     else
-                        for (int y = 0; y < 8; ++y) reinterpret_cast<unsigned short*>(out)[v0 * 8 + y] = 0xff80u;
+                        for (int y = 0; y < 8; ++y) reinterpret_cast<unsigned short*>(out_first)[v0 * 8 + y] = 0xff80u;
                 }
                 sync_all<C>();
 #pragma unroll
                 for (int x = 0; x < kOwn; ++x)
                     if (tid + x * kThreads < heads) {
                         const int at = static_cast<int>(sm.head[tid + x * kThreads]);
-                        const uint32_t w[4] = {cut(v[x].x, at * 8), cut(v[x].y, at * 8 + 2), cut(v[x].z, at * 8 + 4), cut(v[x].w, at * 8 + 6)};
+                        const uint32_t w[4] = {cut(v[x].x, span.index_of(at)), cut(v[x].y, span.index_of(at) + 2), cut(v[x].z, span.index_of(at) + 4), cut(v[x].w, span.index_of(at) + 6)};
                         if (out_vec)
-                            *reinterpret_cast<uint4*>(out + static_cast<int64_t>(at) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4*>(out_first + static_cast<int64_t>(at) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
                         else
 #pragma unroll
                             for (int y = 0; y < 8; ++y)
-                                reinterpret_cast<unsigned short*>(out)[at * 8 + y] = static_cast<unsigned short>(w[y / 2] >> (16 * (y % 2)));
+                                reinterpret_cast<unsigned short*>(out_first)[at * 8 + y] = static_cast<unsigned short>(w[y / 2] >> (16 * (y % 2)));
                     }
             } else if (out_vec) {
                 int v0 = me;
                 for (; v0 + (U - 1) * kAll < vectors; v0 += U * kAll) {
                     uint4 v[U];
 #pragma unroll
-                    for (int u = 0; u < U; ++u) v[u] = ld_hint(row + static_cast<int64_t>(v0 + u * kAll) * 16, drop);
+                    for (int u = 0; u < U; ++u) v[u] = ld_hint(first + static_cast<int64_t>(v0 + u * kAll) * 16, drop);
 #pragma unroll
                     for (int u = 0; u < U; ++u) write(v[u], v0 + u * kAll);
                 }
-                for (; v0 < vectors; v0 += kAll) write(ld_hint(row + static_cast<int64_t>(v0) * 16, drop), v0);
+                for (; v0 < vectors; v0 += kAll) write(ld_hint(first + static_cast<int64_t>(v0) * 16, drop), v0);
             }
-            for (int y = (out_vec || by_head ? vectors * 8 : 0) + me; y < a.V; y += kAll)
+            // the loose ones; and where the result lies otherwise than the row, all of them
+            const int singles = out_vec || by_head ? span.loose : a.V;
+            for (int l = me; l < singles; l += kAll) {
+                const int y = singles == a.V ? l : span.loose_at(l);
                 reinterpret_cast<unsigned short*>(out)[y] = static_cast<unsigned short>(cut(cells[y] | other, y));
+            }
         }
         if (by_list) {
             sync_all<C>();

@@ -352,6 +352,16 @@ def test_rows_of_a_vocabulary(V, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [2056, 7000, 16400, 30008, 30011])
+def test_rows_that_keep_many(V, dtype):
+    """Nuclei of thousands of tokens, and draws from far down."""
+    cut = dict(temperature=[3.0, 1.5, 5.0, 1.0], top_k=[0, 0, 3000, 0], top_p=[0.97, 0.9, 0.9, 1.0], min_p=[0.0, 0.0, 0.0, 1e-6])
+    us = torch.tensor([0.02, 0.6, 0.999]).repeat(4, 1)
+    _check_rows(_rows((4, 3), V, dtype, V), cut, us=us)
+    _check_rows(_rows((4, 3), V, dtype, V)[:, :, 3:], {**cut, "min_p": None, "top_k": None}, us=us)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_rows_with_very_many_of_one_value(dtype):
     """More equal logits than 16 bits count: of either sign, zeros of both, and
     places that a grammar masks."""
