@@ -1066,6 +1066,8 @@ def _logit_rows(t: torch.Tensor, name: str):
         raise ValueError("%s must be a CUDA tensor" % name)
     if stride[-1] != 1 and shape[-1] != 1:
         raise ValueError("%s must be contiguous in its last dimension" % name)
+    if 0 in shape:
+        return shape[0], 1, shape[-1], shape[-1]
     rows, step = 1, None                 # of the dimensions from here on
     for n, s in zip(shape[-2::-1], stride[-2::-1]):
         if n == 1:
@@ -1075,8 +1077,7 @@ def _logit_rows(t: torch.Tensor, name: str):
         elif s != rows * step:
             raise ValueError("the rows of %s must be evenly apart" % name)
         rows *= n
-    per = rows // shape[0] if shape[0] and rows else 1
-    return shape[0], per, shape[-1], shape[-1] if step is None else step
+    return shape[0], rows // shape[0], shape[-1], shape[-1] if step is None else step
 
 
 def _cuts(B: int, temperature, top_k, top_p, min_p):
