@@ -24,9 +24,10 @@ constexpr int kDecRows = 16, kDecRowsE4m3 = 80;
 // before, most of which find nothing to do; up to 16 blocks deep, so that the
 // round trips of a unit's parts are shared (2 chains of 177 nodes, 13 parts a
 // unit: 21 us in 16, 38 us in 8 that read twice; 32 gain nothing more).
-template <bool F16>
+// RAW: rows go out as fp32, for the kernel that this one lets begin (shared prefixes).
+template <bool F16, bool RAW>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, int MT) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (RAW) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 d0 = a.desc[2 * blockIdx.x];
     if (d0.x < 0) return;
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const AttnArgs a, int
         const float inv = nan ? nan_value : sum == 0.0f ? 0.0f : 1.0f / sum;
         const int64_t orow = (static_cast<int64_t>(b) * a.N + node) * a.Hq + h * a.g + row % a.g;
         const float x[4] = {acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv};
-        attn::store_row4<F16>(a, orow, d, x, nan ? nan_value : sum == 0.0f ? -INFINITY : top + log2f(sum));
+        attn::store_row4<F16, RAW>(a, orow, d, x, nan ? nan_value : sum == 0.0f ? -INFINITY : top + log2f(sum));
     }
 }
 
@@ -84,8 +85,9 @@ cudaError_t launch_attn_combine(const AttnArgs& a, bool f16, int MT, cudaStream_
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return f16 ? cudaLaunchKernelEx(&cfg, combine_kernel<true>, a, MT)
-               : cudaLaunchKernelEx(&cfg, combine_kernel<false>, a, MT);
+    if (a.raw)
+        return f16 ? cudaLaunchKernelEx(&cfg, combine_kernel<true, true>, a, MT) : cudaLaunchKernelEx(&cfg, combine_kernel<false, true>, a, MT);
+    return f16 ? cudaLaunchKernelEx(&cfg, combine_kernel<true, false>, a, MT) : cudaLaunchKernelEx(&cfg, combine_kernel<false, false>, a, MT);
 }
 
 size_t attn_workspace_bytes(int nsm) {

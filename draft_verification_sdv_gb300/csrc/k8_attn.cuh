@@ -36,13 +36,13 @@ __device__ __forceinline__ Cut cut_of(const AttnArgs& a, int b) {
     c.ctx = __ldg(a.ctx + b);
     c.cnt = a.count ? __ldg(a.count + b) : a.N;
     c.bad = c.ctx < 0 || c.cnt < 0 || c.cnt > a.N ||
-            static_cast<int64_t>(c.ctx) + (a.W > 0 ? c.cnt : 0) > static_cast<int64_t>(a.max_pages) * a.c.P;
+            static_cast<int64_t>(c.ctx) + (c.cnt & a.own) > static_cast<int64_t>(a.max_pages) * a.c.P;
     if (c.bad) c.ctx = c.cnt = 0;
     return c;
 }
 
 // Positions of the sequence that hold keys: the committed ones and the nodes'.
-__device__ __forceinline__ int held_of(const AttnArgs& a, const Cut& c) { return c.ctx + (a.W > 0 ? c.cnt : 0); }
+__device__ __forceinline__ int held_of(const AttnArgs& a, const Cut& c) { return c.ctx + (c.cnt & a.own); }
 
 // A node's queries (head 0).
 __device__ __forceinline__ const unsigned char* q_of(const AttnArgs& a, int b, int node) {
@@ -371,10 +371,10 @@ template <bool F16> __device__ __forceinline__ uint32_t pack2(float x, float y) 
     return r;
 }
 
-// Four elements, from d on, of a finished row.
-template <bool F16>
+// Four elements, from d on, of a finished row (RAW: it may go out as fp32).
+template <bool F16, bool RAW = true>
 __device__ __forceinline__ void store_row4(const AttnArgs& a, int64_t orow, int d, const float (&x)[4], float log2sum) {
-    if (a.raw) {
+    if (RAW && a.raw) {
         *reinterpret_cast<float4*>(a.raw + orow * a.c.D + d) = make_float4(x[0], x[1], x[2], x[3]);
         if (d == 0) a.raw_log[orow] = log2sum;
     } else {

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const AttnArgs a, const 
     const float inv = empty ? 0.0f : bad ? nan : 1.0f / sum;
 #pragma unroll
     for (int x = 0; x < 4; ++x) o[x] = empty ? 0.0f : o[x] * inv;
-    attn::store_row4<F16>(a, row, d, o, empty ? -INFINITY : bad ? nan : base + log2f(sum));
+    attn::store_row4<F16, false>(a, row, d, o, empty ? -INFINITY : bad ? nan : base + log2f(sum));
 }
 
 // from: rows and logs of the prefix, rows and logs of the parts.
@@ -114,7 +114,7 @@ cudaError_t launch_prefix_attn(const AttnArgs& a, const PrefixArgs& p, int type,
     }
     far.table = p.table, far.max_pages = p.max_pages, far.ctx = p.len;
     far.count = nullptr;
-    far.mask = p.table, far.mask_sb = 0, far.W = 0;  // (a mask without words: no node sees another)
+    far.mask = p.table, far.mask_sb = 0, far.W = far.own = 0;     // (a mask without words: no node sees another)
     far.raw = far_rows, far.raw_log = far_rows + cells;
     cudaError_t e = launch_tree_attn(far, type, e4m3, workspace, nsm, s);
     if (e != cudaSuccess) return e;

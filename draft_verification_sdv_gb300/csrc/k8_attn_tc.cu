@@ -342,8 +342,9 @@ template <bool F16> __device__ __forceinline__ bool odd_values(const unsigned ch
     return __any_sync(0xffffffffu, ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0);
 }
 
-// BOXES: queries come by tile copies.
-template <bool E4, bool F16, bool BOXES>
+// BOXES: queries come by tile copies.  PARTS: rows may go out as fp32, or go on from others'
+// (a.raw, a.far: shared prefixes); a kernel of its own, the others would be 3 % slower.
+template <bool E4, bool F16, bool BOXES, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                                                               const __grid_constant__ CUtensorMap map_v,
                                                               const __grid_constant__ CUtensorMap map_q, int run_rows) {
@@ -469,8 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             if (tid == 0 && u.cut.bad && a.status) atomicOr(a.status, kStatusBadLength);
             float m = -INFINITY, l = 0.0f;
             bool nan_row = false;
-            const bool begun = a.far != nullptr && u.t0 == 0;    // rows go on from others' outputs
-            if (run && begun) {
+            const bool begun = PARTS && a.far != nullptr && u.t0 == 0;    // rows go on from others' outputs
+            if (PARTS && run && begun) {
                 const int64_t from = (static_cast<int64_t>(u.b) * a.N + (live ? node : 0)) * a.Hq + u.h * a.g + row % a.g;
                 const float L = live ? a.far_log[from] : -INFINITY;
                 nan_row = L != L;
@@ -611,12 +612,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const bool empty = l == 0.0f || (!live && !ubad);
             const float inv = empty ? 0.0f : 1.0f / l;
             const float log2sum = ubad ? nanv : empty ? -INFINITY : m + log2f(l);
-            const bool half = whole && !a.raw;      // 16-bit outputs
+            const bool half = whole && !(PARTS && a.raw);      // 16-bit outputs
             if (mine && half && a.lse) a.lse[orow] = log2sum * kLn2;
-            if (mine && whole && a.raw) a.raw_log[orow] = log2sum;
+            if (PARTS && mine && whole && a.raw) a.raw_log[orow] = log2sum;
             if (mine && !whole) prow[MT * D + st * kRows + r] = log2sum;
             unsigned short* dst = static_cast<unsigned short*>(a.out) + orow * D;
-            float* pdst = whole ? a.raw + orow * D : prow + (st * kRows + r) * D;
+            float* pdst = PARTS && whole ? a.raw + orow * D : prow + (st * kRows + r) * D;
             for (int i = 0; i < D; i += 16) {
                 float o[16];
 #pragma unroll
@@ -930,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             if (nt == 0) continue;
             // stream s has a live row (stream 0 has one in every unit with tiles)
             const int streams = (u.mt * MT + kRows) / a.g < u.cut.cnt ? 2 : 1;
-            const bool begun = a.far != nullptr && u.t0 == 0;    // the softmax warps have set the outputs
+            const bool begun = PARTS && a.far != nullptr && u.t0 == 0;    // the softmax warps have set the outputs
             // (the unit before has waited for these keys with its last values)
             if (T == 0) ok = sync.wait(kFull, 0) && ok;
 #pragma unroll
@@ -999,22 +1000,22 @@ bool encode_q(CUtensorMap* map, const AttnArgs& a) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool E4, bool F16, bool BOXES>
+template <bool E4, bool F16, bool BOXES, bool PARTS>
 cudaError_t launch_one(AttnArgs a, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, int rows, int nsm, cudaStream_t s) {
     constexpr int bytes = Smem::bytes;
-    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_tc_kernel<E4, F16, BOXES>), bytes);
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(attn_tc_kernel<E4, F16, BOXES, PARTS>), bytes);
     if (e != cudaSuccess) return e;
     // the exchange of registers needs a launch that has them
     static const int regs = [] {
         cudaFuncAttributes at;
-        return cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(attn_tc_kernel<E4, F16, BOXES>)) == cudaSuccess ? at.numRegs : 0;
+        return cudaFuncGetAttributes(&at, reinterpret_cast<const void*>(attn_tc_kernel<E4, F16, BOXES, PARTS>)) == cudaSuccess ? at.numRegs : 0;
     }();
     if (regs != kRegs) return cudaErrorInvalidKernelImage;
     a.ctas = nsm;
     const int mts = (a.N * a.g + MT - 1) / MT;
     const int64_t units = static_cast<int64_t>(a.B) * a.c.H * mts;
     a.rounds = mts > 1 && units >= 2 * nsm ? static_cast<int>(units / nsm - 1) : 0;
-    attn_tc_kernel<E4, F16, BOXES><<<static_cast<unsigned>(nsm), kThreads, bytes, s>>>(a, k, v, q, rows);
+    attn_tc_kernel<E4, F16, BOXES, PARTS><<<static_cast<unsigned>(nsm), kThreads, bytes, s>>>(a, k, v, q, rows);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_attn_combine(a, F16, MT, s);
 }
@@ -1022,7 +1023,9 @@ cudaError_t launch_one(AttnArgs a, const CUtensorMap& k, const CUtensorMap& v, c
 template <bool E4, bool F16>
 cudaError_t launch(const AttnArgs& a, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& q, bool boxes, int rows, int nsm,
                    cudaStream_t s) {
-    return boxes ? launch_one<E4, F16, true>(a, k, v, q, rows, nsm, s) : launch_one<E4, F16, false>(a, k, v, q, rows, nsm, s);
+    if (a.raw || a.far)
+        return boxes ? launch_one<E4, F16, true, true>(a, k, v, q, rows, nsm, s) : launch_one<E4, F16, false, true>(a, k, v, q, rows, nsm, s);
+    return boxes ? launch_one<E4, F16, true, false>(a, k, v, q, rows, nsm, s) : launch_one<E4, F16, false, false>(a, k, v, q, rows, nsm, s);
 }
 
 }  // namespace

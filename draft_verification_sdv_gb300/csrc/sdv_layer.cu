@@ -125,7 +125,7 @@ sdv_status attn_args(const sdv_kv_cache* cache, int B, int N, int Hq, sdv_dtype 
     a->table = block_table, a->ctx = ctx_len, a->count = count, a->mask = mask, a->mask_sb = mask_sb;
     a->out = out, a->lse = lse;
     a->status = reinterpret_cast<unsigned*>(status);
-    a->B = B, a->N = N, a->Hq = Hq, a->W = (N + 31) / 32, a->max_pages = max_pages;
+    a->B = B, a->N = N, a->Hq = Hq, a->W = (N + 31) / 32, a->own = -1, a->max_pages = max_pages;
     a->scale_log2 = scale * 1.4426950408889634f;
     a->hooks = __atomic_load_n(&test_hooks, __ATOMIC_RELAXED);
     return SDV_OK;

@@ -86,7 +86,8 @@ struct AttnArgs {
     int4* desc;                       // two per CTA: the unit that its start splits
     unsigned* beyond;                 // one per SM: see launch_attn_redo
     int B, N, Hq, g, max_pages;
-    int W;                            // words of a mask row; 0: no node's keys are in the cache (mask is then not read)
+    int W;                            // words of a mask row
+    int own;                          // -1; 0 (with W = 0, and a mask that is not read): no node's keys are in the cache
     float scale_log2;                 // scale * log2(e)
     int ctas, rounds;                 // see k8_attn.cuh
     unsigned hooks;                   // kHook* bits (tests of the waits)
