@@ -26,6 +26,9 @@ namespace {
 
 using namespace attn;
 
+#ifndef ONE_CTAS
+#define ONE_CTAS 3
+#endif
 constexpr int kOneWarps = 4, kOneThreads = 32 * kOneWarps, kOneTile = 16;
 constexpr float kOneSlack = 8.0f;           // how far (log2) scores may pass their reference
 constexpr float kOneUp = 14.0f - kOneSlack; // e4m3: weights of values may reach 2^14
@@ -38,7 +41,7 @@ __device__ __forceinline__ uint4 ld_cells(const unsigned char* p, bool there) {
 
 // H: halves of the 16 rows in use.
 template <int DP, bool E4, bool F16, int H>
-__global__ void __launch_bounds__(kOneThreads, DP == 64 ? 4 : H == 1 ? 3 : 2) attn_one_kernel(const AttnArgs a, const float* far, const float* far_log, int splits, int chunk) {
+__global__ void __launch_bounds__(kOneThreads, DP == 64 ? 4 : H == 1 ? ONE_CTAS : 2) attn_one_kernel(const AttnArgs a, const float* far, const float* far_log, int splits, int chunk) {
     constexpr bool M16 = F16 || E4;                  // the products' type is fp16
     constexpr int KL = E4 ? DP / 64 : DP / 32;       // 16-byte loads of a lane from a key row
     constexpr int VL = E4 ? 1 : DP / 64;             // ... from a value row (e4m3 heads of 64: half of one)
@@ -105,34 +108,41 @@ __global__ void __launch_bounds__(kOneThreads, DP == 64 ? 4 : H == 1 ? 3 : 2) at
 #pragma unroll
     for (int r = 0; r < H; ++r) m[r] = mv[r] = -INFINITY, l[r] = 0.0f;
 
-    // a lane looks up the page of one of the tile's positions, a tile ahead
+    // a lane looks after one of the tile's positions: its page is asked for two tiles ahead,
+    // its cells one; keys (values) are read as soon as those before them are used
     const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
     auto page_at = [&](int pos) { return lane < kOneTile && pos + lane < end ? __ldg(table + (pos + lane) / a.c.P) : 0; };
-    bool nan_row = false;
-    int pos0 = begin + warp * kOneTile;
-    int page = page_at(pos0);
-    for (; pos0 < end; pos0 += kOneWarps * kOneTile) {
+    constexpr int kStep = kOneWarps * kOneTile;
+    struct Place {
+        int64_t at;                                  // the cells' offset, -1: none
+        int ke, ve;
+        bool bad;                                    // a page that is not the cache's
+    };
+    auto place_at = [&](int pos0, int page) {
+        Place p{-1, 127, 127, false};
         const int pos = pos0 + lane;
-        const bool bad = lane < kOneTile && pos < end && (page < 0 || page >= a.c.pages);
-        if (bad && a.status) atomicOr(a.status, kStatusBadPage);
+        if (lane >= kOneTile || pos >= end) return p;
+        p.bad = page < 0 || page >= a.c.pages;
+        if (p.bad) return p;
         const int cell = h * a.c.P + pos % a.c.P;    // within the page
-        const int64_t at = lane < kOneTile && pos < end && !bad
-                               ? page * a.c.page_stride + static_cast<int64_t>(cell) * (a.c.D * (E4 ? 1 : 2)) : -1;
-        int ke = 127, ve = 127;
-        if constexpr (E4)
-            if (at >= 0) ke = a.c.ke[page * a.c.exp_page_stride + cell], ve = a.c.ve[page * a.c.exp_page_stride + cell];
-        page = page_at(pos0 + kOneWarps * kOneTile);
-        // keys g4 and 8 + g4; values 2 t4, 2 t4 + 1, 2 t4 + 8 and 2 t4 + 9
-        uint4 k[2][KL], v[4][VL];
+        p.at = page * a.c.page_stride + static_cast<int64_t>(cell) * (a.c.D * (E4 ? 1 : 2));
+        if constexpr (E4) p.ke = a.c.ke[page * a.c.exp_page_stride + cell], p.ve = a.c.ve[page * a.c.exp_page_stride + cell];
+        return p;
+    };
+    // keys g4 and 8 + g4; values 2 t4, 2 t4 + 1, 2 t4 + 8 and 2 t4 + 9
+    uint4 k[2][KL], v[4][VL];
+    auto load_keys = [&](const Place& p) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int64_t row = __shfl_sync(0xffffffffu, at, i * 8 + g4);
+            const int64_t row = __shfl_sync(0xffffffffu, p.at, i * 8 + g4);
 #pragma unroll
             for (int j = 0; j < KL; ++j) k[i][j] = ld_cells(a.c.k + row + j * 64 + t4 * 16, row >= 0);
         }
+    };
+    auto load_values = [&](const Place& p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t row = __shfl_sync(0xffffffffu, at, 2 * t4 + (i & 1) + 8 * (i >> 1));
+            const int64_t row = __shfl_sync(0xffffffffu, p.at, 2 * t4 + (i & 1) + 8 * (i >> 1));
 #pragma unroll
             for (int j = 0; j < VL; ++j) {
                 if constexpr (E4 && DP == 64) {
@@ -144,6 +154,17 @@ __global__ void __launch_bounds__(kOneThreads, DP == 64 ? 4 : H == 1 ? 3 : 2) at
                 }
             }
         }
+    };
+    bool nan_row = false;
+    int pos0 = begin + warp * kOneTile;
+    int page = page_at(pos0 + kStep);
+    Place here = place_at(pos0, page_at(pos0));
+    load_keys(here);
+    load_values(here);
+    for (; pos0 < end; pos0 += kStep) {
+        const Place next = place_at(pos0 + kStep, page);
+        page = page_at(pos0 + 2 * kStep);
+        if (here.bad && a.status) atomicOr(a.status, kStatusBadPage);
 
         // ---- scores ----
         float s[2][4];
@@ -169,9 +190,11 @@ __global__ void __launch_bounds__(kOneThreads, DP == 64 ? 4 : H == 1 ? 3 : 2) at
             }
         }
 
+        load_keys(next);
+
         // ---- scale, what lies past the end, references ----
         float ev[2][2] = {};
-        const uint32_t odd = __ballot_sync(0xffffffffu, bad || (E4 && at >= 0 && (ke == 255 || ve == 255)));
+        const uint32_t odd = __ballot_sync(0xffffffffu, here.bad || (E4 && here.at >= 0 && (here.ke == 255 || here.ve == 255)));
         nan_row |= odd != 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -180,9 +203,9 @@ __global__ void __launch_bounds__(kOneThreads, DP == 64 ? 4 : H == 1 ? 3 : 2) at
                 const int col = i * 8 + 2 * t4 + x;
                 float kf = 1.0f;
                 if constexpr (E4) {
-                    const int e = __shfl_sync(0xffffffffu, ke, col);
+                    const int e = __shfl_sync(0xffffffffu, here.ke, col);
                     kf = e == 0 ? __int_as_float(0x00400000) : __int_as_float(e << 23);
-                    ev[i][x] = static_cast<float>(__shfl_sync(0xffffffffu, ve, col) - 127);
+                    ev[i][x] = static_cast<float>(__shfl_sync(0xffffffffu, here.ve, col) - 127);
                 }
 #pragma unroll
                 for (int r = 0; r < H; ++r) s[i][2 * r + x] = pos0 + col < end ? s[i][2 * r + x] * rowf[r] * kf : -INFINITY;
@@ -262,6 +285,8 @@ __global__ void __launch_bounds__(kOneThreads, DP == 64 ? 4 : H == 1 ? 3 : 2) at
                 }
             }
         }
+        load_values(next);
+        here = next;
     }
 
     // ---- the warps' outputs join, and then the prefix's ----
