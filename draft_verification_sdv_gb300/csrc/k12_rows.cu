@@ -13,8 +13,11 @@
 // histograms of keys (row_in_passes).
 //
 // A row is shared by a cluster of C CTAs where there are few; the first one has the list.
-// What bounds it: for the first look the row's bytes, for the second the
-// instructions of a weight.
+// What bounds it: for a row that its head settles, the latency of its steps (13 000
+// clocks to list 32001 logits, 9000 to sort 1000 of them, 6500 for the places); a
+// second look takes 35 000 to 50 000 clocks for the instructions of the weights, and
+// bins 50 000 to 70 000.  168 rows of 32001 under top-p or min-p: 60 to 90 us, as many
+// rows need bins (166 when all went in passes, 109 before bins).
 #include "k12_rows.cuh"
 
 namespace sdv {

@@ -17,8 +17,11 @@
 // k8_attn_dec.cu.  The warps' outputs join in shared memory, and with the prefix's
 // row, where nothing was split.
 //
-// Tokens of 128 sequences, 1 to 700 own positions, 8 x 8 heads of 128, 16 bits: see
-// launch_attn_one.
+// What bounds it: the latency of a unit's chain of reads (length, page, cells) and the
+// cells in flight, of which three CTAs an SM (168 registers) hold 16 KB a warp.  One
+// token each of 128 sequences with 1 to 700 own positions, 8 x 8 heads of 128, 16 bits:
+// 56 us, 3.2 TB/s (104 us and two joins in units of k8_attn_dec.cu, of which each costs 9
+// us); 96 sequences of up to 500, e4m3: 29 us (71).
 #include "k8_attn_mma.cuh"
 
 namespace sdv {
@@ -26,9 +29,6 @@ namespace {
 
 using namespace attn;
 
-#ifndef ONE_CTAS
-#define ONE_CTAS 3
-#endif
 constexpr int kOneWarps = 4, kOneThreads = 32 * kOneWarps, kOneTile = 16;
 constexpr float kOneSlack = 8.0f;           // how far (log2) scores may pass their reference
 constexpr float kOneUp = 14.0f - kOneSlack; // e4m3: weights of values may reach 2^14
@@ -41,7 +41,7 @@ __device__ __forceinline__ uint4 ld_cells(const unsigned char* p, bool there) {
 
 // H: halves of the 16 rows in use.
 template <int DP, bool E4, bool F16, int H>
-__global__ void __launch_bounds__(kOneThreads, DP == 64 ? 4 : H == 1 ? ONE_CTAS : 2) attn_one_kernel(const AttnArgs a, const float* far, const float* far_log, int splits, int chunk) {
+__global__ void __launch_bounds__(kOneThreads, DP == 64 ? 4 : H == 1 ? 3 : 2) attn_one_kernel(const AttnArgs a, const float* far, const float* far_log, int splits, int chunk) {
     constexpr bool M16 = F16 || E4;                  // the products' type is fp16
     constexpr int KL = E4 ? DP / 64 : DP / 32;       // 16-byte loads of a lane from a key row
     constexpr int VL = E4 ? 1 : DP / 64;             // ... from a value row (e4m3 heads of 64: half of one)
