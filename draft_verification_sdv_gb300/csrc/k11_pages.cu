@@ -11,9 +11,11 @@
 // kernel after, or behind a barrier where one CTA does it all.
 //
 // Small calls are bound by their launches and a chain of five reads (64 sequences of one
-// token: 4.3 us; 48 trees of 129 nodes: 4.0 and 2.3 us), large ones by barriers behind
-// such chains (300 prompts of up to 8191 tokens: 15.4 us, 1.9 TB/s; their 154 000
-// pages back: 4.9 us, 7.7 with a warp to a sequence).
+// token: 4.7 us; 48 trees of 129 nodes: 4.3 and 2.3 us).  Large ones issue for 60 % of
+// the time (300 prompts of up to 8191 tokens: 9.7 us, 3.0 TB/s of positions and slots;
+// 13.4 us with two divisions a token, which small calls liked better by 0.4); pages that
+// go back wait at barriers behind such chains (154 000: 4.8 us, 7.7 with a warp to a
+// sequence).
 #include "sdv_device.cuh"
 #include "sdv_layer.h"
 #include "sdv_plan.h"
@@ -160,29 +162,39 @@ template <bool EXTEND> __global__ void __launch_bounds__(kThreads) pages_kernel(
             }
         }
         if (EXTEND && n1 > n0) {                     // positions and slots
-            const int wide = n1 - n0;
-            const uint32_t items = static_cast<uint32_t>(seqs) * wide;         // at most 2^9 * 2^20
-            for (uint32_t it = tid; it < items; it += kThreads) {
-                const int i = static_cast<int>(it / wide), n = n0 + static_cast<int>(it - static_cast<uint32_t>(i) * wide);
+            // a power of two of threads to a sequence, and one division for all its tokens
+            const int shift = min(n1 - n0 > 1 ? 32 - __clz(n1 - n0 - 1) : 0, 31 - __clz(kThreads)), group = 1 << shift;
+            const int step_pages = group / a.P, step_in = group - step_pages * a.P;
+            for (int i = tid >> shift; i < seqs; i += kThreads >> shift) {
                 const Seq q = s_seq[i];
-                const int64_t o = static_cast<int64_t>(b0 + i) * a.N + n;
-                int64_t slot = -1;
-                int position = 0;
+                const int32_t* row = a.table + static_cast<int64_t>(b0 + i) * a.max_pages;
+                const int offset = a.base ? a.base[b0 + i] : 0, has = q.held + q.pages;
+                int n = n0 + (tid & (group - 1)), place = 0, in = 0;
                 if (n < q.count) {
-                    const int at = q.at + n, place = at / a.P;
-                    int page = -1;                   // a new page comes from the list: its row is being filled
-                    if (place < q.held)
-                        page = a.table[static_cast<int64_t>(b0 + i) * a.max_pages + place];
-                    else if (place < q.held + q.pages)
-                        page = a.list[height - 1 - (q.before + place - q.held)];
-                    if (page >= 0 && page < a.pages)
-                        slot = static_cast<int64_t>(page) * a.P + (at - place * a.P);
-                    else if (place < q.held + q.pages)
-                        bad |= kStatusBadPage;
-                    position = q.at + (a.depth ? a.depth[o] : n) + (a.base ? a.base[b0 + i] : 0);
+                    place = (q.at + n) / a.P;
+                    in = q.at + n - place * a.P;
                 }
-                if (a.positions) a.positions[o] = position;
-                if (a.slots) a.slots[o] = slot;
+                for (; n < n1; n += group) {
+                    const int64_t o = static_cast<int64_t>(b0 + i) * a.N + n;
+                    int64_t slot = -1;
+                    int position = 0;
+                    if (n < q.count) {
+                        int page = -1;               // a new page comes from the list: its row is being filled
+                        if (place < q.held)
+                            page = row[place];
+                        else if (place < has)
+                            page = a.list[height - 1 - (q.before + place - q.held)];
+                        if (page >= 0 && page < a.pages)
+                            slot = static_cast<int64_t>(page) * a.P + in;
+                        else if (place < has)
+                            bad |= kStatusBadPage;
+                        position = q.at + (a.depth ? a.depth[o] : n) + offset;
+                        place += step_pages, in += step_in;
+                        if (in >= a.P) in -= a.P, ++place;
+                    }
+                    if (a.positions) a.positions[o] = position;
+                    if (a.slots) a.slots[o] = slot;
+                }
             }
         }
         __syncthreads();
@@ -198,7 +210,7 @@ template <bool EXTEND> __global__ void __launch_bounds__(kThreads) finish_kernel
 }
 
 template <bool EXTEND> cudaError_t launch(const PagesArgs& a, int nsm, cudaStream_t s) {
-    // one CTA does it all where there is little: 64 tokens take 4.3 us, and a second launch 2.3
+    // one CTA does it all where there is little: 64 tokens take 4.7 us, and a second launch 2.5
     const int64_t items = static_cast<int64_t>(a.B) * (EXTEND ? a.N : a.max_pages);
     const bool small = items <= 4 * kThreads;
     int each = a.B, columns = a.N > 0 ? a.N : 1;
