@@ -852,7 +852,7 @@ template <bool DRAW, int C> cudaError_t launch_one(const RowsArgs& a, int slots,
 template <bool DRAW> cudaError_t launch(const RowsArgs& a, int nsm, cudaStream_t s) {
     // a row to a cluster, of as many CTAs as the machine has places for (one row of 152064: 37
     // us with one CTA, 27 with four, 22 with eight; 256 rows 65 us with one, 90 with two)
-        const int slots = kCtas * nsm;
+    const int slots = kCtas * nsm;
     if (a.rows * 8 <= slots) return launch_one<DRAW, 8>(a, slots, s);
     if (a.rows * 4 <= slots) return launch_one<DRAW, 4>(a, slots, s);
     if (a.rows * 2 <= slots) return launch_one<DRAW, 2>(a, slots, s);

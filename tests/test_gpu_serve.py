@@ -89,6 +89,20 @@ def test_pages_through_a_step(B, N, P, most):
         s.extend([0] * B, N, [min(n, P) for n in count])
 
 
+@pytest.mark.parametrize("P", [1, 3, 127, 128, 129, 511, 512, 513, 1000, 2600])
+@pytest.mark.parametrize("B,N", [(3, 2500), (70, 129), (40, 65)])
+def test_pages_of_any_size_for_any_number_of_tokens(B, N, P):
+    """A thread's tokens are a number of pages and a rest apart."""
+    r = random.Random(P + N)
+    most = sref.ceil_div(2 * N, P) + 1
+    start = [r.choice([0, 1, N, r.randint(0, most * P - N)]) for _ in range(B)]
+    held = [min(sref.ceil_div(x, P) + r.randint(0, 1), most) for x in start]
+    s = _Pages(r, B, P, most, B * (sref.ceil_div(N, P) + 1), held)
+    s.extend(start, N, [r.choice([0, 1, N - 1, N, r.randint(0, N)]) for _ in range(B)])
+    assert s.host.status == 0
+    s.release(start)
+
+
 @pytest.mark.parametrize("B,N", [(9, 40), (90, 33), (700, 16)])
 def test_pages_that_run_out(B, N):
     """Sequences are served in order until one no longer is; those after it that
@@ -232,6 +246,32 @@ def test_prefix_attn_strides_scale_and_unseen_cells(N, Hq, D, P, dtype, cdtype):
         else:
             t[~seen] = math.nan
     _check_prefix(case, far, ctx, count=count, scale=-0.2)
+
+
+@pytest.mark.parametrize("dtype,cdtype", TYPES)
+@pytest.mark.parametrize("N,Hq,Hk,D", [(1, 8, 1, 128), (1, 5, 1, 80), (3, 8, 2, 64), (40, 8, 1, 128), (70, 7, 1, 64)])
+def test_prefix_attn_of_padded_queries_that_are_no_numbers(N, Hq, Hk, D, dtype, cdtype):
+    """The prefix's pass knows no count: rows behind it come out as nothing, and leave
+    the others as they are."""
+    B, G, far, ctx = 6, 2, [70, 300], [0, 20, 3, 0, 140, 9]
+    count = [0, N, N - N // 2, N, max(N - 1, 1), 0]
+    q, *rest = _prefix_case(B, G, N, Hq, Hk, D, 16, far, ctx, dtype, cdtype, seed=N + D)
+    kc, vc, ke, ve, ptable, table = rest
+    want, wl, tol, tl = sref.prefix_attn(q.cpu(), kc.cpu(), vc.cpu(), ptable.cpu(), far, table.cpu(), ctx, count, None,
+                                         D ** -0.5, None if ke is None else ke.cpu(), None if ve is None else ve.cpu())
+    for bad in (math.nan, math.inf, -math.inf):
+        for b in range(B):
+            q[b, count[b]:] = bad
+        st = _status()
+        out, lse = bd.sdv_prefix_attn(q, kc, vc, ptable, _i32(far), table, _i32(ctx), count=_i32(count), k_exp=ke, v_exp=ve,
+                                      lse=True, status=st)
+        assert int(st) == 0 and not out.isnan().any() and not lse.isnan().any()
+        assert ((out.double().cpu() - want).abs() <= tol).all()
+        assert torch.equal(lse.cpu() == -math.inf, wl == -math.inf)
+        fin = wl > -math.inf
+        assert ((lse.double().cpu() - wl).abs()[fin] <= tl[fin]).all()
+        for b in range(B):
+            assert not out[b, count[b]:].any()
 
 
 def test_prefix_attn_without_a_prefix_and_bad_numbers():
