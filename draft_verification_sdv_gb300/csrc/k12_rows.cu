@@ -7,7 +7,7 @@
 // and the draw are places of running sums.  Where only top-p or the draw limits the
 // row, a second look adds up all weights (whole numbers: the sum is the one that
 // any other order gives), and the head's share of them tells whether the place lies in
-// it.  Other rows are counted and weighed into bins of equal width in (max - x) / T,
+// it, unless it is plain that it does not.  Other rows are counted and weighed into bins of equal width in (max - x) / T,
 // which keep the order, and the bin that holds a place is listed and sorted in turn
 // (row_by_bins); rows with too many logits in one bin go the long way, in passes over
 // histograms of keys (row_in_passes).
@@ -16,8 +16,8 @@
 // What bounds it: for a row that its head settles, the latency of its steps (13 000
 // clocks to list 32001 logits, 9000 to sort 1000 of them, 6500 for the places); a
 // second look takes 35 000 to 50 000 clocks for the instructions of the weights, and
-// bins 50 000 to 70 000.  168 rows of 32001 under top-p or min-p: 60 to 90 us, as many
-// rows need bins (166 when all went in passes, 109 before bins).
+// bins 50 000 to 70 000.  168 rows of 32001 under top-p or min-p: 60 to 80 us, as many
+// rows need bins (166 when all went in passes, 109 before bins, 96 with both for a row).
 #include "k12_rows.cuh"
 
 namespace sdv {
@@ -28,6 +28,10 @@ using namespace rows;
 constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = 4096;
 constexpr int kList = 2048, kOwn = kList / kThreads;
 constexpr uint32_t kOddNan = 1u;
+// What a logit behind the head is taken to weigh, in units of the head's least, where it is
+// guessed whether the place lies there (normal logits: 0.2 for a deviation of 1, 0.02 for 6;
+// the answer does not depend on it).
+constexpr float kRest = 0.125f;
 
 struct Head {
     uint64_t list[kList];                // key << 32 | ~index, 0: none
@@ -256,44 +260,51 @@ __device__ __forceinline__ int find(Head& sm, int n, uint64_t target) {
     return at;
 }
 
-// A row whose places do not lie in its head; the largest logit and the factors are known.
-// The first CTA; false: a bin does not fit the list, and nothing is written.
-template <bool DRAW> __device__ __noinline__ bool row_by_bins(const RowsArgs& a, int r, const Ask q, const Scale scale, float floor) {
+// Bins of equal width in (max - x) / T, which keep the order.
+struct Binned {
+    float top, wide;                     // bins per unit of logit
+    __device__ __forceinline__ explicit Binned(const Scale& s) : top(s.top), wide((kBins / 64) * 0.5f * s.hi) {}
+    __device__ __forceinline__ int of(float x) const { return static_cast<int>(fminf((top - x) * wide, static_cast<float>(kBins - 1))); }
+};
+
+// work(x, index) for each logit of a row, by one CTA.
+template <typename Work> __device__ __forceinline__ void each_logit(const unsigned char* row, int V, Work work) {
     constexpr int U = 2;
+    const int tid = threadIdx.x;
+    const Span span = span_of(row, V, 4);
+    const unsigned char* first = row + span.head * 4;
+    auto four = [&](const uint4& v, int at) {
+        work(__uint_as_float(v.x), at), work(__uint_as_float(v.y), at + 1);
+        work(__uint_as_float(v.z), at + 2), work(__uint_as_float(v.w), at + 3);
+    };
+    int i = tid;
+    for (; i + (U - 1) * kThreads < span.vectors; i += U * kThreads) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = ld_row(first + static_cast<int64_t>(i + u * kThreads) * 16);
+#pragma unroll
+        for (int u = 0; u < U; ++u) four(v[u], span.index_of(i + u * kThreads));
+    }
+    for (; i < span.vectors; i += kThreads) four(ld_row(first + static_cast<int64_t>(i) * 16), span.index_of(i));
+    if (tid < span.loose) work(reinterpret_cast<const float*>(row)[span.loose_at(tid)], span.loose_at(tid));
+}
+
+// All of a row's logits into bins, by one CTA: their weight (head.part[0]), how many are
+// finite (head.count[0]) and reach the floor (head.over).
+__device__ __noinline__ void weigh_bins(const unsigned char* row, int V, const Scale scale, float floor) {
     Bins& sm = smem().bins;
     Head& head = sm.head;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const unsigned char* row = static_cast<const unsigned char*>(a.logits) + r * a.in_stride;
-    const float* cells = reinterpret_cast<const float*>(row);
-    const Span span = span_of(row, a.V, 4);
-    const float wide = (kBins / 64) * 0.5f * scale.hi;           // bins per unit of logit
-    auto bin_of = [&](float x) { return static_cast<int>(fminf((scale.top - x) * wide, static_cast<float>(kBins - 1))); };
-    auto each = [&](auto work) {                     // (x, index)
-        const unsigned char* first = row + span.head * 4;
-        auto four = [&](const uint4& v, int at) {
-            work(__uint_as_float(v.x), at), work(__uint_as_float(v.y), at + 1);
-            work(__uint_as_float(v.z), at + 2), work(__uint_as_float(v.w), at + 3);
-        };
-        int i = tid;
-        for (; i + (U - 1) * kThreads < span.vectors; i += U * kThreads) {
-            uint4 v[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = ld_row(first + static_cast<int64_t>(i + u * kThreads) * 16);
-#pragma unroll
-            for (int u = 0; u < U; ++u) four(v[u], span.index_of(i + u * kThreads));
-        }
-        for (; i < span.vectors; i += kThreads) four(ld_row(first + static_cast<int64_t>(i) * 16), span.index_of(i));
-        if (tid < span.loose) work(cells[span.loose_at(tid)], span.loose_at(tid));
-    };
+    const Binned bins(scale);
     for (int x = tid; x < kBins; x += kThreads) sm.hist.count[x] = 0, sm.hist.mass[x] = 0;
     if (tid == 0) head.over = 0;
     __syncthreads();
     uint64_t weight = 0;
     uint32_t finite = 0, over = 0;
-    each([&](float x, int) {
+    each_logit(row, V, [&](float x, int) {
         if (!(x > -INFINITY)) return;
         const uint64_t w = weight_of(scale, x, head.tables);
-        const int b = bin_of(x);
+        const int b = bins.of(x);
         atomicAdd(&sm.hist.count[b], 1u);
         add_weight(&sm.hist.mass[b], w);
         weight += w;
@@ -306,9 +317,25 @@ template <bool DRAW> __device__ __noinline__ bool row_by_bins(const RowsArgs& a,
     over = __reduce_add_sync(0xffffffffu, over);
     if (lane == 0) head.sum[warp] = weight, head.word[warp] = finite, atomicAdd(&head.over, over);
     __syncthreads();
-    weight = 0, finite = 0;
-    for (int w = 0; w < kWarps; ++w) weight += head.sum[w], finite += head.word[w];
+    if (tid == 0) {
+        weight = 0, finite = 0;
+        for (int w = 0; w < kWarps; ++w) weight += head.sum[w], finite += head.word[w];
+        head.part[0] = weight, head.count[0] = finite;
+    }
     __syncthreads();
+}
+
+// A row whose places do not lie in its head; the largest logit and the factors are known,
+// and the bins are filled (weigh_bins).  The first CTA; false: a bin does not fit the list,
+// and nothing is written.
+template <bool DRAW> __device__ __noinline__ bool row_by_bins(const RowsArgs& a, int r, const Ask q, const Scale scale) {
+    Bins& sm = smem().bins;
+    Head& head = sm.head;
+    const int tid = threadIdx.x;
+    const unsigned char* row = static_cast<const unsigned char*>(a.logits) + r * a.in_stride;
+    const Binned bins(scale);
+    uint64_t weight = head.part[0];
+    const uint32_t finite = head.count[0];
     uint32_t kept = finite, most = min(finite, head.over);
     if (q.top_k > 0) most = min(most, static_cast<uint32_t>(q.top_k));
     // the last of the first `most`; the last before which less than top_p of their weight
@@ -329,8 +356,8 @@ template <bool DRAW> __device__ __noinline__ bool row_by_bins(const RowsArgs& a,
             while (size < n) size <<= 1;
             for (int x = n + tid; x < size; x += kThreads) head.list[x] = 0;
             __syncthreads();
-            each([&](float x, int index) {
-                if (x > -INFINITY && bin_of(x) == bin)
+            each_logit(row, a.V, [&](float x, int index) {
+                if (x > -INFINITY && bins.of(x) == bin)
                     head.list[atomicAdd(&head.listed, 1u)] = static_cast<uint64_t>(key_of(x)) << 32 | static_cast<uint32_t>(~index);
             });
             sort_list(size);
@@ -354,7 +381,7 @@ template <bool DRAW> __device__ __noinline__ bool row_by_bins(const RowsArgs& a,
     if (tid == 0 && a.kept) a.kept[r] = static_cast<int32_t>(kept);
     if constexpr (!DRAW) {
         float* out = reinterpret_cast<float*>(static_cast<unsigned char*>(a.out) + r * a.out_stride);
-        each([&](float x, int index) {
+        each_logit(row, a.V, [&](float x, int index) {
             out[index] = (static_cast<uint64_t>(key_of(x)) << 32 | static_cast<uint32_t>(~index)) >= last ? x : -INFINITY;
         });
     }
@@ -408,7 +435,20 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
         const bool limited = q.T == 0.0f || by_floor || by_k;
         const bool whole = bound == kKeyLow + 1;     // the list holds every finite logit
         const bool sums = usable && !limited && !whole && q.top_k == 0 && q.min_p == 0.0f && (DRAW || q.top_p < 1.0f || a.kept);
-        if (sums) {
+        if (rank == 0 && usable && q.T != 0.0f) sum_list(n, scale);
+        // A place that is likely not to lie in the head is looked for in bins at once, which
+        // saves weighing all logits twice.  32001 normal logits under top-p 0.95, 168 rows:
+        // 96 us against 125 with a second look first (deviation 3); 1088 rows 352 against 470,
+        // and where the head does, 227 against 260 with bins for every row (deviation 6).
+        bool binned = false;
+        if (C == 1 && sums) {
+            const float held = static_cast<float>(sm.total), least = static_cast<float>(weight_of(scale, of_key(bound), sm.tables));
+            const float part = q.top_p < 1.0f ? q.top_p : DRAW ? q.u : 0.0f;
+            binned = part * (held + kRest * least * static_cast<float>(a.V - n)) >= held;
+        }
+        if (binned) {
+            weigh_bins(row, a.V, scale, floor);
+        } else if (sums) {
             sum_all<C>(row, span, rank, scale);
             sync_all<C>();
         }
@@ -421,7 +461,6 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
             } else if (!usable) {
                 verdict = kLongWay;                  // (a row without finite logits too)
             } else if (q.T != 0.0f) {
-                sum_list(n, scale);
                 kept = n, weight = sm.total;
                 if (whole) all = n;
                 if (sums) {
@@ -484,7 +523,8 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
         sync_all<C>();
         const uint32_t verdict = sm.verdict;
         if (verdict == kLongWay) {
-            if (rank == 0 && !(usable && row_by_bins<DRAW>(a, static_cast<int>(r), q, scale, floor))) {
+            if (rank == 0 && usable && !binned) weigh_bins(row, a.V, scale, floor);
+            if (rank == 0 && !(usable && row_by_bins<DRAW>(a, static_cast<int>(r), q, scale))) {
                 PassSmem<kThreads, kBins>& ps = smem().passes;
                 __syncthreads();
                 load_tables(ps.tables, tid, kThreads);
