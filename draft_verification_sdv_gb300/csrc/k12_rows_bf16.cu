@@ -706,7 +706,10 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
         // the head holds every logit from the last value on
         const bool by_head = vectors > 0 && !uncut && !by_index && all.heads <= kHeads && key_of(value_of(key)) >= all.head;
         const uint32_t heads = min(sm.heads, static_cast<uint32_t>(kHeads));
-        auto put = [&](uint32_t token) { lead->list[atomicAdd(&lead->listed, 1u)] = token; };
+        auto put = [&](uint32_t token) {                             // (once for each of the at_n)
+            const uint32_t n = atomicAdd(&lead->listed, 1u);
+            if (n < kListed) lead->list[n] = token;
+        };
         if (DRAW && by_list) {
             auto look_for = [&](const uint4& v, int v0) {
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -726,7 +729,10 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
                 for (int u = 0; u < U; ++u) v[u] = ld_row(first + static_cast<int64_t>(v0 + u * kAll) * 16);
 #pragma unroll
                 for (int u = 0; u < U; ++u) look_for(v[u], v0 + u * kAll);
-                if (C == 1 && *reinterpret_cast<volatile uint32_t*>(&sm.listed) >= at_n) break;      // that was all of them
+                if (C == 1 && *reinterpret_cast<volatile uint32_t*>(&sm.listed) >= at_n) {           // that was all of them
+                    v0 = vectors;
+                    break;
+                }
             }
             for (; v0 < vectors; v0 += kAll) look_for(ld_row(first + static_cast<int64_t>(v0) * 16), v0);
             if (me < span.loose && (halves_of(cells[span.loose_at(me)] | other, pair, sign) & 1)) put(span.loose_at(me));
