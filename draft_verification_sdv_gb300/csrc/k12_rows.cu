@@ -373,7 +373,7 @@ template <bool DRAW> __device__ __noinline__ bool row_by_bins(const RowsArgs& a,
             unit = end - sm.picked.before_w - head.before[at];
             if (tid == 0) {
                 a.tokens[r] = static_cast<int32_t>(~static_cast<uint32_t>(head.list[at]));
-                if (a.logprob) a.logprob[r] = log_share(unit, weight);
+                if (a.logprob) a.logprob[r] = log_share(scale, of_key(static_cast<uint32_t>(head.list[at] >> 32)), unit, weight, head.tables);
             }
         }
         __syncthreads();
@@ -510,7 +510,7 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, 2) rows_
                     if (DRAW && a.logprob) a.logprob[r] = nan;
                 } else if (DRAW && verdict == kDone) {
                     a.tokens[r] = static_cast<int32_t>(~static_cast<uint32_t>(sm.list[drawn]));
-                    if (a.logprob) a.logprob[r] = log_share(unit, weight);
+                    if (a.logprob) a.logprob[r] = log_share(scale, of_key(static_cast<uint32_t>(sm.list[drawn] >> 32)), unit, weight, sm.tables);
                 }
                 if (a.kept && verdict != kLongWay) a.kept[r] = verdict == kBad ? 0 : kept;
             }

@@ -88,13 +88,8 @@ __device__ __forceinline__ float fall_of(const Scale& s, float x, float& low) {
     return p;
 }
 
-// The whole weight of a logit that is at most the largest.  Most logits of a row weigh
-// less than 2^20, which fp32 gives to a unit.
-__device__ __forceinline__ uint64_t weight_of(const Scale& s, float x, const Tables& t) {
-    float low;
-    const float p = fmaxf(fall_of(s, x, low), 0.0f);
-    if (p >= kFallLight) return p < kFallMost ? __float2uint_rn(ex2((static_cast<float>(kOneBits) - p) - low)) : 0u;
-    if (x == s.top) return uint64_t(1) << kOneBits;
+// 2^(44 - p - low) to the next whole number, for p up to kFallMost.
+__device__ __forceinline__ uint64_t weight_of_fall(float p, float low, const Tables& t) {
     const float k = rintf(p), f = k - p;                         // exact; 2^-p = 2^-k 2^f
     const int i = __float2int_rn(f * 128.0f);
     const float g = __fmaf_rn(static_cast<float>(i), -0x1p-7f, f);
@@ -108,8 +103,18 @@ __device__ __forceinline__ uint64_t weight_of(const Scale& s, float x, const Tab
     const int32_t frac = __float2int_rn(y * 0x1p46f) + __float2int_rn(more * 0x1p46f);
     const uint64_t ab = __umul64hi(t.coarse[i + 64], t.fine[j + 64]) << 2;
     const uint64_t w = ab + static_cast<uint64_t>((static_cast<int64_t>(static_cast<uint32_t>(ab >> 31)) * frac) >> 15);   // 2^f in units of 2^-62
-    const int shift = 62 - kOneBits + static_cast<int>(k);       // 18 .. 42
+    const int shift = 62 - kOneBits + static_cast<int>(k);       // 18 .. 64
     return ((w >> (shift - 1)) + 1) >> 1;
+}
+
+// The whole weight of a logit that is at most the largest.  Most logits of a row weigh
+// less than 2^20, which fp32 gives to a unit (the exponent is rounded to 2^-20).
+__device__ __forceinline__ uint64_t weight_of(const Scale& s, float x, const Tables& t) {
+    float low;
+    const float p = fmaxf(fall_of(s, x, low), 0.0f);
+    if (p >= kFallLight) return p < kFallMost ? __float2uint_rn(ex2((static_cast<float>(kOneBits) - p) - low)) : 0u;
+    if (x == s.top) return uint64_t(1) << kOneBits;
+    return weight_of_fall(p, low, t);
 }
 
 // a / b, less than 2^20: off by one at most in fp32.
@@ -202,8 +207,14 @@ __device__ __forceinline__ uint64_t times_up(float p, uint64_t w) {
     return down + left;
 }
 
-// ln(unit / weight), a quotient of whole weights.
-__device__ __forceinline__ float log_share(uint64_t unit, uint64_t weight) {
+// ln(w / weight) for a drawn logit of weight `unit`.  A light one's is worked out again:
+// being off by one would show in the logarithm (5e-6 at 2^17.5).
+static __device__ __noinline__ float log_share(const Scale& s, float x, uint64_t unit, uint64_t weight, const Tables& t) {
+    if (unit < uint64_t(1) << 21) {                  // (2^20 and the one after among them)
+        float low;
+        const float p = fall_of(s, x, low);
+        if (p >= kFallLight && p < kFallMost) unit = max(weight_of_fall(p, low, t), uint64_t(1));
+    }
     const uint64_t rest = weight - unit;
     const float f = __ull2float_rn(rest < unit ? rest : unit) / __ull2float_rn(weight);
     return rest < unit ? log1pf(-f) : logf(f);
@@ -609,7 +620,7 @@ __device__ __noinline__ void row_in_passes(const RowsArgs& a, int64_t r, PassSme
                     if (m >> y & 1) {
                         if (at == rank) {
                             a.tokens[r] = (s * 32 + lane) * E + y;
-                            if (a.logprob) a.logprob[r] = log_share(unit, weight);
+                            if (a.logprob) a.logprob[r] = log_share(row.scale, of_key(key), unit, weight, sm.tables);
                         }
                         ++at;
                     }

@@ -367,7 +367,7 @@ __device__ __noinline__ void settle(const RowsArgs& a, int r, const Ask q, const
     }
     if (lane == 0) {
         if (a.kept) a.kept[r] = static_cast<int32_t>(kept);
-        if (DRAW && a.logprob) a.logprob[r] = log_share(unit, weight);
+        if (DRAW && a.logprob) a.logprob[r] = log_share(scale, value_of(key), unit, weight, sm.tables);
     }
 }
 

@@ -79,3 +79,136 @@ def test_draws_of_a_value_that_many_tokens_have(many):
     _check(x, dict(T=T), u)
     # a truncation that ends among them, and draws from what it leaves
     _check(x, dict(T=T, top_p=p), [r.random() for _ in range(R)])
+
+
+# ---- batches ----
+
+KINDS = ["model", "flat", "few", "equal", "masked", "peak", "far", "nan", "inf", "none"]
+BAD = KINDS[-3:]
+
+
+def _batch(R, V, dtype, seed):
+    """Rows of every kind side by side, and their kinds."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = random.Random(seed)
+    x = torch.randn((R, V), generator=g, device="cuda")
+    at = torch.arange(V, device="cuda")
+    kinds = [r.choice(KINDS[:4] if b % 3 else KINDS) for b in range(R)]
+    for b, kind in enumerate(kinds):
+        y = x[b]
+        if kind == "model":
+            y = r.choice([1.0, 3.0, 6.0]) * y + 8 - 1.1 * torch.log1p(at)
+        elif kind == "flat":
+            y = y * r.choice([1e-3, 0.3])
+        elif kind == "few":                          # many equal values, and zeros of both signs
+            y = (y * 2).round() / 2
+            y = torch.where(y == 0, torch.where(at % 2 == 0, 0.0, -0.0), y)
+        elif kind == "equal":
+            y = torch.full_like(y, -3.25)
+        elif kind in ("masked", "none"):
+            y = torch.where(torch.rand(V, generator=g, device="cuda") < (0.9 if kind == "masked" else 2), -math.inf, 2 * y)
+            if kind == "masked":
+                y[V // 2] = 1.0
+        elif kind == "far":                          # over all magnitudes that the type has
+            y = y * torch.exp2(torch.randint(-120, 120, (V,), generator=g, device="cuda").float())
+        elif kind == "nan":
+            y[r.randrange(V)] = math.nan
+        elif kind == "inf":
+            y[r.randrange(V)] = math.inf
+        x[b] = y
+    return x.to(dtype), kinds
+
+
+def _ask(R, V, seed, which):
+    r = random.Random(seed)
+    some = lambda off, f: [off if r.random() < 0.3 else f() for _ in range(R)]  # noqa: E731
+    cut = dict(T=some(0.0 if "0" in which else 1.0, lambda: r.uniform(0.3, 3.0)) if "T" in which else None,
+               top_k=some(0, lambda: int(math.exp(r.uniform(0, math.log(2 * V))))) if "k" in which else None,
+               top_p=some(1.0, lambda: r.choice([r.uniform(0.05, 0.999), 0.95, 0.999])) if "p" in which else None,
+               min_p=some(0.0, lambda: math.exp(r.uniform(math.log(1e-5), 0))) if "m" in which else None)
+    return cut, [r.choice([r.random(), r.random(), 0.0, 1 - 2.0 ** -24]) for _ in range(R)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("which", ["", "T0p", "p", "Tkp", "m", "T0kpm"])
+@pytest.mark.parametrize("V", [2103, 20011])
+@pytest.mark.parametrize("batch", range(5))
+def test_batches_of_rows(batch, V, which, dtype):
+    """The number of rows picks how many CTAs share one (eight to one, and some that
+    take several): every answer is the definition's, and the one that a few of the rows
+    get by themselves, in place too."""
+    m = _sms()
+    R = [m // 4, m // 4 + 1, m // 2 + 1, m + 1, 2 * m + 97][batch]
+    x, kinds = _batch(R, V, dtype, 100 * batch + V)
+    cut, u = _ask(R, V, batch, which)
+    dev, us = _dev(cut), torch.tensor(u, dtype=F32, device="cuda")
+    st = _status()
+    kept = torch.full((R,), -5, dtype=torch.int32, device="cuda")
+    tokens, logs = bd.sdv_sample(x, us, logprob=True, kept=kept, status=st, **dev)
+    out, many = bd.sdv_logits_truncate(x, kept=True, status=st, **dev)
+    bad = torch.tensor([k in BAD for k in kinds], device="cuda")
+    good = ~bad
+    assert int(st) == (bd.SDV_STATUS_BAD_ROW if bad.any() else 0)
+    assert torch.equal(kept, many)
+    assert (tokens[bad] == -1).all() and logs[bad].isnan().all() and (kept[bad] == 0).all() and out[bad].isnan().all()
+    pick = good.nonzero().flatten().tolist()
+    n, stay, want, wlogs = ref.rows(x[good], u=[u[b] for b in pick], **{k: v and [v[b] for b in pick] for k, v in cut.items()})
+    assert kept[good].tolist() == n
+    assert torch.equal(out[good], x[good].masked_fill(~stay, -math.inf))
+    assert tokens[good].tolist() == want
+    for got, lp in zip(logs[good].tolist(), wlogs):
+        assert abs(got - lp) <= 2.0 ** -23 + 2.0 ** -22 * abs(lp)
+    # a few rows at a time, and without the counts that another way may be taken for
+    eq = lambda a, b: torch.equal(a.view(torch.int32 if a.element_size() == 4 else torch.int16),  # noqa: E731
+                                  b.view(torch.int32 if b.element_size() == 4 else torch.int16))
+    for r0 in range(0, R, 30):
+        part = slice(r0, r0 + 30)
+        few = {name: t[part] for name, t in dev.items()}
+        t, lp = bd.sdv_sample(x[part], us[part], logprob=True, **few)
+        assert torch.equal(t, tokens[part]) and eq(lp, logs[part])
+        assert eq(bd.sdv_logits_truncate(x[part], **few), out[part])
+    same = x.clone()
+    assert eq(bd.sdv_logits_truncate(same, out=same, **dev), out) and same.data_ptr() != x.data_ptr()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_batches_that_share_parameters(dtype):
+    """Several rows a sequence, more than there are places for."""
+    m, per, V = _sms(), 7, 5003
+    B = 2 * m // per + 5
+    x, kinds = _batch(B * per, V, dtype, 5)
+    good = [k not in BAD for k in kinds]
+    x[torch.tensor([not k for k in good], device="cuda")] = 0.5
+    cut, _ = _ask(B, V, 3, "T0kpm")
+    _, u = _ask(B * per, V, 4, "")
+    n, stay, want, _ = ref.rows(x, u=u, **{k: [a for a in v for _ in range(per)] for k, v in cut.items()})
+    x3 = x.view(B, per, V)
+    tokens = bd.sdv_sample(x3, torch.tensor(u, dtype=F32, device="cuda").view(B, per), **_dev(cut))
+    out, many = bd.sdv_logits_truncate(x3, kept=True, **_dev(cut))
+    assert tokens.flatten().tolist() == want and many.flatten().tolist() == n
+    assert torch.equal(out.view(-1, V), x.masked_fill(~stay, -math.inf))
+
+
+# ---- borders ----
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("R", [30, 700])
+@pytest.mark.parametrize("V", [1500, 12000, 100000])
+def test_log_probabilities_of_light_tokens(V, R, dtype):
+    """Five heavy tokens and many of 1 to 2^21 units, of which one of the last is drawn."""
+    falls = torch.linspace(15.5, 29.5, R).to(BF)
+    x = torch.full((R, V), 1.0, dtype=BF)
+    x[:, 5:] = 1.0 - falls[:, None]
+    x = x.to(dtype).cuda()
+    r = random.Random(V)
+    T = [r.uniform(0.98, 1.0) for _ in range(R)]
+    u = torch.full((R,), 1 - 2.0 ** -24, device="cuda")
+    tokens, logs = (t.tolist() for t in bd.sdv_sample(x, u, logprob=True, **_dev(dict(T=T))))
+    last = x[:, -1].double().tolist()
+    for b, (token, got) in enumerate(zip(tokens, logs)):
+        if token >= 5:                               # (what u passes in the rows with the lightest is the heavy ones)
+            w = math.floor(math.exp((last[b] - 1.0) / ref.f32(T[b])) * 2.0 ** 44 + 0.5)
+            # the sum may be off by a unit a token (2^-29 of itself), and is rounded to fp32
+            lp = math.log(w / (5 * 2 ** 44 + (V - 5) * w))
+            assert abs(got - lp) <= 2.0 ** -23 + 2.0 ** -22 * abs(lp), (b, w)
+    assert sum(t >= 5 for t in tokens) > R // 5
