@@ -824,16 +824,16 @@ sdv_status sdv_counts_commit(int B, int K, int gamma, int V, void* stream, const
  * Draws from rows of logits, and their truncation.  Rows r / per share one entry
  * of the parameters.  A row's tokens are ordered by falling logit, equal ones by
  * index, and token i weighs
- *   w_i = round(2^44 e^((x_i - max x) / temperature))       (whole numbers)
+ *   w_i = 2^44 e^((x_i - max x) / temperature)
+ * as a whole number, the nearest or the one next to it.
  * Of that order a row keeps a first part, cut in turn by
  *   min_p  to the tokens with x_i >= max x + temperature * ln(min_p)
  *   top_k  to the first top_k
  *   top_p  to those before which less than top_p * W lies, W being the weight of
  *          what the others keep
  * and a logit of -infinity is never kept.  temperature 0 keeps the first token
- * alone.  Since weights are whole numbers, what is kept and drawn does not depend
- * on how a row is shared out; the two products with W are rounded to 64-bit
- * floating point, as is W.
+ * alone.  W and its products with top_p and u are exact, so that what is kept and
+ * drawn does not depend on how a row is shared out.
  *   logits     device [rows] of V logits, row_stride elements apart (0 with one
  *              row, or to draw from one row several times)
  *   temperature  device float [rows / per], 0 or 2^-64 .. 2^64, or NULL: 1
@@ -850,8 +850,8 @@ sdv_status sdv_counts_commit(int B, int K, int gamma, int V, void* stream, const
  * u * (their sum).
  *   uniform    device float [rows], u in [0, 1)
  *   tokens     device int32 [rows]; -1 for a bad row
- *   logprob    device float [rows] or NULL: ln(w / (sum of kept weights)); NaN for
- *              a bad row
+ *   logprob    device float [rows] or NULL: ln(w / (sum of kept weights)), with the
+ *              nearest whole number for the drawn token's w; NaN for a bad row
  *
  * sdv_logits_truncate: the logits, -infinity where a token is not kept (a bad
  * row: NaN), unscaled: sdv_verify on such rows, with the same temperatures, is

@@ -192,6 +192,54 @@ def test_batches_that_share_parameters(dtype):
 # ---- borders ----
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N", [1024, 1 << 17])
+@pytest.mark.parametrize("R", [1, 400])
+def test_products_with_the_sum_are_exact(R, N, dtype):
+    """Sums beyond 2^53, which 64-bit floating point would round, at a border."""
+    # N equal logits and one that weighs 1: half of N 2^44 + 1 lies just behind N / 2 of them
+    x = torch.zeros((R, N + 1), dtype=dtype, device="cuda")
+    x[:, 77] = -30.5                                 # 2^44 e^-30.5 = 0.9986
+    assert ref.weights(torch.tensor([[0.0, -30.5]], dtype=torch.float64), torch.ones((1, 1), dtype=torch.float64))[0, 1] == 1
+    assert 0.5 * float(N * 2 ** 44 + 1) == N // 2 * 2 ** 44
+    out, kept = bd.sdv_logits_truncate(x, top_p=torch.full((R,), 0.5, device="cuda"), kept=True)
+    assert (kept == N // 2 + 1).all()
+    keep = torch.arange(N + 1, device="cuda") < N // 2 + 2
+    keep[77] = False
+    assert torch.equal(out > -math.inf, keep.expand(R, -1))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("R", [1, 400])
+def test_draws_at_a_border_that_rounding_moves(R, dtype):
+    """u W for a W beyond 2^53 whose rounding passes a border between two tokens."""
+    N, fall, u = 2048, 18.5, 1 - 2.0 ** -24          # u W = W - 2^-24 W lies among the light tokens
+    found = []
+    for i in range(400000):
+        T = 1.0 + i * 2.0 ** -22
+        real = math.exp(-fall / T) * 2.0 ** 44
+        w = math.floor(real + 0.5)
+        # one that fp32 gives exactly: an exponent below 32 is off by 2^-20 at most, and so the
+        # weight by less than 0.7 * 2^-20 of itself
+        if abs(real - w) + 0.7 * 2.0 ** -20 * w > 0.4:
+            continue
+        for m in (2 ** 31 // w + 2, 2 ** 31 // w + 300):
+            W = N * 2 ** 44 + m * w
+            exact, rounded = W - -(-W >> 24), int(u * float(W))
+            a, b = (exact - N * 2 ** 44) // w, (rounded - N * 2 ** 44) // w
+            if a != b and 0 <= a < m and 0 <= b < m:
+                found.append((T, m, a))
+        if len(found) >= 4:
+            break
+    assert found
+    for T, m, rank in found:
+        x = torch.zeros((R, N + m), dtype=dtype, device="cuda")
+        x[:, N // 2:N // 2 + m] = -fall
+        kept = torch.empty((R,), dtype=torch.int32, device="cuda")
+        tokens = bd.sdv_sample(x, torch.full((R,), u, device="cuda"), temperature=torch.full((R,), T, device="cuda"), kept=kept)
+        assert (kept == N + m).all() and (tokens == N // 2 + rank).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("R", [30, 700])
 @pytest.mark.parametrize("V", [1500, 12000, 100000])
 def test_log_probabilities_of_light_tokens(V, R, dtype):
