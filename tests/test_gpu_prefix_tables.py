@@ -1,0 +1,36 @@
+"""Attention behind shared prefixes where block tables are far wider than what the
+sequences hold, as a server's are that has room for its longest request."""
+import pytest
+import torch
+
+from draft_verification_sdv_gb300 import binding as bd
+from test_gpu_layer import TYPES, _i32, _status
+from test_gpu_serve import _check_prefix, _prefix_case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    bd.load(build=True)
+
+
+@pytest.mark.parametrize("dtype,cdtype", TYPES)
+@pytest.mark.parametrize("B,N,Hq,Hk,D,ctx", [(4, 1, 8, 1, 128, [0, 63, 64, 500]), (2, 1, 16, 2, 64, [1, 200]), (160, 1, 4, 1, 128, list(range(160))),
+                                             (3, 4, 8, 2, 128, [0, 70, 300]), (2, 40, 8, 1, 64, [9, 128])])
+def test_wide_tables(B, N, Hq, Hk, D, ctx, dtype, cdtype):
+    far = [300]
+    q, kc, vc, ke, ve, ptable, table = _prefix_case(B, 1, N, Hq, Hk, D, 16, far, ctx, dtype, cdtype, seed=B)
+    # (entries that nothing is held in are no pages: they are not looked at)
+    wide = torch.full((B, 2000), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    wptable = torch.full((1, 4000), 1 << 30, dtype=torch.int32, device="cuda")
+    wptable[:, :ptable.shape[1]] = ptable
+    _check_prefix((q, kc, vc, ke, ve, wptable, wide), far, ctx)
+    st = _status()
+    args = dict(k_exp=ke, v_exp=ve, lse=True, status=st)
+    one = bd.sdv_prefix_attn(q, kc, vc, wptable, _i32(far), wide, _i32(ctx), **args)
+    two = bd.sdv_prefix_attn(q, kc, vc, wptable, _i32(far), wide, _i32(ctx), **args)
+    assert int(st) == 0 and all(torch.equal(a, b) for a, b in zip(one, two))

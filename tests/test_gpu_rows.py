@@ -192,6 +192,40 @@ def test_batches_that_share_parameters(dtype):
 # ---- borders ----
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("R", [1, 400])
+def test_min_p_around_the_head(R, dtype):
+    """A row is first looked through for its largest few hundred logits: min-p's reach
+    onto, just above and just below logits of every rank from 1 to far behind those."""
+    V = 20011
+    g = torch.Generator(device="cuda").manual_seed(9)
+    row = (3 * torch.randn(V, generator=g, device="cuda") + 8).to(dtype)
+    value = torch.unique(row.double()).flip(0).tolist()
+    ranks = list(range(min(len(value), 1500))) if dtype == BF else list(range(0, 4000, 7))
+    T, mins = [], []
+    for i in ranks:
+        t = [1.0, 0.7, 2.5][i % 3]
+        p = torch.tensor(math.exp((value[i] - value[0]) / t), dtype=F32)
+        if not 0 < float(p) <= 1:
+            continue
+        for q in (p, torch.nextafter(p, torch.tensor(0.0)), torch.nextafter(p, torch.tensor(2.0))):
+            if 0 < float(q) <= 1:
+                T.append(t), mins.append(float(q))
+    # logits on the floor itself: T ln(min_p) is exact in 64 bits only at 1, so the floor lies
+    # within 2^-52 of itself from either side of what is asked
+    x = row.expand(len(T), V)
+    for k in (None, [600] * len(T)):
+        for r0 in range(0, len(T), R) if R > 1 else range(0, len(T), 37):
+            part = slice(r0, r0 + R)
+            cut = dict(T=T[part], min_p=mins[part], top_k=k and k[part])
+            kept = torch.empty((len(T[part]),), dtype=torch.int32, device="cuda")
+            bd.sdv_sample(x[part], torch.zeros(kept.shape, device="cuda"), kept=kept, **_dev(cut))
+            out, many = bd.sdv_logits_truncate(x[part], kept=True, **_dev(cut))
+            n, stay, _, _ = ref.rows(x[part], **cut)
+            assert kept.tolist() == n and many.tolist() == n
+            assert torch.equal(out, x[part].masked_fill(~stay, -math.inf))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("N", [1024, 1 << 17])
 @pytest.mark.parametrize("R", [1, 400])
 def test_products_with_the_sum_are_exact(R, N, dtype):
