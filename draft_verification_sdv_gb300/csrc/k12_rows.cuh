@@ -4,16 +4,17 @@
 // A row's tokens are ordered by falling logit, equal ones by index.  Token i weighs
 //   w_i = 2^44 e^((x_i - max) / T)
 // as a whole number, so that sums of weights are exact, the same in any order, and
-// fit 64 bits (V <= 2^19), and so are their products with u and top_p (times_down,
-// times_up): what is kept and drawn does not depend on how the row was shared out.  What a row keeps is then a first part of that order
-// (min-p, top-k and top-p each cut its end), and a draw is the token where the
-// running sum of weights passes u times the sum of those kept.
+// fit 64 bits (V <= 2^19).  Their products with u and top_p are exact too (times_down,
+// times_up): what is kept and drawn does not depend on how the row was shared out.  What a
+// row keeps is then a first part of that order (min-p, top-k and top-p each cut its
+// end), and a draw is the token where the running sum of weights passes u times the
+// sum of those kept.
 //
 // 2^44 e^(-d / T) is computed in pairs of fp32 numbers: p = d log2(e) / T to 2^-47
 // of itself, 2^(frac p) as a product of two table entries (7 bits each) and
 // 1 + z + z^2 / 2 + z^3 / 6 with |z| < 2^-14.9, in 62-bit fixed point: off by less
-// than half a unit before it is rounded.  Weights below 2^20 are fp32's, off by up to
-// 0.7 units there (their exponent is rounded to 2^-20), but for a drawn token's logarithm.
+// than a unit.  Weights below 2^20 are fp32's, off by up to 0.7 units there (their
+// exponent is rounded to 2^-20), but for a drawn token's logarithm.
 #pragma once
 
 #include "sdv_device.cuh"

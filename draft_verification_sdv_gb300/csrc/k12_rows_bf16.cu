@@ -66,7 +66,7 @@ struct Note {
     uint32_t head, heads, odd, beyond;   // the head's bound (a key), its vectors; kOdd* bits; counts beyond the octaves
 };
 struct Rest {
-    uint32_t zeros, infinities, odd;
+    uint32_t zeros, odd;
 };
 enum : uint32_t { kOddNan = 1u, kOddFar = 2u };
 
@@ -115,7 +115,6 @@ __device__ __forceinline__ void look_at(Rest& rest, uint32_t bits) {
     if (m - kBase < static_cast<uint32_t>(kAbove - kBase)) return;
     const bool zero = m == 0, inf = bits == 0xff80u;
     rest.zeros += zero;
-    rest.infinities += inf;
     rest.odd |= zero || inf ? 0u : m >= 0x7f80u ? kOddNan : kOddFar;
 }
 
@@ -625,7 +624,7 @@ template <bool DRAW, int C> __global__ void __launch_bounds__(kThreads, kCtas) r
             if (tid == 0) sm.heads = 0;
             sync_all<C>();
         }
-        Rest rest{0, 0, 0};
+        Rest rest{0, 0};
         if (whole && all.total != static_cast<uint32_t>(a.V)) {  // some logits are not in the octaves: which
             for (int x = me; x < vectors; x += kAll) {
                 const uint4 v = ld_row(first + static_cast<int64_t>(x) * 16);
