@@ -76,7 +76,7 @@ template <int C> __device__ __noinline__ uint32_t list_head(const unsigned char*
     Head& sm = smem().head;
     Head* const lead = of_rank<C>(&sm, 0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = rank * kThreads + threadIdx.x;
-    const uint64_t keep = keep_policy();
+    const uint64_t policy = first_policy();
     const unsigned char* first = row + span.head * 4;
     uint32_t bound = kKeyLow + 1;                    // (a short row is head as a whole)
     if (V > kList) {
@@ -87,7 +87,7 @@ template <int C> __device__ __noinline__ uint32_t list_head(const unsigned char*
             const int n = (rank * kWarps + warp) * 2 + u;
             const int at = (chunks >= kSamples ? static_cast<int>(static_cast<uint32_t>(n) * chunks / kSamples) : n) * 32 + lane;
             float x = -INFINITY;
-            if (at < span.vectors) x = largest_of(ld_hint(first + static_cast<int64_t>(at) * 16, keep));
+            if (at < span.vectors) x = largest_of(ld_hint(first + static_cast<int64_t>(at) * 16, policy));
             const uint32_t top = __reduce_max_sync(0xffffffffu, x > -INFINITY ? key_of(x) : 0u);
             if (top) least = min(least, top);
             most = max(most, top);
@@ -115,11 +115,11 @@ template <int C> __device__ __noinline__ uint32_t list_head(const unsigned char*
     for (; i + (U - 1) * kAll < span.vectors; i += U * kAll) {
         uint4 v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = ld_hint(first + static_cast<int64_t>(i + u * kAll) * 16, keep);
+        for (int u = 0; u < U; ++u) v[u] = ld_hint(first + static_cast<int64_t>(i + u * kAll) * 16, policy);
 #pragma unroll
         for (int u = 0; u < U; ++u) take(v[u], span.index_of(i + u * kAll));
     }
-    for (; i < span.vectors; i += kAll) take(ld_hint(first + static_cast<int64_t>(i) * 16, keep), span.index_of(i));
+    for (; i < span.vectors; i += kAll) take(ld_hint(first + static_cast<int64_t>(i) * 16, policy), span.index_of(i));
     if (me < span.loose) {                           // (six at most)
         const int y = span.loose_at(me);
         const float x = reinterpret_cast<const float*>(row)[y];

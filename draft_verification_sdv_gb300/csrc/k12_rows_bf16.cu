@@ -381,7 +381,7 @@ template <int C, bool COUNT> __device__ __noinline__ uint32_t count_row(const un
     Smem& sm = smem();
     const uint32_t counts = smem_u32(sm.count);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint64_t keep = keep_policy();
+    const uint64_t policy = first_policy();
     const int chunks = (vectors + 31) / 32;
     uint32_t least = 0xffffffffu, most = 0;
     {
@@ -392,7 +392,7 @@ template <int C, bool COUNT> __device__ __noinline__ uint32_t count_row(const un
             const int n = (rank * kWarps + warp) * 2 + u;
             const int at = (chunks >= kSamples ? static_cast<int>(static_cast<uint32_t>(n) * chunks / kSamples) : n) * 32 + lane;
             there[u] = at < vectors;
-            if (there[u]) v[u] = ld_hint(row + static_cast<int64_t>(at) * 16, keep);
+            if (there[u]) v[u] = ld_hint(row + static_cast<int64_t>(at) * 16, policy);
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -407,7 +407,7 @@ template <int C, bool COUNT> __device__ __noinline__ uint32_t count_row(const un
     const bool full = i + (U - 1) * kAll < vectors;
     if (full)                                        // (on their way while the bound is agreed upon)
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = ld_hint(row + static_cast<int64_t>(i + u * kAll) * 16, keep);
+        for (int u = 0; u < U; ++u) v[u] = ld_hint(row + static_cast<int64_t>(i + u * kAll) * 16, policy);
     sync_all<C>();
     uint32_t bound = kKeyLow + 1;                    // (a short row is head as a whole)
     if (vectors > kHeads) bound = min(fourth_smallest<C * kWarps>(sm.word), kKeyHigh);
@@ -431,10 +431,10 @@ template <int C, bool COUNT> __device__ __noinline__ uint32_t count_row(const un
             i += U * kAll;
             if (i + (U - 1) * kAll >= vectors) break;
 #pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = ld_hint(row + static_cast<int64_t>(i + u * kAll) * 16, keep);
+            for (int u = 0; u < U; ++u) v[u] = ld_hint(row + static_cast<int64_t>(i + u * kAll) * 16, policy);
         }
     }
-    for (; i < vectors; i += kAll) take(ld_hint(row + static_cast<int64_t>(i) * 16, keep), i);
+    for (; i < vectors; i += kAll) take(ld_hint(row + static_cast<int64_t>(i) * 16, policy), i);
     if constexpr (!COUNT) {
         const bool odd = !(fmaxf(bf16_lo(most2), bf16_hi(most2)) < INFINITY) || bf16_lo(most2) != bf16_lo(most2) || bf16_hi(most2) != bf16_hi(most2);
         if (odd) atomicOr(&sm.odd, kOddNan);
@@ -442,7 +442,7 @@ template <int C, bool COUNT> __device__ __noinline__ uint32_t count_row(const un
         __syncthreads();
         if (sm.heads <= kHeads)
             for (uint32_t x = threadIdx.x; x < sm.heads; x += kThreads) {
-                const uint4 w = ld_hint(row + static_cast<int64_t>(sm.head[x]) * 16, keep);
+                const uint4 w = ld_hint(row + static_cast<int64_t>(sm.head[x]) * 16, policy);
                 count_above(sm.count, w.x, f), count_above(sm.count, w.y, f), count_above(sm.count, w.z, f), count_above(sm.count, w.w, f);
             }
         if (rank * kThreads + static_cast<int>(threadIdx.x) < span.loose) {

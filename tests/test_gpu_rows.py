@@ -294,3 +294,28 @@ def test_log_probabilities_of_light_tokens(V, R, dtype):
             lp = math.log(w / (5 * 2 ** 44 + (V - 5) * w))
             assert abs(got - lp) <= 2.0 ** -23 + 2.0 ** -22 * abs(lp), (b, w)
     assert sum(t >= 5 for t in tokens) > R // 5
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_leave_the_cache_to_others(dtype):
+    """A kernel that reads what fits the L2 cache over and over is as fast after draws and
+    truncations as before them."""
+    y, out = torch.ones(25 << 20, device="cuda"), torch.empty((), device="cuda")
+
+    def best():
+        times = []
+        for _ in range(40):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            torch.sum(y, dim=0, out=out)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times[10:])
+    before = best()
+    x, _ = _batch(256, 152064, dtype, 1)
+    u = torch.full((256,), 0.5, device="cuda")
+    for cut in (dict(), dict(top_k=[50] * 256), dict(top_p=[0.95] * 256)):
+        bd.sdv_sample(x, u, **_dev(cut))
+        bd.sdv_logits_truncate(x, **_dev(cut))
+    assert best() <= 1.15 * before
