@@ -34,3 +34,31 @@ def test_wide_tables(B, N, Hq, Hk, D, ctx, dtype, cdtype):
     one = bd.sdv_prefix_attn(q, kc, vc, wptable, _i32(far), wide, _i32(ctx), **args)
     two = bd.sdv_prefix_attn(q, kc, vc, wptable, _i32(far), wide, _i32(ctx), **args)
     assert int(st) == 0 and all(torch.equal(a, b) for a, b in zip(one, two))
+
+
+@pytest.mark.parametrize("dtype,cdtype", TYPES)
+@pytest.mark.parametrize("B,N,g,D,far,ctx", [(8, 1, 8, 128, 20000, 50), (6, 40, 4, 128, 20000, 300), (6, 40, 3, 64, 20000, 300), (4, 2, 2, 64, 20000, 300)])
+def test_waits_that_run_out(B, N, g, D, far, ctx, dtype, cdtype):
+    """A tile of the first block never comes, in the prefix's pass and in the own
+    positions': what goes on from that block's rows is no number, the rest is right, and
+    so is the next call."""
+    # (20000 positions of four heads are 628 tiles of 128 or more: the first block has a second one)
+    Hk, lens = 4, [ctx - b for b in range(B)]
+    q, kc, vc, ke, ve, ptable, table = _prefix_case(B, 1, N, Hk * g, Hk, D, 16, [far], lens, dtype, cdtype, seed=N)
+    call = lambda st: bd.sdv_prefix_attn(q, kc, vc, ptable, _i32([far]), table, _i32(lens), k_exp=ke, v_exp=ve, lse=True, status=st)  # noqa: E731
+    good, good_lse = call(_status())
+    st = _status()
+    torch.cuda.synchronize()
+    assert bd.sdv_set_attn_test_hooks(bd.SDV_HOOK_ATTN_NO_COPY) == bd.SDV_OK
+    try:
+        out, lse = call(st)
+        torch.cuda.synchronize()
+    finally:
+        assert bd.sdv_set_attn_test_hooks(0) == bd.SDV_OK
+    assert int(st) == bd.SDV_STATUS_TIMEOUT
+    bad = out.isnan().all(-1)
+    assert torch.equal(bad, lse.isnan()) and torch.equal(bad, out.isnan().any(-1))
+    assert torch.equal(out[~bad], good[~bad]) and torch.equal(lse[~bad], good_lse[~bad])
+    assert bad[0, 0, :g].all() and not bad.all()                # (the first block has the first head's first rows, 16 or more)
+    again, again_lse = call(_status())
+    assert torch.equal(again, good) and torch.equal(again_lse, good_lse)
