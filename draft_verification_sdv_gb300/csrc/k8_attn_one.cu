@@ -18,7 +18,7 @@
 // row, where nothing was split.
 //
 // What bounds it: the latency of a unit's chain of reads (length, page, cells) and the
-// cells in flight, of which three CTAs an SM (168 registers) hold 16 KB a warp.  One
+// cells in flight, of which three CTAs an SM (168 registers) hold 8 KB a warp (e4m3: 4).  One
 // token each of 128 sequences with 1 to 700 own positions, 8 x 8 heads of 128, 16 bits:
 // 56 us, 3.2 TB/s (104 us and two joins in units of k8_attn_dec.cu, of which each costs 9
 // us); 96 sequences of up to 500, e4m3: 29 us (71).
@@ -41,7 +41,7 @@ __device__ __forceinline__ uint4 ld_cells(const unsigned char* p, bool there) {
 
 // H: halves of the 16 rows in use.
 template <int DP, bool E4, bool F16, int H>
-__global__ void __launch_bounds__(kOneThreads, DP == 64 ? 4 : H == 1 ? 3 : 2) attn_one_kernel(const AttnArgs a, const float* far, const float* far_log, int splits, int chunk) {
+__global__ void __launch_bounds__(kOneThreads, DP == 64 ? 4 : H == 1 ? 3 : 2) attn_one_kernel(const AttnArgs a, const float* far, const float* far_log, int splits) {
     constexpr bool M16 = F16 || E4;                  // the products' type is fp16
     constexpr int KL = E4 ? DP / 64 : DP / 32;       // 16-byte loads of a lane from a key row
     constexpr int VL = E4 ? 1 : DP / 64;             // ... from a value row (e4m3 heads of 64: half of one)
@@ -54,6 +54,9 @@ __global__ void __launch_bounds__(kOneThreads, DP == 64 ? 4 : H == 1 ? 3 : 2) at
     const Cut cut = cut_of(a, b);
     const int own = cut.cnt > 0 && (!a.mask || (a.mask[b * a.mask_sb] & 1)) ? 1 : 0;     // does the token see itself
     const int len = cut.cnt > 0 ? cut.ctx + own : 0;
+    // (parts of what is held: the table may be far wider)
+    constexpr int kRound = kOneWarps * kOneTile;
+    const int chunk = ((len + kRound - 1) / kRound + splits - 1) / splits * kRound;
     const int begin = blockIdx.y * chunk, end = min(len, begin + chunk);
     if (tid == 0 && blockIdx.y == 0 && cut.bad && a.status) atomicOr(a.status, kStatusBadLength);
 
@@ -112,7 +115,6 @@ __global__ void __launch_bounds__(kOneThreads, DP == 64 ? 4 : H == 1 ? 3 : 2) at
     // its cells one; keys (values) are read as soon as those before them are used
     const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
     auto page_at = [&](int pos) { return lane < kOneTile && pos + lane < end ? __ldg(table + (pos + lane) / a.c.P) : 0; };
-    constexpr int kStep = kOneWarps * kOneTile;
     struct Place {
         int64_t at;                                  // the cells' offset, -1: none
         int ke, ve;
@@ -157,13 +159,13 @@ __global__ void __launch_bounds__(kOneThreads, DP == 64 ? 4 : H == 1 ? 3 : 2) at
     };
     bool nan_row = false;
     int pos0 = begin + warp * kOneTile;
-    int page = page_at(pos0 + kStep);
+    int page = page_at(pos0 + kRound);
     Place here = place_at(pos0, page_at(pos0));
     load_keys(here);
     load_values(here);
-    for (; pos0 < end; pos0 += kStep) {
-        const Place next = place_at(pos0 + kStep, page);
-        page = page_at(pos0 + 2 * kStep);
+    for (; pos0 < end; pos0 += kRound) {
+        const Place next = place_at(pos0 + kRound, page);
+        page = page_at(pos0 + 2 * kRound);
         if (here.bad && a.status) atomicOr(a.status, kStatusBadPage);
 
         // ---- scores ----
@@ -240,6 +242,8 @@ __global__ void __launch_bounds__(kOneThreads, DP == 64 ? 4 : H == 1 ? 3 : 2) at
         }
 
         // ---- probabilities (fp32 into the sum, 16 bits into the product) and outputs ----
+        // (mma.sync takes 16-bit operands, as the other attention kernels' products do; outputs are off by
+        // 0.0023 rms relative in bf16, and rounding them alone makes 0.0017)
         uint32_t p[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int r = 0; r < H; ++r) {
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(kOneThreads, DP == 64 ? 4 : H == 1 ? 3 : 2) at
 }
 
 template <int DP, bool E4, bool F16, int H>
-cudaError_t one(const AttnArgs& a, const float* far, const float* far_log, int splits, int chunk, cudaStream_t s) {
+cudaError_t one(const AttnArgs& a, const float* far, const float* far_log, int splits, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.B * a.c.H), static_cast<unsigned>(splits));
     cfg.blockDim = dim3(kOneThreads);
@@ -364,14 +368,14 @@ cudaError_t one(const AttnArgs& a, const float* far, const float* far_log, int s
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_one_kernel<DP, E4, F16, H>, a, far, far_log, splits, chunk);
+    return cudaLaunchKernelEx(&cfg, attn_one_kernel<DP, E4, F16, H>, a, far, far_log, splits);
 }
 
 template <int DP, bool E4>
-cudaError_t one_types(const AttnArgs& a, bool f16, const float* far, const float* far_log, int splits, int chunk, cudaStream_t s) {
+cudaError_t one_types(const AttnArgs& a, bool f16, const float* far, const float* far_log, int splits, cudaStream_t s) {
     if (a.g <= 8)
-        return f16 ? one<DP, E4, true, 1>(a, far, far_log, splits, chunk, s) : one<DP, E4, false, 1>(a, far, far_log, splits, chunk, s);
-    return f16 ? one<DP, E4, true, 2>(a, far, far_log, splits, chunk, s) : one<DP, E4, false, 2>(a, far, far_log, splits, chunk, s);
+        return f16 ? one<DP, E4, true, 1>(a, far, far_log, splits, s) : one<DP, E4, false, 1>(a, far, far_log, splits, s);
+    return f16 ? one<DP, E4, true, 2>(a, far, far_log, splits, s) : one<DP, E4, false, 2>(a, far, far_log, splits, s);
 }
 
 }  // namespace
@@ -379,12 +383,9 @@ cudaError_t one_types(const AttnArgs& a, bool f16, const float* far, const float
 bool attn_one_takes(const AttnArgs& a) { return a.N == 1 && a.g <= 16 && (a.c.D == 64 || a.c.D == 128); }
 
 cudaError_t launch_attn_one(const AttnArgs& a, bool f16, bool e4m3, const float* far, const float* far_log, int splits, cudaStream_t s) {
-    const int room = a.max_pages * a.c.P;
-    const int tiles = (room + kOneTile * kOneWarps - 1) / (kOneTile * kOneWarps);
-    const int chunk = (tiles + splits - 1) / splits * (kOneTile * kOneWarps);
     if (a.c.D == 64)
-        return e4m3 ? one_types<64, true>(a, f16, far, far_log, splits, chunk, s) : one_types<64, false>(a, f16, far, far_log, splits, chunk, s);
-    return e4m3 ? one_types<128, true>(a, f16, far, far_log, splits, chunk, s) : one_types<128, false>(a, f16, far, far_log, splits, chunk, s);
+        return e4m3 ? one_types<64, true>(a, f16, far, far_log, splits, s) : one_types<64, false>(a, f16, far, far_log, splits, s);
+    return e4m3 ? one_types<128, true>(a, f16, far, far_log, splits, s) : one_types<128, false>(a, f16, far, far_log, splits, s);
 }
 
 }  // namespace sdv

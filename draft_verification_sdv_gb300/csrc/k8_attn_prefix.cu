@@ -26,6 +26,7 @@ constexpr int kThreads = 256;
 // Parts of single tokens' own positions, where there are few heads to share out.  With 64
 // heads: 4 sequences of 4000 positions 52 us in 8 parts and 142 in one, 16 of them 99 and
 // 152; 48 sequences of 600 positions 70 us in two parts and 62 in one, of 4000 189 and 181.
+// (Each sequence's held positions are cut, however wide the table.)
 constexpr int kMaxSplits = 8;
 int splits_of(int64_t rows, int N) {
     const int64_t n = N > 1 ? 1 : 6000 / rows;
@@ -94,6 +95,8 @@ cudaError_t launch_join(const AttnArgs& a, const float* const (&from)[4], int64_
 
 }  // namespace
 
+// (The second set of rows is not used by calls that go on from the prefix's: which do depends on the
+// cache's type and pages, which the size is asked for without.)
 size_t prefix_workspace_bytes(int B, int N, int Hq, int D, int nsm) {
     const int64_t rows = static_cast<int64_t>(B) * N * Hq;
     const size_t one = static_cast<size_t>(rows) * (D + 1) * sizeof(float);

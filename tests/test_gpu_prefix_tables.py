@@ -18,7 +18,7 @@ def _lib():
 
 
 @pytest.mark.parametrize("dtype,cdtype", TYPES)
-@pytest.mark.parametrize("B,N,Hq,Hk,D,ctx", [(4, 1, 8, 1, 128, [0, 63, 64, 500]), (2, 1, 16, 2, 64, [1, 200]), (160, 1, 4, 1, 128, list(range(160))),
+@pytest.mark.parametrize("B,N,Hq,Hk,D,ctx", [(4, 1, 8, 1, 128, [0, 63, 64, 500]), (3, 1, 8, 2, 128, [1000, 255, 700]), (2, 1, 16, 2, 64, [1, 200]), (160, 1, 4, 1, 128, list(range(160))),
                                              (3, 4, 8, 2, 128, [0, 70, 300]), (2, 40, 8, 1, 64, [9, 128])])
 def test_wide_tables(B, N, Hq, Hk, D, ctx, dtype, cdtype):
     far = [300]
@@ -34,6 +34,9 @@ def test_wide_tables(B, N, Hq, Hk, D, ctx, dtype, cdtype):
     one = bd.sdv_prefix_attn(q, kc, vc, wptable, _i32(far), wide, _i32(ctx), **args)
     two = bd.sdv_prefix_attn(q, kc, vc, wptable, _i32(far), wide, _i32(ctx), **args)
     assert int(st) == 0 and all(torch.equal(a, b) for a, b in zip(one, two))
+    # the same work is shared out the same way whatever the tables' width
+    tight = bd.sdv_prefix_attn(q, kc, vc, ptable, _i32(far), table, _i32(ctx), **args)
+    assert all(torch.equal(a, b) for a, b in zip(one, tight))
 
 
 @pytest.mark.parametrize("dtype,cdtype", TYPES)
