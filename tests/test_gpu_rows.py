@@ -319,3 +319,21 @@ def test_rows_leave_the_cache_to_others(dtype):
         bd.sdv_sample(x, u, **_dev(cut))
         bd.sdv_logits_truncate(x, **_dev(cut))
     assert best() <= 1.15 * before
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("R", [1, 50, 330])
+def test_the_longest_rows(R, dtype):
+    """2^19 logits, all equal: their weights add up to 2^63."""
+    V = 1 << 19
+    x = torch.full((R, V), 2.5, dtype=dtype, device="cuda")
+    r = random.Random(R)
+    u = [r.choice([0.0, 1 - 2.0 ** -24, r.random()]) for _ in range(R)]
+    p = [r.choice([1 - 2.0 ** -24, 0.5, r.random()]) for _ in range(R)]
+    tokens, logs = bd.sdv_sample(x, torch.tensor(u, dtype=F32, device="cuda"), logprob=True)
+    assert tokens.tolist() == [int(ref.f32(v) * V) for v in u]   # (43 bits: exact)
+    assert ((logs + 19 * math.log(2)).abs() <= 2.0 ** -20).all()           # (13.2, rounded to 2^-20, and its logarithm's own)
+    out, kept = bd.sdv_logits_truncate(x, top_p=torch.tensor(p, dtype=F32, device="cuda"), kept=True)
+    want = torch.tensor([math.ceil(ref.f32(v) * V) for v in p], device="cuda")
+    assert torch.equal(kept.long(), want)
+    assert torch.equal(out > -math.inf, torch.arange(V, device="cuda") < want[:, None])
