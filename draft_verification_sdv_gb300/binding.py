@@ -983,8 +983,8 @@ def sdv_prefix_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
 
 
 def sdv_set_attn_test_hooks(hooks: int) -> int:
-    """Fault-path test hooks of later sdv_tree_attn calls (SDV_HOOK_ATTN_NO_COPY
-    or 0)."""
+    """Fault-path test hooks of later sdv_tree_attn and sdv_prefix_attn calls
+    (SDV_HOOK_ATTN_NO_COPY or 0)."""
     return load().sdv_set_attn_test_hooks(int(hooks))
 
 

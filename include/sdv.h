@@ -760,12 +760,12 @@ sdv_status sdv_prefix_attn(const sdv_kv_cache* cache, int B, int groups, int N, 
                            size_t workspace_bytes, int32_t* status);
 
 /*
- * Fault-path test hook of later sdv_tree_attn calls of the process (not part of
- * the method).  With SDV_HOOK_ATTN_NO_COPY the kernels that load by tile copies
- * (head_dim <= 128, page_size a multiple of 8) leave the copies of the first
- * block's second tile out and poll fewer times, so that its bounded waits run out
- * with nothing of it in flight: the rows that this block had still to write
- * become NaN and *status gets SDV_STATUS_TIMEOUT.  hooks = 0 restores normal
+ * Fault-path test hook of later sdv_tree_attn and sdv_prefix_attn calls of the
+ * process (not part of the method).  With SDV_HOOK_ATTN_NO_COPY the kernels that
+ * load by tile copies (head_dim <= 128, page_size a multiple of 8) leave the copies
+ * of the first block's second tile out and poll fewer times, so that its bounded
+ * waits run out with nothing of it in flight: the rows that this block had still to
+ * write become NaN and *status gets SDV_STATUS_TIMEOUT.  hooks = 0 restores normal
  * calls; unknown bits give SDV_ERR_ARG.
  */
 #define SDV_HOOK_ATTN_NO_COPY 2u
