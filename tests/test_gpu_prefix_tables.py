@@ -1,5 +1,8 @@
-"""Attention behind shared prefixes where block tables are far wider than what the
-sequences hold, as a server's are that has room for its longest request."""
+"""Attention behind shared prefixes at its edges: block tables far wider than what the
+sequences hold, as a server's are that has room for its longest request, waits that run
+out, infinities."""
+import math
+
 import pytest
 import torch
 
@@ -65,3 +68,39 @@ def test_waits_that_run_out(B, N, g, D, far, ctx, dtype, cdtype):
     assert bad[0, 0, :g].all() and not bad.all()                # (the first block has the first head's first rows, 16 or more)
     again, again_lse = call(_status())
     assert torch.equal(again, good) and torch.equal(again_lse, good_lse)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("B,N,g,D,P", [(3, 1, 8, 128, 16), (60, 1, 16, 64, 16), (3, 1, 2, 96, 16), (3, 1, 8, 64, 12), (3, 9, 1, 64, 16), (3, 40, 4, 128, 16),
+                                       (2, 30, 1, 192, 16)])
+def test_infinities(B, N, g, D, P, dtype):
+    """A score of -infinity has weight 0 on either side, and nodes that have no other have
+    nothing; +infinity, an infinite value and NaN that a node sees make it not finite."""
+    Hk, far, ctx = 2, [150], [7 + 31 * b % 120 for b in range(B)]
+    q, kc, vc, ke, ve, ptable, table = _prefix_case(B, 1, N, Hk * g, Hk, D, P, far, ctx, dtype, dtype, seed=N)
+    q = q.clone()
+    q[..., 0] = 2.0
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    kp = torch.randn((1, far[0], Hk, D), generator=gen, device="cuda").to(dtype)
+    ko = torch.randn((B, max(ctx) + N, Hk, D), generator=gen, device="cuda").to(dtype)
+
+    def run(fill, prefix=None, own=None, value=None):
+        for k, where, t in ((kp, prefix, ptable), (ko, own, table)):
+            kk, v = k.clone(), k.flip(1).clone()
+            if where is not None:
+                (kk if value is None else v)[:, where, :, 0] = fill if value is None else value
+            bd.sdv_kv_write(kk, v, kc, vc, t, _i32([0] * k.shape[0]))
+        st = _status()
+        got = bd.sdv_prefix_attn(q, kc, vc, ptable, _i32(far), table, _i32(ctx), lse=True, status=st)
+        assert int(st) == 0
+        return got
+    some, every = slice(3, None, 17), slice(None)
+    for prefix, own in ((some, None), (None, some), (some, some), (every, None), (None, every), (every, some)):
+        want, got = run(-6.0e4, prefix, own), run(-math.inf, prefix, own)
+        assert want[0].isfinite().all() and torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    out, lse = run(-math.inf, every, every)
+    assert not out.any() and (lse == -math.inf).all()
+    for prefix, own in ((some, None), (None, slice(3, 4))):
+        for fill in (math.inf, math.nan):
+            assert not run(fill, prefix, own)[0].isfinite().all(-1).any()
+        assert not run(0.0, prefix, own, value=math.inf)[0].isfinite().all(-1).any()
